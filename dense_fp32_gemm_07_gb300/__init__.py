@@ -8,7 +8,8 @@ is no fallback when it is missing.
 Low-level names mirror the C ABI one to one (``b2g_sgemm``, ``b2g_sgemm_ex``,
 ``b2g_sgemm_with_plan``, ...) and take raw device pointers; ``sgemm`` is the
 tensor-level convenience: ``C <- alpha * op(A) @ op(B) + beta * C`` in place;
-``sgemm_colmajor`` is the same for column-major tensors.
+``sgemm_colmajor`` is the same for column-major tensors.  The operators of a
+training step beside the products (include/b2g_train.h) are in ``train.py``.
 """
 from __future__ import annotations
 
@@ -431,3 +432,11 @@ def sgemm_colmajor(A, B, C, alpha: float = 1.0, beta: float = 0.0, transA: bool 
 def plans():
     """Names of the compiled plans, by index."""
     return [b2g_plan_name(i) for i in range(b2g_plan_count())]
+
+
+# --- training-step operators (include/b2g_train.h) ---------------------------------
+
+from .train import (  # noqa: E402
+    B2G_BF16, B2G_ERR_INDEX, B2G_ERR_INVALID_TYPE, B2G_ERR_WORKSPACE, B2G_F32, TRAIN_EXPORTS,
+    clip_grad_norm, embedding, embedding_backward, grad_norm, layer_norm, layer_norm_backward,
+    train_library)

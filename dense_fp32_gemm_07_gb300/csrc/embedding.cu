@@ -1,0 +1,577 @@
+// embedding.cu -- embedding lookup and its gradient (b2g_embedding,
+// b2g_embedding_backward in include/b2g_train.h).
+//
+// Forward: a gather, bound by bytes (each looked-up row read, each output row
+// written).
+//
+// Backward: dtable_v = scale * sum of dout_i over the tokens i with id v.  The
+// tokens are first put in the order of their ids (a stable radix sort, so that
+// equal ids keep their order and the sums their bits), then cut into windows of
+// W consecutive sorted tokens:
+//  1. emb_sort_kernel: one cluster sorts (id, token) pairs; the other blocks of
+//     the same launch write the table's zeros meanwhile (that is most of the
+//     traffic when the table is larger than the batch);
+//  2. emb_window_kernel: each window adds the rows of each run of equal ids.  A
+//     run that lies inside its window is final and goes to dtable; the first and
+//     last run of a window may continue beyond it and go to FP32 partial rows;
+//  3. emb_join_kernel: the block of the window in which a longer run begins adds
+//     its partial rows in window order.
+// Windows make the work even however often the most frequent token occurs.
+#include "tcgen05.cuh"
+#include "train_common.cuh"
+
+namespace b2g {
+namespace {
+
+__device__ __forceinline__ long long id_at(const void* ids, int bytes, long long i) {
+  return bytes == 8 ? static_cast<const long long*>(ids)[i]
+                    : (long long)static_cast<const int*>(ids)[i];
+}
+
+// ------------------------------------------------------------------- forward
+
+struct EmbFwd {
+  long long tokens;
+  int vocab, chunks;  // chunks = width / VEC
+  const void* ids;
+  int id_bytes;
+  const void* table;
+  long long ldt;
+  float scale;
+  void* out;
+  long long ldo;
+  unsigned int* status;
+};
+
+// blockDim.x threads per token, blockDim.y tokens per block; U chunks a thread
+// (its loads are all in flight before the first store); blockIdx.y covers wider
+// rows.
+template <typename T, int VEC, int U>
+__global__ void __launch_bounds__(256) emb_fwd_kernel(const __grid_constant__ EmbFwd p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long i = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  if (i >= p.tokens) return;
+  const long long id = id_at(p.ids, p.id_bytes, i);
+  const int c0 = blockIdx.y * blockDim.x * U + threadIdx.x;
+  T* o = static_cast<T*>(p.out) + i * p.ldo;
+  const bool ok = id >= 0 && id < p.vocab;
+  if (!ok && c0 == 0) atomicOr(p.status, kStatusIndex);
+  const T* r = static_cast<const T*>(p.table) + (ok ? id : 0) * p.ldt;
+  Pack<T, VEC> v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = c0 + u * blockDim.x;
+    v[u].zero();
+    if (ok && c < p.chunks) v[u].load(r + c * VEC);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int c = c0 + u * blockDim.x;
+    if (c < p.chunks) {
+      float f[VEC];
+      v[u].get(f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) f[j] = ok ? f[j] * p.scale : __int_as_float(0x7fc00000);
+      v[u].set(f);
+      v[u].store(o + c * VEC);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------- sort
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortCtas = 8;              // blocks of the sorting cluster (portable limit)
+constexpr int kDigitBits = 8, kDigits = 1 << kDigitBits;
+
+struct EmbSort {
+  int tokens, vocab, passes;
+  int ctas;                  // blocks of the cluster that take part
+  const void* ids;
+  int id_bytes;
+  long long padding;
+  unsigned* key[2];   // tokens ids each, unsorted / sorted by turns; the sort ends in key[0]
+  int* pos[2];        // the token each came from
+  unsigned* hist;     // [kDigits][ctas * kSortWarps] counts, then first places
+  unsigned int* status;
+  // the table to clear (bytes from zero_base, or rows of zero_row bytes zero_ld apart)
+  unsigned char* table;
+  long long rows, row_bytes, ld_bytes;  // rows == 0: nothing to clear
+};
+
+// Zeros over the rows of the table, by blocks `b` of `nb`.
+__device__ __noinline__ void clear_rows(const EmbSort& p, long long b, long long nb) {
+  const bool flat = p.row_bytes == p.ld_bytes;
+  const long long rows = flat ? 1 : p.rows, bytes = flat ? p.rows * p.row_bytes : p.row_bytes;
+  if (flat) {  // one run of bytes: 16-byte stores between its ragged ends
+    unsigned char* t = p.table;
+    const long long head = (16 - (long long)(reinterpret_cast<uintptr_t>(t) & 15)) & 15;
+    const long long h = head < bytes ? head : bytes, vecs = (bytes - h) / 16;
+    uint4* v = reinterpret_cast<uint4*>(t + h);
+    for (long long i = b * kSortThreads + threadIdx.x; i < vecs; i += nb * kSortThreads)
+      v[i] = make_uint4(0, 0, 0, 0);
+    if (b == 0) {
+      for (long long i = threadIdx.x; i < h; i += kSortThreads) t[i] = 0;
+      for (long long i = h + vecs * 16 + threadIdx.x; i < bytes; i += kSortThreads) t[i] = 0;
+    }
+  } else {
+    for (long long r = b; r < rows; r += nb) {
+      unsigned char* t = p.table + r * p.ld_bytes;
+      if (((reinterpret_cast<uintptr_t>(t) | (uintptr_t)bytes) & 15) == 0) {
+        for (long long i = threadIdx.x; i < bytes / 16; i += kSortThreads)
+          reinterpret_cast<uint4*>(t)[i] = make_uint4(0, 0, 0, 0);
+      } else {  // every element type has an even size
+        for (long long i = threadIdx.x; i < bytes / 2; i += kSortThreads)
+          reinterpret_cast<unsigned short*>(t)[i] = 0;
+      }
+    }
+  }
+}
+
+// Cluster 0 sorts, the other clusters clear the table.  The sort: `passes`
+// stable passes over kDigitBits bits each, lowest first.  Warp w of the cluster
+// owns a contiguous range of the input; it counts its digits, the counts are
+// turned into first places (digit by digit, warp by warp), and it then places
+// its pairs in order, 32 at a time: a pair's place is its digit's next one plus
+// the number of lower lanes with the same digit.  An id that takes part in no
+// sum (padding, out of range) sorts last as `vocab`.  Bound: latency; 4096
+// tokens take about as long as writing 100 MB of zeros.
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads)
+    emb_sort_kernel(const __grid_constant__ EmbSort p) {
+  __shared__ unsigned count[kSortWarps][kDigits];
+  __shared__ unsigned scan[kSortWarps];
+  pdl_launch_dependents();
+  pdl_wait();
+  if (blockIdx.x >= kSortCtas) {
+    if (p.rows > 0)
+      clear_rows(p, (long long)blockIdx.x - kSortCtas, (long long)gridDim.x - kSortCtas);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int W = p.ctas * kSortWarps;  // warps that take part
+  const bool active = (int)blockIdx.x < p.ctas;
+  const int gw = blockIdx.x * kSortWarps + warp;
+  // ranges are whole multiples of 32 so that every warp runs full rounds
+  const int per = ((p.tokens + W - 1) / W + 31) / 32 * 32;
+  const long long lo64 = (long long)gw * per;
+  const int lo = active && lo64 < p.tokens ? (int)lo64 : p.tokens;
+  const int hi = lo + per < p.tokens ? lo + per : p.tokens;
+  const unsigned below = (1u << lane) - 1u;
+
+  for (int i = lo + lane; i < hi; i += 32) {
+    const long long id = id_at(p.ids, p.id_bytes, i);
+    const bool in = id >= 0 && id < p.vocab;
+    if (!in && !(p.padding >= 0 && id == p.padding)) atomicOr(p.status, kStatusIndex);
+    p.key[0][i] = in && id != p.padding ? (unsigned)id : (unsigned)p.vocab;
+    p.pos[0][i] = i;
+  }
+  __syncwarp();
+  int src = 0;
+  for (int pass = 0; pass < p.passes; ++pass, src ^= 1) {
+    const int shift = pass * kDigitBits;
+    const unsigned* key = p.key[src];
+    const int* pos = p.pos[src];
+    unsigned* cnt = count[warp];
+    for (int d = lane; d < kDigits; d += 32) cnt[d] = 0;
+    __syncwarp();
+    for (int i = lo + lane; i < hi; i += 32)
+      atomicAdd(&cnt[(key[i] >> shift) & (kDigits - 1)], 1u);
+    __syncwarp();
+    if (active)
+      for (int d = lane; d < kDigits; d += 32) p.hist[(size_t)d * W + gw] = cnt[d];
+    cluster_sync();
+    if (blockIdx.x == 0) {
+      // exclusive prefix sums over [digit][warp]; a thread owns kDigits * W / 1024 of them
+      const int PER = kDigits * p.ctas / 32;  // kDigits * W / kSortThreads, a multiple of 8
+      uint4* h = reinterpret_cast<uint4*>(p.hist) + (size_t)threadIdx.x * (PER / 4);
+      unsigned mine = 0;
+#pragma unroll 2
+      for (int i = 0; i < PER / 4; ++i) {
+        const uint4 v = h[i];
+        mine += v.x + v.y + v.z + v.w;
+      }
+      unsigned incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      if (lane == 31) scan[warp] = incl;
+      __syncthreads();
+      if (warp == 0) {
+        const unsigned mineW = scan[lane];
+        unsigned w = mineW;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned up = __shfl_up_sync(0xffffffffu, w, o);
+          if (lane >= o) w += up;
+        }
+        scan[lane] = w - mineW;
+      }
+      __syncthreads();
+      unsigned at = scan[warp] + incl - mine;
+#pragma unroll 2
+      for (int i = 0; i < PER / 4; ++i) {
+        const uint4 v = h[i];
+        uint4 o;
+        o.x = at, at += v.x;
+        o.y = at, at += v.y;
+        o.z = at, at += v.z;
+        o.w = at, at += v.w;
+        h[i] = o;
+      }
+    }
+    cluster_sync();
+    if (active)
+      for (int d = lane; d < kDigits; d += 32) cnt[d] = p.hist[(size_t)d * W + gw];
+    __syncwarp();
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+      const int i = i0 + lane;
+      const bool in = i < hi;
+      const unsigned k = in ? key[i] : 0u;
+      const int s = in ? pos[i] : 0;
+      const unsigned d = (k >> shift) & (kDigits - 1);
+      unsigned same = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+      for (int b = 0; b < kDigitBits; ++b) {
+        const unsigned one = __ballot_sync(0xffffffffu, (d >> b) & 1u);
+        same &= (d >> b) & 1u ? one : ~one;
+      }
+      unsigned at = 0;
+      if (in) at = cnt[d] + __popc(same & below);
+      __syncwarp();
+      if (in) {
+        if ((same & below) == 0) cnt[d] += __popc(same);
+        p.key[src ^ 1][at] = k, p.pos[src ^ 1][at] = s;
+      }
+      __syncwarp();
+    }
+    cluster_sync();
+  }
+}
+
+// ------------------------------------------------------------------- windows
+
+struct EmbSum {
+  int tokens, vocab, width, chunks, window;
+  const unsigned* key;
+  const int* pos;
+  const void* dout;
+  long long ldd;
+  float scale;
+  int accumulate;
+  void* dtable;
+  long long ldt;
+  float* part;  // [windows][2][width]: the window's first run (0), its last run (1)
+};
+
+// VEC FP32 partial sums to and from a partial row.
+template <int VEC>
+__device__ __forceinline__ void put_part(float* q, const float (&a)[VEC]) {
+  if constexpr (VEC % 4 == 0) {
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4)
+      *reinterpret_cast<float4*>(q + j) = make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) q[j] = a[j];
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void get_part(const float* q, float (&a)[VEC]) {
+  if constexpr (VEC % 4 == 0) {
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(q + j);
+      a[j] = v.x, a[j + 1] = v.y, a[j + 2] = v.z, a[j + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) a[j] = q[j];
+  }
+}
+
+// A sum of one run's columns, scaled and stored (or added) as one final row chunk.
+template <typename T, int VEC>
+__device__ __forceinline__ void put_row(const EmbSum& p, unsigned row, int c, const float (&a)[VEC]) {
+  T* t = static_cast<T*>(p.dtable) + (long long)row * p.ldt + c * VEC;
+  float f[VEC];
+  Pack<T, VEC> k;
+  if (p.accumulate) {
+    k.load(t);
+    k.get(f);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = fmaf(a[j], p.scale, f[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = a[j] * p.scale;
+  }
+  k.set(f);
+  k.store(t);
+}
+
+// blockDim.x threads share a window's columns (one chunk each), blockDim.y
+// windows per block; blockIdx.y covers wider rows.  The rows of the next four
+// tokens are in flight while the last four are added.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) emb_window_kernel(const __grid_constant__ EmbSum p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int w = blockIdx.x * blockDim.y + threadIdx.y;
+  const int c = blockIdx.y * blockDim.x + threadIdx.x;
+  const long long begin = (long long)w * p.window;
+  if (begin >= p.tokens || c >= p.chunks) return;
+  const int b = (int)begin, e = b + p.window < p.tokens ? b + p.window : p.tokens;
+  const unsigned vocab = (unsigned)p.vocab;
+  const T* dout = static_cast<const T*>(p.dout) + c * VEC;
+  const bool from_before = b > 0 && p.key[b - 1] == p.key[b];
+  const bool to_after = e < p.tokens && p.key[e] == p.key[e - 1];
+  bool first = true;
+  unsigned run = p.key[b];
+  float a[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) a[j] = 0.f;
+  float* part = p.part + (size_t)w * 2 * p.width + c * VEC;
+  auto flush = [&](bool last) {
+    if (run < vocab) {
+      const bool head = first && from_before, tail = last && to_after;
+      if (head || tail)
+        put_part<VEC>(head ? part : part + p.width, a);
+      else
+        put_row<T, VEC>(p, run, c, a);
+    }
+  };
+  constexpr int U = 4;
+  for (int i = b; i < e; i += U) {
+    unsigned key[U];
+    Pack<T, VEC> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      key[u] = i + u < e ? p.key[i + u] : vocab;
+      v[u].zero();
+      if (key[u] < vocab) v[u].load(dout + (long long)p.pos[i + u] * p.ldd);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (i + u < e && key[u] != run) {
+        flush(false);
+        first = false, run = key[u];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) a[j] = 0.f;
+      }
+      float f[VEC];
+      v[u].get(f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) a[j] += f[j];
+    }
+  }
+  flush(true);
+}
+
+// The run that begins in window w and continues past it: its last partial row,
+// then the first partial rows of the windows after it up to where the run ends.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) emb_join_kernel(const __grid_constant__ EmbSum p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int w = blockIdx.x * blockDim.y + threadIdx.y;
+  const int c = blockIdx.y * blockDim.x + threadIdx.x;
+  const long long begin = (long long)w * p.window, end = begin + p.window;
+  if (end >= p.tokens || c >= p.chunks) return;
+  const unsigned run = p.key[end - 1];
+  if (run >= (unsigned)p.vocab || p.key[end] != run) return;       // it ends here
+  if (begin > 0 && p.key[begin - 1] == run) return;  // it began in an earlier window
+  float a[VEC];
+  get_part<VEC>(p.part + ((size_t)w * 2 + 1) * p.width + c * VEC, a);
+  // the windows that begin with the run, eight at a time
+  constexpr int U = 8;
+  for (int k = w + 1;; k += U) {
+    bool in[U];
+    float f[U][VEC];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long at = (long long)(k + u) * p.window;
+      in[u] = at < p.tokens && p.key[at] == run;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (in[u]) get_part<VEC>(p.part + (size_t)(k + u) * 2 * p.width + c * VEC, f[u]);
+    bool on = true;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      on = on && in[u];
+      if (on) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) a[j] += f[u][j];
+      }
+    }
+    if (!on) break;
+  }
+  put_row<T, VEC>(p, run, c, a);
+}
+
+// ----------------------------------------------------------------- host side
+
+constexpr long long kMaxTokens = 1LL << 30;
+
+int check(int dtype, long long tokens, int vocab, int width) {
+  if (!type_ok(dtype)) return B2G_ERR_INVALID_TYPE;
+  if (tokens < 0 || vocab < 0 || width < 0 || tokens > kMaxTokens) return B2G_ERR_INVALID_DIM;
+  return 0;
+}
+
+bool ld_ok(long long ld, int width) { return ld >= (width > 1 ? width : 1); }
+
+int pow2_at_least(int n, int lo, int hi) {
+  int t = lo;
+  while (t < n && t < hi) t *= 2;
+  return t;
+}
+
+template <typename T, int VEC>
+cudaError_t fwd_launch(EmbFwd p, int width, int sms, cudaStream_t st) {
+  p.chunks = width / VEC;
+  // Few tokens: one chunk a thread, so that more SMs share the rows.
+  const bool many = p.tokens * p.chunks >= 4LL * 2048 * sms;
+  const int u = many ? 4 : 1;
+  const int tx = pow2_at_least((int)ceil_div(p.chunks, u), 8, 256), ty = 256 / tx;
+  const dim3 grid((unsigned)ceil_div(p.tokens, ty), (unsigned)ceil_div(p.chunks, tx * u));
+  if (many) return launch_train(emb_fwd_kernel<T, VEC, 4>, grid, dim3(tx, ty), 0, st, p);
+  return launch_train(emb_fwd_kernel<T, VEC, 1>, grid, dim3(tx, ty), 0, st, p);
+}
+
+// Sorted tokens per window: enough windows (times column blocks) to fill the
+// GPU about four times over, 16 to 128 tokens each.
+int window_of(long long tokens, int width) {
+  const long long col_blocks = ceil_div(width, 1024);
+  int w = 16;
+  while (w < 128 && ceil_div(tokens, w) * col_blocks > 4 * 152 * 2) w *= 2;
+  return w;
+}
+
+struct BwdSizes {
+  size_t key[2], pos[2], hist, part, total;
+};
+
+BwdSizes bwd_sizes(long long tokens, int width) {
+  BwdSizes s;
+  size_t at = 0;
+  const size_t list = round_up((size_t)tokens * 4, 256);
+  for (int i = 0; i < 2; ++i) s.key[i] = at, at += list;
+  for (int i = 0; i < 2; ++i) s.pos[i] = at, at += list;
+  s.hist = at, at += (size_t)kDigits * kSortCtas * kSortWarps * 4;
+  s.part = at;
+  at += (size_t)ceil_div(tokens, window_of(tokens, width)) * 2 * width * sizeof(float);
+  s.total = at;
+  return s;
+}
+
+template <typename T, int VEC>
+cudaError_t sum_launch(EmbSum p, cudaStream_t st) {
+  p.chunks = p.width / VEC;
+  const int tx = pow2_at_least(p.chunks, 8, 256), ty = 256 / tx;
+  const long long windows = ceil_div(p.tokens, p.window);
+  const dim3 grid((unsigned)ceil_div(windows, ty), (unsigned)ceil_div(p.chunks, tx));
+  cudaError_t e = launch_train(emb_window_kernel<T, VEC>, grid, dim3(tx, ty), 0, st, p);
+  if (e == cudaSuccess && windows > 1)
+    e = launch_train(emb_join_kernel<T, VEC>, grid, dim3(tx, ty), 0, st, p);
+  return e;
+}
+
+}  // namespace
+}  // namespace b2g
+
+using namespace b2g;
+
+extern "C" {
+
+int b2g_embedding(int dtype, long long tokens, int vocab, int width, const void* ids, int id_bytes,
+                  const void* table, long long ldt, float scale, void* out, long long ldo,
+                  void* stream) {
+  int rc = check(dtype, tokens, vocab, width);
+  if (rc) return rc;
+  if (id_bytes != 8 && id_bytes != 4) return B2G_ERR_INVALID_TYPE;
+  if (!ld_ok(ldt, width) || !ld_ok(ldo, width)) return B2G_ERR_INVALID_LD;
+  if (tokens == 0 || width == 0) return 0;
+  if (!ids || !out || (vocab > 0 && !table)) return B2G_ERR_NULL;
+  TrainDevice d;
+  rc = train_device(&d);
+  if (rc) return rc;
+  EmbFwd p{tokens, vocab, 0, ids, id_bytes, table, ldt, scale, out, ldo, d.status};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool v = vec16(table) && vec16(out) && vec16_ld(ldt, dtype) && vec16_ld(ldo, dtype) &&
+                 vec16_ld(width, dtype);
+  if (dtype == B2G_F32)
+    return launch_code(v ? fwd_launch<float, 4>(p, width, d.sms, st)
+                         : fwd_launch<float, 1>(p, width, d.sms, st));
+  return launch_code(v ? fwd_launch<Bf16, 8>(p, width, d.sms, st)
+                       : fwd_launch<Bf16, 1>(p, width, d.sms, st));
+}
+
+int b2g_embedding_backward_workspace_size(int dtype, long long tokens, int vocab, int width,
+                                          size_t* bytes) {
+  const int rc = check(dtype, tokens, vocab, width);
+  if (rc) return rc;
+  if (!bytes) return B2G_ERR_NULL;
+  *bytes = tokens && vocab && width ? bwd_sizes(tokens, width).total : 0;
+  return 0;
+}
+
+int b2g_embedding_backward(int dtype, long long tokens, int vocab, int width, const void* ids,
+                           int id_bytes, const void* dout, long long ldd, float scale,
+                           long long padding, int accumulate, void* dtable, long long ldt,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check(dtype, tokens, vocab, width);
+  if (rc) return rc;
+  if (id_bytes != 8 && id_bytes != 4) return B2G_ERR_INVALID_TYPE;
+  if (!ld_ok(ldd, width) || !ld_ok(ldt, width)) return B2G_ERR_INVALID_LD;
+  if (vocab == 0 || width == 0 || (tokens == 0 && accumulate)) return 0;
+  if (!dtable || (tokens > 0 && (!ids || !dout))) return B2G_ERR_NULL;
+  TrainDevice d;
+  rc = train_device(&d);
+  if (rc) return rc;
+  const long long es = (long long)type_size(dtype);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (tokens == 0)
+    return cudaMemset2DAsync(dtable, ldt * es, 0, width * es, vocab, st) == cudaSuccess
+               ? 0
+               : B2G_ERR_CUDA;
+  const BwdSizes s = bwd_sizes(tokens, width);
+  if (!workspace || !vec16(workspace) || workspace_bytes < s.total) return B2G_ERR_WORKSPACE;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  EmbSort q;
+  q.tokens = (int)tokens, q.vocab = vocab;
+  q.passes = 1;  // the keys run from 0 to vocab, which stands for "in no sum"
+  while (q.passes < 4 && (unsigned)vocab >> (q.passes * kDigitBits)) ++q.passes;
+  q.ctas = (int)(tokens >= 4096LL * kSortCtas ? kSortCtas : ceil_div(tokens, 4096));
+  q.ids = ids, q.id_bytes = id_bytes, q.padding = padding;
+  for (int i = 0; i < 2; ++i) {
+    q.key[i] = reinterpret_cast<unsigned*>(ws + s.key[i]);
+    q.pos[i] = reinterpret_cast<int*>(ws + s.pos[i]);
+  }
+  q.hist = reinterpret_cast<unsigned*>(ws + s.hist);
+  q.status = d.status;
+  q.table = static_cast<unsigned char*>(dtable);
+  q.rows = accumulate ? 0 : vocab;
+  q.row_bytes = width * es, q.ld_bytes = vocab > 1 ? ldt * es : width * es;
+  // One cluster sorts; the clearing blocks fill the other SMs, one each.
+  const int blocks = accumulate ? kSortCtas : (d.sms / kSortCtas) * kSortCtas;
+  cudaError_t e = launch_train(emb_sort_kernel, dim3(blocks < 2 * kSortCtas && !accumulate
+                                                         ? 2 * kSortCtas
+                                                         : blocks),
+                               dim3(kSortThreads), 0, st, q);
+  if (e != cudaSuccess) return B2G_ERR_LAUNCH;
+  const int sorted = q.passes & 1;
+  EmbSum p{(int)tokens, vocab, width, 0, window_of(tokens, width), q.key[sorted], q.pos[sorted],
+           dout, ldd, scale, accumulate != 0, dtable, ldt,
+           reinterpret_cast<float*>(ws + s.part)};
+  const bool v = vec16(dout) && vec16(dtable) && vec16_ld(ldd, dtype) && vec16_ld(ldt, dtype) &&
+                 vec16_ld(width, dtype);
+  if (dtype == B2G_F32)
+    return launch_code(v ? sum_launch<float, 4>(p, st) : sum_launch<float, 1>(p, st));
+  return launch_code(v ? sum_launch<Bf16, 8>(p, st) : sum_launch<Bf16, 1>(p, st));
+}
+
+}  // extern "C"

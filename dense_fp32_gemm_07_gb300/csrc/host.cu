@@ -20,6 +20,7 @@
 #include "ptx.cuh"
 #include "sgemm_params.h"
 #include "tf32x3.h"
+#include "train_common.cuh"
 #include "transpose.h"
 #include "tune_table.h"
 
@@ -1113,6 +1114,19 @@ int run_tf32x3(const Call& c, void* stream, int variant) {
 
 }  // namespace
 
+int train_device(TrainDevice* out) {
+  DeviceState* d = nullptr;
+  const int rc = device_state(&d);
+  if (rc) return rc;
+  if (cudaGetDevice(&out->dev) != cudaSuccess) return B2G_ERR_DEVICE;
+  out->sms = d->sms, out->status = d->status;
+  out->wait_limit_ns = g_wait_limit_ns.load();
+  out->debug_stop = g_debug_stop.load();
+  return 0;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encoder(); }
+
 int sgemm_min_workspace_bytes(int M, int N, int K, float alpha, const float* A, int lda,
                               const float* B, int ldb, const float* C, int ldc, size_t* bytes) {
   if (!bytes) return B2G_ERR_NULL;
@@ -1318,13 +1332,14 @@ int b2g_status(void* stream, unsigned int* flags, int clear) {
     if (cudaStreamSynchronize(st) != cudaSuccess) return B2G_ERR_CUDA;
   }
   *flags = v;
-  return v ? B2G_ERR_TIMEOUT : 0;
+  if (v & ~kStatusIndex) return B2G_ERR_TIMEOUT;
+  return v ? B2G_ERR_INDEX : 0;
 }
 
 int b2g_sgemm_debug_status(void* stream) {
   unsigned int flags = 0;
   const int rc = b2g_status(stream, &flags, 0);
-  if (rc && rc != B2G_ERR_TIMEOUT) return rc;
+  if (rc && rc != B2G_ERR_TIMEOUT && rc != B2G_ERR_INDEX) return rc;
   return (int)(flags & 0x7fffffffu);
 }
 
@@ -1354,6 +1369,9 @@ const char* b2g_strerror(int code) {
     case B2G_ERR_TIMEOUT: return "a kernel's bounded wait ran out (see b2g_status flags)";
     case B2G_ERR_SCRATCH_LIMIT:
       return "the call needs more scratch than b2g_sgemm_noalloc's fixed array holds";
+    case B2G_ERR_INVALID_TYPE: return "unknown element type or index width";
+    case B2G_ERR_WORKSPACE: return "the workspace is missing, misaligned or too small";
+    case B2G_ERR_INDEX: return "an id or target was out of range (see b2g_status flags)";
     default: return "unknown error code";
   }
 }

@@ -271,8 +271,10 @@ int b2g_plan_info(int plan, int* info);
  * Synchronises `stream`, then stores the flags in *flags (0 = none; bit 0 a
  * consumer timed out waiting for data, bit 1 a producer timed out waiting for
  * a free stage, bit 2 a producer timed out waiting for its own copies, bit 3
- * the tensor-core path timed out waiting for its MMAs).  clear != 0 resets the
- * word.  Returns 0, B2G_ERR_TIMEOUT when a flag is set, or B2G_ERR_CUDA.
+ * the tensor-core path timed out waiting for its MMAs, bit 16 an id or target
+ * of a b2g_train.h call was outside its table).  clear != 0 resets the
+ * word.  Returns 0, B2G_ERR_TIMEOUT when a timeout flag is set, B2G_ERR_INDEX
+ * (b2g_train.h) when bit 16 alone is, or B2G_ERR_CUDA.
  */
 int b2g_status(void* stream, unsigned int* flags, int clear);
 

@@ -1,0 +1,190 @@
+"""include/b2g_train.h: every declared call is exported, and the argument checks
+answer with the documented codes before anything reaches a device.  The
+pointers below are never dereferenced."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "b2g_train.h")
+P = 0x100000  # an aligned address
+
+
+@pytest.fixture(scope="module")
+def b2g():
+    from dense_fp32_gemm_07_gb300 import build
+
+    build.build()
+    import dense_fp32_gemm_07_gb300 as pkg
+
+    pkg.train_library()
+    return pkg
+
+
+@pytest.fixture(scope="module")
+def lib(b2g):
+    return b2g.train_library()
+
+
+def test_declared_calls_are_exported(b2g):
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(b2g_\w+)\s*\(", text)))
+    assert names == sorted(b2g.TRAIN_EXPORTS)
+    raw = ctypes.CDLL(b2g.LIB_PATH)
+    assert all(hasattr(raw, n) for n in names)
+
+
+def test_codes_match_header(b2g):
+    for name, val in re.findall(r"#define (B2G_\w+) \(?(-?\d+)\)?", open(HEADER).read()):
+        assert getattr(b2g, name) == int(val), name
+        if int(val) < 0:
+            assert b2g.b2g_strerror(int(val)) != "unknown error code"
+
+
+def size(query, *args):
+    n = ctypes.c_size_t(99)
+    return query(*args, ctypes.byref(n)), n.value
+
+
+@pytest.mark.parametrize("change,code", [
+    ({"dtype": 2}, -12), ({"rows": -1}, -1), ({"cols": -1}, -1), ({"eps": -1.0}, -1),
+    ({"eps": float("nan")}, -1), ({"ldx": 7}, -2), ({"ldy": 7}, -2), ({"x": None}, -3),
+    ({"y": None}, -3), ({"rows": 0, "x": None}, 0), ({"cols": 0, "x": None}, 0),
+    ({"rows": 1 << 31}, -1),
+])
+def test_layernorm_arguments(lib, change, code):
+    a = dict(dtype=0, rows=4, cols=8, x=P, ldx=8, w=P, b=P, eps=1e-5, y=P, ldy=8, mean=P, rstd=P,
+             stream=0)
+    a.update(change)
+    assert lib.b2g_layernorm(*a.values()) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    ({"dtype": -1}, -12), ({"rows": -1}, -1), ({"lddy": 7}, -2), ({"ldx": 7}, -2),
+    ({"lddx": 7}, -2), ({"dy": None}, -3), ({"mean": None}, -3), ({"dx": None}, -3),
+    ({"cols": 0}, 0), ({"rows": 0, "dw": None, "db": None}, 0),
+])
+def test_layernorm_backward_arguments(lib, change, code):
+    a = dict(dtype=0, rows=4, cols=8, dy=P, lddy=8, x=P, ldx=8, w=P, mean=P, rstd=P, dx=P, lddx=8,
+             dw=P, db=P, ws=P, bytes=1 << 20, stream=0)
+    a.update(change)
+    assert lib.b2g_layernorm_backward(*a.values()) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    ({"dtype": 3}, -12), ({"id_bytes": 2}, -12), ({"tokens": -1}, -1), ({"vocab": -1}, -1),
+    ({"width": -1}, -1), ({"ldt": 7}, -2), ({"ldo": 7}, -2), ({"ids": None}, -3),
+    ({"out": None}, -3), ({"tokens": 0, "ids": None}, 0), ({"width": 0}, 0),
+    ({"tokens": (1 << 30) + 1}, -1),
+])
+def test_embedding_arguments(lib, change, code):
+    a = dict(dtype=0, tokens=4, vocab=10, width=8, ids=P, id_bytes=8, table=P, ldt=8, scale=1.0,
+             out=P, ldo=8, stream=0)
+    a.update(change)
+    assert lib.b2g_embedding(*a.values()) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    ({"dtype": 3}, -12), ({"id_bytes": 1}, -12), ({"tokens": -1}, -1), ({"ldd": 7}, -2),
+    ({"ldt": 7}, -2), ({"dtable": None}, -3), ({"ids": None}, -3), ({"vocab": 0}, 0),
+    ({"width": 0}, 0), ({"tokens": 0, "acc": 1}, 0),
+])
+def test_embedding_backward_arguments(lib, change, code):
+    a = dict(dtype=0, tokens=4, vocab=10, width=8, ids=P, id_bytes=8, dout=P, ldd=8, scale=1.0,
+             pad=-1, acc=0, dtable=P, ldt=8, ws=P, bytes=1 << 30, stream=0)
+    a.update(change)
+    assert lib.b2g_embedding_backward(*a.values()) == code
+
+
+def test_clip_arguments(lib):
+    one, n = (ctypes.c_void_p * 1)(P), (ctypes.c_longlong * 1)(5)
+    neg, null = (ctypes.c_longlong * 1)(-5), (ctypes.c_void_p * 1)(None)
+    clip, norm = lib.b2g_clip_grad_norm, lib.b2g_grad_norm
+    assert norm(7, 1, one, n, P, P, 1 << 20, 0) == -12
+    assert norm(0, -1, one, n, P, P, 1 << 20, 0) == -1
+    assert norm(0, 1, one, neg, P, P, 1 << 20, 0) == -1
+    assert norm(0, 1, null, n, P, P, 1 << 20, 0) == -3
+    assert norm(0, 1, None, n, P, P, 1 << 20, 0) == -3
+    assert norm(0, 1, one, n, None, P, 1 << 20, 0) == -3
+    assert clip(0, 1, one, n, -1.0, one, P, P, 1 << 20, 0) == -1
+    assert clip(0, 1, one, n, float("nan"), one, P, P, 1 << 20, 0) == -1
+    assert clip(0, 1, one, n, 1.0, None, P, P, 1 << 20, 0) == -3
+    assert clip(0, 1, one, n, 1.0, null, P, P, 1 << 20, 0) == -3
+
+
+def test_workspace_queries(lib):
+    assert size(lib.b2g_layernorm_backward_workspace_size, 5, 4, 8)[0] == -12
+    assert lib.b2g_layernorm_backward_workspace_size(0, 4, 8, None) == -3
+    rc, n = size(lib.b2g_layernorm_backward_workspace_size, 0, 4, 8)
+    assert rc == 0 and n >= 2 * 8 * 4 and n % 64 == 0  # whole pairs of partial rows
+    assert size(lib.b2g_embedding_backward_workspace_size, 0, 0, 10, 8) == (0, 0)
+    rc, n = size(lib.b2g_embedding_backward_workspace_size, 1, 1000, 10, 8)
+    assert rc == 0 and n > 4 * 4 * 1000  # two copies of ids and places, counts, partial rows
+    lens = (ctypes.c_longlong * 3)(1, 0, 1 << 40)
+    rc, n = size(lib.b2g_grad_norm_workspace_size, 0, 3, lens)
+    assert rc == 0 and 4 <= n <= 4 * 152 * 4 * 4
+    assert size(lib.b2g_grad_norm_workspace_size, 0, 0, None) == (0, 4)
+
+
+def test_no_gpu_means_loud_failure(lib):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    n = (ctypes.c_longlong * 1)(5)
+    one = (ctypes.c_void_p * 1)(P)
+    assert lib.b2g_layernorm(0, 4, 8, P, 8, P, P, 1e-5, P, 8, P, P, 0) == -5
+    assert lib.b2g_embedding(0, 4, 10, 8, P, 8, P, 8, 1.0, P, 8, 0) == -5
+    assert lib.b2g_grad_norm(0, 1, one, n, P, P, 1 << 20, 0) == -5
+
+
+def test_tensor_calls_refuse(b2g):
+    f = torch.zeros(4, 8)
+    with pytest.raises(TypeError):
+        b2g.layer_norm(f)  # not on a GPU
+    with pytest.raises(TypeError):
+        b2g.layer_norm(f.half())
+    with pytest.raises(TypeError):
+        b2g.embedding(torch.zeros(3), f)
+    with pytest.raises(ValueError):
+        b2g.clip_grad_norm([f], -1.0)
+    with pytest.raises(ValueError):
+        b2g.grad_norm([])
+
+
+@pytest.mark.gpu
+def test_tensor_calls_refuse_on_gpu(b2g):
+    x = torch.zeros(6, 8, device="cuda")
+    ids = torch.zeros(6, dtype=torch.int64, device="cuda")
+    bad = [
+        lambda: b2g.layer_norm(x.t()), lambda: b2g.layer_norm(x, x[0, :7]),
+        lambda: b2g.layer_norm(x, out=x[:3]), lambda: b2g.layer_norm(x[:4], out=x[1:5]),
+        lambda: b2g.layer_norm(x[0].expand(6, 8)),
+        lambda: b2g.layer_norm_backward(x, x, None, x[:, 0], x[:, 0]),
+        lambda: b2g.layer_norm_backward(x[:5], x, None, x[0, :6], x[0, :6]),
+        lambda: b2g.embedding(ids[::2], x), lambda: b2g.embedding(ids, x, out=x),
+        lambda: b2g.embedding_backward(ids[:5], x, 10),
+        lambda: b2g.embedding_backward(ids, x, 10, accumulate=True),
+        lambda: b2g.embedding_backward(ids, x, 10, padding_idx=10),
+        lambda: b2g.embedding_backward(ids, x, 6, out=x),
+        lambda: b2g.clip_grad_norm([x.t()], 1.0),
+        lambda: b2g.clip_grad_norm([x], 1.0, out=[x[:5]]),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: b2g.layer_norm(x, x[0].bfloat16()), lambda: b2g.layer_norm(x.double()),
+                 lambda: b2g.embedding(ids.float(), x),
+                 lambda: b2g.grad_norm([x, x.bfloat16()])):
+        with pytest.raises(TypeError):
+            call()
+    n = ctypes.c_size_t(0)
+    lib = b2g.train_library()
+    args = (0, 6, 8, x.data_ptr(), 8, x.data_ptr(), 8, None, x.data_ptr(), x.data_ptr(),
+            x.data_ptr(), 8, x.data_ptr(), None)
+    assert lib.b2g_layernorm_backward(*args, None, 0, 0) == b2g.B2G_ERR_WORKSPACE
+    lib.b2g_layernorm_backward_workspace_size(0, 6, 8, ctypes.byref(n))
+    ws = torch.empty(n.value + 16, dtype=torch.uint8, device="cuda")
+    assert lib.b2g_layernorm_backward(*args, ws.data_ptr(), n.value - 1, 0) == b2g.B2G_ERR_WORKSPACE
+    assert lib.b2g_layernorm_backward(*args, ws.data_ptr() + 4, n.value, 0) == b2g.B2G_ERR_WORKSPACE
