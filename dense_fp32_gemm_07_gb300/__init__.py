@@ -439,4 +439,4 @@ def plans():
 from .train import (  # noqa: E402
     B2G_BF16, B2G_ERR_INDEX, B2G_ERR_INVALID_TYPE, B2G_ERR_WORKSPACE, B2G_F32, TRAIN_EXPORTS,
     clip_grad_norm, embedding, embedding_backward, grad_norm, layer_norm, layer_norm_backward,
-    train_library)
+    linear_cross_entropy, linear_cross_entropy_backward, train_library)

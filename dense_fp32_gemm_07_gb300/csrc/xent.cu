@@ -1,0 +1,961 @@
+// xent.cu -- softmax cross entropy of a linear layer and its gradients
+// (b2g_linear_xent, b2g_linear_xent_backward in include/b2g_train.h), on the
+// 5th-generation tensor cores.
+//
+// With z = h w^T (tokens x vocab):
+//   forward   lse_i = log sum_j exp z_ij,  loss_i = lse_i - z_{i,t_i}
+//   backward  dz_ij = g_i (exp(z_ij - lse_i) - [j == t_i]),  dh = dz w,  dw = dz^T h
+// z is never stored.  The forward product's epilogue keeps, for each row and
+// each 128 columns, the maximum and the sum of the exponentials below it, which a
+// second kernel joins; the backward pass forms z again for a piece of the
+// vocabulary, turns it into dz on its way out of tensor memory, and multiplies
+// that piece by w and by h.  So a training step costs 8 tokens vocab width
+// operations where one that stores z costs 6, and no tokens x vocab array in
+// FP32.
+//
+// One kernel makes all four products, C = A B^T over k, on 256 x 256 tiles of a
+// CTA pair (tcgen05.mma.cta_group::2, BF16 operands, FP32 accumulators in tensor
+// memory, double buffered).  What differs is which index of an operand is
+// contiguous in memory and what happens to a finished tile:
+//   kStats  h w^T, k = width: row statistics and the target's logit
+//   kDz     h w^T, k = width: dz, rounded to BF16
+//   kProdH  dz w,  k = vocab piece: w's columns contiguous ("MN-major" B)
+//   kProdW  dz^T h, k = tokens: both operands MN-major
+// so no transposed copy of anything is made.  FP32 operands are split into three
+// BF16 planes, x = x0 + x1 + x2 to 24 bits, and the k loop runs over the six
+// plane products whose weight is at least 2^-16 of the largest (the next ones are
+// below FP32's rounding), smallest first; dz is stored as three planes the same
+// way.
+//
+// Bound: the tensor cores (from a few hundred tokens up), or reading w (few
+// tokens).
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "tcgen05.cuh"
+#include "train_common.cuh"
+
+namespace b2g {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // host.cu
+
+namespace {
+
+enum Mode { kStats, kDz, kProdH, kProdW };
+
+constexpr int kTile = 256;       // rows and columns of a pair's tile
+constexpr int kBK = 64;          // k per stage: 128 bytes of BF16
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 8;     // two per tensor-memory quarter, 128 columns each
+constexpr int kThreads = 64 + 32 * kEpiWarps;  // warp 0 copies, warp 1 multiplies
+constexpr uint32_t kATile = 128 * kBK * 2;     // a CTA's 128 rows of A: 16 KB
+constexpr uint32_t kBTile = 128 * kBK * 2;     // its 128 rows of B
+constexpr uint32_t kStageBytes = kATile + kBTile;
+constexpr int kNumBars = 2 * kStages + 5;
+constexpr int kSmemBytes = kStages * kStageBytes + 1024 + kNumBars * 8 + 16;
+constexpr uint32_t kTmemCols = 2 * kTile;
+
+struct XentGemm {
+  int rows, cols;              // extents of the product
+  int tiles_m, tiles_n, group_m, k_tiles;
+  int npairs;                  // plane products: 1 (BF16) or 6 (FP32)
+  int slices;                  // k slices per tile (kProdH, kProdW)
+  unsigned long long wait_limit_ns;
+  int debug_stop;              // >= 0: the copy issuer stops early (timeout test)
+  unsigned int* status;
+  // kStats, kDz
+  const void* target;
+  int id_bytes, vocab;
+  long long ignore;
+  int col0;                    // the class of column 0
+  float2* stat;                // [2 * tiles_n][rows]: maximum, sum of exp(z - maximum)
+  float* zt;                   // the target's logit
+  const float* lse;
+  const float* gloss;
+  Bf16* dz;                    // [planes][rows][dz_ld]
+  long long dz_ld, dz_plane;
+  int planes;
+  // kProdH, kProdW
+  float* part;                 // [slices][rows][part_ld] FP32 sums, or NULL: straight to out
+  long long part_ld, part_slice;
+  const float* carry;          // sums of earlier pieces to add, laid out like part, or NULL
+  void* out;
+  long long ldo;
+  int out_bf16, accumulate, out_vec;
+};
+
+// ---------------------------------------------------------------- tensor core
+
+// kind::f16 with BF16 operands and an FP32 accumulator; A or B MN-major when asked.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4)                                  // D: FP32
+         | (1u << 7) | (1u << 10)                   // A, B: BF16
+         | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16)
+         | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Descriptor of an MN-major operand with the 128-byte swizzle: rows of one k hold
+// 64 consecutive m (or n); groups of 8 k are 1024 bytes apart, blocks of 64 m
+// (one bulk-tensor box of 64 x 64) 8192 bytes.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mnmajor(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(8192 >> 4) << 16;  // leading offset: next 64 m
+  d |= (uint64_t)(1024 >> 4) << 32;  // stride offset: next 8 k
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m, int c0,
+                                                 int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// 128 rows of an operand at (row m0, k block kt, plane) into a 16 KB stage tile.
+template <bool MN>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* m, int m0, int kt,
+                                             int plane, uint32_t bar) {
+  if constexpr (MN) {
+    tma_load_3d_pair(dst, m, m0, kt * kBK, plane, bar);
+    tma_load_3d_pair(dst + 8192, m, m0 + 64, kt * kBK, plane, bar);
+  } else {
+    tma_load_3d_pair(dst, m, kt * kBK, m0, plane, bar);
+  }
+}
+
+// Planes of the i-th product of n: with three planes, the products of planes
+// (a, b) with a + b <= 2, the smallest first.
+__device__ __forceinline__ void plane_pair(int i, int n, int& a, int& b) {
+  a = n == 1 ? 0 : (0x001102 >> (20 - 4 * i)) & 15;
+  b = n == 1 ? 0 : (0x010120 >> (20 - 4 * i)) & 15;
+}
+
+// Unit u: k slice u % slices of tile u / slices; tiles in groups of group_m rows
+// of tiles, so that a wave shares operand rows in L2.
+__device__ __forceinline__ void unit_of(const XentGemm& p, int u, int& tm, int& tn, int& slice) {
+  const int tile = u / p.slices;
+  slice = u - tile * p.slices;
+  const int per_group = p.group_m * p.tiles_n;
+  const int g = tile / per_group, first = g * p.group_m;
+  const int size = min(p.tiles_m - first, p.group_m);
+  const int r = tile - g * per_group;
+  tm = first + r % size;
+  tn = r / size;
+}
+
+__device__ __forceinline__ void slice_range(const XentGemm& p, int slice, int& kt0, int& kt1) {
+  kt0 = (int)((long long)slice * p.k_tiles / p.slices);
+  kt1 = (int)((long long)(slice + 1) * p.k_tiles / p.slices);
+}
+
+// ------------------------------------------------------------------ epilogues
+
+__device__ __forceinline__ long long target_at(const XentGemm& p, int i) {
+  return p.id_bytes == 8 ? static_cast<const long long*>(p.target)[i]
+                         : (long long)static_cast<const int*>(p.target)[i];
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// e^x as the hardware's base-2 exponential (relative error 2^-22) of x log2(e),
+// whose rounding adds |x| 2^-24: x is at most about 0 here, so that error grows
+// only where e^x is small.  Results below 2^-126 become 0.
+__device__ __forceinline__ float exp_f32(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+
+// kStats: running maximum and sum over this warp's 128 columns of row r.
+__device__ __forceinline__ void epi_stats(const XentGemm& p, uint32_t taddr, int r, int n0,
+                                          int part) {
+  float top = -INFINITY, sum = 0.f;
+  const long long t = r < p.rows ? target_at(p, r) : -1;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t v[32];
+    tmem_ld32(taddr + 32 * c, v);
+    tmem_ld_wait();
+    const int n = n0 + 32 * c;
+    const int left = p.cols - n;  // columns past the vocabulary hold zeros: leave them out
+    float best = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j >= left) v[j] = __float_as_uint(-INFINITY);
+      best = fmaxf(best, __uint_as_float(v[j]));
+    }
+    const float now = fmaxf(top, best);
+    const float ref = now == -INFINITY ? 0.f : now;  // a row of -infinity so far
+    sum *= exp_f32(top - ref);
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      s0 += exp_f32(__uint_as_float(v[j]) - ref);
+      s1 += exp_f32(__uint_as_float(v[j + 1]) - ref);
+    }
+    sum += s0 + s1;
+    top = now;
+    if (t >= n && t < n + 32 && t < p.cols) {
+      float z = 0.f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) z = j == (int)(t - n) ? __uint_as_float(v[j]) : z;
+      p.zt[r] = z;
+    }
+  }
+  if (r < p.rows) p.stat[(size_t)part * p.rows + r] = make_float2(top, sum);
+}
+
+// kDz: dz of this warp's 128 columns of row r, as one or three BF16 planes.
+__device__ __forceinline__ void epi_dz(const XentGemm& p, uint32_t taddr, int r, int n0) {
+  float lse = 0.f, g = 0.f;
+  int at = -1;  // the target's column
+  if (r < p.rows) {
+    const long long t = target_at(p, r);
+    const bool in = t >= 0 && t < p.vocab;
+    if (t != p.ignore && in)
+      lse = p.lse[r], g = p.gloss[r];
+    else if (t != p.ignore && n0 == 0 && p.col0 == 0)
+      atomicOr(p.status, kStatusIndex);
+    at = t >= p.col0 && t < (long long)p.col0 + p.cols ? (int)(t - p.col0) : -1;
+  }
+  const bool live = g != 0.f;  // also for a NaN weight
+  Bf16* row = p.dz + (long long)r * p.dz_ld;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t v[32];
+    tmem_ld32(taddr + 32 * c, v);
+    tmem_ld_wait();
+    const int n = n0 + 32 * c;
+    if (r >= p.rows || n >= p.cols) continue;
+    float d[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float e = exp_f32(__uint_as_float(v[j]) - lse) - (n + j == at ? 1.f : 0.f);
+      d[j] = live ? g * e : 0.f;
+    }
+    // rows of dz are padded to 32 columns, so a chunk is always written whole
+#pragma unroll 1
+    for (int pl = 0; pl < p.planes; ++pl) {
+      uint4* q = reinterpret_cast<uint4*>(row + pl * p.dz_plane + n);
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[i] = pack_bf16(d[j + 2 * i], d[j + 2 * i + 1]);
+          // what this plane leaves for the next one (exact)
+          d[j + 2 * i] -= __uint_as_float(w[i] << 16);
+          d[j + 2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+        q[j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+}
+
+// kProdH, kProdW: this warp's 128 columns of row r to the partial sums or the result.
+__device__ __forceinline__ void epi_prod(const XentGemm& p, uint32_t taddr, int r, int n0,
+                                         int slice) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t v[32];
+    tmem_ld32(taddr + 32 * c, v);
+    tmem_ld_wait();
+    const int n = n0 + 32 * c;
+    if (r >= p.rows || n >= p.cols) continue;
+    const size_t at = (size_t)slice * p.part_slice + (size_t)r * p.part_ld + n;
+    if (p.carry) {  // partial rows are padded to 32 columns
+      const float4* q = reinterpret_cast<const float4*>(p.carry + at);
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        const float4 x = q[j / 4];
+        v[j] = __float_as_uint(__uint_as_float(v[j]) + x.x);
+        v[j + 1] = __float_as_uint(__uint_as_float(v[j + 1]) + x.y);
+        v[j + 2] = __float_as_uint(__uint_as_float(v[j + 2]) + x.z);
+        v[j + 3] = __float_as_uint(__uint_as_float(v[j + 3]) + x.w);
+      }
+    }
+    if (p.part) {
+      float4* q = reinterpret_cast<float4*>(p.part + at);
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        q[j / 4] = make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
+                               __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+      continue;
+    }
+    const long long o = (long long)r * p.ldo + n;
+    const bool whole = p.out_vec && n + 32 <= p.cols;
+    if (p.out_bf16) {
+      Bf16* q = static_cast<Bf16*>(p.out) + o;
+      if (whole) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8) {
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[j + i]);
+          Pack<Bf16, 8> k;
+          if (p.accumulate) {
+            float old[8];
+            k.load(q + j);
+            k.get(old);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] += old[i];
+          }
+          k.set(f);
+          k.store(q + j);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (n + j < p.cols)
+            q[j] = __float2bfloat16_rn(__uint_as_float(v[j]) +
+                                       (p.accumulate ? __bfloat162float(q[j]) : 0.f));
+      }
+    } else {
+      float* q = static_cast<float*>(p.out) + o;
+      if (whole) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          float4 x = p.accumulate ? *reinterpret_cast<const float4*>(q + j)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+          x.x += __uint_as_float(v[j]), x.y += __uint_as_float(v[j + 1]);
+          x.z += __uint_as_float(v[j + 2]), x.w += __uint_as_float(v[j + 3]);
+          *reinterpret_cast<float4*>(q + j) = x;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (n + j < p.cols) q[j] = __uint_as_float(v[j]) + (p.accumulate ? q[j] : 0.f);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the kernel
+//
+// CTA r of a pair stages rows 128r .. 128r+127 of the tile's A and of its B and
+// holds rows 128r .. of the accumulator.  Both CTAs' copies of a stage complete
+// on the even CTA's `full` barrier; its warp 1 issues the pair's MMAs and commits
+// "stage read" and "accumulator final" to both CTAs.  Every wait is bounded: on a
+// timeout the kernel flags the status word, waits (bounded) for what it started,
+// frees its tensor memory and returns.
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    xent_gemm_kernel(const __grid_constant__ XentGemm p, const __grid_constant__ CUtensorMap mA,
+                     const __grid_constant__ CUtensorMap mB) {
+  constexpr bool A_MN = MODE == kProdW, B_MN = MODE == kProdH || MODE == kProdW;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;  // 128-byte swizzle atoms: 1024-byte aligned
+  const uint32_t bars = base + kStages * kStageBytes;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (kStages + s); };
+  auto tfull = [&](int a) { return bars + 8u * (2 * kStages + a); };
+  auto tempty = [&](int a) { return bars + 8u * (2 * kStages + 2 + a); };
+  const uint32_t drain = bars + 8u * (2 * kStages + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (base - raw) +
+                                                    kStages * kStageBytes + kNumBars * 8);
+  const uint32_t rank = cluster_ctarank() & 1u;
+  const bool even = rank == 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull(a), 1);
+      mbar_init(tempty(a), 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_addr(tmem_slot), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  cluster_sync();
+  tc_fence_after_sync();
+  pdl_wait();
+  const uint32_t tmem =
+      even ? *tmem_slot : ld_shared_cluster_u32(mapa_shared(smem_addr(tmem_slot), 0));
+  const int units = p.tiles_m * p.tiles_n * p.slices;
+  const int pair = blockIdx.x >> 1, npairs_cta = gridDim.x >> 1;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- copy issuer
+    if (lane == 0) {
+      prefetch_tmap(&mA);
+      prefetch_tmap(&mB);
+      int s = 0, issued = 0;
+      uint32_t ph = 0;
+      for (int u = pair; u < units; u += npairs_cta) {
+        int tm, tn, slice, kt0, kt1;
+        unit_of(p, u, tm, tn, slice);
+        slice_range(p, slice, kt0, kt1);
+        const int ma = tm * kTile + (int)rank * 128, nb = tn * kTile + (int)rank * 128;
+        for (int i = 0; i < p.npairs; ++i) {
+          int pa, pb;
+          plane_pair(i, p.npairs, pa, pb);
+          for (int kt = kt0; kt < kt1; ++kt) {
+            if (p.debug_stop >= 0 && issued >= p.debug_stop) goto copies_done;
+            if (!mbar_wait(empty(s), ph ^ 1u, p.wait_limit_ns, p.status, kStatusTimeoutEmpty))
+              goto copies_done;
+            const uint32_t st = base + s * kStageBytes;
+            if (even) mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
+            const uint32_t fb = even ? full(s) : mapa_shared(full(s), 0);
+            load_operand<A_MN>(st, &mA, ma, kt, pa, fb);
+            load_operand<B_MN>(st + kATile, &mB, nb, kt, pb, fb);
+            ++issued;
+            if (++s == kStages) s = 0, ph ^= 1u;
+          }
+        }
+      }
+    copies_done:
+      // leave only after the copies started here have landed (the odd CTA sees
+      // the MMAs release the stages they read)
+      for (int d = 0, pending = min(issued, kStages); d < pending; ++d) {
+        if (--s < 0) s = kStages - 1, ph ^= 1u;
+        if (!mbar_wait(even ? full(s) : empty(s), ph, p.wait_limit_ns, p.status,
+                       kStatusTimeoutDrain))
+          break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer (even CTA)
+    if (even && lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16(kTile, kTile, A_MN, B_MN);
+      int s = 0, a = 0;
+      uint32_t ph = 0, aph = 0;
+      for (int u = pair; u < units; u += npairs_cta) {
+        int tm, tn, slice, kt0, kt1;
+        unit_of(p, u, tm, tn, slice);
+        slice_range(p, slice, kt0, kt1);
+        if (!mbar_wait(tempty(a), aph ^ 1u, p.wait_limit_ns, p.status, kStatusTimeoutTmem))
+          goto mma_done;
+        tc_fence_after_sync();
+        const uint32_t d = tmem + (uint32_t)(a * kTile);
+        const int steps = p.npairs * (kt1 - kt0);
+        for (int it = 0; it < steps; ++it) {
+          if (!mbar_wait(full(s), ph, p.wait_limit_ns, p.status, kStatusTimeoutFull)) goto mma_done;
+          tc_fence_after_sync();
+          const uint32_t st = base + s * kStageBytes;
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk) {  // 16 k an MMA: 32 bytes of a row, or 16 rows
+            const uint64_t da = A_MN ? smem_desc_sw128_mnmajor(st + kk * 2048u)
+                                     : smem_desc_sw128_kmajor(st + kk * 32u);
+            const uint64_t db = B_MN ? smem_desc_sw128_mnmajor(st + kATile + kk * 2048u)
+                                     : smem_desc_sw128_kmajor(st + kATile + kk * 32u);
+            mma_bf16_pair(d, da, db, idesc, (it > 0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit_pair(empty(s));
+          mma_commit_pair(mapa_shared(empty(s), 1));
+          if (++s == kStages) s = 0, ph ^= 1u;
+        }
+        mma_commit_pair(tfull(a));
+        mma_commit_pair(mapa_shared(tfull(a), 1));
+        if (++a == 2) a = 0, aph ^= 1u;
+      }
+    mma_done:
+      mma_commit_pair(drain);
+      mbar_wait(drain, 0, p.wait_limit_ns, p.status, kStatusTimeoutTmem);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- epilogue
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    int a = 0;
+    uint32_t aph = 0;
+    for (int u = pair; u < units; u += npairs_cta) {
+      int tm, tn, slice;
+      unit_of(p, u, tm, tn, slice);
+      if (!mbar_wait(tfull(a), aph, p.wait_limit_ns, p.status, kStatusTimeoutTmem)) break;
+      tc_fence_after_sync();
+      const int r = tm * kTile + (int)rank * 128 + 32 * q + lane;
+      const int n0 = tn * kTile + half * 128;
+      const uint32_t taddr =
+          tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * kTile + half * 128);
+      if constexpr (MODE == kStats)
+        epi_stats(p, taddr, r, n0, tn * 2 + half);
+      else if constexpr (MODE == kDz)
+        epi_dz(p, taddr, r, n0);
+      else
+        epi_prod(p, taddr, r, n0, slice);
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (even)
+          mbar_arrive(tempty(a));
+        else
+          mbar_arrive_remote(mapa_shared(tempty(a), 0));
+      }
+      if (++a == 2) a = 0, aph ^= 1u;
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before_sync();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(*tmem_slot, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- small kernels
+
+// Rows of x as `planes` BF16 planes with rows of ld elements (zeros past cols):
+// plane 0 is x rounded, plane 1 what that leaves rounded, plane 2 the rest (FP32
+// in three planes: 24 bits).  Infinities and NaN stay in plane 0.
+template <typename T>
+__global__ void __launch_bounds__(256) planes_kernel(const T* __restrict__ x, long long ldx,
+                                                     int rows, int cols, Bf16* __restrict__ y,
+                                                     long long ld, long long plane, int planes) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long groups = ld / 8, total = groups * rows;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (long long)gridDim.x * 256) {
+    const long long r = i / groups;
+    const int c = (int)(i - r * groups) * 8;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = c + j < cols ? to_f32(x[r * ldx + c + j]) : 0.f;
+    for (int pl = 0; pl < planes; ++pl) {
+      Pack<Bf16, 8> k;
+      k.set(f);
+      k.store(y + pl * plane + r * ld + c);
+      float g[8];
+      k.get(g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = isfinite(g[j]) ? f[j] - g[j] : 0.f;
+    }
+  }
+}
+
+// lse and loss of 32 rows: thread (x, y) joins the statistics y, y + 32, ... of
+// row x, then warp y == 0 joins the 32 results in order.
+__global__ void __launch_bounds__(1024) xent_join_kernel(const float2* stat, const float* zt,
+                                                         int parts, int rows, const void* target,
+                                                         int id_bytes, long long ignore, int vocab,
+                                                         float* lse, float* loss,
+                                                         unsigned int* status) {
+  __shared__ float2 acc[32][33];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int r = blockIdx.x * 32 + threadIdx.x;
+  float top = -INFINITY, sum = 0.f;
+  auto join = [&](float2 x) {
+    const float now = fmaxf(top, x.x), ref = now == -INFINITY ? 0.f : now;
+    sum = sum * exp_f32(top - ref) + x.y * exp_f32(x.x - ref);
+    top = now;
+  };
+  if (r < rows) {
+#pragma unroll 4
+    for (int i = threadIdx.y; i < parts; i += 32) join(stat[(size_t)i * rows + r]);
+  }
+  acc[threadIdx.y][threadIdx.x] = make_float2(top, sum);
+  __syncthreads();
+  if (threadIdx.y != 0 || r >= rows) return;
+#pragma unroll 4
+  for (int i = 1; i < 32; ++i) join(acc[i][threadIdx.x]);
+  const float l = top + logf(sum);
+  lse[r] = l;
+  const long long t = id_bytes == 8 ? static_cast<const long long*>(target)[r]
+                                    : (long long)static_cast<const int*>(target)[r];
+  const bool in = t >= 0 && t < vocab;
+  if (t != ignore && !in) atomicOr(status, kStatusIndex);
+  if (loss) loss[r] = t == ignore ? 0.f : in ? l - zt[r] : __int_as_float(0x7fc00000);
+}
+
+// out = the slices' sums added in order (plus out when accumulate).
+template <typename T>
+__global__ void __launch_bounds__(256) xent_reduce_kernel(const float* part, int slices,
+                                                          long long part_ld, long long part_slice,
+                                                          int rows, int cols, T* out,
+                                                          long long ldo, int accumulate) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long total = (long long)rows * cols;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (long long)gridDim.x * 256) {
+    const long long r = i / cols;
+    const int c = (int)(i - r * cols);
+    const float* q = part + r * part_ld + c;
+    float s = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < slices; ++k) s += q[k * part_slice];
+    T* o = out + r * ldo + c;
+    *o = from_f32<T>(accumulate ? s + to_f32(*o) : s);
+  }
+}
+
+// ------------------------------------------------------------------- host side
+
+// {inner, outer, planes} BF16 elements with the 128-byte swizzle.
+int encode(CUtensorMap* m, const void* base, long long inner, long long outer, long long ld,
+           int planes, long long plane, int box_outer) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return B2G_ERR_TENSOR_MAP;
+  cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)planes};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, planes > 1 ? (cuuint64_t)plane * 2 : 16};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_outer, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : B2G_ERR_TENSOR_MAP;
+}
+
+// A matrix as BF16 planes: rows x cols, rows ld apart, planes `plane` apart.
+struct Planes {
+  const Bf16* p;
+  int rows, cols;
+  long long ld, plane;
+  int planes;
+};
+int map_k(CUtensorMap* m, const Planes& x) {  // k = the columns
+  return encode(m, x.p, x.cols, x.rows, x.ld, x.planes, x.plane, 128);
+}
+int map_mn(CUtensorMap* m, const Planes& x) {  // k = the rows
+  return encode(m, x.p, x.cols, x.rows, x.ld, x.planes, x.plane, 64);
+}
+
+template <int MODE>
+int resident_pairs(int dev, int sms) {
+  static std::atomic<int> cached[64];
+  if (dev < 0 || dev >= 64) return 0;
+  int pairs = cached[dev].load(std::memory_order_acquire);
+  if (pairs) return pairs;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3((unsigned)(sms & ~1));
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(xent_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmemBytes) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&pairs, xent_gemm_kernel<MODE>, &cfg) != cudaSuccess ||
+      pairs < 1)
+    return 0;
+  cached[dev].store(pairs, std::memory_order_release);
+  return pairs;
+}
+
+// Fills in the tiling and launches one product.
+template <int MODE>
+int launch_gemm(XentGemm p, const CUtensorMap& mA, const CUtensorMap& mB, const TrainDevice& d,
+                cudaStream_t st) {
+  const int pairs = resident_pairs<MODE>(d.dev, d.sms);
+  if (!pairs) return B2G_ERR_CUDA;
+  p.tiles_m = (int)ceil_div(p.rows, kTile), p.tiles_n = (int)ceil_div(p.cols, kTile);
+  p.group_m = 16;
+  p.wait_limit_ns = d.wait_limit_ns, p.debug_stop = d.debug_stop, p.status = d.status;
+  const long long units = (long long)p.tiles_m * p.tiles_n * p.slices;
+  if (units > 0x3fffffffLL) return B2G_ERR_INVALID_DIM;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * (units < pairs ? units : pairs)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  CUtensorMap a = mA, b = mB;
+  void* args[] = {&p, &a, &b};
+  return launch_code(
+      cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&xent_gemm_kernel<MODE>), args));
+}
+
+struct Call {
+  int dtype, tokens, vocab, width;
+  const void* h;
+  long long ldh;
+  const void* w;
+  long long ldw;
+};
+
+int check(const Call& c) {
+  if (!type_ok(c.dtype)) return B2G_ERR_INVALID_TYPE;
+  if (c.tokens < 0 || c.vocab < 1 || c.width < 1) return B2G_ERR_INVALID_DIM;
+  if (c.ldh < c.width || c.ldw < c.width) return B2G_ERR_INVALID_LD;
+  return 0;
+}
+
+// k slices for `tiles` tiles on `pairs` CTA pairs: as many as leave each pair a
+// unit, with at least 8 stages of k each.
+int slices_for(long long tiles, int k_tiles, int pairs) {
+  long long s = pairs / tiles;
+  if (s > k_tiles / 8) s = k_tiles / 8;
+  return s < 1 ? 1 : (int)s;
+}
+
+// dz for one piece of the vocabulary stays below this (the piece is a multiple
+// of 256 classes, at least one).
+constexpr size_t kDzBytes = size_t(512) << 20;
+// The launch shape is planned for this many pairs (GB300: 152 SMs), so that the
+// workspace query needs no device.
+constexpr int kPlanPairs = 76;
+
+struct Layout {
+  int planes;
+  bool copy_h, copy_w;
+  long long ldc;                     // row length of the copies
+  size_t h, w, stat, zt, dz, hpart, wpart, total;
+  int piece, pieces;                 // classes per piece
+  long long dz_ld, part_ld;
+  int slices_h, slices_w;
+};
+
+Layout layout(const Call& c, bool backward) {
+  Layout l;
+  l.planes = c.dtype == B2G_F32 ? 3 : 1;
+  l.copy_h = c.dtype == B2G_F32 || !vec16(c.h) || c.ldh % 8;
+  l.copy_w = c.dtype == B2G_F32 || !vec16(c.w) || c.ldw % 8;
+  l.ldc = (long long)round_up(c.width, 8);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += round_up(bytes, 256);
+    return o;
+  };
+  l.h = l.copy_h ? take((size_t)l.planes * c.tokens * l.ldc * 2) : 0;
+  l.w = l.copy_w ? take((size_t)l.planes * c.vocab * l.ldc * 2) : 0;
+  l.stat = l.zt = l.dz = l.hpart = l.wpart = 0;
+  l.piece = c.vocab, l.pieces = 1, l.slices_h = l.slices_w = 1;
+  if (!backward) {
+    l.stat = take((size_t)2 * ceil_div(c.vocab, kTile) * c.tokens * sizeof(float2));
+    l.zt = take((size_t)c.tokens * sizeof(float));
+  } else {
+    const long long fit = (long long)(kDzBytes / ((size_t)l.planes * c.tokens * 2)) / kTile * kTile;
+    const long long most = fit < kTile ? kTile : fit;
+    l.pieces = (int)ceil_div(c.vocab, most);
+    l.piece = (int)round_up((size_t)ceil_div(c.vocab, l.pieces), kTile);
+    l.pieces = (int)ceil_div(c.vocab, l.piece);
+    l.dz_ld = (long long)round_up(l.piece, 32);
+    l.part_ld = (long long)round_up(c.width, 32);
+    const long long nt = ceil_div(c.width, kTile);
+    l.slices_h = slices_for(ceil_div(c.tokens, kTile) * nt,
+                            (int)ceil_div(l.piece < c.vocab ? l.piece : c.vocab, kBK), kPlanPairs);
+    l.slices_w = slices_for(ceil_div(l.piece, kTile) * nt, (int)ceil_div(c.tokens, kBK), kPlanPairs);
+    l.dz = take((size_t)l.planes * c.tokens * l.dz_ld * 2);
+    if (l.slices_h > 1 || l.pieces > 1)
+      l.hpart = take((size_t)l.slices_h * c.tokens * l.part_ld * 4);
+    if (l.slices_w > 1) l.wpart = take((size_t)l.slices_w * l.piece * l.part_ld * 4);
+  }
+  l.total = at;
+  return l;
+}
+
+// The operand itself, or its planes written to the workspace.
+int planes_of(const void* x, long long ldx, int rows, int cols, int dtype, bool copy, Bf16* to,
+              const Layout& l, const TrainDevice& d, cudaStream_t st, Planes* out) {
+  *out = Planes{static_cast<const Bf16*>(x), rows, cols, ldx, 0, 1};
+  if (!copy) return 0;
+  const long long plane = (long long)rows * l.ldc;
+  *out = Planes{to, rows, cols, l.ldc, plane, l.planes};
+  const long long blocks = ceil_div(l.ldc / 8 * rows, 256), most = 16LL * d.sms;
+  const dim3 grid((unsigned)(blocks < most ? blocks : most));
+  return launch_code(dtype == B2G_F32
+                         ? launch_train(planes_kernel<float>, grid, dim3(256), 0, st,
+                                        static_cast<const float*>(x), ldx, rows, cols, to, l.ldc,
+                                        plane, l.planes)
+                         : launch_train(planes_kernel<Bf16>, grid, dim3(256), 0, st,
+                                        static_cast<const Bf16*>(x), ldx, rows, cols, to, l.ldc,
+                                        plane, l.planes));
+}
+
+template <typename T>
+int reduce(const float* part, int slices, long long ld, long long slice, int rows, int cols,
+           void* out, long long ldo, int accumulate, const TrainDevice& d, cudaStream_t st) {
+  const long long blocks = ceil_div((long long)rows * cols, 256), most = 16LL * d.sms;
+  return launch_code(launch_train(xent_reduce_kernel<T>, dim3((unsigned)(blocks < most ? blocks : most)),
+                                  dim3(256), 0, st, part, slices, ld, slice, rows, cols,
+                                  static_cast<T*>(out), ldo, accumulate));
+}
+
+}  // namespace
+}  // namespace b2g
+
+using namespace b2g;
+
+extern "C" {
+
+int b2g_linear_xent_workspace_size(int dtype, int tokens, int vocab, int width, const void* h,
+                                   long long ldh, const void* w, long long ldw, int backward,
+                                   size_t* bytes) {
+  const Call c{dtype, tokens, vocab, width, h, ldh, w, ldw};
+  const int rc = check(c);
+  if (rc) return rc;
+  if (!bytes) return B2G_ERR_NULL;
+  *bytes = tokens ? layout(c, backward != 0).total : 0;
+  return 0;
+}
+
+int b2g_linear_xent(int dtype, int tokens, int vocab, int width, const void* h, long long ldh,
+                    const void* w, long long ldw, const void* target, int id_bytes,
+                    long long ignore_index, float* loss, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  const Call c{dtype, tokens, vocab, width, h, ldh, w, ldw};
+  int rc = check(c);
+  if (rc) return rc;
+  if (id_bytes != 8 && id_bytes != 4) return B2G_ERR_INVALID_TYPE;
+  if (tokens == 0) return 0;
+  if (!h || !w || !target || !lse) return B2G_ERR_NULL;
+  TrainDevice d;
+  rc = train_device(&d);
+  if (rc) return rc;
+  const Layout l = layout(c, false);
+  if (!workspace || !vec16(workspace) || workspace_bytes < l.total) return B2G_ERR_WORKSPACE;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  Planes ph, pw;
+  rc = planes_of(h, ldh, tokens, width, dtype, l.copy_h, reinterpret_cast<Bf16*>(ws + l.h), l, d,
+                 st, &ph);
+  if (!rc)
+    rc = planes_of(w, ldw, vocab, width, dtype, l.copy_w, reinterpret_cast<Bf16*>(ws + l.w), l, d,
+                   st, &pw);
+  CUtensorMap mh, mw;
+  if (!rc) rc = map_k(&mh, ph);
+  if (!rc) rc = map_k(&mw, pw);
+  if (rc) return rc;
+  XentGemm p = {};
+  p.rows = tokens, p.cols = vocab;
+  p.k_tiles = (int)ceil_div(width, kBK), p.npairs = l.planes == 3 ? 6 : 1, p.slices = 1;
+  p.target = target, p.id_bytes = id_bytes, p.vocab = vocab, p.ignore = ignore_index;
+  p.stat = reinterpret_cast<float2*>(ws + l.stat);
+  p.zt = reinterpret_cast<float*>(ws + l.zt);
+  rc = launch_gemm<kStats>(p, mh, mw, d, st);
+  if (rc) return rc;
+  return launch_code(launch_train(xent_join_kernel, dim3((unsigned)ceil_div(tokens, 32)),
+                                  dim3(32, 32), 0, st, (const float2*)p.stat, (const float*)p.zt,
+                                  (int)(2 * ceil_div(vocab, kTile)), tokens, target, id_bytes,
+                                  ignore_index, vocab, lse, loss, d.status));
+}
+
+int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const void* h,
+                             long long ldh, const void* w, long long ldw, const void* target,
+                             int id_bytes, long long ignore_index, const float* lse,
+                             const float* grad_loss, void* dh, long long lddh, int accumulate,
+                             void* dw, long long lddw, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  const Call c{dtype, tokens, vocab, width, h, ldh, w, ldw};
+  int rc = check(c);
+  if (rc) return rc;
+  if (id_bytes != 8 && id_bytes != 4) return B2G_ERR_INVALID_TYPE;
+  if ((dh && lddh < width) || (dw && lddw < width)) return B2G_ERR_INVALID_LD;
+  if (tokens == 0 && (!dw || accumulate)) return 0;
+  if (!dh && !dw) return 0;
+  if (tokens > 0 && (!h || !w || !target || !lse || !grad_loss)) return B2G_ERR_NULL;
+  TrainDevice d;
+  rc = train_device(&d);
+  if (rc) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const long long es = (long long)type_size(dtype);
+  if (tokens == 0)
+    return cudaMemset2DAsync(dw, lddw * es, 0, width * es, vocab, st) == cudaSuccess ? 0
+                                                                                    : B2G_ERR_CUDA;
+  const Layout l = layout(c, true);
+  if (!workspace || !vec16(workspace) || workspace_bytes < l.total) return B2G_ERR_WORKSPACE;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  Planes ph, pw;
+  rc = planes_of(h, ldh, tokens, width, dtype, l.copy_h, reinterpret_cast<Bf16*>(ws + l.h), l, d,
+                 st, &ph);
+  if (!rc)
+    rc = planes_of(w, ldw, vocab, width, dtype, l.copy_w, reinterpret_cast<Bf16*>(ws + l.w), l, d,
+                   st, &pw);
+  if (rc) return rc;
+  XentGemm base = {};
+  base.npairs = l.planes == 3 ? 6 : 1, base.slices = 1;
+  base.out_bf16 = dtype == B2G_BF16;
+  float* hpart = l.slices_h > 1 || l.pieces > 1 ? reinterpret_cast<float*>(ws + l.hpart) : nullptr;
+  const long long hslice = (long long)tokens * l.part_ld;
+  for (int i = 0; i < l.pieces; ++i) {
+    const int first = i * l.piece;
+    const int n = vocab - first < l.piece ? vocab - first : l.piece;
+    Planes piece = pw;
+    piece.p += (long long)first * pw.ld, piece.rows = n;
+    const Planes dz{reinterpret_cast<Bf16*>(ws + l.dz), tokens, n, l.dz_ld,
+                    (long long)tokens * l.dz_ld, l.planes};
+    CUtensorMap a, b;
+    // dz of these classes
+    XentGemm p = base;
+    p.rows = tokens, p.cols = n, p.k_tiles = (int)ceil_div(width, kBK);
+    p.target = target, p.id_bytes = id_bytes, p.vocab = vocab, p.ignore = ignore_index;
+    p.col0 = first, p.lse = lse, p.gloss = grad_loss;
+    p.dz = const_cast<Bf16*>(dz.p), p.dz_ld = dz.ld, p.dz_plane = dz.plane, p.planes = l.planes;
+    rc = map_k(&a, ph);
+    if (!rc) rc = map_k(&b, piece);
+    if (!rc) rc = launch_gemm<kDz>(p, a, b, d, st);
+    if (rc) return rc;
+    if (dh) {  // dh += dz w over these classes
+      p = base;
+      p.rows = tokens, p.cols = width, p.k_tiles = (int)ceil_div(n, kBK);
+      p.slices = l.slices_h < p.k_tiles ? l.slices_h : p.k_tiles;
+      p.part_ld = l.part_ld, p.part_slice = hslice;
+      p.carry = i ? hpart : nullptr;
+      p.part = l.slices_h > 1 || i + 1 < l.pieces ? hpart : nullptr;
+      p.out = dh, p.ldo = lddh;
+      p.out_vec = vec16(dh) && vec16_ld(lddh, dtype);
+      rc = map_k(&a, dz);
+      if (!rc) rc = map_mn(&b, piece);
+      if (!rc) rc = launch_gemm<kProdH>(p, a, b, d, st);
+      if (rc) return rc;
+    }
+    if (dw) {  // these classes' rows of dw = dz^T h
+      p = base;
+      p.rows = n, p.cols = width, p.k_tiles = (int)ceil_div(tokens, kBK);
+      p.slices = l.slices_w;
+      float* wpart = l.slices_w > 1 ? reinterpret_cast<float*>(ws + l.wpart) : nullptr;
+      unsigned char* out = static_cast<unsigned char*>(dw) + (long long)first * lddw * es;
+      p.part = wpart, p.part_ld = l.part_ld, p.part_slice = (long long)l.piece * l.part_ld;
+      p.out = out, p.ldo = lddw, p.accumulate = accumulate != 0;
+      p.out_vec = vec16(out) && vec16_ld(lddw, dtype);
+      rc = map_mn(&a, dz);
+      if (!rc) rc = map_mn(&b, ph);
+      if (!rc) rc = launch_gemm<kProdW>(p, a, b, d, st);
+      if (!rc && wpart)
+        rc = (dtype == B2G_F32 ? reduce<float> : reduce<Bf16>)(
+            wpart, l.slices_w, l.part_ld, p.part_slice, n, width, out, lddw, p.accumulate, d, st);
+      if (rc) return rc;
+    }
+  }
+  if (dh && l.slices_h > 1)
+    return (dtype == B2G_F32 ? reduce<float> : reduce<Bf16>)(hpart, l.slices_h, l.part_ld, hslice,
+                                                             tokens, width, dh, lddh, 0, d, st);
+  return 0;
+}
+
+}  // extern "C"

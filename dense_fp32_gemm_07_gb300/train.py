@@ -1,5 +1,6 @@
 """Training-step operators beside the SGEMM (include/b2g_train.h): layer norm,
-embedding, clipping by the gradient norm.
+embedding, softmax cross entropy of a linear layer, clipping by the gradient
+norm.
 
 Tensor-level calls on float32 or bfloat16 CUDA tensors.  Every step runs in the
 CUDA library; torch supplies device memory (results and workspaces, from its
@@ -28,6 +29,7 @@ B2G_ERR_INDEX = -14
 TRAIN_EXPORTS = (
     "b2g_layernorm", "b2g_layernorm_backward", "b2g_layernorm_backward_workspace_size",
     "b2g_embedding", "b2g_embedding_backward", "b2g_embedding_backward_workspace_size",
+    "b2g_linear_xent", "b2g_linear_xent_backward", "b2g_linear_xent_workspace_size",
     "b2g_grad_norm", "b2g_clip_grad_norm", "b2g_grad_norm_workspace_size",
 )
 
@@ -54,6 +56,10 @@ def train_library():
     lib.b2g_embedding_backward.argtypes = [i, ll, i, i, vp, i, vp, ll, f, ll, i, vp, ll, vp, sz,
                                            vp]
     lib.b2g_embedding_backward_workspace_size.argtypes = [i, ll, i, i, psz]
+    lib.b2g_linear_xent.argtypes = [i, i, i, i, vp, ll, vp, ll, vp, i, ll, vp, vp, vp, sz, vp]
+    lib.b2g_linear_xent_backward.argtypes = [i, i, i, i, vp, ll, vp, ll, vp, i, ll, vp, vp, vp,
+                                             ll, i, vp, ll, vp, sz, vp]
+    lib.b2g_linear_xent_workspace_size.argtypes = [i, i, i, i, vp, ll, vp, ll, i, psz]
     lib.b2g_grad_norm.argtypes = [i, i, vp, vp, vp, vp, sz, vp]
     lib.b2g_clip_grad_norm.argtypes = [i, i, vp, vp, f, vp, vp, vp, sz, vp]
     lib.b2g_grad_norm_workspace_size.argtypes = [i, i, vp, psz]
@@ -304,6 +310,64 @@ def embedding_backward(ids, dout, num_rows: int, scale: float = 1.0, out=None,
                                       int(accumulate), out.data_ptr(), ldt, p, nb, on.handle))
     on.uses(ids, dout, out)
     return out
+
+
+# --------------------------------------------------------------- cross entropy
+
+def linear_cross_entropy(h, w, target, ignore_index: int = -100, stream=None):
+    """(loss, lse) per row of the logits h @ w.T, which are never stored.
+
+    h is tokens x width, w vocab x width, target a vector of class numbers.
+    loss_i = lse_i - logit_{i, target_i}, 0 where target_i is ignore_index; lse is
+    the log of the sum of the exponentials.  Both are float32 vectors."""
+    lib = train_library()
+    torch = _t()
+    code, n, d, ldh = _matrix(h, "h")
+    _, v, dw, ldw = _matrix(w, "w", h)
+    pt, nt, width = _indices(target, "target", h)
+    if dw != d or nt != n:
+        raise ValueError(f"shape mismatch: h {n}x{d}, w {v}x{dw}, target {nt}")
+    on = _On(stream)
+    loss = on.empty((n,), torch.float32, h.device)
+    lse = on.empty((n,), torch.float32, h.device)
+    ws, p, nb = _workspace(on, h.device, lib.b2g_linear_xent_workspace_size, code, n, v, d,
+                           h.data_ptr(), ldh, w.data_ptr(), ldw, 0)
+    _raise(lib.b2g_linear_xent(code, n, v, d, h.data_ptr(), ldh, w.data_ptr(), ldw, pt, width,
+                               ignore_index, loss.data_ptr(), lse.data_ptr(), p, nb, on.handle))
+    on.uses(h, w, target)
+    return loss, lse
+
+
+def linear_cross_entropy_backward(h, w, target, lse, grad_loss, ignore_index: int = -100,
+                                  dw=None, accumulate: bool = False, stream=None):
+    """(dh, dw): gradients of (grad_loss * loss).sum() for `linear_cross_entropy`.
+
+    lse is the forward call's; grad_loss a float32 vector, one weight per row
+    (1 / n for a mean over n rows).  `dw` takes the head's gradient; with
+    `accumulate` it is added to the values there."""
+    lib = train_library()
+    code, n, d, ldh = _matrix(h, "h")
+    _, v, dh_, ldw = _matrix(w, "w", h)
+    pt, nt, width = _indices(target, "target", h)
+    if dh_ != d or nt != n:
+        raise ValueError(f"shape mismatch: h {n}x{d}, w {v}x{dh_}, target {nt}")
+    pl, pg = _floats(lse, "lse", n, h), _floats(grad_loss, "grad_loss", n, h)
+    on = _On(stream)
+    if dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs dw")
+        dw, lddw = on.empty((v, d), h.dtype, h.device), max(1, d)
+    else:
+        lddw = _result(dw, "dw", (v, d), h)
+        _apart(dw, ("h", h), ("w", w))
+    dh = on.empty((n, d), h.dtype, h.device)
+    ws, p, nb = _workspace(on, h.device, lib.b2g_linear_xent_workspace_size, code, n, v, d,
+                           h.data_ptr(), ldh, w.data_ptr(), ldw, 1)
+    _raise(lib.b2g_linear_xent_backward(
+        code, n, v, d, h.data_ptr(), ldh, w.data_ptr(), ldw, pt, width, ignore_index, pl, pg,
+        dh.data_ptr(), max(1, d), int(accumulate), dw.data_ptr(), lddw, p, nb, on.handle))
+    on.uses(h, w, target, lse, grad_loss, dw)
+    return dh, dw
 
 
 # ------------------------------------------------------------- gradient clipping

@@ -1,7 +1,8 @@
 /*
  * b2g_train.h -- C ABI of the operators that a language model's training and
  * scoring steps run around their matrix products: layer norm, embedding
- * lookup, and clipping by the global gradient norm.  Part of the library behind b2g_sgemm.h, with its rules:
+ * lookup, softmax cross entropy of a linear layer, and clipping by the global
+ * gradient norm.  Part of the library behind b2g_sgemm.h, with its rules:
  * DEVICE pointers owned by the caller, row-major operands with leading
  * dimensions in elements, calls that are asynchronous on `stream` (a
  * cudaStream_t, NULL = the legacy default stream), thread-safe, and a 0 or a
@@ -98,6 +99,55 @@ int b2g_embedding_backward(int dtype, long long tokens, int vocab, int width, co
                            void* workspace, size_t workspace_bytes, void* stream);
 int b2g_embedding_backward_workspace_size(int dtype, long long tokens, int vocab, int width,
                                           size_t* bytes);
+
+/*
+ * Softmax cross entropy of a linear layer, without storing its logits.  With
+ * z = h * w^T (tokens x vocab, FP32):
+ *     lse_i = log(sum_j exp(z_ij)),   loss_i = lse_i - z_{i, target_i}.
+ *   h       tokens x width, ldh.   w  vocab x width, ldw (the head, one row per class).
+ *   target  `tokens` class numbers, id_bytes 8 or 4 as for b2g_embedding.
+ *           ignore_index rows get loss 0; any other target outside [0, vocab)
+ *           gets loss NaN and sets the status word's bit 16.
+ *   loss    `tokens` FP32 values, or NULL.   lse  `tokens` FP32 values.
+ * tokens == 0 launches nothing; vocab and width are at least 1, else
+ * B2G_ERR_INVALID_DIM.
+ * BF16 operands are multiplied exactly and summed in FP32; FP32 operands are
+ * split into three BF16 pieces each, whose six leading products carry 24 bits.
+ */
+int b2g_linear_xent(int dtype, int tokens, int vocab, int width, const void* h, long long ldh,
+                    const void* w, long long ldw, const void* target, int id_bytes,
+                    long long ignore_index, float* loss, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of sum_i grad_loss_i * loss_i.  With
+ *     dz_ij = grad_loss_i * (exp(z_ij - lse_i) - [j == target_i])
+ * (zero in rows whose target is ignore_index or out of range, whatever lse_i is),
+ *     dh = dz * w,   dw = dz^T * h  (plus dw's previous value when accumulate != 0).
+ * z is computed again, a piece of the vocabulary at a time; dz exists for one
+ * piece at a time, rounded to BF16 (BF16 operands) or held in three BF16 pieces
+ * (FP32 operands) for the two products.
+ * A row without a gradient still enters dw as 0 * h_i, so its h must be finite.
+ *   lse        what b2g_linear_xent stored.   grad_loss  `tokens` FP32 values.
+ *   dh         tokens x width, lddh, or NULL.   dw  vocab x width, lddw, or NULL.
+ */
+int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const void* h,
+                             long long ldh, const void* w, long long ldw, const void* target,
+                             int id_bytes, long long ignore_index, const float* lse,
+                             const float* grad_loss, void* dh, long long lddh, int accumulate,
+                             void* dw, long long lddw, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * Workspace bytes of b2g_linear_xent (backward == 0) or
+ * b2g_linear_xent_backward (backward != 0) for these arguments.  h and w are
+ * inspected for their alignment only: BF16 operands that are not on 16-byte
+ * boundaries (base or leading dimension) are copied into the workspace first,
+ * FP32 operands always (as BF16 pieces).
+ */
+int b2g_linear_xent_workspace_size(int dtype, int tokens, int vocab, int width, const void* h,
+                                   long long ldh, const void* w, long long ldw, int backward,
+                                   size_t* bytes);
 
 /*
  * The 2-norm of all elements of `count` tensors together, sqrt(sum x^2), in

@@ -99,6 +99,32 @@ def test_embedding_backward_arguments(lib, change, code):
     assert lib.b2g_embedding_backward(*a.values()) == code
 
 
+@pytest.mark.parametrize("change,code", [
+    ({"dtype": 3}, -12), ({"id_bytes": 1}, -12), ({"tokens": -1}, -1), ({"vocab": 0}, -1),
+    ({"width": 0}, -1), ({"ldh": 7}, -2), ({"ldw": 7}, -2), ({"h": None}, -3), ({"w": None}, -3),
+    ({"target": None}, -3), ({"lse": None}, -3), ({"tokens": 0, "h": None}, 0),
+])
+def test_linear_xent_arguments(lib, change, code):
+    a = dict(dtype=1, tokens=4, vocab=10, width=8, h=P, ldh=8, w=P, ldw=8, target=P, id_bytes=8,
+             ignore=-100, loss=P, lse=P, ws=P, bytes=1 << 30, stream=0)
+    a.update(change)
+    assert lib.b2g_linear_xent(*a.values()) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    ({"dtype": 3}, -12), ({"id_bytes": 1}, -12), ({"tokens": -1}, -1), ({"vocab": 0}, -1),
+    ({"ldh": 7}, -2), ({"ldw": 7}, -2), ({"lddh": 7}, -2), ({"lddw": 7}, -2), ({"h": None}, -3),
+    ({"lse": None}, -3), ({"gloss": None}, -3), ({"dh": None, "dw": None}, 0),
+    ({"tokens": 0, "acc": 1}, 0), ({"tokens": 0, "dw": None}, 0),
+])
+def test_linear_xent_backward_arguments(lib, change, code):
+    a = dict(dtype=1, tokens=4, vocab=10, width=8, h=P, ldh=8, w=P, ldw=8, target=P, id_bytes=8,
+             ignore=-100, lse=P, gloss=P, dh=P, lddh=8, acc=0, dw=P, lddw=8, ws=P, bytes=1 << 30,
+             stream=0)
+    a.update(change)
+    assert lib.b2g_linear_xent_backward(*a.values()) == code
+
+
 def test_clip_arguments(lib):
     one, n = (ctypes.c_void_p * 1)(P), (ctypes.c_longlong * 1)(5)
     neg, null = (ctypes.c_longlong * 1)(-5), (ctypes.c_void_p * 1)(None)
@@ -123,6 +149,17 @@ def test_workspace_queries(lib):
     assert size(lib.b2g_embedding_backward_workspace_size, 0, 0, 10, 8) == (0, 0)
     rc, n = size(lib.b2g_embedding_backward_workspace_size, 1, 1000, 10, 8)
     assert rc == 0 and n > 4 * 4 * 1000  # two copies of ids and places, counts, partial rows
+    q = lib.b2g_linear_xent_workspace_size
+    assert size(q, 1, 4, 10, 0, P, 8, P, 8, 0)[0] == -1 and q(1, 4, 10, 8, P, 8, P, 8, 0, None) == -3
+    assert size(q, 1, 0, 10, 8, P, 8, P, 8, 1) == (0, 0)
+    fwd = size(q, 1, 64, 1000, 128, P, 128, P, 128, 0)[1]
+    assert 0 < fwd < 64 * 1000 * 4          # less than the logits
+    # an operand off the 16-byte boundaries is copied, FP32 ones become three planes
+    assert size(q, 1, 64, 1000, 128, P, 128, P + 2, 128, 0)[1] == fwd + 1000 * 128 * 2
+    assert size(q, 0, 64, 1000, 128, P, 128, P, 128, 0)[1] == fwd + 3 * 1064 * 128 * 2
+    # dz exists a piece at a time: a larger vocabulary needs no more room for it
+    big = [size(q, 1, 8192, v, 512, P, 512, P, 512, 1)[1] for v in (65536, 1 << 20)]
+    assert big[1] <= big[0] < (1 << 30)
     lens = (ctypes.c_longlong * 3)(1, 0, 1 << 40)
     rc, n = size(lib.b2g_grad_norm_workspace_size, 0, 3, lens)
     assert rc == 0 and 4 <= n <= 4 * 152 * 4 * 4
@@ -137,6 +174,7 @@ def test_no_gpu_means_loud_failure(lib):
     assert lib.b2g_layernorm(0, 4, 8, P, 8, P, P, 1e-5, P, 8, P, P, 0) == -5
     assert lib.b2g_embedding(0, 4, 10, 8, P, 8, P, 8, 1.0, P, 8, 0) == -5
     assert lib.b2g_grad_norm(0, 1, one, n, P, P, 1 << 20, 0) == -5
+    assert lib.b2g_linear_xent(1, 4, 10, 8, P, 8, P, 8, P, 8, -100, P, P, P, 1 << 30, 0) == -5
 
 
 def test_tensor_calls_refuse(b2g):
@@ -168,6 +206,11 @@ def test_tensor_calls_refuse_on_gpu(b2g):
         lambda: b2g.embedding_backward(ids, x, 10, accumulate=True),
         lambda: b2g.embedding_backward(ids, x, 10, padding_idx=10),
         lambda: b2g.embedding_backward(ids, x, 6, out=x),
+        lambda: b2g.linear_cross_entropy(x, x[:, :7], ids),
+        lambda: b2g.linear_cross_entropy(x, x, ids[:5]),
+        lambda: b2g.linear_cross_entropy_backward(x, x, ids, x[0, :6], x[0, :5]),
+        lambda: b2g.linear_cross_entropy_backward(x, x, ids, x[0, :6], x[0, :6], dw=x),
+        lambda: b2g.linear_cross_entropy_backward(x, x, ids, x[0, :6], x[0, :6], accumulate=True),
         lambda: b2g.clip_grad_norm([x.t()], 1.0),
         lambda: b2g.clip_grad_norm([x], 1.0, out=[x[:5]]),
     ]
