@@ -75,13 +75,18 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
         k[u].zero();
         if (v + u * kThreads < vecs) k[u].load(q + (v + u * kThreads) * VEC);
       }
+      // these squares first among themselves, so that few rounded additions
+      // reach the long sum
+      float s[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         float f[VEC];
         k[u].get(f);
+        s[u] = f[0] * f[0];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) sum = fmaf(f[j], f[j], sum);
+        for (int j = 1; j < VEC; ++j) s[u] = fmaf(f[j], f[j], s[u]);
       }
+      sum += (s[0] + s[1]) + (s[2] + s[3]);
     }
     const int tail = head + vecs * VEC;
     int e = threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;

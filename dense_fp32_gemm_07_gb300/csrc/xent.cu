@@ -44,23 +44,32 @@ namespace {
 
 enum Mode { kStats, kDz, kProdH, kProdW };
 
-constexpr int kTile = 256;       // rows and columns of a pair's tile
+constexpr int kTile = 256;       // rows and (at most) columns of a pair's tile
 constexpr int kBK = 64;          // k per stage: 128 bytes of BF16
 constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;     // two per tensor-memory quarter, 128 columns each
-constexpr int kThreads = 64 + 32 * kEpiWarps;  // warp 0 copies, warp 1 multiplies
+constexpr int kThreads = 128 + 32 * kEpiWarps;  // warp 0 copies, warp 1 multiplies, 2 and 3 idle
+// Registers: the block starts with 168 a thread (64,512 of the SM's 65,536); the
+// first warpgroup gives up its share so that the epilogue's threads can hold 128
+// sums each: 128 * 64 + 256 * 216 = 63,488.
+constexpr int kIssueRegs = 64, kEpiRegs = 216;
 constexpr uint32_t kATile = 128 * kBK * 2;     // a CTA's 128 rows of A: 16 KB
 constexpr uint32_t kBTile = 128 * kBK * 2;     // its 128 rows of B
 constexpr uint32_t kStageBytes = kATile + kBTile;
 constexpr int kNumBars = 2 * kStages + 5;
-constexpr int kSmemBytes = kStages * kStageBytes + 1024 + kNumBars * 8 + 16;
+constexpr uint32_t kOutBytes = 4096;           // an epilogue warp's 32 rows of 128 bytes on their way out
+constexpr int kSmemBytes =
+    kStages * kStageBytes + kEpiWarps * kOutBytes + 1024 + kNumBars * 8 + 16;
 constexpr uint32_t kTmemCols = 2 * kTile;
 
 struct XentGemm {
   int rows, cols;              // extents of the product
   int tiles_m, tiles_n, group_m, k_tiles;
+  int tile_n;                  // columns of a tile, at most 256
+  uint32_t stage_tx;           // bytes a CTA's copies bring to a stage
   int npairs;                  // plane products: 1 (BF16) or 6 (FP32)
   int slices;                  // k slices per tile (kProdH, kProdW)
+  int group;                   // stages that add up in tensor memory before FP32 takes over
   unsigned long long wait_limit_ns;
   int debug_stop;              // >= 0: the copy issuer stops early (timeout test)
   unsigned int* status;
@@ -69,20 +78,20 @@ struct XentGemm {
   int id_bytes, vocab;
   long long ignore;
   int col0;                    // the class of column 0
-  float2* stat;                // [2 * tiles_n][rows]: maximum, sum of exp(z - maximum)
+  float2* stat;                // [parts][rows]: maximum, sum of exp(z - maximum); a part is
+                               // (up to) 128 columns of a tile
   float* zt;                   // the target's logit
   const float* lse;
   const float* gloss;
-  Bf16* dz;                    // [planes][rows][dz_ld]
-  long long dz_ld, dz_plane;
-  int planes;
+  float* scale;                // the largest weight: written by kDz, read by kProdH and kProdW
+  int planes;                  // BF16 planes of dz
   // kProdH, kProdW
-  float* part;                 // [slices][rows][part_ld] FP32 sums, or NULL: straight to out
-  long long part_ld, part_slice;
-  const float* carry;          // sums of earlier pieces to add, laid out like part, or NULL
+  int to_part;                 // mOut is [slices][rows][..] FP32 sums
+  int add;                     // to_part: add to what is there
+  int out_tma;                 // mOut is the result; else `out` is written element by element
   void* out;
   long long ldo;
-  int out_bf16, accumulate, out_vec;
+  int out_bf16, accumulate;
 };
 
 // ---------------------------------------------------------------- tensor core
@@ -127,6 +136,21 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
+// mbar_wait without a function call: registers are redistributed among the warps
+// here, and a called function would have to fit the smallest share.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const XentGemm& p,
+                                           unsigned int flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_ns() - t0 > p.wait_limit_ns) {
+      atomicOr(p.status, flag);
+      return false;
+    }
+  }
+  return true;
+}
+
 // 128 rows of an operand at (row m0, k block kt, plane) into a 16 KB stage tile.
 template <bool MN>
 __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* m, int m0, int kt,
@@ -164,6 +188,25 @@ __device__ __forceinline__ void slice_range(const XentGemm& p, int slice, int& k
   kt1 = (int)((long long)(slice + 1) * p.k_tiles / p.slices);
 }
 
+// The unit's stages in order are npairs passes over the k tiles; its accumulation
+// groups are runs of `group` stages in the last pass (the leading planes) and of
+// 16 * group in the passes before it, whose terms are 2^-8 of the last one's.  The
+// tensor core truncates when it adds to its FP32 accumulator, which over a long k
+// would add up to a bias of steps * 2^-24; a group bounds that, and the groups are
+// added in registers, rounded to nearest.
+__device__ __forceinline__ int small_stages(const XentGemm& p, int kts) {
+  return (p.npairs - 1) * kts;
+}
+__device__ __forceinline__ int groups_of(const XentGemm& p, int kts) {
+  const int big = 16 * p.group;
+  return (small_stages(p, kts) + big - 1) / big + (kts + p.group - 1) / p.group;
+}
+// Stages of group g.
+__device__ __forceinline__ int group_stages(const XentGemm& p, int kts, int g) {
+  const int big = 16 * p.group, small = small_stages(p, kts), n = (small + big - 1) / big;
+  return g < n ? min(big, small - g * big) : min(p.group, kts - (g - n) * p.group);
+}
+
 // ------------------------------------------------------------------ epilogues
 
 __device__ __forceinline__ long long target_at(const XentGemm& p, int i) {
@@ -185,174 +228,247 @@ __device__ __forceinline__ float exp_f32(float x) {
   return y;
 }
 
-// kStats: running maximum and sum over this warp's 128 columns of row r.
-__device__ __forceinline__ void epi_stats(const XentGemm& p, uint32_t taddr, int r, int n0,
-                                          int part) {
-  float top = -INFINITY, sum = 0.f;
-  const long long t = r < p.rows ? target_at(p, r) : -1;
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t v[32];
-    tmem_ld32(taddr + 32 * c, v);
-    tmem_ld_wait();
-    const int n = n0 + 32 * c;
-    const int left = p.cols - n;  // columns past the vocabulary hold zeros: leave them out
-    float best = -INFINITY;
+// v (plus the old values) to up to 128 columns of a result row, for
+// results that a bulk-tensor store cannot write (alignment) or add to (BF16).
+template <typename T>
+__device__ __forceinline__ void put_row(T* q, const float (&v)[128], int left,
+                                        int accumulate) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (j >= left) v[j] = __float_as_uint(-INFINITY);
-      best = fmaxf(best, __uint_as_float(v[j]));
-    }
-    const float now = fmaxf(top, best);
-    const float ref = now == -INFINITY ? 0.f : now;  // a row of -infinity so far
-    sum *= exp_f32(top - ref);
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      s0 += exp_f32(__uint_as_float(v[j]) - ref);
-      s1 += exp_f32(__uint_as_float(v[j + 1]) - ref);
-    }
-    sum += s0 + s1;
-    top = now;
-    if (t >= n && t < n + 32 && t < p.cols) {
-      float z = 0.f;
-#pragma unroll
-      for (int j = 0; j < 32; ++j) z = j == (int)(t - n) ? __uint_as_float(v[j]) : z;
-      p.zt[r] = z;
-    }
-  }
-  if (r < p.rows) p.stat[(size_t)part * p.rows + r] = make_float2(top, sum);
+  for (int j = 0; j < 128; ++j)
+    if (j < left) q[j] = from_f32<T>(accumulate ? v[j] + to_f32(q[j]) : v[j]);
 }
 
-// kDz: dz of this warp's 128 columns of row r, as one or three BF16 planes.
-__device__ __forceinline__ void epi_dz(const XentGemm& p, uint32_t taddr, int r, int n0) {
+// The loads into v are complete; tying v to the wait keeps its uses behind it.
+__device__ __forceinline__ void tie32(uint32_t (&v)[32]) {
+  asm volatile(""
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])::"memory");
+}
+
+// This warp's 128 columns of the accumulators that `tfull` announces, added up
+// over the unit's accumulation groups: acc holds FP32 sums rounded to nearest.
+// Two loads are in flight at a time.  Returns false when a wait ran out.
+__device__ __forceinline__ bool collect(const XentGemm& p, float (&acc)[128], uint32_t tmem_lane,
+                                        int groups, int& a, uint32_t& aph, uint32_t tfull0,
+                                        uint32_t tempty0, uint32_t tempty0_even, bool even,
+                                        int lane) {
+  for (int g = 0; g < groups; ++g) {
+    if (!wait_phase(tfull0 + 8u * a, aph, p, kStatusTimeoutTmem)) return false;
+    tc_fence_after_sync();
+#pragma unroll
+    for (int c = 0; c < 128; c += 64) {
+      uint32_t v[32], w[32];
+      tmem_ld32(tmem_lane + (uint32_t)(a * kTile + c), v);
+      tmem_ld32(tmem_lane + (uint32_t)(a * kTile + c + 32), w);
+      tmem_ld_wait();
+      tie32(v);
+      tie32(w);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        acc[c + j] = g == 0 ? __uint_as_float(v[j]) : acc[c + j] + __uint_as_float(v[j]);
+        acc[c + 32 + j] = g == 0 ? __uint_as_float(w[j]) : acc[c + 32 + j] + __uint_as_float(w[j]);
+      }
+    }
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) {  // the tile may be overwritten
+      if (even)
+        mbar_arrive(tempty0 + 8u * a);
+      else
+        mbar_arrive_remote(tempty0_even + 8u * a);
+    }
+    if (++a == 2) a = 0, aph ^= 1u;
+  }
+  return true;
+}
+
+// A warp's 32 rows of 128 bytes through its shared-memory buffer to (x, y, z) of
+// an output tensor: eight 16-byte pieces a lane, in the 128-byte swizzle (no bank
+// conflicts, and full lines leave the SM), then one bulk-tensor store, which
+// leaves out rows and columns past the tensor.
+__device__ __forceinline__ void store_rows(uint32_t buf, const CUtensorMap* m, int x, int y, int z,
+                                           const uint4 (&w)[8], bool add, int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();  // the buffer's last store has been read
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t at = buf + lane * 128u + (uint32_t)((i ^ (lane & 7)) * 16);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[i].x), "r"(w[i].y),
+                 "r"(w[i].z), "r"(w[i].w)
+                 : "memory");
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (add)
+      asm volatile(
+          "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
+          " [%0, {%1, %2, %3}], [%4];" ::"l"(reinterpret_cast<uint64_t>(m)),
+          "r"(x), "r"(y), "r"(z), "r"(buf)
+          : "memory");
+    else
+      asm volatile(
+          "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group"
+          " [%0, {%1, %2, %3}], [%4];" ::"l"(reinterpret_cast<uint64_t>(m)),
+          "r"(x), "r"(y), "r"(z), "r"(buf)
+          : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
+// Before the block ends: the stores of this thread have been written.
+__device__ __forceinline__ void stores_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// kStats: maximum and sum over this warp's `left` columns (at most 128) of row r.
+__device__ __forceinline__ void epi_stats(const XentGemm& p, float (&z)[128], int r, int n0,
+                                          int left, int part) {
+  if (r >= p.rows) return;
+  if (left < 128) {
+#pragma unroll
+    for (int j = 0; j < 128; ++j)
+      if (j >= left) z[j] = -INFINITY;
+  }
+  const long long t = target_at(p, r);
+  if (t >= n0 && t < (long long)n0 + left) {
+    const int at = (int)(t - n0);
+    float zt = 0.f;
+#pragma unroll
+    for (int j = 0; j < 128; ++j) zt = j == at ? z[j] : zt;
+    p.zt[r] = zt;
+  }
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int j = 0; j < 128; ++j) m[j & 3] = fmaxf(m[j & 3], z[j]);
+  const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  const float ref = top == -INFINITY ? 0.f : top;  // a row of -infinity
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 128; ++j) s[j & 3] += exp_f32(z[j] - ref);
+  p.stat[(size_t)part * p.rows + r] = make_float2(top, (s[0] + s[1]) + (s[2] + s[3]));
+}
+
+// kDz: dz of this warp's columns of row r = row0 + lane, divided by the largest
+// weight, as one or three BF16 planes.  The division keeps a mean's equal weights
+// out of the rounding to BF16 (a factor 1/n would shift all of them alike, by up
+// to 2^-8).
+__device__ __forceinline__ void epi_dz(const XentGemm& p, float (&z)[128], int row0, int lane,
+                                       int n0, int left, float inv_scale, uint32_t buf,
+                                       const CUtensorMap* m) {
+  if (row0 >= p.rows) return;
+  const int r = row0 + lane;
   float lse = 0.f, g = 0.f;
   int at = -1;  // the target's column
   if (r < p.rows) {
     const long long t = target_at(p, r);
     const bool in = t >= 0 && t < p.vocab;
     if (t != p.ignore && in)
-      lse = p.lse[r], g = p.gloss[r];
+      lse = p.lse[r], g = p.gloss[r] * inv_scale;
     else if (t != p.ignore && n0 == 0 && p.col0 == 0)
       atomicOr(p.status, kStatusIndex);
-    at = t >= p.col0 && t < (long long)p.col0 + p.cols ? (int)(t - p.col0) : -1;
+    const long long first = (long long)p.col0 + n0;
+    if (t >= first && t < first + 128) at = (int)(t - first);
   }
   const bool live = g != 0.f;  // also for a NaN weight
-  Bf16* row = p.dz + (long long)r * p.dz_ld;
+#pragma unroll
+  for (int c = 0; c < 128; c += 64) {
+    if (c < left) {
+#pragma unroll
+      for (int j = c; j < c + 64; ++j) {
+        const float e = exp_f32(z[j] - lse) - (j == at ? 1.f : 0.f);
+        z[j] = live ? g * e : 0.f;
+      }
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t v[32];
-    tmem_ld32(taddr + 32 * c, v);
-    tmem_ld_wait();
-    const int n = n0 + 32 * c;
-    if (r >= p.rows || n >= p.cols) continue;
-    float d[32];
+      for (int pl = 0; pl < p.planes; ++pl) {
+        uint4 w[8];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float e = exp_f32(__uint_as_float(v[j]) - lse) - (n + j == at ? 1.f : 0.f);
-      d[j] = live ? g * e : 0.f;
-    }
-    // rows of dz are padded to 32 columns, so a chunk is always written whole
-#pragma unroll 1
-    for (int pl = 0; pl < p.planes; ++pl) {
-      uint4* q = reinterpret_cast<uint4*>(row + pl * p.dz_plane + n);
+        for (int j = 0; j < 8; ++j) {
+          uint32_t b[4];
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = pack_bf16(d[j + 2 * i], d[j + 2 * i + 1]);
-          // what this plane leaves for the next one (exact)
-          d[j + 2 * i] -= __uint_as_float(w[i] << 16);
-          d[j + 2 * i + 1] -= __uint_as_float(w[i] & 0xFFFF0000u);
+          for (int i = 0; i < 4; ++i) {
+            float& lo = z[c + 8 * j + 2 * i];
+            float& hi = z[c + 8 * j + 2 * i + 1];
+            b[i] = pack_bf16(lo, hi);
+            // what this plane leaves for the next one (exact)
+            lo -= __uint_as_float(b[i] << 16);
+            hi -= __uint_as_float(b[i] & 0xFFFF0000u);
+          }
+          w[j] = make_uint4(b[0], b[1], b[2], b[3]);
         }
-        q[j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+        store_rows(buf, m, n0 + c, row0, pl, w, false, lane);
       }
     }
   }
 }
 
-// kProdH, kProdW: this warp's 128 columns of row r to the partial sums or the result.
-__device__ __forceinline__ void epi_prod(const XentGemm& p, uint32_t taddr, int r, int n0,
-                                         int slice) {
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t v[32];
-    tmem_ld32(taddr + 32 * c, v);
-    tmem_ld_wait();
-    const int n = n0 + 32 * c;
-    if (r >= p.rows || n >= p.cols) continue;
-    const size_t at = (size_t)slice * p.part_slice + (size_t)r * p.part_ld + n;
-    if (p.carry) {  // partial rows are padded to 32 columns
-      const float4* q = reinterpret_cast<const float4*>(p.carry + at);
+// The largest finite |weight|, by the block's epilogue threads (`tid` of
+// 32 * kEpiWarps) through `red`.
+__device__ __forceinline__ float largest_weight(const XentGemm& p, float* red, int tid) {
+  float m = 0.f;
+  for (int i = tid; i < p.rows; i += 32 * kEpiWarps) {
+    const float g = fabsf(p.gloss[i]);
+    if (isfinite(g)) m = fmaxf(m, g);
+  }
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 x = q[j / 4];
-        v[j] = __float_as_uint(__uint_as_float(v[j]) + x.x);
-        v[j + 1] = __float_as_uint(__uint_as_float(v[j + 1]) + x.y);
-        v[j + 2] = __float_as_uint(__uint_as_float(v[j + 2]) + x.z);
-        v[j + 3] = __float_as_uint(__uint_as_float(v[j + 3]) + x.w);
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((tid & 31) == 0) red[tid >> 5] = m;
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
+#pragma unroll
+  for (int i = 0; i < kEpiWarps; ++i) m = fmaxf(m, red[i]);
+  return m;
+}
+
+// kProdH, kProdW: this warp's columns of rows row0 .. row0 + 31 to the partial sums
+// or the result.
+__device__ __forceinline__ void epi_prod(const XentGemm& p, float (&v)[128], int row0, int lane,
+                                         int n0, int left, int slice, float scale, uint32_t buf,
+                                         const CUtensorMap* m) {
+  if (row0 >= p.rows) return;
+#pragma unroll
+  for (int j = 0; j < 128; ++j) v[j] *= scale;
+  if (p.to_part || (p.out_tma && !p.out_bf16)) {
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) {
+      if (c < left) {
+        uint4 w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          w[j] = make_uint4(__float_as_uint(v[c + 4 * j]), __float_as_uint(v[c + 4 * j + 1]),
+                            __float_as_uint(v[c + 4 * j + 2]), __float_as_uint(v[c + 4 * j + 3]));
+        store_rows(buf, m, n0 + c, row0, p.to_part ? slice : 0, w, p.add, lane);
       }
     }
-    if (p.part) {
-      float4* q = reinterpret_cast<float4*>(p.part + at);
+  } else if (p.out_tma) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 4)
-        q[j / 4] = make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
-                               __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
-      continue;
-    }
-    const long long o = (long long)r * p.ldo + n;
-    const bool whole = p.out_vec && n + 32 <= p.cols;
-    if (p.out_bf16) {
-      Bf16* q = static_cast<Bf16*>(p.out) + o;
-      if (whole) {
+    for (int c = 0; c < 128; c += 64) {
+      if (c < left) {
+        uint4 w[8];
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          float f[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[j + i]);
-          Pack<Bf16, 8> k;
-          if (p.accumulate) {
-            float old[8];
-            k.load(q + j);
-            k.get(old);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] += old[i];
-          }
-          k.set(f);
-          k.store(q + j);
+        for (int j = 0; j < 8; ++j) {
+          const int i = c + 8 * j;
+          w[j] = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
+                            pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (n + j < p.cols)
-            q[j] = __float2bfloat16_rn(__uint_as_float(v[j]) +
-                                       (p.accumulate ? __bfloat162float(q[j]) : 0.f));
-      }
-    } else {
-      float* q = static_cast<float*>(p.out) + o;
-      if (whole) {
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          float4 x = p.accumulate ? *reinterpret_cast<const float4*>(q + j)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-          x.x += __uint_as_float(v[j]), x.y += __uint_as_float(v[j + 1]);
-          x.z += __uint_as_float(v[j + 2]), x.w += __uint_as_float(v[j + 3]);
-          *reinterpret_cast<float4*>(q + j) = x;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (n + j < p.cols) q[j] = __uint_as_float(v[j]) + (p.accumulate ? q[j] : 0.f);
+        store_rows(buf, m, n0 + c, row0, 0, w, false, lane);
       }
     }
+  } else if (row0 + lane < p.rows) {
+    const long long o = (long long)(row0 + lane) * p.ldo + n0;
+    if (p.out_bf16)
+      put_row(static_cast<Bf16*>(p.out) + o, v, left, p.accumulate);
+    else
+      put_row(static_cast<float*>(p.out) + o, v, left, p.accumulate);
   }
 }
 
 // ------------------------------------------------------------------ the kernel
 //
-// CTA r of a pair stages rows 128r .. 128r+127 of the tile's A and of its B and
+// CTA r of a pair stages rows 128r .. 128r+127 of the tile's A and half of its B and
 // holds rows 128r .. of the accumulator.  Both CTAs' copies of a stage complete
 // on the even CTA's `full` barrier; its warp 1 issues the pair's MMAs and commits
 // "stage read" and "accumulator final" to both CTAs.  Every wait is bounded: on a
@@ -361,19 +477,22 @@ __device__ __forceinline__ void epi_prod(const XentGemm& p, uint32_t taddr, int 
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     xent_gemm_kernel(const __grid_constant__ XentGemm p, const __grid_constant__ CUtensorMap mA,
-                     const __grid_constant__ CUtensorMap mB) {
+                     const __grid_constant__ CUtensorMap mB,
+                     const __grid_constant__ CUtensorMap mOut) {
   constexpr bool A_MN = MODE == kProdW, B_MN = MODE == kProdH || MODE == kProdW;
   extern __shared__ unsigned char smem_raw[];
+  __shared__ float wred[kEpiWarps];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // 128-byte swizzle atoms: 1024-byte aligned
-  const uint32_t bars = base + kStages * kStageBytes;
+  const uint32_t outs = base + kStages * kStageBytes;  // the epilogue warps' buffers
+  const uint32_t bars = outs + kEpiWarps * kOutBytes;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (kStages + s); };
   auto tfull = [&](int a) { return bars + 8u * (2 * kStages + a); };
   auto tempty = [&](int a) { return bars + 8u * (2 * kStages + 2 + a); };
   const uint32_t drain = bars + 8u * (2 * kStages + 4);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (base - raw) +
-                                                    kStages * kStageBytes + kNumBars * 8);
+  uint32_t* tmem_slot =
+      reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + kNumBars * 8);
   const uint32_t rank = cluster_ctarank() & 1u;
   const bool even = rank == 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -405,6 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int units = p.tiles_m * p.tiles_n * p.slices;
   const int pair = blockIdx.x >> 1, npairs_cta = gridDim.x >> 1;
 
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
   if (warp == 0) {
     // ---------------------------------------------------------- copy issuer
     if (lane == 0) {
@@ -416,16 +537,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         int tm, tn, slice, kt0, kt1;
         unit_of(p, u, tm, tn, slice);
         slice_range(p, slice, kt0, kt1);
-        const int ma = tm * kTile + (int)rank * 128, nb = tn * kTile + (int)rank * 128;
+        const int ma = tm * kTile + (int)rank * 128, nb = tn * p.tile_n + (int)rank * (p.tile_n / 2);
         for (int i = 0; i < p.npairs; ++i) {
           int pa, pb;
           plane_pair(i, p.npairs, pa, pb);
           for (int kt = kt0; kt < kt1; ++kt) {
             if (p.debug_stop >= 0 && issued >= p.debug_stop) goto copies_done;
-            if (!mbar_wait(empty(s), ph ^ 1u, p.wait_limit_ns, p.status, kStatusTimeoutEmpty))
+            if (!wait_phase(empty(s), ph ^ 1u, p, kStatusTimeoutEmpty))
               goto copies_done;
             const uint32_t st = base + s * kStageBytes;
-            if (even) mbar_arrive_expect_tx(full(s), 2 * kStageBytes);
+            if (even) mbar_arrive_expect_tx(full(s), 2 * p.stage_tx);
             const uint32_t fb = even ? full(s) : mapa_shared(full(s), 0);
             load_operand<A_MN>(st, &mA, ma, kt, pa, fb);
             load_operand<B_MN>(st + kATile, &mB, nb, kt, pb, fb);
@@ -439,8 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the MMAs release the stages they read)
       for (int d = 0, pending = min(issued, kStages); d < pending; ++d) {
         if (--s < 0) s = kStages - 1, ph ^= 1u;
-        if (!mbar_wait(even ? full(s) : empty(s), ph, p.wait_limit_ns, p.status,
-                       kStatusTimeoutDrain))
+        if (!wait_phase(even ? full(s) : empty(s), ph, p, kStatusTimeoutDrain))
           break;
       }
     }
@@ -448,72 +568,88 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer (even CTA)
     if (even && lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16(kTile, kTile, A_MN, B_MN);
+      const uint32_t idesc = idesc_bf16(kTile, p.tile_n, A_MN, B_MN);
       int s = 0, a = 0;
       uint32_t ph = 0, aph = 0;
       for (int u = pair; u < units; u += npairs_cta) {
         int tm, tn, slice, kt0, kt1;
         unit_of(p, u, tm, tn, slice);
         slice_range(p, slice, kt0, kt1);
-        if (!mbar_wait(tempty(a), aph ^ 1u, p.wait_limit_ns, p.status, kStatusTimeoutTmem))
-          goto mma_done;
-        tc_fence_after_sync();
-        const uint32_t d = tmem + (uint32_t)(a * kTile);
-        const int steps = p.npairs * (kt1 - kt0);
-        for (int it = 0; it < steps; ++it) {
-          if (!mbar_wait(full(s), ph, p.wait_limit_ns, p.status, kStatusTimeoutFull)) goto mma_done;
+        const int groups = groups_of(p, kt1 - kt0);
+        for (int g = 0; g < groups; ++g) {
+          if (!wait_phase(tempty(a), aph ^ 1u, p, kStatusTimeoutTmem))
+            goto mma_done;
           tc_fence_after_sync();
-          const uint32_t st = base + s * kStageBytes;
+          const uint32_t d = tmem + (uint32_t)(a * kTile);
+          const int steps = group_stages(p, kt1 - kt0, g);
+          for (int it = 0; it < steps; ++it) {
+            if (!wait_phase(full(s), ph, p, kStatusTimeoutFull))
+              goto mma_done;
+            tc_fence_after_sync();
+            const uint32_t st = base + s * kStageBytes;
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk) {  // 16 k an MMA: 32 bytes of a row, or 16 rows
-            const uint64_t da = A_MN ? smem_desc_sw128_mnmajor(st + kk * 2048u)
-                                     : smem_desc_sw128_kmajor(st + kk * 32u);
-            const uint64_t db = B_MN ? smem_desc_sw128_mnmajor(st + kATile + kk * 2048u)
-                                     : smem_desc_sw128_kmajor(st + kATile + kk * 32u);
-            mma_bf16_pair(d, da, db, idesc, (it > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < kBK / 16; ++kk) {  // 16 k an MMA: 32 bytes of a row, or 16 rows
+              const uint64_t da = A_MN ? smem_desc_sw128_mnmajor(st + kk * 2048u)
+                                       : smem_desc_sw128_kmajor(st + kk * 32u);
+              const uint64_t db = B_MN ? smem_desc_sw128_mnmajor(st + kATile + kk * 2048u)
+                                       : smem_desc_sw128_kmajor(st + kATile + kk * 32u);
+              mma_bf16_pair(d, da, db, idesc, (it > 0 || kk > 0) ? 1u : 0u);
+            }
+            mma_commit_pair(empty(s));
+            mma_commit_pair(mapa_shared(empty(s), 1));
+            if (++s == kStages) s = 0, ph ^= 1u;
           }
-          mma_commit_pair(empty(s));
-          mma_commit_pair(mapa_shared(empty(s), 1));
-          if (++s == kStages) s = 0, ph ^= 1u;
+          mma_commit_pair(tfull(a));
+          mma_commit_pair(mapa_shared(tfull(a), 1));
+          if (++a == 2) a = 0, aph ^= 1u;
         }
-        mma_commit_pair(tfull(a));
-        mma_commit_pair(mapa_shared(tfull(a), 1));
-        if (++a == 2) a = 0, aph ^= 1u;
       }
     mma_done:
       mma_commit_pair(drain);
-      mbar_wait(drain, 0, p.wait_limit_ns, p.status, kStatusTimeoutTmem);
+      wait_phase(drain, 0, p, kStatusTimeoutTmem);
     }
     __syncwarp();
+  }
   } else {
     // ---------------------------------------------------------- epilogue
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t tmem_lane = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * 128);
+    const uint32_t buf = outs + (uint32_t)(warp - 4) * kOutBytes;
+    const uint32_t tempty_even = even ? 0u : mapa_shared(tempty(0), 0);
+    float scale = 1.f;
+    if constexpr (MODE == kDz) {
+      scale = largest_weight(p, wred, threadIdx.x - 128);
+      if (blockIdx.x == 0 && threadIdx.x == 128) *p.scale = scale;
+      scale = scale > 0.f ? 1.f / scale : 0.f;
+    } else if constexpr (MODE != kStats) {
+      scale = *p.scale;
+    }
     int a = 0;
     uint32_t aph = 0;
     for (int u = pair; u < units; u += npairs_cta) {
-      int tm, tn, slice;
+      int tm, tn, slice, kt0, kt1;
       unit_of(p, u, tm, tn, slice);
-      if (!mbar_wait(tfull(a), aph, p.wait_limit_ns, p.status, kStatusTimeoutTmem)) break;
-      tc_fence_after_sync();
-      const int r = tm * kTile + (int)rank * 128 + 32 * q + lane;
-      const int n0 = tn * kTile + half * 128;
-      const uint32_t taddr =
-          tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(a * kTile + half * 128);
-      if constexpr (MODE == kStats)
-        epi_stats(p, taddr, r, n0, tn * 2 + half);
-      else if constexpr (MODE == kDz)
-        epi_dz(p, taddr, r, n0);
-      else
-        epi_prod(p, taddr, r, n0, slice);
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        if (even)
-          mbar_arrive(tempty(a));
+      slice_range(p, slice, kt0, kt1);
+      float acc[128];
+      if (!collect(p, acc, tmem_lane, groups_of(p, kt1 - kt0), a, aph, tfull(0), tempty(0),
+                   tempty_even, even, lane))
+        break;
+      const int row0 = tm * kTile + (int)rank * 128 + 32 * q;
+      const int n0 = tn * p.tile_n + half * 128;
+      // this warp's columns of the tile that exist (none in the second half of a narrow tile)
+      const int left = min(min(p.tile_n - half * 128, 128), p.cols - n0);
+      if (left > 0) {
+        if constexpr (MODE == kStats)
+          epi_stats(p, acc, row0 + lane, n0, left, p.tile_n > 128 ? 2 * tn + half : tn);
+        else if constexpr (MODE == kDz)
+          epi_dz(p, acc, row0, lane, n0, left, scale, buf, &mOut);
         else
-          mbar_arrive_remote(mapa_shared(tempty(a), 0));
+          epi_prod(p, acc, row0, lane, n0, left, slice, scale, buf, &mOut);
       }
-      if (++a == 2) a = 0, aph ^= 1u;
+    }
+    if constexpr (MODE != kStats) {
+      if (lane == 0) stores_done();
     }
   }
 
@@ -616,19 +752,22 @@ __global__ void __launch_bounds__(256) xent_reduce_kernel(const float* part, int
 
 // ------------------------------------------------------------------- host side
 
-// {inner, outer, planes} BF16 elements with the 128-byte swizzle.
-int encode(CUtensorMap* m, const void* base, long long inner, long long outer, long long ld,
-           int planes, long long plane, int box_outer) {
+// {inner, outer, planes} BF16 or FP32 elements, boxes of 128 bytes x box_outer
+// rows with the 128-byte swizzle; ld and plane in elements.
+int encode(CUtensorMap* m, bool f32, const void* base, long long inner, long long outer,
+           long long ld, int planes, long long plane, int box_outer) {
   auto enc = tensor_map_encoder();
   if (!enc) return B2G_ERR_TENSOR_MAP;
+  const cuuint64_t es = f32 ? 4 : 2;
   cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)planes};
-  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, planes > 1 ? (cuuint64_t)plane * 2 : 16};
-  cuuint32_t box[3] = {64, (cuuint32_t)box_outer, 1};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * es, planes > 1 ? (cuuint64_t)plane * es : 16};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)box_outer, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r =
-      enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? 0 : B2G_ERR_TENSOR_MAP;
 }
 
@@ -639,11 +778,47 @@ struct Planes {
   long long ld, plane;
   int planes;
 };
-int map_k(CUtensorMap* m, const Planes& x) {  // k = the columns
-  return encode(m, x.p, x.cols, x.rows, x.ld, x.planes, x.plane, 128);
+// As an operand whose k runs along the columns, `box` rows a copy; as one whose k
+// runs along the rows; and as the output of 32-row stores.
+int map_k(CUtensorMap* m, const Planes& x, int box) {
+  return encode(m, false, x.p, x.cols, x.rows, x.ld, x.planes, x.plane, box);
 }
-int map_mn(CUtensorMap* m, const Planes& x) {  // k = the rows
-  return encode(m, x.p, x.cols, x.rows, x.ld, x.planes, x.plane, 64);
+int map_mn(CUtensorMap* m, const Planes& x) {
+  return encode(m, false, x.p, x.cols, x.rows, x.ld, x.planes, x.plane, 64);
+}
+int map_out(CUtensorMap* m, const Planes& x) {
+  return encode(m, false, x.p, x.cols, x.rows, x.ld, x.planes, x.plane, 32);
+}
+
+// The launch shapes are planned for this many pairs (GB300: 152 SMs), so that the
+// workspace query needs no device.
+constexpr int kPlanPairs = 76;
+
+// Rows of h a CTA copies to a stage: all 128, or fewer where the tokens fit one
+// CTA's half (what its other rows then multiply is never stored).
+int token_box(int tokens) { return tokens >= 128 ? 128 : (int)round_up(tokens, 8); }
+
+// Columns of a tile of h w^T, a multiple of `step`: what makes the pairs' rounds
+// cheapest when a stage costs a CTA's rows of both operands (shared memory and
+// copies, not the MMA, bound a narrower tile).  2048 x 32768 classes: 256; 16
+// tokens: 224 (two full rounds; 256 leaves a quarter of the pairs idle in the
+// second one).
+int choose_tile_n(int tokens, int classes, int step) {
+  const long long tiles_m = ceil_div(tokens, kTile), a = 2 * token_box(tokens);
+  int best = kTile;
+  long long cost = -1;
+  for (int tn = kTile; tn >= 64; tn -= step) {
+    const long long c = ceil_div(tiles_m * ceil_div(classes, tn), kPlanPairs) * (a + tn);
+    if (cost < 0 || c < cost) best = tn, cost = c;
+  }
+  return best;
+}
+
+// The statistics' parts: 128 columns of a tile each, one in a narrow tile.
+int stat_parts(int classes, int tile_n) {
+  const int tiles = (int)ceil_div(classes, tile_n);
+  if (tile_n <= 128) return tiles;
+  return 2 * tiles - (classes - (tiles - 1) * tile_n > 128 ? 0 : 1);
 }
 
 template <int MODE>
@@ -672,11 +847,11 @@ int resident_pairs(int dev, int sms) {
 
 // Fills in the tiling and launches one product.
 template <int MODE>
-int launch_gemm(XentGemm p, const CUtensorMap& mA, const CUtensorMap& mB, const TrainDevice& d,
-                cudaStream_t st) {
+int launch_gemm(XentGemm p, const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mOut,
+                const TrainDevice& d, cudaStream_t st) {
   const int pairs = resident_pairs<MODE>(d.dev, d.sms);
   if (!pairs) return B2G_ERR_CUDA;
-  p.tiles_m = (int)ceil_div(p.rows, kTile), p.tiles_n = (int)ceil_div(p.cols, kTile);
+  p.tiles_m = (int)ceil_div(p.rows, kTile), p.tiles_n = (int)ceil_div(p.cols, p.tile_n);
   p.group_m = 16;
   p.wait_limit_ns = d.wait_limit_ns, p.debug_stop = d.debug_stop, p.status = d.status;
   const long long units = (long long)p.tiles_m * p.tiles_n * p.slices;
@@ -693,11 +868,16 @@ int launch_gemm(XentGemm p, const CUtensorMap& mA, const CUtensorMap& mB, const 
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  CUtensorMap a = mA, b = mB;
-  void* args[] = {&p, &a, &b};
+  CUtensorMap a = mA, b = mB, o = mOut;
+  void* args[] = {&p, &a, &b, &o};
   return launch_code(
       cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&xent_gemm_kernel<MODE>), args));
 }
+
+// Stages of 64 k in one accumulation group: 4 with FP32 operands; 16 for logits of
+// BF16 operands (FP32 results from shorter products); products that are rounded to
+// BF16 do not show the truncation.
+int group_of(int dtype, bool logits) { return dtype == B2G_F32 ? 4 : logits ? 16 : 1 << 20; }
 
 struct Call {
   int dtype, tokens, vocab, width;
@@ -725,18 +905,16 @@ int slices_for(long long tiles, int k_tiles, int pairs) {
 // dz for one piece of the vocabulary stays below this (the piece is a multiple
 // of 256 classes, at least one).
 constexpr size_t kDzBytes = size_t(512) << 20;
-// The launch shape is planned for this many pairs (GB300: 152 SMs), so that the
-// workspace query needs no device.
-constexpr int kPlanPairs = 76;
-
 struct Layout {
   int planes;
   bool copy_h, copy_w;
   long long ldc;                     // row length of the copies
-  size_t h, w, stat, zt, dz, hpart, wpart, total;
+  size_t h, w, stat, zt, scale, dz, hpart, wpart, total;
   int piece, pieces;                 // classes per piece
   long long dz_ld, part_ld;
   int slices_h, slices_w;
+  int tile_n;                        // of h w^T
+  bool h_sums;                       // dh goes through FP32 sums
 };
 
 Layout layout(const Call& c, bool backward) {
@@ -753,10 +931,11 @@ Layout layout(const Call& c, bool backward) {
   };
   l.h = l.copy_h ? take((size_t)l.planes * c.tokens * l.ldc * 2) : 0;
   l.w = l.copy_w ? take((size_t)l.planes * c.vocab * l.ldc * 2) : 0;
-  l.stat = l.zt = l.dz = l.hpart = l.wpart = 0;
-  l.piece = c.vocab, l.pieces = 1, l.slices_h = l.slices_w = 1;
+  l.stat = l.zt = l.scale = l.dz = l.hpart = l.wpart = 0;
+  l.piece = c.vocab, l.pieces = 1, l.slices_h = l.slices_w = 1, l.h_sums = false;
   if (!backward) {
-    l.stat = take((size_t)2 * ceil_div(c.vocab, kTile) * c.tokens * sizeof(float2));
+    l.tile_n = choose_tile_n(c.tokens, c.vocab, 16);
+    l.stat = take((size_t)stat_parts(c.vocab, l.tile_n) * c.tokens * sizeof(float2));
     l.zt = take((size_t)c.tokens * sizeof(float));
   } else {
     const long long fit = (long long)(kDzBytes / ((size_t)l.planes * c.tokens * 2)) / kTile * kTile;
@@ -764,14 +943,17 @@ Layout layout(const Call& c, bool backward) {
     l.pieces = (int)ceil_div(c.vocab, most);
     l.piece = (int)round_up((size_t)ceil_div(c.vocab, l.pieces), kTile);
     l.pieces = (int)ceil_div(c.vocab, l.piece);
-    l.dz_ld = (long long)round_up(l.piece, 32);
-    l.part_ld = (long long)round_up(c.width, 32);
+    l.tile_n = choose_tile_n(c.tokens, l.piece, 64);  // whole 64-column stores
+    l.dz_ld = l.piece;
+    l.part_ld = (long long)round_up(c.width, 4);
     const long long nt = ceil_div(c.width, kTile);
     l.slices_h = slices_for(ceil_div(c.tokens, kTile) * nt,
                             (int)ceil_div(l.piece < c.vocab ? l.piece : c.vocab, kBK), kPlanPairs);
     l.slices_w = slices_for(ceil_div(l.piece, kTile) * nt, (int)ceil_div(c.tokens, kBK), kPlanPairs);
+    l.scale = take(sizeof(float));
     l.dz = take((size_t)l.planes * c.tokens * l.dz_ld * 2);
-    if (l.slices_h > 1 || l.pieces > 1)
+    l.h_sums = l.slices_h > 1 || l.pieces > 1;
+    if (l.h_sums)
       l.hpart = take((size_t)l.slices_h * c.tokens * l.part_ld * 4);
     if (l.slices_w > 1) l.wpart = take((size_t)l.slices_w * l.piece * l.part_ld * 4);
   }
@@ -848,20 +1030,22 @@ int b2g_linear_xent(int dtype, int tokens, int vocab, int width, const void* h, 
     rc = planes_of(w, ldw, vocab, width, dtype, l.copy_w, reinterpret_cast<Bf16*>(ws + l.w), l, d,
                    st, &pw);
   CUtensorMap mh, mw;
-  if (!rc) rc = map_k(&mh, ph);
-  if (!rc) rc = map_k(&mw, pw);
+  if (!rc) rc = map_k(&mh, ph, token_box(tokens));
+  if (!rc) rc = map_k(&mw, pw, l.tile_n / 2);
   if (rc) return rc;
   XentGemm p = {};
+  p.tile_n = l.tile_n, p.stage_tx = (token_box(tokens) + l.tile_n / 2) * 128;
   p.rows = tokens, p.cols = vocab;
   p.k_tiles = (int)ceil_div(width, kBK), p.npairs = l.planes == 3 ? 6 : 1, p.slices = 1;
+  p.group = group_of(dtype, true);
   p.target = target, p.id_bytes = id_bytes, p.vocab = vocab, p.ignore = ignore_index;
   p.stat = reinterpret_cast<float2*>(ws + l.stat);
   p.zt = reinterpret_cast<float*>(ws + l.zt);
-  rc = launch_gemm<kStats>(p, mh, mw, d, st);
+  rc = launch_gemm<kStats>(p, mh, mw, mw, d, st);
   if (rc) return rc;
   return launch_code(launch_train(xent_join_kernel, dim3((unsigned)ceil_div(tokens, 32)),
                                   dim3(32, 32), 0, st, (const float2*)p.stat, (const float*)p.zt,
-                                  (int)(2 * ceil_div(vocab, kTile)), tokens, target, id_bytes,
+                                  stat_parts(vocab, l.tile_n), tokens, target, id_bytes,
                                   ignore_index, vocab, lse, loss, d.status));
 }
 
@@ -900,8 +1084,13 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
   XentGemm base = {};
   base.npairs = l.planes == 3 ? 6 : 1, base.slices = 1;
   base.out_bf16 = dtype == B2G_BF16;
-  float* hpart = l.slices_h > 1 || l.pieces > 1 ? reinterpret_cast<float*>(ws + l.hpart) : nullptr;
-  const long long hslice = (long long)tokens * l.part_ld;
+  base.scale = reinterpret_cast<float*>(ws + l.scale);
+  base.group = group_of(dtype, false);
+  float* hpart = reinterpret_cast<float*>(ws + l.hpart);
+  float* wpart = reinterpret_cast<float*>(ws + l.wpart);
+  const bool f32 = dtype == B2G_F32;
+  const long long hslice = (long long)tokens * l.part_ld, wslice = (long long)l.piece * l.part_ld;
+  const auto reduce_to = f32 ? reduce<float> : reduce<Bf16>;
   for (int i = 0; i < l.pieces; ++i) {
     const int first = i * l.piece;
     const int n = vocab - first < l.piece ? vocab - first : l.piece;
@@ -909,52 +1098,60 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
     piece.p += (long long)first * pw.ld, piece.rows = n;
     const Planes dz{reinterpret_cast<Bf16*>(ws + l.dz), tokens, n, l.dz_ld,
                     (long long)tokens * l.dz_ld, l.planes};
-    CUtensorMap a, b;
+    CUtensorMap a, b, o = {};
     // dz of these classes
     XentGemm p = base;
     p.rows = tokens, p.cols = n, p.k_tiles = (int)ceil_div(width, kBK);
+    p.tile_n = l.tile_n, p.stage_tx = (token_box(tokens) + l.tile_n / 2) * 128;
+    p.group = group_of(dtype, true);
     p.target = target, p.id_bytes = id_bytes, p.vocab = vocab, p.ignore = ignore_index;
-    p.col0 = first, p.lse = lse, p.gloss = grad_loss;
-    p.dz = const_cast<Bf16*>(dz.p), p.dz_ld = dz.ld, p.dz_plane = dz.plane, p.planes = l.planes;
-    rc = map_k(&a, ph);
-    if (!rc) rc = map_k(&b, piece);
-    if (!rc) rc = launch_gemm<kDz>(p, a, b, d, st);
+    p.col0 = first, p.lse = lse, p.gloss = grad_loss, p.planes = l.planes;
+    rc = map_k(&a, ph, token_box(tokens));
+    if (!rc) rc = map_k(&b, piece, l.tile_n / 2);
+    if (!rc) rc = map_out(&o, dz);
+    if (!rc) rc = launch_gemm<kDz>(p, a, b, o, d, st);
     if (rc) return rc;
     if (dh) {  // dh += dz w over these classes
       p = base;
       p.rows = tokens, p.cols = width, p.k_tiles = (int)ceil_div(n, kBK);
+      p.tile_n = kTile, p.stage_tx = kStageBytes;
       p.slices = l.slices_h < p.k_tiles ? l.slices_h : p.k_tiles;
-      p.part_ld = l.part_ld, p.part_slice = hslice;
-      p.carry = i ? hpart : nullptr;
-      p.part = l.slices_h > 1 || i + 1 < l.pieces ? hpart : nullptr;
+      p.to_part = l.h_sums, p.add = i > 0;
       p.out = dh, p.ldo = lddh;
-      p.out_vec = vec16(dh) && vec16_ld(lddh, dtype);
-      rc = map_k(&a, dz);
+      p.out_tma = vec16(dh) && vec16_ld(lddh, dtype);
+      rc = map_k(&a, dz, 128);
       if (!rc) rc = map_mn(&b, piece);
-      if (!rc) rc = launch_gemm<kProdH>(p, a, b, d, st);
+      if (!rc && (p.to_part || p.out_tma))
+        rc = p.to_part ? encode(&o, true, hpart, width, tokens, l.part_ld, l.slices_h, hslice, 32)
+                       : encode(&o, f32, dh, width, tokens, lddh, 1, 0, 32);
+      if (!rc) rc = launch_gemm<kProdH>(p, a, b, o, d, st);
       if (rc) return rc;
     }
     if (dw) {  // these classes' rows of dw = dz^T h
       p = base;
       p.rows = n, p.cols = width, p.k_tiles = (int)ceil_div(tokens, kBK);
+      p.tile_n = kTile, p.stage_tx = kStageBytes;
       p.slices = l.slices_w;
-      float* wpart = l.slices_w > 1 ? reinterpret_cast<float*>(ws + l.wpart) : nullptr;
       unsigned char* out = static_cast<unsigned char*>(dw) + (long long)first * lddw * es;
-      p.part = wpart, p.part_ld = l.part_ld, p.part_slice = (long long)l.piece * l.part_ld;
+      p.to_part = l.slices_w > 1;
       p.out = out, p.ldo = lddw, p.accumulate = accumulate != 0;
-      p.out_vec = vec16(out) && vec16_ld(lddw, dtype);
+      // a bulk-tensor store adds in the output's type: right for FP32 only
+      p.out_tma = vec16(out) && vec16_ld(lddw, dtype) && !(accumulate && !f32);
+      p.add = !p.to_part && accumulate;
       rc = map_mn(&a, dz);
       if (!rc) rc = map_mn(&b, ph);
-      if (!rc) rc = launch_gemm<kProdW>(p, a, b, d, st);
-      if (!rc && wpart)
-        rc = (dtype == B2G_F32 ? reduce<float> : reduce<Bf16>)(
-            wpart, l.slices_w, l.part_ld, p.part_slice, n, width, out, lddw, p.accumulate, d, st);
+      if (!rc && (p.to_part || p.out_tma))
+        rc = p.to_part ? encode(&o, true, wpart, width, n, l.part_ld, l.slices_w, wslice, 32)
+                       : encode(&o, f32, out, width, n, lddw, 1, 0, 32);
+      if (!rc) rc = launch_gemm<kProdW>(p, a, b, o, d, st);
+      if (!rc && p.to_part)
+        rc = reduce_to(wpart, l.slices_w, l.part_ld, wslice, n, width, out, lddw, p.accumulate,
+                       d, st);
       if (rc) return rc;
     }
   }
-  if (dh && l.slices_h > 1)
-    return (dtype == B2G_F32 ? reduce<float> : reduce<Bf16>)(hpart, l.slices_h, l.part_ld, hslice,
-                                                             tokens, width, dh, lddh, 0, d, st);
+  if (dh && l.h_sums)
+    return reduce_to(hpart, l.slices_h, l.part_ld, hslice, tokens, width, dh, lddh, 0, d, st);
   return 0;
 }
 
