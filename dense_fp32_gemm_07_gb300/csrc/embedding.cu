@@ -17,6 +17,8 @@
 //  3. emb_join_kernel: the block of the window in which a longer run begins adds
 //     its partial rows in window order.
 // Windows make the work even however often the most frequent token occurs.
+#include <atomic>
+
 #include "tcgen05.cuh"
 #include "train_common.cuh"
 
@@ -83,22 +85,22 @@ __global__ void __launch_bounds__(256) emb_fwd_kernel(const __grid_constant__ Em
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortCtas = 8;              // blocks of the sorting cluster (portable limit)
-constexpr int kDigitBits = 8, kDigits = 1 << kDigitBits;
+constexpr int kSortCtas = 8;              // most blocks of the sorting cluster (portable limit)
+constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
+constexpr int kSortSmem = (kSortWarps + 1) * kDigits * 4;
 
 struct EmbSort {
   int tokens, vocab, passes;
-  int ctas;                  // blocks of the cluster that take part
   const void* ids;
   int id_bytes;
   long long padding;
-  unsigned* key[2];   // tokens ids each, unsorted / sorted by turns; the sort ends in key[0]
+  unsigned* key[2];   // tokens ids each, unsorted / sorted by turns
   int* pos[2];        // the token each came from
-  unsigned* hist;     // [kDigits][ctas * kSortWarps] counts, then first places
+  unsigned* totals;   // [blocks of the cluster][kDigits]
   unsigned int* status;
-  // the table to clear (bytes from zero_base, or rows of zero_row bytes zero_ld apart)
+  // the table to clear; rows == 0: nothing to clear
   unsigned char* table;
-  long long rows, row_bytes, ld_bytes;  // rows == 0: nothing to clear
+  long long rows, row_bytes, ld_bytes;
 };
 
 // Zeros over the rows of the table, by blocks `b` of `nb`.
@@ -110,11 +112,16 @@ __device__ __noinline__ void clear_rows(const EmbSort& p, long long b, long long
     const long long head = (16 - (long long)(reinterpret_cast<uintptr_t>(t) & 15)) & 15;
     const long long h = head < bytes ? head : bytes, vecs = (bytes - h) / 16;
     uint4* v = reinterpret_cast<uint4*>(t + h);
-    for (long long i = b * kSortThreads + threadIdx.x; i < vecs; i += nb * kSortThreads)
-      v[i] = make_uint4(0, 0, 0, 0);
+    const long long step = nb * kSortThreads;
+    long long i = b * kSortThreads + threadIdx.x;
+    for (; i + 3 * step < vecs; i += 4 * step) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[i + u * step] = make_uint4(0, 0, 0, 0);
+    }
+    for (; i < vecs; i += step) v[i] = make_uint4(0, 0, 0, 0);
     if (b == 0) {
-      for (long long i = threadIdx.x; i < h; i += kSortThreads) t[i] = 0;
-      for (long long i = h + vecs * 16 + threadIdx.x; i < bytes; i += kSortThreads) t[i] = 0;
+      for (long long j = threadIdx.x; j < h; j += kSortThreads) t[j] = 0;
+      for (long long j = h + vecs * 16 + threadIdx.x; j < bytes; j += kSortThreads) t[j] = 0;
     }
   } else {
     for (long long r = b; r < rows; r += nb) {
@@ -130,33 +137,34 @@ __device__ __noinline__ void clear_rows(const EmbSort& p, long long b, long long
   }
 }
 
-// Cluster 0 sorts, the other clusters clear the table.  The sort: `passes`
+// The first cluster sorts, the other ones clear the table.  The sort: `passes`
 // stable passes over kDigitBits bits each, lowest first.  Warp w of the cluster
-// owns a contiguous range of the input; it counts its digits, the counts are
-// turned into first places (digit by digit, warp by warp), and it then places
-// its pairs in order, 32 at a time: a pair's place is its digit's next one plus
-// the number of lower lanes with the same digit.  An id that takes part in no
-// sum (padding, out of range) sorts last as `vocab`.  Bound: latency; 4096
-// tokens take about as long as writing 100 MB of zeros.
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads)
-    emb_sort_kernel(const __grid_constant__ EmbSort p) {
-  __shared__ unsigned count[kSortWarps][kDigits];
-  __shared__ unsigned scan[kSortWarps];
+// owns a contiguous range of the input.  It counts its digits; the block adds
+// the counts up digit by digit and shares its totals with the cluster, so that
+// each block knows where its pairs of a digit begin; and each warp then places its
+// pairs in order, 32 at a time: a pair's place is its digit's next one plus the
+// number of lower lanes with the same digit.  An id that takes part in no sum
+// (padding, out of range) sorts last as `vocab`.  Bound: latency, a few
+// microseconds a pass, behind the clearing of a table that is much larger than the
+// batch.
+__global__ void __launch_bounds__(kSortThreads)
+    emb_sort_kernel(const __grid_constant__ EmbSort p, int ctas) {
+  extern __shared__ unsigned counts[];  // [kSortWarps][kDigits], then [kDigits] first places
+  __shared__ unsigned scan[kDigits / 32];
   pdl_launch_dependents();
   pdl_wait();
-  if (blockIdx.x >= kSortCtas) {
-    if (p.rows > 0)
-      clear_rows(p, (long long)blockIdx.x - kSortCtas, (long long)gridDim.x - kSortCtas);
+  if ((int)blockIdx.x >= ctas) {
+    clear_rows(p, (long long)blockIdx.x - ctas, (long long)gridDim.x - ctas);
     return;
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int W = p.ctas * kSortWarps;  // warps that take part
-  const bool active = (int)blockIdx.x < p.ctas;
-  const int gw = blockIdx.x * kSortWarps + warp;
+  unsigned* first = counts + kSortWarps * kDigits;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+  const int W = ctas * kSortWarps;
+  const int gw = cta * kSortWarps + warp;
   // ranges are whole multiples of 32 so that every warp runs full rounds
   const int per = ((p.tokens + W - 1) / W + 31) / 32 * 32;
   const long long lo64 = (long long)gw * per;
-  const int lo = active && lo64 < p.tokens ? (int)lo64 : p.tokens;
+  const int lo = lo64 < p.tokens ? (int)lo64 : p.tokens;
   const int hi = lo + per < p.tokens ? lo + per : p.tokens;
   const unsigned below = (1u << lane) - 1u;
 
@@ -167,71 +175,65 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
     p.key[0][i] = in && id != p.padding ? (unsigned)id : (unsigned)p.vocab;
     p.pos[0][i] = i;
   }
-  __syncwarp();
-  int src = 0;
-  for (int pass = 0; pass < p.passes; ++pass, src ^= 1) {
-    const int shift = pass * kDigitBits;
-    const unsigned* key = p.key[src];
-    const int* pos = p.pos[src];
-    unsigned* cnt = count[warp];
+  // (the lists are read past L1: the other blocks of the cluster write them too)
+  unsigned* cnt = counts + warp * kDigits;
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * kDigitBits, src = pass & 1;
+    const unsigned* key = src ? p.key[1] : p.key[0];
+    const int* pos = src ? p.pos[1] : p.pos[0];
+    unsigned* key_out = src ? p.key[0] : p.key[1];
+    int* pos_out = src ? p.pos[0] : p.pos[1];
     for (int d = lane; d < kDigits; d += 32) cnt[d] = 0;
     __syncwarp();
     for (int i = lo + lane; i < hi; i += 32)
-      atomicAdd(&cnt[(key[i] >> shift) & (kDigits - 1)], 1u);
-    __syncwarp();
-    if (active)
-      for (int d = lane; d < kDigits; d += 32) p.hist[(size_t)d * W + gw] = cnt[d];
+      atomicAdd(&cnt[(__ldcg(key + i) >> shift) & (kDigits - 1)], 1u);
+    __syncthreads();
+    // two threads per digit, 16 warps' counts each: counts become offsets in the block
+    static_assert(kSortThreads == 2 * kDigits, "two threads per digit");
+    const int digit = threadIdx.x >> 1;
+    unsigned* col = counts + (threadIdx.x & 1) * (kSortWarps / 2) * kDigits + digit;
+    unsigned mine = 0;
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps / 2; ++w) mine += col[w * kDigits];
+    const unsigned other = __shfl_xor_sync(0xffffffffu, mine, 1);
+    unsigned at = threadIdx.x & 1 ? other : 0u;  // the digit's pairs in the warps before mine
+    if (!(threadIdx.x & 1)) p.totals[cta * kDigits + digit] = mine + other;
     cluster_sync();
-    if (blockIdx.x == 0) {
-      // exclusive prefix sums over [digit][warp]; a thread owns kDigits * W / 1024 of them
-      const int PER = kDigits * p.ctas / 32;  // kDigits * W / kSortThreads, a multiple of 8
-      uint4* h = reinterpret_cast<uint4*>(p.hist) + (size_t)threadIdx.x * (PER / 4);
-      unsigned mine = 0;
-#pragma unroll 2
-      for (int i = 0; i < PER / 4; ++i) {
-        const uint4 v = h[i];
-        mine += v.x + v.y + v.z + v.w;
+    // where the digit's pairs begin: lower digits anywhere, this digit in earlier blocks
+    if (threadIdx.x < kDigits) {
+      unsigned all = 0, earlier = 0;
+      for (int c = 0; c < ctas; ++c) {
+        const unsigned t = __ldcg(p.totals + c * kDigits + threadIdx.x);
+        all += t;
+        earlier += c < cta ? t : 0u;
       }
-      unsigned incl = mine;
+      unsigned incl = all;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
       }
       if (lane == 31) scan[warp] = incl;
-      __syncthreads();
-      if (warp == 0) {
-        const unsigned mineW = scan[lane];
-        unsigned w = mineW;
+      asm volatile("bar.sync 1, %0;" ::"n"(kDigits) : "memory");
+      unsigned lower = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned up = __shfl_up_sync(0xffffffffu, w, o);
-          if (lane >= o) w += up;
-        }
-        scan[lane] = w - mineW;
-      }
-      __syncthreads();
-      unsigned at = scan[warp] + incl - mine;
-#pragma unroll 2
-      for (int i = 0; i < PER / 4; ++i) {
-        const uint4 v = h[i];
-        uint4 o;
-        o.x = at, at += v.x;
-        o.y = at, at += v.y;
-        o.z = at, at += v.z;
-        o.w = at, at += v.w;
-        h[i] = o;
-      }
+      for (int w = 0; w < kDigits / 32; ++w) lower += w < warp ? scan[w] : 0u;
+      first[threadIdx.x] = lower + incl - all + earlier;
     }
-    cluster_sync();
-    if (active)
-      for (int d = lane; d < kDigits; d += 32) cnt[d] = p.hist[(size_t)d * W + gw];
-    __syncwarp();
+    __syncthreads();
+    at += first[digit];
+#pragma unroll 4
+    for (int w = 0; w < kSortWarps / 2; ++w) {
+      const unsigned n = col[w * kDigits];
+      col[w * kDigits] = at;
+      at += n;
+    }
+    __syncthreads();
     for (int i0 = lo; i0 < hi; i0 += 32) {
       const int i = i0 + lane;
       const bool in = i < hi;
-      const unsigned k = in ? key[i] : 0u;
-      const int s = in ? pos[i] : 0;
+      const unsigned k = in ? __ldcg(key + i) : 0u;
+      const int from = in ? __ldcg(pos + i) : 0;
       const unsigned d = (k >> shift) & (kDigits - 1);
       unsigned same = __ballot_sync(0xffffffffu, in);
 #pragma unroll
@@ -239,12 +241,12 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
         const unsigned one = __ballot_sync(0xffffffffu, (d >> b) & 1u);
         same &= (d >> b) & 1u ? one : ~one;
       }
-      unsigned at = 0;
-      if (in) at = cnt[d] + __popc(same & below);
+      unsigned to = 0;
+      if (in) to = cnt[d] + __popc(same & below);
       __syncwarp();
       if (in) {
         if ((same & below) == 0) cnt[d] += __popc(same);
-        p.key[src ^ 1][at] = k, p.pos[src ^ 1][at] = s;
+        key_out[to] = k, pos_out[to] = from;
       }
       __syncwarp();
     }
@@ -452,7 +454,7 @@ int window_of(long long tokens, int width) {
 }
 
 struct BwdSizes {
-  size_t key[2], pos[2], hist, part, total;
+  size_t key[2], pos[2], totals, part, total;
 };
 
 BwdSizes bwd_sizes(long long tokens, int width) {
@@ -461,11 +463,45 @@ BwdSizes bwd_sizes(long long tokens, int width) {
   const size_t list = round_up((size_t)tokens * 4, 256);
   for (int i = 0; i < 2; ++i) s.key[i] = at, at += list;
   for (int i = 0; i < 2; ++i) s.pos[i] = at, at += list;
-  s.hist = at, at += (size_t)kDigits * kSortCtas * kSortWarps * 4;
+  s.totals = at, at += (size_t)kDigits * kSortCtas * 4;
   s.part = at;
   at += (size_t)ceil_div(tokens, window_of(tokens, width)) * 2 * width * sizeof(float);
   s.total = at;
   return s;
+}
+
+// One cluster sorts, with a block per 4096 tokens (a power of two, at most
+// kSortCtas); the clearing blocks, in clusters of the same size, fill the GPU twice
+// over.
+cudaError_t launch_sort(const EmbSort& q, long long tokens, const TrainDevice& d, cudaStream_t st) {
+  static std::atomic<int> configured[64];
+  if (d.dev < 0 || d.dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[d.dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        emb_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem);
+    if (e != cudaSuccess) return e;
+    configured[d.dev].store(1, std::memory_order_release);
+  }
+  int ctas = 1;
+  while (ctas < kSortCtas && ctas * 4096LL < tokens) ctas *= 2;
+  const long long bytes = q.rows * q.row_bytes;
+  const long long want = ceil_div(bytes, 16LL * kSortThreads), most = 2LL * d.sms - ctas;
+  const long long clear = (want < most ? want : most) / ctas * ctas;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(ctas + (bytes && clear < ctas ? ctas : clear)));
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = kSortSmem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  EmbSort p = q;
+  void* args[] = {&p, &ctas};
+  return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&emb_sort_kernel), args);
 }
 
 template <typename T, int VEC>
@@ -545,24 +581,17 @@ int b2g_embedding_backward(int dtype, long long tokens, int vocab, int width, co
   q.tokens = (int)tokens, q.vocab = vocab;
   q.passes = 1;  // the keys run from 0 to vocab, which stands for "in no sum"
   while (q.passes < 4 && (unsigned)vocab >> (q.passes * kDigitBits)) ++q.passes;
-  q.ctas = (int)(tokens >= 4096LL * kSortCtas ? kSortCtas : ceil_div(tokens, 4096));
   q.ids = ids, q.id_bytes = id_bytes, q.padding = padding;
   for (int i = 0; i < 2; ++i) {
     q.key[i] = reinterpret_cast<unsigned*>(ws + s.key[i]);
     q.pos[i] = reinterpret_cast<int*>(ws + s.pos[i]);
   }
-  q.hist = reinterpret_cast<unsigned*>(ws + s.hist);
+  q.totals = reinterpret_cast<unsigned*>(ws + s.totals);
   q.status = d.status;
   q.table = static_cast<unsigned char*>(dtable);
   q.rows = accumulate ? 0 : vocab;
   q.row_bytes = width * es, q.ld_bytes = vocab > 1 ? ldt * es : width * es;
-  // One cluster sorts; the clearing blocks fill the other SMs, one each.
-  const int blocks = accumulate ? kSortCtas : (d.sms / kSortCtas) * kSortCtas;
-  cudaError_t e = launch_train(emb_sort_kernel, dim3(blocks < 2 * kSortCtas && !accumulate
-                                                         ? 2 * kSortCtas
-                                                         : blocks),
-                               dim3(kSortThreads), 0, st, q);
-  if (e != cudaSuccess) return B2G_ERR_LAUNCH;
+  if (launch_sort(q, tokens, d, st) != cudaSuccess) return B2G_ERR_LAUNCH;
   const int sorted = q.passes & 1;
   EmbSum p{(int)tokens, vocab, width, 0, window_of(tokens, width), q.key[sorted], q.pos[sorted],
            dout, ldd, scale, accumulate != 0, dtable, ldt,

@@ -10,6 +10,12 @@
 // leaves one FP32 partial row of each for a second kernel to add in block order
 // (no atomics: the same bits every run).  x and dy are read once, dx written
 // once.
+//
+// Rows on 16-byte boundaries run on kernels that keep the next rows on their way
+// while one is worked on (registers in the forward pass, a ring of bulk copies in
+// shared memory in the backward pass); other rows are read element by element.
+#include <atomic>
+
 #include "train_common.cuh"
 
 namespace b2g {
@@ -101,6 +107,96 @@ __global__ void __launch_bounds__(512) ln_fwd_kernel(const __grid_constant__ LnF
   if (t == 0) {
     if (p.mean) p.mean[row] = mean;
     if (p.rstd) p.rstd[row] = rstd;
+  }
+}
+
+// Many rows: 16 warps per SM, G warps per row, each thread with NCH chunks of the
+// row at hand and the same chunks of its next row already on their way.  With two
+// warps a row, 8192 rows of 4096 BF16 values keep 128 KB an SM in flight.
+template <typename T, int VEC, int NCH, int G>
+__global__ void __launch_bounds__(512, 1) ln_fwd_rows_kernel(const __grid_constant__ LnFwd p) {
+  constexpr int NT = 32 * G, GROUPS = 16 / G;
+  __shared__ float red[2][16];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int group = threadIdx.x / NT, t = threadIdx.x % NT;
+  const T* w = static_cast<const T*>(p.w);
+  const T* b = static_cast<const T*>(p.b);
+  const float inv = 1.f / (float)p.cols;
+  const long long step = (long long)gridDim.x * GROUPS;
+  long long row = (long long)group * gridDim.x + blockIdx.x;
+  Pack<T, VEC> next[NCH];
+  auto fetch = [&](long long r) {
+    const T* x = static_cast<const T*>(p.x) + r * p.ldx;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = t + i * NT;
+      if (c < p.chunks) next[i].load(x + c * VEC);
+    }
+  };
+  // Sum over the group's threads; `k` alternates the exchange buffers.
+  auto total = [&](float v, int k) {
+    v = warp_sum(v);
+    if (G == 1) return v;
+    float* mine = red[k] + group * G;
+    if ((threadIdx.x & 31) == 0) mine[(threadIdx.x % NT) / 32] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(NT) : "memory");
+    float s = mine[0];
+#pragma unroll
+    for (int i = 1; i < G; ++i) s += mine[i];
+    return s;
+  };
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) next[i].zero();
+  if (row < p.rows) fetch(row);
+  for (; row < p.rows; row += step) {
+    Pack<T, VEC> raw[NCH];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      raw[i] = next[i];
+      float f[VEC];
+      raw[i].get(f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) sum += f[j];
+    }
+    if (row + step < p.rows) fetch(row + step);
+    const float mean = total(sum, 0) * inv;
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      float f[VEC];
+      raw[i].get(f);
+      if (t + i * NT < p.chunks) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sq = fmaf(f[j] - mean, f[j] - mean, sq);
+      }
+    }
+    const float rstd = 1.f / sqrtf(total(sq, 1) * inv + p.eps);
+    T* y = static_cast<T*>(p.y) + row * p.ldy;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = t + i * NT;
+      if (c < p.chunks) {
+        Pack<T, VEC> k;
+        float f[VEC], wf[VEC], bf[VEC];
+        raw[i].get(f);
+        k.zero();
+        if (w) k.load(w + c * VEC);
+        k.get(wf);
+        k.zero();
+        if (b) k.load(b + c * VEC);
+        k.get(bf);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) f[j] = fmaf((f[j] - mean) * rstd, w ? wf[j] : 1.f, bf[j]);
+        k.set(f);
+        k.store(y + c * VEC);
+      }
+    }
+    if (t == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
   }
 }
 
@@ -238,6 +334,143 @@ __global__ void __launch_bounds__(512) ln_bwd_kernel(const __grid_constant__ LnB
   }
 }
 
+// The same for rows on 16-byte boundaries: one block of 512 threads an SM in groups
+// of NT threads, a row per group.  A group's first thread keeps `stages` rows of x
+// and dy on their way into the group's ring in shared memory (bulk copies that
+// arrive on a barrier per slot; 160 KB an SM), so the rows' latency is not waited
+// for; a slot is refilled once the group's sums have been exchanged, when every
+// thread has read it.  At the end the groups' column sums are added in shared
+// memory in group order.
+constexpr int kRingBytes = 160 * 1024;
+constexpr int kRingStages = 16;  // at most
+
+template <typename T, int VEC, int NCH>
+__global__ void __launch_bounds__(512, 1)
+    ln_bwd_ring_kernel(const __grid_constant__ LnBwd p, int nt, int stages,
+                       unsigned int* status, unsigned long long wait_limit_ns) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ __align__(8) unsigned long long bars[512 / 32 * kRingStages];
+  __shared__ float red[2][2][16];
+  pdl_launch_dependents();
+  const int group = threadIdx.x / nt, t = threadIdx.x - group * nt, groups = 512 / nt;
+  const int warps = nt >> 5;
+  const uint32_t bytes = (uint32_t)(p.cols * (int)sizeof(T));
+  const uint32_t bar0 = smem_addr(bars) + 8u * (uint32_t)(group * kRingStages);
+  unsigned char* mine = ring + (size_t)group * stages * 2 * bytes;
+  if (t == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(bar0 + 8u * s, 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  pdl_wait();
+  const float inv = 1.f / (float)p.cols;
+  const long long step = (long long)gridDim.x * groups;
+  const long long row0 = (long long)group * gridDim.x + blockIdx.x;
+  auto issue = [&](long long row, int s) {
+    const uint32_t bar = bar0 + 8u * s, dst = smem_addr(mine + (size_t)s * 2 * bytes);
+    mbar_arrive_expect_tx(bar, 2 * bytes);
+    bulk_load(dst, static_cast<const T*>(p.x) + row * p.ldx, bytes, bar);
+    bulk_load(dst + bytes, static_cast<const T*>(p.dy) + row * p.lddy, bytes, bar);
+  };
+  if (t == 0) {
+    long long row = row0;
+    for (int s = 0; s < stages && row < p.rows; ++s, row += step) issue(row, s);
+  }
+  float aw[NCH][VEC], ab[NCH][VEC];
+  Pack<T, VEC> wr[NCH];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = t + i * nt;
+    wr[i].zero();
+    if (p.w && c < p.chunks) wr[i].load(static_cast<const T*>(p.w) + c * VEC);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) aw[i][j] = ab[i][j] = 0.f;
+  }
+  float mean = 0.f, rstd = 0.f;
+  if (row0 < p.rows) mean = p.mean[row0], rstd = p.rstd[row0];
+  int s = 0, k = 0;
+  uint32_t ph = 0;
+  bool alive = true;  // false once a wait has run out: no more waits, no more copies
+  for (long long row = row0; row < p.rows; row += step) {
+    const float m = mean, r = rstd;
+    if (row + step < p.rows) mean = p.mean[row + step], rstd = p.rstd[row + step];
+    if (alive)
+      alive = mbar_wait(bar0 + 8u * s, ph, wait_limit_ns, status, kStatusTimeoutFull);
+    const T* xs = reinterpret_cast<const T*>(mine + (size_t)s * 2 * bytes);
+    const T* ds = reinterpret_cast<const T*>(mine + (size_t)s * 2 * bytes + bytes);
+    Pack<T, VEC> xc[NCH], dc[NCH];
+    float s1 = 0.f, s2 = 0.f;  // sums of g and of g * xhat
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = t + i * nt;
+      xc[i].zero(), dc[i].zero();
+      if (c < p.chunks) {
+        xc[i].load(xs + c * VEC), dc[i].load(ds + c * VEC);
+        float xf[VEC], df[VEC], wf[VEC];
+        xc[i].get(xf), dc[i].get(df), wr[i].get(wf);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float xh = (xf[j] - m) * r, g = p.w ? df[j] * wf[j] : df[j];
+          s1 += g, s2 = fmaf(g, xh, s2);
+          aw[i][j] = fmaf(df[j], xh, aw[i][j]), ab[i][j] += df[j];
+        }
+      }
+    }
+    s1 = warp_sum(s1), s2 = warp_sum(s2);
+    if (warps > 1) {
+      float(&ex)[2][16] = red[k];
+      if ((threadIdx.x & 31) == 0) ex[0][threadIdx.x >> 5] = s1, ex[1][threadIdx.x >> 5] = s2;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(nt) : "memory");
+      s1 = s2 = 0.f;
+      for (int i = 0; i < warps; ++i) s1 += ex[0][group * warps + i], s2 += ex[1][group * warps + i];
+    }
+    if (t == 0 && alive && row + (long long)stages * step < p.rows)
+      issue(row + (long long)stages * step, s);
+    const float c1 = s1 * inv, c2 = s2 * inv;
+    T* dx = static_cast<T*>(p.dx) + row * p.lddx;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = t + i * nt;
+      if (c < p.chunks) {
+        float xf[VEC], df[VEC], wf[VEC], o[VEC];
+        xc[i].get(xf), dc[i].get(df), wr[i].get(wf);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float xh = (xf[j] - m) * r, g = p.w ? df[j] * wf[j] : df[j];
+          o[j] = r * (g - c1 - xh * c2);
+        }
+        Pack<T, VEC> v;
+        v.set(o);
+        v.store(dx + c * VEC);
+      }
+    }
+    k ^= 1;
+    if (++s == stages) s = 0, ph ^= 1u;
+  }
+  if (!p.part) return;
+  __syncthreads();  // every ring is drained: its memory now takes the groups' sums
+  float* sums = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = t + i * nt;
+    if (c < p.chunks) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        sums[(size_t)(2 * group) * p.cols + c * VEC + j] = aw[i][j];
+        sums[(size_t)(2 * group + 1) * p.cols + c * VEC + j] = ab[i][j];
+      }
+    }
+  }
+  __syncthreads();
+  float* out = p.part + (size_t)blockIdx.x * 2 * p.cols;
+  for (int c = threadIdx.x; c < 2 * p.cols; c += 512) {
+    float a = sums[c];
+    for (int g = 1; g < groups; ++g) a += sums[(size_t)2 * g * p.cols + c];
+    out[c] = a;
+  }
+}
+
 // Rows wider than the registers of a block: dx in two passes over the row.
 template <typename T>
 __global__ void __launch_bounds__(1024) ln_bwd_wide_kernel(const __grid_constant__ LnBwd p) {
@@ -334,9 +567,27 @@ cudaError_t fwd_kernel(int nch, dim3 grid, dim3 block, cudaStream_t st, const Ln
   return launch_train(ln_fwd_kernel<T, VEC, NCH>, grid, block, 0, st, p);
 }
 
+// Warps per row of the many-rows kernel (8 chunks a thread), 0 when 4 are too few.
+template <typename T, int VEC>
+cudaError_t fwd_rows(LnFwd p, int sms, cudaStream_t st) {
+  const long long warps = ceil_div(p.chunks, 256);
+  const int g = warps <= 1 ? 1 : warps <= 2 ? 2 : 4;
+  const long long blocks = ceil_div(p.rows, 16 / g);
+  const dim3 grid((unsigned)(blocks < sms ? blocks : sms)), block(512);
+  const int nch = (int)ceil_div(p.chunks, 32 * g);
+  if (g == 4) return launch_train(ln_fwd_rows_kernel<T, VEC, 8, 4>, grid, block, 0, st, p);
+  if (g == 2) return launch_train(ln_fwd_rows_kernel<T, VEC, 8, 2>, grid, block, 0, st, p);
+  if (nch <= 2) return launch_train(ln_fwd_rows_kernel<T, VEC, 2, 1>, grid, block, 0, st, p);
+  if (nch <= 4) return launch_train(ln_fwd_rows_kernel<T, VEC, 4, 1>, grid, block, 0, st, p);
+  return launch_train(ln_fwd_rows_kernel<T, VEC, 8, 1>, grid, block, 0, st, p);
+}
+
 template <typename T, int VEC>
 cudaError_t fwd_launch(LnFwd p, int sms, cudaStream_t st) {
   p.chunks = p.cols / VEC;
+  if constexpr (VEC > 1) {
+    if (p.rows > 4 * sms && p.chunks <= 1024) return fwd_rows<T, VEC>(p, sms, st);
+  }
   // Few rows: one chunk a thread, for the shortest path; many: several, for the
   // fewest barriers per byte.
   int nt = p.rows <= 2 * sms ? row_threads(p.chunks, 1) : 0;
@@ -348,13 +599,29 @@ cudaError_t fwd_launch(LnFwd p, int sms, cudaStream_t st) {
   return fwd_kernel<T, VEC>((int)ceil_div(p.chunks, nt), grid, block, st, p);
 }
 
-// Blocks of the backward kernel, each leaving one partial row of dweight and of
-// dbias: about 1024 threads an SM, and few enough that the partial rows (two
-// FP32 rows a block) stay a small share of the traffic.
-int bwd_parts(long long rows, int cols, int sms) {
-  const int nt = row_threads(cols, 16);
-  const long long per_sm = nt == 0 || nt >= 512 ? 2 : 1024 / nt < 8 ? 1024 / nt : 8;
-  const long long most = per_sm * sms, fair = ceil_div(rows, 4);
+// The ring kernel's groups: threads a row (16 columns each), rows in the ring;
+// stages == 0 when a row is too wide for it.
+struct Ring {
+  int nt, groups, stages;
+};
+Ring ring_of(int cols, int dtype) {
+  Ring r{32, 0, 0};
+  while (r.nt < 512 && r.nt * 16 < cols) r.nt *= 2;
+  r.groups = 512 / r.nt;
+  if (r.nt * 16 < cols) return r;
+  const long long pair = 2LL * cols * (long long)type_size(dtype);
+  const long long s = kRingBytes / (pair * r.groups);
+  r.stages = (int)(s < kRingStages ? s : kRingStages);
+  return r;
+}
+
+// Blocks of a backward kernel, each leaving one partial row of dweight and of
+// dbias: one an SM in the ring kernel, up to four rows a block otherwise, at most
+// four blocks an SM (the partial rows stay a small share of the traffic).
+int bwd_parts(long long rows, int cols, int dtype, int sms, bool vec) {
+  const Ring r = ring_of(cols, dtype);
+  const long long most = vec && r.stages >= 2 ? sms : 4LL * sms;
+  const long long fair = ceil_div(rows, vec && r.stages >= 2 ? r.groups : 4);
   return (int)(fair < most ? fair : most);
 }
 
@@ -367,11 +634,39 @@ cudaError_t bwd_kernel(int nch, dim3 grid, dim3 block, cudaStream_t st, const Ln
 }
 
 template <typename T, int VEC>
-cudaError_t bwd_launch(LnBwd p, T* dweight, T* dbias, int parts, cudaStream_t st) {
+cudaError_t bwd_ring(const LnBwd& p, const Ring& r, int parts, const TrainDevice& d,
+                     cudaStream_t st) {
+  static std::atomic<int> configured[64];
+  constexpr int NCH = 16 / VEC;
+  // the rings, and at the end the groups' column sums (64 KB at most)
+  const size_t rings = (size_t)r.groups * r.stages * 2 * p.cols * sizeof(T);
+  const size_t sums = (size_t)r.groups * 2 * p.cols * sizeof(float);
+  const size_t smem = rings > sums ? rings : sums;
+  if (d.dev < 0 || d.dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[d.dev].load(std::memory_order_acquire)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(ln_bwd_ring_kernel<T, VEC, NCH>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e != cudaSuccess) return e;
+    configured[d.dev].store(1, std::memory_order_release);
+  }
+  return launch_train(ln_bwd_ring_kernel<T, VEC, NCH>, dim3(parts), dim3(512), smem, st, p, r.nt,
+                      r.stages, d.status, d.wait_limit_ns);
+}
+
+template <typename T, int VEC>
+cudaError_t bwd_launch(LnBwd p, int dtype, T* dweight, T* dbias, int parts, const TrainDevice& d,
+                       cudaStream_t st) {
   p.chunks = p.cols / VEC;
   cudaError_t e = cudaSuccess;
   const int nt = row_threads(p.chunks, kMaxBwd<VEC>);
-  if (nt) {
+  const Ring r = ring_of(p.cols, dtype);
+  bool done = false;
+  if constexpr (VEC > 1) {
+    if (r.stages >= 2) e = bwd_ring<T, VEC>(p, r, parts, d, st), done = true;
+  }
+  if (done) {
+  } else if (nt) {
     e = bwd_kernel<T, VEC>((int)ceil_div(p.chunks, nt), dim3(parts), dim3(nt), st, p);
   } else {
     if (p.part)
@@ -394,8 +689,10 @@ int check_rows(int dtype, long long rows, int cols) {
 
 bool ld_ok(long long ld, int cols) { return ld >= (cols > 1 ? cols : 1); }
 
-size_t bwd_bytes(long long rows, int cols, int sms) {
-  return (size_t)bwd_parts(rows, cols, sms) * 2 * cols * sizeof(float);
+// Partial rows of either kind of kernel: the query does not know the alignment.
+size_t bwd_bytes(long long rows, int cols, int dtype, int sms) {
+  const int a = bwd_parts(rows, cols, dtype, sms, true), b = bwd_parts(rows, cols, dtype, sms, false);
+  return (size_t)(a > b ? a : b) * 2 * cols * sizeof(float);
 }
 
 }  // namespace
@@ -432,7 +729,7 @@ int b2g_layernorm_backward_workspace_size(int dtype, long long rows, int cols, s
   if (!bytes) return B2G_ERR_NULL;
   TrainDevice d;
   const int sms = train_device(&d) ? 152 : d.sms;  // without a device: GB300's count
-  *bytes = bwd_bytes(rows, cols, sms);
+  *bytes = bwd_bytes(rows, cols, dtype, sms);
   return 0;
 }
 
@@ -451,7 +748,7 @@ int b2g_layernorm_backward(int dtype, long long rows, int cols, const void* dy, 
   if (rc) return rc;
   const bool sums = dweight || dbias;
   if (sums && rows > 0 &&
-      (!workspace || !vec16(workspace) || workspace_bytes < bwd_bytes(rows, cols, d.sms)))
+      (!workspace || !vec16(workspace) || workspace_bytes < bwd_bytes(rows, cols, dtype, d.sms)))
     return B2G_ERR_WORKSPACE;
   float* part = sums ? static_cast<float*>(workspace) : nullptr;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -462,19 +759,19 @@ int b2g_layernorm_backward(int dtype, long long rows, int cols, const void* dy, 
     return e == cudaSuccess ? 0 : B2G_ERR_CUDA;
   }
   LnBwd p{rows, cols, 0, dy, lddy, x, ldx, weight, mean, rstd, dx, lddx, part};
-  const int parts = bwd_parts(rows, cols, d.sms);
   const bool v = vec16(dy) && vec16(x) && vec16(weight) && vec16(dx) && vec16_ld(lddy, dtype) &&
                  vec16_ld(ldx, dtype) && vec16_ld(lddx, dtype) && vec16_ld(cols, dtype);
+  const int parts = bwd_parts(rows, cols, dtype, d.sms, v);
   if (dtype == B2G_F32) {
     float* dw = static_cast<float*>(dweight);
     float* db = static_cast<float*>(dbias);
-    return launch_code(v ? bwd_launch<float, 4>(p, dw, db, parts, st)
-                         : bwd_launch<float, 1>(p, dw, db, parts, st));
+    return launch_code(v ? bwd_launch<float, 4>(p, dtype, dw, db, parts, d, st)
+                         : bwd_launch<float, 1>(p, dtype, dw, db, parts, d, st));
   }
   Bf16* dw = static_cast<Bf16*>(dweight);
   Bf16* db = static_cast<Bf16*>(dbias);
-  return launch_code(v ? bwd_launch<Bf16, 8>(p, dw, db, parts, st)
-                       : bwd_launch<Bf16, 1>(p, dw, db, parts, st));
+  return launch_code(v ? bwd_launch<Bf16, 8>(p, dtype, dw, db, parts, d, st)
+                       : bwd_launch<Bf16, 1>(p, dtype, dw, db, parts, d, st));
 }
 
 }  // extern "C"

@@ -116,6 +116,17 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float* red, int w
                      warp_sum(lane < warps ? red[32 + lane] : 0.f));
 }
 
+// `bytes` (a multiple of 16) from global to shared memory, both 16-byte aligned;
+// completion is counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // ------------------------------------------------------------------ host side
 
 inline size_t type_size(int dtype) { return dtype == B2G_F32 ? 4 : 2; }

@@ -14,6 +14,7 @@ codes ``B2GError``; ids and targets out of range are reported by ``b2g_status``
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 from . import B2GError, _load, _stream_handle, _t
@@ -67,77 +68,79 @@ def train_library():
     return lib
 
 
-_codes = None
+_torch = None
+_CODES = {}  # torch element type -> the library's code
 
 
-def _dtype(t, name, like=None):
-    """The library's code of a tensor's element type (`like`: the type it must have)."""
-    global _codes
-    torch = _t()
-    if _codes is None:
-        _codes = {torch.float32: B2G_F32, torch.bfloat16: B2G_BF16}
-    if not isinstance(t, torch.Tensor) or t.dtype not in _codes:
+def _setup():
+    """torch, and the table of element types, on first use."""
+    global _torch
+    _torch = _t()
+    _CODES.update({_torch.float32: B2G_F32, _torch.bfloat16: B2G_BF16})
+    train_library()
+
+
+# The checks below run in every call; each looks at as few attributes as it can
+# (a tensor's cost about 0.1 us each), and says what is wrong only once something is.
+
+def _matrix(t, name, dt=None, dev=None):
+    """(rows, columns, leading dimension) of a row-major CUDA matrix, of element
+    type dt on device number dev where those are given."""
+    if _torch is None:
+        _setup()
+    if not isinstance(t, _torch.Tensor) or t.dtype not in _CODES:
         raise TypeError(f"{name} must be a torch.float32 or torch.bfloat16 tensor")
-    if not t.is_cuda:
+    d = t.get_device()
+    if d < 0:
         raise TypeError(f"{name} must be on a CUDA device")
-    if like is not None and t.dtype is not like.dtype:
-        raise TypeError(f"{name} must have the type {like.dtype}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}")
-    return _codes[t.dtype]
-
-
-def _matrix(t, name, like=None):
-    """(type code, rows, columns, leading dimension) of a row-major matrix."""
-    code = _dtype(t, name, like)
-    if t.dim() != 2:
+    if dt is not None and t.dtype is not dt:
+        raise TypeError(f"{name} must have the type {dt}")
+    if dev is not None and d != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    r, c = t.shape
+    r, c = shape
+    if t.is_contiguous():
+        return r, c, (c or 1)
     s0, s1 = t.stride()
     if c > 1 and s1 != 1:
         raise ValueError(f"{name} must have unit column stride (row-major rows)")
     if r > 1 and s0 < c:
         raise ValueError(f"{name} must not have overlapping rows")
-    return code, r, c, (s0 if r > 1 else max(1, c))
+    return r, c, (s0 if r > 1 else max(1, c))
 
 
-def _vector(t, name, n, like):
-    """The pointer of a vector of n elements of `like`'s type; None stays None."""
+def _vector(t, name, n, dt, dev):
+    """The pointer of a contiguous vector of n elements of type dt; None stays None."""
     if t is None:
         return None
-    _dtype(t, name, like)
-    if t.dim() != 1 or t.size(0) != n or (n > 1 and t.stride(0) != 1):
+    if not isinstance(t, _torch.Tensor) or t.dtype is not dt:
+        raise TypeError(f"{name} must be a {dt} tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector of {n} elements")
     return t.data_ptr()
 
 
-def _floats(t, name, n, like):
-    """The pointer of a contiguous float32 vector of n elements."""
-    torch = _t()
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
-        raise TypeError(f"{name} must be a torch.float32 tensor")
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}")
-    if t.dim() != 1 or t.size(0) != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous vector of {n} elements")
-    return t.data_ptr()
-
-
-def _indices(t, name, like):
+def _indices(t, name, dev):
     """(pointer, count, bytes each) of a contiguous vector of row numbers."""
-    torch = _t()
-    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.int64, torch.int32):
+    size = None
+    if isinstance(t, _torch.Tensor):
+        size = 8 if t.dtype is _torch.int64 else 4 if t.dtype is _torch.int32 else None
+    if size is None:
         raise TypeError(f"{name} must be a torch.int64 or torch.int32 tensor")
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}")
-    if t.dim() != 1 or (t.size(0) > 1 and t.stride(0) != 1):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    if t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous vector")
-    return t.data_ptr(), t.size(0), t.element_size()
+    return t.data_ptr(), t.shape[0], size
 
 
-def _result(t, name, shape, like):
+def _result(t, name, shape, dt, dev):
     """The leading dimension of a given result matrix."""
-    _, r, c, ld = _matrix(t, name, like)
+    r, c, ld = _matrix(t, name, dt, dev)
     if (r, c) != shape:
         raise ValueError(f"{name} must be {shape[0]} x {shape[1]}")
     return ld
@@ -160,48 +163,60 @@ def _span(t):
     return (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
 
 
-class _On:
-    """The stream a call runs on.  Results and workspaces are allocated for it:
-    with a `stream` given, torch's allocator is told so, since memory freed by
-    Python may otherwise be reused while that stream still works on it."""
+class _OnStream:
+    """Where a call with a `stream` argument runs.  Its results and workspaces are
+    allocated for that stream, and torch's allocator is told which tensors the
+    stream works on, since memory that Python frees may otherwise be reused while
+    it does."""
 
     def __init__(self, stream):
         self.handle = _stream_handle(stream)
-        self.other = None
-        if stream is not None:
-            torch = _t()
-            self.other = (stream if isinstance(stream, torch.cuda.Stream)
-                          else torch.cuda.ExternalStream(self.handle) if self.handle
-                          else torch.cuda.default_stream())
+        self.stream = (stream if isinstance(stream, _torch.cuda.Stream)
+                       else _torch.cuda.ExternalStream(self.handle) if self.handle
+                       else _torch.cuda.default_stream())
 
     def empty(self, shape, dtype, device):
-        torch = _t()
-        if self.other is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(self.other):
-            return torch.empty(shape, dtype=dtype, device=device)
+        with _torch.cuda.stream(self.stream):
+            return _torch.empty(shape, dtype=dtype, device=device)
 
     def uses(self, *tensors):
-        """Inputs of another stream's allocator stay reserved until this stream is done."""
-        if self.other is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.other)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(self.stream)
 
 
-def _raise(rc):
+class _OnCurrent:
+    """A call on the current stream of a device: torch allocates for that stream."""
+
+    __slots__ = ("handle", "empty")
+
+    def __init__(self, dev):
+        self.handle = _torch._C._cuda_getCurrentRawStream(dev)
+        self.empty = _empty
+
+    def uses(self, *tensors):
+        pass
+
+
+def _empty(shape, dtype, device):
+    return _torch.empty(shape, dtype=dtype, device=device)
+
+
+def _on(stream, dev):
+    """The stream a call on device number dev runs on; the library's calls run on
+    the current device, which has to be that one."""
+    if dev != _torch._C._cuda_getDevice():
+        raise ValueError(f"cuda:{dev} must be the current device")
+    return _OnCurrent(dev) if stream is None else _OnStream(stream)
+
+
+def _size(query, *args):
+    """The workspace size that a query names."""
+    n = ctypes.c_size_t(0)
+    rc = query(*args, ctypes.byref(n))
     if rc:
         raise B2GError(rc)
-
-
-def _workspace(on, device, query, *args):
-    """(tensor to keep alive, pointer, bytes) of the size a query names."""
-    n = ctypes.c_size_t(0)
-    _raise(query(*args, ctypes.byref(n)))
-    if n.value == 0:
-        return None, None, 0
-    ws = on.empty((n.value,), _t().uint8, device)
-    return ws, ws.data_ptr(), n.value
+    return n.value
 
 
 # ------------------------------------------------------------------ layer norm
@@ -212,21 +227,22 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
     x is rows x cols; weight and bias are vectors of cols elements of its type
     (None: ones, zeros).  mean and rstd are float32 vectors for the backward pass.
     `out` takes y and may be x itself."""
-    lib = train_library()
-    torch = _t()
-    code, r, c, ldx = _matrix(x, "x")
-    pw, pb = _vector(weight, "weight", c, x), _vector(bias, "bias", c, x)
-    on = _On(stream)
+    r, c, ldx = _matrix(x, "x")
+    dt, device, dev = x.dtype, x.device, x.get_device()
+    pw, pb = _vector(weight, "weight", c, dt, dev), _vector(bias, "bias", c, dt, dev)
+    on = _on(stream, dev)
     if out is None:
-        out, ldy = on.empty((r, c), x.dtype, x.device), max(1, c)
+        out, ldy = on.empty((r, c), dt, device), c or 1
     else:
-        ldy = _result(out, "out", (r, c), x)
+        ldy = _result(out, "out", (r, c), dt, dev)
         if out.data_ptr() != x.data_ptr() or ldx != ldy:
             _apart(out, ("x", x))
-    mean = on.empty((r,), torch.float32, x.device)
-    rstd = on.empty((r,), torch.float32, x.device)
-    _raise(lib.b2g_layernorm(code, r, c, x.data_ptr(), ldx, pw, pb, float(eps), out.data_ptr(),
-                             ldy, mean.data_ptr(), rstd.data_ptr(), on.handle))
+    mean = on.empty((r,), _torch.float32, device)
+    rstd = on.empty((r,), _torch.float32, device)
+    rc = _lib.b2g_layernorm(_CODES[dt], r, c, x.data_ptr(), ldx, pw, pb, eps, out.data_ptr(), ldy,
+                            mean.data_ptr(), rstd.data_ptr(), on.handle)
+    if rc:
+        raise B2GError(rc)
     on.uses(x, weight, bias, out)
     return out, mean, rstd
 
@@ -236,28 +252,33 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, out=None, 
 
     weight, mean and rstd as in the forward call; dweight is None when weight is
     None, dbias when `bias` is false.  `out` takes dx and may be dy itself."""
-    lib = train_library()
-    code, r, c, ldx = _matrix(x, "x")
-    _, rd, cd, lddy = _matrix(dy, "dy", x)
-    if (rd, cd) != (r, c):
+    r, c, ldx = _matrix(x, "x")
+    dt, device, dev = x.dtype, x.device, x.get_device()
+    rd, cd, lddy = _matrix(dy, "dy", dt, dev)
+    if rd != r or cd != c:
         raise ValueError("dy must have x's shape")
-    pw = _vector(weight, "weight", c, x)
-    pm, pr = _floats(mean, "mean", r, x), _floats(rstd, "rstd", r, x)
-    on = _On(stream)
+    pw = _vector(weight, "weight", c, dt, dev)
+    pm = _vector(mean, "mean", r, _torch.float32, dev)
+    pr = _vector(rstd, "rstd", r, _torch.float32, dev)
+    on = _on(stream, dev)
     if out is None:
-        out, lddx = on.empty((r, c), x.dtype, x.device), max(1, c)
+        out, lddx = on.empty((r, c), dt, device), c or 1
     else:
-        lddx = _result(out, "out", (r, c), x)
+        lddx = _result(out, "out", (r, c), dt, dev)
         _apart(out, ("x", x))
         if out.data_ptr() != dy.data_ptr() or lddx != lddy:
             _apart(out, ("dy", dy))
-    dw = on.empty((c,), x.dtype, x.device) if weight is not None else None
-    db = on.empty((c,), x.dtype, x.device) if bias else None
-    ws, p, n = _workspace(on, x.device, lib.b2g_layernorm_backward_workspace_size, code, r, c)
-    _raise(lib.b2g_layernorm_backward(
+    dw = None if weight is None else on.empty((c,), dt, device)
+    db = on.empty((c,), dt, device) if bias else None
+    code = _CODES[dt]
+    n = _size(_lib.b2g_layernorm_backward_workspace_size, code, r, c)
+    ws = on.empty((n,), _torch.uint8, device)
+    rc = _lib.b2g_layernorm_backward(
         code, r, c, dy.data_ptr(), lddy, x.data_ptr(), ldx, pw, pm, pr, out.data_ptr(), lddx,
-        None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(), p, n,
-        on.handle))
+        None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(),
+        ws.data_ptr(), n, on.handle)
+    if rc:
+        raise B2GError(rc)
     on.uses(dy, x, weight, mean, rstd, out)
     return out, dw, db
 
@@ -266,17 +287,19 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, out=None, 
 
 def embedding(ids, table, scale: float = 1.0, out=None, stream=None):
     """scale * table[ids], one row per id; an id out of range gives a row of NaN."""
-    lib = train_library()
-    code, v, d, ldt = _matrix(table, "table")
-    pi, n, width = _indices(ids, "ids", table)
-    on = _On(stream)
+    v, d, ldt = _matrix(table, "table")
+    dt, device, dev = table.dtype, table.device, table.get_device()
+    pi, n, width = _indices(ids, "ids", dev)
+    on = _on(stream, dev)
     if out is None:
-        out, ldo = on.empty((n, d), table.dtype, table.device), max(1, d)
+        out, ldo = on.empty((n, d), dt, device), d or 1
     else:
-        ldo = _result(out, "out", (n, d), table)
+        ldo = _result(out, "out", (n, d), dt, dev)
         _apart(out, ("table", table), ("ids", ids))
-    _raise(lib.b2g_embedding(code, n, v, d, pi, width, table.data_ptr(), ldt, float(scale),
-                             out.data_ptr(), ldo, on.handle))
+    rc = _lib.b2g_embedding(_CODES[dt], n, v, d, pi, width, table.data_ptr(), ldt, scale,
+                            out.data_ptr(), ldo, on.handle)
+    if rc:
+        raise B2GError(rc)
     on.uses(ids, table, out)
     return out
 
@@ -286,28 +309,32 @@ def embedding_backward(ids, dout, num_rows: int, scale: float = 1.0, out=None,
     """The gradient of a table of num_rows rows: row v is scale times the sum of
     the rows of dout whose id is v, except padding_idx.  With `accumulate` it is
     added to `out`'s values (only rows with a token are touched)."""
-    lib = train_library()
-    code, n, d, ldd = _matrix(dout, "dout")
-    pi, ni, width = _indices(ids, "ids", dout)
+    n, d, ldd = _matrix(dout, "dout")
+    dt, device, dev = dout.dtype, dout.device, dout.get_device()
+    pi, ni, width = _indices(ids, "ids", dev)
     if ni != n:
         raise ValueError("ids and dout must have the same number of rows")
     if num_rows < 0:
         raise ValueError("num_rows must not be negative")
     if padding_idx is not None and not 0 <= padding_idx < num_rows:
         raise ValueError("padding_idx must be a row of the table")
-    on = _On(stream)
+    on = _on(stream, dev)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out, ldt = on.empty((num_rows, d), dout.dtype, dout.device), max(1, d)
+        out, ldt = on.empty((num_rows, d), dt, device), d or 1
     else:
-        ldt = _result(out, "out", (num_rows, d), dout)
+        ldt = _result(out, "out", (num_rows, d), dt, dev)
         _apart(out, ("dout", dout), ("ids", ids))
-    ws, p, nb = _workspace(on, dout.device, lib.b2g_embedding_backward_workspace_size, code, n,
-                           num_rows, d)
-    _raise(lib.b2g_embedding_backward(code, n, num_rows, d, pi, width, dout.data_ptr(), ldd,
-                                      float(scale), -1 if padding_idx is None else padding_idx,
-                                      int(accumulate), out.data_ptr(), ldt, p, nb, on.handle))
+    code = _CODES[dt]
+    nb = _size(_lib.b2g_embedding_backward_workspace_size, code, n, num_rows, d)
+    ws = on.empty((nb,), _torch.uint8, device)
+    rc = _lib.b2g_embedding_backward(code, n, num_rows, d, pi, width, dout.data_ptr(), ldd, scale,
+                                     -1 if padding_idx is None else padding_idx,
+                                     1 if accumulate else 0, out.data_ptr(), ldt, ws.data_ptr(),
+                                     nb, on.handle)
+    if rc:
+        raise B2GError(rc)
     on.uses(ids, dout, out)
     return out
 
@@ -320,20 +347,22 @@ def linear_cross_entropy(h, w, target, ignore_index: int = -100, stream=None):
     h is tokens x width, w vocab x width, target a vector of class numbers.
     loss_i = lse_i - logit_{i, target_i}, 0 where target_i is ignore_index; lse is
     the log of the sum of the exponentials.  Both are float32 vectors."""
-    lib = train_library()
-    torch = _t()
-    code, n, d, ldh = _matrix(h, "h")
-    _, v, dw, ldw = _matrix(w, "w", h)
-    pt, nt, width = _indices(target, "target", h)
+    n, d, ldh = _matrix(h, "h")
+    dt, device, dev = h.dtype, h.device, h.get_device()
+    v, dw, ldw = _matrix(w, "w", dt, dev)
+    pt, nt, width = _indices(target, "target", dev)
     if dw != d or nt != n:
         raise ValueError(f"shape mismatch: h {n}x{d}, w {v}x{dw}, target {nt}")
-    on = _On(stream)
-    loss = on.empty((n,), torch.float32, h.device)
-    lse = on.empty((n,), torch.float32, h.device)
-    ws, p, nb = _workspace(on, h.device, lib.b2g_linear_xent_workspace_size, code, n, v, d,
-                           h.data_ptr(), ldh, w.data_ptr(), ldw, 0)
-    _raise(lib.b2g_linear_xent(code, n, v, d, h.data_ptr(), ldh, w.data_ptr(), ldw, pt, width,
-                               ignore_index, loss.data_ptr(), lse.data_ptr(), p, nb, on.handle))
+    on = _on(stream, dev)
+    loss = on.empty((n,), _torch.float32, device)
+    lse = on.empty((n,), _torch.float32, device)
+    code, ph, pw = _CODES[dt], h.data_ptr(), w.data_ptr()
+    nb = _size(_lib.b2g_linear_xent_workspace_size, code, n, v, d, ph, ldh, pw, ldw, 0)
+    ws = on.empty((nb,), _torch.uint8, device)
+    rc = _lib.b2g_linear_xent(code, n, v, d, ph, ldh, pw, ldw, pt, width, ignore_index,
+                              loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), nb, on.handle)
+    if rc:
+        raise B2GError(rc)
     on.uses(h, w, target)
     return loss, lse
 
@@ -345,49 +374,57 @@ def linear_cross_entropy_backward(h, w, target, lse, grad_loss, ignore_index: in
     lse is the forward call's; grad_loss a float32 vector, one weight per row
     (1 / n for a mean over n rows).  `dw` takes the head's gradient; with
     `accumulate` it is added to the values there."""
-    lib = train_library()
-    code, n, d, ldh = _matrix(h, "h")
-    _, v, dh_, ldw = _matrix(w, "w", h)
-    pt, nt, width = _indices(target, "target", h)
-    if dh_ != d or nt != n:
-        raise ValueError(f"shape mismatch: h {n}x{d}, w {v}x{dh_}, target {nt}")
-    pl, pg = _floats(lse, "lse", n, h), _floats(grad_loss, "grad_loss", n, h)
-    on = _On(stream)
+    n, d, ldh = _matrix(h, "h")
+    dt, device, dev = h.dtype, h.device, h.get_device()
+    v, dv, ldw = _matrix(w, "w", dt, dev)
+    pt, nt, width = _indices(target, "target", dev)
+    if dv != d or nt != n:
+        raise ValueError(f"shape mismatch: h {n}x{d}, w {v}x{dv}, target {nt}")
+    pl = _vector(lse, "lse", n, _torch.float32, dev)
+    pg = _vector(grad_loss, "grad_loss", n, _torch.float32, dev)
+    on = _on(stream, dev)
     if dw is None:
         if accumulate:
             raise ValueError("accumulate needs dw")
-        dw, lddw = on.empty((v, d), h.dtype, h.device), max(1, d)
+        dw, lddw = on.empty((v, d), dt, device), d or 1
     else:
-        lddw = _result(dw, "dw", (v, d), h)
+        lddw = _result(dw, "dw", (v, d), dt, dev)
         _apart(dw, ("h", h), ("w", w))
-    dh = on.empty((n, d), h.dtype, h.device)
-    ws, p, nb = _workspace(on, h.device, lib.b2g_linear_xent_workspace_size, code, n, v, d,
-                           h.data_ptr(), ldh, w.data_ptr(), ldw, 1)
-    _raise(lib.b2g_linear_xent_backward(
-        code, n, v, d, h.data_ptr(), ldh, w.data_ptr(), ldw, pt, width, ignore_index, pl, pg,
-        dh.data_ptr(), max(1, d), int(accumulate), dw.data_ptr(), lddw, p, nb, on.handle))
+    dh = on.empty((n, d), dt, device)
+    code, ph, pw = _CODES[dt], h.data_ptr(), w.data_ptr()
+    nb = _size(_lib.b2g_linear_xent_workspace_size, code, n, v, d, ph, ldh, pw, ldw, 1)
+    ws = on.empty((nb,), _torch.uint8, device)
+    rc = _lib.b2g_linear_xent_backward(code, n, v, d, ph, ldh, pw, ldw, pt, width, ignore_index,
+                                       pl, pg, dh.data_ptr(), d or 1, 1 if accumulate else 0,
+                                       dw.data_ptr(), lddw, ws.data_ptr(), nb, on.handle)
+    if rc:
+        raise B2GError(rc)
     on.uses(h, w, target, lse, grad_loss, dw)
     return dh, dw
 
 
 # ------------------------------------------------------------- gradient clipping
 
-def _tensor_list(tensors, name):
-    """(type code, pointer array, length array, device) of a list of contiguous tensors."""
-    torch = _t()
+def _tensor_list(tensors, name, dt=None, dev=None):
+    """(element type, device number, addresses, lengths) of a list of contiguous
+    tensors of one type on one device."""
+    if _torch is None:
+        _setup()
     if not tensors:
         raise ValueError(f"{name} must hold at least one tensor")
-    first = tensors[0]
-    code = _dtype(first, f"{name}[0]")
-    dt, dev = first.dtype, first.device
-    for i, t in enumerate(tensors):
-        if t.dtype is not dt or t.device != dev:
-            raise TypeError(f"{name}[{i}] must have the type and device of {name}[0]")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be contiguous")
-    n = len(tensors)
-    return (code, (ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
-            (ctypes.c_longlong * n)(*[t.numel() for t in tensors]), dev)
+    if dt is None:
+        first = tensors[0]
+        if not isinstance(first, _torch.Tensor) or first.dtype not in _CODES:
+            raise TypeError(f"{name} must hold torch.float32 or torch.bfloat16 tensors")
+        dt, dev = first.dtype, first.get_device()
+        if dev < 0:
+            raise TypeError(f"{name} must be on a CUDA device")
+    for t in tensors:
+        if t.dtype is not dt:
+            raise TypeError(f"every tensor of {name} must have the type {dt}")
+        if not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"every tensor of {name} must be contiguous and on cuda:{dev}")
+    return dt, dev, [t.data_ptr() for t in tensors], [t.numel() for t in tensors]
 
 
 def grad_norm(grads, stream=None):
@@ -403,27 +440,38 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
         raise ValueError("max_norm must not be negative")
     grads = list(grads)
     outs = grads if out is None else list(out)
-    return _norm(grads, outs, float(max_norm), stream)
+    return _norm(grads, outs, max_norm, stream)
 
 
 def _norm(grads, outs, max_norm, stream):
-    lib = train_library()
-    torch = _t()
-    code, ptrs, numels, dev = _tensor_list(grads, "grads")
-    n = len(grads)
-    on = _On(stream)
-    norm = on.empty((), torch.float32, dev)
-    ws, p, nb = _workspace(on, dev, lib.b2g_grad_norm_workspace_size, code, n, numels)
-    if outs is None:
-        _raise(lib.b2g_grad_norm(code, n, ptrs, numels, norm.data_ptr(), p, nb, on.handle))
-        on.uses(*grads)
-        return norm
+    dt, dev, ptrs, lens = _tensor_list(grads, "grads")
+    n = len(ptrs)
     optrs = ptrs
-    if outs is not grads:
-        ocode, optrs, olens, odev = _tensor_list(outs, "out")
-        if ocode != code or odev != dev or list(olens) != list(numels):
-            raise ValueError("out must hold tensors of the lengths and type of grads")
-    _raise(lib.b2g_clip_grad_norm(code, n, ptrs, numels, max_norm, optrs, norm.data_ptr(), p, nb,
-                                  on.handle))
-    on.uses(*grads, *outs)
+    if outs is not None and outs is not grads:
+        _, _, optrs, olens = _tensor_list(outs, "out", dt, dev)
+        if olens != lens:
+            raise ValueError("out must hold tensors of the lengths of grads")
+    on = _on(stream, dev)
+    device = grads[0].device
+    norm = on.empty((), _torch.float32, device)
+    code, table = _CODES[dt], _ADDRESSES(n)
+    addresses, lengths = table(*ptrs), table(*lens)
+    nb = _size(_lib.b2g_grad_norm_workspace_size, code, n, lengths)
+    ws = on.empty((nb,), _torch.uint8, device)
+    if outs is None:
+        rc = _lib.b2g_grad_norm(code, n, addresses, lengths, norm.data_ptr(), ws.data_ptr(), nb,
+                                on.handle)
+    else:
+        rc = _lib.b2g_clip_grad_norm(code, n, addresses, lengths, max_norm,
+                                     addresses if optrs is ptrs else table(*optrs),
+                                     norm.data_ptr(), ws.data_ptr(), nb, on.handle)
+    if rc:
+        raise B2GError(rc)
+    on.uses(*grads, *(outs or ()))
     return norm
+
+
+@functools.lru_cache(maxsize=None)
+def _ADDRESSES(n):
+    """The ctypes array type of n 64-bit addresses or lengths."""
+    return ctypes.c_longlong * n

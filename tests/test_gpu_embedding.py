@@ -61,6 +61,7 @@ CASES = [
     (1, 1, 1), (1, 7, 64), (2, 3, 5), (15, 4, 8), (16, 1000, 128), (17, 40, 33), (31, 300, 256),
     (257, 50, 129), (1000, 70000, 24), (2048, 17, 512), (4095, 5003, 100), (4097, 33, 40),
     (20000, 300, 16), (40001, 70001, 8), (128, 129, 4096), (33, 12, 9000),
+    (33000, 300001, 4),  # three digits
 ]
 
 
