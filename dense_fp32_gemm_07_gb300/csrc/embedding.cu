@@ -137,6 +137,23 @@ __device__ __noinline__ void clear_rows(const EmbSort& p, long long b, long long
   }
 }
 
+constexpr int kRounds = 4;
+
+// The keys of tokens i, i + 32, ... (kRounds of them, below hi): their ids, or
+// `vocab` for one that takes part in no sum.
+__device__ __forceinline__ void load_ids(const EmbSort& p, int i, int hi, unsigned (&k)[kRounds]) {
+  long long id[kRounds];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r)
+    id[r] = i + 32 * r < hi ? id_at(p.ids, p.id_bytes, i + 32 * r) : 0;
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const bool in = id[r] >= 0 && id[r] < p.vocab, pad = p.padding >= 0 && id[r] == p.padding;
+    if (!in && !pad && i + 32 * r < hi) atomicOr(p.status, kStatusIndex);
+    k[r] = in && !pad ? (unsigned)id[r] : (unsigned)p.vocab;
+  }
+}
+
 // The first cluster sorts, the other ones clear the table.  The sort: `passes`
 // stable passes over kDigitBits bits each, lowest first.  Warp w of the cluster
 // owns a contiguous range of the input.  It counts its digits; the block adds
@@ -168,25 +185,33 @@ __global__ void __launch_bounds__(kSortThreads)
   const int hi = lo + per < p.tokens ? lo + per : p.tokens;
   const unsigned below = (1u << lane) - 1u;
 
-  for (int i = lo + lane; i < hi; i += 32) {
-    const long long id = id_at(p.ids, p.id_bytes, i);
-    const bool in = id >= 0 && id < p.vocab;
-    if (!in && !(p.padding >= 0 && id == p.padding)) atomicOr(p.status, kStatusIndex);
-    p.key[0][i] = in && id != p.padding ? (unsigned)id : (unsigned)p.vocab;
-    p.pos[0][i] = i;
-  }
-  // (the lists are read past L1: the other blocks of the cluster write them too)
   unsigned* cnt = counts + warp * kDigits;
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * kDigitBits, src = pass & 1;
+    // (the lists are read past L1: the other blocks of the cluster write them too)
     const unsigned* key = src ? p.key[1] : p.key[0];
     const int* pos = src ? p.pos[1] : p.pos[0];
     unsigned* key_out = src ? p.key[0] : p.key[1];
     int* pos_out = src ? p.pos[0] : p.pos[1];
     for (int d = lane; d < kDigits; d += 32) cnt[d] = 0;
     __syncwarp();
-    for (int i = lo + lane; i < hi; i += 32)
-      atomicAdd(&cnt[(__ldcg(key + i) >> shift) & (kDigits - 1)], 1u);
+    // kRounds rounds of 32 pairs at a time, their loads together
+    unsigned k[kRounds];
+    for (int i0 = lo; i0 < hi; i0 += 32 * kRounds) {
+      if (pass == 0) {
+        load_ids(p, i0 + lane, hi, k);
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r)
+          if (i0 + 32 * r + lane < hi) p.key[0][i0 + 32 * r + lane] = k[r];
+      } else {
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r)
+          k[r] = i0 + 32 * r + lane < hi ? __ldcg(key + i0 + 32 * r + lane) : 0u;
+      }
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r)
+        if (i0 + 32 * r + lane < hi) atomicAdd(&cnt[(k[r] >> shift) & (kDigits - 1)], 1u);
+    }
     __syncthreads();
     // two threads per digit, 16 warps' counts each: counts become offsets in the block
     static_assert(kSortThreads == 2 * kDigits, "two threads per digit");
@@ -197,12 +222,20 @@ __global__ void __launch_bounds__(kSortThreads)
     for (int w = 0; w < kSortWarps / 2; ++w) mine += col[w * kDigits];
     const unsigned other = __shfl_xor_sync(0xffffffffu, mine, 1);
     unsigned at = threadIdx.x & 1 ? other : 0u;  // the digit's pairs in the warps before mine
-    if (!(threadIdx.x & 1)) p.totals[cta * kDigits + digit] = mine + other;
-    cluster_sync();
+    if (!(threadIdx.x & 1)) {
+      if (ctas > 1)
+        p.totals[cta * kDigits + digit] = mine + other;
+      else
+        first[digit] = mine + other;
+    }
+    if (ctas > 1)
+      cluster_sync();
+    else
+      __syncthreads();
     // where the digit's pairs begin: lower digits anywhere, this digit in earlier blocks
     if (threadIdx.x < kDigits) {
-      unsigned all = 0, earlier = 0;
-      for (int c = 0; c < ctas; ++c) {
+      unsigned all = ctas > 1 ? 0u : first[threadIdx.x], earlier = 0;
+      for (int c = 0; c < ctas && ctas > 1; ++c) {
         const unsigned t = __ldcg(p.totals + c * kDigits + threadIdx.x);
         all += t;
         earlier += c < cta ? t : 0u;
@@ -229,28 +262,39 @@ __global__ void __launch_bounds__(kSortThreads)
       at += n;
     }
     __syncthreads();
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-      const int i = i0 + lane;
-      const bool in = i < hi;
-      const unsigned k = in ? __ldcg(key + i) : 0u;
-      const int from = in ? __ldcg(pos + i) : 0;
-      const unsigned d = (k >> shift) & (kDigits - 1);
-      unsigned same = __ballot_sync(0xffffffffu, in);
+    const bool once = hi - lo <= 32 * kRounds;  // the keys are still in registers
+    for (int i0 = lo; i0 < hi; i0 += 32 * kRounds) {
+      int from[kRounds];
 #pragma unroll
-      for (int b = 0; b < kDigitBits; ++b) {
-        const unsigned one = __ballot_sync(0xffffffffu, (d >> b) & 1u);
-        same &= (d >> b) & 1u ? one : ~one;
+      for (int r = 0; r < kRounds; ++r) {
+        const int i = i0 + 32 * r + lane;
+        if (!once) k[r] = i < hi ? __ldcg(key + i) : 0u;
+        from[r] = pass == 0 ? i : i < hi ? __ldcg(pos + i) : 0;
       }
-      unsigned to = 0;
-      if (in) to = cnt[d] + __popc(same & below);
-      __syncwarp();
-      if (in) {
-        if ((same & below) == 0) cnt[d] += __popc(same);
-        key_out[to] = k, pos_out[to] = from;
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        const bool in = i0 + 32 * r + lane < hi;
+        const unsigned d = (k[r] >> shift) & (kDigits - 1);
+        unsigned same = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+        for (int b = 0; b < kDigitBits; ++b) {
+          const unsigned one = __ballot_sync(0xffffffffu, (d >> b) & 1u);
+          same &= (d >> b) & 1u ? one : ~one;
+        }
+        unsigned to = 0;
+        if (in) to = cnt[d] + __popc(same & below);
+        __syncwarp();
+        if (in) {
+          if ((same & below) == 0) cnt[d] += __popc(same);
+          key_out[to] = k[r], pos_out[to] = from[r];
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
-    cluster_sync();
+    if (ctas > 1)
+      cluster_sync();
+    else
+      __syncthreads();
   }
 }
 

@@ -12,8 +12,8 @@
 // once.
 //
 // Rows on 16-byte boundaries run on kernels that keep the next rows on their way
-// while one is worked on (registers in the forward pass, a ring of bulk copies in
-// shared memory in the backward pass); other rows are read element by element.
+// while one is worked on (a ring of bulk copies in shared memory); other rows are
+// read element by element.
 #include <atomic>
 
 #include "train_common.cuh"
@@ -110,86 +110,157 @@ __global__ void __launch_bounds__(512) ln_fwd_kernel(const __grid_constant__ LnF
   }
 }
 
-// Many rows: 16 warps per SM, G warps per row, each thread with NCH chunks of the
-// row at hand and the same chunks of its next row already on their way.  With two
-// warps a row, 8192 rows of 4096 BF16 values keep 128 KB an SM in flight.
-template <typename T, int VEC, int NCH, int G>
-__global__ void __launch_bounds__(512, 1) ln_fwd_rows_kernel(const __grid_constant__ LnFwd p) {
-  constexpr int NT = 32 * G, GROUPS = 16 / G;
+// Rows on 16-byte boundaries: one block an SM, in groups of `nt` threads with a row
+// each.  A group's first thread keeps `stages` rows on their way
+// into the group's ring in shared memory (bulk copies that arrive on a barrier per
+// slot; up to 192 KB an SM), so a row's latency is not waited for; a slot is
+// refilled once the group's first sum has been exchanged, when every thread has
+// read it.
+constexpr int kFwdThreads = 512, kBwdThreads = 256;  // 32 columns a thread in either
+constexpr int kRingBytes = 192 * 1024;
+constexpr int kRingStages = 16;  // at most
+
+struct Ring {
+  int nt, groups, stages;
+};
+
+struct RingPos {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) s = 0, ph ^= 1u;
+  }
+};
+
+// Two sums over a group's nt threads at once; `ex` is one of two exchange buffers
+// used by turns.
+__device__ __forceinline__ F2 group_sum2(F2 v, F2 (&ex)[16], int group, int nt) {
+  auto over = [&](F2 x, int o) {
+    float a, b;
+    f2_split(x, a, b);
+    return add2(x, f2(__shfl_xor_sync(0xffffffffu, a, o), __shfl_xor_sync(0xffffffffu, b, o)));
+  };
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = over(v, o);
+  const int warps = nt >> 5, lane = threadIdx.x & 31;
+  if (warps == 1) return v;
+  if (lane == 0) ex[threadIdx.x >> 5] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(nt) : "memory");
+  v = lane < warps ? ex[group * warps + lane] : f2(0.f, 0.f);
+#pragma unroll
+  for (int o = 8; o; o >>= 1)
+    if (o < warps) v = over(v, o);  // lanes 0 .. warps - 1 hold the sum
+  float a, b;
+  f2_split(v, a, b);
+  return f2(__shfl_sync(0xffffffffu, a, 0), __shfl_sync(0xffffffffu, b, 0));
+}
+// One sum.
+__device__ __forceinline__ float group_sum(float v, float (&ex)[16], int group, int nt) {
+  v = warp_sum(v);
+  const int warps = nt >> 5, lane = threadIdx.x & 31;
+  if (warps == 1) return v;
+  if (lane == 0) ex[threadIdx.x >> 5] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(nt) : "memory");
+  v = lane < warps ? ex[group * warps + lane] : 0.f;
+#pragma unroll
+  for (int o = 8; o; o >>= 1)
+    if (o < warps) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
+// NCH chunks a thread; FULL: every thread has all of them.  The weights stand in
+// shared memory after the rings: next to rings of this size L1 is too small to keep
+// them, and fetching them from L2 for every row took 43 us at 8192 x 4096 BF16, where this
+// takes 24 (5.5 TB/s).
+template <typename T, int VEC, int NCH, bool FULL>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    ln_fwd_ring_kernel(const __grid_constant__ LnFwd p, const __grid_constant__ Ring g,
+                       unsigned int* status, unsigned long long wait_limit_ns) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ __align__(8) unsigned long long bars[kFwdThreads / 32 * kRingStages];
   __shared__ float red[2][16];
+  constexpr int H = VEC / 2;
   pdl_launch_dependents();
+  const int group = threadIdx.x / g.nt, t = threadIdx.x - group * g.nt;
+  const uint32_t bytes = (uint32_t)(p.cols * (int)sizeof(T));
+  const uint32_t bar0 = smem_addr(bars) + 8u * (uint32_t)(group * kRingStages);
+  unsigned char* mine = ring + (size_t)group * g.stages * bytes;
+  T* ws = reinterpret_cast<T*>(ring + (size_t)g.groups * g.stages * bytes);
+  T* bs = ws + p.cols;
+  if (t == 0) {
+    for (int s = 0; s < g.stages; ++s) mbar_init(bar0 + 8u * s, 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
   pdl_wait();
-  const int group = threadIdx.x / NT, t = threadIdx.x % NT;
-  const T* w = static_cast<const T*>(p.w);
-  const T* b = static_cast<const T*>(p.b);
   const float inv = 1.f / (float)p.cols;
-  const long long step = (long long)gridDim.x * GROUPS;
-  long long row = (long long)group * gridDim.x + blockIdx.x;
-  Pack<T, VEC> next[NCH];
-  auto fetch = [&](long long r) {
-    const T* x = static_cast<const T*>(p.x) + r * p.ldx;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = t + i * NT;
-      if (c < p.chunks) next[i].load(x + c * VEC);
-    }
+  const long long step = (long long)gridDim.x * g.groups;
+  const long long row0 = (long long)group * gridDim.x + blockIdx.x;
+  auto issue = [&](long long row, int s) {
+    mbar_arrive_expect_tx(bar0 + 8u * s, bytes);
+    bulk_load(smem_addr(mine + (size_t)s * bytes), static_cast<const T*>(p.x) + row * p.ldx, bytes,
+              bar0 + 8u * s);
   };
-  // Sum over the group's threads; `k` alternates the exchange buffers.
-  auto total = [&](float v, int k) {
-    v = warp_sum(v);
-    if (G == 1) return v;
-    float* mine = red[k] + group * G;
-    if ((threadIdx.x & 31) == 0) mine[(threadIdx.x % NT) / 32] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(NT) : "memory");
-    float s = mine[0];
-#pragma unroll
-    for (int i = 1; i < G; ++i) s += mine[i];
-    return s;
-  };
-#pragma unroll
-  for (int i = 0; i < NCH; ++i) next[i].zero();
-  if (row < p.rows) fetch(row);
-  for (; row < p.rows; row += step) {
-    Pack<T, VEC> raw[NCH];
-    float sum = 0.f;
+  if (t == 0) {
+    long long row = row0;
+    for (int s = 0; s < g.stages && row < p.rows; ++s, row += step) issue(row, s);
+  }
+  for (int c = threadIdx.x; c < p.cols; c += kFwdThreads) {
+    ws[c] = p.w ? static_cast<const T*>(p.w)[c] : from_f32<T>(1.f);
+    bs[c] = p.b ? static_cast<const T*>(p.b)[c] : from_f32<T>(0.f);
+  }
+  __syncthreads();
+  RingPos at;
+  bool alive = true;  // false once a wait has run out: no more waits, no more copies
+  for (long long row = row0; row < p.rows; row += step) {
+    if (alive) alive = mbar_wait(bar0 + 8u * at.s, at.ph, wait_limit_ns, status, kStatusTimeoutFull);
+    const T* xs = reinterpret_cast<const T*>(mine + (size_t)at.s * bytes);
+    F2 x[NCH][H];
+    F2 s0 = f2(0.f, 0.f), s1 = f2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      raw[i] = next[i];
-      float f[VEC];
-      raw[i].get(f);
+      const int c = t + i * g.nt;
+      if (FULL || c < p.chunks) {
+        Pack<T, VEC> k;
+        k.load(xs + c * VEC);
+        k.get2(x[i]);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) sum += f[j];
-    }
-    if (row + step < p.rows) fetch(row + step);
-    const float mean = total(sum, 0) * inv;
-    float sq = 0.f;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      float f[VEC];
-      raw[i].get(f);
-      if (t + i * NT < p.chunks) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) sq = fmaf(f[j] - mean, f[j] - mean, sq);
+        for (int j = 0; j < H; j += 2) s0 = add2(s0, x[i][j]), s1 = add2(s1, x[i][j + 1]);
       }
     }
-    const float rstd = 1.f / sqrtf(total(sq, 1) * inv + p.eps);
+    const float mean = group_sum(f2_sum(add2(s0, s1)), red[0], group, g.nt) * inv;
+    if (t == 0 && alive && row + (long long)g.stages * step < p.rows)
+      issue(row + (long long)g.stages * step, at.s);
+    const F2 minus = f2(-mean, -mean);
+    s0 = s1 = f2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      if (FULL || t + i * g.nt < p.chunks) {
+#pragma unroll
+        for (int j = 0; j < H; j += 2) {
+          x[i][j] = add2(x[i][j], minus), x[i][j + 1] = add2(x[i][j + 1], minus);
+          s0 = fma2(x[i][j], x[i][j], s0), s1 = fma2(x[i][j + 1], x[i][j + 1], s1);
+        }
+      }
+    }
+    const float var = group_sum(f2_sum(add2(s0, s1)), red[1], group, g.nt) * inv;
+    const float rstd = 1.f / sqrtf(var + p.eps);
+    const F2 r2 = f2(rstd, rstd);
     T* y = static_cast<T*>(p.y) + row * p.ldy;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int c = t + i * NT;
-      if (c < p.chunks) {
+      const int c = t + i * g.nt;
+      if (FULL || c < p.chunks) {
         Pack<T, VEC> k;
-        float f[VEC], wf[VEC], bf[VEC];
-        raw[i].get(f);
-        k.zero();
-        if (w) k.load(w + c * VEC);
-        k.get(wf);
-        k.zero();
-        if (b) k.load(b + c * VEC);
-        k.get(bf);
+        F2 wf[H], bf[H];
+        k.load(ws + c * VEC);
+        k.get2(wf);
+        k.load(bs + c * VEC);
+        k.get2(bf);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) f[j] = fmaf((f[j] - mean) * rstd, w ? wf[j] : 1.f, bf[j]);
-        k.set(f);
+        for (int j = 0; j < H; ++j) x[i][j] = fma2(mul2(x[i][j], r2), wf[j], bf[j]);
+        k.set2(x[i]);
         k.store(y + c * VEC);
       }
     }
@@ -197,6 +268,7 @@ __global__ void __launch_bounds__(512, 1) ln_fwd_rows_kernel(const __grid_consta
       if (p.mean) p.mean[row] = mean;
       if (p.rstd) p.rstd[row] = rstd;
     }
+    at.next(g.stages);
   }
 }
 
@@ -334,38 +406,33 @@ __global__ void __launch_bounds__(512) ln_bwd_kernel(const __grid_constant__ LnB
   }
 }
 
-// The same for rows on 16-byte boundaries: one block of 512 threads an SM in groups
-// of NT threads, a row per group.  A group's first thread keeps `stages` rows of x
-// and dy on their way into the group's ring in shared memory (bulk copies that
-// arrive on a barrier per slot; 160 KB an SM), so the rows' latency is not waited
-// for; a slot is refilled once the group's sums have been exchanged, when every
-// thread has read it.  At the end the groups' column sums are added in shared
-// memory in group order.
-constexpr int kRingBytes = 160 * 1024;
-constexpr int kRingStages = 16;  // at most
-
-template <typename T, int VEC, int NCH>
-__global__ void __launch_bounds__(512, 1)
-    ln_bwd_ring_kernel(const __grid_constant__ LnBwd p, int nt, int stages,
+// Rows on 16-byte boundaries: the ring above with rows of x and dy together, 32
+// columns a thread (FULL: every thread has all of them).  With t = x - mean,
+//     dx = rstd g + (-rstd^3 mean(g t)) t - rstd mean(g),
+// two operations an element once g and t are there.  At the end the groups' column
+// sums are added in shared memory in group order.
+template <typename T, int VEC, bool FULL>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    ln_bwd_ring_kernel(const __grid_constant__ LnBwd p, const __grid_constant__ Ring g,
                        unsigned int* status, unsigned long long wait_limit_ns) {
   extern __shared__ __align__(128) unsigned char ring[];
-  __shared__ __align__(8) unsigned long long bars[512 / 32 * kRingStages];
-  __shared__ float red[2][2][16];
+  __shared__ __align__(8) unsigned long long bars[kBwdThreads / 32 * kRingStages];
+  __shared__ F2 red[2][16];
+  constexpr int H = VEC / 2, NCH = 32 / VEC;
   pdl_launch_dependents();
-  const int group = threadIdx.x / nt, t = threadIdx.x - group * nt, groups = 512 / nt;
-  const int warps = nt >> 5;
+  const int group = threadIdx.x / g.nt, t = threadIdx.x - group * g.nt;
   const uint32_t bytes = (uint32_t)(p.cols * (int)sizeof(T));
   const uint32_t bar0 = smem_addr(bars) + 8u * (uint32_t)(group * kRingStages);
-  unsigned char* mine = ring + (size_t)group * stages * 2 * bytes;
+  unsigned char* mine = ring + (size_t)group * g.stages * 2 * bytes;
   if (t == 0) {
-    for (int s = 0; s < stages; ++s) mbar_init(bar0 + 8u * s, 1);
+    for (int s = 0; s < g.stages; ++s) mbar_init(bar0 + 8u * s, 1);
     fence_mbar_init();
     fence_proxy_async_smem();
   }
   __syncthreads();
   pdl_wait();
   const float inv = 1.f / (float)p.cols;
-  const long long step = (long long)gridDim.x * groups;
+  const long long step = (long long)gridDim.x * g.groups;
   const long long row0 = (long long)group * gridDim.x + blockIdx.x;
   auto issue = [&](long long row, int s) {
     const uint32_t bar = bar0 + 8u * s, dst = smem_addr(mine + (size_t)s * 2 * bytes);
@@ -375,98 +442,94 @@ __global__ void __launch_bounds__(512, 1)
   };
   if (t == 0) {
     long long row = row0;
-    for (int s = 0; s < stages && row < p.rows; ++s, row += step) issue(row, s);
+    for (int s = 0; s < g.stages && row < p.rows; ++s, row += step) issue(row, s);
   }
-  float aw[NCH][VEC], ab[NCH][VEC];
-  Pack<T, VEC> wr[NCH];
+  F2 aw[NCH][H], ab[NCH][H], wf[NCH][H];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int c = t + i * nt;
-    wr[i].zero();
-    if (p.w && c < p.chunks) wr[i].load(static_cast<const T*>(p.w) + c * VEC);
+    const int c = t + i * g.nt;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) aw[i][j] = ab[i][j] = 0.f;
+    for (int j = 0; j < H; ++j) aw[i][j] = ab[i][j] = f2(0.f, 0.f), wf[i][j] = f2(1.f, 1.f);
+    if (p.w && c < p.chunks) {
+      Pack<T, VEC> k;
+      k.load(static_cast<const T*>(p.w) + c * VEC);
+      k.get2(wf[i]);
+    }
   }
   float mean = 0.f, rstd = 0.f;
   if (row0 < p.rows) mean = p.mean[row0], rstd = p.rstd[row0];
-  int s = 0, k = 0;
-  uint32_t ph = 0;
+  RingPos at;
+  int turn = 0;
   bool alive = true;  // false once a wait has run out: no more waits, no more copies
   for (long long row = row0; row < p.rows; row += step) {
-    const float m = mean, r = rstd;
+    const F2 m2 = f2(-mean, -mean), r2 = f2(rstd, rstd);
     if (row + step < p.rows) mean = p.mean[row + step], rstd = p.rstd[row + step];
-    if (alive)
-      alive = mbar_wait(bar0 + 8u * s, ph, wait_limit_ns, status, kStatusTimeoutFull);
-    const T* xs = reinterpret_cast<const T*>(mine + (size_t)s * 2 * bytes);
-    const T* ds = reinterpret_cast<const T*>(mine + (size_t)s * 2 * bytes + bytes);
-    Pack<T, VEC> xc[NCH], dc[NCH];
-    float s1 = 0.f, s2 = 0.f;  // sums of g and of g * xhat
+    if (alive) alive = mbar_wait(bar0 + 8u * at.s, at.ph, wait_limit_ns, status, kStatusTimeoutFull);
+    const T* xs = reinterpret_cast<const T*>(mine + (size_t)at.s * 2 * bytes);
+    const T* ds = reinterpret_cast<const T*>(mine + (size_t)at.s * 2 * bytes + bytes);
+    F2 x[NCH][H], gr[NCH][H];  // x - mean and g = dy * weight
+    F2 s1 = f2(0.f, 0.f), s2 = f2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int c = t + i * nt;
-      xc[i].zero(), dc[i].zero();
-      if (c < p.chunks) {
-        xc[i].load(xs + c * VEC), dc[i].load(ds + c * VEC);
-        float xf[VEC], df[VEC], wf[VEC];
-        xc[i].get(xf), dc[i].get(df), wr[i].get(wf);
+      const int c = t + i * g.nt;
+      if (FULL || c < p.chunks) {
+        Pack<T, VEC> k;
+        F2 d[H];
+        k.load(xs + c * VEC);
+        k.get2(x[i]);
+        k.load(ds + c * VEC);
+        k.get2(d);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float xh = (xf[j] - m) * r, g = p.w ? df[j] * wf[j] : df[j];
-          s1 += g, s2 = fmaf(g, xh, s2);
-          aw[i][j] = fmaf(df[j], xh, aw[i][j]), ab[i][j] += df[j];
+        for (int j = 0; j < H; ++j) {
+          x[i][j] = add2(x[i][j], m2);
+          gr[i][j] = mul2(d[j], wf[i][j]);
+          s1 = add2(s1, gr[i][j]), s2 = fma2(gr[i][j], x[i][j], s2);
+          aw[i][j] = fma2(d[j], mul2(x[i][j], r2), aw[i][j]), ab[i][j] = add2(ab[i][j], d[j]);
         }
       }
     }
-    s1 = warp_sum(s1), s2 = warp_sum(s2);
-    if (warps > 1) {
-      float(&ex)[2][16] = red[k];
-      if ((threadIdx.x & 31) == 0) ex[0][threadIdx.x >> 5] = s1, ex[1][threadIdx.x >> 5] = s2;
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(nt) : "memory");
-      s1 = s2 = 0.f;
-      for (int i = 0; i < warps; ++i) s1 += ex[0][group * warps + i], s2 += ex[1][group * warps + i];
-    }
-    if (t == 0 && alive && row + (long long)stages * step < p.rows)
-      issue(row + (long long)stages * step, s);
-    const float c1 = s1 * inv, c2 = s2 * inv;
+    const F2 sums2 = group_sum2(f2(f2_sum(s1), f2_sum(s2)), red[turn], group, g.nt);
+    if (t == 0 && alive && row + (long long)g.stages * step < p.rows)
+      issue(row + (long long)g.stages * step, at.s);
+    float sg, sgt, r, unused;
+    f2_split(sums2, sg, sgt), f2_split(r2, r, unused);
+    const float c1 = -r * (sg * inv), c2 = -r * (r * (r * (sgt * inv)));
+    const F2 k1 = f2(c1, c1), k2 = f2(c2, c2);
     T* dx = static_cast<T*>(p.dx) + row * p.lddx;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int c = t + i * nt;
-      if (c < p.chunks) {
-        float xf[VEC], df[VEC], wf[VEC], o[VEC];
-        xc[i].get(xf), dc[i].get(df), wr[i].get(wf);
+      const int c = t + i * g.nt;
+      if (FULL || c < p.chunks) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float xh = (xf[j] - m) * r, g = p.w ? df[j] * wf[j] : df[j];
-          o[j] = r * (g - c1 - xh * c2);
-        }
-        Pack<T, VEC> v;
-        v.set(o);
-        v.store(dx + c * VEC);
+        for (int j = 0; j < H; ++j) gr[i][j] = fma2(gr[i][j], r2, fma2(x[i][j], k2, k1));
+        Pack<T, VEC> k;
+        k.set2(gr[i]);
+        k.store(dx + c * VEC);
       }
     }
-    k ^= 1;
-    if (++s == stages) s = 0, ph ^= 1u;
+    turn ^= 1;
+    at.next(g.stages);
   }
   if (!p.part) return;
   __syncthreads();  // every ring is drained: its memory now takes the groups' sums
   float* sums = reinterpret_cast<float*>(ring);
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int c = t + i * nt;
-    if (c < p.chunks) {
+    const int c = t + i * g.nt;
+    if (FULL || c < p.chunks) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        sums[(size_t)(2 * group) * p.cols + c * VEC + j] = aw[i][j];
-        sums[(size_t)(2 * group + 1) * p.cols + c * VEC + j] = ab[i][j];
+      for (int j = 0; j < H; ++j) {
+        F2* q = reinterpret_cast<F2*>(sums + (size_t)2 * group * p.cols + c * VEC) + j;
+        q[0] = aw[i][j];
+        q[p.cols / 2] = ab[i][j];
       }
     }
   }
   __syncthreads();
   float* out = p.part + (size_t)blockIdx.x * 2 * p.cols;
-  for (int c = threadIdx.x; c < 2 * p.cols; c += 512) {
+  for (int c = threadIdx.x; c < 2 * p.cols; c += kBwdThreads) {
     float a = sums[c];
-    for (int g = 1; g < groups; ++g) a += sums[(size_t)2 * g * p.cols + c];
+    for (int i = 1; i < g.groups; ++i) a += sums[(size_t)2 * i * p.cols + c];
     out[c] = a;
   }
 }
@@ -516,12 +579,12 @@ __global__ void __launch_bounds__(256) ln_bwd_cols_kernel(const __grid_constant_
   pw[c] = aw, pw[p.cols + c] = ab;
 }
 
-// dweight (blockIdx.y == 0) and dbias (1): the partial rows added in order, a
-// quarter-interleaved set per warp, then the eight warps' sums in warp order.
+// dweight (blockIdx.y == 0) and dbias (1): warp y adds the partial rows y, y + 16,
+// ... in order, then the warps' sums are added in warp order.
 template <typename T>
-__global__ void __launch_bounds__(256) ln_bwd_reduce_kernel(const float* part, int parts, int cols,
+__global__ void __launch_bounds__(512) ln_bwd_reduce_kernel(const float* part, int parts, int cols,
                                                             T* dweight, T* dbias) {
-  __shared__ float acc[8][32];
+  __shared__ float acc[16][32];
   pdl_launch_dependents();
   pdl_wait();
   T* out = blockIdx.y ? dbias : dweight;
@@ -530,14 +593,14 @@ __global__ void __launch_bounds__(256) ln_bwd_reduce_kernel(const float* part, i
   float a = 0.f;
   if (c < cols) {
     const float* p0 = part + (size_t)blockIdx.y * cols + c;
-#pragma unroll 4
-    for (int i = threadIdx.y; i < parts; i += 8) a += p0[(size_t)i * 2 * cols];
+#pragma unroll 10
+    for (int i = threadIdx.y; i < parts; i += 16) a += p0[(size_t)i * 2 * cols];
   }
   acc[threadIdx.y][threadIdx.x] = a;
   __syncthreads();
   if (threadIdx.y == 0 && c < cols) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) a += acc[i][threadIdx.x];
+    for (int i = 1; i < 16; ++i) a += acc[i][threadIdx.x];
     out[c] = from_f32<T>(a);
   }
 }
@@ -567,26 +630,60 @@ cudaError_t fwd_kernel(int nch, dim3 grid, dim3 block, cudaStream_t st, const Ln
   return launch_train(ln_fwd_kernel<T, VEC, NCH>, grid, block, 0, st, p);
 }
 
-// Warps per row of the many-rows kernel (8 chunks a thread), 0 when 4 are too few.
-template <typename T, int VEC>
-cudaError_t fwd_rows(LnFwd p, int sms, cudaStream_t st) {
-  const long long warps = ceil_div(p.chunks, 256);
-  const int g = warps <= 1 ? 1 : warps <= 2 ? 2 : 4;
-  const long long blocks = ceil_div(p.rows, 16 / g);
-  const dim3 grid((unsigned)(blocks < sms ? blocks : sms)), block(512);
-  const int nch = (int)ceil_div(p.chunks, 32 * g);
-  if (g == 4) return launch_train(ln_fwd_rows_kernel<T, VEC, 8, 4>, grid, block, 0, st, p);
-  if (g == 2) return launch_train(ln_fwd_rows_kernel<T, VEC, 8, 2>, grid, block, 0, st, p);
-  if (nch <= 2) return launch_train(ln_fwd_rows_kernel<T, VEC, 2, 1>, grid, block, 0, st, p);
-  if (nch <= 4) return launch_train(ln_fwd_rows_kernel<T, VEC, 4, 1>, grid, block, 0, st, p);
-  return launch_train(ln_fwd_rows_kernel<T, VEC, 8, 1>, grid, block, 0, st, p);
+// The ring of a block of `threads` for rows of `cols` values of `es` bytes, `copies`
+// rows to a slot and at most 32 columns a thread, leaving `reserved` bytes; stages <
+// 2 when they do not fit.
+Ring ring_of(int threads, int cols, int es, int copies, int reserved) {
+  constexpr int per = 32;
+  Ring r{32, 0, 0};
+  while (r.nt < threads && r.nt * per < cols) r.nt *= 2;
+  r.groups = threads / r.nt;
+  if (r.nt * per < cols) return r;
+  const long long s = (kRingBytes - reserved) / ((long long)copies * cols * es * r.groups);
+  r.stages = (int)(s < kRingStages ? s : kRingStages);
+  return r;
+}
+Ring fwd_ring_of(int cols, int dtype) {
+  const int es = (int)type_size(dtype);
+  return ring_of(kFwdThreads, cols, es, 1, 2 * es * cols);
+}
+Ring bwd_ring_of(int cols, int dtype) { return ring_of(kBwdThreads, cols, (int)type_size(dtype), 2, 0); }
+
+// Opt in to the ring's shared memory, once per device and kernel.
+cudaError_t allow_ring(const void* kern, std::atomic<int> (&done)[64], int dev) {
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e == cudaSuccess) done[dev].store(1, std::memory_order_release);
+  return e;
+}
+
+template <typename T, int VEC, int NCH, bool FULL>
+cudaError_t fwd_ring(const LnFwd& p, const Ring& r, const TrainDevice& d, cudaStream_t st) {
+  static std::atomic<int> done[64];
+  const cudaError_t e =
+      allow_ring(reinterpret_cast<const void*>(&ln_fwd_ring_kernel<T, VEC, NCH, FULL>), done, d.dev);
+  if (e != cudaSuccess) return e;
+  const long long blocks = ceil_div(p.rows, r.groups);
+  return launch_train(ln_fwd_ring_kernel<T, VEC, NCH, FULL>,
+                      dim3((unsigned)(blocks < d.sms ? blocks : d.sms)), dim3(kFwdThreads),
+                      ((size_t)r.groups * r.stages + 2) * p.cols * sizeof(T), st, p, r,
+                      d.status, d.wait_limit_ns);
 }
 
 template <typename T, int VEC>
-cudaError_t fwd_launch(LnFwd p, int sms, cudaStream_t st) {
+cudaError_t fwd_launch(LnFwd p, int dtype, const TrainDevice& d, cudaStream_t st) {
+  const int sms = d.sms;
   p.chunks = p.cols / VEC;
   if constexpr (VEC > 1) {
-    if (p.rows > 4 * sms && p.chunks <= 1024) return fwd_rows<T, VEC>(p, sms, st);
+    const Ring r = fwd_ring_of(p.cols, dtype);
+    if (p.rows > 4 * sms && r.stages >= 2) {
+      constexpr int N = 32 / VEC;
+      if (p.chunks == r.nt * N) return fwd_ring<T, VEC, N, true>(p, r, d, st);
+      if (p.chunks <= r.nt * N / 2) return fwd_ring<T, VEC, N / 2, false>(p, r, d, st);
+      return fwd_ring<T, VEC, N, false>(p, r, d, st);
+    }
   }
   // Few rows: one chunk a thread, for the shortest path; many: several, for the
   // fewest barriers per byte.
@@ -599,27 +696,11 @@ cudaError_t fwd_launch(LnFwd p, int sms, cudaStream_t st) {
   return fwd_kernel<T, VEC>((int)ceil_div(p.chunks, nt), grid, block, st, p);
 }
 
-// The ring kernel's groups: threads a row (16 columns each), rows in the ring;
-// stages == 0 when a row is too wide for it.
-struct Ring {
-  int nt, groups, stages;
-};
-Ring ring_of(int cols, int dtype) {
-  Ring r{32, 0, 0};
-  while (r.nt < 512 && r.nt * 16 < cols) r.nt *= 2;
-  r.groups = 512 / r.nt;
-  if (r.nt * 16 < cols) return r;
-  const long long pair = 2LL * cols * (long long)type_size(dtype);
-  const long long s = kRingBytes / (pair * r.groups);
-  r.stages = (int)(s < kRingStages ? s : kRingStages);
-  return r;
-}
-
 // Blocks of a backward kernel, each leaving one partial row of dweight and of
 // dbias: one an SM in the ring kernel, up to four rows a block otherwise, at most
 // four blocks an SM (the partial rows stay a small share of the traffic).
 int bwd_parts(long long rows, int cols, int dtype, int sms, bool vec) {
-  const Ring r = ring_of(cols, dtype);
+  const Ring r = bwd_ring_of(cols, dtype);
   const long long most = vec && r.stages >= 2 ? sms : 4LL * sms;
   const long long fair = ceil_div(rows, vec && r.stages >= 2 ? r.groups : 4);
   return (int)(fair < most ? fair : most);
@@ -633,25 +714,18 @@ cudaError_t bwd_kernel(int nch, dim3 grid, dim3 block, cudaStream_t st, const Ln
   return launch_train(ln_bwd_kernel<T, VEC, NCH>, grid, block, 0, st, p);
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool FULL>
 cudaError_t bwd_ring(const LnBwd& p, const Ring& r, int parts, const TrainDevice& d,
                      cudaStream_t st) {
-  static std::atomic<int> configured[64];
-  constexpr int NCH = 16 / VEC;
+  static std::atomic<int> done[64];
+  const cudaError_t e =
+      allow_ring(reinterpret_cast<const void*>(&ln_bwd_ring_kernel<T, VEC, FULL>), done, d.dev);
+  if (e != cudaSuccess) return e;
   // the rings, and at the end the groups' column sums (64 KB at most)
   const size_t rings = (size_t)r.groups * r.stages * 2 * p.cols * sizeof(T);
   const size_t sums = (size_t)r.groups * 2 * p.cols * sizeof(float);
-  const size_t smem = rings > sums ? rings : sums;
-  if (d.dev < 0 || d.dev >= 64) return cudaErrorInvalidDevice;
-  if (!configured[d.dev].load(std::memory_order_acquire)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(ln_bwd_ring_kernel<T, VEC, NCH>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-    if (e != cudaSuccess) return e;
-    configured[d.dev].store(1, std::memory_order_release);
-  }
-  return launch_train(ln_bwd_ring_kernel<T, VEC, NCH>, dim3(parts), dim3(512), smem, st, p, r.nt,
-                      r.stages, d.status, d.wait_limit_ns);
+  return launch_train(ln_bwd_ring_kernel<T, VEC, FULL>, dim3(parts), dim3(kBwdThreads),
+                      rings > sums ? rings : sums, st, p, r, d.status, d.wait_limit_ns);
 }
 
 template <typename T, int VEC>
@@ -660,10 +734,14 @@ cudaError_t bwd_launch(LnBwd p, int dtype, T* dweight, T* dbias, int parts, cons
   p.chunks = p.cols / VEC;
   cudaError_t e = cudaSuccess;
   const int nt = row_threads(p.chunks, kMaxBwd<VEC>);
-  const Ring r = ring_of(p.cols, dtype);
+  const Ring r = bwd_ring_of(p.cols, dtype);
   bool done = false;
   if constexpr (VEC > 1) {
-    if (r.stages >= 2) e = bwd_ring<T, VEC>(p, r, parts, d, st), done = true;
+    if (r.stages >= 2) {
+      e = r.nt * 32 == p.cols ? bwd_ring<T, VEC, true>(p, r, parts, d, st)
+                              : bwd_ring<T, VEC, false>(p, r, parts, d, st);
+      done = true;
+    }
   }
   if (done) {
   } else if (nt) {
@@ -677,7 +755,7 @@ cudaError_t bwd_launch(LnBwd p, int dtype, T* dweight, T* dbias, int parts, cons
   }
   if (e == cudaSuccess && p.part)
     e = launch_train(ln_bwd_reduce_kernel<T>, dim3((unsigned)ceil_div(p.cols, 32), 2),
-                     dim3(32, 8), 0, st, (const float*)p.part, parts, p.cols, dweight, dbias);
+                     dim3(32, 16), 0, st, (const float*)p.part, parts, p.cols, dweight, dbias);
   return e;
 }
 
@@ -719,8 +797,8 @@ int b2g_layernorm(int dtype, long long rows, int cols, const void* x, long long 
   const bool v = vec16(x) && vec16(y) && vec16(weight) && vec16(bias) && vec16_ld(ldx, dtype) &&
                  vec16_ld(ldy, dtype) && vec16_ld(cols, dtype);
   if (dtype == B2G_F32)
-    return launch_code(v ? fwd_launch<float, 4>(p, d.sms, st) : fwd_launch<float, 1>(p, d.sms, st));
-  return launch_code(v ? fwd_launch<Bf16, 8>(p, d.sms, st) : fwd_launch<Bf16, 1>(p, d.sms, st));
+    return launch_code(v ? fwd_launch<float, 4>(p, dtype, d, st) : fwd_launch<float, 1>(p, dtype, d, st));
+  return launch_code(v ? fwd_launch<Bf16, 8>(p, dtype, d, st) : fwd_launch<Bf16, 1>(p, dtype, d, st));
 }
 
 int b2g_layernorm_backward_workspace_size(int dtype, long long rows, int cols, size_t* bytes) {

@@ -27,6 +27,38 @@ int train_device(TrainDevice* out);  // 0 or a B2G_ERR_* code (host.cu)
 
 using Bf16 = __nv_bfloat16;
 
+// Two FP32 values in a 64-bit register pair, for the packed FP32 instructions
+// (each lane rounded like the scalar one).
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f2_split(F2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ float f2_sum(F2 v) {
+  float a, b;
+  f2_split(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(Bf16 x) { return __bfloat162float(x); }
 template <typename T>
@@ -60,6 +92,18 @@ struct Pack {
         f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
       }
     }
+  }
+  __device__ __forceinline__ void get2(F2 (&f)[VEC / 2]) const {
+    float g[VEC];
+    get(g);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) f[i] = f2(g[2 * i], g[2 * i + 1]);
+  }
+  __device__ __forceinline__ void set2(const F2 (&f)[VEC / 2]) {
+    float g[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) f2_split(f[i], g[2 * i], g[2 * i + 1]);
+    set(g);
   }
   __device__ __forceinline__ void set(const float (&f)[VEC]) {
     uint32_t w[4];
