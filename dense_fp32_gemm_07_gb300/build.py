@@ -6,6 +6,10 @@ shared library with the CUDA runtime linked statically.  `-Xptxas -v` output
 and the build fails when ptxas reports a register spill in any kernel: the
 packed FFMA kernels are capped at 128 registers to keep three CTAs per SM, and
 a spill there would otherwise show up only as a quiet loss of speed.
+
+csrc/train_binding.cpp, the native side of the tensor calls in train.py, is
+compiled next to them with the host compiler against the installed torch and
+linked into _train_binding.so.
 """
 from __future__ import annotations
 
@@ -15,11 +19,13 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "build")
 LIB = os.path.join(PKG, "libb2g_sgemm.so")
+BINDING = os.path.join(PKG, "_train_binding.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -44,9 +50,9 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -86,20 +92,65 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _torch_paths():
+    """(include, library) directories of the installed torch."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    return ([os.path.join(root, "include"),
+             os.path.join(root, "include", "torch", "csrc", "api", "include")],
+            os.path.join(root, "lib"))
+
+
+def _compile_binding() -> str:
+    """csrc/train_binding.cpp -> build/train_binding.o."""
+    import torch
+
+    cxx = shutil.which("g++") or "g++"
+    obj = os.path.join(BUILD, "train_binding.o")
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    abi = int(getattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", True))
+    cmd = [cxx, "-O1", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", INCLUDE, "-I", os.path.join(cuda, "include"),
+           "-I", sysconfig.get_paths()["include"]]
+    for d in _torch_paths()[0]:
+        cmd += ["-isystem", d]
+    cmd += ["-c", os.path.join(CSRC, "train_binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on train_binding.cpp:\n{r.stderr[-4000:]}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    lib = _torch_paths()[1]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", PKG, "-lb2g_sgemm",
+           "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stderr[-4000:]}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build the library if any source is newer than it; return its path."""
+    """Build the library and the binding if any source is newer; return the library's path."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, srcs))
+        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     if verbose:
         for s in srcs:
             with open(os.path.join(BUILD, f"ptxas_{s[:-3]}.log")) as f:

@@ -10,6 +10,10 @@ to it.  Matrices are 2-D with unit column stride; their row stride is the
 leading dimension.  Argument errors raise TypeError or ValueError, library error
 codes ``B2GError``; ids and targets out of range are reported by ``b2g_status``
 (``B2G_ERR_INDEX``), since finding them would need a synchronisation.
+
+Calls with plain arguments (contiguous operands, results allocated by the call,
+the current stream) go straight through the native binding
+(csrc/train_binding.cpp); the checks here serve all others and name what is wrong.
 """
 from __future__ import annotations
 
@@ -68,16 +72,29 @@ def train_library():
     return lib
 
 
+_fast = None   # the native binding
 _torch = None
 _CODES = {}  # torch element type -> the library's code
 
 
 def _setup():
-    """torch, and the table of element types, on first use."""
-    global _torch
+    """torch, the table of element types, the library and its native binding, on
+    first use.  There is no fallback where they have not been built."""
+    global _torch, _fast
+    train_library()
     _torch = _t()
     _CODES.update({_torch.float32: B2G_F32, _torch.bfloat16: B2G_BF16})
-    train_library()
+    from . import _train_binding
+
+    _fast = _train_binding
+    return _fast
+
+
+def _plain(got):
+    """What the binding answered for plain arguments: a result or an error code."""
+    if got.__class__ is int:
+        raise B2GError(got)
+    return got
 
 
 # The checks below run in every call; each looks at as few attributes as it can
@@ -227,6 +244,10 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
     x is rows x cols; weight and bias are vectors of cols elements of its type
     (None: ones, zeros).  mean and rstd are float32 vectors for the backward pass.
     `out` takes y and may be x itself."""
+    if out is None and stream is None:
+        got = (_fast or _setup()).layer_norm(x, weight, bias, eps)
+        if got is not None:
+            return _plain(got)
     r, c, ldx = _matrix(x, "x")
     dt, device, dev = x.dtype, x.device, x.get_device()
     pw, pb = _vector(weight, "weight", c, dt, dev), _vector(bias, "bias", c, dt, dev)
@@ -252,6 +273,10 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, out=None, 
 
     weight, mean and rstd as in the forward call; dweight is None when weight is
     None, dbias when `bias` is false.  `out` takes dx and may be dy itself."""
+    if out is None and stream is None:
+        got = (_fast or _setup()).layer_norm_backward(dy, x, weight, mean, rstd, bias)
+        if got is not None:
+            return _plain(got)
     r, c, ldx = _matrix(x, "x")
     dt, device, dev = x.dtype, x.device, x.get_device()
     rd, cd, lddy = _matrix(dy, "dy", dt, dev)
@@ -287,6 +312,10 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, out=None, 
 
 def embedding(ids, table, scale: float = 1.0, out=None, stream=None):
     """scale * table[ids], one row per id; an id out of range gives a row of NaN."""
+    if out is None and stream is None:
+        got = (_fast or _setup()).embedding(ids, table, scale)
+        if got is not None:
+            return _plain(got)
     v, d, ldt = _matrix(table, "table")
     dt, device, dev = table.dtype, table.device, table.get_device()
     pi, n, width = _indices(ids, "ids", dev)
@@ -309,6 +338,10 @@ def embedding_backward(ids, dout, num_rows: int, scale: float = 1.0, out=None,
     """The gradient of a table of num_rows rows: row v is scale times the sum of
     the rows of dout whose id is v, except padding_idx.  With `accumulate` it is
     added to `out`'s values (only rows with a token are touched)."""
+    if out is None and padding_idx is None and stream is None and not accumulate:
+        got = (_fast or _setup()).embedding_backward(ids, dout, num_rows, scale)
+        if got is not None:
+            return _plain(got)
     n, d, ldd = _matrix(dout, "dout")
     dt, device, dev = dout.dtype, dout.device, dout.get_device()
     pi, ni, width = _indices(ids, "ids", dev)
@@ -347,6 +380,10 @@ def linear_cross_entropy(h, w, target, ignore_index: int = -100, stream=None):
     h is tokens x width, w vocab x width, target a vector of class numbers.
     loss_i = lse_i - logit_{i, target_i}, 0 where target_i is ignore_index; lse is
     the log of the sum of the exponentials.  Both are float32 vectors."""
+    if stream is None:
+        got = (_fast or _setup()).linear_cross_entropy(h, w, target, ignore_index)
+        if got is not None:
+            return _plain(got)
     n, d, ldh = _matrix(h, "h")
     dt, device, dev = h.dtype, h.device, h.get_device()
     v, dw, ldw = _matrix(w, "w", dt, dev)
@@ -374,6 +411,11 @@ def linear_cross_entropy_backward(h, w, target, lse, grad_loss, ignore_index: in
     lse is the forward call's; grad_loss a float32 vector, one weight per row
     (1 / n for a mean over n rows).  `dw` takes the head's gradient; with
     `accumulate` it is added to the values there."""
+    if dw is None and stream is None and not accumulate:
+        got = (_fast or _setup()).linear_cross_entropy_backward(h, w, target, lse, grad_loss,
+                                                               ignore_index)
+        if got is not None:
+            return _plain(got)
     n, d, ldh = _matrix(h, "h")
     dt, device, dev = h.dtype, h.device, h.get_device()
     v, dv, ldw = _matrix(w, "w", dt, dev)
@@ -429,7 +471,12 @@ def _tensor_list(tensors, name, dt=None, dev=None):
 
 def grad_norm(grads, stream=None):
     """The 2-norm of all elements of the tensors in the list, a 0-d float32 tensor."""
-    return _norm(list(grads), None, None, stream)
+    grads = list(grads)
+    if stream is None:
+        got = (_fast or _setup()).clip(grads)
+        if got is not None:
+            return _plain(got)
+    return _norm(grads, None, None, stream)
 
 
 def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
@@ -440,6 +487,10 @@ def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
         raise ValueError("max_norm must not be negative")
     grads = list(grads)
     outs = grads if out is None else list(out)
+    if stream is None:
+        got = (_fast or _setup()).clip(grads, outs, max_norm)
+        if got is not None:
+            return _plain(got)
     return _norm(grads, outs, max_norm, stream)
 
 
