@@ -90,7 +90,7 @@ constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int kSortSmem = (kSortWarps + 1) * kDigits * 4;
 
 struct EmbSort {
-  int tokens, vocab, passes;
+  int tokens, vocab, passes, bits;  // bits a pass, at most kDigitBits
   const void* ids;
   int id_bytes;
   long long padding;
@@ -155,7 +155,7 @@ __device__ __forceinline__ void load_ids(const EmbSort& p, int i, int hi, unsign
 }
 
 // The first cluster sorts, the other ones clear the table.  The sort: `passes`
-// stable passes over kDigitBits bits each, lowest first.  Warp w of the cluster
+// stable passes over `bits` bits each (at most kDigitBits), lowest first.  Warp w of the cluster
 // owns a contiguous range of the input.  It counts its digits; the block adds
 // the counts up digit by digit and shares its totals with the cluster, so that
 // each block knows where its pairs of a digit begin; and each warp then places its
@@ -174,7 +174,9 @@ __global__ void __launch_bounds__(kSortThreads)
     clear_rows(p, (long long)blockIdx.x - ctas, (long long)gridDim.x - ctas);
     return;
   }
-  unsigned* first = counts + kSortWarps * kDigits;
+  const int digits = 1 << p.bits;
+  const unsigned mask = (unsigned)digits - 1u;
+  unsigned* first = counts + kSortWarps * digits;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
   const int W = ctas * kSortWarps;
   const int gw = cta * kSortWarps + warp;
@@ -185,15 +187,15 @@ __global__ void __launch_bounds__(kSortThreads)
   const int hi = lo + per < p.tokens ? lo + per : p.tokens;
   const unsigned below = (1u << lane) - 1u;
 
-  unsigned* cnt = counts + warp * kDigits;
+  unsigned* cnt = counts + warp * digits;
   for (int pass = 0; pass < p.passes; ++pass) {
-    const int shift = pass * kDigitBits, src = pass & 1;
+    const int shift = pass * p.bits, src = pass & 1;
     // (the lists are read past L1: the other blocks of the cluster write them too)
     const unsigned* key = src ? p.key[1] : p.key[0];
     const int* pos = src ? p.pos[1] : p.pos[0];
     unsigned* key_out = src ? p.key[0] : p.key[1];
     int* pos_out = src ? p.pos[0] : p.pos[1];
-    for (int d = lane; d < kDigits; d += 32) cnt[d] = 0;
+    for (int d = lane; d < digits; d += 32) cnt[d] = 0;
     __syncwarp();
     // kRounds rounds of 32 pairs at a time, their loads together
     unsigned k[kRounds];
@@ -210,19 +212,20 @@ __global__ void __launch_bounds__(kSortThreads)
       }
 #pragma unroll
       for (int r = 0; r < kRounds; ++r)
-        if (i0 + 32 * r + lane < hi) atomicAdd(&cnt[(k[r] >> shift) & (kDigits - 1)], 1u);
+        if (i0 + 32 * r + lane < hi) atomicAdd(&cnt[(k[r] >> shift) & mask], 1u);
     }
     __syncthreads();
-    // two threads per digit, 16 warps' counts each: counts become offsets in the block
-    static_assert(kSortThreads == 2 * kDigits, "two threads per digit");
-    const int digit = threadIdx.x >> 1;
-    unsigned* col = counts + (threadIdx.x & 1) * (kSortWarps / 2) * kDigits + digit;
-    unsigned mine = 0;
-#pragma unroll 8
-    for (int w = 0; w < kSortWarps / 2; ++w) mine += col[w * kDigits];
+    // Two neighbouring threads per digit, 16 warps' counts each: counts become
+    // offsets in the block.
+    const int digit = threadIdx.x >> 1, half = threadIdx.x & 1;
+    unsigned* col = counts + half * (kSortWarps / 2) * digits + digit;
+    unsigned n[kSortWarps / 2], mine = 0;
+    if (digit < digits) {
+#pragma unroll
+      for (int w = 0; w < kSortWarps / 2; ++w) mine += n[w] = col[w * digits];
+    }
     const unsigned other = __shfl_xor_sync(0xffffffffu, mine, 1);
-    unsigned at = threadIdx.x & 1 ? other : 0u;  // the digit's pairs in the warps before mine
-    if (!(threadIdx.x & 1)) {
+    if (!half && digit < digits) {
       if (ctas > 1)
         p.totals[cta * kDigits + digit] = mine + other;
       else
@@ -234,11 +237,14 @@ __global__ void __launch_bounds__(kSortThreads)
       __syncthreads();
     // where the digit's pairs begin: lower digits anywhere, this digit in earlier blocks
     if (threadIdx.x < kDigits) {
-      unsigned all = ctas > 1 ? 0u : first[threadIdx.x], earlier = 0;
-      for (int c = 0; c < ctas && ctas > 1; ++c) {
-        const unsigned t = __ldcg(p.totals + c * kDigits + threadIdx.x);
-        all += t;
-        earlier += c < cta ? t : 0u;
+      unsigned all = 0, earlier = 0;
+      if ((int)threadIdx.x < digits) {
+        if (ctas == 1) all = first[threadIdx.x];
+        for (int c = 0; c < ctas && ctas > 1; ++c) {
+          const unsigned t = __ldcg(p.totals + c * kDigits + threadIdx.x);
+          all += t;
+          earlier += c < cta ? t : 0u;
+        }
       }
       unsigned incl = all;
 #pragma unroll
@@ -251,15 +257,16 @@ __global__ void __launch_bounds__(kSortThreads)
       unsigned lower = 0;
 #pragma unroll
       for (int w = 0; w < kDigits / 32; ++w) lower += w < warp ? scan[w] : 0u;
-      first[threadIdx.x] = lower + incl - all + earlier;
+      if ((int)threadIdx.x < digits) first[threadIdx.x] = lower + incl - all + earlier;
     }
     __syncthreads();
-    at += first[digit];
-#pragma unroll 4
-    for (int w = 0; w < kSortWarps / 2; ++w) {
-      const unsigned n = col[w * kDigits];
-      col[w * kDigits] = at;
-      at += n;
+    if (digit < digits) {
+      unsigned at = first[digit] + (half ? other : 0u);
+#pragma unroll
+      for (int w = 0; w < kSortWarps / 2; ++w) {
+        col[w * digits] = at;
+        at += n[w];
+      }
     }
     __syncthreads();
     const bool once = hi - lo <= 32 * kRounds;  // the keys are still in registers
@@ -274,12 +281,14 @@ __global__ void __launch_bounds__(kSortThreads)
 #pragma unroll
       for (int r = 0; r < kRounds; ++r) {
         const bool in = i0 + 32 * r + lane < hi;
-        const unsigned d = (k[r] >> shift) & (kDigits - 1);
+        const unsigned d = (k[r] >> shift) & mask;
         unsigned same = __ballot_sync(0xffffffffu, in);
 #pragma unroll
         for (int b = 0; b < kDigitBits; ++b) {
-          const unsigned one = __ballot_sync(0xffffffffu, (d >> b) & 1u);
-          same &= (d >> b) & 1u ? one : ~one;
+          if (b < p.bits) {
+            const unsigned one = __ballot_sync(0xffffffffu, (d >> b) & 1u);
+            same &= (d >> b) & 1u ? one : ~one;
+          }
         }
         unsigned to = 0;
         if (in) to = cnt[d] + __popc(same & below);
@@ -339,15 +348,15 @@ __device__ __forceinline__ void get_part(const float* q, float (&a)[VEC]) {
   }
 }
 
-// A sum of one run's columns, scaled and stored (or added) as one final row chunk.
+// A sum of one run's columns, scaled and stored as one final row chunk; `old` is
+// what was there, for accumulate.
 template <typename T, int VEC>
-__device__ __forceinline__ void put_row(const EmbSum& p, unsigned row, int c, const float (&a)[VEC]) {
-  T* t = static_cast<T*>(p.dtable) + (long long)row * p.ldt + c * VEC;
+__device__ __forceinline__ void put_row(const EmbSum& p, unsigned row, int c, const float (&a)[VEC],
+                                        const Pack<T, VEC>& old) {
   float f[VEC];
   Pack<T, VEC> k;
   if (p.accumulate) {
-    k.load(t);
-    k.get(f);
+    old.get(f);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) f[j] = fmaf(a[j], p.scale, f[j]);
   } else {
@@ -355,55 +364,81 @@ __device__ __forceinline__ void put_row(const EmbSum& p, unsigned row, int c, co
     for (int j = 0; j < VEC; ++j) f[j] = a[j] * p.scale;
   }
   k.set(f);
-  k.store(t);
+  k.store(static_cast<T*>(p.dtable) + (long long)row * p.ldt + c * VEC);
 }
 
+constexpr int kMaxWindow = 128;
+
 // blockDim.x threads share a window's columns (one chunk each), blockDim.y
-// windows per block; blockIdx.y covers wider rows.  The rows of the next four
-// tokens are in flight while the last four are added.
-template <typename T, int VEC>
+// windows per block; blockIdx.y covers wider rows.  The window's ids and places are
+// fetched into shared memory first, so that only the rows themselves are waited
+// for, U at a time.  Runs that begin before the window or continue after it go
+// to the window's partial rows.
+template <typename T, int VEC, int U, bool ACC>
 __global__ void __launch_bounds__(256) emb_window_kernel(const __grid_constant__ EmbSum p) {
+  extern __shared__ unsigned keys[];  // blockDim.y windows' ids, then their places
+  int* places = reinterpret_cast<int*>(keys + blockDim.y * p.window);
   pdl_launch_dependents();
   pdl_wait();
+  const long long first_token = (long long)blockIdx.x * blockDim.y * p.window;
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+  for (int i = tid; i < (int)blockDim.y * p.window; i += 256) {
+    const bool in = first_token + i < p.tokens;
+    keys[i] = in ? p.key[first_token + i] : 0u;
+    places[i] = in ? p.pos[first_token + i] : 0;
+  }
   const int w = blockIdx.x * blockDim.y + threadIdx.y;
   const int c = blockIdx.y * blockDim.x + threadIdx.x;
   const long long begin = (long long)w * p.window;
-  if (begin >= p.tokens || c >= p.chunks) return;
+  const bool mine = begin < p.tokens && c < p.chunks;
   const int b = (int)begin, e = b + p.window < p.tokens ? b + p.window : p.tokens;
-  const unsigned vocab = (unsigned)p.vocab;
+  const unsigned before = mine && b > 0 ? p.key[b - 1] : ~0u;  // no id is ~0
+  const unsigned after = mine && e < p.tokens ? p.key[e] : ~0u;
+  __syncthreads();
+  if (!mine) return;
+  const unsigned* key = keys + threadIdx.y * p.window - b;
+  const int* pos = places + threadIdx.y * p.window - b;
+  const unsigned vocab = (unsigned)p.vocab, key_b = key[b];
   const T* dout = static_cast<const T*>(p.dout) + c * VEC;
-  const bool from_before = b > 0 && p.key[b - 1] == p.key[b];
-  const bool to_after = e < p.tokens && p.key[e] == p.key[e - 1];
-  bool first = true;
-  unsigned run = p.key[b];
+  const T* table = static_cast<const T*>(p.dtable) + c * VEC;
+  const bool from_before = before == key_b;
+  float* part = p.part + (size_t)w * 2 * p.width + c * VEC;
+  // The rows of U tokens at a time, and for accumulate the old values of the runs
+  // that end among them.
+  Pack<T, VEC> v[U], old[U], none, held;  // held: of the last token before these
+  none.zero(), held.zero();
   float a[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; ++j) a[j] = 0.f;
-  float* part = p.part + (size_t)w * 2 * p.width + c * VEC;
-  auto flush = [&](bool last) {
+  unsigned run = key_b;
+  bool first = true;
+  auto flush = [&](bool last, const Pack<T, VEC>& was) {
     if (run < vocab) {
-      const bool head = first && from_before, tail = last && to_after;
+      const bool head = first && from_before, tail = last && run == after;
       if (head || tail)
         put_part<VEC>(head ? part : part + p.width, a);
       else
-        put_row<T, VEC>(p, run, c, a);
+        put_row<T, VEC>(p, run, c, a, was);
     }
   };
-  constexpr int U = 4;
-  for (int i = b; i < e; i += U) {
-    unsigned key[U];
-    Pack<T, VEC> v[U];
+  for (int i0 = b; i0 < e; i0 += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      key[u] = i + u < e ? p.key[i + u] : vocab;
+      const int i = i0 + u;
       v[u].zero();
-      if (key[u] < vocab) v[u].load(dout + (long long)p.pos[i + u] * p.ldd);
+      if (i < e && key[i] < vocab) v[u].load(dout + (long long)pos[i] * p.ldd);
+      if (ACC) {  // what the run ending at i adds to
+        old[u].zero();
+        if (i < e && key[i] < vocab && (i + 1 == e || key[i + 1] != key[i]))
+          old[u].load(table + (long long)key[i] * p.ldt);
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i + u < e && key[u] != run) {
-        flush(false);
-        first = false, run = key[u];
+      const unsigned k = i0 + u < e ? key[i0 + u] : run;
+      if (k != run) {
+        flush(false, ACC ? (u ? old[u - 1] : held) : none);
+        first = false, run = k;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) a[j] = 0.f;
       }
@@ -411,9 +446,11 @@ __global__ void __launch_bounds__(256) emb_window_kernel(const __grid_constant__
       v[u].get(f);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) a[j] += f[j];
+      if (ACC && i0 + u + 1 == e) held = old[u];
     }
+    if (ACC && i0 + U < e) held = old[U - 1];
   }
-  flush(true);
+  flush(true, ACC ? held : none);
 }
 
 // The run that begins in window w and continues past it: its last partial row,
@@ -426,9 +463,13 @@ __global__ void __launch_bounds__(256) emb_join_kernel(const __grid_constant__ E
   const int c = blockIdx.y * blockDim.x + threadIdx.x;
   const long long begin = (long long)w * p.window, end = begin + p.window;
   if (end >= p.tokens || c >= p.chunks) return;
-  const unsigned run = p.key[end - 1];
-  if (run >= (unsigned)p.vocab || p.key[end] != run) return;       // it ends here
-  if (begin > 0 && p.key[begin - 1] == run) return;  // it began in an earlier window
+  const unsigned run = p.key[end - 1], next = p.key[end];
+  const unsigned first = p.key[begin], before = begin > 0 ? p.key[begin - 1] : ~0u;
+  if (run >= (unsigned)p.vocab || next != run) return;  // it ends here
+  if (first == run && before == run) return;            // it began in an earlier window
+  Pack<T, VEC> old;
+  old.zero();
+  if (p.accumulate) old.load(static_cast<const T*>(p.dtable) + (long long)run * p.ldt + c * VEC);
   float a[VEC];
   get_part<VEC>(p.part + ((size_t)w * 2 + 1) * p.width + c * VEC, a);
   // the windows that begin with the run, eight at a time
@@ -455,7 +496,7 @@ __global__ void __launch_bounds__(256) emb_join_kernel(const __grid_constant__ E
     }
     if (!on) break;
   }
-  put_row<T, VEC>(p, run, c, a);
+  put_row<T, VEC>(p, run, c, a, old);
 }
 
 // ----------------------------------------------------------------- host side
@@ -493,7 +534,7 @@ cudaError_t fwd_launch(EmbFwd p, int width, int sms, cudaStream_t st) {
 int window_of(long long tokens, int width) {
   const long long col_blocks = ceil_div(width, 1024);
   int w = 16;
-  while (w < 128 && ceil_div(tokens, w) * col_blocks > 4 * 152 * 2) w *= 2;
+  while (w < kMaxWindow && ceil_div(tokens, w) * col_blocks > 4 * 152 * 2) w *= 2;
   return w;
 }
 
@@ -554,7 +595,16 @@ cudaError_t sum_launch(EmbSum p, cudaStream_t st) {
   const int tx = pow2_at_least(p.chunks, 8, 256), ty = 256 / tx;
   const long long windows = ceil_div(p.tokens, p.window);
   const dim3 grid((unsigned)ceil_div(windows, ty), (unsigned)ceil_div(p.chunks, tx));
-  cudaError_t e = launch_train(emb_window_kernel<T, VEC>, grid, dim3(tx, ty), 0, st, p);
+  // Eight rows in flight a thread in short windows, where few threads run (4095 x 512
+  // FP32: 9 us with four, 7 with eight); four in long ones, where eight cost the
+  // occupancy that hides their latency (32768 x 4096 BF16: 66 us with four, 86 with
+  // eight).
+  const size_t smem = (size_t)ty * p.window * 8;
+  const auto kern = p.window <= 16 ? (p.accumulate ? emb_window_kernel<T, VEC, 8, true>
+                                                   : emb_window_kernel<T, VEC, 8, false>)
+                                   : (p.accumulate ? emb_window_kernel<T, VEC, 4, true>
+                                                   : emb_window_kernel<T, VEC, 4, false>);
+  cudaError_t e = launch_train(kern, grid, dim3(tx, ty), smem, st, p);
   if (e == cudaSuccess && windows > 1)
     e = launch_train(emb_join_kernel<T, VEC>, grid, dim3(tx, ty), 0, st, p);
   return e;
@@ -623,8 +673,10 @@ int b2g_embedding_backward(int dtype, long long tokens, int vocab, int width, co
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   EmbSort q;
   q.tokens = (int)tokens, q.vocab = vocab;
-  q.passes = 1;  // the keys run from 0 to vocab, which stands for "in no sum"
-  while (q.passes < 4 && (unsigned)vocab >> (q.passes * kDigitBits)) ++q.passes;
+  int bits = 1;  // the keys run from 0 to vocab, which stands for "in no sum"
+  while (bits < 32 && (unsigned)vocab >> bits) ++bits;
+  q.passes = (bits + kDigitBits - 1) / kDigitBits;
+  q.bits = (bits + q.passes - 1) / q.passes;
   q.ids = ids, q.id_bytes = id_bytes, q.padding = padding;
   for (int i = 0; i < 2; ++i) {
     q.key[i] = reinterpret_cast<unsigned*>(ws + s.key[i]);
