@@ -29,17 +29,11 @@
 //
 // Bound: the tensor cores (from a few hundred tokens up), or reading w (few
 // tokens).
-#include <cudaTypedefs.h>
-
 #include <atomic>
 
-#include "tcgen05.cuh"
-#include "train_common.cuh"
+#include "xent.cuh"
 
 namespace b2g {
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // host.cu
-
 namespace {
 
 enum Mode { kStats, kDz, kProdH, kProdW };
@@ -96,34 +90,14 @@ struct XentGemm {
 
 // ---------------------------------------------------------------- tensor core
 
-// kind::f16 with BF16 operands and an FP32 accumulator; A or B MN-major when asked.
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4)                                  // D: FP32
-         | (1u << 7) | (1u << 10)                   // A, B: BF16
-         | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16)
-         | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// Descriptor of an MN-major operand with the 128-byte swizzle: rows of one k hold
-// 64 consecutive m (or n); groups of 8 k are 1024 bytes apart, blocks of 64 m
-// (one bulk-tensor box of 64 x 64) 8192 bytes.
-__device__ __forceinline__ uint64_t smem_desc_sw128_mnmajor(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(8192 >> 4) << 16;  // leading offset: next 64 m
-  d |= (uint64_t)(1024 >> 4) << 32;  // stride offset: next 8 k
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
-__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
       : "memory");
 }
 
@@ -161,13 +135,6 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* m,
   } else {
     tma_load_3d_pair(dst, m, kt * kBK, m0, plane, bar);
   }
-}
-
-// Planes of the i-th product of n: with three planes, the products of planes
-// (a, b) with a + b <= 2, the smallest first.
-__device__ __forceinline__ void plane_pair(int i, int n, int& a, int& b) {
-  a = n == 1 ? 0 : (0x001102 >> (20 - 4 * i)) & 15;
-  b = n == 1 ? 0 : (0x010120 >> (20 - 4 * i)) & 15;
 }
 
 // Unit u: k slice u % slices of tile u / slices; tiles in groups of group_m rows
@@ -210,20 +177,6 @@ __device__ __forceinline__ long long target_at(const XentGemm& p, int i) {
                          : (long long)static_cast<const int*>(p.target)[i];
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// e^x as the hardware's base-2 exponential (relative error 2^-22) of x log2(e),
-// whose rounding adds |x| 2^-24: x is at most about 0 here, so that error grows
-// only where e^x is small.  Results below 2^-126 become 0.
-__device__ __forceinline__ float exp_f32(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
-  return y;
-}
-
 // v (plus the old values) to up to 128 columns of a result row, for
 // results that a bulk-tensor store cannot write (alignment) or add to (BF16).
 template <typename T>
@@ -234,17 +187,6 @@ __device__ __forceinline__ void put_row(T* q, const float (&v)[128], int left,
     if (j < left) q[j] = from_f32<T>(accumulate ? v[j] + to_f32(q[j]) : v[j]);
 }
 
-// The loads into v are complete; tying v to the wait keeps its uses behind it.
-__device__ __forceinline__ void tie32(uint32_t (&v)[32]) {
-  asm volatile(""
-               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
-                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
-                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
-                 "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
-                 "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
-                 "+r"(v[30]), "+r"(v[31])::"memory");
-}
-
 // This warp's 128 columns of the accumulators that `tfull` announces, added up
 // over the unit's accumulation groups: acc holds FP32 sums rounded to nearest.
 // Two loads are in flight at a time.  Returns false when a wait ran out.
@@ -253,7 +195,8 @@ __device__ __forceinline__ bool collect(const XentGemm& p, float (&acc)[128], ui
                                         uint32_t tempty0, uint32_t tempty0_even, bool even,
                                         int lane) {
   for (int g = 0; g < groups; ++g) {
-    if (!wait_phase(tfull0 + 8u * a, aph, p, kStatusTimeoutTmem)) return false;
+    if (!__all_sync(0xffffffffu, wait_phase(tfull0 + 8u * a, aph, p, kStatusTimeoutTmem)))
+      return false;
     tc_fence_after_sync();
 #pragma unroll
     for (int c = 0; c < 128; c += 64) {
@@ -387,12 +330,7 @@ __device__ __forceinline__ void epi_dz(const XentGemm& p, float (&z)[128], int r
           uint32_t b[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float& lo = z[c + 8 * j + 2 * i];
-            float& hi = z[c + 8 * j + 2 * i + 1];
-            b[i] = pack_bf16(lo, hi);
-            // what this plane leaves for the next one (exact)
-            lo -= __uint_as_float(b[i] << 16);
-            hi -= __uint_as_float(b[i] & 0xFFFF0000u);
+            b[i] = split_plane<false>(z[c + 8 * j + 2 * i], z[c + 8 * j + 2 * i + 1]);
           }
           w[j] = make_uint4(b[0], b[1], b[2], b[3]);
         }
@@ -529,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       prefetch_tmap(&mB);
       int s = 0, issued = 0;
       uint32_t ph = 0;
+      const uint32_t full_even = even ? full(0) : mapa_shared(full(0), 0);
       for (int u = pair; u < units; u += npairs_cta) {
         int tm, tn, slice, kt0, kt1;
         unit_of(p, u, tm, tn, slice);
@@ -544,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!wait_phase(empty(s), ph ^ 1u, p, kStatusTimeoutEmpty)) goto copies_done;
               const uint32_t st = base + s * kStageBytes;
               if (even) mbar_arrive_expect_tx(full(s), 2 * p.stage_tx);
-              const uint32_t fb = even ? full(s) : mapa_shared(full(s), 0);
+              const uint32_t fb = full_even + 8u * s;
               load_operand<A_MN>(st, &mA, ma, kt, pa, fb);
               load_operand<B_MN>(st + kATile, &mB, nb, kt, pb, fb);
               ++issued;
@@ -569,6 +508,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc = idesc_bf16(kTile, p.tile_n, A_MN, B_MN);
       int s = 0, a = 0;
       uint32_t ph = 0, aph = 0;
+      // One thread issues everything, a few cycles an instruction: what can be is
+      // computed once.
+      const uint32_t empty_odd = mapa_shared(empty(0), 1), tfull_odd = mapa_shared(tfull(0), 1);
+      const uint32_t a0 = desc_lo<A_MN>(base), b0 = desc_lo<B_MN>(base + kATile);
       for (int u = pair; u < units; u += npairs_cta) {
         int tm, tn, slice, kt0, kt1;
         unit_of(p, u, tm, tn, slice);
@@ -584,21 +527,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait_phase(full(s), ph, p, kStatusTimeoutFull))
               goto mma_done;
             tc_fence_after_sync();
-            const uint32_t st = base + s * kStageBytes;
+            const uint32_t off = (uint32_t)s * (kStageBytes >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {  // 16 k an MMA: 32 bytes of a row, or 16 rows
-              const uint64_t da = A_MN ? smem_desc_sw128_mnmajor(st + kk * 2048u)
-                                       : smem_desc_sw128_kmajor(st + kk * 32u);
-              const uint64_t db = B_MN ? smem_desc_sw128_mnmajor(st + kATile + kk * 2048u)
-                                       : smem_desc_sw128_kmajor(st + kATile + kk * 32u);
-              mma_bf16_pair(d, da, db, idesc, (it > 0 || kk > 0) ? 1u : 0u);
-            }
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              mma_bf16_pair(d, a0 + off + kk * kDescStep<A_MN>, b0 + off + kk * kDescStep<B_MN>,
+                            idesc, (it > 0 || kk > 0) ? 1u : 0u);
             mma_commit_pair(empty(s));
-            mma_commit_pair(mapa_shared(empty(s), 1));
+            mma_commit_pair(empty_odd + 8u * s);
             if (++s == kStages) s = 0, ph ^= 1u;
           }
           mma_commit_pair(tfull(a));
-          mma_commit_pair(mapa_shared(tfull(a), 1));
+          mma_commit_pair(tfull_odd + 8u * a);
           if (++a == 2) a = 0, aph ^= 1u;
         }
       }
@@ -664,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Rows of x as `planes` BF16 planes with rows of ld elements (zeros past cols):
 // plane 0 is x rounded, plane 1 what that leaves rounded, plane 2 the rest (FP32
-// in three planes: 24 bits).  Infinities and NaN stay in plane 0.
+// in three planes: 24 bits).
 template <typename T>
 __global__ void __launch_bounds__(256) planes_kernel(const T* __restrict__ x, long long ldx,
                                                      int rows, int cols, Bf16* __restrict__ y,
@@ -680,13 +619,13 @@ __global__ void __launch_bounds__(256) planes_kernel(const T* __restrict__ x, lo
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = c + j < cols ? to_f32(x[r * ldx + c + j]) : 0.f;
     for (int pl = 0; pl < planes; ++pl) {
-      Pack<Bf16, 8> k;
-      k.set(f);
-      k.store(y + pl * plane + r * ld + c);
-      float g[8];
-      k.get(g);
+      uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = isfinite(g[j]) ? f[j] - g[j] : 0.f;
+      for (int j = 0; j < 4; ++j)
+        w[j] = planes == 1 ? pack_bf16(f[2 * j], f[2 * j + 1])
+               : pl == 0   ? split_plane<true>(f[2 * j], f[2 * j + 1])
+                           : split_plane<false>(f[2 * j], f[2 * j + 1]);
+      *reinterpret_cast<uint4*>(y + pl * plane + r * ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -750,42 +689,16 @@ __global__ void __launch_bounds__(256) xent_reduce_kernel(const float* part, int
 
 // ------------------------------------------------------------------- host side
 
-// {inner, outer, planes} BF16 or FP32 elements, boxes of 128 bytes x box_outer
-// rows with the 128-byte swizzle; ld and plane in elements.
-int encode(CUtensorMap* m, bool f32, const void* base, long long inner, long long outer,
-           long long ld, int planes, long long plane, int box_outer) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return B2G_ERR_TENSOR_MAP;
-  const cuuint64_t es = f32 ? 4 : 2;
-  cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)planes};
-  cuuint64_t strides[2] = {(cuuint64_t)ld * es, planes > 1 ? (cuuint64_t)plane * es : 16};
-  cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)box_outer, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r =
-      enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? 0 : B2G_ERR_TENSOR_MAP;
-}
-
-// A matrix as BF16 planes: rows x cols, rows ld apart, planes `plane` apart.
-struct Planes {
-  const Bf16* p;
-  int rows, cols;
-  long long ld, plane;
-  int planes;
-};
 // As an operand whose k runs along the columns, `box` rows a copy; as one whose k
 // runs along the rows; and as the output of 32-row stores.
 int map_k(CUtensorMap* m, const Planes& x, int box) {
-  return encode(m, false, x.p, x.cols, x.rows, x.ld, x.planes, x.plane, box);
+  return encode_rows(m, false, x.p, x.cols, x.rows, x.ld, x.planes, x.plane, box);
 }
 int map_mn(CUtensorMap* m, const Planes& x) {
-  return encode(m, false, x.p, x.cols, x.rows, x.ld, x.planes, x.plane, 64);
+  return encode_rows(m, false, x.p, x.cols, x.rows, x.ld, x.planes, x.plane, 64);
 }
 int map_out(CUtensorMap* m, const Planes& x) {
-  return encode(m, false, x.p, x.cols, x.rows, x.ld, x.planes, x.plane, 32);
+  return encode_rows(m, false, x.p, x.cols, x.rows, x.ld, x.planes, x.plane, 32);
 }
 
 // The launch shapes are planned for this many pairs (GB300: 152 SMs), so that the
@@ -905,6 +818,7 @@ int slices_for(long long tiles, int k_tiles, int pairs) {
 // of 256 classes, at least one).
 constexpr size_t kDzBytes = size_t(512) << 20;
 struct Layout {
+  bool few;                          // the few-token form
   int planes;
   bool copy_h, copy_w;
   long long ldc;                     // row length of the copies
@@ -913,6 +827,7 @@ struct Layout {
   long long dz_ld, part_ld;
   int slices_h, slices_w;
   int tile_n;                        // of h w^T
+  int parts;                         // its statistics' parts
   bool h_sums;                       // dh goes through FP32 sums
 };
 
@@ -920,7 +835,8 @@ Layout layout(const Call& c, bool backward) {
   Layout l;
   l.planes = c.dtype == B2G_F32 ? 3 : 1;
   l.copy_h = c.dtype == B2G_F32 || !vec16(c.h) || c.ldh % 8;
-  l.copy_w = c.dtype == B2G_F32 || !vec16(c.w) || c.ldw % 8;
+  l.few = c.tokens <= kFewTokens && vec16(c.w) && vec16_ld(c.ldw, c.dtype);
+  l.copy_w = !l.few && (c.dtype == B2G_F32 || !vec16(c.w) || c.ldw % 8);
   l.ldc = (long long)round_up(c.width, 8);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -934,7 +850,8 @@ Layout layout(const Call& c, bool backward) {
   l.piece = c.vocab, l.pieces = 1, l.slices_h = l.slices_w = 1, l.h_sums = false;
   if (!backward) {
     l.tile_n = choose_tile_n(c.tokens, c.vocab, 16);
-    l.stat = take((size_t)stat_parts(c.vocab, l.tile_n) * c.tokens * sizeof(float2));
+    l.parts = l.few ? few_stat_parts(c.vocab) : stat_parts(c.vocab, l.tile_n);
+    l.stat = take((size_t)l.parts * c.tokens * sizeof(float2));
     l.zt = take((size_t)c.tokens * sizeof(float));
   } else {
     const long long fit = (long long)(kDzBytes / ((size_t)l.planes * c.tokens * 2)) / kTile * kTile;
@@ -951,7 +868,8 @@ Layout layout(const Call& c, bool backward) {
     l.slices_w = slices_for(ceil_div(l.piece, kTile) * nt, (int)ceil_div(c.tokens, kBK), kPlanPairs);
     l.scale = take(sizeof(float));
     l.dz = take((size_t)l.planes * c.tokens * l.dz_ld * 2);
-    l.h_sums = l.slices_h > 1 || l.pieces > 1;
+    if (l.few) l.slices_h = l.pieces * few_slices(c.width, c.vocab < l.piece ? c.vocab : l.piece);
+    l.h_sums = l.few || l.slices_h > 1 || l.pieces > 1;
     if (l.h_sums)
       l.hpart = take((size_t)l.slices_h * c.tokens * l.part_ld * 4);
     if (l.slices_w > 1) l.wpart = take((size_t)l.slices_w * l.piece * l.part_ld * 4);
@@ -1025,9 +943,22 @@ int b2g_linear_xent(int dtype, int tokens, int vocab, int width, const void* h, 
   Planes ph, pw;
   rc = planes_of(h, ldh, tokens, width, dtype, l.copy_h, reinterpret_cast<Bf16*>(ws + l.h), l, d,
                  st, &ph);
-  if (!rc)
-    rc = planes_of(w, ldw, vocab, width, dtype, l.copy_w, reinterpret_cast<Bf16*>(ws + l.w), l, d,
-                   st, &pw);
+  if (rc) return rc;
+  float2* stat = reinterpret_cast<float2*>(ws + l.stat);
+  float* zt = reinterpret_cast<float*>(ws + l.zt);
+  auto join = [&] {
+    return launch_code(launch_train(xent_join_kernel, dim3((unsigned)ceil_div(tokens, 32)),
+                                    dim3(32, 32), 0, st, (const float2*)stat, (const float*)zt,
+                                    l.parts, tokens, target, id_bytes, ignore_index, vocab, lse,
+                                    loss, d.status));
+  };
+  if (l.few) {
+    const XentRows rows{tokens, vocab, width, target, id_bytes, ignore_index};
+    rc = launch_few_stats(rows, ph, FewHead{w, ldw, dtype == B2G_F32}, stat, zt, d, st);
+    return rc ? rc : join();
+  }
+  rc = planes_of(w, ldw, vocab, width, dtype, l.copy_w, reinterpret_cast<Bf16*>(ws + l.w), l, d, st,
+                 &pw);
   CUtensorMap mh, mw;
   if (!rc) rc = map_k(&mh, ph, token_box(tokens));
   if (!rc) rc = map_k(&mw, pw, l.tile_n / 2);
@@ -1038,14 +969,9 @@ int b2g_linear_xent(int dtype, int tokens, int vocab, int width, const void* h, 
   p.k_tiles = (int)ceil_div(width, kBK), p.npairs = l.planes == 3 ? 6 : 1, p.slices = 1;
   p.group = group_of(dtype, true);
   p.target = target, p.id_bytes = id_bytes, p.vocab = vocab, p.ignore = ignore_index;
-  p.stat = reinterpret_cast<float2*>(ws + l.stat);
-  p.zt = reinterpret_cast<float*>(ws + l.zt);
+  p.stat = stat, p.zt = zt;
   rc = launch_gemm<kStats>(p, mh, mw, mw, d, st);
-  if (rc) return rc;
-  return launch_code(launch_train(xent_join_kernel, dim3((unsigned)ceil_div(tokens, 32)),
-                                  dim3(32, 32), 0, st, (const float2*)p.stat, (const float*)p.zt,
-                                  stat_parts(vocab, l.tile_n), tokens, target, id_bytes,
-                                  ignore_index, vocab, lse, loss, d.status));
+  return rc ? rc : join();
 }
 
 int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const void* h,
@@ -1076,10 +1002,12 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
   Planes ph, pw;
   rc = planes_of(h, ldh, tokens, width, dtype, l.copy_h, reinterpret_cast<Bf16*>(ws + l.h), l, d,
                  st, &ph);
-  if (!rc)
+  if (!rc && !l.few)
     rc = planes_of(w, ldw, vocab, width, dtype, l.copy_w, reinterpret_cast<Bf16*>(ws + l.w), l, d,
                    st, &pw);
   if (rc) return rc;
+  const XentRows few_rows{tokens, vocab, width, target, id_bytes, ignore_index};
+  const FewHead head{w, ldw, dtype == B2G_F32};
   XentGemm base = {};
   base.npairs = l.planes == 3 ? 6 : 1, base.slices = 1;
   base.out_bf16 = dtype == B2G_BF16;
@@ -1093,13 +1021,20 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
   for (int i = 0; i < l.pieces; ++i) {
     const int first = i * l.piece;
     const int n = vocab - first < l.piece ? vocab - first : l.piece;
-    Planes piece = pw;
-    piece.p += (long long)first * pw.ld, piece.rows = n;
+    Planes piece = {};
+    if (!l.few) piece = pw, piece.p += (long long)first * pw.ld, piece.rows = n;
     const Planes dz{reinterpret_cast<Bf16*>(ws + l.dz), tokens, n, l.dz_ld,
                     (long long)tokens * l.dz_ld, l.planes};
     CUtensorMap a, b, o = {};
     // dz of these classes
     XentGemm p = base;
+    if (l.few) {
+      rc = launch_few_dz(few_rows, ph, head, first, n, lse, grad_loss, dz, base.scale, d, st);
+      const int each = l.slices_h / l.pieces;
+      if (!rc && dh)
+        rc = launch_few_dh(few_rows, dz, head, first, n, base.scale, each,
+                           hpart + (size_t)i * each * hslice, l.part_ld, d, st);
+    } else {
     p.rows = tokens, p.cols = n, p.k_tiles = (int)ceil_div(width, kBK);
     p.tile_n = l.tile_n, p.stage_tx = (token_box(tokens) + l.tile_n / 2) * 128;
     p.group = group_of(dtype, true);
@@ -1109,8 +1044,9 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
     if (!rc) rc = map_k(&b, piece, l.tile_n / 2);
     if (!rc) rc = map_out(&o, dz);
     if (!rc) rc = launch_gemm<kDz>(p, a, b, o, d, st);
+    }
     if (rc) return rc;
-    if (dh) {  // dh += dz w over these classes
+    if (dh && !l.few) {  // dh += dz w over these classes
       p = base;
       p.rows = tokens, p.cols = width, p.k_tiles = (int)ceil_div(n, kBK);
       p.tile_n = kTile, p.stage_tx = kStageBytes;
@@ -1121,8 +1057,8 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
       rc = map_k(&a, dz, 128);
       if (!rc) rc = map_mn(&b, piece);
       if (!rc && (p.to_part || p.out_tma))
-        rc = p.to_part ? encode(&o, true, hpart, width, tokens, l.part_ld, l.slices_h, hslice, 32)
-                       : encode(&o, f32, dh, width, tokens, lddh, 1, 0, 32);
+        rc = p.to_part ? encode_rows(&o, true, hpart, width, tokens, l.part_ld, l.slices_h, hslice, 32)
+                       : encode_rows(&o, f32, dh, width, tokens, lddh, 1, 0, 32);
       if (!rc) rc = launch_gemm<kProdH>(p, a, b, o, d, st);
       if (rc) return rc;
     }
@@ -1140,8 +1076,8 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
       rc = map_mn(&a, dz);
       if (!rc) rc = map_mn(&b, ph);
       if (!rc && (p.to_part || p.out_tma))
-        rc = p.to_part ? encode(&o, true, wpart, width, n, l.part_ld, l.slices_w, wslice, 32)
-                       : encode(&o, f32, out, width, n, lddw, 1, 0, 32);
+        rc = p.to_part ? encode_rows(&o, true, wpart, width, n, l.part_ld, l.slices_w, wslice, 32)
+                       : encode_rows(&o, f32, out, width, n, lddw, 1, 0, 32);
       if (!rc) rc = launch_gemm<kProdW>(p, a, b, o, d, st);
       if (!rc && p.to_part)
         rc = reduce_to(wpart, l.slices_w, l.part_ld, wslice, n, width, out, lddw, p.accumulate,

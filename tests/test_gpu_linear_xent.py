@@ -110,7 +110,8 @@ def check(b2g, h, w, t, g, ignore=-100, **kw):
 SHAPES = [
     (1, 1, 1), (1, 2, 8), (3, 5, 7), (2, 257, 64), (129, 300, 65), (256, 256, 64), (257, 511, 130),
     (64, 1000, 33), (16, 5000, 512), (1, 40000, 256), (300, 700, 1000), (513, 1025, 264),
-    (1000, 2048, 128), (130, 20001, 128), (5000, 130, 72), (100, 100, 4104), (384, 4096, 777),
+    (1000, 2048, 128), (130, 20001, 128), (5000, 130, 72), (64, 64, 8), (65, 300, 40), (33, 513, 136),
+    (17, 20000, 72), (64, 3000, 520), (48, 40000, 64), (100, 100, 4104), (384, 4096, 777),
 ]
 
 
@@ -122,9 +123,10 @@ def test_forward_and_backward(b2g, tokens, vocab, width, dtype):
     assert status(b2g) == (0, 0)
 
 
-@pytest.mark.parametrize("dtype,vocab", [(F32, 12000), (BF16, 40000)])
-def test_several_pieces_of_the_vocabulary(b2g, dtype, vocab):
-    h, w, t, g = make(8192, vocab, 64, dtype)
+@pytest.mark.parametrize("dtype,tokens,vocab,width", [
+    (F32, 8192, 12000, 64), (BF16, 8192, 40000, 64), (F32, 64, 1500000, 8)])
+def test_several_pieces_of_the_vocabulary(b2g, dtype, tokens, vocab, width):
+    h, w, t, g = make(tokens, vocab, width, dtype)
     check(b2g, h, w, t, g)
 
 
@@ -190,6 +192,21 @@ def test_masked_classes(b2g):
     t[(t >= 37) & (t < 41)] = 0
     loss, lse, dh, dw = check(b2g, h, w, t, g)
     assert torch.isfinite(loss).all() and not dw[37:41].any()
+
+
+@pytest.mark.parametrize("tokens", [40, 130])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_classes_masked_by_the_lowest_value(b2g, tokens, dtype):
+    """Logits of the type's lowest value, which FP32's BF16 planes must not round
+    to infinity."""
+    h, w, t, g = make(tokens, 700, 32, dtype, ignored=0)
+    h[:, 0], w[:, 0] = 1.0, 0.0
+    w[600:605] = 0
+    w[600:605, 0] = torch.finfo(dtype).min
+    t[(t >= 600) & (t < 605)] = 0
+    loss, lse, dh, dw = check(b2g, h, w, t, g)
+    assert torch.isfinite(loss).all() and torch.isfinite(dh[:, 1:]).all()
+    assert not dw[600:605].any()
 
 
 def test_weights_of_zero_and_nonfinite_lse(b2g):

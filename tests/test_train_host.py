@@ -152,11 +152,14 @@ def test_workspace_queries(lib):
     q = lib.b2g_linear_xent_workspace_size
     assert size(q, 1, 4, 10, 0, P, 8, P, 8, 0)[0] == -1 and q(1, 4, 10, 8, P, 8, P, 8, 0, None) == -3
     assert size(q, 1, 0, 10, 8, P, 8, P, 8, 1) == (0, 0)
-    fwd = size(q, 1, 64, 1000, 128, P, 128, P, 128, 0)[1]
-    assert 0 < fwd < 64 * 1000 * 4          # less than the logits
+    fwd = size(q, 1, 128, 1000, 128, P, 128, P, 128, 0)[1]
+    assert 0 < fwd < 128 * 1000 * 4         # less than the logits
     # an operand off the 16-byte boundaries is copied, FP32 ones become three planes
-    assert size(q, 1, 64, 1000, 128, P, 128, P + 2, 128, 0)[1] == fwd + 1000 * 128 * 2
-    assert size(q, 0, 64, 1000, 128, P, 128, P, 128, 0)[1] == fwd + 3 * 1064 * 128 * 2
+    assert size(q, 1, 128, 1000, 128, P, 128, P + 2, 128, 0)[1] == fwd + 1000 * 128 * 2
+    assert size(q, 0, 128, 1000, 128, P, 128, P, 128, 0)[1] == fwd + 3 * 1128 * 128 * 2
+    # up to 64 tokens FP32's w is read as it is: only h becomes planes
+    few = size(q, 1, 64, 1000, 128, P, 128, P, 128, 0)[1]
+    assert size(q, 0, 64, 1000, 128, P, 128, P, 128, 0)[1] == few + 3 * 64 * 128 * 2
     # dz exists a piece at a time: a larger vocabulary needs no more room for it
     big = [size(q, 1, 8192, v, 512, P, 512, P, 512, 1)[1] for v in (65536, 1 << 20)]
     assert big[1] <= big[0] < (1 << 30)
