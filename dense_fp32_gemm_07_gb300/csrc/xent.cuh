@@ -50,13 +50,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // Two FP32 values to their next BF16 plane: the rounded pair is returned and x, y
-// become what it leaves (exact).  For the FIRST plane values beyond BF16's largest
-// are clamped to it, so that FP32's largest values do not round to infinity.
+// become what it leaves (exact).  The FIRST plane saturates, so that FP32's largest
+// values do not round to infinity.
 template <bool FIRST>
 __device__ __forceinline__ uint32_t split_plane(float& x, float& y) {
-  constexpr float top = 3.38953139e38f;  // BF16's largest finite value
-  const uint32_t b = FIRST ? pack_bf16(fminf(fmaxf(x, -top), top), fminf(fmaxf(y, -top), top))
-                           : pack_bf16(x, y);
+  uint32_t b;
+  if (FIRST)
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(y), "f"(x));
+  else
+    b = pack_bf16(x, y);
   x -= __uint_as_float(b << 16);
   y -= __uint_as_float(b & 0xFFFF0000u);
   return b;

@@ -5,9 +5,9 @@
 // form is laid out around that read.  The classes are the rows of the MMA (M = 128
 // per CTA) and the tokens its columns (N = 16, 32 or 64), where xent.cu's tiles
 // would multiply mostly padding; the tile's height is chosen so that the SMs get
-// equal shares of w; and an FP32 w is read by eight converter warps, two steps ahead
+// equal shares of w; and an FP32 w is read by eight converter warps, three steps ahead
 // in registers, and split into its BF16 planes on the way to shared memory, instead
-// of by a pass over all of w (which costs 16 bytes an element: 478 us became XX at 16
+// of by a pass over all of w (which costs 16 bytes an element: 478 us became 148 at 16
 // x 32768 x 4096).  Modes:
 //   kStats  z^T = w h^T: per token and CTA, the maximum and the sum of the
 //           exponentials below it, and the target's logit
@@ -27,7 +27,13 @@ enum FewMode { kStats, kDz, kDh };
 constexpr int kM = 128, kBK = 64;
 constexpr int kMaxStages = 6;
 constexpr uint32_t kPlane = kM * kBK * 2;      // a plane of A: 16 KB
-constexpr uint32_t kAccCols = 64;              // tensor-memory columns of an accumulator
+// Tensor-memory columns of an accumulator: the tokens; with planes, three blocks of
+// them.  The planes of B stand behind one another in shared memory, so one MMA
+// multiplies a plane of A by several planes of B (N = 3, 2 and 1 times the tokens for
+// A's planes 0, 1 and 2): three MMAs where the six products taken one by one would be
+// six, each as long as its 128 rows of A.  The epilogue adds the blocks.
+template <bool F32>
+constexpr uint32_t kAccCols = F32 ? 256 : 64;
 constexpr int kNumBars = 4 * kMaxStages + 5;
 constexpr int kConvWarps = 8;
 
@@ -181,8 +187,16 @@ __global__ void __launch_bounds__(Cfg<F32>::kThreads, 1)
   auto tempty = [&](int a) { return bars + 8u * (4 * kMaxStages + 2 + a); };
   const uint32_t drain = bars + 8u * (4 * kMaxStages + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto wait = [&](uint32_t bar, uint32_t ph, unsigned int flag) {
-    return mbar_wait(bar, ph, p.wait_limit_ns, p.status, flag);
+  auto wait = [&](uint32_t bar, uint32_t ph, unsigned int flag) {  // mbar_wait without a call
+    if (mbar_try_wait(bar, ph)) return true;
+    const uint64_t t0 = global_ns();
+    while (!mbar_try_wait(bar, ph)) {
+      if (global_ns() - t0 > p.wait_limit_ns) {
+        atomicOr(p.status, flag);
+        return false;
+      }
+    }
+    return true;
   };
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -201,7 +215,7 @@ __global__ void __launch_bounds__(Cfg<F32>::kThreads, 1)
     fence_proxy_async_smem();
   }
   if (warp == 1) {
-    tmem_alloc(smem_addr(&tmem_slot), 2 * kAccCols);
+    tmem_alloc(smem_addr(&tmem_slot), 2 * kAccCols<F32>);
     tmem_relinquish();
   }
   __syncwarp();
@@ -288,7 +302,7 @@ __global__ void __launch_bounds__(Cfg<F32>::kThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0) {
-      const uint32_t idesc = idesc_bf16(kM, p.nt, MN, false);
+      const uint32_t idesc = idesc_bf16(kM, p.nt, MN, false);  // N is N / 8 << 17
       // One thread issues everything, a few cycles an instruction: with the
       // descriptors built and the group found by division at every step, a stage of
       // 14 KB took 1260 cycles and w came in at 3.1 TB/s.
@@ -309,16 +323,17 @@ __global__ void __launch_bounds__(Cfg<F32>::kThreads, 1)
           if (!wait(afull(a.s), a.ph, kStatusTimeoutFull)) goto mma_done;
           if (F32 && !wait(bfull(b.s), b.ph, kStatusTimeoutFull)) goto mma_done;
           tc_fence_after_sync();
-          const uint32_t d = tmem + (uint32_t)acc.s * kAccCols;
+          const uint32_t d = tmem + (uint32_t)acc.s * kAccCols<F32>;
           const uint32_t as = a0 + a.s * a_step, bs = b0 + (F32 ? b.s : a.s) * b_step;
-#pragma unroll 1
-          for (int i = 0; i < (F32 ? 6 : kSub); ++i) {
-            int pa = i, pb = i;  // BF16: the stage's 64-k tiles
-            if (F32) plane_pair(i, 6, pa, pb);
-            const uint32_t ai = as + pa * (kPlane >> 4), bi = bs + pb * bp;
+          // FP32: plane 0 of A first (it covers all columns), then the smaller ones;
+          // BF16: the stage's 64-k tiles.
+#pragma unroll
+          for (int i = 0; i < (F32 ? 3 : kSub); ++i) {
+            const uint32_t ai = as + i * (kPlane >> 4), bi = bs + (F32 ? 0 : i * bp);
+            const uint32_t id = F32 ? idesc + (uint32_t)((2 - i) * p.nt >> 3 << 17) : idesc;
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk)
-              mma_bf16(d, ai + kk * kDescStep<MN>, bi + kk * kDescStep<false>, idesc,
+              mma_bf16(d, ai + kk * kDescStep<MN>, bi + kk * kDescStep<false>, id,
                        begin && i == 0 && kk == 0 ? 0u : 1u);
           }
           mma_commit(aempty(a.s));
@@ -342,7 +357,7 @@ __global__ void __launch_bounds__(Cfg<F32>::kThreads, 1)
     // ---------------------------------------------------------- converters
     const int ct = (int)threadIdx.x - 256;
     unsigned char* sets = smem_raw + (abase - raw);
-    // This CTA's 64-k tiles in order; the pieces of the next two are on their way.
+    // This CTA's 64-k tiles in order; the pieces of the next three are on their way.
     struct Walk {
       int u, tile, kt, kt1;
     } w;
@@ -371,14 +386,15 @@ __global__ void __launch_bounds__(Cfg<F32>::kThreads, 1)
       return true;
     };
     enter(blockIdx.x);
-    Pieces<MN> x, y;
-    bool have_x = fetch(x), have_y = fetch(y);
+    Pieces<MN> x, y, z;
+    bool have_x = fetch(x), have_y = fetch(y), have_z = fetch(z);
     while (have_x) {
       if (!put(x)) break;
       have_x = fetch(x);
-      if (!have_y) break;
-      if (!put(y)) break;
+      if (!have_y || !put(y)) break;
       have_y = fetch(y);
+      if (!have_z || !put(z)) break;
+      have_z = fetch(z);
     }
   } else if (warp >= 4 && warp < 8) {
     // ---------------------------------------------------------- epilogue
@@ -413,12 +429,15 @@ __global__ void __launch_bounds__(Cfg<F32>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < kFewTokens; c += 16) {
           if (c < p.nt) {
-            uint32_t v[16];
-            tmem_ld16(tmem_lane + (uint32_t)at.s * kAccCols + c, v);
-            tmem_ld_wait();
-            tie16(v);
+#pragma unroll 1
+            for (int b = F32 ? 2 : 0; b >= 0; --b) {  // the smallest products first
+              uint32_t v[16];
+              tmem_ld16(tmem_lane + (uint32_t)at.s * kAccCols<F32> + b * p.nt + c, v);
+              tmem_ld_wait();
+              tie16(v);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) z[c + j] += __uint_as_float(v[j]);
+              for (int j = 0; j < 16; ++j) z[c + j] += __uint_as_float(v[j]);
+            }
           }
         }
         tc_fence_before_sync();
@@ -522,7 +541,7 @@ __global__ void __launch_bounds__(Cfg<F32>::kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, 2 * kAccCols);
+    tmem_dealloc(tmem, 2 * kAccCols<F32>);
   }
 }
 
