@@ -177,16 +177,6 @@ __device__ __forceinline__ long long target_at(const XentGemm& p, int i) {
                          : (long long)static_cast<const int*>(p.target)[i];
 }
 
-// v (plus the old values) to up to 128 columns of a result row, for
-// results that a bulk-tensor store cannot write (alignment) or add to (BF16).
-template <typename T>
-__device__ __forceinline__ void put_row(T* q, const float (&v)[128], int left,
-                                        int accumulate) {
-#pragma unroll
-  for (int j = 0; j < 128; ++j)
-    if (j < left) q[j] = from_f32<T>(accumulate ? v[j] + to_f32(q[j]) : v[j]);
-}
-
 // This warp's 128 columns of the accumulators that `tfull` announces, added up
 // over the unit's accumulation groups: acc holds FP32 sums rounded to nearest.
 // Two loads are in flight at a time.  Returns false when a wait ran out.
@@ -225,6 +215,17 @@ __device__ __forceinline__ bool collect(const XentGemm& p, float (&acc)[128], ui
   return true;
 }
 
+// A lane's row of 128 bytes to its warp's buffer, in the 128-byte swizzle.
+__device__ __forceinline__ void stage_rows(uint32_t buf, const uint4 (&w)[8], int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t at = buf + lane * 128u + (uint32_t)((i ^ (lane & 7)) * 16);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[i].x), "r"(w[i].y),
+                 "r"(w[i].z), "r"(w[i].w)
+                 : "memory");
+  }
+}
+
 // A warp's 32 rows of 128 bytes through its shared-memory buffer to (x, y, z) of
 // an output tensor: eight 16-byte pieces a lane, in the 128-byte swizzle (no bank
 // conflicts, and full lines leave the SM), then one bulk-tensor store, which
@@ -233,13 +234,7 @@ __device__ __forceinline__ void store_rows(uint32_t buf, const CUtensorMap* m, i
                                            const uint4 (&w)[8], bool add, int lane) {
   if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncwarp();  // the buffer's last store has been read
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t at = buf + lane * 128u + (uint32_t)((i ^ (lane & 7)) * 16);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[i].x), "r"(w[i].y),
-                 "r"(w[i].z), "r"(w[i].w)
-                 : "memory");
-  }
+  stage_rows(buf, w, lane);
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
@@ -357,6 +352,39 @@ __device__ __forceinline__ float largest_weight(const XentGemm& p, float* red, i
   return m;
 }
 
+// v (plus the old values) to a warp's rows of a result that a bulk-tensor store
+// cannot write (alignment) or add to (BF16): 32 columns at a time through the buffer,
+// so that each store is a stretch of one row.
+template <typename T>
+__device__ __forceinline__ void put_rows(T* out, const float (&v)[128], const XentGemm& p, int row0,
+                                         int left, uint32_t buf, int lane) {
+#pragma unroll
+  for (int c = 0; c < 128; c += 32) {
+    if (c < left) {
+      uint4 w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        w[j] = make_uint4(__float_as_uint(v[c + 4 * j]), __float_as_uint(v[c + 4 * j + 1]),
+                          __float_as_uint(v[c + 4 * j + 2]), __float_as_uint(v[c + 4 * j + 3]));
+      stage_rows(buf, w, lane);
+      __syncwarp();
+      const int rows = min(32, p.rows - row0);
+      if (c + lane < left) {
+#pragma unroll 4
+        for (int i = 0; i < rows; ++i) {
+          float x;
+          asm volatile("ld.shared.f32 %0, [%1];"
+                       : "=f"(x)
+                       : "r"(buf + i * 128u + (uint32_t)(((lane >> 2) ^ (i & 7)) * 16 + (lane & 3) * 4)));
+          T* q = out + (long long)i * p.ldo + c + lane;
+          *q = from_f32<T>(p.accumulate ? x + to_f32(*q) : x);
+        }
+      }
+      __syncwarp();
+    }
+  }
+}
+
 // kProdH, kProdW: this warp's columns of rows row0 .. row0 + 31 to the partial sums
 // or the result.
 __device__ __forceinline__ void epi_prod(const XentGemm& p, float (&v)[128], int row0, int lane,
@@ -391,12 +419,10 @@ __device__ __forceinline__ void epi_prod(const XentGemm& p, float (&v)[128], int
         store_rows(buf, m, n0 + c, row0, 0, w, false, lane);
       }
     }
-  } else if (row0 + lane < p.rows) {
-    const long long o = (long long)(row0 + lane) * p.ldo + n0;
-    if (p.out_bf16)
-      put_row(static_cast<Bf16*>(p.out) + o, v, left, p.accumulate);
-    else
-      put_row(static_cast<float*>(p.out) + o, v, left, p.accumulate);
+  } else if (p.out_bf16) {
+    put_rows(static_cast<Bf16*>(p.out) + (long long)row0 * p.ldo + n0, v, p, row0, left, buf, lane);
+  } else {
+    put_rows(static_cast<float*>(p.out) + (long long)row0 * p.ldo + n0, v, p, row0, left, buf, lane);
   }
 }
 
