@@ -11,9 +11,9 @@
 // (no atomics: the same bits every run).  x and dy are read once, dx written
 // once.
 //
-// Rows on 16-byte boundaries run on kernels that keep the next rows on their way
-// while one is worked on (a ring of bulk copies in shared memory); other rows are
-// read element by element.
+// With many rows, both keep the next ones on their way while one is worked on, in rings
+// of bulk copies in shared memory; rows that do not fit there twice, or that are wider
+// than 8192 columns, take kernels that read them several times.
 #include <atomic>
 
 #include "train_common.cuh"
@@ -37,10 +37,26 @@ struct LnFwd {
   float* rstd;
 };
 
-// One row per blockDim.x threads (threadIdx.y picks the row of a one-warp-per-
-// row block), NCH chunks of VEC columns per thread.  The weights are fetched
-// with the row, ahead of the two sums, so that their latency is not added to
-// the row's (one row of 4096: 5.0 us with, see below).
+// A sum over the nt lanes (a power of two, up to 32, consecutive) that share a row, or
+// over the nt threads of a block.
+__device__ __forceinline__ float row_sum(float v, float* red, int nt) {
+  if (nt > 32) return block_sum(v, red, nt >> 5);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float w = __shfl_xor_sync(0xffffffffu, v, o);
+    if (o < nt) v += w;
+  }
+  return v;
+}
+
+// One row per blockDim.x threads (from 8 lanes of a warp up; threadIdx.y picks the row
+// of a block that has several), NCH chunks of VEC columns per thread.  The weights are
+// fetched with the row, ahead of the two sums, so that their latency is not added to the
+// row's.  Serves few or short rows (one row of 4096: 2.1 us, which is the latency of a
+// launch, a read, two block sums and a write) and rows off the 16-byte boundaries,
+// element by element (8192 x 4095: 91 us in BF16, 90 in FP32; the ring of the backward
+// pass off the boundaries, tried here, took 87, 82 and, at 4000 x 777 BF16, 11.8 for
+// 10.5: not worth a second kernel).
 template <typename T, int VEC, int NCH>
 __global__ void __launch_bounds__(512) ln_fwd_kernel(const __grid_constant__ LnFwd p) {
   __shared__ float red[2][32];
@@ -49,21 +65,20 @@ __global__ void __launch_bounds__(512) ln_fwd_kernel(const __grid_constant__ LnF
   const T* w = static_cast<const T*>(p.w);
   const T* b = static_cast<const T*>(p.b);
   pdl_wait();
-  if (row >= p.rows) return;  // blockDim.y > 1 only with one warp per row: no barrier follows
+  const bool live = row < p.rows;  // the others of the warp take part in its sums
   const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-  const int t = threadIdx.x, nt = blockDim.x;
-  const int warps = nt >> 5;
+  const int t = threadIdx.x, nt = blockDim.x, chunks = live ? p.chunks : 0;
   Pack<T, VEC> raw[NCH], wr[NCH], br[NCH];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = t + i * nt;
     raw[i].zero(), wr[i].zero(), br[i].zero();
-    if (c < p.chunks) raw[i].load(x + c * VEC);
+    if (c < chunks) raw[i].load(x + c * VEC);
   }
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = t + i * nt;
-    if (c < p.chunks) {
+    if (c < chunks) {
       if (w) wr[i].load(w + c * VEC);
       if (b) br[i].load(b + c * VEC);
     }
@@ -77,23 +92,23 @@ __global__ void __launch_bounds__(512) ln_fwd_kernel(const __grid_constant__ LnF
     for (int j = 0; j < VEC; ++j) sum += f[j];
   }
   const float inv = 1.f / (float)p.cols;
-  const float mean = block_sum(sum, red[0], warps) * inv;
+  const float mean = row_sum(sum, red[0], nt) * inv;
   float sq = 0.f;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     float f[VEC];
     raw[i].get(f);
-    if (t + i * nt < p.chunks) {
+    if (t + i * nt < chunks) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) sq = fmaf(f[j] - mean, f[j] - mean, sq);
     }
   }
-  const float rstd = 1.f / sqrtf(block_sum(sq, red[1], warps) * inv + p.eps);
+  const float rstd = 1.f / sqrtf(row_sum(sq, red[1], nt) * inv + p.eps);
   T* y = static_cast<T*>(p.y) + row * p.ldy;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = t + i * nt;
-    if (c < p.chunks) {
+    if (c < chunks) {
       float f[VEC], wf[VEC], bf[VEC];
       raw[i].get(f), wr[i].get(wf), br[i].get(bf);
 #pragma unroll
@@ -104,7 +119,7 @@ __global__ void __launch_bounds__(512) ln_fwd_kernel(const __grid_constant__ LnF
       o.store(y + c * VEC);
     }
   }
-  if (t == 0) {
+  if (t == 0 && live) {
     if (p.mean) p.mean[row] = mean;
     if (p.rstd) p.rstd[row] = rstd;
   }
@@ -117,6 +132,7 @@ __global__ void __launch_bounds__(512) ln_fwd_kernel(const __grid_constant__ LnF
 // refilled once the group's first sum has been exchanged, when every thread has
 // read it.
 constexpr int kFwdThreads = 512, kBwdThreads = 256;  // 32 columns a thread in either
+constexpr int kAnyThreads = 512;                     // 16: the backward pass off the boundaries
 constexpr int kRingBytes = 192 * 1024;
 constexpr int kRingStages = 16;  // at most
 
@@ -168,18 +184,18 @@ __device__ __forceinline__ float group_sum(float v, float (&ex)[16], int group, 
   return __shfl_sync(0xffffffffu, v, 0);
 }
 
-// NCH chunks a thread; FULL: every thread has all of them.  The weights stand in
+// 32 columns a thread (FULL: every thread has all of them).  The weights stand in
 // shared memory after the rings: next to rings of this size L1 is too small to keep
 // them, and fetching them from L2 for every row took 43 us at 8192 x 4096 BF16, where this
 // takes 24 (5.5 TB/s).
-template <typename T, int VEC, int NCH, bool FULL>
+template <typename T, int VEC, bool FULL>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     ln_fwd_ring_kernel(const __grid_constant__ LnFwd p, const __grid_constant__ Ring g,
                        unsigned int* status, unsigned long long wait_limit_ns) {
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ __align__(8) unsigned long long bars[kFwdThreads / 32 * kRingStages];
   __shared__ float red[2][16];
-  constexpr int H = VEC / 2;
+  constexpr int H = VEC / 2, NCH = 32 / VEC;
   pdl_launch_dependents();
   const int group = threadIdx.x / g.nt, t = threadIdx.x - group * g.nt;
   const uint32_t bytes = (uint32_t)(p.cols * (int)sizeof(T));
@@ -321,91 +337,6 @@ struct LnBwd {
   float* part;  // [grid][2][cols]: partial dweight, then dbias; NULL: neither is wanted
 };
 
-// Block b takes rows b, b + grid, ...; thread t the chunks t + i * blockDim.x.
-// The next row's x and dy are fetched before this row's two sums.
-template <typename T, int VEC, int NCH>
-__global__ void __launch_bounds__(512) ln_bwd_kernel(const __grid_constant__ LnBwd p) {
-  __shared__ float red[2][64];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int t = threadIdx.x, nt = blockDim.x, warps = nt >> 5;
-  const float inv = 1.f / (float)p.cols;
-  float aw[NCH][VEC], ab[NCH][VEC];
-  Pack<T, VEC> wr[NCH], xn[NCH], dn[NCH];
-#pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int c = t + i * nt;
-    wr[i].zero(), xn[i].zero(), dn[i].zero();
-    if (p.w && c < p.chunks) wr[i].load(static_cast<const T*>(p.w) + c * VEC);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) aw[i][j] = ab[i][j] = 0.f;
-  }
-  auto fetch = [&](long long row) {
-    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-    const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = t + i * nt;
-      if (c < p.chunks) xn[i].load(x + c * VEC), dn[i].load(dy + c * VEC);
-    }
-  };
-  long long row = blockIdx.x;
-  float mean = 0.f, rstd = 0.f;
-  if (row < p.rows) fetch(row), mean = p.mean[row], rstd = p.rstd[row];
-  for (int it = 0; row < p.rows; row += gridDim.x, ++it) {
-    float s1 = 0.f, s2 = 0.f;  // sums of g and of g * xhat
-    Pack<T, VEC> xc[NCH], dc[NCH];
-    const float m = mean, r = rstd;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      xc[i] = xn[i], dc[i] = dn[i];
-      float xf[VEC], df[VEC], wf[VEC];
-      xc[i].get(xf), dc[i].get(df), wr[i].get(wf);
-      if (t + i * nt < p.chunks) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float xh = (xf[j] - m) * r, g = p.w ? df[j] * wf[j] : df[j];
-          s1 += g, s2 = fmaf(g, xh, s2);
-          aw[i][j] = fmaf(df[j], xh, aw[i][j]), ab[i][j] += df[j];
-        }
-      }
-    }
-    const long long next = row + gridDim.x;
-    if (next < p.rows) fetch(next), mean = p.mean[next], rstd = p.rstd[next];
-    const float2 s = block_sum2(s1, s2, red[it & 1], warps);
-    const float c1 = s.x * inv, c2 = s.y * inv;
-    T* dx = static_cast<T*>(p.dx) + row * p.lddx;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = t + i * nt;
-      if (c < p.chunks) {
-        float xf[VEC], df[VEC], wf[VEC], o[VEC];
-        xc[i].get(xf), dc[i].get(df), wr[i].get(wf);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float xh = (xf[j] - m) * r, g = p.w ? df[j] * wf[j] : df[j];
-          o[j] = r * (g - c1 - xh * c2);
-        }
-        Pack<T, VEC> v;
-        v.set(o);
-        v.store(dx + c * VEC);
-      }
-    }
-  }
-  if (p.part) {
-    float* pw = p.part + (size_t)blockIdx.x * 2 * p.cols;
-    float* pb = pw + p.cols;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = t + i * nt;
-      if (c < p.chunks) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) pw[c * VEC + j] = aw[i][j], pb[c * VEC + j] = ab[i][j];
-      }
-    }
-  }
-}
-
 // Rows on 16-byte boundaries: the ring above with rows of x and dy together, 32
 // columns a thread (FULL: every thread has all of them).  With t = x - mean,
 //     dx = rstd g + (-rstd^3 mean(g t)) t - rstd mean(g),
@@ -534,6 +465,171 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 }
 
+// A row of any alignment on its way through a slot of the ring: a bulk copy moves the
+// 16-byte units that lie inside the row, to the place they have within a 16-byte unit;
+// the few elements before and after them are read where they are.
+template <typename T>
+struct AnyRow {
+  const T* row;
+  uint32_t off;    // of the row's first byte within its 16-byte unit
+  int head, in;    // elements [head, head + in) are in the slot
+  __device__ __forceinline__ AnyRow(const T* r, int cols) : row(r) {
+    const uintptr_t start = reinterpret_cast<uintptr_t>(r), end = start + (size_t)cols * sizeof(T);
+    off = (uint32_t)(start & 15u);
+    const uintptr_t a = (start + 15u) & ~(uintptr_t)15u, b = end & ~(uintptr_t)15u;
+    head = (int)((a - start) / sizeof(T));
+    in = b > a ? (int)((b - a) / sizeof(T)) : 0;
+  }
+  __device__ __forceinline__ uint32_t bytes() const { return (uint32_t)(in * (int)sizeof(T)); }
+  __device__ __forceinline__ void copy(uint32_t slot, uint32_t bar) const {
+    if (in) bulk_load(slot + (off ? 16u : 0u), row + head, bytes(), bar);
+  }
+  // Element c as the slot has it: only the elements [head, head + in) are the row's.
+  __device__ __forceinline__ float at(const unsigned char* slot, int c) const {
+    return to_f32(reinterpret_cast<const T*>(slot + off)[c]);
+  }
+  // The others, at most 16 bytes' worth at either end: thread t of nt holds columns
+  // t + i * nt, so at most one of each end, in i = 0 and in its last column.
+  struct Ends {
+    bool first, last;
+    int i_last;
+    float v_first, v_last;
+    __device__ __forceinline__ float pick(int i, float v) const {
+      if (i == 0 && first) v = v_first;
+      return last && i == i_last ? v_last : v;
+    }
+  };
+  __device__ __forceinline__ Ends ends(int t, int nt, int cols) const {
+    Ends e;
+    const int c = t < cols ? cols - 1 - (cols - 1 - t) % nt : 0;  // this thread's last column
+    e.first = t < head && t < cols, e.last = t < cols && c >= head + in;
+    e.i_last = c / nt;
+    e.v_first = e.first ? to_f32(row[t]) : 0.f, e.v_last = e.last ? to_f32(row[c]) : 0.f;
+    return e;
+  }
+};
+// Bytes of a slot for one such row.
+inline __host__ __device__ size_t any_slot(int cols, size_t es) {
+  return ((size_t)cols * es + 15) / 16 * 16 + 16;
+}
+
+// The same for rows off the 16-byte boundaries, each thread with the 16 columns
+// t + i * nt (in twice the threads) and the weights in shared memory.  8192 x 4095:
+// 91 us in BF16, 87 in FP32 (2.3 and 4.6 TB/s), against 182 and 197 with the rows read
+// element by element from global memory; element by element it is still issue that
+// bounds it, on the boundaries the same size takes 41 in BF16.
+template <typename T>
+__global__ void __launch_bounds__(kAnyThreads, 1)
+    ln_bwd_any_kernel(const __grid_constant__ LnBwd p, const __grid_constant__ Ring g,
+                      unsigned int* status, unsigned long long wait_limit_ns) {
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ __align__(8) unsigned long long bars[kAnyThreads / 32 * kRingStages];
+  __shared__ F2 red[2][16];
+  constexpr int N = 16;
+  pdl_launch_dependents();
+  const int group = threadIdx.x / g.nt, t = threadIdx.x - group * g.nt;
+  const size_t slot = any_slot(p.cols, sizeof(T));
+  const uint32_t bar0 = smem_addr(bars) + 8u * (uint32_t)(group * kRingStages);
+  unsigned char* mine = ring + (size_t)group * g.stages * 2 * slot;
+  if (t == 0) {
+    for (int s = 0; s < g.stages; ++s) mbar_init(bar0 + 8u * s, 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  pdl_wait();
+  const float inv = 1.f / (float)p.cols;
+  const long long step = (long long)gridDim.x * g.groups;
+  const long long row0 = (long long)group * gridDim.x + blockIdx.x;
+  auto x_row = [&](long long row) {
+    return AnyRow<T>(static_cast<const T*>(p.x) + row * p.ldx, p.cols);
+  };
+  auto d_row = [&](long long row) {
+    return AnyRow<T>(static_cast<const T*>(p.dy) + row * p.lddy, p.cols);
+  };
+  auto issue = [&](long long row, int s) {
+    const uint32_t bar = bar0 + 8u * s, dst = smem_addr(mine + (size_t)s * 2 * slot);
+    const AnyRow<T> x = x_row(row), d = d_row(row);
+    mbar_arrive_expect_tx(bar, x.bytes() + d.bytes());
+    x.copy(dst, bar);
+    d.copy(dst + (uint32_t)slot, bar);
+  };
+  if (t == 0) {
+    long long row = row0;
+    for (int s = 0; s < g.stages && row < p.rows; ++s, row += step) issue(row, s);
+  }
+  T* ws = reinterpret_cast<T*>(ring + (size_t)g.groups * g.stages * 2 * slot);
+  for (int c = threadIdx.x; c < p.cols; c += kAnyThreads)
+    ws[c] = p.w ? static_cast<const T*>(p.w)[c] : from_f32<T>(1.f);
+  __syncthreads();
+  float aw[N], ab[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) aw[i] = ab[i] = 0.f;
+  float mean = 0.f, rstd = 0.f;
+  if (row0 < p.rows) mean = p.mean[row0], rstd = p.rstd[row0];
+  RingPos at;
+  int turn = 0;
+  bool alive = true;  // false once a wait has run out: no more waits, no more copies
+  for (long long row = row0; row < p.rows; row += step) {
+    const float m = mean, r = rstd;
+    if (row + step < p.rows) mean = p.mean[row + step], rstd = p.rstd[row + step];
+    if (alive) alive = mbar_wait(bar0 + 8u * at.s, at.ph, wait_limit_ns, status, kStatusTimeoutFull);
+    const unsigned char* here = mine + (size_t)at.s * 2 * slot;
+    const AnyRow<T> xr = x_row(row), dr = d_row(row);
+    const typename AnyRow<T>::Ends xe = xr.ends(t, g.nt, p.cols), de = dr.ends(t, g.nt, p.cols);
+    float x[N], gr[N];  // x - mean and g = dy * weight
+    float s1 = 0.f, s2 = 0.f;
+    // The columns are computed anew in each of the two loops: kept for all rows, with
+    // what depends on them, they would spill.
+    int c0 = t, nt = g.nt;
+    asm volatile("" : "+r"(c0), "+r"(nt));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = c0 + i * nt;
+      x[i] = gr[i] = 0.f;
+      if (c < p.cols) {
+        x[i] = xe.pick(i, xr.at(here, c)) - m;
+        const float d = de.pick(i, dr.at(here + slot, c));
+        gr[i] = d * to_f32(ws[c]);
+        s1 += gr[i], s2 = fmaf(gr[i], x[i], s2);
+        aw[i] = fmaf(d, x[i] * r, aw[i]), ab[i] += d;
+      }
+      if (i % 4 == 3) asm volatile("" : "+r"(c0), "+r"(nt)::"memory");
+    }
+    const F2 sums2 = group_sum2(f2(s1, s2), red[turn], group, g.nt);
+    if (t == 0 && alive && row + (long long)g.stages * step < p.rows)
+      issue(row + (long long)g.stages * step, at.s);
+    float sg, sgt;
+    f2_split(sums2, sg, sgt);
+    const float k1 = -r * (sg * inv), k2 = -r * (r * (r * (sgt * inv)));
+    T* dx = static_cast<T*>(p.dx) + row * p.lddx;
+    asm volatile("" : "+r"(c0), "+r"(nt));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = c0 + i * nt;
+      if (c < p.cols) dx[c] = from_f32<T>(fmaf(gr[i], r, fmaf(x[i], k2, k1)));
+    }
+    turn ^= 1;
+    at.next(g.stages);
+  }
+  if (!p.part) return;
+  __syncthreads();  // every ring is drained: its memory now takes the groups' sums
+  float* sums = reinterpret_cast<float*>(ring) + (size_t)2 * group * p.cols;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int c = t + i * g.nt;
+    if (c < p.cols) sums[c] = aw[i], sums[p.cols + c] = ab[i];
+  }
+  __syncthreads();
+  const float* all = reinterpret_cast<const float*>(ring);
+  float* out = p.part + (size_t)blockIdx.x * 2 * p.cols;
+  for (int c = threadIdx.x; c < 2 * p.cols; c += kAnyThreads) {
+    float a = all[c];
+    for (int i = 1; i < g.groups; ++i) a += all[(size_t)2 * i * p.cols + c];
+    out[c] = a;
+  }
+}
+
 // Rows wider than the registers of a block: dx in two passes over the row.
 template <typename T>
 __global__ void __launch_bounds__(1024) ln_bwd_wide_kernel(const __grid_constant__ LnBwd p) {
@@ -610,14 +706,12 @@ __global__ void __launch_bounds__(512) ln_bwd_reduce_kernel(const float* part, i
 // Chunks a thread may hold (powers of two) without spilling at 512 threads.
 template <int VEC>
 constexpr int kMaxFwd = VEC == 1 ? 16 : 4;
-template <int VEC>
-constexpr int kMaxBwd = VEC == 1 ? 4 : 2;
 constexpr int kMaxRowThreads = 512;
 
 // Threads for one row of `chunks` chunks with at most `per` chunks a thread:
-// the smallest power of two from 32 to kMaxRowThreads, or 0 when those are too few.
-int row_threads(int chunks, int per) {
-  for (int t = 32; t <= kMaxRowThreads; t *= 2)
+// the smallest power of two from `least` to kMaxRowThreads, or 0 when those are too few.
+int row_threads(int chunks, int per, int least) {
+  for (int t = least; t <= kMaxRowThreads; t *= 2)
     if ((long long)t * per >= chunks) return t;
   return 0;
 }
@@ -630,24 +724,27 @@ cudaError_t fwd_kernel(int nch, dim3 grid, dim3 block, cudaStream_t st, const Ln
   return launch_train(ln_fwd_kernel<T, VEC, NCH>, grid, block, 0, st, p);
 }
 
-// The ring of a block of `threads` for rows of `cols` values of `es` bytes, `copies`
-// rows to a slot and at most 32 columns a thread, leaving `reserved` bytes; stages <
-// 2 when they do not fit.
-Ring ring_of(int threads, int cols, int es, int copies, int reserved) {
-  constexpr int per = 32;
+// The ring of a block of `threads` for rows of `cols` columns in slots of `slot` bytes,
+// `per` columns a thread, leaving `reserved` bytes; stages < 2 when they do not fit.
+Ring ring_of(int threads, int per, int cols, size_t slot, size_t reserved) {
   Ring r{32, 0, 0};
   while (r.nt < threads && r.nt * per < cols) r.nt *= 2;
   r.groups = threads / r.nt;
-  if (r.nt * per < cols) return r;
-  const long long s = (kRingBytes - reserved) / ((long long)copies * cols * es * r.groups);
-  r.stages = (int)(s < kRingStages ? s : kRingStages);
+  if (r.nt * per < cols || reserved >= kRingBytes) return r;
+  const size_t s = (kRingBytes - reserved) / (slot * r.groups);
+  r.stages = (int)(s < (size_t)kRingStages ? s : (size_t)kRingStages);
   return r;
 }
 Ring fwd_ring_of(int cols, int dtype) {
-  const int es = (int)type_size(dtype);
-  return ring_of(kFwdThreads, cols, es, 1, 2 * es * cols);
+  const size_t es = type_size(dtype);
+  return ring_of(kFwdThreads, 32, cols, cols * es, 2 * es * cols);
 }
-Ring bwd_ring_of(int cols, int dtype) { return ring_of(kBwdThreads, cols, (int)type_size(dtype), 2, 0); }
+// vec: rows on 16-byte boundaries.
+Ring bwd_ring_of(int cols, int dtype, bool vec) {
+  const size_t es = type_size(dtype);
+  return vec ? ring_of(kBwdThreads, 32, cols, 2 * cols * es, 0)
+             : ring_of(kAnyThreads, 16, cols, 2 * any_slot(cols, es), es * cols);
+}
 
 // Opt in to the ring's shared memory, once per device and kernel.
 cudaError_t allow_ring(const void* kern, std::atomic<int> (&done)[64], int dev) {
@@ -659,14 +756,14 @@ cudaError_t allow_ring(const void* kern, std::atomic<int> (&done)[64], int dev) 
   return e;
 }
 
-template <typename T, int VEC, int NCH, bool FULL>
+template <typename T, int VEC, bool FULL>
 cudaError_t fwd_ring(const LnFwd& p, const Ring& r, const TrainDevice& d, cudaStream_t st) {
   static std::atomic<int> done[64];
   const cudaError_t e =
-      allow_ring(reinterpret_cast<const void*>(&ln_fwd_ring_kernel<T, VEC, NCH, FULL>), done, d.dev);
+      allow_ring(reinterpret_cast<const void*>(&ln_fwd_ring_kernel<T, VEC, FULL>), done, d.dev);
   if (e != cudaSuccess) return e;
   const long long blocks = ceil_div(p.rows, r.groups);
-  return launch_train(ln_fwd_ring_kernel<T, VEC, NCH, FULL>,
+  return launch_train(ln_fwd_ring_kernel<T, VEC, FULL>,
                       dim3((unsigned)(blocks < d.sms ? blocks : d.sms)), dim3(kFwdThreads),
                       ((size_t)r.groups * r.stages + 2) * p.cols * sizeof(T), st, p, r,
                       d.status, d.wait_limit_ns);
@@ -678,40 +775,33 @@ cudaError_t fwd_launch(LnFwd p, int dtype, const TrainDevice& d, cudaStream_t st
   p.chunks = p.cols / VEC;
   if constexpr (VEC > 1) {
     const Ring r = fwd_ring_of(p.cols, dtype);
-    if (p.rows > 4 * sms && r.stages >= 2) {
-      constexpr int N = 32 / VEC;
-      if (p.chunks == r.nt * N) return fwd_ring<T, VEC, N, true>(p, r, d, st);
-      if (p.chunks <= r.nt * N / 2) return fwd_ring<T, VEC, N / 2, false>(p, r, d, st);
-      return fwd_ring<T, VEC, N, false>(p, r, d, st);
-    }
+    // Few elements or short rows go faster a row (or four) a block, with more blocks an SM
+    // and no second row to wait for.  BF16, us, the ring and the other: 608 x 4096 3.7 and
+    // 3.7, 912 x 4096 4.7 and 5.3, 2432 x 4096 8.5 and 10.1; 2432 x 1024 3.6 and 3.4, 4864 x
+    // 1024 5.1 and 5.2; 4864 x 512 4.0 and 3.3, 65536 x 256 24.0 and 18.3.
+    if (p.cols >= 1024 && p.rows * p.cols > 16384LL * sms && r.stages >= 2)
+      return p.cols == r.nt * 32 ? fwd_ring<T, VEC, true>(p, r, d, st)
+                                 : fwd_ring<T, VEC, false>(p, r, d, st);
   }
   // Few rows: one chunk a thread, for the shortest path; many: several, for the
   // fewest barriers per byte.
-  int nt = p.rows <= 2 * sms ? row_threads(p.chunks, 1) : 0;
-  if (!nt) nt = row_threads(p.chunks, kMaxFwd<VEC>);
+  constexpr int least = VEC > 1 ? 8 : 32;  // lanes a row: whole 128-byte lines
+  int nt = p.rows <= 2 * sms ? row_threads(p.chunks, 1, least) : 0;
+  if (!nt) nt = row_threads(p.chunks, kMaxFwd<VEC>, least);
   if (!nt)
     return launch_train(ln_fwd_wide_kernel<T>, dim3((unsigned)p.rows), dim3(1024), 0, st, p);
-  const int ry = nt == 32 ? 4 : 1;
+  const int ry = nt <= 32 ? 128 / nt : 1;
   const dim3 grid((unsigned)ceil_div(p.rows, ry)), block(nt, ry);
   return fwd_kernel<T, VEC>((int)ceil_div(p.chunks, nt), grid, block, st, p);
 }
 
 // Blocks of a backward kernel, each leaving one partial row of dweight and of
-// dbias: one an SM in the ring kernel, up to four rows a block otherwise, at most
-// four blocks an SM (the partial rows stay a small share of the traffic).
+// dbias: one an SM in the ring kernels, row slices of the wide one otherwise.
 int bwd_parts(long long rows, int cols, int dtype, int sms, bool vec) {
-  const Ring r = bwd_ring_of(cols, dtype);
-  const long long most = vec && r.stages >= 2 ? sms : 4LL * sms;
-  const long long fair = ceil_div(rows, vec && r.stages >= 2 ? r.groups : 4);
+  const Ring r = bwd_ring_of(cols, dtype, vec);
+  const long long most = r.stages >= 2 ? sms : 4LL * sms;
+  const long long fair = ceil_div(rows, r.stages >= 2 ? r.groups : 4);
   return (int)(fair < most ? fair : most);
-}
-
-template <typename T, int VEC, int NCH = 1>
-cudaError_t bwd_kernel(int nch, dim3 grid, dim3 block, cudaStream_t st, const LnBwd& p) {
-  if constexpr (NCH < kMaxBwd<VEC>) {
-    if (nch > NCH) return bwd_kernel<T, VEC, 2 * NCH>(nch, grid, block, st, p);
-  }
-  return launch_train(ln_bwd_kernel<T, VEC, NCH>, grid, block, 0, st, p);
 }
 
 template <typename T, int VEC, bool FULL>
@@ -728,24 +818,32 @@ cudaError_t bwd_ring(const LnBwd& p, const Ring& r, int parts, const TrainDevice
                       rings > sums ? rings : sums, st, p, r, d.status, d.wait_limit_ns);
 }
 
+template <typename T>
+cudaError_t bwd_any(const LnBwd& p, const Ring& r, int parts, const TrainDevice& d,
+                    cudaStream_t st) {
+  static std::atomic<int> done[64];
+  const cudaError_t e =
+      allow_ring(reinterpret_cast<const void*>(&ln_bwd_any_kernel<T>), done, d.dev);
+  if (e != cudaSuccess) return e;
+  const size_t rings =
+      (size_t)r.groups * r.stages * 2 * any_slot(p.cols, sizeof(T)) + p.cols * sizeof(T);
+  const size_t sums = (size_t)r.groups * 2 * p.cols * sizeof(float);
+  return launch_train(ln_bwd_any_kernel<T>, dim3(parts), dim3(kAnyThreads),
+                      rings > sums ? rings : sums, st, p, r, d.status, d.wait_limit_ns);
+}
+
 template <typename T, int VEC>
 cudaError_t bwd_launch(LnBwd p, int dtype, T* dweight, T* dbias, int parts, const TrainDevice& d,
                        cudaStream_t st) {
   p.chunks = p.cols / VEC;
   cudaError_t e = cudaSuccess;
-  const int nt = row_threads(p.chunks, kMaxBwd<VEC>);
-  const Ring r = bwd_ring_of(p.cols, dtype);
-  bool done = false;
-  if constexpr (VEC > 1) {
-    if (r.stages >= 2) {
+  const Ring r = bwd_ring_of(p.cols, dtype, VEC > 1);
+  if (r.stages >= 2) {
+    if constexpr (VEC > 1)
       e = r.nt * 32 == p.cols ? bwd_ring<T, VEC, true>(p, r, parts, d, st)
                               : bwd_ring<T, VEC, false>(p, r, parts, d, st);
-      done = true;
-    }
-  }
-  if (done) {
-  } else if (nt) {
-    e = bwd_kernel<T, VEC>((int)ceil_div(p.chunks, nt), dim3(parts), dim3(nt), st, p);
+    else
+      e = bwd_any<T>(p, r, parts, d, st);
   } else {
     if (p.part)
       e = launch_train(ln_bwd_cols_kernel<T>, dim3((unsigned)ceil_div(p.cols, 256), parts),

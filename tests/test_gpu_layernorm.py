@@ -55,6 +55,9 @@ SHAPES = [
     (1, 1), (3, 2), (5, 7), (1, 4096), (2, 31), (33, 32), (7, 129), (64, 256), (19, 1000),
     (40, 1025), (9, 2048), (700, 512), (305, 2049), (3, 4096), (610, 4096), (2, 8192), (31, 8193),
     (3, 16384), (2, 20001), (1217, 64), (5000, 96),
+    # many rows: rings, aligned or not, up to their widest
+    (700, 7), (2000, 33), (1300, 777), (900, 1025), (650, 4095), (640, 8192), (640, 8191),
+    (620, 9001),
 ]
 
 
