@@ -112,7 +112,8 @@ int b2g_embedding_backward_workspace_size(int dtype, long long tokens, int vocab
  * tokens == 0 launches nothing; vocab and width are at least 1, else
  * B2G_ERR_INVALID_DIM.
  * BF16 operands are multiplied exactly and summed in FP32; FP32 operands are
- * split into three BF16 pieces each, whose six leading products carry 24 bits.
+ * split into three BF16 pieces each, whose six leading products carry 24 bits: they
+ * must be finite (an infinity's pieces make its row's results NaN).
  */
 int b2g_linear_xent(int dtype, int tokens, int vocab, int width, const void* h, long long ldh,
                     const void* w, long long ldw, const void* target, int id_bytes,
@@ -143,7 +144,9 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
  * b2g_linear_xent_backward (backward != 0) for these arguments.  h and w are
  * inspected for their alignment only: BF16 operands that are not on 16-byte
  * boundaries (base or leading dimension) are copied into the workspace first,
- * FP32 operands always (as BF16 pieces).
+ * FP32 operands always (as BF16 pieces), except that up to 64 tokens read a w on
+ * 16-byte boundaries where it is.  The backward pass also holds one piece of dz
+ * there, at most about 512 MB.
  */
 int b2g_linear_xent_workspace_size(int dtype, int tokens, int vocab, int width, const void* h,
                                    long long ldh, const void* w, long long ldw, int backward,
