@@ -22,10 +22,11 @@
 //   kProdH  dz w,  k = vocab piece: w's columns contiguous ("MN-major" B)
 //   kProdW  dz^T h, k = tokens: both operands MN-major
 // so no transposed copy of anything is made.  FP32 operands are split into three
-// BF16 planes, x = x0 + x1 + x2 to 24 bits, and the k loop runs over the six
-// plane products whose weight is at least 2^-16 of the largest (the next ones are
-// below FP32's rounding); dz is stored as three planes the same
-// way.
+// BF16 planes, x = x0 + x1 + x2 to 24 bits, of which the six products whose weight is at
+// least 2^-16 of the largest are added up (the next ones are below FP32's rounding); dz
+// is stored as three planes the same way.  The three planes of a k tile are in shared
+// memory together and each is copied there once, half the copies that fetching both
+// planes of each product would take.
 //
 // Bound: the tensor cores (from a few hundred tokens up), or reading w (few
 // tokens).
@@ -50,6 +51,8 @@ constexpr int kIssueRegs = 64, kEpiRegs = 216;
 constexpr uint32_t kATile = 128 * kBK * 2;     // a CTA's 128 rows of A: 16 KB
 constexpr uint32_t kBTile = 128 * kBK * 2;     // its 128 rows of B
 constexpr uint32_t kStageBytes = kATile + kBTile;
+constexpr uint32_t kStageStep = kStageBytes >> 4;  // in descriptors
+static_assert(kStages % 3 == 0, "a k tile's three planes lie in stages of one phase");
 constexpr int kNumBars = 2 * kStages + 5;
 constexpr uint32_t kOutBytes = 4096;           // an epilogue warp's 32 rows of 128 bytes on their way out
 constexpr int kSmemBytes =
@@ -61,9 +64,9 @@ struct XentGemm {
   int tiles_m, tiles_n, group_m, k_tiles;
   int tile_n;                  // columns of a tile, at most 256
   uint32_t stage_tx;           // bytes a CTA's copies bring to a stage
-  int npairs;                  // plane products: 1 (BF16) or 6 (FP32)
+  int planes;                  // BF16 planes of the operands and of dz: 1 (BF16) or 3 (FP32)
   int slices;                  // k slices per tile (kProdH, kProdW)
-  int group;                   // stages that add up in tensor memory before FP32 takes over
+  int group;                   // k tiles that add up in tensor memory before FP32 takes over
   unsigned long long wait_limit_ns;
   int debug_stop;              // >= 0: the copy issuer stops early (timeout test)
   unsigned int* status;
@@ -72,13 +75,11 @@ struct XentGemm {
   int id_bytes, vocab;
   long long ignore;
   int col0;                    // the class of column 0
-  float2* stat;                // [parts][rows]: maximum, sum of exp(z - maximum); a part is
-                               // (up to) 128 columns of a tile
+  float2* stat;                // [parts][rows]: maximum, sum of exp(z - maximum)
   float* zt;                   // the target's logit
   const float* lse;
   const float* gloss;
   float* scale;                // the largest weight: written by kDz, read by kProdH and kProdW
-  int planes;                  // BF16 planes of dz
   // kProdH, kProdW
   int to_part;                 // mOut is [slices][rows][..] FP32 sums
   int add;                     // to_part: add to what is there
@@ -87,6 +88,12 @@ struct XentGemm {
   long long ldo;
   int out_bf16, accumulate;
 };
+
+// Columns of a tile that one epilogue warp takes, and the warps that have any: a tile of
+// up to 128 columns is shared between two like a wider one (100 x 5000 x 512 BF16, loss and
+// gradients: 38 us for 44).
+__host__ __device__ __forceinline__ int span_of(int tile_n) { return tile_n > 128 ? 128 : 64; }
+__host__ __device__ __forceinline__ int parts_of(int tile_n) { return tile_n > 64 ? 2 : 1; }
 
 // ---------------------------------------------------------------- tensor core
 
@@ -125,13 +132,14 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const 
   return true;
 }
 
-// 128 rows of an operand at (row m0, k block kt, plane) into a 16 KB stage tile.
+// 128 rows (64 in MN-major order where `wide` is false) of an operand at (row m0, k block
+// kt, plane) into a 16 KB stage tile.
 template <bool MN>
 __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* m, int m0, int kt,
-                                             int plane, uint32_t bar) {
+                                             int plane, uint32_t bar, bool wide = true) {
   if constexpr (MN) {
     tma_load_3d_pair(dst, m, m0, kt * kBK, plane, bar);
-    tma_load_3d_pair(dst + 8192, m, m0 + 64, kt * kBK, plane, bar);
+    if (wide) tma_load_3d_pair(dst + 8192, m, m0 + 64, kt * kBK, plane, bar);
   } else {
     tma_load_3d_pair(dst, m, kt * kBK, m0, plane, bar);
   }
@@ -155,19 +163,21 @@ __device__ __forceinline__ void slice_range(const XentGemm& p, int slice, int& k
   kt1 = (int)((long long)(slice + 1) * p.k_tiles / p.slices);
 }
 
-// The order of a unit's stages: accumulation groups of `group` k tiles, and in each
-// group the plane products one after another, the smallest first.  A group adds up
-// in tensor memory and is then added to the unit's sums in registers, rounded to
-// nearest.  The tensor core truncates when it adds to its FP32 accumulator, which
-// over a long k would add up to a bias of steps * 2^-24; a short group bounds that
-// (with planes, the steps that count are those of the leading product: the others
-// come first, at 2^-8 of its size).
+// Three planes: the products (a, b) of A's and B's planes in the order in which they are
+// added: a + b = 2, then 1, then 0, the smallest first.  The planes are copied in the
+// order 1, 2, 0, so that the first product needs the first stage only; the first two
+// stages are free again before the last product.
+constexpr int kPairs = 6;
+__device__ __forceinline__ constexpr int plane_a(int i) { return (0x102010 >> (20 - 4 * i)) & 15; }
+__device__ __forceinline__ constexpr int plane_b(int i) { return (0x120100 >> (20 - 4 * i)) & 15; }
+__device__ __forceinline__ constexpr int stage_of(int plane) { return (plane + 2) % 3; }
+
+// A unit's k tiles add up in tensor memory in groups of `group`, and the groups' sums
+// in registers, rounded to nearest.  The tensor core truncates when it adds to its FP32
+// accumulator, which over a long k would add up to a bias of steps * 2^-24; a short
+// group bounds that.
 __device__ __forceinline__ int groups_of(const XentGemm& p, int kts) {
   return (kts + p.group - 1) / p.group;
-}
-// Stages of group g.
-__device__ __forceinline__ int group_stages(const XentGemm& p, int kts, int g) {
-  return p.npairs * min(p.group, kts - g * p.group);
 }
 
 // ------------------------------------------------------------------ epilogues
@@ -177,11 +187,11 @@ __device__ __forceinline__ long long target_at(const XentGemm& p, int i) {
                          : (long long)static_cast<const int*>(p.target)[i];
 }
 
-// This warp's 128 columns of the accumulators that `tfull` announces, added up
+// This warp's `span` columns (64 or 128) of the accumulators that `tfull` announces, added up
 // over the unit's accumulation groups: acc holds FP32 sums rounded to nearest.
 // Two loads are in flight at a time.  Returns false when a wait ran out.
 __device__ __forceinline__ bool collect(const XentGemm& p, float (&acc)[128], uint32_t tmem_lane,
-                                        int groups, int& a, uint32_t& aph, uint32_t tfull0,
+                                        int span, int groups, int& a, uint32_t& aph, uint32_t tfull0,
                                         uint32_t tempty0, uint32_t tempty0_even, bool even,
                                         int lane) {
   for (int g = 0; g < groups; ++g) {
@@ -190,6 +200,7 @@ __device__ __forceinline__ bool collect(const XentGemm& p, float (&acc)[128], ui
     tc_fence_after_sync();
 #pragma unroll
     for (int c = 0; c < 128; c += 64) {
+      if (c >= span) continue;
       uint32_t v[32], w[32];
       tmem_ld32(tmem_lane + (uint32_t)(a * kTile + c), v);
       tmem_ld32(tmem_lane + (uint32_t)(a * kTile + c + 32), w);
@@ -291,6 +302,7 @@ __device__ __forceinline__ void epi_stats(const XentGemm& p, float (&z)[128], in
 // weight, as one or three BF16 planes.  The division keeps a mean's equal weights
 // out of the rounding to BF16 (a factor 1/n would shift all of them alike, by up
 // to 2^-8).
+template <int PLANES>
 __device__ __forceinline__ void epi_dz(const XentGemm& p, float (&z)[128], int row0, int lane,
                                        int n0, int left, float inv_scale, uint32_t buf,
                                        const CUtensorMap* m) {
@@ -318,7 +330,7 @@ __device__ __forceinline__ void epi_dz(const XentGemm& p, float (&z)[128], int r
         z[j] = live ? g * e : 0.f;
       }
 #pragma unroll 1
-      for (int pl = 0; pl < p.planes; ++pl) {
+      for (int pl = 0; pl < PLANES; ++pl) {
         uint4 w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -434,7 +446,7 @@ __device__ __forceinline__ void epi_prod(const XentGemm& p, float (&v)[128], int
 // "stage read" and "accumulator final" to both CTAs.  Every wait is bounded: on a
 // timeout the kernel flags the status word, waits (bounded) for what it started,
 // frees its tensor memory and returns.
-template <int MODE>
+template <int MODE, int PLANES>
 __global__ void __launch_bounds__(kThreads, 1)
     xent_gemm_kernel(const __grid_constant__ XentGemm p, const __grid_constant__ CUtensorMap mA,
                      const __grid_constant__ CUtensorMap mB,
@@ -486,98 +498,122 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-  if (warp == 0) {
-    // ---------------------------------------------------------- copy issuer
-    if (lane == 0) {
-      prefetch_tmap(&mA);
-      prefetch_tmap(&mB);
-      int s = 0, issued = 0;
-      uint32_t ph = 0;
-      const uint32_t full_even = even ? full(0) : mapa_shared(full(0), 0);
-      for (int u = pair; u < units; u += npairs_cta) {
-        int tm, tn, slice, kt0, kt1;
-        unit_of(p, u, tm, tn, slice);
-        slice_range(p, slice, kt0, kt1);
-        const int ma = tm * kTile + (int)rank * 128, nb = tn * p.tile_n + (int)rank * (p.tile_n / 2);
-        for (int kb = kt0; kb < kt1; kb += p.group) {
-          const int ke = min(kb + p.group, kt1);
-          for (int i = 0; i < p.npairs; ++i) {
-            int pa, pb;
-            plane_pair(i, p.npairs, pa, pb);
-            for (int kt = kb; kt < ke; ++kt) {
+    if (warp == 0) {
+      // ---------------------------------------------------------- copy issuer
+      if (lane == 0) {
+        prefetch_tmap(&mA);
+        prefetch_tmap(&mB);
+        int s = 0, issued = 0;
+        uint32_t ph = 0;
+        const uint32_t full_even = even ? full(0) : mapa_shared(full(0), 0);
+        for (int u = pair; u < units; u += npairs_cta) {
+          int tm, tn, slice, kt0, kt1;
+          unit_of(p, u, tm, tn, slice);
+          slice_range(p, slice, kt0, kt1);
+          const int ma = tm * kTile + (int)rank * 128, nb = tn * p.tile_n + (int)rank * (p.tile_n / 2);
+          for (int kt = kt0; kt < kt1; ++kt) {
+            #pragma unroll
+            for (int i = 0; i < PLANES; ++i) {
+              const int plane = PLANES == 1 ? 0 : (i + 1) % 3;
               if (p.debug_stop >= 0 && issued >= p.debug_stop) goto copies_done;
               if (!wait_phase(empty(s), ph ^ 1u, p, kStatusTimeoutEmpty)) goto copies_done;
               const uint32_t st = base + s * kStageBytes;
               if (even) mbar_arrive_expect_tx(full(s), 2 * p.stage_tx);
               const uint32_t fb = full_even + 8u * s;
-              load_operand<A_MN>(st, &mA, ma, kt, pa, fb);
-              load_operand<B_MN>(st + kATile, &mB, nb, kt, pb, fb);
+              load_operand<A_MN>(st, &mA, ma, kt, plane, fb);
+              load_operand<B_MN>(st + kATile, &mB, nb, kt, plane, fb, p.tile_n > 128);
               ++issued;
               if (++s == kStages) s = 0, ph ^= 1u;
             }
           }
         }
-      }
-    copies_done:
-      // leave only after the copies started here have landed (the odd CTA sees
-      // the MMAs release the stages they read)
-      for (int d = 0, pending = min(issued, kStages); d < pending; ++d) {
-        if (--s < 0) s = kStages - 1, ph ^= 1u;
-        if (!wait_phase(even ? full(s) : empty(s), ph, p, kStatusTimeoutDrain))
-          break;
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer (even CTA)
-    if (even && lane == 0) {
-      const uint32_t idesc = idesc_bf16(kTile, p.tile_n, A_MN, B_MN);
-      int s = 0, a = 0;
-      uint32_t ph = 0, aph = 0;
-      // One thread issues everything, a few cycles an instruction: what can be is
-      // computed once.
-      const uint32_t empty_odd = mapa_shared(empty(0), 1), tfull_odd = mapa_shared(tfull(0), 1);
-      const uint32_t a0 = desc_lo<A_MN>(base), b0 = desc_lo<B_MN>(base + kATile);
-      for (int u = pair; u < units; u += npairs_cta) {
-        int tm, tn, slice, kt0, kt1;
-        unit_of(p, u, tm, tn, slice);
-        slice_range(p, slice, kt0, kt1);
-        const int groups = groups_of(p, kt1 - kt0);
-        for (int g = 0; g < groups; ++g) {
-          if (!wait_phase(tempty(a), aph ^ 1u, p, kStatusTimeoutTmem))
-            goto mma_done;
-          tc_fence_after_sync();
-          const uint32_t d = tmem + (uint32_t)(a * kTile);
-          const int steps = group_stages(p, kt1 - kt0, g);
-          for (int it = 0; it < steps; ++it) {
-            if (!wait_phase(full(s), ph, p, kStatusTimeoutFull))
-              goto mma_done;
-            tc_fence_after_sync();
-            const uint32_t off = (uint32_t)s * (kStageBytes >> 4);
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              mma_bf16_pair(d, a0 + off + kk * kDescStep<A_MN>, b0 + off + kk * kDescStep<B_MN>,
-                            idesc, (it > 0 || kk > 0) ? 1u : 0u);
-            mma_commit_pair(empty(s));
-            mma_commit_pair(empty_odd + 8u * s);
-            if (++s == kStages) s = 0, ph ^= 1u;
-          }
-          mma_commit_pair(tfull(a));
-          mma_commit_pair(tfull_odd + 8u * a);
-          if (++a == 2) a = 0, aph ^= 1u;
+      copies_done:
+        // leave only after the copies started here have landed (the odd CTA sees
+        // the MMAs release the stages they read)
+        for (int d = 0, pending = min(issued, kStages); d < pending; ++d) {
+          if (--s < 0) s = kStages - 1, ph ^= 1u;
+          if (!wait_phase(even ? full(s) : empty(s), ph, p, kStatusTimeoutDrain))
+            break;
         }
       }
-    mma_done:
-      mma_commit_pair(drain);
-      wait_phase(drain, 0, p, kStatusTimeoutTmem);
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer (even CTA)
+      if (even && lane == 0) {
+        const uint32_t idesc = idesc_bf16(kTile, p.tile_n, A_MN, B_MN);
+        int s = 0, a = 0;
+        uint32_t ph = 0, aph = 0;
+        // One thread issues everything, a few cycles an instruction: what can be is
+        // computed once.
+        const uint32_t empty_odd = mapa_shared(empty(0), 1), tfull_odd = mapa_shared(tfull(0), 1);
+        const uint32_t a0 = desc_lo<A_MN>(base), b0 = desc_lo<B_MN>(base + kATile);
+        for (int u = pair; u < units; u += npairs_cta) {
+          int tm, tn, slice, kt0, kt1;
+          unit_of(p, u, tm, tn, slice);
+          slice_range(p, slice, kt0, kt1);
+          const int groups = groups_of(p, kt1 - kt0);
+          for (int g = 0; g < groups; ++g) {
+            if (!wait_phase(tempty(a), aph ^ 1u, p, kStatusTimeoutTmem))
+              goto mma_done;
+            tc_fence_after_sync();
+            const uint32_t d = tmem + (uint32_t)(a * kTile);
+            const int kts = min(p.group, kt1 - kt0 - g * p.group);
+            for (int it = 0; it < kts; ++it) {
+              if (!wait_phase(full(s), ph, p, kStatusTimeoutFull))
+                goto mma_done;
+              tc_fence_after_sync();
+              const uint32_t off = (uint32_t)s * kStageStep;
+              if constexpr (PLANES == 1) {
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; ++kk)
+                  mma_bf16_pair(d, a0 + off + kk * kDescStep<A_MN>, b0 + off + kk * kDescStep<B_MN>,
+                                idesc, (it > 0 || kk > 0) ? 1u : 0u);
+                mma_commit_pair(empty(s));
+                mma_commit_pair(empty_odd + 8u * s);
+                if (++s == kStages) s = 0, ph ^= 1u;
+              } else {
+#pragma unroll
+                for (int i = 0; i < kPairs; ++i) {
+                  const uint32_t ai = a0 + off + stage_of(plane_a(i)) * kStageStep;
+                  const uint32_t bi = b0 + off + stage_of(plane_b(i)) * kStageStep;
+                  if (i == 1) {  // the other two planes
+                    if (!wait_phase(full(s + 1), ph, p, kStatusTimeoutFull) ||
+                        !wait_phase(full(s + 2), ph, p, kStatusTimeoutFull))
+                      goto mma_done;
+                    tc_fence_after_sync();
+                  }
+#pragma unroll
+                  for (int kk = 0; kk < kBK / 16; ++kk)
+                    mma_bf16_pair(d, ai + kk * kDescStep<A_MN>, bi + kk * kDescStep<B_MN>, idesc,
+                                  (it > 0 || i > 0 || kk > 0) ? 1u : 0u);
+                  // planes 2, 1 and 0 have been read after products 2, 4 and 5
+                  if (i == 2 || i >= 4) {
+                    const int done = s + stage_of(i == 2 ? 2 : 5 - i);
+                    mma_commit_pair(empty(done));
+                    mma_commit_pair(empty_odd + 8u * done);
+                  }
+                }
+                s += 3;
+                if (s == kStages) s = 0, ph ^= 1u;
+              }
+            }
+            mma_commit_pair(tfull(a));
+            mma_commit_pair(tfull_odd + 8u * a);
+            if (++a == 2) a = 0, aph ^= 1u;
+          }
+        }
+      mma_done:
+        mma_commit_pair(drain);
+        wait_phase(drain, 0, p, kStatusTimeoutTmem);
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     // ---------------------------------------------------------- epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int q = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t tmem_lane = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * 128);
+    const int span = span_of(p.tile_n);
+    const uint32_t tmem_lane = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * span);
     const uint32_t buf = outs + (uint32_t)(warp - 4) * kOutBytes;
     const uint32_t tempty_even = even ? 0u : mapa_shared(tempty(0), 0);
     float scale = 1.f;
@@ -595,18 +631,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       unit_of(p, u, tm, tn, slice);
       slice_range(p, slice, kt0, kt1);
       float acc[128];
-      if (!collect(p, acc, tmem_lane, groups_of(p, kt1 - kt0), a, aph, tfull(0), tempty(0),
-                   tempty_even, even, lane))
+      if (!collect(p, acc, tmem_lane, span, groups_of(p, kt1 - kt0), a, aph,
+                   tfull(0), tempty(0), tempty_even, even, lane))
         break;
       const int row0 = tm * kTile + (int)rank * 128 + 32 * q;
-      const int n0 = tn * p.tile_n + half * 128;
-      // this warp's columns of the tile that exist (none in the second half of a narrow tile)
-      const int left = min(min(p.tile_n - half * 128, 128), p.cols - n0);
+      const int n0 = tn * p.tile_n + half * span;
+      // this warp's columns of the tile that exist
+      const int left = min(min(p.tile_n - half * span, span), p.cols - n0);
       if (left > 0) {
         if constexpr (MODE == kStats)
-          epi_stats(p, acc, row0 + lane, n0, left, p.tile_n > 128 ? 2 * tn + half : tn);
+          epi_stats(p, acc, row0 + lane, n0, left, tn * parts_of(p.tile_n) + half);
         else if constexpr (MODE == kDz)
-          epi_dz(p, acc, row0, lane, n0, left, scale, buf, &mOut);
+          epi_dz<PLANES>(p, acc, row0, lane, n0, left, scale, buf, &mOut);
         else
           epi_prod(p, acc, row0, lane, n0, left, slice, scale, buf, &mOut);
       }
@@ -730,35 +766,43 @@ int map_out(CUtensorMap* m, const Planes& x) {
 // The launch shapes are planned for this many pairs (GB300: 152 SMs), so that the
 // workspace query needs no device.
 constexpr int kPlanPairs = 76;
+constexpr int kMaxSlices = 76;
 
 // Rows of h a CTA copies to a stage: all 128, or fewer where the tokens fit one
 // CTA's half (what its other rows then multiply is never stored).
 int token_box(int tokens) { return tokens >= 128 ? 128 : (int)round_up(tokens, 8); }
 
+// What a k tile of a pair's tile costs, in cycles.  BF16: its copies, 64 bytes a cycle
+// and SM (`rows`: those of both operands that a CTA copies, twice).  FP32: six products of
+// which each takes as long in a tile of 128 columns as in one of 256 (1000 x 11007 x 777,
+// loss and gradients: 433 us where 128 saves a third of the columns, 386 with 256).
+long long k_tile_cost(int planes, long long rows) { return planes == 1 ? rows : 3200; }
+// What a column of a tile costs once a launch, after its last k tile: narrow tiles win
+// where all have a pair of their own (FP32, 300 x 4000 x 256, all gradients: 54 us for 68).
+constexpr long long kColumnCost = 30;
+
 // Columns of a tile of h w^T, a multiple of `step`: what makes the pairs' rounds
-// cheapest when a stage costs a CTA's rows of both operands (shared memory and
-// copies, not the MMA, bound a narrower tile).  2048 x 32768 classes: 256; 16
-// tokens: 224 (two full rounds; 256 leaves a quarter of the pairs idle in the
-// second one).
-int choose_tile_n(int tokens, int classes, int step) {
+// cheapest.  BF16, 2048 x 32768 classes: 256; 100 tokens: 224 (two full rounds; 256 leaves
+// a quarter of the pairs idle in the second one).
+int choose_tile_n(int planes, int tokens, int classes, int k_tiles, int step) {
   const long long tiles_m = ceil_div(tokens, kTile), a = 2 * token_box(tokens);
   int best = kTile;
   long long cost = -1;
   for (int tn = kTile; tn >= 64; tn -= step) {
-    const long long c = ceil_div(tiles_m * ceil_div(classes, tn), kPlanPairs) * (a + tn);
+    const long long c = ceil_div(tiles_m * ceil_div(classes, tn), kPlanPairs) * k_tiles *
+                            k_tile_cost(planes, a + tn) + (planes == 1 ? 0 : kColumnCost * tn);
     if (cost < 0 || c < cost) best = tn, cost = c;
   }
   return best;
 }
 
-// The statistics' parts: 128 columns of a tile each, one in a narrow tile.
+// The statistics' parts: an epilogue warp's columns each.
 int stat_parts(int classes, int tile_n) {
-  const int tiles = (int)ceil_div(classes, tile_n);
-  if (tile_n <= 128) return tiles;
-  return 2 * tiles - (classes - (tiles - 1) * tile_n > 128 ? 0 : 1);
+  const int tiles = (int)ceil_div(classes, tile_n), last = classes - (tiles - 1) * tile_n;
+  return (tiles - 1) * parts_of(tile_n) + (last > span_of(tile_n) ? 2 : 1);
 }
 
-template <int MODE>
+template <int MODE, int PLANES>
 int resident_pairs(int dev, int sms) {
   static std::atomic<int> cached[64];
   if (dev < 0 || dev >= 64) return 0;
@@ -773,9 +817,9 @@ int resident_pairs(int dev, int sms) {
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaFuncSetAttribute(xent_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(xent_gemm_kernel<MODE, PLANES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSmemBytes) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&pairs, xent_gemm_kernel<MODE>, &cfg) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&pairs, xent_gemm_kernel<MODE, PLANES>, &cfg) != cudaSuccess ||
       pairs < 1)
     return 0;
   cached[dev].store(pairs, std::memory_order_release);
@@ -783,10 +827,10 @@ int resident_pairs(int dev, int sms) {
 }
 
 // Fills in the tiling and launches one product.
-template <int MODE>
-int launch_gemm(XentGemm p, const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mOut,
+template <int MODE, int PLANES>
+int launch_planes(XentGemm p, const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mOut,
                 const TrainDevice& d, cudaStream_t st) {
-  const int pairs = resident_pairs<MODE>(d.dev, d.sms);
+  const int pairs = resident_pairs<MODE, PLANES>(d.dev, d.sms);
   if (!pairs) return B2G_ERR_CUDA;
   p.tiles_m = (int)ceil_div(p.rows, kTile), p.tiles_n = (int)ceil_div(p.cols, p.tile_n);
   p.group_m = 16;
@@ -808,14 +852,22 @@ int launch_gemm(XentGemm p, const CUtensorMap& mA, const CUtensorMap& mB, const 
   CUtensorMap a = mA, b = mB, o = mOut;
   void* args[] = {&p, &a, &b, &o};
   return launch_code(
-      cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&xent_gemm_kernel<MODE>), args));
+      cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&xent_gemm_kernel<MODE, PLANES>), args));
 }
 
-// k tiles of an accumulation group.  FP32, 1000 x 11007 x 777 (loss and both
-// gradients; the largest relative error against 64 bits): 1: 524 us, 4.5e-7; 2: 488
-// us, 8.7e-7; 4: 468 us, 1.8e-6.  Logits of BF16 operands: 16, whose error of the
-// loss is that of FP32 products.  Products that are rounded to BF16 do not show it.
-int group_of(int dtype, bool logits) { return dtype == B2G_F32 ? 2 : logits ? 16 : 1 << 20; }
+// k tiles of an accumulation group.  FP32: one, whose products are added the smallest
+// first (two would add the second one's small products to the first one's sum; taking
+// the sums out once a k tile instead of once in eight costs 386 us for 357 at 1000 x 11007 x
+// 777).  Logits of BF16 operands: 16, whose error of the loss is that of FP32 products.  Products that
+// are rounded to BF16 do not show it.
+int group_of(int dtype, bool logits) { return dtype == B2G_F32 ? 1 : logits ? 16 : 1 << 20; }
+
+template <int MODE>
+int launch_gemm(const XentGemm& p, const CUtensorMap& mA, const CUtensorMap& mB,
+                const CUtensorMap& mOut, const TrainDevice& d, cudaStream_t st) {
+  return p.planes == 1 ? launch_planes<MODE, 1>(p, mA, mB, mOut, d, st)
+                       : launch_planes<MODE, 3>(p, mA, mB, mOut, d, st);
+}
 
 struct Call {
   int dtype, tokens, vocab, width;
@@ -832,12 +884,26 @@ int check(const Call& c) {
   return 0;
 }
 
-// k slices for `tiles` tiles on `pairs` CTA pairs: as many as leave each pair a
-// unit, with at least 8 stages of k each.
-int slices_for(long long tiles, int k_tiles, int pairs) {
-  long long s = pairs / tiles;
-  if (s > k_tiles / 8) s = k_tiles / 8;
-  return s < 1 ? 1 : (int)s;
+// Columns of a tile of a gradient (128 or 256) and its k slices: the cheapest rounds,
+// counting what several slices' partial sums cost (written and read at about 3400 bytes
+// a cycle, and a launch that adds them).  Slices have at least 8 k tiles each; a narrower
+// tile or another slice has to save a twentieth.
+struct Plan {
+  int tile_n, slices;
+};
+Plan plan_product(int planes, long long rows, int cols, int k_tiles) {
+  Plan best{kTile, 1};
+  long long cost = -1;
+  for (int tn = kTile; tn >= 128; tn -= 128) {
+    const long long tiles = ceil_div(rows, kTile) * ceil_div(cols, tn);
+    for (int s = 1; s == 1 || (s <= kMaxSlices && s <= k_tiles / 8); ++s) {
+      const long long c = ceil_div(tiles * s, kPlanPairs) * ceil_div(k_tiles, s) *
+                              k_tile_cost(planes, kTile + tn) + kColumnCost * tn +
+                          (s > 1 ? 4000 + s * rows * cols * 8 / 3400 : 0);
+      if (cost < 0 || c < cost - cost / 20) best = Plan{tn, s}, cost = c;
+    }
+  }
+  return best;
 }
 
 // dz for one piece of the vocabulary stays below this (the piece is a multiple
@@ -851,7 +917,7 @@ struct Layout {
   size_t h, w, stat, zt, scale, dz, hpart, wpart, total;
   int piece, pieces;                 // classes per piece
   long long dz_ld, part_ld;
-  int slices_h, slices_w;
+  int slices_h, slices_w, tile_h, tile_w;  // of dz w and of dz^T h
   int tile_n;                        // of h w^T
   int parts;                         // its statistics' parts
   bool h_sums;                       // dh goes through FP32 sums
@@ -874,8 +940,10 @@ Layout layout(const Call& c, bool backward) {
   l.w = l.copy_w ? take((size_t)l.planes * c.vocab * l.ldc * 2) : 0;
   l.stat = l.zt = l.scale = l.dz = l.hpart = l.wpart = 0;
   l.piece = c.vocab, l.pieces = 1, l.slices_h = l.slices_w = 1, l.h_sums = false;
+  l.tile_h = l.tile_w = kTile;
+  const int k_tiles = (int)ceil_div(c.width, kBK);
   if (!backward) {
-    l.tile_n = choose_tile_n(c.tokens, c.vocab, 16);
+    l.tile_n = choose_tile_n(l.planes, c.tokens, c.vocab, k_tiles, 16);
     l.parts = l.few ? few_stat_parts(c.vocab) : stat_parts(c.vocab, l.tile_n);
     l.stat = take((size_t)l.parts * c.tokens * sizeof(float2));
     l.zt = take((size_t)c.tokens * sizeof(float));
@@ -885,13 +953,13 @@ Layout layout(const Call& c, bool backward) {
     l.pieces = (int)ceil_div(c.vocab, most);
     l.piece = (int)round_up((size_t)ceil_div(c.vocab, l.pieces), kTile);
     l.pieces = (int)ceil_div(c.vocab, l.piece);
-    l.tile_n = choose_tile_n(c.tokens, l.piece, 64);  // whole 64-column stores
+    l.tile_n = choose_tile_n(l.planes, c.tokens, l.piece, k_tiles, 64);  // whole 64-column stores
     l.dz_ld = l.piece;
     l.part_ld = (long long)round_up(c.width, 4);
-    const long long nt = ceil_div(c.width, kTile);
-    l.slices_h = slices_for(ceil_div(c.tokens, kTile) * nt,
-                            (int)ceil_div(l.piece < c.vocab ? l.piece : c.vocab, kBK), kPlanPairs);
-    l.slices_w = slices_for(ceil_div(l.piece, kTile) * nt, (int)ceil_div(c.tokens, kBK), kPlanPairs);
+    const int classes = l.piece < c.vocab ? l.piece : c.vocab;
+    const Plan ph = plan_product(l.planes, c.tokens, c.width, (int)ceil_div(classes, kBK));
+    const Plan pw = plan_product(l.planes, classes, c.width, (int)ceil_div(c.tokens, kBK));
+    l.tile_h = ph.tile_n, l.slices_h = ph.slices, l.tile_w = pw.tile_n, l.slices_w = pw.slices;
     l.scale = take(sizeof(float));
     l.dz = take((size_t)l.planes * c.tokens * l.dz_ld * 2);
     if (l.few) l.slices_h = l.pieces * few_slices(c.width, c.vocab < l.piece ? c.vocab : l.piece);
@@ -992,7 +1060,7 @@ int b2g_linear_xent(int dtype, int tokens, int vocab, int width, const void* h, 
   XentGemm p = {};
   p.tile_n = l.tile_n, p.stage_tx = (token_box(tokens) + l.tile_n / 2) * 128;
   p.rows = tokens, p.cols = vocab;
-  p.k_tiles = (int)ceil_div(width, kBK), p.npairs = l.planes == 3 ? 6 : 1, p.slices = 1;
+  p.k_tiles = (int)ceil_div(width, kBK), p.planes = l.planes, p.slices = 1;
   p.group = group_of(dtype, true);
   p.target = target, p.id_bytes = id_bytes, p.vocab = vocab, p.ignore = ignore_index;
   p.stat = stat, p.zt = zt;
@@ -1035,7 +1103,7 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
   const XentRows few_rows{tokens, vocab, width, target, id_bytes, ignore_index};
   const FewHead head{w, ldw, dtype == B2G_F32};
   XentGemm base = {};
-  base.npairs = l.planes == 3 ? 6 : 1, base.slices = 1;
+  base.planes = l.planes, base.slices = 1;
   base.out_bf16 = dtype == B2G_BF16;
   base.scale = reinterpret_cast<float*>(ws + l.scale);
   base.group = group_of(dtype, false);
@@ -1061,21 +1129,21 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
         rc = launch_few_dh(few_rows, dz, head, first, n, base.scale, each,
                            hpart + (size_t)i * each * hslice, l.part_ld, d, st);
     } else {
-    p.rows = tokens, p.cols = n, p.k_tiles = (int)ceil_div(width, kBK);
-    p.tile_n = l.tile_n, p.stage_tx = (token_box(tokens) + l.tile_n / 2) * 128;
-    p.group = group_of(dtype, true);
-    p.target = target, p.id_bytes = id_bytes, p.vocab = vocab, p.ignore = ignore_index;
-    p.col0 = first, p.lse = lse, p.gloss = grad_loss, p.planes = l.planes;
-    rc = map_k(&a, ph, token_box(tokens));
-    if (!rc) rc = map_k(&b, piece, l.tile_n / 2);
-    if (!rc) rc = map_out(&o, dz);
-    if (!rc) rc = launch_gemm<kDz>(p, a, b, o, d, st);
+      p.rows = tokens, p.cols = n, p.k_tiles = (int)ceil_div(width, kBK);
+      p.tile_n = l.tile_n, p.stage_tx = (token_box(tokens) + l.tile_n / 2) * 128;
+      p.group = group_of(dtype, true);
+      p.target = target, p.id_bytes = id_bytes, p.vocab = vocab, p.ignore = ignore_index;
+      p.col0 = first, p.lse = lse, p.gloss = grad_loss;
+      rc = map_k(&a, ph, token_box(tokens));
+      if (!rc) rc = map_k(&b, piece, l.tile_n / 2);
+      if (!rc) rc = map_out(&o, dz);
+      if (!rc) rc = launch_gemm<kDz>(p, a, b, o, d, st);
     }
     if (rc) return rc;
     if (dh && !l.few) {  // dh += dz w over these classes
       p = base;
       p.rows = tokens, p.cols = width, p.k_tiles = (int)ceil_div(n, kBK);
-      p.tile_n = kTile, p.stage_tx = kStageBytes;
+      p.tile_n = l.tile_h, p.stage_tx = kATile + l.tile_h / 2 * 128;
       p.slices = l.slices_h < p.k_tiles ? l.slices_h : p.k_tiles;
       p.to_part = l.h_sums, p.add = i > 0;
       p.out = dh, p.ldo = lddh;
@@ -1091,7 +1159,7 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
     if (dw) {  // these classes' rows of dw = dz^T h
       p = base;
       p.rows = n, p.cols = width, p.k_tiles = (int)ceil_div(tokens, kBK);
-      p.tile_n = kTile, p.stage_tx = kStageBytes;
+      p.tile_n = l.tile_w, p.stage_tx = kATile + l.tile_w / 2 * 128;
       p.slices = l.slices_w;
       unsigned char* out = static_cast<unsigned char*>(dw) + (long long)first * lddw * es;
       p.to_part = l.slices_w > 1;

@@ -37,13 +37,6 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) {
 template <bool MN>
 constexpr uint32_t kDescStep = MN ? 2048u >> 4 : 32u >> 4;
 
-// Planes of the i-th product of n: with three planes, the products of planes
-// (a, b) with a + b <= 2, the smallest first.
-__device__ __forceinline__ void plane_pair(int i, int n, int& a, int& b) {
-  a = n == 1 ? 0 : (0x001102 >> (20 - 4 * i)) & 15;
-  b = n == 1 ? 0 : (0x010120 >> (20 - 4 * i)) & 15;
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
