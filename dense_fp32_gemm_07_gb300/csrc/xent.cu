@@ -775,7 +775,8 @@ int token_box(int tokens) { return tokens >= 128 ? 128 : (int)round_up(tokens, 8
 // What a k tile of a pair's tile costs, in cycles.  BF16: its copies, 64 bytes a cycle
 // and SM (`rows`: those of both operands that a CTA copies, twice).  FP32: six products of
 // which each takes as long in a tile of 128 columns as in one of 256 (1000 x 11007 x 777,
-// loss and gradients: 433 us where 128 saves a third of the columns, 386 with 256).
+// loss and gradients: 433 us where 128 saves a third of the columns, 386 with 256,
+// one k tile a group).
 long long k_tile_cost(int planes, long long rows) { return planes == 1 ? rows : 3200; }
 // What a column of a tile costs once a launch, after its last k tile: narrow tiles win
 // where all have a pair of their own (FP32, 300 x 4000 x 256, all gradients: 54 us for 68).
@@ -855,12 +856,12 @@ int launch_planes(XentGemm p, const CUtensorMap& mA, const CUtensorMap& mB, cons
       cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&xent_gemm_kernel<MODE, PLANES>), args));
 }
 
-// k tiles of an accumulation group.  FP32: one, whose products are added the smallest
-// first (two would add the second one's small products to the first one's sum; taking
-// the sums out once a k tile instead of once in eight costs 386 us for 357 at 1000 x 11007 x
-// 777).  Logits of BF16 operands: 16, whose error of the loss is that of FP32 products.  Products that
-// are rounded to BF16 do not show it.
-int group_of(int dtype, bool logits) { return dtype == B2G_F32 ? 1 : logits ? 16 : 1 << 20; }
+// k tiles of an accumulation group.  FP32, the time of loss and gradients at 1000 x 11007 x
+// 777 and the relative error of dh at 1205 x 1703 x 2136 (FP32 library products: 1.2e-6):
+// 1: 384 us, 1.9e-7; 2: 357 us, 5.3e-7; 4: 349 us, 1.3e-6; 8: 348 us, 2.8e-6.  Logits of BF16
+// operands: 16, whose error of the loss is that of FP32 products.  Products that are
+// rounded to BF16 do not show it.
+int group_of(int dtype, bool logits) { return dtype == B2G_F32 ? 2 : logits ? 16 : 1 << 20; }
 
 template <int MODE>
 int launch_gemm(const XentGemm& p, const CUtensorMap& mA, const CUtensorMap& mB,

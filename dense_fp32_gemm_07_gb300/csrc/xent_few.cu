@@ -600,7 +600,7 @@ int launch_rows(FewGemm p, const XentRows& r, const Planes& h, const FewHead& w,
   p.tokens = r.tokens, p.nt = padded_tokens(r.tokens);
   p.tile_rows = tile_rows_for(p.rows), p.tiles = (int)ceil_div(p.rows, p.tile_rows);
   p.k_tiles = (int)ceil_div(r.width, w.f32 ? kBK : 2 * kBK), p.slices = 1;
-  p.group = w.f32 ? 1 : 8;  // k: 64 and 1024, as in xent.cu
+  p.group = w.f32 ? 1 : 8;  // 64 and 1024 k
   p.a_tx = (uint32_t)(p.tile_rows * kBK * es);
   p.target = r.target, p.id_bytes = r.id_bytes, p.vocab = r.vocab, p.ignore = r.ignore;
   CUtensorMap a = {}, b = {};
