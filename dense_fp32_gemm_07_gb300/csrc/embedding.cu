@@ -81,6 +81,66 @@ __global__ void __launch_bounds__(256) emb_fwd_kernel(const __grid_constant__ Em
   }
 }
 
+// Rows off the 16-byte boundaries, in 4-byte words of the output row (BF16: two
+// elements, from a word of the table or from two halves, with an element alone at either
+// end of a row): U words a thread in flight, the row's threads striding over it.
+// 20000 x 1111: BF16 18.8 us (4.7 TB/s), element by element 47; FP32 25 and 49.
+template <typename T, int U>
+__global__ void __launch_bounds__(256) emb_fwd_words_kernel(const __grid_constant__ EmbFwd p) {
+  constexpr int E = 4 / (int)sizeof(T);  // elements a word; chunks counts elements
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long i = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  if (i >= p.tokens) return;
+  const long long id = id_at(p.ids, p.id_bytes, i);
+  T* o = static_cast<T*>(p.out) + i * p.ldo;
+  const bool ok = id >= 0 && id < p.vocab;
+  const T* r = static_cast<const T*>(p.table) + (ok ? id : 0) * p.ldt;
+  const float scale = ok ? p.scale : __int_as_float(0x7fc00000);
+  const int head = E == 2 ? (int)(reinterpret_cast<uintptr_t>(o) >> 1 & 1) : 0;
+  const int words = (p.chunks - head) / E;
+  if (threadIdx.x == 0) {
+    if (!ok) atomicOr(p.status, kStatusIndex);
+    const int last = p.chunks - 1;
+    if (head) o[0] = from_f32<T>((ok ? to_f32(r[0]) : 0.f) * scale);
+    if (E == 2 && head + 2 * words <= last)
+      o[last] = from_f32<T>((ok ? to_f32(r[last]) : 0.f) * scale);
+  }
+  const T* src = r + head;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(o + head);
+  const bool whole = E == 1 || (reinterpret_cast<uintptr_t>(src) & 3) == 0;
+  for (int c0 = threadIdx.x; c0 < words; c0 += U * blockDim.x) {
+    uint32_t v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * blockDim.x;
+      v[u] = 0;
+      if (ok && c < words) {
+        if (whole) {
+          v[u] = reinterpret_cast<const uint32_t*>(src)[c];
+        } else {
+          const unsigned short* h = reinterpret_cast<const unsigned short*>(src) + 2 * c;
+          v[u] = h[0] | (uint32_t)h[1] << 16;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * blockDim.x;
+      if (c < words) {
+        if constexpr (E == 1) {
+          v[u] = __float_as_uint(__uint_as_float(v[u]) * scale);
+        } else {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(
+              __uint_as_float(v[u] << 16) * scale, __uint_as_float(v[u] & 0xFFFF0000u) * scale);
+          v[u] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        dst[c] = v[u];
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------------- sort
 
 constexpr int kSortThreads = 1024;
@@ -522,6 +582,14 @@ cudaError_t fwd_launch(EmbFwd p, int width, int sms, cudaStream_t st) {
   p.chunks = width / VEC;
   // Few tokens: one chunk a thread, so that more SMs share the rows.
   const bool many = p.tokens * p.chunks >= 4LL * 2048 * sms;
+  if constexpr (VEC == 1) {
+    if (many) {
+      const int words = width * (int)sizeof(T) / 4, tx = pow2_at_least(words / 16, 8, 256);
+      const int ty = 256 / tx;
+      return launch_train(emb_fwd_words_kernel<T, 4>, dim3((unsigned)ceil_div(p.tokens, ty)),
+                          dim3(tx, ty), 0, st, p);
+    }
+  }
   const int u = many ? 4 : 1;
   const int tx = pow2_at_least((int)ceil_div(p.chunks, u), 8, 256), ty = 256 / tx;
   const dim3 grid((unsigned)ceil_div(p.tokens, ty), (unsigned)ceil_div(p.chunks, tx * u));

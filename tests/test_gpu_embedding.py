@@ -131,6 +131,31 @@ def test_strides_alignment_and_guards(b2g, extra, offset, dtype):
     assert untouched(flat, dt, before)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("tokens,width,ldt,ldo,ot,oo", [
+    (5000, 257, 257, 257, 0, 0), (5000, 257, 260, 263, 1, 3), (700, 2001, 2001, 2003, 2, 1),
+    (30000, 43, 43, 43, 1, 0), (20000, 70, 71, 72, 0, 2)])
+def test_large_lookup_at_any_alignment(b2g, tokens, width, ldt, ldo, ot, oo, dtype):
+    """Lookups off the 16-byte boundaries, in words of the output row; ids out of range."""
+    gen = torch.Generator().manual_seed(width + ot)
+    vocab = 500
+    ids = torch.randint(0, vocab, (tokens,), generator=gen).cuda()
+    table, _ = padded(torch.randn(vocab, width, generator=gen, dtype=torch.float64), dtype, ldt, ot)
+    out, flat = padded(torch.zeros(tokens, width, dtype=torch.float64), dtype, ldo, oo)
+    before = flat.clone()
+    check_forward(b2g, ids, table, -0.75, out=out)
+    assert untouched(flat, out, before)
+    assert status(b2g)[0] == 0
+    bad = ids.clone()
+    bad[3], bad[tokens - 1] = -1, vocab
+    got = b2g.embedding(bad, table, out=out)
+    assert torch.isnan(got[3]).all() and torch.isnan(got[-1]).all()
+    keep = torch.ones(tokens, dtype=torch.bool, device="cuda")
+    keep[3] = keep[-1] = False
+    assert torch.equal(got[keep], table[ids[keep]])
+    assert status(b2g)[0] == b2g.B2G_ERR_INDEX
+
+
 def test_padding_and_out_of_range(b2g):
     table, dout = torch.randn(10, 32, device="cuda"), torch.randn(6, 32, device="cuda")
     ids = torch.tensor([4, 0, 9, 4, 0, 2], device="cuda")
