@@ -52,13 +52,15 @@ __device__ __forceinline__ float row_sum(float v, float* red, int nt) {
 // One row per blockDim.x threads (from 8 lanes of a warp up; threadIdx.y picks the row
 // of a block that has several), NCH chunks of VEC columns per thread.  The weights are
 // fetched with the row, ahead of the two sums, so that their latency is not added to the
-// row's.  Serves few or short rows (one row of 4096: 2.1 us, which is the latency of a
-// launch, a read, two block sums and a write) and rows off the 16-byte boundaries,
-// element by element (8192 x 4095: 91 us in BF16, 90 in FP32; the ring of the backward
-// pass off the boundaries, tried here, took 87, 82 and, at 4000 x 777 BF16, 11.8 for
-// 10.5: not worth a second kernel).
+// row's; except where many single elements a thread would take the registers of blocks
+// that hide it better (8192 x 4095: BF16 89 us so, 74 with the weights fetched at the end).
+// Serves few or short rows (one row of 4096: 2.1 us, which is the latency of a launch,
+// a read, two block sums and a write) and rows off the 16-byte boundaries, element by
+// element (8192 x 4095: 74 us in BF16, 71 in FP32, 1.8 and 3.8 TB/s; the ring of the
+// backward pass off the boundaries, tried here, took 87 and 82).
 template <typename T, int VEC, int NCH>
 __global__ void __launch_bounds__(512) ln_fwd_kernel(const __grid_constant__ LnFwd p) {
+  constexpr bool kEarly = VEC > 1 || NCH <= 2;
   __shared__ float red[2][32];
   pdl_launch_dependents();
   const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
@@ -78,7 +80,7 @@ __global__ void __launch_bounds__(512) ln_fwd_kernel(const __grid_constant__ LnF
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = t + i * nt;
-    if (c < chunks) {
+    if (kEarly && c < chunks) {
       if (w) wr[i].load(w + c * VEC);
       if (b) br[i].load(b + c * VEC);
     }
@@ -109,6 +111,10 @@ __global__ void __launch_bounds__(512) ln_fwd_kernel(const __grid_constant__ LnF
   for (int i = 0; i < NCH; ++i) {
     const int c = t + i * nt;
     if (c < chunks) {
+      if (!kEarly) {
+        if (w) wr[i].load(w + c * VEC);
+        if (b) br[i].load(b + c * VEC);
+      }
       float f[VEC], wf[VEC], bf[VEC];
       raw[i].get(f), wr[i].get(wf), br[i].get(bf);
 #pragma unroll
@@ -784,9 +790,11 @@ cudaError_t fwd_launch(LnFwd p, int dtype, const TrainDevice& d, cudaStream_t st
                                  : fwd_ring<T, VEC, false>(p, r, d, st);
   }
   // Few rows: one chunk a thread, for the shortest path; many: several, for the
-  // fewest barriers per byte.
+  // fewest barriers per byte (single elements: 8 rather than 16 where that is enough, 8.7 us
+  // and 10.8 at 4000 x 777 BF16).
   constexpr int least = VEC > 1 ? 8 : 32;  // lanes a row: whole 128-byte lines
   int nt = p.rows <= 2 * sms ? row_threads(p.chunks, 1, least) : 0;
+  if (!nt && VEC == 1) nt = row_threads(p.chunks, kMaxFwd<VEC> / 2, least);
   if (!nt) nt = row_threads(p.chunks, kMaxFwd<VEC>, least);
   if (!nt)
     return launch_train(ln_fwd_wide_kernel<T>, dim3((unsigned)p.rows), dim3(1024), 0, st, p);
