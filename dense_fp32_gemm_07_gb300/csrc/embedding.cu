@@ -447,6 +447,7 @@ __global__ void __launch_bounds__(256) emb_window_kernel(const __grid_constant__
   const unsigned vocab = (unsigned)p.vocab, key_b = key[b];
   const T* dout = static_cast<const T*>(p.dout) + c * VEC;
   const T* table = static_cast<const T*>(p.dtable) + c * VEC;
+  if (key_b >= vocab) return;  // nothing but padding
   const bool from_before = before == key_b;
   float* part = p.part + (size_t)w * 2 * p.width + c * VEC;
   // The rows of U tokens at a time, and for accumulate the old values of the runs
@@ -470,9 +471,8 @@ __global__ void __launch_bounds__(256) emb_window_kernel(const __grid_constant__
   for (int i0 = b; i0 < e; i0 += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u;
-      v[u].zero();
-      if (i < e && key[i] < vocab) v[u].load(dout + (long long)pos[i] * p.ldd);
+      const int i = min(i0 + u, e - 1);
+      v[u].load(dout + (long long)pos[i] * p.ldd);
       if (ACC) {  // what the run ending at i adds to
         old[u].zero();
         if (i < e && key[i] < vocab && (i + 1 == e || key[i + 1] != key[i]))
@@ -490,8 +490,9 @@ __global__ void __launch_bounds__(256) emb_window_kernel(const __grid_constant__
       }
       float f[VEC];
       v[u].get(f);
+      const bool in = i0 + u < e;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) a[j] += f[j];
+      for (int j = 0; j < VEC; ++j) a[j] = in ? a[j] + f[j] : a[j];
       if (ACC && i0 + u + 1 == e) held = old[u];
     }
     if (ACC && i0 + U < e) held = old[U - 1];
