@@ -663,31 +663,43 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- small kernels
 
-// Rows of x as `planes` BF16 planes with rows of ld elements (zeros past cols):
-// plane 0 is x rounded, plane 1 what that leaves rounded, plane 2 the rest (FP32
-// in three planes: 24 bits).
+// Rows of one or two matrices as `planes` BF16 planes with rows of ld elements (zeros
+// past cols): plane 0 is x rounded, plane 1 what that leaves rounded, plane 2 the rest
+// (FP32 in three planes: 24 bits).  Bound: bytes (11007 + 1000 rows of 777 FP32: 13 us, 6.7
+// TB/s).
+struct PlaneCopy {
+  const void* x[2];
+  long long ldx[2];
+  int rows[2];  // 0: no such matrix
+  Bf16* y[2];
+  int cols, planes;
+  long long ld;
+};
 template <typename T>
-__global__ void __launch_bounds__(256) planes_kernel(const T* __restrict__ x, long long ldx,
-                                                     int rows, int cols, Bf16* __restrict__ y,
-                                                     long long ld, long long plane, int planes) {
+__global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ PlaneCopy p) {
   pdl_launch_dependents();
   pdl_wait();
-  const long long groups = ld / 8, total = groups * rows;
+  const long long groups = p.ld / 8, total = groups * ((long long)p.rows[0] + p.rows[1]);
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (long long)gridDim.x * 256) {
-    const long long r = i / groups;
-    const int c = (int)(i - r * groups) * 8;
+    const long long at = i / groups;
+    const int c = (int)(i - at * groups) * 8;
+    const bool second = at >= p.rows[0];
+    const long long r = second ? at - p.rows[0] : at;
+    const T* x = static_cast<const T*>(second ? p.x[1] : p.x[0]) + r * (second ? p.ldx[1] : p.ldx[0]);
+    Bf16* y = (second ? p.y[1] : p.y[0]) + r * p.ld + c;
+    const long long plane = (second ? p.rows[1] : p.rows[0]) * p.ld;
     float f[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = c + j < cols ? to_f32(x[r * ldx + c + j]) : 0.f;
-    for (int pl = 0; pl < planes; ++pl) {
+    for (int j = 0; j < 8; ++j) f[j] = c + j < p.cols ? to_f32(x[c + j]) : 0.f;
+    for (int pl = 0; pl < p.planes; ++pl) {
       uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        w[j] = planes == 1 ? pack_bf16(f[2 * j], f[2 * j + 1])
-               : pl == 0   ? split_plane<true>(f[2 * j], f[2 * j + 1])
-                           : split_plane<false>(f[2 * j], f[2 * j + 1]);
-      *reinterpret_cast<uint4*>(y + pl * plane + r * ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        w[j] = p.planes == 1 ? pack_bf16(f[2 * j], f[2 * j + 1])
+               : pl == 0     ? split_plane<true>(f[2 * j], f[2 * j + 1])
+                             : split_plane<false>(f[2 * j], f[2 * j + 1]);
+      *reinterpret_cast<uint4*>(y + pl * plane) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -973,22 +985,27 @@ Layout layout(const Call& c, bool backward) {
   return l;
 }
 
-// The operand itself, or its planes written to the workspace.
-int planes_of(const void* x, long long ldx, int rows, int cols, int dtype, bool copy, Bf16* to,
-              const Layout& l, const TrainDevice& d, cudaStream_t st, Planes* out) {
-  *out = Planes{static_cast<const Bf16*>(x), rows, cols, ldx, 0, 1};
-  if (!copy) return 0;
-  const long long plane = (long long)rows * l.ldc;
-  *out = Planes{to, rows, cols, l.ldc, plane, l.planes};
-  const long long blocks = ceil_div(l.ldc / 8 * rows, 256), most = 16LL * d.sms;
-  const dim3 grid((unsigned)(blocks < most ? blocks : most));
-  return launch_code(dtype == B2G_F32
-                         ? launch_train(planes_kernel<float>, grid, dim3(256), 0, st,
-                                        static_cast<const float*>(x), ldx, rows, cols, to, l.ldc,
-                                        plane, l.planes)
-                         : launch_train(planes_kernel<Bf16>, grid, dim3(256), 0, st,
-                                        static_cast<const Bf16*>(x), ldx, rows, cols, to, l.ldc,
-                                        plane, l.planes));
+// h and w (unless pw is NULL) themselves, or their planes written to the workspace.
+int operands(const Call& c, const Layout& l, unsigned char* ws, const TrainDevice& d,
+             cudaStream_t st, Planes* ph, Planes* pw) {
+  PlaneCopy q = {};
+  q.cols = c.width, q.planes = l.planes, q.ld = l.ldc;
+  int n = 0;
+  auto one = [&](const void* x, long long ldx, int rows, bool copy, size_t at, Planes* out) {
+    *out = Planes{static_cast<const Bf16*>(x), rows, c.width, ldx, 0, 1};
+    if (!copy) return;
+    Bf16* to = reinterpret_cast<Bf16*>(ws + at);
+    *out = Planes{to, rows, c.width, l.ldc, (long long)rows * l.ldc, l.planes};
+    q.x[n] = x, q.ldx[n] = ldx, q.rows[n] = rows, q.y[n] = to, ++n;
+  };
+  one(c.h, c.ldh, c.tokens, l.copy_h, l.h, ph);
+  if (pw) one(c.w, c.ldw, c.vocab, l.copy_w, l.w, pw);
+  if (!n) return 0;
+  const long long blocks = ceil_div(l.ldc / 8 * ((long long)q.rows[0] + q.rows[1]), 256);
+  const dim3 grid((unsigned)(blocks < 16LL * d.sms ? blocks : 16LL * d.sms));
+  return launch_code(c.dtype == B2G_F32
+                         ? launch_train(planes_kernel<float>, grid, dim3(256), 0, st, q)
+                         : launch_train(planes_kernel<Bf16>, grid, dim3(256), 0, st, q));
 }
 
 template <typename T>
@@ -1036,8 +1053,7 @@ int b2g_linear_xent(int dtype, int tokens, int vocab, int width, const void* h, 
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   Planes ph, pw;
-  rc = planes_of(h, ldh, tokens, width, dtype, l.copy_h, reinterpret_cast<Bf16*>(ws + l.h), l, d,
-                 st, &ph);
+  rc = operands(c, l, ws, d, st, &ph, l.few ? nullptr : &pw);
   if (rc) return rc;
   float2* stat = reinterpret_cast<float2*>(ws + l.stat);
   float* zt = reinterpret_cast<float*>(ws + l.zt);
@@ -1052,10 +1068,8 @@ int b2g_linear_xent(int dtype, int tokens, int vocab, int width, const void* h, 
     rc = launch_few_stats(rows, ph, FewHead{w, ldw, dtype == B2G_F32}, stat, zt, d, st);
     return rc ? rc : join();
   }
-  rc = planes_of(w, ldw, vocab, width, dtype, l.copy_w, reinterpret_cast<Bf16*>(ws + l.w), l, d, st,
-                 &pw);
   CUtensorMap mh, mw;
-  if (!rc) rc = map_k(&mh, ph, token_box(tokens));
+  rc = map_k(&mh, ph, token_box(tokens));
   if (!rc) rc = map_k(&mw, pw, l.tile_n / 2);
   if (rc) return rc;
   XentGemm p = {};
@@ -1095,11 +1109,7 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
   if (!workspace || !vec16(workspace) || workspace_bytes < l.total) return B2G_ERR_WORKSPACE;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   Planes ph, pw;
-  rc = planes_of(h, ldh, tokens, width, dtype, l.copy_h, reinterpret_cast<Bf16*>(ws + l.h), l, d,
-                 st, &ph);
-  if (!rc && !l.few)
-    rc = planes_of(w, ldw, vocab, width, dtype, l.copy_w, reinterpret_cast<Bf16*>(ws + l.w), l, d,
-                   st, &pw);
+  rc = operands(c, l, ws, d, st, &ph, l.few ? nullptr : &pw);
   if (rc) return rc;
   const XentRows few_rows{tokens, vocab, width, target, id_bytes, ignore_index};
   const FewHead head{w, ldw, dtype == B2G_F32};
