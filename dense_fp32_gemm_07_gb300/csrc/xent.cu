@@ -19,8 +19,9 @@
 // contiguous in memory and what happens to a finished tile:
 //   kStats  h w^T, k = width: row statistics and the target's logit
 //   kDz     h w^T, k = width: dz, rounded to BF16
-//   kProdH  dz w,  k = vocab piece: w's columns contiguous ("MN-major" B)
-//   kProdW  dz^T h, k = tokens: both operands MN-major
+//   kProd   both gradients in one launch, whose tiles fill the CTA pairs together:
+//           job 0: dz w,   k = vocab piece: w's columns contiguous ("MN-major" B)
+//           job 1: dz^T h, k = tokens: both operands MN-major
 // so no transposed copy of anything is made.  FP32 operands are split into three
 // BF16 planes, x = x0 + x1 + x2 to 24 bits, of which the six products whose weight is at
 // least 2^-16 of the largest are added up (the next ones are below FP32's rounding); dz
@@ -37,7 +38,7 @@
 namespace b2g {
 namespace {
 
-enum Mode { kStats, kDz, kProdH, kProdW };
+enum Mode { kStats, kDz, kProd };
 
 constexpr int kTile = 256;       // rows and (at most) columns of a pair's tile
 constexpr int kBK = 64;          // k per stage: 128 bytes of BF16
@@ -46,8 +47,8 @@ constexpr int kEpiWarps = 8;     // two per tensor-memory quarter, 128 columns e
 constexpr int kThreads = 128 + 32 * kEpiWarps;  // warp 0 copies, warp 1 multiplies, 2 and 3 idle
 // Registers: the block starts with 168 a thread (64,512 of the SM's 65,536); the
 // first warpgroup gives up its share so that the epilogue's threads can hold 128
-// sums each: 128 * 64 + 256 * 216 = 63,488.
-constexpr int kIssueRegs = 64, kEpiRegs = 216;
+// sums each: 128 * 72 + 256 * 216 = 64,512.
+constexpr int kIssueRegs = 72, kEpiRegs = 216;
 constexpr uint32_t kATile = 128 * kBK * 2;     // a CTA's 128 rows of A: 16 KB
 constexpr uint32_t kBTile = 128 * kBK * 2;     // its 128 rows of B
 constexpr uint32_t kStageBytes = kATile + kBTile;
@@ -65,7 +66,7 @@ struct XentGemm {
   int tile_n;                  // columns of a tile, at most 256
   uint32_t stage_tx;           // bytes a CTA's copies bring to a stage
   int planes;                  // BF16 planes of the operands and of dz: 1 (BF16) or 3 (FP32)
-  int slices;                  // k slices per tile (kProdH, kProdW)
+  int slices;                  // k slices per tile (kProd)
   int group;                   // k tiles that add up in tensor memory before FP32 takes over
   unsigned long long wait_limit_ns;
   int debug_stop;              // >= 0: the copy issuer stops early (timeout test)
@@ -79,11 +80,11 @@ struct XentGemm {
   float* zt;                   // the target's logit
   const float* lse;
   const float* gloss;
-  float* scale;                // the largest weight: written by kDz, read by kProdH and kProdW
-  // kProdH, kProdW
-  int to_part;                 // mOut is [slices][rows][..] FP32 sums
+  float* scale;                // the largest weight: written by kDz, read by kProd
+  // kProd
+  int to_part;                 // the output map is [slices][rows][..] FP32 sums
   int add;                     // to_part: add to what is there
-  int out_tma;                 // mOut is the result; else `out` is written element by element
+  int out_tma;                 // it is the result; else `out` is written element by element
   void* out;
   long long ldo;
   int out_bf16, accumulate;
@@ -94,6 +95,47 @@ struct XentGemm {
 // gradients: 38 us for 44).
 __host__ __device__ __forceinline__ int span_of(int tile_n) { return tile_n > 128 ? 128 : 64; }
 __host__ __device__ __forceinline__ int parts_of(int tile_n) { return tile_n > 64 ? 2 : 1; }
+
+// What a launch computes: one product (job 0), or with kProd two.  Pair p's units: first
+// the long ones of job 0 (p, p + pairs, ...), of which the first `rest` pairs have one more
+// than the others; these take `extra` units of job 1 meanwhile, then all go on alike.  One
+// launch instead of two: 1000 x 11007 x 777 FP32, loss and gradients, 331 us for 352; 300 x
+// 4000 x 256 BF16 33 for 40; 2048 x 32768 x 2048 BF16, gradients, 504 to 525 for 517 to 536.
+struct XentJobs {
+  XentGemm p[2];
+  int units[2];
+  int full, rest, extra;
+};
+struct alignas(64) XentMaps {
+  CUtensorMap a[2], b[2], out[2];
+};
+
+// Whether A is MN-major, as a type.
+template <bool B>
+struct Mn {
+  static constexpr bool value = B;
+};
+
+// The k-th unit of this pair; false: there is none.
+template <int MODE>
+__device__ __forceinline__ bool unit_at(const XentJobs& j, int pair, int pairs, int k, int& job,
+                                        int& unit) {
+  job = 0, unit = k * pairs + pair;
+  if constexpr (MODE == kProd) {
+    const bool more = pair < j.rest;
+    const int mine = j.full + (more ? 1 : 0);
+    if (k < mine) return true;
+    k -= mine, job = 1;
+    const int others = pairs - j.rest;
+    if (!more && k < j.extra)
+      unit = k * others + pair - j.rest;
+    else
+      unit = j.extra * others + (k - (more ? 0 : j.extra)) * pairs + pair;
+    return unit < j.units[1];
+  } else {
+    return unit < j.units[0];
+  }
+}
 
 // ---------------------------------------------------------------- tensor core
 
@@ -397,7 +439,7 @@ __device__ __forceinline__ void put_rows(T* out, const float (&v)[128], const Xe
   }
 }
 
-// kProdH, kProdW: this warp's columns of rows row0 .. row0 + 31 to the partial sums
+// kProd: this warp's columns of rows row0 .. row0 + 31 to the partial sums
 // or the result.
 __device__ __forceinline__ void epi_prod(const XentGemm& p, float (&v)[128], int row0, int lane,
                                          int n0, int left, int slice, float scale, uint32_t buf,
@@ -448,10 +490,7 @@ __device__ __forceinline__ void epi_prod(const XentGemm& p, float (&v)[128], int
 // frees its tensor memory and returns.
 template <int MODE, int PLANES>
 __global__ void __launch_bounds__(kThreads, 1)
-    xent_gemm_kernel(const __grid_constant__ XentGemm p, const __grid_constant__ CUtensorMap mA,
-                     const __grid_constant__ CUtensorMap mB,
-                     const __grid_constant__ CUtensorMap mOut) {
-  constexpr bool A_MN = MODE == kProdW, B_MN = MODE == kProdH || MODE == kProdW;
+    xent_gemm_kernel(const __grid_constant__ XentJobs jobs, const __grid_constant__ XentMaps maps) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ float wred[kEpiWarps];
   const uint32_t raw = smem_addr(smem_raw);
@@ -493,46 +532,58 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   const uint32_t tmem =
       even ? *tmem_slot : ld_shared_cluster_u32(mapa_shared(smem_addr(tmem_slot), 0));
-  const int units = p.tiles_m * p.tiles_n * p.slices;
-  const int pair = blockIdx.x >> 1, npairs_cta = gridDim.x >> 1;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const XentGemm& p0 = jobs.p[0];  // what both jobs have in common
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 0) {
       // ---------------------------------------------------------- copy issuer
       if (lane == 0) {
-        prefetch_tmap(&mA);
-        prefetch_tmap(&mB);
+        for (int j = 0; j < (MODE == kProd ? 2 : 1); ++j)
+          if (jobs.units[j]) prefetch_tmap(&maps.a[j]), prefetch_tmap(&maps.b[j]);
         int s = 0, issued = 0;
         uint32_t ph = 0;
         const uint32_t full_even = even ? full(0) : mapa_shared(full(0), 0);
-        for (int u = pair; u < units; u += npairs_cta) {
+        // false: stop
+        auto copy_unit = [&](auto mn, const XentGemm& p, const CUtensorMap* mA,
+                             const CUtensorMap* mB, int u) {
+          constexpr bool A_MN = decltype(mn)::value;
           int tm, tn, slice, kt0, kt1;
           unit_of(p, u, tm, tn, slice);
           slice_range(p, slice, kt0, kt1);
           const int ma = tm * kTile + (int)rank * 128, nb = tn * p.tile_n + (int)rank * (p.tile_n / 2);
+          const bool wide = p.tile_n > 128;
+          const uint32_t tx = 2 * p.stage_tx;
           for (int kt = kt0; kt < kt1; ++kt) {
-            #pragma unroll
+#pragma unroll
             for (int i = 0; i < PLANES; ++i) {
               const int plane = PLANES == 1 ? 0 : (i + 1) % 3;
-              if (p.debug_stop >= 0 && issued >= p.debug_stop) goto copies_done;
-              if (!wait_phase(empty(s), ph ^ 1u, p, kStatusTimeoutEmpty)) goto copies_done;
+              if (p0.debug_stop >= 0 && issued >= p0.debug_stop) return false;
+              if (!wait_phase(empty(s), ph ^ 1u, p0, kStatusTimeoutEmpty)) return false;
               const uint32_t st = base + s * kStageBytes;
-              if (even) mbar_arrive_expect_tx(full(s), 2 * p.stage_tx);
+              if (even) mbar_arrive_expect_tx(full(s), tx);
               const uint32_t fb = full_even + 8u * s;
-              load_operand<A_MN>(st, &mA, ma, kt, plane, fb);
-              load_operand<B_MN>(st + kATile, &mB, nb, kt, plane, fb, p.tile_n > 128);
+              load_operand<A_MN>(st, mA, ma, kt, plane, fb);
+              load_operand<MODE == kProd>(st + kATile, mB, nb, kt, plane, fb, wide);
               ++issued;
               if (++s == kStages) s = 0, ph ^= 1u;
             }
           }
+          return true;
+        };
+        for (int k = 0, job, u; unit_at<MODE>(jobs, pair, pairs, k, job, u); ++k) {
+          const bool on = MODE == kProd && job == 1
+                              ? copy_unit(Mn<MODE == kProd>(), jobs.p[1], &maps.a[1],
+                                          &maps.b[1], u)
+                              : copy_unit(Mn<false>(), jobs.p[0], &maps.a[0], &maps.b[0], u);
+          if (!on) break;
         }
-      copies_done:
         // leave only after the copies started here have landed (the odd CTA sees
         // the MMAs release the stages they read)
         for (int d = 0, pending = min(issued, kStages); d < pending; ++d) {
           if (--s < 0) s = kStages - 1, ph ^= 1u;
-          if (!wait_phase(even ? full(s) : empty(s), ph, p, kStatusTimeoutDrain))
+          if (!wait_phase(even ? full(s) : empty(s), ph, p0, kStatusTimeoutDrain))
             break;
         }
       }
@@ -540,34 +591,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       // ---------------------------------------------------------- MMA issuer (even CTA)
       if (even && lane == 0) {
-        const uint32_t idesc = idesc_bf16(kTile, p.tile_n, A_MN, B_MN);
         int s = 0, a = 0;
         uint32_t ph = 0, aph = 0;
         // One thread issues everything, a few cycles an instruction: what can be is
         // computed once.
         const uint32_t empty_odd = mapa_shared(empty(0), 1), tfull_odd = mapa_shared(tfull(0), 1);
-        const uint32_t a0 = desc_lo<A_MN>(base), b0 = desc_lo<B_MN>(base + kATile);
-        for (int u = pair; u < units; u += npairs_cta) {
+        const uint32_t b0 = desc_lo<MODE == kProd>(base + kATile);
+        constexpr uint32_t bstep = kDescStep<MODE == kProd>;
+        // false: a wait has run out
+        auto mma_unit = [&](auto mn, const XentGemm& p, int u) {
+          constexpr bool A_MN = decltype(mn)::value;
+          const uint32_t idesc = idesc_bf16(kTile, p.tile_n, A_MN, MODE == kProd);
+          const uint32_t a0 = desc_lo<A_MN>(base);
+          constexpr uint32_t astep = kDescStep<A_MN>;
+          const int group = p.group;
           int tm, tn, slice, kt0, kt1;
           unit_of(p, u, tm, tn, slice);
           slice_range(p, slice, kt0, kt1);
           const int groups = groups_of(p, kt1 - kt0);
           for (int g = 0; g < groups; ++g) {
-            if (!wait_phase(tempty(a), aph ^ 1u, p, kStatusTimeoutTmem))
-              goto mma_done;
+            if (!wait_phase(tempty(a), aph ^ 1u, p0, kStatusTimeoutTmem))
+              return false;
             tc_fence_after_sync();
             const uint32_t d = tmem + (uint32_t)(a * kTile);
-            const int kts = min(p.group, kt1 - kt0 - g * p.group);
+            const int kts = min(group, kt1 - kt0 - g * group);
             for (int it = 0; it < kts; ++it) {
-              if (!wait_phase(full(s), ph, p, kStatusTimeoutFull))
-                goto mma_done;
+              if (!wait_phase(full(s), ph, p0, kStatusTimeoutFull))
+                return false;
               tc_fence_after_sync();
               const uint32_t off = (uint32_t)s * kStageStep;
               if constexpr (PLANES == 1) {
 #pragma unroll
                 for (int kk = 0; kk < kBK / 16; ++kk)
-                  mma_bf16_pair(d, a0 + off + kk * kDescStep<A_MN>, b0 + off + kk * kDescStep<B_MN>,
-                                idesc, (it > 0 || kk > 0) ? 1u : 0u);
+                  mma_bf16_pair(d, a0 + off + kk * astep, b0 + off + kk * bstep, idesc,
+                                (it > 0 || kk > 0) ? 1u : 0u);
                 mma_commit_pair(empty(s));
                 mma_commit_pair(empty_odd + 8u * s);
                 if (++s == kStages) s = 0, ph ^= 1u;
@@ -577,14 +634,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const uint32_t ai = a0 + off + stage_of(plane_a(i)) * kStageStep;
                   const uint32_t bi = b0 + off + stage_of(plane_b(i)) * kStageStep;
                   if (i == 1) {  // the other two planes
-                    if (!wait_phase(full(s + 1), ph, p, kStatusTimeoutFull) ||
-                        !wait_phase(full(s + 2), ph, p, kStatusTimeoutFull))
-                      goto mma_done;
+                    if (!wait_phase(full(s + 1), ph, p0, kStatusTimeoutFull) ||
+                        !wait_phase(full(s + 2), ph, p0, kStatusTimeoutFull))
+                      return false;
                     tc_fence_after_sync();
                   }
 #pragma unroll
                   for (int kk = 0; kk < kBK / 16; ++kk)
-                    mma_bf16_pair(d, ai + kk * kDescStep<A_MN>, bi + kk * kDescStep<B_MN>, idesc,
+                    mma_bf16_pair(d, ai + kk * astep, bi + kk * bstep, idesc,
                                   (it > 0 || i > 0 || kk > 0) ? 1u : 0u);
                   // planes 2, 1 and 0 have been read after products 2, 4 and 5
                   if (i == 2 || i >= 4) {
@@ -601,10 +658,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit_pair(tfull_odd + 8u * a);
             if (++a == 2) a = 0, aph ^= 1u;
           }
-        }
-      mma_done:
+          return true;
+        };
+        for (int k = 0, job, u; unit_at<MODE>(jobs, pair, pairs, k, job, u); ++k)
+          if (!(MODE == kProd && job == 1 ? mma_unit(Mn<MODE == kProd>(), jobs.p[1], u)
+                                        : mma_unit(Mn<false>(), jobs.p[0], u)))
+            break;
         mma_commit_pair(drain);
-        wait_phase(drain, 0, p, kStatusTimeoutTmem);
+        wait_phase(drain, 0, p0, kStatusTimeoutTmem);
       }
       __syncwarp();
     }
@@ -612,26 +673,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------- epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int q = warp & 3, half = (warp - 4) >> 2;
-    const int span = span_of(p.tile_n);
-    const uint32_t tmem_lane = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * span);
+    const uint32_t tmem_row = tmem + ((uint32_t)(32 * q) << 16);
     const uint32_t buf = outs + (uint32_t)(warp - 4) * kOutBytes;
     const uint32_t tempty_even = even ? 0u : mapa_shared(tempty(0), 0);
     float scale = 1.f;
     if constexpr (MODE == kDz) {
-      scale = largest_weight(p, wred, threadIdx.x - 128);
-      if (blockIdx.x == 0 && threadIdx.x == 128) *p.scale = scale;
+      scale = largest_weight(p0, wred, threadIdx.x - 128);
+      if (blockIdx.x == 0 && threadIdx.x == 128) *p0.scale = scale;
       scale = scale > 0.f ? 1.f / scale : 0.f;
     } else if constexpr (MODE != kStats) {
-      scale = *p.scale;
+      scale = *p0.scale;
     }
     int a = 0;
     uint32_t aph = 0;
-    for (int u = pair; u < units; u += npairs_cta) {
+    for (int k = 0, job, u; unit_at<MODE>(jobs, pair, pairs, k, job, u); ++k) {
+      const XentGemm& p = jobs.p[MODE == kProd ? job : 0];
+      const CUtensorMap* out = &maps.out[MODE == kProd ? job : 0];
+      const int span = span_of(p.tile_n);
       int tm, tn, slice, kt0, kt1;
       unit_of(p, u, tm, tn, slice);
       slice_range(p, slice, kt0, kt1);
       float acc[128];
-      if (!collect(p, acc, tmem_lane, span, groups_of(p, kt1 - kt0), a, aph,
+      if (!collect(p0, acc, tmem_row + (uint32_t)(half * span), span, groups_of(p, kt1 - kt0), a, aph,
                    tfull(0), tempty(0), tempty_even, even, lane))
         break;
       const int row0 = tm * kTile + (int)rank * 128 + 32 * q;
@@ -642,9 +705,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (MODE == kStats)
           epi_stats(p, acc, row0 + lane, n0, left, tn * parts_of(p.tile_n) + half);
         else if constexpr (MODE == kDz)
-          epi_dz<PLANES>(p, acc, row0, lane, n0, left, scale, buf, &mOut);
+          epi_dz<PLANES>(p, acc, row0, lane, n0, left, scale, buf, out);
         else
-          epi_prod(p, acc, row0, lane, n0, left, slice, scale, buf, &mOut);
+          epi_prod(p, acc, row0, lane, n0, left, slice, scale, buf, out);
       }
     }
     if constexpr (MODE != kStats) {
@@ -839,31 +902,52 @@ int resident_pairs(int dev, int sms) {
   return pairs;
 }
 
-// Fills in the tiling and launches one product.
+// Fills in the tiling and launches the jobs that have a tile width.
 template <int MODE, int PLANES>
-int launch_planes(XentGemm p, const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mOut,
-                const TrainDevice& d, cudaStream_t st) {
+int launch_planes(XentJobs& jobs, const XentMaps& maps, const TrainDevice& d, cudaStream_t st) {
   const int pairs = resident_pairs<MODE, PLANES>(d.dev, d.sms);
   if (!pairs) return B2G_ERR_CUDA;
-  p.tiles_m = (int)ceil_div(p.rows, kTile), p.tiles_n = (int)ceil_div(p.cols, p.tile_n);
-  p.group_m = 16;
-  p.wait_limit_ns = d.wait_limit_ns, p.debug_stop = d.debug_stop, p.status = d.status;
-  const long long units = (long long)p.tiles_m * p.tiles_n * p.slices;
-  if (units > 0x3fffffffLL) return B2G_ERR_INVALID_DIM;
+  long long units = 0, cost[2] = {0, 0};
+  for (int j = 0; j < 2; ++j) {
+    XentGemm& p = jobs.p[j];
+    p.wait_limit_ns = d.wait_limit_ns, p.debug_stop = d.debug_stop, p.status = d.status;
+    jobs.units[j] = 0;
+    if (!p.tile_n) continue;
+    p.tiles_m = (int)ceil_div(p.rows, kTile), p.tiles_n = (int)ceil_div(p.cols, p.tile_n);
+    p.group_m = 16;
+    const long long n = (long long)p.tiles_m * p.tiles_n * p.slices;
+    units += n;
+    if (units > 0x3fffffffLL) return B2G_ERR_INVALID_DIM;
+    jobs.units[j] = (int)n;
+    cost[j] = ceil_div(p.k_tiles, p.slices) * k_tile_cost(PLANES, kTile + p.tile_n);
+  }
+  const int used = (int)(units < pairs ? units : pairs);
+  jobs.full = jobs.units[0] / used, jobs.rest = jobs.units[0] % used, jobs.extra = 0;
+  if (jobs.rest && jobs.units[1]) {  // as many as job 0's last units take, one more or not
+    const long long others = used - jobs.rest, most = ceil_div(jobs.units[1], others);
+    long long best = -1;
+    for (long long e = cost[0] / cost[1], i = 0; i < 2; ++i, ++e) {
+      const long long x = e < most ? e : most;
+      const long long after = jobs.units[1] > x * others ? jobs.units[1] - x * others : 0;
+      const long long all = after / used, left = after % used;
+      const long long t0 = cost[0] + (all + (left > 0)) * cost[1];
+      const long long t1 = (x + all + (left > jobs.rest)) * cost[1];
+      if (best < 0 || (t0 > t1 ? t0 : t1) < best) best = t0 > t1 ? t0 : t1, jobs.extra = (int)x;
+    }
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * (units < pairs ? units : pairs)));
+  cfg.gridDim = dim3((unsigned)(2 * used));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  CUtensorMap a = mA, b = mB, o = mOut;
-  void* args[] = {&p, &a, &b, &o};
+  void* args[] = {&jobs, const_cast<XentMaps*>(&maps)};
   return launch_code(
       cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&xent_gemm_kernel<MODE, PLANES>), args));
 }
@@ -876,10 +960,9 @@ int launch_planes(XentGemm p, const CUtensorMap& mA, const CUtensorMap& mB, cons
 int group_of(int dtype, bool logits) { return dtype == B2G_F32 ? 2 : logits ? 16 : 1 << 20; }
 
 template <int MODE>
-int launch_gemm(const XentGemm& p, const CUtensorMap& mA, const CUtensorMap& mB,
-                const CUtensorMap& mOut, const TrainDevice& d, cudaStream_t st) {
-  return p.planes == 1 ? launch_planes<MODE, 1>(p, mA, mB, mOut, d, st)
-                       : launch_planes<MODE, 3>(p, mA, mB, mOut, d, st);
+int launch_gemm(XentJobs& jobs, const XentMaps& maps, const TrainDevice& d, cudaStream_t st) {
+  return jobs.p[0].planes == 1 ? launch_planes<MODE, 1>(jobs, maps, d, st)
+                               : launch_planes<MODE, 3>(jobs, maps, d, st);
 }
 
 struct Call {
@@ -897,21 +980,24 @@ int check(const Call& c) {
   return 0;
 }
 
-// Columns of a tile of a gradient (128 or 256) and its k slices: the cheapest rounds,
-// counting what several slices' partial sums cost (written and read at about 3400 bytes
+// Columns of a tile of a gradient (128 or 256) and its k slices: the cheapest rounds, with
+// `beside` cycles of the other gradient's units to fill them up, counting what several
+// slices' partial sums cost (written and read at about 3400 bytes
 // a cycle, and a launch that adds them).  Slices have at least 8 k tiles each; a narrower
 // tile or another slice has to save a twentieth.
 struct Plan {
   int tile_n, slices;
 };
-Plan plan_product(int planes, long long rows, int cols, int k_tiles) {
+Plan plan_product(int planes, long long rows, int cols, int k_tiles, long long beside) {
   Plan best{kTile, 1};
   long long cost = -1;
   for (int tn = kTile; tn >= 128; tn -= 128) {
     const long long tiles = ceil_div(rows, kTile) * ceil_div(cols, tn);
     for (int s = 1; s == 1 || (s <= kMaxSlices && s <= k_tiles / 8); ++s) {
-      const long long c = ceil_div(tiles * s, kPlanPairs) * ceil_div(k_tiles, s) *
-                              k_tile_cost(planes, kTile + tn) + kColumnCost * tn +
+      const long long unit = ceil_div(k_tiles, s) * k_tile_cost(planes, kTile + tn);
+      const long long alone = ceil_div(tiles * s, kPlanPairs) * unit;
+      const long long shared = (tiles * s * unit + beside) / kPlanPairs;
+      const long long c = (alone > shared ? alone : shared) + kColumnCost * tn +
                           (s > 1 ? 4000 + s * rows * cols * 8 / 3400 : 0);
       if (cost < 0 || c < cost - cost / 20) best = Plan{tn, s}, cost = c;
     }
@@ -970,8 +1056,11 @@ Layout layout(const Call& c, bool backward) {
     l.dz_ld = l.piece;
     l.part_ld = (long long)round_up(c.width, 4);
     const int classes = l.piece < c.vocab ? l.piece : c.vocab;
-    const Plan ph = plan_product(l.planes, c.tokens, c.width, (int)ceil_div(classes, kBK));
-    const Plan pw = plan_product(l.planes, classes, c.width, (int)ceil_div(c.tokens, kBK));
+    const int kh = (int)ceil_div(classes, kBK), kw = (int)ceil_div(c.tokens, kBK);
+    const Plan pw = plan_product(l.planes, classes, c.width, kw, 0);
+    const Plan ph = plan_product(l.planes, c.tokens, c.width, kh,
+                                 ceil_div(classes, kTile) * ceil_div(c.width, pw.tile_n) * kw *
+                                     k_tile_cost(l.planes, kTile + pw.tile_n));
     l.tile_h = ph.tile_n, l.slices_h = ph.slices, l.tile_w = pw.tile_n, l.slices_w = pw.slices;
     l.scale = take(sizeof(float));
     l.dz = take((size_t)l.planes * c.tokens * l.dz_ld * 2);
@@ -1068,18 +1157,19 @@ int b2g_linear_xent(int dtype, int tokens, int vocab, int width, const void* h, 
     rc = launch_few_stats(rows, ph, FewHead{w, ldw, dtype == B2G_F32}, stat, zt, d, st);
     return rc ? rc : join();
   }
-  CUtensorMap mh, mw;
-  rc = map_k(&mh, ph, token_box(tokens));
-  if (!rc) rc = map_k(&mw, pw, l.tile_n / 2);
+  XentMaps maps = {};
+  rc = map_k(&maps.a[0], ph, token_box(tokens));
+  if (!rc) rc = map_k(&maps.b[0], pw, l.tile_n / 2);
   if (rc) return rc;
-  XentGemm p = {};
+  XentJobs jobs = {};
+  XentGemm& p = jobs.p[0];
   p.tile_n = l.tile_n, p.stage_tx = (token_box(tokens) + l.tile_n / 2) * 128;
   p.rows = tokens, p.cols = vocab;
   p.k_tiles = (int)ceil_div(width, kBK), p.planes = l.planes, p.slices = 1;
   p.group = group_of(dtype, true);
   p.target = target, p.id_bytes = id_bytes, p.vocab = vocab, p.ignore = ignore_index;
   p.stat = stat, p.zt = zt;
-  rc = launch_gemm<kStats>(p, mh, mw, mw, d, st);
+  rc = launch_gemm<kStats>(jobs, maps, d, st);
   return rc ? rc : join();
 }
 
@@ -1130,9 +1220,7 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
     if (!l.few) piece = pw, piece.p += (long long)first * pw.ld, piece.rows = n;
     const Planes dz{reinterpret_cast<Bf16*>(ws + l.dz), tokens, n, l.dz_ld,
                     (long long)tokens * l.dz_ld, l.planes};
-    CUtensorMap a, b, o = {};
     // dz of these classes
-    XentGemm p = base;
     if (l.few) {
       rc = launch_few_dz(few_rows, ph, head, first, n, lse, grad_loss, dz, base.scale, d, st);
       const int each = l.slices_h / l.pieces;
@@ -1140,55 +1228,65 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
         rc = launch_few_dh(few_rows, dz, head, first, n, base.scale, each,
                            hpart + (size_t)i * each * hslice, l.part_ld, d, st);
     } else {
+      XentJobs jobs = {};
+      XentMaps maps = {};
+      XentGemm& p = jobs.p[0];
+      p = base;
       p.rows = tokens, p.cols = n, p.k_tiles = (int)ceil_div(width, kBK);
       p.tile_n = l.tile_n, p.stage_tx = (token_box(tokens) + l.tile_n / 2) * 128;
       p.group = group_of(dtype, true);
       p.target = target, p.id_bytes = id_bytes, p.vocab = vocab, p.ignore = ignore_index;
       p.col0 = first, p.lse = lse, p.gloss = grad_loss;
-      rc = map_k(&a, ph, token_box(tokens));
-      if (!rc) rc = map_k(&b, piece, l.tile_n / 2);
-      if (!rc) rc = map_out(&o, dz);
-      if (!rc) rc = launch_gemm<kDz>(p, a, b, o, d, st);
+      rc = map_k(&maps.a[0], ph, token_box(tokens));
+      if (!rc) rc = map_k(&maps.b[0], piece, l.tile_n / 2);
+      if (!rc) rc = map_out(&maps.out[0], dz);
+      if (!rc) rc = launch_gemm<kDz>(jobs, maps, d, st);
     }
     if (rc) return rc;
+    XentJobs jobs = {};
+    XentMaps maps = {};
+    jobs.p[0] = jobs.p[1] = base;
     if (dh && !l.few) {  // dh += dz w over these classes
-      p = base;
+      XentGemm& p = jobs.p[0];
       p.rows = tokens, p.cols = width, p.k_tiles = (int)ceil_div(n, kBK);
       p.tile_n = l.tile_h, p.stage_tx = kATile + l.tile_h / 2 * 128;
       p.slices = l.slices_h < p.k_tiles ? l.slices_h : p.k_tiles;
       p.to_part = l.h_sums, p.add = i > 0;
       p.out = dh, p.ldo = lddh;
       p.out_tma = vec16(dh) && vec16_ld(lddh, dtype);
-      rc = map_k(&a, dz, 128);
-      if (!rc) rc = map_mn(&b, piece);
+      rc = map_k(&maps.a[0], dz, 128);
+      if (!rc) rc = map_mn(&maps.b[0], piece);
       if (!rc && (p.to_part || p.out_tma))
-        rc = p.to_part ? encode_rows(&o, true, hpart, width, tokens, l.part_ld, l.slices_h, hslice, 32)
-                       : encode_rows(&o, f32, dh, width, tokens, lddh, 1, 0, 32);
-      if (!rc) rc = launch_gemm<kProdH>(p, a, b, o, d, st);
+        rc = p.to_part ? encode_rows(&maps.out[0], true, hpart, width, tokens, l.part_ld,
+                                     l.slices_h, hslice, 32)
+                       : encode_rows(&maps.out[0], f32, dh, width, tokens, lddh, 1, 0, 32);
       if (rc) return rc;
     }
+    unsigned char* dw_rows =
+        dw ? static_cast<unsigned char*>(dw) + (long long)first * lddw * es : nullptr;
     if (dw) {  // these classes' rows of dw = dz^T h
-      p = base;
+      XentGemm& p = jobs.p[1];
       p.rows = n, p.cols = width, p.k_tiles = (int)ceil_div(tokens, kBK);
       p.tile_n = l.tile_w, p.stage_tx = kATile + l.tile_w / 2 * 128;
       p.slices = l.slices_w;
-      unsigned char* out = static_cast<unsigned char*>(dw) + (long long)first * lddw * es;
       p.to_part = l.slices_w > 1;
-      p.out = out, p.ldo = lddw, p.accumulate = accumulate != 0;
+      p.out = dw_rows, p.ldo = lddw, p.accumulate = accumulate != 0;
       // a bulk-tensor store adds in the output's type: right for FP32 only
-      p.out_tma = vec16(out) && vec16_ld(lddw, dtype) && !(accumulate && !f32);
+      p.out_tma = vec16(dw_rows) && vec16_ld(lddw, dtype) && !(accumulate && !f32);
       p.add = !p.to_part && accumulate;
-      rc = map_mn(&a, dz);
-      if (!rc) rc = map_mn(&b, ph);
+      rc = map_mn(&maps.a[1], dz);
+      if (!rc) rc = map_mn(&maps.b[1], ph);
       if (!rc && (p.to_part || p.out_tma))
-        rc = p.to_part ? encode_rows(&o, true, wpart, width, n, l.part_ld, l.slices_w, wslice, 32)
-                       : encode_rows(&o, f32, out, width, n, lddw, 1, 0, 32);
-      if (!rc) rc = launch_gemm<kProdW>(p, a, b, o, d, st);
-      if (!rc && p.to_part)
-        rc = reduce_to(wpart, l.slices_w, l.part_ld, wslice, n, width, out, lddw, p.accumulate,
-                       d, st);
+        rc = p.to_part ? encode_rows(&maps.out[1], true, wpart, width, n, l.part_ld, l.slices_w,
+                                     wslice, 32)
+                       : encode_rows(&maps.out[1], f32, dw_rows, width, n, lddw, 1, 0, 32);
       if (rc) return rc;
     }
+    if (jobs.p[0].tile_n || jobs.p[1].tile_n) rc = launch_gemm<kProd>(jobs, maps, d, st);
+    if (!rc && jobs.p[1].to_part)
+      rc = reduce_to(wpart, l.slices_w, l.part_ld, wslice, n, width, dw_rows, lddw,
+                     jobs.p[1].accumulate, d, st);
+    if (rc) return rc;
   }
   if (dh && l.h_sums)
     return reduce_to(hpart, l.slices_h, l.part_ld, hslice, tokens, width, dh, lddh, 0, d, st);
