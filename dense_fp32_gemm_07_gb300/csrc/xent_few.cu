@@ -14,7 +14,8 @@
 //   kDz     the same product, turned into dz (tokens x classes, BF16 planes)
 //   kDh     dh^T = w^T dz^T: w's columns are the rows of the MMA ("MN-major" A), k
 //           runs over the classes, cut into slices whose sums another kernel adds
-// Bound: the bytes of w.
+// Bound: the bytes of w: 16 x 32768 x 4096, scoring, 46 us in BF16 (5.9 TB/s); FP32 147 us
+// (3.7 TB/s), where splitting the values on their way holds the reads up.
 #include <atomic>
 
 #include "xent.cuh"

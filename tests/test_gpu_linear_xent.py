@@ -9,6 +9,8 @@ add the dropped plane products (4 * 2^-27) and five more passes of terms that ar
     (1.1 k / 16 + 8) 2^-22 + 2^-25
 of sum |a||b|.  From there the errors follow the formulas.
 """
+import ctypes
+
 import pytest
 import torch
 
@@ -241,6 +243,35 @@ def test_same_bits_every_run(b2g, dtype):
         assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
         got = b2g.linear_cross_entropy_backward(h, w, t, lse, g)
         assert all(torch.equal(p, q) for p, q in zip(first, got))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("tokens,vocab,width", [(40, 3000, 136), (300, 5000, 200), (700, 9000, 520)])
+def test_one_gradient_alone(b2g, tokens, vocab, width, dtype):
+    """dh or dw not wanted (NULL): the other one has the bits it has with both."""
+    lib, code = b2g.train.train_library(), 0 if dtype is F32 else 1
+    gen = torch.Generator().manual_seed(tokens)
+    h = torch.randn(tokens, width, generator=gen).to(dtype).cuda()
+    w = (torch.randn(vocab, width, generator=gen) * width ** -0.5).to(dtype).cuda()
+    target = torch.randint(0, vocab, (tokens,), generator=gen).cuda()
+    loss, lse = b2g.linear_cross_entropy(h, w, target)
+    g = torch.full((tokens,), 1.0 / tokens, device="cuda")
+    dh, dw = b2g.linear_cross_entropy_backward(h, w, target, lse, g)
+    nb = ctypes.c_size_t()
+    assert lib.b2g_linear_xent_workspace_size(code, tokens, vocab, width, h.data_ptr(), width,
+                                              w.data_ptr(), width, 1, ctypes.byref(nb)) == 0
+    ws = torch.empty(nb.value, dtype=torch.uint8, device="cuda")
+    for want in ("dh", "dw"):
+        out = torch.full_like(dh if want == "dh" else dw, float("nan"))
+        p = out.data_ptr()
+        rc = lib.b2g_linear_xent_backward(
+            code, tokens, vocab, width, h.data_ptr(), width, w.data_ptr(), width,
+            target.data_ptr(), 8, -100, lse.data_ptr(), g.data_ptr(), p if want == "dh" else None,
+            width, 0, p if want == "dw" else None, width, ws.data_ptr(), nb.value,
+            torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        assert torch.equal(out, dh if want == "dh" else dw), want
+    assert status(b2g)[0] == 0
 
 
 def test_gradient_against_differences(b2g):
