@@ -552,7 +552,9 @@ constexpr long long kMaxTokens = 1LL << 30;
 
 int check(int dtype, long long tokens, int vocab, int width) {
   if (!type_ok(dtype)) return B2G_ERR_INVALID_TYPE;
-  if (tokens < 0 || vocab < 0 || width < 0 || tokens > kMaxTokens) return B2G_ERR_INVALID_DIM;
+  if (tokens < 0 || vocab < 0 || width < 0 || tokens > kMaxTokens || vocab > kMaxLength ||
+      width > kMaxLength)
+    return B2G_ERR_INVALID_DIM;
   return 0;
 }
 

@@ -869,7 +869,7 @@ cudaError_t bwd_launch(LnBwd p, int dtype, T* dweight, T* dbias, int parts, cons
 
 int check_rows(int dtype, long long rows, int cols) {
   if (!type_ok(dtype)) return B2G_ERR_INVALID_TYPE;
-  if (rows < 0 || cols < 0 || rows > 0x7fffffffLL) return B2G_ERR_INVALID_DIM;
+  if (rows < 0 || cols < 0 || rows > 0x7fffffffLL || cols > kMaxLength) return B2G_ERR_INVALID_DIM;
   return 0;
 }
 

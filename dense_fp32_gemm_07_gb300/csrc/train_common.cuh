@@ -23,6 +23,9 @@ struct TrainDevice {
   unsigned long long wait_limit_ns;
   int debug_stop;
 };
+// Row lengths, classes and tokens of a product: a column index plus what a block strides
+// over stays below 2^31.
+constexpr int kMaxLength = 0x7fff0000;
 int train_device(TrainDevice* out);  // 0 or a B2G_ERR_* code (host.cu)
 
 using Bf16 = __nv_bfloat16;

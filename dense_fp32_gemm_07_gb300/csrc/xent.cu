@@ -976,7 +976,9 @@ struct Call {
 
 int check(const Call& c) {
   if (!type_ok(c.dtype)) return B2G_ERR_INVALID_TYPE;
-  if (c.tokens < 0 || c.vocab < 1 || c.width < 1) return B2G_ERR_INVALID_DIM;
+  if (c.tokens < 0 || c.vocab < 1 || c.width < 1 || c.tokens > kMaxLength ||
+      c.vocab > kMaxLength || c.width > kMaxLength)
+    return B2G_ERR_INVALID_DIM;
   if (c.ldh < c.width || c.ldw < c.width) return B2G_ERR_INVALID_LD;
   return 0;
 }

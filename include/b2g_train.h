@@ -23,6 +23,9 @@
  * Results are the same bits run to run for given arguments: every sum has a
  * fixed order, and no floating-point atomics are used.
  *
+ * Sizes: row lengths, vocab and the cross entropy's tokens are at most 2^31 - 2^16,
+ * layer norm's rows 2^31 - 1 and the embedding's tokens 2^30, else B2G_ERR_INVALID_DIM.
+ *
  * Alignment: any.  Operands whose base is 16-byte aligned and whose leading
  * dimensions (and width) are multiples of 16 bytes run with 16-byte accesses.
  */

@@ -125,6 +125,22 @@ def test_linear_xent_backward_arguments(lib, change, code):
     assert lib.b2g_linear_xent_backward(*a.values()) == code
 
 
+LONG = (1 << 31) - (1 << 16) + 1
+
+
+def test_lengths_past_the_limits(lib):
+    """Refused before anything else of the call is looked at."""
+    n = ctypes.c_size_t()
+    assert lib.b2g_layernorm(0, 4, LONG, P, LONG, P, P, 1e-5, P, LONG, P, P, 0) == -1
+    assert lib.b2g_layernorm_backward_workspace_size(0, 4, LONG, ctypes.byref(n)) == -1
+    for vocab, width in ((LONG, 8), (8, LONG)):
+        assert lib.b2g_embedding(0, 4, vocab, width, P, 8, P, LONG, 1.0, P, LONG, 0) == -1
+        assert lib.b2g_embedding_backward_workspace_size(0, 4, vocab, width, ctypes.byref(n)) == -1
+    for tokens, vocab, width in ((LONG, 8, 8), (8, LONG, 8), (8, 8, LONG)):
+        assert lib.b2g_linear_xent_workspace_size(1, tokens, vocab, width, P, LONG, P, LONG, 0,
+                                                  ctypes.byref(n)) == -1
+
+
 def test_clip_arguments(lib):
     one, n = (ctypes.c_void_p * 1)(P), (ctypes.c_longlong * 1)(5)
     neg, null = (ctypes.c_longlong * 1)(-5), (ctypes.c_void_p * 1)(None)
