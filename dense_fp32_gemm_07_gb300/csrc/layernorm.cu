@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(512) ln_fwd_kernel(const __grid_constant__ LnF
 // slot; up to 192 KB an SM), so a row's latency is not waited for; a slot is
 // refilled once the group's first sum has been exchanged, when every thread has
 // read it.
-constexpr int kFwdThreads = 512, kBwdThreads = 256;  // 32 columns a thread in either
-constexpr int kAnyThreads = 512;                     // 16: the backward pass off the boundaries
+constexpr int kFwdThreads = 512;  // 32 columns a thread
+constexpr int kBwdThreads = 512;  // 16
 constexpr int kRingBytes = 192 * 1024;
 constexpr int kRingStages = 16;  // at most
 
@@ -343,13 +343,13 @@ struct LnBwd {
   float* part;  // [grid][2][cols]: partial dweight, then dbias; NULL: neither is wanted
 };
 
-// Rows on 16-byte boundaries: the ring above with rows of x and dy together, 32
+// Rows on 16-byte boundaries: the ring above with rows of x and dy together, 16
 // columns a thread (FULL: every thread has all of them).  With t = x - mean,
 //     dx = rstd g + (-rstd^3 mean(g t)) t - rstd mean(g),
 // two operations an element once g and t are there.  At the end the groups' column
-// sums are added in shared memory in group order.  8192 x 4096 BF16: 41 us with the
-// reduction (4.9 TB/s); the weights and 64 column sums a thread leave room for one block of 256
-// threads, whose latency per row the ring hides only in part.
+// sums are added in shared memory in group order.  8192 x 4096 BF16: 40 us with the
+// reduction (5.0 TB/s; the ring alone 36, 5.6 TB/s); 65536 x 256 BF16 29 us, 41 with 32
+// columns a thread in half the threads.
 template <typename T, int VEC, bool FULL>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     ln_bwd_ring_kernel(const __grid_constant__ LnBwd p, const __grid_constant__ Ring g,
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ __align__(8) unsigned long long bars[kBwdThreads / 32 * kRingStages];
   __shared__ F2 red[2][16];
-  constexpr int H = VEC / 2, NCH = 32 / VEC;
+  constexpr int H = VEC / 2, NCH = 16 / VEC;
   pdl_launch_dependents();
   const int group = threadIdx.x / g.nt, t = threadIdx.x - group * g.nt;
   const uint32_t bytes = (uint32_t)(p.cols * (int)sizeof(T));
@@ -522,16 +522,16 @@ inline __host__ __device__ size_t any_slot(int cols, size_t es) {
 }
 
 // The same for rows off the 16-byte boundaries, each thread with the 16 columns
-// t + i * nt (in twice the threads) and the weights in shared memory.  8192 x 4095:
+// t + i * nt and the weights in shared memory.  8192 x 4095:
 // 91 us in BF16, 87 in FP32 (2.3 and 4.6 TB/s), against 182 and 197 with the rows read
 // element by element from global memory; element by element it is still issue that
 // bounds it, on the boundaries the same size takes 41 in BF16.
 template <typename T>
-__global__ void __launch_bounds__(kAnyThreads, 1)
+__global__ void __launch_bounds__(kBwdThreads, 1)
     ln_bwd_any_kernel(const __grid_constant__ LnBwd p, const __grid_constant__ Ring g,
                       unsigned int* status, unsigned long long wait_limit_ns) {
   extern __shared__ __align__(128) unsigned char ring[];
-  __shared__ __align__(8) unsigned long long bars[kAnyThreads / 32 * kRingStages];
+  __shared__ __align__(8) unsigned long long bars[kBwdThreads / 32 * kRingStages];
   __shared__ F2 red[2][16];
   constexpr int N = 16;
   pdl_launch_dependents();
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kAnyThreads, 1)
     for (int s = 0; s < g.stages && row < p.rows; ++s, row += step) issue(row, s);
   }
   T* ws = reinterpret_cast<T*>(ring + (size_t)g.groups * g.stages * 2 * slot);
-  for (int c = threadIdx.x; c < p.cols; c += kAnyThreads)
+  for (int c = threadIdx.x; c < p.cols; c += kBwdThreads)
     ws[c] = p.w ? static_cast<const T*>(p.w)[c] : from_f32<T>(1.f);
   __syncthreads();
   float aw[N], ab[N];
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kAnyThreads, 1)
   __syncthreads();
   const float* all = reinterpret_cast<const float*>(ring);
   float* out = p.part + (size_t)blockIdx.x * 2 * p.cols;
-  for (int c = threadIdx.x; c < 2 * p.cols; c += kAnyThreads) {
+  for (int c = threadIdx.x; c < 2 * p.cols; c += kBwdThreads) {
     float a = all[c];
     for (int i = 1; i < g.groups; ++i) a += all[(size_t)2 * i * p.cols + c];
     out[c] = a;
@@ -750,8 +750,8 @@ Ring fwd_ring_of(int cols, int dtype) {
 // vec: rows on 16-byte boundaries.
 Ring bwd_ring_of(int cols, int dtype, bool vec) {
   const size_t es = type_size(dtype);
-  return vec ? ring_of(kBwdThreads, 32, cols, 2 * cols * es, 0)
-             : ring_of(kAnyThreads, 16, cols, 2 * any_slot(cols, es), es * cols);
+  return vec ? ring_of(kBwdThreads, 16, cols, 2 * cols * es, 0)
+             : ring_of(kBwdThreads, 16, cols, 2 * any_slot(cols, es), es * cols);
 }
 
 // Opt in to the ring's shared memory, once per device and kernel.
@@ -838,7 +838,7 @@ cudaError_t bwd_any(const LnBwd& p, const Ring& r, int parts, const TrainDevice&
   const size_t rings =
       (size_t)r.groups * r.stages * 2 * any_slot(p.cols, sizeof(T)) + p.cols * sizeof(T);
   const size_t sums = (size_t)r.groups * 2 * p.cols * sizeof(float);
-  return launch_train(ln_bwd_any_kernel<T>, dim3(parts), dim3(kAnyThreads),
+  return launch_train(ln_bwd_any_kernel<T>, dim3(parts), dim3(kBwdThreads),
                       rings > sums ? rings : sums, st, p, r, d.status, d.wait_limit_ns);
 }
 
@@ -850,7 +850,7 @@ cudaError_t bwd_launch(LnBwd p, int dtype, T* dweight, T* dbias, int parts, cons
   const Ring r = bwd_ring_of(p.cols, dtype, VEC > 1);
   if (r.stages >= 2) {
     if constexpr (VEC > 1)
-      e = r.nt * 32 == p.cols ? bwd_ring<T, VEC, true>(p, r, parts, d, st)
+      e = r.nt * 16 == p.cols ? bwd_ring<T, VEC, true>(p, r, parts, d, st)
                               : bwd_ring<T, VEC, false>(p, r, parts, d, st);
     else
       e = bwd_any<T>(p, r, parts, d, st);
