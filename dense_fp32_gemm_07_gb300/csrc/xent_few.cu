@@ -110,26 +110,33 @@ struct Pieces {
     else
       row = (ct >> 3) + 32 * i, col = (ct & 7) * 8;   // 128 classes x 64 k
   }
-  // Rows of w stand on 16-byte boundaries; past its end there are zeros.
+  // Rows of w stand on 16-byte boundaries; past its end there are zeros.  Where all the
+  // tile's columns exist the loads are predicated, not branched around: a branch would
+  // wait for each load before the next one.
   __device__ __forceinline__ void load(const FewGemm& p, int m0, int k0, int ct) {
+    const int c0 = MN ? m0 : k0, rows = MN ? 64 : p.tile_rows;
+    const bool whole = c0 + (MN ? kM : kBK) <= p.acols;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       int row, col;
       where(i, ct, row, col);
-      const int r = (MN ? k0 : m0) + row, c = (MN ? m0 : k0) + col;
-      const bool in = r < p.arows && (MN || row < p.tile_rows);
+      const int r = (MN ? k0 : m0) + row, c = c0 + col;
+      const bool in = r < p.arows && row < rows;
       const float* q = p.wf + (long long)r * p.ldw + c;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (in && c + 4 * h + 4 <= p.acols) {
-          v = *reinterpret_cast<const float4*>(q + 4 * h);
-        } else if (in) {  // the last columns of a width that is no multiple of 4
-          if (c + 4 * h < p.acols) v.x = q[4 * h];
-          if (c + 4 * h + 1 < p.acols) v.y = q[4 * h + 1];
-          if (c + 4 * h + 2 < p.acols) v.z = q[4 * h + 2];
-        }
-        f[i][4 * h] = v.x, f[i][4 * h + 1] = v.y, f[i][4 * h + 2] = v.z, f[i][4 * h + 3] = v.w;
+      for (int j = 0; j < 8; ++j) f[i][j] = 0.f;
+      if (whole) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 4)
+          asm volatile(
+              "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\t"
+              "@p ld.global.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
+              : "+f"(f[i][j]), "+f"(f[i][j + 1]), "+f"(f[i][j + 2]), "+f"(f[i][j + 3])
+              : "l"(q + j), "r"((int)in));
+      } else if (in) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < p.acols) f[i][j] = q[j];
       }
     }
   }
