@@ -7,15 +7,15 @@
 // would multiply mostly padding; the tile's height is chosen so that the SMs get
 // equal shares of w; and an FP32 w is read by eight converter warps, three steps ahead
 // in registers, and split into its BF16 planes on the way to shared memory, instead
-// of by a pass over all of w (which costs 16 bytes an element: 478 us became 148 at 16
+// of by a pass over all of w (which costs 16 bytes an element: 478 us became 134 at 16
 // x 32768 x 4096).  Modes:
 //   kStats  z^T = w h^T: per token and CTA, the maximum and the sum of the
 //           exponentials below it, and the target's logit
 //   kDz     the same product, turned into dz (tokens x classes, BF16 planes)
 //   kDh     dh^T = w^T dz^T: w's columns are the rows of the MMA ("MN-major" A), k
 //           runs over the classes, cut into slices whose sums another kernel adds
-// Bound: the bytes of w: 16 x 32768 x 4096, scoring, 46 us in BF16 (5.9 TB/s); FP32 147 us
-// (3.7 TB/s), where splitting the values on their way holds the reads up.
+// Bound: the bytes of w: 16 x 32768 x 4096, scoring, 46 us in BF16 (5.9 TB/s); FP32 134 us
+// (4.0 TB/s), where splitting the values on their way holds the reads up.
 #include <atomic>
 
 #include "xent.cuh"
@@ -608,7 +608,9 @@ int launch_rows(FewGemm p, const XentRows& r, const Planes& h, const FewHead& w,
   p.tokens = r.tokens, p.nt = padded_tokens(r.tokens);
   p.tile_rows = tile_rows_for(p.rows), p.tiles = (int)ceil_div(p.rows, p.tile_rows);
   p.k_tiles = (int)ceil_div(r.width, w.f32 ? kBK : 2 * kBK), p.slices = 1;
-  p.group = w.f32 ? 1 : 8;  // 64 and 1024 k
+  // 64 and 1024 k.  (FP32: 256 k would take 131 us for 134 at 16 x 32768 x 4096, with three
+  // times the error of the loss.)
+  p.group = w.f32 ? 1 : 8;
   p.a_tx = (uint32_t)(p.tile_rows * kBK * es);
   p.target = r.target, p.id_bytes = r.id_bytes, p.vocab = r.vocab, p.ignore = r.ignore;
   CUtensorMap a = {}, b = {};
