@@ -269,8 +269,13 @@ __device__ __forceinline__ bool collect(const XentGemm& p, float (&acc)[128], ui
   return true;
 }
 
-// A lane's row of 128 bytes to its warp's buffer, in the 128-byte swizzle.
+// A lane's row of 128 bytes to its warp's buffer, in the 128-byte swizzle.  Every write to
+// the buffer goes through here and first waits for whoever still reads it: the last
+// bulk-tensor store (lane 0 committed it; a unit of the other gradient may have left
+// through one just before), then the warp's other lanes.
 __device__ __forceinline__ void stage_rows(uint32_t buf, const uint4 (&w)[8], int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t at = buf + lane * 128u + (uint32_t)((i ^ (lane & 7)) * 16);
@@ -286,8 +291,6 @@ __device__ __forceinline__ void stage_rows(uint32_t buf, const uint4 (&w)[8], in
 // leaves out rows and columns past the tensor.
 __device__ __forceinline__ void store_rows(uint32_t buf, const CUtensorMap* m, int x, int y, int z,
                                            const uint4 (&w)[8], bool add, int lane) {
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-  __syncwarp();  // the buffer's last store has been read
   stage_rows(buf, w, lane);
   fence_proxy_async_smem();
   __syncwarp();
@@ -435,7 +438,6 @@ __device__ __forceinline__ void put_rows(T* out, const float (&v)[128], const Xe
           *q = from_f32<T>(p.accumulate ? x + to_f32(*q) : x);
         }
       }
-      __syncwarp();
     }
   }
 }

@@ -245,6 +245,24 @@ def test_same_bits_every_run(b2g, dtype):
         assert all(torch.equal(p, q) for p, q in zip(first, got))
 
 
+@pytest.mark.parametrize("dtype,tokens,vocab,width,accumulate", [
+    (BF16, 100, 5000, 777, False), (BF16, 700, 20001, 1001, False), (F32, 1000, 11007, 777, False),
+    (BF16, 100, 60000, 512, True), (F32, 200, 9000, 333, True)])
+def test_gradients_that_leave_in_two_ways(b2g, dtype, tokens, vocab, width, accumulate):
+    """One launch in which a warp's buffer takes tiles of dh for bulk-tensor stores and then
+    tiles of dw that go out element by element (an odd width, or adding to BF16 values):
+    the 64-bit bound, and the same bits every time."""
+    h, w, t, g = make(tokens, vocab, width, dtype)
+    old = w.flip(0).contiguous() * 1e-3
+    given = {"dw": old.clone(), "accumulate": True} if accumulate else {}
+    _, lse, dh, dw = check(b2g, h, w, t, g, **given)
+    first = dh.clone(), dw.clone()
+    for _ in range(40):
+        given = {"dw": old.clone(), "accumulate": True} if accumulate else {}
+        got = b2g.linear_cross_entropy_backward(h, w, t, lse, g, **given)
+        assert all(torch.equal(p, q) for p, q in zip(first, got))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("tokens,vocab,width", [(40, 3000, 136), (300, 5000, 200), (700, 9000, 520)])
 def test_one_gradient_alone(b2g, tokens, vocab, width, dtype):
