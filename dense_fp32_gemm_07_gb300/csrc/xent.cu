@@ -81,7 +81,7 @@ struct XentGemm {
   float* zt;                   // the target's logit
   const float* lse;
   const float* gloss;
-  float* scale;                // the largest weight: written by kDz, read by kProd
+  float* scale;                // what dz is divided by: written by kDz, read by kProd
   // kProd
   int to_part;                 // the output map is [slices][rows][..] FP32 sums
   int add;                     // to_part: add to what is there
@@ -681,9 +681,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tempty_even = even ? 0u : mapa_shared(tempty(0), 0);
     float scale = 1.f;
     if constexpr (MODE == kDz) {
-      scale = largest_weight(p0, wred, threadIdx.x - 128);
+      scale = divisor_of(largest_weight(p0, wred, threadIdx.x - 128));
       if (blockIdx.x == 0 && threadIdx.x == 128) *p0.scale = scale;
-      scale = scale > 0.f ? 1.f / scale : 0.f;
+      scale = 1.f / scale;
     } else if constexpr (MODE != kStats) {
       scale = *p0.scale;
     }

@@ -66,6 +66,10 @@ __device__ __forceinline__ float exp_f32(float x) {
   return y;
 }
 
+// What dz is divided by before it is rounded to BF16, for the largest of the weights: at
+// least FP32's smallest normal number, so that its reciprocal is finite.
+__device__ __forceinline__ float divisor_of(float largest) { return fmaxf(largest, 0x1p-126f); }
+
 // The loads into v are complete; tying v to the wait keeps its uses behind it.
 __device__ __forceinline__ void tie16(uint32_t (&v)[16]) {
   asm volatile(""

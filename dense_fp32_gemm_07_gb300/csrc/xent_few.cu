@@ -412,9 +412,9 @@ __global__ void __launch_bounds__(Cfg<F32>::kThreads, 1)
     if (MODE == kDz) {
       float m = 0.f;
       for (int j = lane; j < kFewTokens; j += 32) m = fmaxf(m, isfinite(weight[j]) ? fabsf(weight[j]) : 0.f);
-      m = warp_max(m);
+      m = divisor_of(warp_max(m));
       if (blockIdx.x == 0 && threadIdx.x == 128) *p.scale = m;
-      scale = m > 0.f ? 1.f / m : 0.f;
+      scale = 1.f / m;
     } else if (MODE == kDh) {
       scale = *p.scale;
     }

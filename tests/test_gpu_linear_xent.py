@@ -222,6 +222,23 @@ def test_weights_of_zero_and_nonfinite_lse(b2g):
     assert not ref[0][4].any() and all(torch.equal(p, q) for p, q in zip(ref, got))
 
 
+@pytest.mark.parametrize("tokens", [40, 300])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_subnormal_weights(b2g, tokens, dtype):
+    """Weights whose reciprocal is infinite, next to weights of exactly 0 and classes of
+    probability 0: the gradients are finite, and 0 in the rows of weight 0."""
+    h, w, t, g = make(tokens, 700, 32, dtype, ignored=0)
+    h[:, 0], w[:, 0] = 1.0, 0.0
+    w[600:605] = 0
+    w[600:605, 0] = torch.finfo(dtype).min
+    t[(t >= 600) & (t < 605)] = 0
+    g[:] = 2e-39
+    g[::3] = 0
+    _, _, dh, dw = check(b2g, h, w, t, g)
+    assert torch.isfinite(dh[:, 1:]).all() and torch.isfinite(dw).all()
+    assert not dh[::3].any() and dw[:, 1:].any()
+
+
 def test_no_tokens(b2g):
     h, w = torch.empty(0, 64, device="cuda"), torch.randn(50, 64, device="cuda")
     t, e = torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
