@@ -393,13 +393,14 @@ __device__ __forceinline__ void epi_dz(const XentGemm& p, float (&z)[128], int r
   }
 }
 
-// The largest finite |weight|, by the block's epilogue threads (`tid` of
-// 32 * kEpiWarps) through `red`.
+// The largest finite |weight| of the rows that have a gradient (the others' weights may be
+// anything), by the block's epilogue threads (`tid` of 32 * kEpiWarps) through `red`.
 __device__ __forceinline__ float largest_weight(const XentGemm& p, float* red, int tid) {
   float m = 0.f;
   for (int i = tid; i < p.rows; i += 32 * kEpiWarps) {
     const float g = fabsf(p.gloss[i]);
-    if (isfinite(g)) m = fmaxf(m, g);
+    const long long t = target_at(p, i);
+    if (t != p.ignore && t >= 0 && t < p.vocab && isfinite(g)) m = fmaxf(m, g);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));

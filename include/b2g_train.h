@@ -126,7 +126,8 @@ int b2g_linear_xent(int dtype, int tokens, int vocab, int width, const void* h, 
 /*
  * Gradients of sum_i grad_loss_i * loss_i.  With
  *     dz_ij = grad_loss_i * (exp(z_ij - lse_i) - [j == target_i])
- * (zero in rows whose target is ignore_index or out of range, whatever lse_i is),
+ * (zero in rows whose target is ignore_index or out of range, whatever lse_i and
+ * grad_loss_i are),
  *     dh = dz * w,   dw = dz^T * h  (plus dw's previous value when accumulate != 0).
  * z is computed again, a piece of the vocabulary at a time; dz exists for one
  * piece at a time, rounded to BF16 (BF16 operands) or held in three BF16 pieces

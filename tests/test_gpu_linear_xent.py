@@ -239,6 +239,21 @@ def test_subnormal_weights(b2g, tokens, dtype):
     assert not dh[::3].any() and dw[:, 1:].any()
 
 
+@pytest.mark.parametrize("tokens", [40, 130])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_weights_of_rows_without_a_gradient(b2g, tokens, dtype):
+    """The weights of ignored and out-of-range rows are not looked at: any values there
+    leave the other rows' gradients the bits they have with 0."""
+    h, w, t, g = make(tokens, 700, 96, dtype, ignored=0)
+    t[5], t[11], t[17] = -100, 700, -3
+    g[[5, 11, 17]] = 0
+    _, lse, dh, dw = check(b2g, h, w, t, g)
+    for value in (1e38, float("inf"), float("nan"), 1e-30):
+        g[[5, 11, 17]] = value
+        got = b2g.linear_cross_entropy_backward(h, w, t, lse, g)
+        assert torch.equal(got[0], dh) and torch.equal(got[1], dw), value
+
+
 def test_no_tokens(b2g):
     h, w = torch.empty(0, 64, device="cuda"), torch.randn(50, 64, device="cuda")
     t, e = torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
