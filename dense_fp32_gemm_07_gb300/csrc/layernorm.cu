@@ -154,6 +154,33 @@ struct RingPos {
   }
 };
 
+// A ring's waits, and where its copies stop in a test of them.
+struct RingWait {
+  unsigned int* status;
+  unsigned long long limit_ns;
+  int debug_stop;  // >= 0: rows a group starts to copy
+};
+
+// After a wait for `row` has run out: the group's copies still on their way, which are those
+// of the next `stages` rows at most, land before its ring is used for anything else or left
+// (one wait that runs out again ends this).
+__device__ __noinline__ void drain_ring(uint32_t bar0, int s, uint32_t ph, int stages, long long row,
+                                        long long step, long long rows, const RingWait& w) {
+  for (int i = 0; i < stages && row < rows; ++i, row += step) {
+    if (!mbar_wait(bar0 + 8u * s, ph, w.limit_ns, w.status, kStatusTimeoutDrain)) return;
+    if (++s == stages) s = 0, ph ^= 1u;
+  }
+}
+
+// Wait for `row`'s copy; `first`: the thread that started it.  False when the wait ran out.
+__device__ __forceinline__ bool wait_row(uint32_t bar0, const RingPos& at, int stages, long long row,
+                                         long long step, long long rows, bool first,
+                                         const RingWait& w) {
+  if (mbar_wait(bar0 + 8u * at.s, at.ph, w.limit_ns, w.status, kStatusTimeoutFull)) return true;
+  if (first) drain_ring(bar0, at.s, at.ph, stages, row, step, rows, w);
+  return false;
+}
+
 // Two sums over a group's nt threads at once; `ex` is one of two exchange buffers
 // used by turns.
 __device__ __forceinline__ F2 group_sum2(F2 v, F2 (&ex)[16], int group, int nt) {
@@ -197,7 +224,7 @@ __device__ __forceinline__ float group_sum(float v, float (&ex)[16], int group, 
 template <typename T, int VEC, bool FULL>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     ln_fwd_ring_kernel(const __grid_constant__ LnFwd p, const __grid_constant__ Ring g,
-                       unsigned int* status, unsigned long long wait_limit_ns) {
+                       const __grid_constant__ RingWait wait) {
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ __align__(8) unsigned long long bars[kFwdThreads / 32 * kRingStages];
   __shared__ float red[2][16];
@@ -220,6 +247,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const long long step = (long long)gridDim.x * g.groups;
   const long long row0 = (long long)group * gridDim.x + blockIdx.x;
   auto issue = [&](long long row, int s) {
+    if (wait.debug_stop >= 0 && (row - row0) / step >= wait.debug_stop) return;
     mbar_arrive_expect_tx(bar0 + 8u * s, bytes);
     bulk_load(smem_addr(mine + (size_t)s * bytes), static_cast<const T*>(p.x) + row * p.ldx, bytes,
               bar0 + 8u * s);
@@ -236,7 +264,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   RingPos at;
   bool alive = true;  // false once a wait has run out: no more waits, no more copies
   for (long long row = row0; row < p.rows; row += step) {
-    if (alive) alive = mbar_wait(bar0 + 8u * at.s, at.ph, wait_limit_ns, status, kStatusTimeoutFull);
+    if (alive) alive = wait_row(bar0, at, g.stages, row, step, p.rows, t == 0, wait);
     const T* xs = reinterpret_cast<const T*>(mine + (size_t)at.s * bytes);
     F2 x[NCH][H];
     F2 s0 = f2(0.f, 0.f), s1 = f2(0.f, 0.f);
@@ -353,7 +381,7 @@ struct LnBwd {
 template <typename T, int VEC, bool FULL>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     ln_bwd_ring_kernel(const __grid_constant__ LnBwd p, const __grid_constant__ Ring g,
-                       unsigned int* status, unsigned long long wait_limit_ns) {
+                       const __grid_constant__ RingWait wait) {
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ __align__(8) unsigned long long bars[kBwdThreads / 32 * kRingStages];
   __shared__ F2 red[2][16];
@@ -374,6 +402,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const long long step = (long long)gridDim.x * g.groups;
   const long long row0 = (long long)group * gridDim.x + blockIdx.x;
   auto issue = [&](long long row, int s) {
+    if (wait.debug_stop >= 0 && (row - row0) / step >= wait.debug_stop) return;
     const uint32_t bar = bar0 + 8u * s, dst = smem_addr(mine + (size_t)s * 2 * bytes);
     mbar_arrive_expect_tx(bar, 2 * bytes);
     bulk_load(dst, static_cast<const T*>(p.x) + row * p.ldx, bytes, bar);
@@ -403,7 +432,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   for (long long row = row0; row < p.rows; row += step) {
     const F2 m2 = f2(-mean, -mean), r2 = f2(rstd, rstd);
     if (row + step < p.rows) mean = p.mean[row + step], rstd = p.rstd[row + step];
-    if (alive) alive = mbar_wait(bar0 + 8u * at.s, at.ph, wait_limit_ns, status, kStatusTimeoutFull);
+    if (alive) alive = wait_row(bar0, at, g.stages, row, step, p.rows, t == 0, wait);
     const T* xs = reinterpret_cast<const T*>(mine + (size_t)at.s * 2 * bytes);
     const T* ds = reinterpret_cast<const T*>(mine + (size_t)at.s * 2 * bytes + bytes);
     F2 x[NCH][H], gr[NCH][H];  // x - mean and g = dy * weight
@@ -450,7 +479,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     at.next(g.stages);
   }
   if (!p.part) return;
-  __syncthreads();  // every ring is drained: its memory now takes the groups' sums
+  __syncthreads();  // no ring has a copy on its way: its memory now takes the groups' sums
   float* sums = reinterpret_cast<float*>(ring);
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
@@ -529,7 +558,7 @@ inline __host__ __device__ size_t any_slot(int cols, size_t es) {
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     ln_bwd_any_kernel(const __grid_constant__ LnBwd p, const __grid_constant__ Ring g,
-                      unsigned int* status, unsigned long long wait_limit_ns) {
+                      const __grid_constant__ RingWait wait) {
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ __align__(8) unsigned long long bars[kBwdThreads / 32 * kRingStages];
   __shared__ F2 red[2][16];
@@ -556,6 +585,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     return AnyRow<T>(static_cast<const T*>(p.dy) + row * p.lddy, p.cols);
   };
   auto issue = [&](long long row, int s) {
+    if (wait.debug_stop >= 0 && (row - row0) / step >= wait.debug_stop) return;
     const uint32_t bar = bar0 + 8u * s, dst = smem_addr(mine + (size_t)s * 2 * slot);
     const AnyRow<T> x = x_row(row), d = d_row(row);
     mbar_arrive_expect_tx(bar, x.bytes() + d.bytes());
@@ -581,7 +611,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   for (long long row = row0; row < p.rows; row += step) {
     const float m = mean, r = rstd;
     if (row + step < p.rows) mean = p.mean[row + step], rstd = p.rstd[row + step];
-    if (alive) alive = mbar_wait(bar0 + 8u * at.s, at.ph, wait_limit_ns, status, kStatusTimeoutFull);
+    if (alive) alive = wait_row(bar0, at, g.stages, row, step, p.rows, t == 0, wait);
     const unsigned char* here = mine + (size_t)at.s * 2 * slot;
     const AnyRow<T> xr = x_row(row), dr = d_row(row);
     const typename AnyRow<T>::Ends xe = xr.ends(t, g.nt, p.cols), de = dr.ends(t, g.nt, p.cols);
@@ -621,7 +651,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     at.next(g.stages);
   }
   if (!p.part) return;
-  __syncthreads();  // every ring is drained: its memory now takes the groups' sums
+  __syncthreads();  // no ring has a copy on its way: its memory now takes the groups' sums
   float* sums = reinterpret_cast<float*>(ring) + (size_t)2 * group * p.cols;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -774,7 +804,7 @@ cudaError_t fwd_ring(const LnFwd& p, const Ring& r, const TrainDevice& d, cudaSt
   return launch_train(ln_fwd_ring_kernel<T, VEC, FULL>,
                       dim3((unsigned)(blocks < d.sms ? blocks : d.sms)), dim3(kFwdThreads),
                       ((size_t)r.groups * r.stages + 2) * p.cols * sizeof(T), st, p, r,
-                      d.status, d.wait_limit_ns);
+                      RingWait{d.status, d.wait_limit_ns, d.debug_stop});
 }
 
 template <typename T, int VEC>
@@ -825,7 +855,7 @@ cudaError_t bwd_ring(const LnBwd& p, const Ring& r, int parts, const TrainDevice
   const size_t rings = (size_t)r.groups * r.stages * 2 * p.cols * sizeof(T);
   const size_t sums = (size_t)r.groups * 2 * p.cols * sizeof(float);
   return launch_train(ln_bwd_ring_kernel<T, VEC, FULL>, dim3(parts), dim3(kBwdThreads),
-                      rings > sums ? rings : sums, st, p, r, d.status, d.wait_limit_ns);
+                      rings > sums ? rings : sums, st, p, r, RingWait{d.status, d.wait_limit_ns, d.debug_stop});
 }
 
 template <typename T>
@@ -839,7 +869,7 @@ cudaError_t bwd_any(const LnBwd& p, const Ring& r, int parts, const TrainDevice&
       (size_t)r.groups * r.stages * 2 * any_slot(p.cols, sizeof(T)) + p.cols * sizeof(T);
   const size_t sums = (size_t)r.groups * 2 * p.cols * sizeof(float);
   return launch_train(ln_bwd_any_kernel<T>, dim3(parts), dim3(kBwdThreads),
-                      rings > sums ? rings : sums, st, p, r, d.status, d.wait_limit_ns);
+                      rings > sums ? rings : sums, st, p, r, RingWait{d.status, d.wait_limit_ns, d.debug_stop});
 }
 
 template <typename T, int VEC>

@@ -214,3 +214,36 @@ def test_other_stream(b2g):
     dx, _, _ = b2g.layer_norm_backward(x, x, None, mean, rstd, stream=s)
     s.synchronize()
     assert torch.equal(y, ref) and bool(torch.isfinite(dx).all())
+
+
+@pytest.mark.parametrize("cols", [2048, 2040, 2047])
+def test_bounded_waits_of_the_rings(b2g, cols):
+    """With each group's copies stopped after one row the waits run out, the calls return
+    and the status word says so; the next calls work again."""
+    x = torch.randn(8192, cols, device="cuda").bfloat16()
+    w = torch.randn(cols, device="cuda").bfloat16()
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def forward():
+        return b2g.layer_norm(x, w, w)
+
+    y, mean, rstd = forward()
+
+    def backward():
+        return b2g.layer_norm_backward(y, x, w, mean, rstd)
+
+    for call in (forward, backward) if cols % 8 == 0 else (backward,):  # odd rows: one ring
+        first = call()
+        torch.cuda.synchronize()
+        try:
+            b2g.b2g_set_wait_limit_ns(2_000_000)
+            b2g.b2g_debug_stop_after(1)
+            call()
+            rc, flags = b2g.b2g_status(stream)
+            assert rc == b2g.B2G_ERR_TIMEOUT and flags & 1 and flags & 4
+        finally:
+            b2g.b2g_debug_stop_after(-1)
+            b2g.b2g_set_wait_limit_ns(2_000_000_000)
+        again = call()
+        assert all(torch.equal(p, q) for p, q in zip(first, again))
+        assert b2g.b2g_status(stream) == (0, 0)
