@@ -32,6 +32,9 @@ __device__ __forceinline__ long long id_at(const void* ids, int bytes, long long
                     : (long long)static_cast<const int*>(ids)[i];
 }
 
+// Blocks of columns stand in the grid's y, and past its 65535 in z as well.
+__device__ __forceinline__ int column_block() { return blockIdx.z * gridDim.y + blockIdx.y; }
+
 // ------------------------------------------------------------------- forward
 
 struct EmbFwd {
@@ -48,7 +51,7 @@ struct EmbFwd {
 };
 
 // blockDim.x threads per token, blockDim.y tokens per block; U chunks a thread
-// (its loads are all in flight before the first store); blockIdx.y covers wider
+// (its loads are all in flight before the first store); column_block() covers wider
 // rows.
 template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(256) emb_fwd_kernel(const __grid_constant__ EmbFwd p) {
@@ -57,7 +60,7 @@ __global__ void __launch_bounds__(256) emb_fwd_kernel(const __grid_constant__ Em
   const long long i = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   if (i >= p.tokens) return;
   const long long id = id_at(p.ids, p.id_bytes, i);
-  const int c0 = blockIdx.y * blockDim.x * U + threadIdx.x;
+  const int c0 = column_block() * blockDim.x * U + threadIdx.x;
   T* o = static_cast<T*>(p.out) + i * p.ldo;
   const bool ok = id >= 0 && id < p.vocab;
   if (!ok && c0 == 0) atomicOr(p.status, kStatusIndex);
@@ -418,7 +421,7 @@ __device__ __forceinline__ void put_row(const EmbSum& p, unsigned row, int c, co
 constexpr int kMaxWindow = 128;
 
 // blockDim.x threads share a window's columns (one chunk each), blockDim.y
-// windows per block; blockIdx.y covers wider rows.  The window's ids and places are
+// windows per block; column_block() covers wider rows.  The window's ids and places are
 // fetched into shared memory first, so that only the rows themselves are waited
 // for, U at a time.  Runs that begin before the window or continue after it go
 // to the window's partial rows.
@@ -436,7 +439,7 @@ __global__ void __launch_bounds__(256) emb_window_kernel(const __grid_constant__
     places[i] = in ? p.pos[first_token + i] : 0;
   }
   const int w = blockIdx.x * blockDim.y + threadIdx.y;
-  const int c = blockIdx.y * blockDim.x + threadIdx.x;
+  const int c = column_block() * blockDim.x + threadIdx.x;
   const long long begin = (long long)w * p.window;
   const bool mine = begin < p.tokens && c < p.chunks;
   const int b = (int)begin, e = b + p.window < p.tokens ? b + p.window : p.tokens;
@@ -513,7 +516,7 @@ __global__ void __launch_bounds__(256) emb_join_kernel(const __grid_constant__ E
   pdl_launch_dependents();
   pdl_wait();
   const int w = blockIdx.x * blockDim.y + threadIdx.y;
-  const int c = blockIdx.y * blockDim.x + threadIdx.x;
+  const int c = column_block() * blockDim.x + threadIdx.x;
   const long long begin = (long long)w * p.window, end = begin + p.window;
   if (end >= p.tokens || c >= p.width) return;
   const unsigned run = p.key[end - 1], next = p.key[end];
@@ -566,6 +569,14 @@ int pow2_at_least(int n, int lo, int hi) {
   return t;
 }
 
+// `rows` blocks times `columns` blocks.  z is as small as possible and y even over it, so
+// that at most z blocks have no column (fewer than 2^16 threads: their column numbers stay
+// below 2^31).
+dim3 grid_of(long long rows, long long columns) {
+  const long long z = ceil_div(columns, 65535);
+  return dim3((unsigned)rows, (unsigned)ceil_div(columns, z), (unsigned)z);
+}
+
 template <typename T, int VEC>
 cudaError_t fwd_launch(EmbFwd p, int width, int sms, cudaStream_t st) {
   p.chunks = width / VEC;
@@ -581,7 +592,7 @@ cudaError_t fwd_launch(EmbFwd p, int width, int sms, cudaStream_t st) {
   }
   const int u = many ? 4 : 1;
   const int tx = pow2_at_least((int)ceil_div(p.chunks, u), 8, 256), ty = 256 / tx;
-  const dim3 grid((unsigned)ceil_div(p.tokens, ty), (unsigned)ceil_div(p.chunks, tx * u));
+  const dim3 grid = grid_of(ceil_div(p.tokens, ty), ceil_div(p.chunks, tx * u));
   if (many) return launch_train(emb_fwd_kernel<T, VEC, 4>, grid, dim3(tx, ty), 0, st, p);
   return launch_train(emb_fwd_kernel<T, VEC, 1>, grid, dim3(tx, ty), 0, st, p);
 }
@@ -652,7 +663,7 @@ cudaError_t sum_launch(EmbSum p, cudaStream_t st) {
   p.chunks = p.width / VEC;
   const int tx = pow2_at_least(p.chunks, 8, 256), ty = 256 / tx;
   const long long windows = ceil_div(p.tokens, p.window);
-  const dim3 grid((unsigned)ceil_div(windows, ty), (unsigned)ceil_div(p.chunks, tx));
+  const dim3 grid = grid_of(ceil_div(windows, ty), ceil_div(p.chunks, tx));
   // Eight rows in flight a thread in short windows, where few threads run (4095 x 512
   // FP32: 9 us with four, 7 with eight); four in long ones, where eight cost the
   // occupancy that hides their latency (32768 x 4096 BF16: 66 us with four, 86 with
@@ -666,8 +677,7 @@ cudaError_t sum_launch(EmbSum p, cudaStream_t st) {
   if (e == cudaSuccess && windows > 1) {
     const int jx = pow2_at_least(p.width, 8, 256), jy = 256 / jx;
     e = launch_train(emb_join_kernel<T>,
-                     dim3((unsigned)ceil_div(windows, jy), (unsigned)ceil_div(p.width, jx)),
-                     dim3(jx, jy), 0, st, p);
+                     grid_of(ceil_div(windows, jy), ceil_div(p.width, jx)), dim3(jx, jy), 0, st, p);
   }
   return e;
 }

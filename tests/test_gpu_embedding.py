@@ -223,3 +223,30 @@ def test_offsets_past_32_bits(b2g):
     b2g.embedding_backward(ids, out, vocab, out=table, accumulate=True)
     want = before.double() * 2
     close(table[ids], want, U[BF16] * want.abs(), "dtable")
+
+
+@pytest.mark.parametrize("width", [65536 * 256 + 8, 65535 * 256 + 1])
+def test_gradient_of_very_wide_rows(b2g, width):
+    """More than 65535 blocks of columns, on and off the 16-byte boundaries, and a run that
+    two windows share.  Whole numbers: every FP32 sum is exact."""
+    tokens = 130
+    dout = torch.randint(-4, 5, (tokens, width), device="cuda", dtype=torch.int8).bfloat16()
+    ids = torch.full((tokens,), 2, device="cuda")
+    ids[:3] = 0
+    got = b2g.embedding_backward(ids, dout, 4)
+    assert status(b2g) == (0, 0)
+    for c in range(0, width, 1 << 21):
+        part = dout[:, c:c + (1 << 21)]
+        assert torch.equal(got[0, c:c + (1 << 21)], part[:3].float().sum(0).bfloat16())
+        assert torch.equal(got[2, c:c + (1 << 21)], part[3:].float().sum(0).bfloat16())
+    assert not got[1].any() and not got[3].any()
+
+
+def test_lookup_of_very_wide_rows(b2g):
+    width = 65535 * 4096 + 4
+    table = torch.empty(2, width, device="cuda")
+    table[0], table[1] = 1.0, 2.0
+    table[:, -5:] = torch.arange(10, device="cuda").view(2, 5).float()
+    out = b2g.embedding(torch.tensor([1, 0], device="cuda"), table, scale=0.5)
+    assert status(b2g) == (0, 0)
+    assert torch.equal(out, table.flip(0) * 0.5)
