@@ -15,6 +15,8 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <algorithm>
+#include <cstdint>
 #include <vector>
 
 #include "../../include/b2g_train.h"
@@ -276,6 +278,38 @@ bool listed(PyObject* list, Kind* k, bool first, std::vector<void*>* at, std::ve
   return count > 0;
 }
 
+// Whether no result shares memory with another one, nor with an input other than the tensor
+// it replaces.
+bool apart(const std::vector<void*>& in, const std::vector<void*>& out,
+           const std::vector<long long>& n, int64_t bytes) {
+  struct Span {
+    uintptr_t from, to;
+    size_t i;
+    bool operator<(const Span& o) const { return from < o.from; }
+  };
+  auto span = [&](const std::vector<void*>& at, size_t i) {
+    const uintptr_t from = reinterpret_cast<uintptr_t>(at[i]);
+    return Span{from, from + (uintptr_t)(n[i] * bytes), i};
+  };
+  std::vector<Span> outs;
+  outs.reserve(out.size());
+  for (size_t i = 0; i < out.size(); ++i)
+    if (n[i]) outs.push_back(span(out, i));
+  if (!std::is_sorted(outs.begin(), outs.end())) std::sort(outs.begin(), outs.end());
+  for (size_t k = 1; k < outs.size(); ++k)
+    if (outs[k].from < outs[k - 1].to) return false;
+  if (&in == &out) return true;
+  for (size_t i = 0; i < in.size(); ++i) {
+    if (!n[i]) continue;
+    const Span x = span(in, i);
+    // the results that begin before x's end, from the last one back to x's beginning
+    for (auto o = std::lower_bound(outs.begin(), outs.end(), Span{x.to, 0, 0});
+         o != outs.begin() && (o - 1)->to > x.from; --o)
+      if ((o - 1)->i != i || (o - 1)->from != x.from) return false;
+  }
+  return true;
+}
+
 // grad_norm(grads), or clip_grad_norm(grads, outs, max_norm)
 PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -286,10 +320,10 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if ((n != 1 && n != 3) || !listed(a[0], &k, true, &in, &len)) Py_RETURN_NONE;
   if (n == 3) {
     if (!number(a[2], &max_norm)) Py_RETURN_NONE;
-    if (a[1] == a[0])
-      out = in;
-    else if (!listed(a[1], &k, false, &out, &out_len) || out_len != len)
-      Py_RETURN_NONE;
+    const bool in_place = a[1] == a[0];
+    if (!in_place && (!listed(a[1], &k, false, &out, &out_len) || out_len != len)) Py_RETURN_NONE;
+    if (!apart(in, in_place ? in : out, len, k.code == B2G_F32 ? 4 : 2)) Py_RETURN_NONE;
+    if (in_place) out = in;
   }
   const int count = (int)in.size();
   size_t bytes = 0;

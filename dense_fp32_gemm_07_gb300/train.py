@@ -17,6 +17,7 @@ the current stream) go straight through the native binding
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import functools
 from typing import Optional
@@ -482,7 +483,9 @@ def grad_norm(grads, stream=None):
 def clip_grad_norm(grads, max_norm: float, out=None, stream=None):
     """Multiply every tensor of the list by min(1, max_norm / (norm + 1e-6)), with
     the 2-norm of all of them together, and return that norm (a 0-d float32
-    tensor).  In place, or into the tensors of the list `out`."""
+    tensor).  In place, or into the tensors of the list `out`.  No result may share
+    memory with another one (so no tensor may be clipped in place twice), nor with a
+    tensor of `grads` other than the one it replaces."""
     if not max_norm >= 0:
         raise ValueError("max_norm must not be negative")
     grads = list(grads)
@@ -502,6 +505,8 @@ def _norm(grads, outs, max_norm, stream):
         _, _, optrs, olens = _tensor_list(outs, "out", dt, dev)
         if olens != lens:
             raise ValueError("out must hold tensors of the lengths of grads")
+    if outs is not None:
+        _all_apart(ptrs, optrs, lens, grads[0].element_size())
     on = _on(stream, dev)
     device = grads[0].device
     norm = on.empty((), _torch.float32, device)
@@ -520,6 +525,25 @@ def _norm(grads, outs, max_norm, stream):
         raise B2GError(rc)
     on.uses(*grads, *(outs or ()))
     return norm
+
+
+def _all_apart(ptrs, optrs, lens, bytes_each):
+    """Raise when a result of a list shares memory with another one, or with an input
+    other than the tensor it replaces."""
+    def spans(at):
+        return [(p, p + n * bytes_each, i) for i, (p, n) in enumerate(zip(at, lens)) if n]
+
+    outs = sorted(spans(optrs))
+    for (_, end, i), (start, _, j) in zip(outs, outs[1:]):
+        if start < end:
+            raise ValueError(f"the results of tensors {min(i, j)} and {max(i, j)} overlap")
+    starts = [o[0] for o in outs]
+    for start, end, i in spans(ptrs) if optrs is not ptrs else ():
+        k = bisect.bisect_left(starts, end) - 1
+        while k >= 0 and outs[k][1] > start:
+            if outs[k][2] != i or outs[k][0] != start:
+                raise ValueError(f"the result of tensor {outs[k][2]} must not overlap tensor {i}")
+            k -= 1
 
 
 @functools.lru_cache(maxsize=None)

@@ -123,3 +123,34 @@ def test_captured_in_a_graph(b2g):
     g.replay()
     ref = b2g.clip_grad_norm(grads, 1.0, out=[torch.empty_like(t) for t in grads])
     assert torch.equal(norm, ref)
+
+
+def test_overlapping_results_are_refused(b2g):
+    """A result that shares memory with another one, or with a tensor other than its own,
+    on the current stream and on another one; what does not overlap is served."""
+    flat = torch.arange(1.0, 101.0, device="cuda")
+    a, b, c = flat[:40], flat[40:60], flat[60:]
+    other = torch.zeros(100, device="cuda")
+    empty = torch.empty(0, device="cuda")
+    before = flat.clone()
+    bad = [
+        ([a, b, a], None),                            # the same tensor twice, in place
+        ([flat, b], None),                            # a tensor and a part of it
+        ([a, b], [other[:40], other[30:50]]),         # two results
+        ([a, b], [flat[1:41], other[:20]]),           # a result one element past its tensor
+        ([b, flat[80:]], [flat[80:], other[:20]]),    # another tensor's memory
+        ([a, a], [a, other[:40]]),                    # in place, and still read as the other
+        ([b, a, empty], [other[:20], flat[20:60], empty]),
+    ]
+    for stream in (None, torch.cuda.Stream()):
+        for grads, out in bad:
+            with pytest.raises(ValueError, match="overlap"):
+                b2g.clip_grad_norm(grads, 1.0, out=out, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(flat, before) and not other.any()
+    for grads, out in (([c, a, empty, b], None), ([a, b], [a, other[:20]]),
+                       ([a, a], [other[:40], other[50:90]]), ([b, a], [other[:20], a])):
+        check(b2g, [g.clone() for g in grads] if out is None else grads, 1e9, out)
+        b2g.clip_grad_norm(grads, 1e9, out=out)
+    assert torch.equal(flat, before)
+    assert float(b2g.grad_norm([a, a])) > 0           # the norm only reads
