@@ -463,8 +463,8 @@ def _tensor_list(tensors, name, dt=None, dev=None):
         if dev < 0:
             raise TypeError(f"{name} must be on a CUDA device")
     for t in tensors:
-        if t.dtype is not dt:
-            raise TypeError(f"every tensor of {name} must have the type {dt}")
+        if not isinstance(t, _torch.Tensor) or t.dtype is not dt:
+            raise TypeError(f"{name} must hold {dt} tensors only")
         if not t.is_contiguous() or t.get_device() != dev:
             raise ValueError(f"every tensor of {name} must be contiguous and on cuda:{dev}")
     return dt, dev, [t.data_ptr() for t in tensors], [t.numel() for t in tensors]

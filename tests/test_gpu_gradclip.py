@@ -154,3 +154,16 @@ def test_overlapping_results_are_refused(b2g):
         b2g.clip_grad_norm(grads, 1e9, out=out)
     assert torch.equal(flat, before)
     assert float(b2g.grad_norm([a, a])) > 0           # the norm only reads
+
+
+def test_lists_of_other_things_are_refused(b2g):
+    """A parameter without a gradient leaves a None in the list."""
+    x = torch.ones(5, device="cuda")
+    for call in (lambda: b2g.grad_norm([x, None]), lambda: b2g.clip_grad_norm([None, x], 1.0),
+                 lambda: b2g.clip_grad_norm([x, x.bfloat16()], 1.0),
+                 lambda: b2g.clip_grad_norm([x], 1.0, out=[None]),
+                 lambda: b2g.clip_grad_norm([x], 1.0, out=[x.tolist()])):
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(ValueError):
+        b2g.clip_grad_norm([x, x.cpu()], 1.0)
