@@ -170,8 +170,20 @@ def _apart(out, *inputs):
     a1 = a0 + _span(out)
     for name, t in inputs:
         b0 = t.data_ptr()
-        if a0 < b0 + _span(t) and b0 < a1:
+        if a0 < b0 + _span(t) and b0 < a1 and not _side_by_side(out, t):
             raise ValueError(f"the result must not overlap {name}")
+
+
+def _side_by_side(a, b):
+    """Whether two matrices are different columns of the same rows (one row stride, as
+    in the halves of a wider matrix): their spans overlap, their elements do not."""
+    if a.dim() != 2 or b.dim() != 2 or a.shape[0] < 2 or b.shape[0] < 2:
+        return False
+    row = a.stride(0) * a.element_size()
+    if row != b.stride(0) * b.element_size():
+        return False
+    at = (b.data_ptr() - a.data_ptr()) % row  # where b's columns begin, from a's first one
+    return at >= a.shape[1] * a.element_size() and at + b.shape[1] * b.element_size() <= row
 
 
 def _span(t):

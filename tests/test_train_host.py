@@ -210,6 +210,56 @@ def test_tensor_calls_refuse(b2g):
         b2g.grad_norm([])
 
 
+def test_results_beside_their_inputs(b2g):
+    """Columns of one buffer that share no element may be result and input; a shared
+    column, row or element may not."""
+    apart = b2g.train._apart
+    flat = torch.zeros(6 * 24 + 40)
+    buf = flat[:144].view(6, 24)
+    left, right, middle = buf[:, :8], buf[:, 8:20], buf[:, 7:9]
+    for out, x in ((left, right), (right, left), (buf[:, 20:], left), (left[2:], right[:5]),
+                   (left, right[1:]), (buf[:3], buf[3:]), (left, flat[140:170])):
+        apart(out, ("x", x))
+    shifted = flat[20:20 + 120].view(5, 24)[:, :8]   # columns 20 .. 23, then 0 .. 3 of the next row
+    for out, x in ((left, left), (left, middle), (right, middle), (left, shifted), (shifted, left),
+                   (buf, left), (left, flat[3:30]), (left, flat[:144].view(18, 8)[3:5]),
+                   (left[:1], left[:1])):
+        with pytest.raises(ValueError):
+            apart(out, ("x", x))
+    apart(buf[:, 12:20], ("x", shifted))
+    half = torch.zeros(4, 32, dtype=torch.bfloat16)
+    apart(half[:, 16:], ("x", half[:, :16]))
+    with pytest.raises(ValueError):
+        apart(half[:, 15:], ("x", half[:, :16]))
+
+
+@pytest.mark.gpu
+def test_result_beside_its_input_on_gpu(b2g):
+    """Each call with a given result, whose rows lie between its input's rows."""
+    torch.manual_seed(0)
+    for dt in (torch.float32, torch.bfloat16):
+        buf = torch.randn(300, 160, device="cuda").to(dt)
+        x, out = buf[:, :80], buf[:, 80:]
+        w = torch.randn(80, device="cuda").to(dt)
+        y, mean, rstd = b2g.layer_norm(x.contiguous(), w, w)
+        assert torch.equal(b2g.layer_norm(x, w, w, out=out)[0], y) and torch.equal(out, y)
+        dx = b2g.layer_norm_backward(y, x.contiguous(), w, mean, rstd)[0]
+        got = b2g.layer_norm_backward(y, x, w, mean, rstd, out=out)[0]
+        assert torch.equal(got, dx)
+        ids = torch.arange(300, device="cuda").flip(0)
+        want = b2g.embedding(ids, x.contiguous())
+        assert torch.equal(b2g.embedding(ids, x, out=out), want)
+        want = b2g.embedding_backward(ids, x.contiguous(), 300)
+        assert torch.equal(b2g.embedding_backward(ids, x, 300, out=out), want)
+        h, t = torch.randn(100, 80, device="cuda").to(dt), ids[:100].contiguous()
+        _, lse = b2g.linear_cross_entropy(h, x, t)
+        g = torch.full((100,), 0.01, device="cuda")
+        keep = x.clone()
+        want = b2g.linear_cross_entropy_backward(h, keep, t, lse, g)
+        got = b2g.linear_cross_entropy_backward(h, x, t, lse, g, dw=out)
+        assert all(torch.equal(p, q) for p, q in zip(got, want)) and torch.equal(x, keep)
+
+
 @pytest.mark.gpu
 def test_tensor_calls_refuse_on_gpu(b2g):
     x = torch.zeros(6, 8, device="cuda")
