@@ -169,6 +169,8 @@ def _apart(out, *inputs):
     a0 = out.data_ptr()
     a1 = a0 + _span(out)
     for name, t in inputs:
+        if t is None:
+            continue
         b0 = t.data_ptr()
         if a0 < b0 + _span(t) and b0 < a1 and not _side_by_side(out, t):
             raise ValueError(f"the result must not overlap {name}")
@@ -271,6 +273,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
         ldy = _result(out, "out", (r, c), dt, dev)
         if out.data_ptr() != x.data_ptr() or ldx != ldy:
             _apart(out, ("x", x))
+        _apart(out, ("weight", weight), ("bias", bias))
     mean = on.empty((r,), _torch.float32, device)
     rstd = on.empty((r,), _torch.float32, device)
     rc = _lib.b2g_layernorm(_CODES[dt], r, c, x.data_ptr(), ldx, pw, pb, eps, out.data_ptr(), ldy,
@@ -303,7 +306,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, bias: bool = True, out=None, 
         out, lddx = on.empty((r, c), dt, device), c or 1
     else:
         lddx = _result(out, "out", (r, c), dt, dev)
-        _apart(out, ("x", x))
+        _apart(out, ("x", x), ("weight", weight), ("mean", mean), ("rstd", rstd))
         if out.data_ptr() != dy.data_ptr() or lddx != lddy:
             _apart(out, ("dy", dy))
     dw = None if weight is None else on.empty((c,), dt, device)
@@ -444,7 +447,7 @@ def linear_cross_entropy_backward(h, w, target, lse, grad_loss, ignore_index: in
         dw, lddw = on.empty((v, d), dt, device), d or 1
     else:
         lddw = _result(dw, "dw", (v, d), dt, dev)
-        _apart(dw, ("h", h), ("w", w))
+        _apart(dw, ("h", h), ("w", w), ("target", target), ("lse", lse), ("grad_loss", grad_loss))
     dh = on.empty((n, d), dt, device)
     code, ph, pw = _CODES[dt], h.data_ptr(), w.data_ptr()
     nb = _size(_lib.b2g_linear_xent_workspace_size, code, n, v, d, ph, ldh, pw, ldw, 1)

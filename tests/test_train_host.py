@@ -300,3 +300,27 @@ def test_tensor_calls_refuse_on_gpu(b2g):
     ws = torch.empty(n.value + 16, dtype=torch.uint8, device="cuda")
     assert lib.b2g_layernorm_backward(*args, ws.data_ptr(), n.value - 1, 0) == b2g.B2G_ERR_WORKSPACE
     assert lib.b2g_layernorm_backward(*args, ws.data_ptr() + 4, n.value, 0) == b2g.B2G_ERR_WORKSPACE
+
+
+@pytest.mark.gpu
+def test_results_over_smaller_inputs_are_refused(b2g):
+    """A result must not overlap a call's vectors either: other rows still read them."""
+    x = torch.ones(6, 8, device="cuda")
+    buf = torch.ones(200, device="cuda")
+    out, part = buf[:48].view(6, 8), buf[40:48]
+    six, n = buf[44:50], x[:, 0].contiguous()
+    ids = torch.zeros(6, dtype=torch.int64, device="cuda")
+    bad = [
+        lambda: b2g.layer_norm(x, part, out=out), lambda: b2g.layer_norm(x, None, part, out=out),
+        lambda: b2g.layer_norm_backward(x, x, part, n, n, out=out),
+        lambda: b2g.layer_norm_backward(x, x, None, six, n, out=out),
+        lambda: b2g.layer_norm_backward(x, x, None, n, six, out=out),
+        lambda: b2g.linear_cross_entropy_backward(x, x, ids, six, n, dw=out),
+        lambda: b2g.linear_cross_entropy_backward(x, x, ids, n, six, dw=out),
+        lambda: b2g.linear_cross_entropy_backward(x, x, out.view(torch.int64).view(-1)[:6], n, n,
+                                                  dw=out),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    assert (buf == 1).all()
