@@ -128,7 +128,7 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Kind k;
   if (!k.take(x) || !k.matrix(x)) Py_RETURN_NONE;
   const int64_t r = x.size(0), c = x.size(1);
-  if (!small(c) || (w.defined() && !k.vector(w, k.type, c)) ||
+  if (!small(c) || c == 0 || (w.defined() && !k.vector(w, k.type, c)) ||
       (b.defined() && !k.vector(b, k.type, c)))
     Py_RETURN_NONE;
   const Tensor y = k.empty({r, c}), mean = k.empty({r}, at::kFloat), rstd = k.empty({r}, at::kFloat);

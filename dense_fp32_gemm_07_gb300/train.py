@@ -211,6 +211,10 @@ class _OnStream:
         with _torch.cuda.stream(self.stream):
             return _torch.empty(shape, dtype=dtype, device=device)
 
+    def fill(self, t, value):
+        with _torch.cuda.stream(self.stream):
+            t.fill_(value)
+
     def uses(self, *tensors):
         for t in tensors:
             if t is not None:
@@ -225,6 +229,9 @@ class _OnCurrent:
     def __init__(self, dev):
         self.handle = _torch._C._cuda_getCurrentRawStream(dev)
         self.empty = _empty
+
+    def fill(self, t, value):
+        t.fill_(value)
 
     def uses(self, *tensors):
         pass
@@ -276,6 +283,9 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
         _apart(out, ("weight", weight), ("bias", bias))
     mean = on.empty((r,), _torch.float32, device)
     rstd = on.empty((r,), _torch.float32, device)
+    if c == 0:  # nothing is launched: rows of nothing have no mean
+        on.fill(mean, float("nan"))
+        on.fill(rstd, float("nan"))
     rc = _lib.b2g_layernorm(_CODES[dt], r, c, x.data_ptr(), ldx, pw, pb, eps, out.data_ptr(), ldy,
                             mean.data_ptr(), rstd.data_ptr(), on.handle)
     if rc:

@@ -55,7 +55,7 @@ extern "C" {
  *   mean, rstd    rows FP32 values each, for the backward pass; either may be NULL.
  *   eps           >= 0 (else B2G_ERR_INVALID_DIM).
  * y may be x itself (same leading dimension) and must not overlap it otherwise.
- * rows == 0 or cols == 0: nothing is launched.
+ * rows == 0 or cols == 0: nothing is launched, and nothing written.
  */
 int b2g_layernorm(int dtype, long long rows, int cols, const void* x, long long ldx,
                   const void* weight, const void* bias, float eps, void* y, long long ldy,

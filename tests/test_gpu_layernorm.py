@@ -247,3 +247,18 @@ def test_bounded_waits_of_the_rings(b2g, cols):
         again = call()
         assert all(torch.equal(p, q) for p, q in zip(first, again))
         assert b2g.b2g_status(stream) == (0, 0)
+
+
+@pytest.mark.parametrize("side", [False, True])
+def test_no_columns(b2g, side):
+    """Rows of nothing have no mean: NaN, not what the memory held."""
+    stream = torch.cuda.Stream() if side else None
+    x = torch.empty(1000, 0, device="cuda")
+    junk = [torch.full((1000,), 7.0, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    del junk  # the allocator hands these out again
+    y, mean, rstd = b2g.layer_norm(x, stream=stream)
+    dx, dw, db = b2g.layer_norm_backward(x, x, x[0], mean, rstd, stream=stream)
+    torch.cuda.synchronize()
+    assert y.shape == dx.shape == (1000, 0) and dw.shape == db.shape == (0,)
+    assert torch.isnan(mean).all() and torch.isnan(rstd).all()
