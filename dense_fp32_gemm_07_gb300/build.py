@@ -9,11 +9,15 @@ a spill there would otherwise show up only as a quiet loss of speed.
 
 csrc/train_binding.cpp, the native side of the tensor calls in train.py, is
 compiled next to them with the host compiler against the installed torch and
-linked into _train_binding.so.
+linked into _train_binding.so.  The library needs neither: where torch is not
+installed it is built alone, and it is linked before a failure of the binding is
+reported.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
+import importlib.util
 import os
 import re
 import shutil
@@ -49,11 +53,40 @@ def _deps():
         os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _newer(path) -> bool:
+    """Whether `path` is newer than every source."""
+    if not os.path.exists(path):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = os.path.getmtime(path)
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _torch_stamp():
+    """Which torch is installed (found without importing it); None where there is none."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "unknown"
+    return f"{version} {spec.origin}"
+
+
+def _binding_up_to_date() -> bool:
+    """The binding is newer than its sources and linked against the torch that is there."""
+    stamp = _torch_stamp()
+    if stamp is None:
+        return True  # nothing to bind to
+    try:
+        with open(os.path.join(BUILD, "binding_torch.txt")) as f:
+            return f.read() == stamp and _newer(BINDING)
+    except FileNotFoundError:
+        return False
+
+
+def up_to_date() -> bool:
+    return _newer(LIB) and _binding_up_to_date()
 
 
 _SPILL = re.compile(r"(\d+) bytes spill stores, (\d+) bytes spill loads")
@@ -132,25 +165,29 @@ def _link_binding(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, BINDING)
+    with open(os.path.join(BUILD, "binding_torch.txt"), "w") as f:
+        f.write(_torch_stamp())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Build the library and the binding if any source is newer; return the library's path."""
+    """Build the library and the binding if any source is newer, or the binding's torch
+    another one; return the library's path."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        binding = ex.submit(_compile_binding)
-        objs = list(ex.map(_compile, srcs))
-        binding_obj = binding.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
-    os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+        binding = ex.submit(_compile_binding) if _torch_stamp() else None
+        if force or not _newer(LIB):
+            objs = list(ex.map(_compile, srcs))
+            tmp = LIB + f".tmp{os.getpid()}"
+            cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
+            os.replace(tmp, LIB)
+    if binding:
+        _link_binding(binding.result())
     if verbose:
         for s in srcs:
             with open(os.path.join(BUILD, f"ptxas_{s[:-3]}.log")) as f:

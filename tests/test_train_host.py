@@ -4,6 +4,8 @@ pointers below are never dereferenced."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -208,6 +210,46 @@ def test_tensor_calls_refuse(b2g):
         b2g.clip_grad_norm([f], -1.0)
     with pytest.raises(ValueError):
         b2g.grad_norm([])
+
+
+BUILD_ALONE = """
+import os, sys
+sys.path.insert(0, sys.argv[1])
+from dense_fp32_gemm_07_gb300 import build as b
+out, how = sys.argv[2:]
+b.BUILD, b.LIB = os.path.join(out, "build"), os.path.join(out, "libb2g_sgemm.so")
+b.BINDING = os.path.join(out, "_train_binding.so")
+b.sources = lambda: ["noalloc.cu"]     # one small file stands for all
+if how == "hidden":
+    sys.modules["torch"] = None        # as where it is not installed
+else:
+    b.shutil.which = lambda name, which=b.shutil.which: "/bin/false" if name == "g++" else which(name)
+assert not b.up_to_date()
+try:
+    assert b.build() == b.LIB and how == "hidden"
+    assert b.up_to_date() and "torch" not in [m for m in sys.modules if sys.modules[m]]
+except RuntimeError as e:
+    assert how == "broken" and "train_binding.cpp" in str(e), e
+    assert not b.up_to_date()
+assert os.path.exists(b.LIB) and not os.path.exists(b.BINDING)
+"""
+
+
+@pytest.mark.parametrize("how", ["hidden", "broken"])
+def test_library_builds_without_the_binding(tmp_path, how):
+    """Without torch the C library is built alone; a binding that fails is reported, with
+    the library linked all the same."""
+    subprocess.run([sys.executable, "-c", BUILD_ALONE, ROOT, str(tmp_path), how], check=True)
+
+
+def test_another_torch_makes_the_binding_stale(b2g, monkeypatch, tmp_path):
+    from dense_fp32_gemm_07_gb300 import build
+
+    assert build.up_to_date()
+    monkeypatch.setattr(build, "_torch_stamp", lambda: "0.0 elsewhere")
+    assert not build.up_to_date()
+    monkeypatch.setattr(build, "_torch_stamp", lambda: None)
+    assert build.up_to_date()
 
 
 def test_results_beside_their_inputs(b2g):
