@@ -960,8 +960,10 @@ int launch_planes(XentJobs& jobs, const XentMaps& maps, const TrainDevice& d, cu
 // 777 and the relative error of dh at 1205 x 1703 x 2136 (FP32 library products: 1.2e-6):
 // 1: 384 us, 1.9e-7; 2: 357 us, 5.3e-7; 4: 349 us, 1.3e-6; 8: 348 us, 2.8e-6.  Logits of BF16
 // operands: 16, whose error of the loss is that of FP32 products.  Products that are
-// rounded to BF16 do not show it.
-int group_of(int dtype, bool logits) { return dtype == B2G_F32 ? 2 : logits ? 16 : 1 << 20; }
+// rounded to BF16: kGroupK.
+int group_of(int dtype, bool logits) {
+  return dtype == B2G_F32 ? 2 : logits ? 16 : kGroupK / kBK;
+}
 
 template <int MODE>
 int launch_gemm(XentJobs& jobs, const XentMaps& maps, const TrainDevice& d, cudaStream_t st) {

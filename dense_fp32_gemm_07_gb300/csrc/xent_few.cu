@@ -667,7 +667,7 @@ int launch_few_dh(const XentRows& r, const Planes& dz, const FewHead& w, int fir
   p.tile_rows = kM, p.tiles = (int)ceil_div(r.width, kM);
   p.k_tiles = (int)ceil_div(n, w.f32 ? kBK : 2 * kBK);
   p.slices = slices;
-  p.group = w.f32 ? 1 : 1 << 20;
+  p.group = w.f32 ? 1 : kGroupK / (2 * kBK);
   p.a_tx = (uint32_t)(kM * kBK * es);
   p.scale = const_cast<float*>(scale), p.part = part, p.part_ld = ld;
   CUtensorMap a = {}, b = {};

@@ -254,6 +254,29 @@ def test_weights_of_rows_without_a_gradient(b2g, tokens, dtype):
         assert torch.equal(got[0], dh) and torch.equal(got[1], dw), value
 
 
+def test_products_over_very_many_classes(b2g):
+    """dh over 2^28 classes, whose terms all have one sign.  The tensor core truncates each
+    addition (2^-23 of the sum at most), 2048 of them in a row before FP32 registers take
+    over.  Every logit is 0 and each probability 2^-28 to 2^-18 (its exponential's error and
+    that of lse), which rounds to BF16's 2^-28; the target's row of w is 0, so dh is the mean
+    of w's rows."""
+    vocab, width = 1 << 28, 8
+    w = torch.empty(vocab, width, dtype=BF16, device="cuda")
+    gen, mean = torch.Generator(device="cuda").manual_seed(0), 0
+    for i in range(0, vocab, 1 << 25):
+        w[i:i + (1 << 25)] = torch.rand(1 << 25, width, generator=gen, device="cuda") + 1
+        if i == 0:
+            w[77] = 0
+        mean = mean + w[i:i + (1 << 25)].double().sum(0) / vocab
+    h, t = torch.zeros(1, width, dtype=BF16, device="cuda"), torch.tensor([77], device="cuda")
+    loss, lse = b2g.linear_cross_entropy(h, w, t)
+    want = 28 * 0.6931471805599453
+    assert abs(float(lse) - want) <= 2.0 ** -20 + 8 * U32 * want and float(loss) == float(lse)
+    dh, dw = b2g.linear_cross_entropy_backward(h, w, t, lse, torch.ones(1, device="cuda"))
+    close(dh[0], mean, (U[BF16] + 2048 * 2.0 ** -23 + 2.0 ** -18) * mean, "dh")
+    assert not dw.any()  # h is 0
+
+
 def test_no_tokens(b2g):
     h, w = torch.empty(0, 64, device="cuda"), torch.randn(50, 64, device="cuda")
     t, e = torch.empty(0, dtype=torch.int64, device="cuda"), torch.empty(0, device="cuda")
