@@ -125,6 +125,16 @@ def test_forward_and_backward(b2g, tokens, vocab, width, dtype):
     assert status(b2g) == (0, 0)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("tokens,vocab,width", [
+    (65, 5207, 40), (66, 7310, 40), (67, 10114, 72), (65, 12217, 40), (70, 15021, 72), (65, 17124, 40),
+    (300, 9000, 200), (500, 20001, 40)])
+def test_widths_of_a_tile(b2g, tokens, vocab, width, dtype):
+    """Tiles of 96, 128, 160, 192, 224 and 256 classes, the last one of a row ragged."""
+    h, w, t, g = make(tokens, vocab, width, dtype)
+    check(b2g, h, w, t, g)
+
+
 @pytest.mark.parametrize("dtype,tokens,vocab,width", [
     (F32, 8192, 12000, 64), (BF16, 8192, 40000, 64), (F32, 64, 1500000, 8)])
 def test_several_pieces_of_the_vocabulary(b2g, dtype, tokens, vocab, width):
