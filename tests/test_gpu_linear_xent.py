@@ -413,3 +413,30 @@ def test_bounded_wait_reports(b2g):
         b2g.b2g_set_wait_limit_ns(2_000_000_000)
     again = b2g.linear_cross_entropy(h, w, t)
     assert torch.equal(again[0], loss) and status(b2g) == (0, 0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("tokens,vocab", [(40, 2000), (300, 1000)])
+@pytest.mark.parametrize("stop", [1, 2, 7])
+def test_bounded_waits_of_both_forms(b2g, tokens, vocab, dtype, stop):
+    """The same for the loss and for the gradients, up to 64 tokens and in CTA pairs, the
+    copies stopped within and after a k tile's planes."""
+    h, w, t, g = make(tokens, vocab, 1024, dtype)
+    loss, lse = b2g.linear_cross_entropy(h, w, t)
+    first = b2g.linear_cross_entropy_backward(h, w, t, lse, g)
+    torch.cuda.synchronize()
+    for call in (lambda: b2g.linear_cross_entropy(h, w, t),
+                 lambda: b2g.linear_cross_entropy_backward(h, w, t, lse, g)):
+        try:
+            b2g.b2g_set_wait_limit_ns(2_000_000)
+            b2g.b2g_debug_stop_after(stop)
+            call()
+            rc, flags = status(b2g)
+            assert rc == b2g.B2G_ERR_TIMEOUT and flags & 0xF
+        finally:
+            b2g.b2g_debug_stop_after(-1)
+            b2g.b2g_set_wait_limit_ns(2_000_000_000)
+    again = b2g.linear_cross_entropy(h, w, t)
+    assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
+    got = b2g.linear_cross_entropy_backward(h, w, t, lse, g)
+    assert all(torch.equal(p, q) for p, q in zip(first, got)) and status(b2g) == (0, 0)
