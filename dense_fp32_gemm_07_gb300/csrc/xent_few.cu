@@ -15,7 +15,8 @@
 //   kDh     dh^T = w^T dz^T: w's columns are the rows of the MMA ("MN-major" A), k
 //           runs over the classes, cut into slices whose sums another kernel adds
 // Bound: the bytes of w: 16 x 32768 x 4096, scoring, 46 us in BF16 (5.9 TB/s); FP32 134 us
-// (4.0 TB/s), where splitting the values on their way holds the reads up.
+// (4.0 TB/s).  What holds FP32's reads up has not been measured: of about 2200 cycles that a
+// 64-k tile takes, issuing the split's instructions is some 520.
 #include <atomic>
 
 #include "xent.cuh"
