@@ -26,7 +26,7 @@
  * Sizes: row lengths, vocab and the cross entropy's tokens are at most 2^31 - 2^16,
  * layer norm's rows 2^31 - 1 and the embedding's tokens 2^30, else B2G_ERR_INVALID_DIM.
  *
- * Alignment: any.  Operands whose base is 16-byte aligned and whose leading
+ * Alignment: any multiple of the element's size.  Operands whose base is 16-byte aligned and whose leading
  * dimensions (and width) are multiples of 16 bytes run with 16-byte accesses.
  */
 #ifndef B2G_TRAIN_H
