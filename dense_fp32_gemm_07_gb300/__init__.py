@@ -9,7 +9,8 @@ Low-level names mirror the C ABI one to one (``b2g_sgemm``, ``b2g_sgemm_ex``,
 ``b2g_sgemm_with_plan``, ...) and take raw device pointers; ``sgemm`` is the
 tensor-level convenience: ``C <- alpha * op(A) @ op(B) + beta * C`` in place;
 ``sgemm_colmajor`` is the same for column-major tensors.  The operators of a
-training step beside the products (include/b2g_train.h) are in ``train.py``.
+training step beside the products (include/b2g_train.h) are in ``train.py``, those
+on activations kept in 8 bits in ``activations.py``.
 """
 from __future__ import annotations
 
@@ -440,3 +441,6 @@ from .train import (  # noqa: E402
     B2G_BF16, B2G_ERR_INDEX, B2G_ERR_INVALID_TYPE, B2G_ERR_WORKSPACE, B2G_F32, TRAIN_EXPORTS,
     clip_grad_norm, embedding, embedding_backward, grad_norm, layer_norm, layer_norm_backward,
     linear_cross_entropy, linear_cross_entropy_backward, train_library)
+from .activations import (  # noqa: E402
+    dequantize_8bit, linear_weight_grad_8bit, quantize_8bit, rms_norm, rms_norm_8bit,
+    rms_norm_backward)

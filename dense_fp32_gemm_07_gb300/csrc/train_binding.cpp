@@ -1,4 +1,4 @@
-// train_binding.cpp -- the tensor calls of train.py for plain arguments, in native
+// train_binding.cpp -- the tensor calls of train.py and activations.py for plain arguments, in native
 // code: contiguous operands of one type on the current device, results that the
 // call allocates, the current stream.  Such a call costs the host a few
 // microseconds where the same checks and conversions in Python cost 10 to 40,
@@ -8,6 +8,7 @@
 // code as an int, or None when an argument is not of that plain kind (strided,
 // another stream, `out` given, wrong in some way); train.py then goes through its
 // own checks, which serve it or say what is wrong.
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -40,6 +41,10 @@ struct Kind {
       code = B2G_BF16;
     else
       return false;
+    return at(t);
+  }
+  // The device alone.
+  bool at(const Tensor& t) {
     device = t.device();
     if (!device.is_cuda() || device.index() != c10::cuda::current_device()) return false;
     stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
@@ -338,6 +343,182 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// Codes and scales in 8 bits: matrices with unit column stride.
+struct Eight {
+  Tensor q, s;
+  int64_t rows, cols;
+  long long ldq, lds;
+
+  // New ones, rows on 16-byte boundaries.
+  Eight(const Kind& k, int64_t r, int64_t c) : rows(r), cols(c), ldq((c + 15) / 16 * 16), lds((c + 31) / 32) {
+    q = k.empty({r, (int64_t)ldq}, at::kFloat8_e4m3fn);
+    if (ldq != c) q = q.narrow(1, 0, c);
+    s = k.empty({r, (int64_t)lds}, at::kFloat8_e8m0fnu);
+  }
+  Eight(const Tensor& codes, const Tensor& scales) : q(codes), s(scales) {}
+  // Whether given ones are on the kind's device and fit each other.
+  bool take(const Kind& k) {
+    if (q.scalar_type() != at::kFloat8_e4m3fn || s.scalar_type() != at::kFloat8_e8m0fnu ||
+        q.device() != k.device || s.device() != k.device || q.dim() != 2 || s.dim() != 2 ||
+        !s.is_contiguous())
+      return false;
+    rows = q.size(0), cols = q.size(1), ldq = q.stride(0), lds = s.size(1);
+    return rows > 0 && cols > 1 && q.stride(1) == 1 && ldq >= cols && s.size(0) == rows &&
+           lds == (cols + 31) / 32;
+  }
+};
+
+PyObject* pair(const Eight& e) {
+  PyObject* t = PyTuple_New(2);
+  if (!t) return nullptr;
+  PyTuple_SET_ITEM(t, 0, wrap(e.q));
+  PyTuple_SET_ITEM(t, 1, wrap(e.s));
+  return t;
+}
+
+// quantize_8bit(x)
+PyObject* quantize_8bit(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 1 || !is_tensor(a[0])) Py_RETURN_NONE;
+  const Tensor& x = tensor(a[0]);
+  Kind k;
+  if (!k.take(x) || !k.matrix(x)) Py_RETURN_NONE;
+  const int64_t r = x.size(0), c = x.size(1);
+  if (!small(c) || c == 0) Py_RETURN_NONE;
+  const Eight e(k, r, c);
+  const int rc = b2g_quantize8(k.code, r, (int)c, ptr(x), c, ptr(e.q), e.ldq, ptr(e.s), e.lds, k.stream);
+  return rc ? PyLong_FromLong(rc) : pair(e);
+  END_HANDLE_TH_ERRORS
+}
+
+// dequantize_8bit(codes, scales, dtype or None)
+PyObject* dequantize_8bit(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 3 || !is_tensor(a[0]) || !is_tensor(a[1])) Py_RETURN_NONE;
+  at::ScalarType type = at::kBFloat16;
+  if (a[2] != Py_None) {
+    if (!THPDtype_Check(a[2])) Py_RETURN_NONE;
+    type = reinterpret_cast<THPDtype*>(a[2])->scalar_type;
+    if (type != at::kFloat && type != at::kBFloat16) Py_RETURN_NONE;
+  }
+  Eight e(tensor(a[0]), tensor(a[1]));
+  Kind k;
+  if (!k.at(e.q) || !e.take(k) || !small(e.cols)) Py_RETURN_NONE;
+  const Tensor y = k.empty({e.rows, e.cols}, type);
+  const int rc = b2g_dequantize8(type == at::kFloat ? B2G_F32 : B2G_BF16, e.rows, (int)e.cols, ptr(e.q),
+                                 e.ldq, ptr(e.s), e.lds, ptr(y), e.cols, k.stream);
+  return answer(rc, y);
+  END_HANDLE_TH_ERRORS
+}
+
+// rms_norm(x, weight, residual, eps), or rms_norm_8bit(.., with_y, keep_total)
+PyObject* rms(PyObject* const* a, Py_ssize_t n, bool eight) {
+  double eps;
+  if (n != (eight ? 6 : 4) || !is_tensor(a[0]) || !is_tensor_or_none(a[1]) ||
+      !is_tensor_or_none(a[2]) || !number(a[3], &eps) ||
+      (eight && (!PyBool_Check(a[4]) || !PyBool_Check(a[5]))))
+    Py_RETURN_NONE;
+  const Tensor &x = tensor(a[0]), &w = tensor(a[1]), &res = tensor(a[2]);
+  Kind k;
+  if (!k.take(x) || !k.matrix(x)) Py_RETURN_NONE;
+  const int64_t r = x.size(0), c = x.size(1);
+  if (!small(c) || c == 0 || (w.defined() && !k.vector(w, k.type, c)) ||
+      (res.defined() && (!k.matrix(res) || res.sizes() != x.sizes())))
+    Py_RETURN_NONE;
+  const bool with_y = !eight || a[4] == Py_True, keep = eight && a[5] == Py_True;
+  const Tensor y = with_y ? k.empty({r, c}) : Tensor(), total = res.defined() ? k.empty({r, c}) : x,
+               rstd = k.empty({r}, at::kFloat);
+  const Eight none{Tensor(), Tensor()};
+  const Eight y8 = eight ? Eight(k, r, c) : none, t8 = keep ? Eight(k, r, c) : none;
+  auto at = [](const Tensor& t) { return t.defined() ? ptr(t) : nullptr; };
+  const int rc = b2g_rmsnorm(k.code, r, (int)c, ptr(x), c, at(res), c, at(w), (float)eps,
+                             res.defined() ? ptr(total) : nullptr, c, at(y), c, at(y8.q), eight ? y8.ldq : 0,
+                             at(y8.s), eight ? y8.lds : 0, at(t8.q), keep ? t8.ldq : 0, at(t8.s),
+                             keep ? t8.lds : 0, rstd.data_ptr<float>(), k.stream);
+  if (!eight) return answer(rc, y, total, rstd);
+  if (rc) return PyLong_FromLong(rc);
+  PyObject* out = PyTuple_New(5);
+  if (!out) return nullptr;
+  PyTuple_SET_ITEM(out, 0, wrap(y));
+  PyTuple_SET_ITEM(out, 1, wrap(total));
+  PyTuple_SET_ITEM(out, 2, wrap(rstd));
+  PyObject *p = pair(y8), *q = keep ? pair(t8) : Py_NewRef(Py_None);
+  PyTuple_SET_ITEM(out, 3, p);
+  PyTuple_SET_ITEM(out, 4, q);
+  if (p && q) return out;
+  Py_DECREF(out);
+  return nullptr;
+}
+PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return rms(a, n, false);
+  END_HANDLE_TH_ERRORS
+}
+PyObject* rms_norm_8bit(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return rms(a, n, true);
+  END_HANDLE_TH_ERRORS
+}
+
+// rms_norm_backward(dy, total or (codes, scales), weight, rstd, dtotal)
+PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 5 || !is_tensor(a[0]) || !is_tensor_or_none(a[2]) || !is_tensor(a[3]) ||
+      !is_tensor_or_none(a[4]))
+    Py_RETURN_NONE;
+  const Tensor &dy = tensor(a[0]), &w = tensor(a[2]), &rstd = tensor(a[3]), &dt = tensor(a[4]);
+  Kind k;
+  if (!k.take(dy) || !k.matrix(dy)) Py_RETURN_NONE;
+  const int64_t r = dy.size(0), c = dy.size(1);
+  const void *x, *scales = nullptr;
+  long long ldx = c, lds = 0;
+  if (is_tensor(a[1])) {
+    const Tensor& t = tensor(a[1]);
+    if (!k.matrix(t) || t.sizes() != dy.sizes()) Py_RETURN_NONE;
+    x = ptr(t);
+  } else {
+    if (!PyTuple_CheckExact(a[1]) || PyTuple_GET_SIZE(a[1]) != 2 ||
+        !is_tensor(PyTuple_GET_ITEM(a[1], 0)) || !is_tensor(PyTuple_GET_ITEM(a[1], 1)))
+      Py_RETURN_NONE;
+    Eight e(tensor(PyTuple_GET_ITEM(a[1], 0)), tensor(PyTuple_GET_ITEM(a[1], 1)));
+    if (!e.take(k) || e.rows != r || e.cols != c) Py_RETURN_NONE;
+    x = ptr(e.q), ldx = e.ldq, scales = ptr(e.s), lds = e.lds;
+  }
+  if (!small(c) || c == 0 || (w.defined() && !k.vector(w, k.type, c)) || !k.vector(rstd, at::kFloat, r) ||
+      (dt.defined() && (!k.matrix(dt) || dt.sizes() != dy.sizes())))
+    Py_RETURN_NONE;
+  size_t bytes = 0;
+  int rc = w.defined() ? b2g_rmsnorm_backward_workspace_size(k.code, r, (int)c, &bytes) : 0;
+  if (rc) return PyLong_FromLong(rc);
+  const Tensor dx = k.empty({r, c}), dw = w.defined() ? k.empty({c}) : Tensor(), ws = k.bytes(bytes);
+  rc = b2g_rmsnorm_backward(k.code, r, (int)c, ptr(dy), c, x, ldx, scales, lds,
+                            w.defined() ? ptr(w) : nullptr, rstd.data_ptr<float>(),
+                            dt.defined() ? ptr(dt) : nullptr, c, ptr(dx), c,
+                            dw.defined() ? ptr(dw) : nullptr, ptr(ws), bytes, k.stream);
+  return answer(rc, dx, dw);
+  END_HANDLE_TH_ERRORS
+}
+
+// linear_weight_grad_8bit(dy, codes, scales)
+PyObject* linear_weight_grad_8bit(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 3 || !is_tensor(a[0]) || !is_tensor(a[1]) || !is_tensor(a[2])) Py_RETURN_NONE;
+  const Tensor& dy = tensor(a[0]);
+  Eight e(tensor(a[1]), tensor(a[2]));
+  Kind k;
+  if (!k.take(dy) || !k.matrix(dy) || !e.take(k) || e.rows != dy.size(0)) Py_RETURN_NONE;
+  const int64_t t = e.rows, o = dy.size(1);
+  if (!small(t) || !small(o) || !small(e.cols)) Py_RETURN_NONE;
+  size_t bytes = 0;
+  int rc = b2g_linear_dweight8_workspace_size(k.code, (int)t, (int)o, (int)e.cols, ptr(dy), ld(o), &bytes);
+  if (rc) return PyLong_FromLong(rc);
+  const Tensor dw = k.empty({o, e.cols}), ws = k.bytes(bytes);
+  rc = b2g_linear_dweight8(k.code, (int)t, (int)o, (int)e.cols, ptr(dy), ld(o), ptr(e.q), e.ldq, ptr(e.s),
+                           e.lds, 0, ptr(dw), e.cols, ptr(ws), bytes, k.stream);
+  return answer(rc, dw);
+  END_HANDLE_TH_ERRORS
+}
+
 #define FAST(name, fn) \
   {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(fn)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
@@ -348,6 +529,12 @@ PyMethodDef methods[] = {
     FAST("linear_cross_entropy", linear_cross_entropy),
     FAST("linear_cross_entropy_backward", linear_cross_entropy_backward),
     FAST("clip", clip),
+    FAST("quantize_8bit", quantize_8bit),
+    FAST("dequantize_8bit", dequantize_8bit),
+    FAST("rms_norm", rms_norm),
+    FAST("rms_norm_8bit", rms_norm_8bit),
+    FAST("rms_norm_backward", rms_norm_backward),
+    FAST("linear_weight_grad_8bit", linear_weight_grad_8bit),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_train_binding", nullptr, -1, methods,

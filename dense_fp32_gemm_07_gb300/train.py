@@ -37,6 +37,9 @@ TRAIN_EXPORTS = (
     "b2g_embedding", "b2g_embedding_backward", "b2g_embedding_backward_workspace_size",
     "b2g_linear_xent", "b2g_linear_xent_backward", "b2g_linear_xent_workspace_size",
     "b2g_grad_norm", "b2g_clip_grad_norm", "b2g_grad_norm_workspace_size",
+    "b2g_rmsnorm", "b2g_rmsnorm_backward", "b2g_rmsnorm_backward_workspace_size",
+    "b2g_quantize8", "b2g_dequantize8",
+    "b2g_linear_dweight8", "b2g_linear_dweight8_workspace_size",
 )
 
 _lib = None
@@ -69,6 +72,15 @@ def train_library():
     lib.b2g_grad_norm.argtypes = [i, i, vp, vp, vp, vp, sz, vp]
     lib.b2g_clip_grad_norm.argtypes = [i, i, vp, vp, f, vp, vp, vp, sz, vp]
     lib.b2g_grad_norm_workspace_size.argtypes = [i, i, vp, psz]
+    lib.b2g_rmsnorm.argtypes = [i, ll, i, vp, ll, vp, ll, vp, f, vp, ll, vp, ll, vp, ll, vp, ll, vp,
+                                ll, vp, ll, vp, vp]
+    lib.b2g_rmsnorm_backward.argtypes = [i, ll, i, vp, ll, vp, ll, vp, ll, vp, vp, vp, ll, vp, ll,
+                                         vp, vp, sz, vp]
+    lib.b2g_rmsnorm_backward_workspace_size.argtypes = [i, ll, i, psz]
+    lib.b2g_quantize8.argtypes = [i, ll, i, vp, ll, vp, ll, vp, ll, vp]
+    lib.b2g_dequantize8.argtypes = [i, ll, i, vp, ll, vp, ll, vp, ll, vp]
+    lib.b2g_linear_dweight8.argtypes = [i, i, i, i, vp, ll, vp, ll, vp, ll, i, vp, ll, vp, sz, vp]
+    lib.b2g_linear_dweight8_workspace_size.argtypes = [i, i, i, i, vp, ll, psz]
     _lib = lib
     return lib
 

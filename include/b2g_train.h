@@ -1,8 +1,8 @@
 /*
  * b2g_train.h -- C ABI of the operators that a language model's training and
- * scoring steps run around their matrix products: layer norm, embedding
- * lookup, softmax cross entropy of a linear layer, and clipping by the global
- * gradient norm.  Part of the library behind b2g_sgemm.h, with its rules:
+ * scoring steps run around their matrix products: layer norm, root-mean-square
+ * norm, embedding lookup, softmax cross entropy of a linear layer, clipping by the
+ * global gradient norm, and activations kept in 8 bits for the backward pass.  Part of the library behind b2g_sgemm.h, with its rules:
  * DEVICE pointers owned by the caller, row-major operands with leading
  * dimensions in elements, calls that are asynchronous on `stream` (a
  * cudaStream_t, NULL = the legacy default stream), thread-safe, and a 0 or a
@@ -23,8 +23,8 @@
  * Results are the same bits run to run for given arguments: every sum has a
  * fixed order, and no floating-point atomics are used.
  *
- * Sizes: row lengths, vocab and the cross entropy's tokens are at most 2^31 - 2^16,
- * layer norm's rows 2^31 - 1 and the embedding's tokens 2^30, else B2G_ERR_INVALID_DIM.
+ * Sizes: row lengths, vocab and the cross entropy's and weight gradient's tokens are at
+ * most 2^31 - 2^16, the norms' and 8-bit forms' rows 2^31 - 1 and the embedding's tokens 2^30, else B2G_ERR_INVALID_DIM.
  *
  * Alignment: any multiple of the element's size.  Operands whose base is 16-byte aligned and whose leading
  * dimensions (and width) are multiples of 16 bytes run with 16-byte accesses.
@@ -175,6 +175,82 @@ int b2g_clip_grad_norm(int dtype, int count, const void* const* tensors, const l
                        float max_norm, void* const* outs, float* norm, void* workspace,
                        size_t workspace_bytes, void* stream);
 int b2g_grad_norm_workspace_size(int dtype, int count, const long long* numels, size_t* bytes);
+
+/*
+ * The 8-bit form of a rows x cols matrix: e4m3 codes, one byte each (rows ldq bytes
+ * apart), and for each 32 columns of a row (the last block may be shorter) a scale, one
+ * byte b that stands for 2^(b - 127) (e8m0; rows of ceil(cols / 32) of them, lds bytes
+ * apart).  The value is code * scale.  The scale is the smallest power of two, 2^-110 at
+ * least, that brings the largest finite magnitude of its block to 448 or below; a code is
+ * x / scale rounded to nearest even, off by at most 2^-4 of x or 2^-10 of the scale.
+ * Infinities and NaN become the code NaN and leave their block's scale alone.
+ * Codes whose base and ldq are multiples of 8 go with rows of x on 16-byte boundaries.
+ */
+int b2g_quantize8(int dtype, long long rows, int cols, const void* x, long long ldx, void* codes,
+                  long long ldq, void* scales, long long lds, void* stream);
+
+/*
+ * y = code * scale, rounded once to dtype (exact for what b2g_quantize8 made, but for
+ * values rounded up to 2^128, which are infinite).  Any scale is taken: 255 is NaN.
+ */
+int b2g_dequantize8(int dtype, long long rows, int cols, const void* codes, long long ldq,
+                    const void* scales, long long lds, void* y, long long ldy, void* stream);
+
+/*
+ * Root-mean-square norm of each row of x + residual:
+ *     total = x + residual (rounded to dtype; x where residual is NULL),
+ *     rstd = 1 / sqrt(sum_j total_j^2 / cols + eps),   y_j = total_j * rstd * weight_j.
+ *   weight                     cols values; NULL: ones.
+ *   total, y                   rows x cols each; either may be NULL (not stored).
+ *   y_codes, y_scales          y in 8 bits, rounded from FP32; both NULL: not wanted.
+ *   total_codes, total_scales  total in 8 bits; both NULL: not wanted.
+ *   rstd                       rows FP32 values, for the backward pass; may be NULL.
+ *   eps                        >= 0 (else B2G_ERR_INVALID_DIM).
+ * total and y may be x or residual itself (same leading dimension); no other overlap.
+ * rows == 0 or cols == 0: nothing is launched, and nothing written.
+ */
+int b2g_rmsnorm(int dtype, long long rows, int cols, const void* x, long long ldx,
+                const void* residual, long long ldr, const void* weight, float eps, void* total,
+                long long ldt, void* y, long long ldy, void* y_codes, long long ldyq, void* y_scales,
+                long long ldys, void* total_codes, long long ldtq, void* total_scales,
+                long long ldts, float* rstd, void* stream);
+
+/*
+ * Gradients of b2g_rmsnorm.  With xhat = total * rstd and g = dy * weight:
+ *     dx      = rstd * (g - xhat * mean_j(g * xhat)) + dtotal,
+ *     dweight = sum over the rows of dy * xhat.
+ * dx is the gradient of x and of residual alike.
+ *   total, total_scales  what b2g_rmsnorm stored: total in dtype with total_scales NULL, or
+ *                        its codes (ldt in bytes) and scales.
+ *   dtotal               the gradient that reaches total past the norm; NULL: none.
+ *   dweight              cols values, or NULL (then no workspace is needed).  rows == 0
+ *                        writes zeros.
+ * dx may be dy or dtotal itself (same leading dimension); no other overlap.
+ */
+int b2g_rmsnorm_backward(int dtype, long long rows, int cols, const void* dy, long long lddy,
+                         const void* total, long long ldt, const void* total_scales, long long ldts,
+                         const void* weight, const float* rstd, const void* dtotal, long long lddt,
+                         void* dx, long long lddx, void* dweight, void* workspace,
+                         size_t workspace_bytes, void* stream);
+int b2g_rmsnorm_backward_workspace_size(int dtype, long long rows, int cols, size_t* bytes);
+
+/*
+ * The weight gradient of a linear layer y = x w^T whose input was kept in 8 bits:
+ *     dw = dy^T x  (plus dw's previous value when accumulate != 0).
+ *   dy             tokens x outs, lddy.   codes, scales  x: tokens x width, ldq, lds.
+ *   dw             outs x width, lddw; it must not overlap the operands.
+ * x's values enter as BF16, in which those of b2g_quantize8 are exact; BF16 dy enters as it
+ * is, FP32 dy as three BF16 pieces that carry its 24 bits (it must be finite).  Products add
+ * up in FP32.  A value of x that is NaN or infinite makes its column of dw NaN or infinite
+ * whatever dy is.  tokens == 0 writes zeros (nothing when accumulate != 0).
+ */
+int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* dy, long long lddy,
+                        const void* codes, long long ldq, const void* scales, long long lds,
+                        int accumulate, void* dw, long long lddw, void* workspace,
+                        size_t workspace_bytes, void* stream);
+/* dy is inspected for its alignment only. */
+int b2g_linear_dweight8_workspace_size(int dtype, int tokens, int outs, int width, const void* dy,
+                                       long long lddy, size_t* bytes);
 
 #ifdef __cplusplus
 }
