@@ -1091,7 +1091,8 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
       p.slices = l.slices_h < p.k_tiles ? l.slices_h : p.k_tiles;
       p.to_part = l.h_sums, p.add = i > 0;
       p.out = dh, p.ldo = lddh;
-      p.out_tma = vec16(dh) && vec16_ld(lddh, dtype);
+      // a bulk-tensor store writes whole 16-byte units, those past the last column too
+      p.out_tma = vec16(dh) && vec16_ld(lddh, dtype) && vec16_ld(width, dtype);
       rc = map_k(&maps.a[0], dz, 128);
       if (!rc) rc = map_mn(&maps.b[0], piece);
       if (!rc && (p.to_part || p.out_tma))
@@ -1109,8 +1110,9 @@ int b2g_linear_xent_backward(int dtype, int tokens, int vocab, int width, const 
       p.slices = l.slices_w;
       p.to_part = l.slices_w > 1;
       p.out = dw_rows, p.ldo = lddw, p.accumulate = accumulate != 0;
-      // a bulk-tensor store adds in the output's type: right for FP32 only
-      p.out_tma = vec16(dw_rows) && vec16_ld(lddw, dtype) && !(accumulate && !f32);
+      // as for dh; and it adds in the output's type: right for FP32 only
+      p.out_tma = vec16(dw_rows) && vec16_ld(lddw, dtype) && vec16_ld(width, dtype) &&
+                  !(accumulate && !f32);
       p.add = !p.to_part && accumulate;
       rc = map_mn(&maps.a[1], dz);
       if (!rc) rc = map_mn(&maps.b[1], ph);
