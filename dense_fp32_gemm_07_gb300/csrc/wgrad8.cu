@@ -1,63 +1,401 @@
 // wgrad8.cu -- a linear layer's weight gradient dw = dy^T x from an x kept in 8 bits
-// (b2g_linear_dweight8 in include/b2g_train.h).
+// (b2g_linear_dweight8 in include/b2g_train.h), on the 5th-generation tensor cores.
 //
-// Blocks of 64 x 64 results, 4 x 4 a thread, 16 tokens at a time through shared memory.
+// dw (outs x width) is a sum over the tokens, so both operands are read with their rows
+// as k ("MN-major") and nothing is transposed.  x's values have 4 significant bits and
+// power-of-two scales: a first kernel writes them as BF16, exactly.  BF16 dy is multiplied
+// as it is; FP32 dy is split into three BF16 planes, dy = d0 + d1 + d2 to 24 bits, and
+// the three products d x are added up, the smallest first.
+//
+// The product runs on 256 x 256 tiles of a CTA pair (tcgen05.mma.cta_group::2, FP32
+// accumulators in tensor memory, double buffered).  As many tiles as fill all pairs are
+// whole; the k range of the rest, taken one after another, is cut into equal pieces, one a
+// pair, so that all pairs end together.  A piece that is not a whole tile leaves FP32 sums,
+// which a last kernel adds in order.
+#include <atomic>
+
 #include "eightbit.cuh"
+#include "pair.cuh"
 
 namespace b2g {
 namespace {
 
-struct Dw8 {
-  int tokens, outs, width;
+constexpr int kThreads = 128 + 32 * kEpiWarps;  // warp 0 copies, warp 1 multiplies, 2 and 3 idle
+// Registers, as in the cross entropy's product: 128 * 72 + 256 * 216 = 64,512 of the 168 a
+// thread that the block starts with.
+constexpr int kIssueRegs = 72, kEpiRegs = 216;
+constexpr uint32_t kOperand = 128 * kBK * 2;    // a CTA's 128 rows of one plane: 16 KB
+// A stage holds all planes of a k tile of dy, and x's.
+template <int PLANES>
+constexpr int kStages = 12 / (PLANES + 1);
+template <int PLANES>
+constexpr uint32_t kStageBytes = (PLANES + 1) * kOperand;
+constexpr int kMaxStages = 6;
+constexpr int kNumBars = 2 * kMaxStages + 5;
+constexpr int kSmemBytes = 12 * kOperand + kEpiWarps * kOutBytes + 1024 + kNumBars * 8 + 16;
+constexpr uint32_t kTmemCols = 2 * kTile;
+constexpr int kPairs = 76;  // what the work is shared out among (GB300: 152 SMs)
+
+struct Dw8Gemm {
+  int rows, cols;            // outs, width
+  int tiles_m, tiles_n, k_tiles;
+  int tile_n;                // columns of a tile: 256, or 128
+  int full, rest;            // whole tiles a pair; tiles that remain
+  long long piece;           // k tiles of a pair's piece of the rest
+  int split;                 // pieces leave sums
+  int group;                 // k tiles that add up in tensor memory before FP32 takes over
+  unsigned long long wait_limit_ns;
+  int debug_stop;            // >= 0: the copy issuer stops early (timeout test)
+  unsigned int* status;
+  int add;                   // a bulk-tensor store adds to what is there
+  int out_tma;               // whole tiles leave by bulk-tensor stores; else element by element
+  void* out;
+  long long ldo;
+  int out_bf16, accumulate;
+};
+struct alignas(64) Dw8Maps {
+  CUtensorMap dy, x, out, part;
+};
+
+struct Unit {
+  int tile, kt0, kt1, slot;  // slot: of the sums, -1 for a whole tile
+};
+
+// The k-th unit of this pair; false: there is none.
+__device__ __forceinline__ bool unit_at(const Dw8Gemm& p, int pair, int pairs, int k, Unit& u) {
+  if (k < p.full) {
+    u = Unit{k * pairs + pair, 0, p.k_tiles, -1};
+    return true;
+  }
+  k -= p.full;
+  const long long all = (long long)p.rest * p.k_tiles;
+  const long long from = pair * p.piece, to = min(from + p.piece, all);
+  const long long tile = from / p.k_tiles, edge = (tile + 1) * p.k_tiles;  // a piece spans two tiles at most
+  if (k > 1 || from >= to || (k == 1 && to <= edge)) return false;
+  const long long a = k ? edge : from, b = k ? to : min(to, edge), base = (tile + k) * p.k_tiles;
+  u = Unit{p.full * pairs + (int)tile + k, (int)(a - base), (int)(b - base), p.split ? 2 * pair + k : -1};
+  return true;
+}
+
+// Tiles in groups of 16 rows of tiles, so that a wave shares operand rows in L2.
+__device__ __forceinline__ void tile_at(const Dw8Gemm& p, int tile, int& tm, int& tn) {
+  constexpr int kGroup = 16;
+  const int per = kGroup * p.tiles_n, g = tile / per, first = g * kGroup;
+  const int size = min(p.tiles_m - first, kGroup), r = tile - g * per;
+  tm = first + r % size;
+  tn = r / size;
+}
+
+__device__ __forceinline__ int groups_of(const Dw8Gemm& p, int kts) {
+  return (kts + p.group - 1) / p.group;
+}
+
+// This warp's columns of rows row0 .. row0 + 31 of a finished tile to the result, or to
+// the sums in `slot`.
+__device__ __forceinline__ void put_tile(const Dw8Gemm& p, const Dw8Maps& maps, float (&v)[128],
+                                         int row0, int local_row, int n0, int local_n, int left,
+                                         int slot, uint32_t buf, int lane) {
+  if (row0 >= p.rows || left <= 0) return;
+  if (slot >= 0 || (p.out_tma && !p.out_bf16)) {
+    const CUtensorMap* m = slot >= 0 ? &maps.part : &maps.out;
+    const int x = slot >= 0 ? local_n : n0, y = slot >= 0 ? slot * kTile + local_row : row0;
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) {
+      if (c < left) {
+        uint4 w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          w[j] = make_uint4(__float_as_uint(v[c + 4 * j]), __float_as_uint(v[c + 4 * j + 1]),
+                            __float_as_uint(v[c + 4 * j + 2]), __float_as_uint(v[c + 4 * j + 3]));
+        store_rows(buf, m, x + c, y, 0, w, slot < 0 && p.add, lane);
+      }
+    }
+  } else if (p.out_tma) {
+#pragma unroll
+    for (int c = 0; c < 128; c += 64) {
+      if (c < left) {
+        uint4 w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i = c + 8 * j;
+          w[j] = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
+                            pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
+        }
+        store_rows(buf, &maps.out, n0 + c, row0, 0, w, false, lane);
+      }
+    }
+  } else if (p.out_bf16) {
+    put_rows(static_cast<Bf16*>(p.out) + (long long)row0 * p.ldo + n0, v, p, row0, left, buf, lane);
+  } else {
+    put_rows(static_cast<float*>(p.out) + (long long)row0 * p.ldo + n0, v, p, row0, left, buf, lane);
+  }
+}
+
+// CTA r of a pair stages columns 128r .. of the tile's part of dy and its half of x's and
+// holds rows 128r .. of the accumulator.  Both CTAs' copies of a stage complete on the even
+// CTA's `full` barrier; its warp 1 issues the pair's MMAs and commits "stage read" and
+// "accumulator final" to both CTAs.  Every wait is bounded: on a timeout the kernel flags
+// the status word, waits (bounded) for what it started, frees its tensor memory and returns.
+template <int PLANES>
+__global__ void __launch_bounds__(kThreads, 1)
+    dw8_kernel(const __grid_constant__ Dw8Gemm p, const __grid_constant__ Dw8Maps maps) {
+  constexpr int S = kStages<PLANES>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;  // 128-byte swizzle atoms: 1024-byte aligned
+  const uint32_t outs = base + 12 * kOperand;    // the epilogue warps' buffers
+  const uint32_t bars = outs + kEpiWarps * kOutBytes;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (kMaxStages + s); };
+  auto tfull = [&](int a) { return bars + 8u * (2 * kMaxStages + a); };
+  auto tempty = [&](int a) { return bars + 8u * (2 * kMaxStages + 2 + a); };
+  const uint32_t drain = bars + 8u * (2 * kMaxStages + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + kNumBars * 8);
+  const uint32_t rank = cluster_ctarank() & 1u;
+  const bool even = rank == 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull(a), 1);
+      mbar_init(tempty(a), 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_addr(tmem_slot), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  cluster_sync();
+  tc_fence_after_sync();
+  pdl_wait();
+  const uint32_t tmem =
+      even ? *tmem_slot : ld_shared_cluster_u32(mapa_shared(smem_addr(tmem_slot), 0));
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 0) {
+      // ---------------------------------------------------------- copy issuer
+      if (lane == 0) {
+        prefetch_tmap(&maps.dy), prefetch_tmap(&maps.x);
+        int s = 0, issued = 0;
+        uint32_t ph = 0;
+        const uint32_t full_even = even ? full(0) : mapa_shared(full(0), 0);
+        const bool wide = p.tile_n > 128;
+        const uint32_t tx = 2 * (PLANES * kOperand + (uint32_t)(p.tile_n / 2) * kBK * 2);
+        bool on = true;
+        Unit u;
+        for (int k = 0; on && unit_at(p, pair, pairs, k, u); ++k) {
+          int tm, tn;
+          tile_at(p, u.tile, tm, tn);
+          const int m0 = tm * kTile + (int)rank * 128, n0 = tn * p.tile_n + (int)rank * (p.tile_n / 2);
+          for (int kt = u.kt0; kt < u.kt1; ++kt) {
+            if ((p.debug_stop >= 0 && issued >= p.debug_stop) ||
+                !wait_phase(empty(s), ph ^ 1u, p, kStatusTimeoutEmpty)) {
+              on = false;
+              break;
+            }
+            const uint32_t st = base + s * kStageBytes<PLANES>;
+            if (even) mbar_arrive_expect_tx(full(s), tx);
+            const uint32_t fb = full_even + 8u * s;
+#pragma unroll
+            for (int i = 0; i < PLANES; ++i)
+              load_operand<true>(st + i * kOperand, &maps.dy, m0, kt, i, fb);
+            load_operand<true>(st + PLANES * kOperand, &maps.x, n0, kt, 0, fb, wide);
+            ++issued;
+            if (++s == S) s = 0, ph ^= 1u;
+          }
+        }
+        // leave only after the copies started here have landed (the odd CTA sees the MMAs
+        // release the stages they read)
+        for (int d = 0, pending = min(issued, S); d < pending; ++d) {
+          if (--s < 0) s = S - 1, ph ^= 1u;
+          if (!wait_phase(even ? full(s) : empty(s), ph, p, kStatusTimeoutDrain)) break;
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer (even CTA)
+      if (even && lane == 0) {
+        int s = 0, a = 0;
+        uint32_t ph = 0, aph = 0;
+        const uint32_t empty_odd = mapa_shared(empty(0), 1), tfull_odd = mapa_shared(tfull(0), 1);
+        const uint32_t a0 = desc_lo<true>(base), b0 = desc_lo<true>(base + PLANES * kOperand);
+        const uint32_t idesc = idesc_bf16(kTile, p.tile_n, true, true);
+        constexpr uint32_t step = kDescStep<true>;
+        bool on = true;
+        Unit u;
+        for (int k = 0; on && unit_at(p, pair, pairs, k, u); ++k) {
+          const int groups = groups_of(p, u.kt1 - u.kt0);
+          for (int g = 0; on && g < groups; ++g) {
+            if (!(on = wait_phase(tempty(a), aph ^ 1u, p, kStatusTimeoutTmem))) break;
+            tc_fence_after_sync();
+            const uint32_t d = tmem + (uint32_t)(a * kTile);
+            const int kts = min(p.group, u.kt1 - u.kt0 - g * p.group);
+            for (int it = 0; it < kts; ++it) {
+              if (!(on = wait_phase(full(s), ph, p, kStatusTimeoutFull))) break;
+              tc_fence_after_sync();
+              const uint32_t off = (uint32_t)s * (kStageBytes<PLANES> >> 4);
+#pragma unroll
+              for (int i = PLANES - 1; i >= 0; --i)
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; ++kk)
+                  mma_bf16_pair(d, a0 + off + i * (kOperand >> 4) + kk * step, b0 + off + kk * step,
+                                idesc, (it > 0 || i < PLANES - 1 || kk > 0) ? 1u : 0u);
+              mma_commit_pair(empty(s));
+              mma_commit_pair(empty_odd + 8u * s);
+              if (++s == S) s = 0, ph ^= 1u;
+            }
+            if (!on) break;
+            mma_commit_pair(tfull(a));
+            mma_commit_pair(tfull_odd + 8u * a);
+            if (++a == 2) a = 0, aph ^= 1u;
+          }
+        }
+        mma_commit_pair(drain);
+        wait_phase(drain, 0, p, kStatusTimeoutTmem);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const int span = p.tile_n / 2;  // this warp's columns
+    const uint32_t tmem_row = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * span);
+    const uint32_t buf = outs + (uint32_t)(warp - 4) * kOutBytes;
+    const uint32_t tempty_even = even ? 0u : mapa_shared(tempty(0), 0);
+    int a = 0;
+    uint32_t aph = 0;
+    Unit u;
+    for (int k = 0; unit_at(p, pair, pairs, k, u); ++k) {
+      float acc[128];
+      if (!collect(p, acc, tmem_row, span, groups_of(p, u.kt1 - u.kt0), a, aph, tfull(0), tempty(0),
+                   tempty_even, even, lane))
+        break;
+      int tm, tn;
+      tile_at(p, u.tile, tm, tn);
+      const int local_row = (int)rank * 128 + 32 * q, n0 = tn * p.tile_n + half * span;
+      put_tile(p, maps, acc, tm * kTile + local_row, local_row, n0, half * span,
+               min(span, p.cols - n0), u.slot, buf, lane);
+    }
+    if (lane == 0) stores_done();
+  }
+
+  __syncwarp();
+  tc_fence_before_sync();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after_sync();
+    tmem_dealloc_pair(*tmem_slot, kTmemCols);
+  }
+}
+
+// The remaining tiles' results: their pieces' sums, added in the order of k.
+// Block (t, y): rows 4y .. 4y + 3 of tile t.
+template <typename T>
+__global__ void __launch_bounds__(256) dw8_join_kernel(const __grid_constant__ Dw8Gemm p,
+                                                       const float* part, int pairs) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int t = blockIdx.x, row = blockIdx.y * 4 + (threadIdx.x >> 6), col = (threadIdx.x & 63) * 4;
+  int tm, tn;
+  tile_at(p, p.full * pairs + t, tm, tn);
+  const int r = tm * kTile + row, c = tn * p.tile_n + col;
+  if (r >= p.rows || c >= p.cols || col >= p.tile_n) return;
+  const long long from = (long long)t * p.k_tiles, last = (from + p.k_tiles - 1) / p.piece;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (long long i = from / p.piece; i <= last; ++i) {
+    const long long slot = 2 * i + (i * p.piece < from ? 1 : 0);
+    const float4 v = *reinterpret_cast<const float4*>(part + (slot * kTile + row) * p.tile_n + col);
+    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  }
+  T* o = static_cast<T*>(p.out) + (long long)r * p.ldo + c;
+  const float f[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (c + j < p.cols) o[j] = from_f32<T>(p.accumulate ? f[j] + to_f32(o[j]) : f[j]);
+}
+
+// ---------------------------------------------------------------- operands
+
+// x from its 8-bit form to BF16 rows of ldo elements (zeros past the width), and dy to
+// `planes` BF16 planes where it cannot be read as it is (planes == 0: it is).  Eight
+// columns a thread.
+struct Prepare {
+  int tokens;
+  Rows8 k;
+  int width, vec;
+  Bf16* x;
+  long long ldx;
   const void* dy;
   long long lddy;
-  Rows8 x;
-  int accumulate;
-  void* dw;
-  long long lddw;
+  int outs, planes;
+  Bf16* d;
+  long long ldd;
 };
 
 template <typename T>
-__global__ void __launch_bounds__(256) dw8_kernel(const __grid_constant__ Dw8 p) {
-  __shared__ float a[16][64], b[16][64];
+__global__ void __launch_bounds__(256) dw8_prepare_kernel(const __grid_constant__ Prepare p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int n0 = blockIdx.x * 64, m0 = blockIdx.y * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < p.tokens; k0 += 16) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < 1024; i += 256) {
-      const int k = i >> 6, c = i & 63;
-      const long long row = k0 + k;
-      const bool in = row < p.tokens;
-      a[k][c] = in && m0 + c < p.outs ? to_f32(static_cast<const T*>(p.dy)[row * p.lddy + m0 + c]) : 0.f;
-      float v = 0.f, none;
-      if (in && n0 + c < p.width) {
-        decode2(p.x.q[row * p.x.ldq + n0 + c], v, none);
-        v *= scale_value(p.x.s[row * p.x.lds + (n0 + c) / kScaleBlock]);
+  const long long gx = p.ldx / 8, gd = p.planes ? p.ldd / 8 : 0;
+  const long long nx = gx * p.tokens, total = nx + gd * p.tokens;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (long long)gridDim.x * 256) {
+    if (i < nx) {
+      const long long row = i / gx;
+      const int c = (int)(i - row * gx) * 8;
+      const unsigned char* q = p.k.q + row * p.k.ldq + c;
+      Codes<8> codes;
+      if (p.vec) {
+        codes.load(q);
+      } else {
+        codes.zero();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < p.width) codes.w[j >> 2] |= (uint32_t)q[j] << (8 * (j & 3));
       }
-      b[k][c] = v;
+      const float s = scale_value(p.k.s[row * p.k.lds + c / kScaleBlock]);
+      float f[8];
+      codes.get(f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= s;
+      Pack<Bf16, 8> o;
+      o.set(f);
+      o.store(p.x + row * p.ldx + c);
+    } else {
+      const long long at = i - nx, row = at / gd;
+      const int c = (int)(at - row * gd) * 8;
+      const T* y = static_cast<const T*>(p.dy) + row * p.lddy + c;
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = c + j < p.outs ? to_f32(y[j]) : 0.f;
+      for (int pl = 0; pl < p.planes; ++pl) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = p.planes == 1 ? pack_bf16(f[2 * j], f[2 * j + 1])
+                 : pl == 0     ? split_plane<true>(f[2 * j], f[2 * j + 1])
+                               : split_plane<false>(f[2 * j], f[2 * j + 1]);
+        *reinterpret_cast<uint4*>(p.d + (pl * (long long)p.tokens + row) * p.ldd + c) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[k][ty * 4 + i], b[k][tx * 4 + j], acc[i][j]);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m < p.outs && n < p.width) {
-        T* o = static_cast<T*>(p.dw) + m * p.lddw + n;
-        *o = from_f32<T>(p.accumulate ? acc[i][j] + to_f32(*o) : acc[i][j]);
-      }
-    }
 }
+
+// ----------------------------------------------------------------- host side
 
 int check(int dtype, int tokens, int outs, int width) {
   if (!type_ok(dtype)) return B2G_ERR_INVALID_TYPE;
@@ -65,6 +403,80 @@ int check(int dtype, int tokens, int outs, int width) {
       width > kMaxLength)
     return B2G_ERR_INVALID_DIM;
   return 0;
+}
+
+// How the tiles are shared out, and where the operands' copies and the sums stand in the
+// workspace.
+struct Layout {
+  int planes;
+  bool copy_dy;
+  long long ldx, ldd;
+  int tile_n, tiles_m, tiles_n, k_tiles, pairs, full, rest;
+  long long piece;
+  bool split;
+  size_t x, d, part, total;
+};
+
+// Cycles of a k tile: BF16 its copies (64 bytes a cycle and SM), FP32 its three products.
+// Leaving sums costs about 6000 more, for the launch that adds them.
+long long k_tile_cost(int planes, int tile_n) { return planes == 1 ? kTile + tile_n : 1600; }
+constexpr long long kJoinCost = 6000;
+
+// false: more tiles than can be counted.
+bool layout(int dtype, int tokens, int outs, int width, const void* dy, long long lddy, Layout& l) {
+  l.planes = dtype == B2G_F32 ? 3 : 1;
+  l.copy_dy = dtype == B2G_F32 || !vec16(dy) || lddy % 8;
+  l.ldx = (long long)round_up(width, 8), l.ldd = (long long)round_up(outs, 8);
+  l.tile_n = width > 128 ? 256 : 128;
+  l.k_tiles = (int)ceil_div(tokens, kBK);
+  l.tiles_m = (int)ceil_div(outs, kTile), l.tiles_n = (int)ceil_div(width, l.tile_n);
+  const long long tiles = (long long)l.tiles_m * l.tiles_n;
+  if (tiles > 0x3fffffffLL) return false;
+  l.full = (int)(tiles / kPairs), l.rest = (int)(tiles % kPairs);
+  const long long all = (long long)l.rest * l.k_tiles;
+  l.piece = l.k_tiles, l.split = false;
+  if (all) {
+    const long long least = ceil_div(all, kPairs);
+    if ((l.k_tiles - least) * k_tile_cost(l.planes, l.tile_n) > kJoinCost) l.piece = least, l.split = true;
+  }
+  l.pairs = l.full ? kPairs : (int)ceil_div(all, l.piece);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += round_up(bytes, 256);
+    return o;
+  };
+  l.x = take((size_t)tokens * l.ldx * 2);
+  l.d = l.copy_dy ? take((size_t)l.planes * tokens * l.ldd * 2) : 0;
+  l.part = l.split ? take((size_t)2 * ceil_div(all, l.piece) * kTile * l.tile_n * 4) : 0;
+  l.total = at;
+  return true;
+}
+
+template <int PLANES>
+int launch(const Dw8Gemm& g, const Dw8Maps& maps, int pairs, const TrainDevice& d, cudaStream_t st) {
+  static std::atomic<int> done[64];
+  if (d.dev < 0 || d.dev >= 64) return B2G_ERR_DEVICE;
+  if (!done[d.dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(dw8_kernel<PLANES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemBytes) != cudaSuccess)
+      return B2G_ERR_CUDA;
+    done[d.dev].store(1, std::memory_order_release);
+  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  void* args[] = {const_cast<Dw8Gemm*>(&g), const_cast<Dw8Maps*>(&maps)};
+  return launch_code(cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&dw8_kernel<PLANES>), args));
 }
 
 }  // namespace
@@ -80,6 +492,10 @@ int b2g_linear_dweight8_workspace_size(int dtype, int tokens, int outs, int widt
   if (rc) return rc;
   if (!bytes) return B2G_ERR_NULL;
   *bytes = 0;
+  if (!tokens || !outs || !width) return 0;
+  Layout l;
+  if (!layout(dtype, tokens, outs, width, dy, lddy, l)) return B2G_ERR_INVALID_DIM;
+  *bytes = l.total;
   return 0;
 }
 
@@ -99,13 +515,59 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
   rc = train_device(&d);
   if (rc) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  Dw8 p{tokens, outs, width, dy, lddy,
-        {static_cast<unsigned char*>(const_cast<void*>(codes)), ldq,
-         static_cast<unsigned char*>(const_cast<void*>(scales)), lds},
-        accumulate, dw, lddw};
-  const dim3 grid((unsigned)ceil_div(width, 64), (unsigned)ceil_div(outs, 64));
-  return launch_code(dtype == B2G_F32 ? launch_train(dw8_kernel<float>, grid, dim3(256), 0, st, p)
-                                      : launch_train(dw8_kernel<Bf16>, grid, dim3(256), 0, st, p));
+  const bool f32 = dtype == B2G_F32;
+  const size_t es = type_size(dtype);
+  if (tokens == 0)
+    return cudaMemset2DAsync(dw, lddw * es, 0, width * es, outs, st) == cudaSuccess ? 0 : B2G_ERR_CUDA;
+  Layout l;
+  if (!layout(dtype, tokens, outs, width, dy, lddy, l)) return B2G_ERR_INVALID_DIM;
+  if (!workspace || !vec16(workspace) || workspace_bytes < l.total) return B2G_ERR_WORKSPACE;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+
+  Prepare q = {};
+  q.tokens = tokens;
+  q.k = Rows8{static_cast<unsigned char*>(const_cast<void*>(codes)), ldq,
+              static_cast<unsigned char*>(const_cast<void*>(scales)), lds};
+  q.width = width, q.x = reinterpret_cast<Bf16*>(ws + l.x), q.ldx = l.ldx;
+  // eight codes at once: also where the last ones are past the row but inside its stride
+  q.vec = codes_vec(q.k, 8) && (width % 8 == 0);
+  q.dy = dy, q.lddy = lddy, q.outs = outs, q.planes = l.copy_dy ? l.planes : 0;
+  q.d = reinterpret_cast<Bf16*>(ws + l.d), q.ldd = l.ldd;
+  const long long blocks = ceil_div((l.ldx + (l.copy_dy ? l.ldd : 0)) / 8 * tokens, 256);
+  const dim3 grid((unsigned)(blocks < 16LL * d.sms ? blocks : 16LL * d.sms));
+  rc = launch_code(f32 ? launch_train(dw8_prepare_kernel<float>, grid, dim3(256), 0, st, q)
+                       : launch_train(dw8_prepare_kernel<Bf16>, grid, dim3(256), 0, st, q));
+  if (rc) return rc;
+
+  Dw8Gemm g = {};
+  g.rows = outs, g.cols = width;
+  g.tiles_m = l.tiles_m, g.tiles_n = l.tiles_n, g.k_tiles = l.k_tiles, g.tile_n = l.tile_n;
+  g.full = l.full, g.rest = l.rest, g.piece = l.piece, g.split = l.split;
+  g.group = f32 ? 4 : kGroupK / kBK;
+  g.wait_limit_ns = d.wait_limit_ns, g.debug_stop = d.debug_stop, g.status = d.status;
+  g.out = dw, g.ldo = lddw, g.out_bf16 = !f32, g.accumulate = accumulate != 0;
+  // a bulk-tensor store writes whole 16-byte units, those past the last column too; and it
+  // adds in the output's type: right for FP32 only
+  g.out_tma = vec16(dw) && vec16_ld(lddw, dtype) && vec16_ld(width, dtype) && !(accumulate && !f32);
+  g.add = accumulate != 0;
+  float* part = reinterpret_cast<float*>(ws + l.part);
+  Dw8Maps maps = {};
+  rc = l.copy_dy ? encode_rows(&maps.dy, false, q.d, outs, tokens, l.ldd, l.planes,
+                               (long long)tokens * l.ldd, 64)
+                 : encode_rows(&maps.dy, false, dy, outs, tokens, lddy, 1, 0, 64);
+  if (!rc) rc = encode_rows(&maps.x, false, q.x, width, tokens, l.ldx, 1, 0, 64);
+  if (!rc && g.out_tma) rc = encode_rows(&maps.out, f32, dw, width, outs, lddw, 1, 0, 32);
+  if (!rc && l.split)
+    rc = encode_rows(&maps.part, true, part, l.tile_n,
+                     2 * ceil_div((long long)l.rest * l.k_tiles, l.piece) * kTile, l.tile_n, 1, 0, 32);
+  if (rc) return rc;
+  rc = f32 ? launch<3>(g, maps, l.pairs, d, st) : launch<1>(g, maps, l.pairs, d, st);
+  if (rc || !l.split) return rc;
+  const dim3 tiles((unsigned)l.rest, kTile / 4);
+  return launch_code(f32 ? launch_train(dw8_join_kernel<float>, tiles, dim3(256), 0, st, g,
+                                        (const float*)part, l.pairs)
+                         : launch_train(dw8_join_kernel<Bf16>, tiles, dim3(256), 0, st, g,
+                                        (const float*)part, l.pairs));
 }
 
 }  // extern "C"

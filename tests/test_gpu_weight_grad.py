@@ -168,3 +168,24 @@ def test_rows_past_32_bits_of_offset(b2g):
     x = torch.ones(70000, 48, dtype=BF16, device="cuda")
     dw = b2g.linear_weight_grad_8bit(dy, *b2g.quantize_8bit(x))
     assert (dw == -2).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_bounded_waits(b2g, dtype):
+    """With the copies stopped the waits run out, the call returns and the status word says
+    so; the next call works again."""
+    dy, kept = operands(2000, 600, 520, dtype)
+    stream = torch.cuda.current_stream().cuda_stream
+    first = b2g.linear_weight_grad_8bit(dy, *kept)
+    torch.cuda.synchronize()
+    try:
+        b2g.b2g_set_wait_limit_ns(2_000_000)
+        b2g.b2g_debug_stop_after(2)
+        b2g.linear_weight_grad_8bit(dy, *kept)
+        rc, flags = b2g.b2g_status(stream)
+        assert rc == b2g.B2G_ERR_TIMEOUT and flags & 1 and flags & 8
+    finally:
+        b2g.b2g_debug_stop_after(-1)
+        b2g.b2g_set_wait_limit_ns(2_000_000_000)
+    assert torch.equal(first, b2g.linear_weight_grad_8bit(dy, *kept))
+    assert b2g.b2g_status(stream) == (0, 0)
