@@ -8,51 +8,84 @@ namespace {
 struct Convert {
   long long rows;
   int cols;
+  unsigned chunks, per;  // chunks of a row: those that exist, and with the last block filled up
   void* x;       // read by quantize, written by dequantize
   long long ldx;
   Rows8 k;
 };
 
-// A warp's lanes hold consecutive chunks of VEC columns of one row.
-template <typename T, int VEC>
+// A row counts as `per` chunks of VEC columns, whole blocks of 32 columns; a block takes
+// 256 * U consecutive chunks of the matrix, so that a scale's block is in one warp and
+// short rows fill it, and a thread has U of them on their way at a time.
+struct Place {
+  long long row;
+  unsigned c;
+};
+template <int U>
+struct Chunks {
+  long long row0;
+  unsigned c0, per;
+  __device__ __forceinline__ Chunks(unsigned per_) : per(per_) {
+    const long long first = (long long)blockIdx.x * (256 * U);
+    row0 = first / per, c0 = (unsigned)(first - row0 * per);
+  }
+  __device__ __forceinline__ Place at(int u) const {
+    const unsigned i = c0 + threadIdx.x + 256u * u, r = i / per;
+    return Place{row0 + r, i - r * per};
+  }
+};
+
+// Bound: bytes.
+template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ Convert p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int chunks = (p.cols + VEC - 1) / VEC, per = (chunks + 31) / 32;
-  const long long total = p.rows * per;
-  for (long long u = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); u < total;
-       u += (long long)gridDim.x * 8) {
-    const long long row = u / per;
-    const int c = (int)(u - row * per) * 32 + (threadIdx.x & 31);
-    Pack<T, VEC> k;
-    k.zero();
-    if (c < chunks) k.load(static_cast<const T*>(p.x) + row * p.ldx + (long long)c * VEC);
+  const Chunks<U> all(p.per);
+  Pack<T, VEC> k[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Place at = all.at(u);
+    k[u].zero();
+    if (at.row < p.rows && at.c < p.chunks)
+      k[u].load(static_cast<const T*>(p.x) + at.row * p.ldx + (long long)at.c * VEC);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Place at = all.at(u);
     float f[VEC];
-    k.get(f);
-    encode_to<VEC>(p.k, row, c, c < chunks, f);
+    k[u].get(f);
+    encode_to<VEC>(p.k, at.row, (int)at.c, at.row < p.rows && at.c < p.chunks, f);
   }
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, int U>
 __global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__ Convert p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int chunks = p.cols / VEC;
-  const long long total = p.rows * chunks;
-  for (long long u = (long long)blockIdx.x * 256 + threadIdx.x; u < total;
-       u += (long long)gridDim.x * 256) {
-    const long long row = u / chunks;
-    const int c = (int)(u - row * chunks);
-    Codes<VEC> k;
-    k.load(p.k.q + row * p.k.ldq + (long long)c * VEC);
-    const float scale = scale_value(p.k.s[row * p.k.lds + c / (kScaleBlock / VEC)]);
-    float f[VEC];
-    k.get(f);
+  const Chunks<U> all(p.per);
+  Codes<VEC> k[U];
+  uint32_t byte[U];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) f[j] *= scale;
-    Pack<T, VEC> o;
-    o.set(f);
-    o.store(static_cast<T*>(p.x) + row * p.ldx + (long long)c * VEC);
+  for (int u = 0; u < U; ++u) {
+    const Place at = all.at(u);
+    if (at.row < p.rows && at.c < p.chunks) {
+      k[u].load(p.k.q + at.row * p.k.ldq + (long long)at.c * VEC);
+      byte[u] = p.k.s[at.row * p.k.lds + at.c / (kScaleBlock / VEC)];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const Place at = all.at(u);
+    if (at.row < p.rows && at.c < p.chunks) {
+      const float scale = scale_value(byte[u]);
+      float f[VEC];
+      k[u].get(f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) f[j] *= scale;
+      Pack<T, VEC> o;
+      o.set(f);
+      o.store(static_cast<T*>(p.x) + at.row * p.ldx + (long long)at.c * VEC);
+    }
   }
 }
 
@@ -67,12 +100,14 @@ int check(int dtype, long long rows, int cols, const void* x, long long ldx, con
 }
 
 template <typename T, int VEC>
-cudaError_t launch(bool back, const Convert& p, int sms, cudaStream_t st) {
-  const long long warps = p.rows * ceil_div(ceil_div(p.cols, VEC), 32);
-  const long long blocks = ceil_div(warps, 8), most = 16LL * sms;
-  const dim3 grid((unsigned)(blocks < most ? blocks : most));
-  return launch_train(back ? dequantize_kernel<T, VEC> : quantize_kernel<T, VEC>, grid, dim3(256), 0,
-                      st, p);
+cudaError_t launch(bool back, Convert p, cudaStream_t st) {
+  constexpr int U = VEC > 1 ? 4 : 8;
+  p.chunks = (unsigned)(p.cols / VEC);
+  p.per = (unsigned)(scale_count(p.cols) * (kScaleBlock / VEC));
+  const long long blocks = ceil_div(p.rows * p.per, 256 * U);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_train(back ? dequantize_kernel<T, VEC, U> : quantize_kernel<T, VEC, U>,
+                      dim3((unsigned)blocks), dim3(256), 0, st, p);
 }
 
 int convert(bool back, int dtype, const Convert& p, void* stream) {
@@ -83,8 +118,8 @@ int convert(bool back, int dtype, const Convert& p, void* stream) {
   const bool f32 = dtype == B2G_F32;
   const bool v = vec16(p.x) && vec16_ld(p.ldx, dtype) && vec16_ld(p.cols, dtype) &&
                  codes_vec(p.k, f32 ? 4 : 8);
-  if (f32) return launch_code(v ? launch<float, 4>(back, p, d.sms, st) : launch<float, 1>(back, p, d.sms, st));
-  return launch_code(v ? launch<Bf16, 8>(back, p, d.sms, st) : launch<Bf16, 1>(back, p, d.sms, st));
+  if (f32) return launch_code(v ? launch<float, 4>(back, p, st) : launch<float, 1>(back, p, st));
+  return launch_code(v ? launch<Bf16, 8>(back, p, st) : launch<Bf16, 1>(back, p, st));
 }
 
 }  // namespace
@@ -99,7 +134,7 @@ int b2g_quantize8(int dtype, long long rows, int cols, const void* x, long long 
   const int rc = check(dtype, rows, cols, x, ldx, codes, ldq, scales, lds);
   if (rc || rows == 0 || cols == 0) return rc;
   return convert(false, dtype,
-                 Convert{rows, cols, const_cast<void*>(x), ldx,
+                 Convert{rows, cols, 0, 0, const_cast<void*>(x), ldx,
                          {static_cast<unsigned char*>(codes), ldq, static_cast<unsigned char*>(scales), lds}},
                  stream);
 }
@@ -109,7 +144,7 @@ int b2g_dequantize8(int dtype, long long rows, int cols, const void* codes, long
   const int rc = check(dtype, rows, cols, y, ldy, codes, ldq, scales, lds);
   if (rc || rows == 0 || cols == 0) return rc;
   return convert(true, dtype,
-                 Convert{rows, cols, y, ldy,
+                 Convert{rows, cols, 0, 0, y, ldy,
                          {static_cast<unsigned char*>(const_cast<void*>(codes)), ldq,
                           static_cast<unsigned char*>(const_cast<void*>(scales)), lds}},
                  stream);

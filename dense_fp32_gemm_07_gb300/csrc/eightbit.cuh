@@ -46,6 +46,16 @@ __device__ __forceinline__ void decode2(uint32_t codes, float& lo, float& hi) {
   lo = __low2float(v), hi = __high2float(v);
 }
 
+// One code as an element of a row.
+struct E4m3 {
+  unsigned char b;
+};
+__device__ __forceinline__ float to_f32(E4m3 x) {
+  float v, none;
+  decode2(x.b, v, none);
+  return v;
+}
+
 // VEC consecutive codes as loaded or stored: VEC bytes on a boundary of their size.
 template <int VEC>
 struct Codes {
@@ -100,21 +110,34 @@ struct Codes<1> {
 template <int VEC>
 __device__ __forceinline__ float block_largest(float (&f)[VEC]) {
   constexpr int lanes = kScaleBlock / VEC;
+  // as whole numbers, magnitudes stand in the same order, infinity above all finite ones
+  // and NaN above it
   auto largest = [&] {
-    float m = fabsf(f[0]);
+    uint32_t m = __float_as_uint(f[0]) & 0x7fffffffu;
 #pragma unroll
-    for (int j = 1; j < VEC; ++j) m = fmaxf(m, fabsf(f[j]));  // a NaN is passed over
+    for (int j = 1; j < VEC; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
+    if constexpr (lanes == 32) {
+      m = __reduce_max_sync(0xffffffffu, m);
+    } else {
 #pragma unroll
-    for (int o = lanes / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    return m == m ? m : 0.f;  // nothing but NaN
+      for (int o = lanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
+    return m;
   };
-  float m = largest();
-  if (__any_sync(0xffffffffu, m == INFINITY)) {
+  uint32_t m = largest();
+  if (__any_sync(0xffffffffu, m >= 0x7f800000u)) {  // rare: once more without those
+    float g[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) f[j] = fabsf(f[j]) == INFINITY ? __int_as_float(0x7fffffff) : f[j];
+    for (int j = 0; j < VEC; ++j) {
+      const bool bad = (__float_as_uint(f[j]) & 0x7fffffffu) >= 0x7f800000u;
+      g[j] = bad ? __int_as_float(0x7fffffff) : f[j];
+      f[j] = bad ? 0.f : f[j];
+    }
     m = largest();
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = g[j];
   }
-  return m;
+  return __uint_as_float(m);
 }
 
 // VEC columns of a row to their codes; the scale's byte is the same in all lanes of a block.

@@ -93,7 +93,7 @@ SHAPES = [
     (40, 1025), (9, 2048), (700, 512), (305, 2049), (610, 4096), (2, 8192), (31, 8193),
     (3, 16384), (2, 20001), (1217, 64), (5000, 96), (128, 4096), (1000, 5120),
     (700, 7), (2000, 33), (1300, 777), (900, 1025), (650, 4095), (640, 8192), (640, 8191),
-    (620, 9001), (1500, 1032), (4000, 2048),
+    (620, 9001), (1500, 1032), (4000, 2048), (9000, 40), (3000, 512), (3000, 528), (2500, 3000),
 ]
 
 
@@ -286,3 +286,29 @@ def test_rows_past_32_bits_of_offset(b2g):
     dx, dw = b2g.rms_norm_backward(x, x, torch.ones(48, device="cuda", dtype=BF16), rstd, out=out)
     assert not dx[1:-1].any() and dx[0].any() and dx[-1].any()
     close(dw, torch.full((48,), float(9 * want[0] + 4 * want[1])), 2.0 ** -8 * 10)
+
+
+@pytest.mark.parametrize("cols", [2048, 2032, 2047])
+@pytest.mark.parametrize("eight", [False, True])
+def test_bounded_waits_of_the_rings(b2g, cols, eight):
+    """With each group's copies stopped after one row the waits run out, the call returns and
+    the status word says so; the next call works again."""
+    x = torch.randn(8192, cols, device="cuda").bfloat16()
+    w = torch.randn(cols, device="cuda").bfloat16()
+    stream = torch.cuda.current_stream().cuda_stream
+    y, total, rstd = b2g.rms_norm(x, w, x)
+    kept = b2g.quantize_8bit(total) if eight else total
+    first = b2g.rms_norm_backward(y, kept, w, rstd, x)
+    torch.cuda.synchronize()
+    try:
+        b2g.b2g_set_wait_limit_ns(2_000_000)
+        b2g.b2g_debug_stop_after(1)
+        b2g.rms_norm_backward(y, kept, w, rstd, x)
+        rc, flags = b2g.b2g_status(stream)
+        assert rc == b2g.B2G_ERR_TIMEOUT and flags & 1 and flags & 4
+    finally:
+        b2g.b2g_debug_stop_after(-1)
+        b2g.b2g_set_wait_limit_ns(2_000_000_000)
+    again = b2g.rms_norm_backward(y, kept, w, rstd, x)
+    assert all(torch.equal(p, q) for p, q in zip(first, again))
+    assert b2g.b2g_status(stream) == (0, 0)
