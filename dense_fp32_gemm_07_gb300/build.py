@@ -159,7 +159,8 @@ def _link_binding(obj: str) -> None:
     lib = _torch_paths()[1]
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", PKG, "-lb2g_sgemm",
-           "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-L", lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
+           "-lc10_cuda",
            "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -5,87 +5,121 @@
 namespace b2g {
 namespace {
 
+constexpr int kPasses = 4;
+
+// Four chunks of 16 bytes of x a thread.  A warp's lanes stand in 2^lane_rows rows of consecutive
+// chunks; its four passes are 2^pass_cols of them along the rows, the others down the matrix.
+// So a scale's block is in one pass, long rows and short ones fill a warp, and places come
+// without divisions but one by the pieces of a row.
 struct Convert {
   long long rows;
   int cols;
-  unsigned chunks, per;  // chunks of a row: those that exist, and with the last block filled up
-  void* x;       // read by quantize, written by dequantize
+  int chunks;     // of a row
+  unsigned pieces;  // warps a row
+  int lane_rows, pass_cols;
+  void* x;        // read by quantize, written by dequantize
   long long ldx;
   Rows8 k;
 };
 
-// A row counts as `per` chunks of VEC columns, whole blocks of 32 columns; a block takes
-// 256 * U consecutive chunks of the matrix, so that a scale's block is in one warp and
-// short rows fill it, and a thread has U of them on their way at a time.
-struct Place {
-  long long row;
-  unsigned c;
-};
 template <int U>
-struct Chunks {
-  long long row0;
-  unsigned c0, per;
-  __device__ __forceinline__ Chunks(unsigned per_) : per(per_) {
-    const long long first = (long long)blockIdx.x * (256 * U);
-    row0 = first / per, c0 = (unsigned)(first - row0 * per);
+struct Places {
+  long long row;
+  int c, lanes, rows, mask, shift;
+  __device__ __forceinline__ Places(const Convert& p) {
+    const long long warp = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const long long line = p.pieces == 1 ? warp : warp / p.pieces;
+    const int piece = (int)(warp - line * p.pieces);
+    lanes = 32 >> p.lane_rows, rows = 1 << p.lane_rows;
+    shift = p.pass_cols, mask = (1 << shift) - 1;
+    row = line * ((U >> shift) * rows) + lane / lanes;
+    c = (piece << shift) * 32 + (lane & (lanes - 1));
   }
-  __device__ __forceinline__ Place at(int u) const {
-    const unsigned i = c0 + threadIdx.x + 256u * u, r = i / per;
-    return Place{row0 + r, i - r * per};
-  }
+  __device__ __forceinline__ long long row_of(int u) const { return row + (u >> shift) * rows; }
+  __device__ __forceinline__ int chunk_of(int u) const { return c + (u & mask) * 32; }
 };
 
 // Bound: bytes.
-template <typename T, int VEC, int U>
+template <typename T, bool ANY>
 __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ Convert p) {
+  constexpr int VEC = kVec<T>, U = kPasses, lanes = kScaleBlock / VEC;
   pdl_launch_dependents();
+  const Places<U> at(p);
   pdl_wait();
-  const Chunks<U> all(p.per);
   Pack<T, VEC> k[U];
+  Fetched raw[ANY ? U : 1];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const Place at = all.at(u);
-    k[u].zero();
-    if (at.row < p.rows && at.c < p.chunks)
-      k[u].load(static_cast<const T*>(p.x) + at.row * p.ldx + (long long)at.c * VEC);
+    const long long row = at.row_of(u);
+    const int c = at.chunk_of(u);
+    const bool in = row < p.rows && c < p.chunks;
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+    if constexpr (ANY) {
+      fetch<T>(raw[u], x, c * VEC, p.cols, in);
+    } else {
+      k[u].zero();
+      if (in) k[u].load(x + (long long)c * VEC);
+    }
   }
+  float f[U][VEC];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const Place at = all.at(u);
-    float f[VEC];
-    k[u].get(f);
-    encode_to<VEC>(p.k, at.row, (int)at.c, at.row < p.rows && at.c < p.chunks, f);
+    if constexpr (ANY) {
+      const long long row = at.row_of(u);
+      const int c = at.chunk_of(u);
+      finish<T>(k[u], raw[u], static_cast<const T*>(p.x) + row * p.ldx, c * VEC, p.cols,
+                row < p.rows && c < p.chunks);
+    }
+    k[u].get(f[u]);
+  }
+  Codes<VEC> codes[U];
+  uint32_t byte[U];
+  encode<VEC, U>(f, codes, byte);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long row = at.row_of(u);
+    const int c = at.chunk_of(u);
+    if (row < p.rows && c < p.chunks) {
+      store_codes<VEC, ANY>(codes[u], p.k, row, c, p.cols);
+      if (c % lanes == 0) p.k.s[row * p.k.lds + c / lanes] = (unsigned char)byte[u];
+    }
   }
 }
 
-template <typename T, int VEC, int U>
+template <typename T, bool ANY>
 __global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__ Convert p) {
+  constexpr int VEC = kVec<T>, U = kPasses;
   pdl_launch_dependents();
+  const Places<U> at(p);
   pdl_wait();
-  const Chunks<U> all(p.per);
   Codes<VEC> k[U];
   uint32_t byte[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const Place at = all.at(u);
-    if (at.row < p.rows && at.c < p.chunks) {
-      k[u].load(p.k.q + at.row * p.k.ldq + (long long)at.c * VEC);
-      byte[u] = p.k.s[at.row * p.k.lds + at.c / (kScaleBlock / VEC)];
+    const long long row = at.row_of(u);
+    const int c = at.chunk_of(u);
+    if (row < p.rows && c < p.chunks) {
+      load_codes<VEC, ANY>(k[u], p.k, row, c, p.cols);
+      byte[u] = p.k.s[row * p.k.lds + c / (kScaleBlock / VEC)];
     }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const Place at = all.at(u);
-    if (at.row < p.rows && at.c < p.chunks) {
+    const long long row = at.row_of(u);
+    const int c = at.chunk_of(u);
+    const bool in = row < p.rows && c < p.chunks;
+    Pack<T, VEC> o;
+    o.zero();
+    if (in) {
       const float scale = scale_value(byte[u]);
       float f[VEC];
       k[u].get(f);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) f[j] *= scale;
-      Pack<T, VEC> o;
       o.set(f);
-      o.store(static_cast<T*>(p.x) + at.row * p.ldx + (long long)at.c * VEC);
     }
+    store_chunk<T, ANY>(o, static_cast<T*>(p.x) + row * p.ldx, c, p.cols, in, at.lanes);
   }
 }
 
@@ -99,27 +133,31 @@ int check(int dtype, long long rows, int cols, const void* x, long long ldx, con
   return x && codes && scales ? 0 : B2G_ERR_NULL;
 }
 
-template <typename T, int VEC>
+template <typename T, bool ANY>
 cudaError_t launch(bool back, Convert p, cudaStream_t st) {
-  constexpr int U = VEC > 1 ? 4 : 8;
-  p.chunks = (unsigned)(p.cols / VEC);
-  p.per = (unsigned)(scale_count(p.cols) * (kScaleBlock / VEC));
-  const long long blocks = ceil_div(p.rows * p.per, 256 * U);
+  constexpr int U = kPasses, lanes = kScaleBlock / kVec<T>;
+  p.chunks = (int)ceil_div(p.cols, kVec<T>);
+  while ((32 >> p.lane_rows) / 2 >= lanes && (32 >> p.lane_rows) / 2 >= p.chunks)
+    ++p.lane_rows;  // whole scale blocks a row
+  while ((1 << p.pass_cols) < U && (32 << p.pass_cols) < p.chunks) ++p.pass_cols;
+  p.pieces = (unsigned)ceil_div(p.chunks, 32 << p.pass_cols);
+  const long long lines = ceil_div(p.rows, (long long)(U >> p.pass_cols) << p.lane_rows);
+  const long long blocks = ceil_div(lines * p.pieces, 8);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_train(back ? dequantize_kernel<T, VEC, U> : quantize_kernel<T, VEC, U>,
-                      dim3((unsigned)blocks), dim3(256), 0, st, p);
+  return launch_train(back ? dequantize_kernel<T, ANY> : quantize_kernel<T, ANY>, dim3((unsigned)blocks),
+                      dim3(256), 0, st, p);
 }
 
-int convert(bool back, int dtype, const Convert& p, void* stream) {
+int convert(bool back, int dtype, Convert p, void* stream) {
   TrainDevice d;
   const int rc = train_device(&d);
   if (rc) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = dtype == B2G_F32;
-  const bool v = vec16(p.x) && vec16_ld(p.ldx, dtype) && vec16_ld(p.cols, dtype) &&
-                 codes_vec(p.k, f32 ? 4 : 8);
-  if (f32) return launch_code(v ? launch<float, 4>(back, p, st) : launch<float, 1>(back, p, st));
-  return launch_code(v ? launch<Bf16, 8>(back, p, st) : launch<Bf16, 1>(back, p, st));
+  p.k.vec = codes_vec(p.k, f32 ? 4 : 8);
+  const bool v = vec16(p.x) && vec16_ld(p.ldx, dtype) && vec16_ld(p.cols, dtype) && p.k.vec;
+  if (f32) return launch_code(v ? launch<float, false>(back, p, st) : launch<float, true>(back, p, st));
+  return launch_code(v ? launch<Bf16, false>(back, p, st) : launch<Bf16, true>(back, p, st));
 }
 
 }  // namespace
@@ -134,8 +172,8 @@ int b2g_quantize8(int dtype, long long rows, int cols, const void* x, long long 
   const int rc = check(dtype, rows, cols, x, ldx, codes, ldq, scales, lds);
   if (rc || rows == 0 || cols == 0) return rc;
   return convert(false, dtype,
-                 Convert{rows, cols, 0, 0, const_cast<void*>(x), ldx,
-                         {static_cast<unsigned char*>(codes), ldq, static_cast<unsigned char*>(scales), lds}},
+                 Convert{rows, cols, 0, 0, 0, 0, const_cast<void*>(x), ldx,
+                         {static_cast<unsigned char*>(codes), ldq, static_cast<unsigned char*>(scales), lds, 0}},
                  stream);
 }
 
@@ -144,9 +182,9 @@ int b2g_dequantize8(int dtype, long long rows, int cols, const void* codes, long
   const int rc = check(dtype, rows, cols, y, ldy, codes, ldq, scales, lds);
   if (rc || rows == 0 || cols == 0) return rc;
   return convert(true, dtype,
-                 Convert{rows, cols, 0, 0, y, ldy,
+                 Convert{rows, cols, 0, 0, 0, 0, y, ldy,
                          {static_cast<unsigned char*>(const_cast<void*>(codes)), ldq,
-                          static_cast<unsigned char*>(const_cast<void*>(scales)), lds}},
+                          static_cast<unsigned char*>(const_cast<void*>(scales)), lds, 0}},
                  stream);
 }
 

@@ -6,7 +6,7 @@
 // powers of two, scales lose nothing when they are divided out or multiplied back, and a
 // value read back has 4 significant bits: it is exact in BF16.
 #pragma once
-#include "train_common.cuh"
+#include "anyrow.cuh"
 
 namespace b2g {
 
@@ -46,16 +46,6 @@ __device__ __forceinline__ void decode2(uint32_t codes, float& lo, float& hi) {
   lo = __low2float(v), hi = __high2float(v);
 }
 
-// One code as an element of a row.
-struct E4m3 {
-  unsigned char b;
-};
-__device__ __forceinline__ float to_f32(E4m3 x) {
-  float v, none;
-  decode2(x.b, v, none);
-  return v;
-}
-
 // VEC consecutive codes as loaded or stored: VEC bytes on a boundary of their size.
 template <int VEC>
 struct Codes {
@@ -74,6 +64,30 @@ struct Codes {
     else
       *reinterpret_cast<uint32_t*>(p) = w[0];
   }
+  // Those of [from, to), byte by byte.
+  __device__ __forceinline__ void load(const unsigned char* p, int from, int to) {
+    zero();
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (j >= from && j < to) w[j / 4] |= (uint32_t)p[j] << (8 * (j & 3));
+  }
+  __device__ __forceinline__ void store(unsigned char* p, int n) const {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (j < n) p[j] = (unsigned char)(w[j / 4] >> (8 * (j & 3)));
+  }
+  // Codes outside [from, to) become zero.
+  __device__ __forceinline__ void keep(int from, int to) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (j < from || j >= to) w[j / 4] &= ~(0xFFu << (8 * (j & 3)));
+  }
+  // From byte `off` of shared memory on 16-byte boundaries, which holds 4 more.
+  __device__ __forceinline__ void load_shared(const unsigned char* base, uint32_t off) {
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(base + (off & ~3u));
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) w[i] = __funnelshift_r(v[i], v[i + 1], 8 * (off & 3u));
+  }
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i) w[i] = 0;
@@ -91,65 +105,55 @@ struct Codes {
     }
   }
 };
-template <>
-struct Codes<1> {
-  uint32_t w;
-  __device__ __forceinline__ void load(const unsigned char* p) { w = *p; }
-  __device__ __forceinline__ void store(unsigned char* p) const { *p = (unsigned char)w; }
-  __device__ __forceinline__ void zero() { w = 0; }
-  __device__ __forceinline__ void set(const float (&f)[1]) { w = encode2(f[0], 0.f) & 0xFFu; }
-  __device__ __forceinline__ void get(float (&f)[1]) const {
-    float none;
-    decode2(w, f[0], none);
-  }
-};
-
-// The largest finite magnitude of a block whose columns the 32 / VEC lanes of an aligned
+// The largest finite magnitudes of N blocks whose columns the 32 / VEC lanes of an aligned
 // group hold, VEC each (zeros past the row).  Infinities become NaN, the code they get.
 // The whole warp takes part.
-template <int VEC>
-__device__ __forceinline__ float block_largest(float (&f)[VEC]) {
+template <int VEC, int N>
+__device__ __forceinline__ void block_largest(float (&f)[N][VEC], float (&m)[N]) {
   constexpr int lanes = kScaleBlock / VEC;
-  // as whole numbers, magnitudes stand in the same order, infinity above all finite ones
-  // and NaN above it
   auto largest = [&] {
-    uint32_t m = __float_as_uint(f[0]) & 0x7fffffffu;
 #pragma unroll
-    for (int j = 1; j < VEC; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
-    if constexpr (lanes == 32) {
-      m = __reduce_max_sync(0xffffffffu, m);
-    } else {
+    for (int i = 0; i < N; ++i) {
+      m[i] = fabsf(f[i][0]);
 #pragma unroll
-      for (int o = lanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int j = 1; j < VEC; ++j) m[i] = fmaxf(m[i], fabsf(f[i][j]));  // a NaN is passed over
     }
-    return m;
+#pragma unroll
+    for (int o = lanes / 2; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
   };
-  uint32_t m = largest();
-  if (__any_sync(0xffffffffu, m >= 0x7f800000u)) {  // rare: once more without those
-    float g[VEC];
+  largest();
+  bool fine = true;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const bool bad = (__float_as_uint(f[j]) & 0x7fffffffu) >= 0x7f800000u;
-      g[j] = bad ? __int_as_float(0x7fffffff) : f[j];
-      f[j] = bad ? 0.f : f[j];
-    }
-    m = largest();
+  for (int i = 0; i < N; ++i) fine = fine && m[i] < INFINITY;
+  if (__any_sync(0xffffffffu, !fine)) {  // rare: once more without those
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) f[j] = g[j];
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        f[i][j] = fabsf(f[i][j]) < INFINITY ? f[i][j] : __int_as_float(0x7fffffff);
+    largest();
+#pragma unroll
+    for (int i = 0; i < N; ++i) m[i] = m[i] == m[i] ? m[i] : 0.f;  // nothing but NaN
   }
-  return __uint_as_float(m);
 }
 
-// VEC columns of a row to their codes; the scale's byte is the same in all lanes of a block.
-template <int VEC>
-__device__ __forceinline__ uint32_t encode(float (&f)[VEC], Codes<VEC>& codes) {
-  const uint32_t byte = scale_byte(block_largest<VEC>(f));
-  const float inv = scale_inverse(byte);
-  float g[VEC];
+// N times VEC columns of rows to their codes; the bytes of the scales are the same in all
+// lanes of a block.
+template <int VEC, int N>
+__device__ __forceinline__ void encode(float (&f)[N][VEC], Codes<VEC> (&codes)[N], uint32_t (&byte)[N]) {
+  float m[N];
+  block_largest<VEC, N>(f, m);
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) g[j] = f[j] * inv;
-  codes.set(g);
-  return byte;
+  for (int i = 0; i < N; ++i) {
+    byte[i] = scale_byte(m[i]);
+    const float inv = scale_inverse(byte[i]);
+    float g[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) g[j] = f[i][j] * inv;
+    codes[i].set(g);
+  }
 }
 
 // Codes and scales of a matrix.
@@ -158,20 +162,44 @@ struct Rows8 {
   long long ldq;
   unsigned char* s;
   long long lds;
+  int vec;  // rows on boundaries of a chunk's codes
 };
-// Chunk c (VEC columns) of row `row`, of which `in` says whether it exists.
-template <int VEC>
-__device__ __forceinline__ void encode_to(const Rows8& to, long long row, int c, bool in,
-                                          float (&f)[VEC]) {
+// Chunk c (VEC codes) of a row.  Without ANY it is whole and on its boundary.
+template <int VEC, bool ANY>
+__device__ __forceinline__ void load_codes(Codes<VEC>& k, const Rows8& from, long long row, int c, int cols) {
+  const unsigned char* q = from.q + row * from.ldq + (long long)c * VEC;
+  if (!ANY || (from.vec && (c + 1) * VEC <= cols))
+    k.load(q);
+  else
+    k.load(q, 0, cols - c * VEC);
+}
+template <int VEC, bool ANY>
+__device__ __forceinline__ void store_codes(const Codes<VEC>& k, const Rows8& to, long long row, int c,
+                                            int cols) {
+  unsigned char* q = to.q + row * to.ldq + (long long)c * VEC;
+  if (!ANY || (to.vec && (c + 1) * VEC <= cols))
+    k.store(q);
+  else
+    k.store(q, min(VEC, cols - c * VEC));
+}
+// Chunks c, c + step, ... (VEC columns each) of row `row`, those below `chunks`.
+template <int VEC, int N, bool ANY>
+__device__ __forceinline__ void encode_to(const Rows8& to, long long row, int c, int step, int chunks,
+                                          int cols, float (&f)[N][VEC]) {
   constexpr int lanes = kScaleBlock / VEC;
-  Codes<VEC> k;
-  const uint32_t byte = encode<VEC>(f, k);
-  if (in) {
-    k.store(to.q + row * to.ldq + (long long)c * VEC);
-    if (c % lanes == 0) to.s[row * to.lds + c / lanes] = (unsigned char)byte;
+  Codes<VEC> k[N];
+  uint32_t byte[N];
+  encode<VEC, N>(f, k, byte);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int at = c + i * step;
+    if (at < chunks) {
+      store_codes<VEC, ANY>(k[i], to, row, at, cols);
+      if (at % lanes == 0) to.s[row * to.lds + at / lanes] = (unsigned char)byte[i];
+    }
   }
 }
-// Whether codes may be read and written VEC at a time (VEC a power of two).
+// Whether codes may be read and written `vec` at a time (a power of two).
 inline bool codes_vec(const Rows8& r, int vec) {
   return !r.q || (reinterpret_cast<uintptr_t>(r.q) % vec == 0 && r.ldq % vec == 0);
 }

@@ -138,21 +138,23 @@ inline int row_threads(int chunks, int per, int least) {
 
 // The ring of a block of `threads` for rows of `cols` columns in slots of `slot` bytes,
 // `per` columns a thread, leaving `reserved` bytes; stages < 2 when they do not fit.
-inline Ring ring_of(int threads, int per, int cols, size_t slot, size_t reserved) {
+inline Ring ring_of(int threads, int per, int cols, size_t slot, size_t reserved,
+                    size_t bytes = kRingBytes) {
   Ring r{32, 0, 0};
   while (r.nt < threads && r.nt * per < cols) r.nt *= 2;
   r.groups = threads / r.nt;
-  if (r.nt * per < cols || reserved >= kRingBytes) return r;
-  const size_t s = (kRingBytes - reserved) / (slot * r.groups);
+  if (r.nt * per < cols || reserved >= bytes) return r;
+  const size_t s = (bytes - reserved) / (slot * r.groups);
   r.stages = (int)(s < (size_t)kRingStages ? s : (size_t)kRingStages);
   return r;
 }
 // Opt in to the ring's shared memory, once per device and kernel.
-inline cudaError_t allow_ring(const void* kern, std::atomic<int> (&done)[64], int dev) {
+inline cudaError_t allow_ring(const void* kern, std::atomic<int> (&done)[64], int dev,
+                              int bytes = kRingBytes) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
   const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess) done[dev].store(1, std::memory_order_release);
   return e;
 }

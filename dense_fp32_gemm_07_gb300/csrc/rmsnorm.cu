@@ -24,7 +24,7 @@ namespace {
 
 struct RmsFwd {
   long long rows;
-  int cols, chunks;  // chunks = cols / VEC
+  int cols, chunks;  // chunks of 16 bytes of a row, the last one perhaps cut short
   const void* x;
   long long ldx;
   const void* res;
@@ -39,63 +39,93 @@ struct RmsFwd {
   float* rstd;
 };
 
+// total of one chunk of x and of the residual, rounded, and its values.
+template <typename T>
+__device__ __forceinline__ void add_residual(Pack<T, kVec<T>>& x, const Pack<T, kVec<T>>& res,
+                                             float (&f)[kVec<T>]) {
+  float g[kVec<T>];
+  x.get(f), res.get(g);
+#pragma unroll
+  for (int j = 0; j < kVec<T>; ++j) f[j] += g[j];
+  x.set(f);
+  x.get(f);
+}
+
+// How a call's rows stand in memory (anyrow.cuh): on 16-byte boundaries; all of its
+// matrices' at the same places within a 16-byte unit; anyhow.
+enum Rows { kAligned, kPhase, kAny };
+
 // One row per blockDim.x threads (from 8 lanes of a warp up; threadIdx.y picks the row of
-// a block that has several), NCH chunks of VEC columns a thread.
-template <typename T, int VEC, int NCH>
-__global__ void __launch_bounds__(512) rms_fwd_kernel(const __grid_constant__ RmsFwd p) {
+// a block that has several), NCH chunks a thread, the weights fetched with the row.
+template <typename T, int NCH, Rows ROWS>
+__global__ void __launch_bounds__(kMaxRowThreads) rms_fwd_kernel(const __grid_constant__ RmsFwd p) {
+  constexpr int VEC = kVec<T>;
+  constexpr bool ANY = ROWS != kAligned;
   __shared__ float red[32];
   pdl_launch_dependents();
   pdl_wait();
   const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   const bool live = row < p.rows;  // the others of the warp take part in its sums
-  const int t = threadIdx.x, nt = blockDim.x, chunks = live ? p.chunks : 0;
-  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-  const T* r = static_cast<const T*>(p.res) + row * p.ldr;
+  const int t = threadIdx.x, nt = blockDim.x, seg = nt < 32 ? nt : 32;
   const T* w = static_cast<const T*>(p.w);
+  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+  const T* res = static_cast<const T*>(p.res) + row * p.ldr;
+  const int pad = ROWS == kPhase ? (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T)) : 0;
+  const int chunks = live ? ROWS == kPhase ? (p.cols + pad + VEC - 1) / VEC : p.chunks : 0;
+  const int e0 = t * VEC - pad, step = nt * VEC;
+  auto in = [&](int i) { return t + i * nt < chunks; };
   Pack<T, VEC> raw[NCH], add[NCH], wr[NCH];
-#pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int c = t + i * nt;
-    raw[i].zero(), add[i].zero(), wr[i].zero();
-    if (c < chunks) {
-      raw[i].load(x + c * VEC);
-      if (p.res) add[i].load(r + c * VEC);
-      if (w) wr[i].load(w + c * VEC);
-    }
+  if constexpr (ROWS == kPhase) {
+    start_at<T>(raw, x, e0, step, p.cols, in);
+    if (p.res) start_at<T>(add, res, e0, step, p.cols, in);
+    ends_at<T>(raw, x, e0, step, p.cols, in);
+    if (p.res) ends_at<T>(add, res, e0, step, p.cols, in);
+  } else {
+    Fetched fx[ANY ? NCH : 1], fr[ANY ? NCH : 1];
+    load_chunks<T, ANY>(raw, fx, x, e0, step, p.cols, in);
+    if (p.res) load_chunks<T, ANY>(add, fr, res, e0, step, p.cols, in);
+    finish_chunks<T, ANY>(raw, fx, x, e0, step, p.cols, in);
+    if (p.res) finish_chunks<T, ANY>(add, fr, res, e0, step, p.cols, in);
   }
+  {
+    Fetched fw[ANY ? NCH : 1];
+    if (w) load_chunks<T, ANY>(wr, fw, w, e0, step, p.cols, in);
+    if (w) finish_chunks<T, ANY>(wr, fw, w, e0, step, p.cols, in);
+  }
+  auto put = [&](void* to, long long ld, const Pack<T, VEC>& k, int i) {
+    T* o = static_cast<T*>(to) + row * ld;
+    if constexpr (ROWS == kPhase) {
+      if (in(i)) store_at<T>(k, o, e0 + i * step, p.cols);
+    } else {
+      store_chunk<T, ANY>(k, o, t + i * nt, p.cols, in(i), seg);
+    }
+  };
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int c = t + i * nt;
-    float f[VEC];
-    raw[i].get(f);
-    if (p.res) {
-      float g[VEC];
-      add[i].get(g);
+    float f[1][VEC];
+    if (p.res)
+      add_residual<T>(raw[i], add[i], f[0]);
+    else
+      raw[i].get(f[0]);
+    if (p.total) put(p.total, p.ldt, raw[i], i);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) f[j] += g[j];
-      raw[i].set(f);
-      raw[i].get(f);
-    }
-    if (p.total && c < chunks) raw[i].store(static_cast<T*>(p.total) + row * p.ldt + c * VEC);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) sum = fmaf(f[j], f[j], sum);
-    if (p.t8.q) encode_to<VEC>(p.t8, row, c, c < chunks, f);
+    for (int j = 0; j < VEC; ++j) sum = fmaf(f[0][j], f[0][j], sum);
+    if (ROWS != kPhase && p.t8.q) encode_to<VEC, 1, ANY>(p.t8, row, t + i * nt, 0, chunks, p.cols, f);
   }
   const float rstd = 1.f / sqrtf(row_sum(sum, red, nt) / (float)p.cols + p.eps);
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int c = t + i * nt;
-    float f[VEC], wf[VEC];
-    raw[i].get(f), wr[i].get(wf);
+    float f[1][VEC], wf[VEC];
+    raw[i].get(f[0]), wr[i].get(wf);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) f[j] = f[j] * (w ? wf[j] : 1.f) * rstd;  // BF16: one rounding
-    if (p.y && c < chunks) {
+    for (int j = 0; j < VEC; ++j) f[0][j] = f[0][j] * (w ? wf[j] : 1.f) * rstd;  // BF16: one rounding
+    if (p.y) {
       Pack<T, VEC> o;
-      o.set(f);
-      o.store(static_cast<T*>(p.y) + row * p.ldy + c * VEC);
+      o.set(f[0]);
+      put(p.y, p.ldy, o, i);
     }
-    if (p.y8.q) encode_to<VEC>(p.y8, row, c, c < chunks, f);
+    if (ROWS != kPhase && p.y8.q) encode_to<VEC, 1, ANY>(p.y8, row, t + i * nt, 0, chunks, p.cols, f);
   }
   if (t == 0 && live && p.rstd) p.rstd[row] = rstd;
 }
@@ -103,35 +133,50 @@ __global__ void __launch_bounds__(512) rms_fwd_kernel(const __grid_constant__ Rm
 // Rows wider than the registers of a block: two passes, the second one from the caches.
 template <typename T>
 __global__ void __launch_bounds__(1024) rms_fwd_wide_kernel(const __grid_constant__ RmsFwd p) {
+  constexpr int VEC = kVec<T>;
   __shared__ float red[32];
   pdl_launch_dependents();
   pdl_wait();
   const long long row = blockIdx.x;
-  const T* x = static_cast<const T*>(p.x) + row * p.ldx;
-  const T* r = static_cast<const T*>(p.res) + row * p.ldr;
   const T* w = static_cast<const T*>(p.w);
-  auto at = [&](int c) {
-    return p.res ? to_f32(from_f32<T>(to_f32(x[c]) + to_f32(r[c]))) : to_f32(x[c]);
+  auto load = [&](int c, Pack<T, VEC>& k, float (&f)[1][VEC]) {
+    k.zero();
+    if (c < p.chunks) load_chunk<T, true>(k, static_cast<const T*>(p.x) + row * p.ldx, c, p.cols);
+    if (p.res) {
+      Pack<T, VEC> r;
+      r.zero();
+      if (c < p.chunks) load_chunk<T, true>(r, static_cast<const T*>(p.res) + row * p.ldr, c, p.cols);
+      add_residual<T>(k, r, f[0]);
+    } else {
+      k.get(f[0]);
+    }
   };
-  float sum = 0.f;
-  for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
-    const float v = at(c);
-    sum = fmaf(v, v, sum);
+  Pack<T, VEC> k;
+  float f[1][VEC], sum = 0.f;
+  for (int c = threadIdx.x; c < p.chunks; c += blockDim.x) {
+    load(c, k, f);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) sum = fmaf(f[0][j], f[0][j], sum);
   }
   const float rstd = 1.f / sqrtf(block_sum(sum, red, blockDim.x >> 5) / (float)p.cols + p.eps);
-  // whole blocks of 32 columns, for the scales
-  const int end = (int)(scale_count(p.cols) * kScaleBlock);
-  for (int c = threadIdx.x; c < end; c += blockDim.x) {
-    const bool in = c < p.cols;
-    float f[1] = {in ? at(c) : 0.f};
-    const float v = f[0] * (w && in ? to_f32(w[c]) : 1.f) * rstd;
-    if (in) {
-      if (p.total) static_cast<T*>(p.total)[row * p.ldt + c] = from_f32<T>(f[0]);
-      if (p.y) static_cast<T*>(p.y)[row * p.ldy + c] = from_f32<T>(v);
+  for (int c0 = 0; c0 < p.chunks; c0 += blockDim.x) {  // whole warps, for the scales
+    const int c = c0 + threadIdx.x;
+    load(c, k, f);
+    if (p.total) store_chunk<T, true>(k, static_cast<T*>(p.total) + row * p.ldt, c, p.cols, c < p.chunks, 32);
+    if (p.t8.q) {
+      encode_to<VEC, 1, true>(p.t8, row, c, 0, p.chunks, p.cols, f);
+      k.get(f[0]);
     }
-    if (p.t8.q) encode_to<1>(p.t8, row, c, in, f);
-    f[0] = v;
-    if (p.y8.q) encode_to<1>(p.y8, row, c, in, f);
+    Pack<T, VEC> o;
+    float wf[VEC];
+    o.zero();
+    if (w && c < p.chunks) load_chunk<T, true>(o, w, c, p.cols);
+    o.get(wf);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[0][j] = f[0][j] * (w ? wf[j] : 1.f) * rstd;
+    o.set(f[0]);
+    if (p.y) store_chunk<T, true>(o, static_cast<T*>(p.y) + row * p.ldy, c, p.cols, c < p.chunks, 32);
+    if (p.y8.q) encode_to<VEC, 1, true>(p.y8, row, c, 0, p.chunks, p.cols, f);
   }
   if (threadIdx.x == 0 && p.rstd) p.rstd[row] = rstd;
 }
@@ -157,20 +202,23 @@ struct RmsBwd {
 };
 
 constexpr int kBwdThreads = 512;  // 16 columns a thread
+// Rows off the 16-byte boundaries: 24 columns a thread and a third more registers, which their
+// ends take.
+constexpr int kPhaseThreads = 384, kPhaseCols = 24;
 
-// VEC columns of a row of t, from the type or from 8 bits.
-template <typename T, int VEC, bool Q8>
-__device__ __forceinline__ void load_t(const RmsBwd& p, long long row, int c, float (&f)[VEC]) {
+// Chunk c of the kept rows, from the type or from 8 bits.
+template <typename T, bool Q8, bool ANY>
+__device__ __forceinline__ void load_kept(const RmsBwd& p, long long row, int c, float (&f)[kVec<T>]) {
   if constexpr (Q8) {
-    Codes<VEC> k;
-    k.load(p.k8.q + row * p.k8.ldq + (long long)c * VEC);
-    const float s = scale_value(p.k8.s[row * p.k8.lds + c / (kScaleBlock / VEC)]);
+    Codes<kVec<T>> k;
+    load_codes<kVec<T>, ANY>(k, p.k8, row, c, p.cols);
+    const float s = scale_value(p.k8.s[row * p.k8.lds + c / (kScaleBlock / kVec<T>)]);
     k.get(f);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) f[j] *= s;
+    for (int j = 0; j < kVec<T>; ++j) f[j] *= s;
   } else {
-    Pack<T, VEC> k;
-    k.load(static_cast<const T*>(p.x) + row * p.ldx + (long long)c * VEC);
+    Pack<T, kVec<T>> k;
+    load_chunk<T, ANY>(k, static_cast<const T*>(p.x) + row * p.ldx, c, p.cols);
     k.get(f);
   }
 }
@@ -179,7 +227,7 @@ __device__ __forceinline__ void load_t(const RmsBwd& p, long long row, int c, fl
 // added in group order.
 template <typename T>
 __device__ __forceinline__ void leave_sums(const RmsBwd& p, const float* sums, int groups) {
-  for (int c = threadIdx.x; c < p.cols; c += kBwdThreads) {
+  for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
     float a = sums[c];
     for (int i = 1; i < groups; ++i) a += sums[(size_t)i * p.cols + c];
     if (gridDim.x == 1)
@@ -189,14 +237,14 @@ __device__ __forceinline__ void leave_sums(const RmsBwd& p, const float* sums, i
   }
 }
 
-// Few or short rows, on 16-byte boundaries: groups of nt threads (from 4 lanes of a warp
-// up) with a row each, 16 columns a thread, all of whose loads are on their way together.
-template <typename T, int VEC, bool Q8>
+// Few or short rows: groups of nt threads (from 4 lanes of a warp up) with a row each, 16
+// columns a thread, all of whose loads are on their way together.
+template <typename T, bool Q8, bool ANY>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     rms_bwd_kernel(const __grid_constant__ RmsBwd p, int nt, int groups) {
   extern __shared__ __align__(16) float sums[];  // [groups][cols], at the end
   __shared__ float red[2][16];
-  constexpr int NCH = 16 / VEC;
+  constexpr int VEC = kVec<T>, NCH = 16 / VEC;
   pdl_launch_dependents();
   pdl_wait();
   const int group = threadIdx.x / nt, t = threadIdx.x - group * nt;
@@ -210,7 +258,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) aw[i][j] = 0.f;
     wr[i].zero();
-    if (w && c < p.chunks) wr[i].load(w + c * VEC);
+    if (!ANY && w && c < p.chunks) wr[i].load(w + c * VEC);
   }
   int turn = 0;
   // every group makes as many rounds: the lanes of a warp take part in one another's sums
@@ -221,26 +269,52 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     Pack<T, VEC> dy[NCH], x[NCH], dt[NCH];
     Codes<VEC> q[NCH];
     uint32_t byte[NCH];
+    const T* rd = static_cast<const T*>(p.dy) + row * p.lddy;
+    const T* rx = static_cast<const T*>(p.x) + row * p.ldx;
+    const T* rt = static_cast<const T*>(p.dtotal) + row * p.lddt;
+    const int e0 = t * VEC, step = nt * VEC;
+    auto in = [&](int i) { return t + i * nt < chunks; };
+    // with ANY two chunks at a time: the vectors on their way take twice the registers
+    auto load = [&](Pack<T, VEC>(&k)[NCH], const T* from) {
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = t + i * nt;
-      dy[i].zero(), x[i].zero(), dt[i].zero(), q[i].zero(), byte[i] = 127;
-      if (c < chunks) {
-        dy[i].load(static_cast<const T*>(p.dy) + row * p.lddy + (long long)c * VEC);
-        if constexpr (Q8) {
-          q[i].load(p.k8.q + row * p.k8.ldq + (long long)c * VEC);
-          byte[i] = p.k8.s[row * p.k8.lds + c / (kScaleBlock / VEC)];
+      for (int i = 0; i < NCH; i += 2) {
+        if constexpr (ANY) {
+          Fetched f[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) fetch<T>(f[j], from, e0 + (i + j) * step, p.cols, in(i + j));
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            finish<T>(k[i + j], f[j], from, e0 + (i + j) * step, p.cols, in(i + j));
         } else {
-          x[i].load(static_cast<const T*>(p.x) + row * p.ldx + (long long)c * VEC);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            k[i + j].zero();
+            if (in(i + j)) k[i + j].load(from + e0 + (i + j) * step);
+          }
         }
-        if (p.dtotal) dt[i].load(static_cast<const T*>(p.dtotal) + row * p.lddt + (long long)c * VEC);
       }
+    };
+    load(dy, rd);
+    if constexpr (Q8) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        const int c = t + i * nt;
+        q[i].zero(), byte[i] = 127;
+        if (c < chunks) {
+          load_codes<VEC, ANY>(q[i], p.k8, row, c, p.cols);
+          byte[i] = p.k8.s[row * p.k8.lds + c / (kScaleBlock / VEC)];
+        }
+        if (ANY) asm volatile("" ::: "memory");  // one after another, for the registers
+      }
+    } else {
+      load(x, rx);
     }
+    if (!ANY && p.dtotal) load(dt, rt);
+    if (ANY && w) load(wr, w);
     float xh[NCH][VEC], g[NCH][VEC], along = 0.f;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       float wf[VEC];
-      float scale = rstd;
       if constexpr (Q8) {
         q[i].get(xh[i]);
         const float s = scale_value(byte[i]);
@@ -252,7 +326,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       dy[i].get(g[i]), wr[i].get(wf);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        xh[i][j] *= scale;
+        xh[i][j] *= rstd;
         aw[i][j] = fmaf(g[i][j], xh[i][j], aw[i][j]);
         if (w) g[i][j] *= wf[j];
         along = fmaf(g[i][j], xh[i][j], along);
@@ -260,212 +334,76 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     const float mean = (nt < 32 ? row_sum(along, nullptr, nt) : group_sum(along, red[turn], group, nt)) * inv;
     turn ^= 1;
+    if (ANY && p.dtotal) load(dt, rt);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int c = t + i * nt;
       float d[VEC];
+      if (!p.dtotal) dt[i].zero();
       dt[i].get(d);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) d[j] = fmaf(rstd, fmaf(-xh[i][j], mean, g[i][j]), d[j]);
-      if (c < chunks) {
-        Pack<T, VEC> k;
-        k.set(d);
-        k.store(static_cast<T*>(p.dx) + row * p.lddx + (long long)c * VEC);
-      }
+      Pack<T, VEC> k;
+      k.set(d);
+      store_chunk<T, ANY>(k, static_cast<T*>(p.dx) + row * p.lddx, c, p.cols, c < chunks, nt < 32 ? nt : 32);
     }
   }
   if (!p.dw) return;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int c = t + i * nt;
-    if (c < p.chunks) {
+    const int c = (t + i * nt) * VEC;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) sums[(size_t)group * p.cols + c * VEC + j] = aw[i][j];
-    }
+    for (int j = 0; j < VEC; ++j)
+      if (c + j < p.cols) sums[(size_t)group * p.cols + c + j] = aw[i][j];
   }
   __syncthreads();
   leave_sums<T>(p, sums, groups);
 }
 
-// Bytes of a slot's part for one row of the kept rows.
-template <typename T, bool Q8>
-__host__ __device__ constexpr int kept_bytes(int cols) {
-  return cols * (Q8 ? 1 : (int)sizeof(T));
+// Bytes of a ring's slot that one row of `cols` elements of `es` bytes takes: with PHASE, in
+// the 16-byte units that it lies across, and one before them.
+template <bool PHASE>
+__host__ __device__ constexpr uint32_t row_slot(int cols, int es) {
+  return PHASE ? (uint32_t)((cols * es + 15) / 16 * 16 + 32) : (uint32_t)(cols * es);
 }
 
-// Many rows on 16-byte boundaries: a ring (ring.cuh) of the rows of dy, of the kept rows and
-// of dtotal together, 16 columns a thread (FULL: every thread has all of them); the scales
-// of 8-bit rows are fetched a row ahead.
-template <typename T, int VEC, bool FULL, bool Q8>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+// The 16-byte units that a row lies across, and whether they are all of the matrix (not at its
+// very ends).
+struct RowUnits {
+  const unsigned char* from;
+  uint32_t bytes;
+  bool inside;
+  __device__ __forceinline__ RowUnits(const void* base, long long row, long long ld, long long rows, int cols,
+                                      int es) {
+    const uintptr_t first = reinterpret_cast<uintptr_t>(base), start = first + row * ld * es;
+    const uintptr_t end = start + (uintptr_t)cols * es, last = first + ((rows - 1) * ld + cols) * es;
+    const uintptr_t a = start & ~(uintptr_t)15, b = (end + 15) & ~(uintptr_t)15;
+    from = reinterpret_cast<const unsigned char*>(a), bytes = (uint32_t)(b - a);
+    inside = a >= first && b <= last;
+  }
+};
+
+// Many rows: a ring (ring.cuh) of the rows of dy, of the kept rows and of dtotal together, 16
+// columns a thread; the scales of 8-bit rows are fetched a row ahead.  FULL: every thread has
+// all of its columns.
+// PHASE: rows off the 16-byte boundaries, all at the same place within a 16-byte unit (8-bit
+// rows on the boundaries).  The step from row to row of a group is a multiple of 16 bytes, so
+// that the place, and with it a thread's columns, stays; the slots hold whole units.  The
+// first and last rows, whose units may begin before the matrix or end after it, are read where
+// they are.
+template <typename T, bool FULL, bool Q8, bool PHASE>
+__global__ void __launch_bounds__(PHASE ? kPhaseThreads : kBwdThreads, 1)
     rms_bwd_ring_kernel(const __grid_constant__ RmsBwd p, const __grid_constant__ Ring g,
                         const __grid_constant__ RingWait wait) {
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ __align__(8) unsigned long long bars[kBwdThreads / 32 * kRingStages];
   __shared__ float red[2][16];
-  constexpr int H = VEC / 2, NCH = 16 / VEC;
+  constexpr int VEC = kVec<T>, H = VEC / 2, NCH = (PHASE ? kPhaseCols : 16) / VEC, ES = (int)sizeof(T);
+  constexpr int KS = Q8 ? 1 : ES;
+  constexpr uint32_t kBefore = PHASE ? 16 : 0;  // where a row's units begin in its part of a slot
   pdl_launch_dependents();
   const int group = threadIdx.x / g.nt, t = threadIdx.x - group * g.nt;
-  const uint32_t bytes = (uint32_t)(p.cols * (int)sizeof(T)), kept = (uint32_t)kept_bytes<T, Q8>(p.cols);
-  const uint32_t slot = kept + bytes * (p.dtotal ? 2 : 1);
-  const uint32_t bar0 = smem_addr(bars) + 8u * (uint32_t)(group * kRingStages);
-  unsigned char* mine = ring + (size_t)group * g.stages * slot;
-  if (t == 0) {
-    for (int s = 0; s < g.stages; ++s) mbar_init(bar0 + 8u * s, 1);
-    fence_mbar_init();
-    fence_proxy_async_smem();
-  }
-  __syncthreads();
-  pdl_wait();
-  const float inv = 1.f / (float)p.cols;
-  const long long step = (long long)gridDim.x * g.groups;
-  const long long row0 = (long long)group * gridDim.x + blockIdx.x;
-  auto issue = [&](long long row, int s) {
-    if (wait.debug_stop >= 0 && (row - row0) / step >= wait.debug_stop) return;
-    const uint32_t bar = bar0 + 8u * s, dst = smem_addr(mine + (size_t)s * slot);
-    mbar_arrive_expect_tx(bar, slot);
-    bulk_load(dst, static_cast<const T*>(p.dy) + row * p.lddy, bytes, bar);
-    if constexpr (Q8)
-      bulk_load(dst + bytes, p.k8.q + row * p.k8.ldq, kept, bar);
-    else
-      bulk_load(dst + bytes, static_cast<const T*>(p.x) + row * p.ldx, kept, bar);
-    if (p.dtotal)
-      bulk_load(dst + bytes + kept, static_cast<const T*>(p.dtotal) + row * p.lddt, bytes, bar);
-  };
-  if (t == 0) {
-    long long row = row0;
-    for (int s = 0; s < g.stages && row < p.rows; ++s, row += step) issue(row, s);
-  }
-  F2 aw[NCH][H], wf[NCH][H];
-#pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int c = t + i * g.nt;
-#pragma unroll
-    for (int j = 0; j < H; ++j) aw[i][j] = f2(0.f, 0.f), wf[i][j] = f2(1.f, 1.f);
-    if (p.w && c < p.chunks) {
-      Pack<T, VEC> k;
-      k.load(static_cast<const T*>(p.w) + c * VEC);
-      k.get2(wf[i]);
-    }
-  }
-  float rstd = 0.f;
-  uint32_t byte[NCH];
-  auto ahead = [&](long long row) {  // what is fetched past the ring
-    rstd = p.rstd[row];
-    if constexpr (Q8) {
-#pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        const int c = t + i * g.nt;
-        byte[i] = FULL || c < p.chunks ? p.k8.s[row * p.k8.lds + c / (kScaleBlock / VEC)] : 127;
-      }
-    }
-  };
-  if (row0 < p.rows) ahead(row0);
-  RingPos at;
-  int turn = 0;
-  bool alive = true;  // false once a wait has run out: no more waits, no more copies
-  for (long long row = row0; row < p.rows; row += step) {
-    const float r = rstd;
-    const F2 r2 = f2(r, r);
-    F2 scale[NCH];
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      if constexpr (Q8) {
-        const float s = scale_value(byte[i]);
-        scale[i] = f2(s, s);
-      }
-    }
-    if (row + step < p.rows) ahead(row + step);
-    if (alive) alive = wait_row(bar0, at, g.stages, row, step, p.rows, t == 0, wait);
-    const unsigned char* here = mine + (size_t)at.s * slot;
-    F2 xh[NCH][H], gr[NCH][H];  // xhat, and g = dy weight
-    Pack<T, VEC> past[NCH];
-    F2 s0 = f2(0.f, 0.f), s1 = f2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = t + i * g.nt;
-      past[i].zero();
-      if (FULL || c < p.chunks) {
-        Pack<T, VEC> k;
-        F2 d[H];
-        k.load(reinterpret_cast<const T*>(here) + c * VEC);
-        k.get2(d);
-        if constexpr (Q8) {
-          Codes<VEC> q;
-          float f[VEC];
-          q.load(here + bytes + c * VEC);
-          q.get(f);
-#pragma unroll
-          for (int j = 0; j < H; ++j) xh[i][j] = mul2(f2(f[2 * j], f[2 * j + 1]), scale[i]);
-        } else {
-          k.load(reinterpret_cast<const T*>(here + bytes) + c * VEC);
-          k.get2(xh[i]);
-        }
-        if (p.dtotal) past[i].load(reinterpret_cast<const T*>(here + bytes + kept) + c * VEC);
-#pragma unroll
-        for (int j = 0; j < H; ++j) {
-          xh[i][j] = mul2(xh[i][j], r2);
-          gr[i][j] = mul2(d[j], wf[i][j]);
-          aw[i][j] = fma2(d[j], xh[i][j], aw[i][j]);
-          if (j & 1)
-            s1 = fma2(gr[i][j], xh[i][j], s1);
-          else
-            s0 = fma2(gr[i][j], xh[i][j], s0);
-        }
-      }
-    }
-    const float mean = group_sum(f2_sum(add2(s0, s1)), red[turn], group, g.nt) * inv;
-    if (t == 0 && alive && row + (long long)g.stages * step < p.rows)
-      issue(row + (long long)g.stages * step, at.s);
-    const F2 minus = f2(-mean, -mean);
-    T* dx = static_cast<T*>(p.dx) + row * p.lddx;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = t + i * g.nt;
-      if (FULL || c < p.chunks) {
-        F2 d[H];
-        past[i].get2(d);
-#pragma unroll
-        for (int j = 0; j < H; ++j) d[j] = fma2(r2, fma2(xh[i][j], minus, gr[i][j]), d[j]);
-        Pack<T, VEC> k;
-        k.set2(d);
-        k.store(dx + c * VEC);
-      }
-    }
-    turn ^= 1;
-    at.next(g.stages);
-  }
-  if (!p.dw) return;
-  __syncthreads();  // no ring has a copy on its way: its memory now takes the groups' sums
-  float* sums = reinterpret_cast<float*>(ring);
-#pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int c = t + i * g.nt;
-    if (FULL || c < p.chunks) {
-#pragma unroll
-      for (int j = 0; j < H; ++j)
-        reinterpret_cast<F2*>(sums + (size_t)group * p.cols + c * VEC)[j] = aw[i][j];
-    }
-  }
-  __syncthreads();
-  leave_sums<T>(p, sums, g.groups);
-}
-
-// The same for rows off the 16-byte boundaries, each thread with the 16 columns t + i * nt
-// and the weights in shared memory.  A block of 32 columns is a warp's; its scales are
-// fetched a row ahead, lane i that of column t + i * nt.
-template <typename T, bool Q8>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-    rms_bwd_any_kernel(const __grid_constant__ RmsBwd p, const __grid_constant__ Ring g,
-                       const __grid_constant__ RingWait wait) {
-  using K = std::conditional_t<Q8, E4m3, T>;
-  extern __shared__ __align__(128) unsigned char ring[];
-  __shared__ __align__(8) unsigned long long bars[kBwdThreads / 32 * kRingStages];
-  __shared__ float red[2][16];
-  constexpr int N = 16;
-  pdl_launch_dependents();
-  const int group = threadIdx.x / g.nt, t = threadIdx.x - group * g.nt, lane = threadIdx.x & 31;
-  const uint32_t dslot = (uint32_t)any_slot(p.cols, sizeof(T)), kslot = (uint32_t)any_slot(p.cols, sizeof(K));
+  const uint32_t dslot = row_slot<PHASE>(p.cols, ES), kslot = row_slot<PHASE>(p.cols, KS);
   const uint32_t slot = kslot + dslot * (p.dtotal ? 2 : 1);
   const uint32_t bar0 = smem_addr(bars) + 8u * (uint32_t)(group * kRingStages);
   unsigned char* mine = ring + (size_t)group * g.stages * slot;
@@ -479,113 +417,206 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const float inv = 1.f / (float)p.cols;
   const long long step = (long long)gridDim.x * g.groups;
   const long long row0 = (long long)group * gridDim.x + blockIdx.x;
-  auto d_row = [&](long long row) {
-    return AnyRow<T>(static_cast<const T*>(p.dy) + row * p.lddy, p.cols);
+  const T* dy0 = static_cast<const T*>(p.dy) + row0 * p.lddy;
+  const int pad = PHASE ? (int)((reinterpret_cast<uintptr_t>(dy0) & 15u) / ES) : 0;
+  const int chunks = PHASE ? (p.cols + pad + VEC - 1) / VEC : p.chunks;
+  // A chunk's first column; of 8-bit rows computed anew each time with PHASE, as keeping what depends on it
+  // for all rows would spill.
+  auto first_of = [&](int i) {
+    int c = t + i * g.nt;
+    if (PHASE && Q8) asm volatile("" : "+r"(c));
+    return c * VEC - pad;
   };
-  auto k_row = [&](long long row) {
-    if constexpr (Q8)
-      return AnyRow<K>(reinterpret_cast<const E4m3*>(p.k8.q) + row * p.k8.ldq, p.cols);
-    else
-      return AnyRow<K>(static_cast<const T*>(p.x) + row * p.ldx, p.cols);
-  };
-  auto p_row = [&](long long row) {
-    return AnyRow<T>(static_cast<const T*>(p.dtotal) + row * p.lddt, p.cols);
-  };
+  const void* kept = Q8 ? p.k8.q : p.x;
+  const long long ldk = Q8 ? p.k8.ldq : p.ldx;
   auto issue = [&](long long row, int s) {
     if (wait.debug_stop >= 0 && (row - row0) / step >= wait.debug_stop) return;
-    const uint32_t bar = bar0 + 8u * s, dst = smem_addr(mine + (size_t)s * slot);
-    const AnyRow<T> d = d_row(row);
-    const AnyRow<K> k = k_row(row);
-    uint32_t bytes = d.bytes() + k.bytes();
-    if (p.dtotal) bytes += p_row(row).bytes();
-    mbar_arrive_expect_tx(bar, bytes);
-    d.copy(dst, bar);
-    k.copy(dst + dslot, bar);
-    if (p.dtotal) p_row(row).copy(dst + dslot + kslot, bar);
+    const uint32_t bar = bar0 + 8u * s, dst = smem_addr(mine + (size_t)s * slot) + kBefore;
+    const RowUnits d(p.dy, row, p.lddy, p.rows, p.cols, ES), k(kept, row, ldk, p.rows, p.cols, KS);
+    const RowUnits q(p.dtotal ? p.dtotal : p.dy, row, p.dtotal ? p.lddt : p.lddy, p.rows, p.cols, ES);
+    if (PHASE && !(d.inside && k.inside && q.inside)) {
+      mbar_arrive(bar);  // nothing to wait for
+      return;
+    }
+    mbar_arrive_expect_tx(bar, d.bytes + k.bytes + (p.dtotal ? q.bytes : 0));
+    bulk_load(dst, d.from, d.bytes, bar);
+    bulk_load(dst + dslot, k.from, k.bytes, bar);
+    if (p.dtotal) bulk_load(dst + dslot + kslot, q.from, q.bytes, bar);
+  };
+  auto in_slot = [&](long long row) {
+    if (!PHASE) return true;
+    return RowUnits(p.dy, row, p.lddy, p.rows, p.cols, ES).inside &&
+           RowUnits(kept, row, ldk, p.rows, p.cols, KS).inside &&
+           (!p.dtotal || RowUnits(p.dtotal, row, p.lddt, p.rows, p.cols, ES).inside);
+  };
+  auto direct = [&](Pack<T, VEC>& to, const void* m, long long ld, long long row, int e) {
+    const T* from = static_cast<const T*>(m) + row * ld;
+    Fetched f;
+    fetch<T>(f, from, e, p.cols, true);
+    finish<T>(to, f, from, e, p.cols, true);
   };
   if (t == 0) {
     long long row = row0;
     for (int s = 0; s < g.stages && row < p.rows; ++s, row += step) issue(row, s);
   }
-  T* ws = reinterpret_cast<T*>(ring + (size_t)g.groups * g.stages * slot);
-  for (int c = threadIdx.x; c < p.cols; c += kBwdThreads)
-    ws[c] = p.w ? static_cast<const T*>(p.w)[c] : from_f32<T>(1.f);
-  __syncthreads();
-  float aw[N];
+  F2 aw[NCH][H];
+  Pack<T, VEC> wr[NCH];
 #pragma unroll
-  for (int i = 0; i < N; ++i) aw[i] = 0.f;
-  float rstd = 0.f, next_scale = 1.f;
-  auto ahead = [&](long long row) {
-    rstd = p.rstd[row];
+  for (int i = 0; i < NCH; ++i) {
+#pragma unroll
+    for (int j = 0; j < H; ++j) aw[i][j] = f2(0.f, 0.f);
+    float one[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) one[j] = 1.f;
+    wr[i].set(one);
+    if (p.w && t + i * g.nt < chunks) {
+      Fetched f;
+      fetch<T>(f, static_cast<const T*>(p.w), first_of(i), p.cols, true);
+      finish<T>(wr[i], f, static_cast<const T*>(p.w), first_of(i), p.cols, true);
+    }
+  }
+  float rstd = 0.f;
+  // The scales of a chunk's columns: one, or with PHASE those of both blocks it lies across
+  // (the second in the upper byte).
+  uint32_t byte[NCH];
+  auto fetch_scales = [&](long long row) {
     if constexpr (Q8) {
-      const int c = t - lane + lane * g.nt;
-      next_scale = lane < N && c < p.cols ? scale_value(p.k8.s[row * p.k8.lds + c / kScaleBlock]) : 1.f;
+      const unsigned char* s = p.k8.s + row * p.k8.lds;
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        byte[i] = 127;
+        if (FULL || t + i * g.nt < chunks) {
+          const int c = first_of(i);
+          byte[i] = s[(PHASE ? max(c, 0) : c) / kScaleBlock];
+          if (PHASE) byte[i] |= (uint32_t)s[min(c + VEC - 1, p.cols - 1) / kScaleBlock] << 8;
+        }
+      }
     }
   };
-  if (row0 < p.rows) ahead(row0);
+  // what is fetched past the ring, a row ahead (with PHASE, which is short of registers, the
+  // scales of the row itself)
+  if (row0 < p.rows) {
+    rstd = p.rstd[row0];
+    if (!PHASE) fetch_scales(row0);
+  }
   RingPos at;
   int turn = 0;
   bool alive = true;  // false once a wait has run out: no more waits, no more copies
   for (long long row = row0; row < p.rows; row += step) {
-    const float r = rstd, scale = next_scale;
-    if (row + step < p.rows) ahead(row + step);
+    const float r = rstd;
+    const F2 r2 = f2(r, r);
+    if (PHASE) fetch_scales(row);
+    uint32_t scales[NCH];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) scales[i] = Q8 ? byte[i] : 0;
+    if (row + step < p.rows) {
+      rstd = p.rstd[row + step];
+      if (!PHASE) fetch_scales(row + step);
+    }
     if (alive) alive = wait_row(bar0, at, g.stages, row, step, p.rows, t == 0, wait);
-    const unsigned char* here = mine + (size_t)at.s * slot;
-    float xh[N], gr[N];
-    float along = 0.f;
-    // The columns are computed anew in each loop: kept for all rows, with what depends on
-    // them, they would spill.
-    int c0 = t, nt = g.nt;
-    asm volatile("" : "+r"(c0), "+r"(nt));
-    {
-      const AnyRow<T> dr = d_row(row);
-      const AnyRow<K> kr = k_row(row);
-      const typename AnyRow<T>::Ends de = dr.ends(t, g.nt, p.cols);
-      const typename AnyRow<K>::Ends ke = kr.ends(t, g.nt, p.cols);
+    const unsigned char* here = mine + (size_t)at.s * slot + kBefore;
+    const bool there = in_slot(row);
+    F2 xh[NCH][H], gr[NCH][H];  // xhat, and g = dy weight
+    Pack<T, VEC> past[NCH];
+    F2 s0 = f2(0.f, 0.f), s1 = f2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int c = c0 + i * nt;
-        xh[i] = gr[i] = 0.f;
-        float s = r;
-        if constexpr (Q8) s = __shfl_sync(0xffffffffu, scale, i);
-        if (c < p.cols) {
-          const float k = ke.pick(i, kr.at(here + dslot, c));
-          xh[i] = Q8 ? k * s * r : k * r;
-          const float d = de.pick(i, dr.at(here, c));
-          gr[i] = d * to_f32(ws[c]);
-          along = fmaf(gr[i], xh[i], along);
-          aw[i] = fmaf(d, xh[i], aw[i]);
+    for (int i = 0; i < NCH; ++i) {
+      const int c = t + i * g.nt, e = first_of(i);
+      past[i].zero();
+      if (FULL || c < chunks) {
+        Pack<T, VEC> k, dk;
+        Codes<VEC> q;
+        F2 d[H], wf[H];
+        if (!PHASE || there) {
+          dk.load(reinterpret_cast<const T*>(here) + c * VEC);
+          if constexpr (!Q8)
+            k.load(reinterpret_cast<const T*>(here + dslot) + c * VEC);
+          else if constexpr (PHASE)
+            q.load_shared(here + dslot - kBefore, kBefore + e);  // the row begins on a boundary
+          else
+            q.load(here + dslot + c * VEC);
+          if (!PHASE && p.dtotal) past[i].load(reinterpret_cast<const T*>(here + dslot + kslot) + c * VEC);
+          if (PHASE && (e < 0 || e + VEC > p.cols)) {
+            cut<T>(dk, -e, p.cols - e);
+            if constexpr (Q8)
+              q.keep(-e, p.cols - e);
+            else
+              cut<T>(k, -e, p.cols - e);
+          }
+        } else {
+          direct(dk, p.dy, p.lddy, row, e);
+          if constexpr (Q8)
+            q.load(p.k8.q + row * p.k8.ldq + e, -e, p.cols - e);
+          else
+            direct(k, p.x, p.ldx, row, e);
         }
-        if (i % 4 == 3) asm volatile("" : "+r"(c0), "+r"(nt)::"memory");
+        dk.get2(d), wr[i].get2(wf);
+        if constexpr (Q8) {
+          float f[VEC];
+          q.get(f);
+          const float lo = scale_value(scales[i] & 255u);
+          if constexpr (PHASE) {
+            const float hi = scale_value(scales[i] >> 8);
+            const int edge = kScaleBlock - (e & (kScaleBlock - 1));  // from here on the second block
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) f[j] *= j < edge ? lo : hi;
+          } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) f[j] *= lo;
+          }
+#pragma unroll
+          for (int j = 0; j < H; ++j) xh[i][j] = f2(f[2 * j], f[2 * j + 1]);
+        } else {
+          k.get2(xh[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          xh[i][j] = mul2(xh[i][j], r2);
+          gr[i][j] = mul2(d[j], wf[j]);
+          aw[i][j] = fma2(d[j], xh[i][j], aw[i][j]);
+          if (j & 1)
+            s1 = fma2(gr[i][j], xh[i][j], s1);
+          else
+            s0 = fma2(gr[i][j], xh[i][j], s0);
+        }
       }
     }
-    const float mean = group_sum(along, red[turn], group, g.nt) * inv;
+    if (g.nt == 32) __syncwarp();  // no barrier in the sum: the warp's reads of the slot
+    const float mean = group_sum(f2_sum(add2(s0, s1)), red[turn], group, g.nt) * inv;
+    // the slot may be filled again: all of the group have read it (but for dtotal with PHASE)
+    auto refill = [&] {
+      if (t == 0 && alive && row + (long long)g.stages * step < p.rows)
+        issue(row + (long long)g.stages * step, at.s);
+    };
+    if (!PHASE) refill();
+    const F2 minus = f2(-mean, -mean);
     T* dx = static_cast<T*>(p.dx) + row * p.lddx;
-    asm volatile("" : "+r"(c0), "+r"(nt));
-    if (p.dtotal) {
-      const AnyRow<T> pr = p_row(row);
-      const typename AnyRow<T>::Ends pe = pr.ends(t, g.nt, p.cols);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int c = c0 + i * nt;
-        if (c < p.cols)
-          dx[c] = from_f32<T>(fmaf(r, fmaf(-xh[i], mean, gr[i]), pe.pick(i, pr.at(here + dslot + kslot, c))));
-        if (i % 4 == 3) asm volatile("" : "+r"(c0), "+r"(nt)::"memory");
-      }
-    } else {
+    for (int i = 0; i < NCH; ++i) {
+      const int c = t + i * g.nt;
+      if (FULL || c < chunks) {
+        F2 d[H];
+        if (PHASE && p.dtotal) {  // only now: no registers to keep it in
+          if (there)
+            past[i].load(reinterpret_cast<const T*>(here + dslot + kslot) + c * VEC);
+          else
+            direct(past[i], p.dtotal, p.lddt, row, first_of(i));
+        }
+        past[i].get2(d);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int c = c0 + i * nt;
-        if (c < p.cols) dx[c] = from_f32<T>(r * fmaf(-xh[i], mean, gr[i]));
+        for (int j = 0; j < H; ++j) d[j] = fma2(r2, fma2(xh[i][j], minus, gr[i][j]), d[j]);
+        Pack<T, VEC> k;
+        k.set2(d);
+        if constexpr (PHASE)
+          store_at<T>(k, dx, first_of(i), p.cols);
+        else
+          k.store(dx + c * VEC);
       }
     }
-    // the slot has been read by all of the group
-    if (g.nt > 32)
+    if (PHASE) {
       asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(g.nt) : "memory");
-    else
-      __syncwarp();
-    if (t == 0 && alive && row + (long long)g.stages * step < p.rows)
-      issue(row + (long long)g.stages * step, at.s);
+      refill();
+    }
     turn ^= 1;
     at.next(g.stages);
   }
@@ -593,9 +624,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();  // no ring has a copy on its way: its memory now takes the groups' sums
   float* sums = reinterpret_cast<float*>(ring);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int c = t + i * g.nt;
-    if (c < p.cols) sums[(size_t)group * p.cols + c] = aw[i];
+  for (int i = 0; i < NCH; ++i) {
+    const int c = first_of(i);
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+      float* q = sums + (size_t)group * p.cols + c + 2 * j;
+      if constexpr (PHASE) {
+        float a, b;
+        f2_split(aw[i][j], a, b);
+        if (c + 2 * j >= 0 && c + 2 * j < p.cols) q[0] = a;
+        if (c + 2 * j + 1 >= 0 && c + 2 * j + 1 < p.cols) q[1] = b;
+      } else if (FULL || c < p.cols) {
+        *reinterpret_cast<F2*>(q) = aw[i][j];
+      }
+    }
   }
   __syncthreads();
   leave_sums<T>(p, sums, g.groups);
@@ -604,41 +646,75 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // Rows wider than the registers of a block: dx in two passes over the row.
 template <typename T, bool Q8>
 __global__ void __launch_bounds__(1024) rms_bwd_wide_kernel(const __grid_constant__ RmsBwd p) {
+  constexpr int VEC = kVec<T>;
   __shared__ float red[32];
   pdl_launch_dependents();
   pdl_wait();
   const long long row = blockIdx.x;
-  const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
   const T* w = static_cast<const T*>(p.w);
   const float rstd = p.rstd[row];
-  float along = 0.f, t[1];
-  for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
-    load_t<T, 1, Q8>(p, row, c, t);
-    along = fmaf(to_f32(dy[c]) * (w ? to_f32(w[c]) : 1.f), t[0] * rstd, along);
+  // xhat and g of chunk c
+  auto load = [&](int c, float (&xh)[VEC], float (&g)[VEC]) {
+    load_kept<T, Q8, true>(p, row, c, xh);
+    Pack<T, VEC> k;
+    load_chunk<T, true>(k, static_cast<const T*>(p.dy) + row * p.lddy, c, p.cols);
+    k.get(g);
+    float wf[VEC];
+    if (w) {
+      load_chunk<T, true>(k, w, c, p.cols);
+      k.get(wf);
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) xh[j] *= rstd, g[j] *= w ? wf[j] : 1.f;
+  };
+  float along = 0.f, xh[VEC], g[VEC];
+  for (int c = threadIdx.x; c < p.chunks; c += blockDim.x) {
+    load(c, xh, g);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) along = fmaf(g[j], xh[j], along);
   }
   const float mean = block_sum(along, red, blockDim.x >> 5) / (float)p.cols;
-  for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
-    load_t<T, 1, Q8>(p, row, c, t);
-    const float g = to_f32(dy[c]) * (w ? to_f32(w[c]) : 1.f);
-    const float d = p.dtotal ? to_f32(static_cast<const T*>(p.dtotal)[row * p.lddt + c]) : 0.f;
-    static_cast<T*>(p.dx)[row * p.lddx + c] = from_f32<T>(fmaf(rstd, g - t[0] * rstd * mean, d));
+  for (int c0 = 0; c0 < p.chunks; c0 += blockDim.x) {
+    const int c = c0 + threadIdx.x;
+    Pack<T, VEC> k;
+    k.zero();
+    if (c < p.chunks) {
+      float d[VEC];
+      load(c, xh, g);
+      if (p.dtotal) load_chunk<T, true>(k, static_cast<const T*>(p.dtotal) + row * p.lddt, c, p.cols);
+      k.get(d);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) d[j] = fmaf(rstd, fmaf(-xh[j], mean, g[j]), d[j]);
+      k.set(d);
+    }
+    store_chunk<T, true>(k, static_cast<T*>(p.dx) + row * p.lddx, c, p.cols, c < p.chunks, 32);
   }
 }
 
-// The wide rows' dweight: block (x, y) adds rows y, y + gridDim.y, ... of its 256 columns
-// into partial row y.  Runs before rms_bwd_wide_kernel, which may overwrite dy.
+// The wide rows' dweight: block (x, y) adds rows y, y + gridDim.y, ... of its 64 chunks into
+// partial row y.  Runs before rms_bwd_wide_kernel, which may overwrite dy.
 template <typename T, bool Q8>
-__global__ void __launch_bounds__(256) rms_bwd_cols_kernel(const __grid_constant__ RmsBwd p) {
+__global__ void __launch_bounds__(64) rms_bwd_cols_kernel(const __grid_constant__ RmsBwd p) {
+  constexpr int VEC = kVec<T>;
   pdl_launch_dependents();
   pdl_wait();
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= p.cols) return;
-  float a = 0.f, t[1];
+  const int c = blockIdx.x * 64 + threadIdx.x;
+  if (c >= p.chunks) return;
+  float a[VEC], xh[VEC], d[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) a[j] = 0.f;
   for (long long row = blockIdx.y; row < p.rows; row += gridDim.y) {
-    load_t<T, 1, Q8>(p, row, c, t);
-    a = fmaf(to_f32(static_cast<const T*>(p.dy)[row * p.lddy + c]), t[0] * p.rstd[row], a);
+    load_kept<T, Q8, true>(p, row, c, xh);
+    Pack<T, VEC> k;
+    load_chunk<T, true>(k, static_cast<const T*>(p.dy) + row * p.lddy, c, p.cols);
+    k.get(d);
+    const float rstd = p.rstd[row];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) a[j] = fmaf(d[j], xh[j] * rstd, a[j]);
   }
-  p.part[(size_t)blockIdx.y * p.cols + c] = a;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j)
+    if (c * VEC + j < p.cols) p.part[(size_t)blockIdx.y * p.cols + c * VEC + j] = a[j];
 }
 
 // dweight: warp y adds the partial rows y, y + 16, ... in order, then the warps' sums are
@@ -666,127 +742,142 @@ __global__ void __launch_bounds__(512) rms_bwd_reduce_kernel(const float* part, 
 
 // ----------------------------------------------------------------- host side
 
-// Chunks a thread may hold (powers of two).
-template <int VEC>
-constexpr int kMaxFwd = VEC == 1 ? 16 : 4;
+// Chunks a thread may hold; one more for the part of a unit before the row.
+template <Rows ROWS>
+constexpr int kMaxFwd = ROWS == kPhase ? 5 : 4;
 
-template <typename T, int VEC, int NCH = 1>
+template <typename T, Rows ROWS, int NCH = 1>
 cudaError_t fwd_kernel(int nch, dim3 grid, dim3 block, cudaStream_t st, const RmsFwd& p) {
-  if constexpr (NCH < kMaxFwd<VEC>) {
-    if (nch > NCH) return fwd_kernel<T, VEC, 2 * NCH>(nch, grid, block, st, p);
+  if constexpr (NCH < kMaxFwd<ROWS>) {
+    if (nch > NCH) return fwd_kernel<T, ROWS, NCH + 1>(nch, grid, block, st, p);
   }
-  return launch_train(rms_fwd_kernel<T, VEC, NCH>, grid, block, 0, st, p);
+  return launch_train(rms_fwd_kernel<T, NCH, ROWS>, grid, block, 0, st, p);
 }
 
-template <typename T, int VEC>
+template <typename T, Rows ROWS>
 cudaError_t fwd_launch(RmsFwd p, int sms, cudaStream_t st) {
-  p.chunks = p.cols / VEC;
-  // a block of 32 columns stays within a warp: 8 lanes at 4 columns, 32 at single ones
-  constexpr int least = VEC > 1 ? 8 : 32;
-  int nt = p.rows <= 2 * sms ? row_threads(p.chunks, 1, least) : 0;
-  if (!nt) nt = row_threads(p.chunks, kMaxFwd<VEC>, least);
+  p.chunks = (int)ceil_div(p.cols, kVec<T>);
+  const int most = (int)ceil_div(p.cols + (ROWS == kPhase ? kVec<T> - 1 : 0), kVec<T>);  // of any row
+  constexpr int least = 8;  // lanes a row: a block of 32 columns stays within a warp
+  // chunks a thread: one where there are few rows, for the shortest path; more otherwise, for
+  // the fewest barriers a byte, but two where rows off the boundaries take twice the registers
+  int nt = 0;
+  for (int per = p.rows <= 2 * sms ? 1 : ROWS == kAligned ? 4 : 2; !nt && per <= kMaxFwd<ROWS>; ++per)
+    nt = most <= 32 * per ? row_threads(most, per, least)
+         : most <= kMaxRowThreads * per ? (int)round_up(ceil_div(most, per), 32) : 0;
   if (!nt)
     return launch_train(rms_fwd_wide_kernel<T>, dim3((unsigned)p.rows), dim3(1024), 0, st, p);
   const int ry = nt <= 32 ? 128 / nt : 1;
   const dim3 grid((unsigned)ceil_div(p.rows, ry)), block(nt, ry);
-  return fwd_kernel<T, VEC>((int)ceil_div(p.chunks, nt), grid, block, st, p);
+  return fwd_kernel<T, ROWS>((int)ceil_div(most, nt), grid, block, st, p);
 }
 
 // How the backward pass runs.
-enum BwdKind { kDirect, kRing, kAny, kWide };
+enum BwdKind { kDirect, kRing, kWide };
 struct BwdPlan {
   BwdKind kind;
   Ring r;     // stages only where there is a ring
   int parts;  // blocks, each leaving one partial row of dweight
 };
 
-// vec: rows on 16-byte boundaries; past: a dtotal; q8: 8-bit rows.
-BwdPlan bwd_plan(long long rows, int cols, int dtype, int sms, bool vec, bool past, bool q8) {
-  const size_t es = type_size(dtype), ks = q8 ? 1 : es;
+constexpr int kBwdRing = 224 * 1024;  // bytes of the rings
+constexpr int kNarrow = 128;          // columns of a row that a warp has too many lanes for
+
+uint32_t slot_of(int cols, size_t es, bool phase, bool past, bool q8) {
+  const int e = (int)es, k = q8 ? 1 : e;
+  return phase ? row_slot<true>(cols, k) + row_slot<true>(cols, e) * (past ? 2 : 1)
+               : row_slot<false>(cols, k) + row_slot<false>(cols, e) * (past ? 2 : 1);
+}
+
+// past: a dtotal; q8: 8-bit rows.
+BwdPlan bwd_plan(long long rows, int cols, int dtype, int sms, Rows how, bool past, bool q8) {
   BwdPlan b{kWide, {}, 0};
-  if (vec) {
-    b.r = ring_of(kBwdThreads, 16, cols, (size_t)cols * (ks + es * (past ? 2 : 1)), 0);
-    if (b.r.nt * 16 >= cols) {
-      if (rows <= (long long)b.r.groups * sms || cols <= 512 || b.r.stages < 2) {
-        b.kind = kDirect;
-        b.r.nt = 4;
-        while (b.r.nt * 16 < cols) b.r.nt *= 2;
-        b.r.groups = kBwdThreads / b.r.nt;
-      } else {
-        b.kind = kRing;
-      }
+  const size_t es = type_size(dtype);
+  // whole warps that hold a row with the part of a unit before it
+  auto ring = [&](int threads, int per, bool phase) {
+    const long long need = ceil_div(cols + (phase ? 16 / (int)es - 1 : 0), per);
+    Ring r{(int)round_up(need, 32), 0, 0};
+    if (r.nt > threads) return r;
+    r.groups = threads / r.nt;
+    const size_t s = kBwdRing / ((size_t)slot_of(cols, es, phase, past, q8) * r.groups);
+    r.stages = (int)(s < (size_t)kRingStages ? s : (size_t)kRingStages);
+    return r;
+  };
+  if (cols <= 16 * kBwdThreads) {
+    b.r = how == kPhase ? ring(kPhaseThreads, kPhaseCols, true) : ring(kBwdThreads, 16, false);
+    b.kind = kRing;
+    // short rows, and one row a group: no second row to wait for
+    if (how == kAny || (how == kPhase && sms < 8) || rows <= (long long)b.r.groups * sms ||
+        cols <= kNarrow || b.r.stages < 2) {
+      b.kind = kDirect;
+      b.r.nt = 4;
+      while (b.r.nt * 16 < cols) b.r.nt *= 2;
+      b.r.groups = kBwdThreads / b.r.nt;
     }
-  } else {
-    b.r = ring_of(kBwdThreads, 16, cols, any_slot(cols, ks) + any_slot(cols, es) * (past ? 2 : 1), es * cols);
-    if (b.r.nt * 16 >= cols && b.r.stages >= 2) b.kind = kAny;
   }
-  const long long most = b.kind != kWide ? sms : 4LL * sms, each = b.kind != kWide ? b.r.groups : 4;
-  const long long fair = ceil_div(rows, each);
+  long long most = b.kind != kWide ? sms : 4LL * sms;
+  const long long fair = ceil_div(rows, b.kind != kWide ? b.r.groups : 4);
+  if (b.kind == kRing && how == kPhase) most = sms / 8 * 8;  // steps of whole 16-byte units
   b.parts = (int)(fair < most ? fair : most);
   return b;
 }
 
-template <typename T, bool Q8>
-size_t ring_bytes(const RmsBwd& p, const BwdPlan& b) {
-  const size_t d = p.dtotal ? 2 : 1;
-  const size_t slot = b.kind == kRing
-                          ? (size_t)p.cols * sizeof(T) * d + kept_bytes<T, Q8>(p.cols)
-                          : any_slot(p.cols, sizeof(T)) * d + any_slot(p.cols, Q8 ? 1 : sizeof(T));
-  const size_t rings = b.r.groups * b.r.stages * slot + (b.kind == kAny ? p.cols * sizeof(T) : 0);
-  const size_t sums = (size_t)b.r.groups * p.cols * sizeof(float);
-  return rings > sums ? rings : sums;
-}
-
-template <typename T, int VEC, bool FULL, bool Q8>
+template <typename T, bool FULL, bool Q8, bool PHASE>
 cudaError_t bwd_ring(const RmsBwd& p, const BwdPlan& b, const TrainDevice& d, cudaStream_t st) {
   static std::atomic<int> done[64];
   const cudaError_t e = allow_ring(
-      reinterpret_cast<const void*>(&rms_bwd_ring_kernel<T, VEC, FULL, Q8>), done, d.dev);
+      reinterpret_cast<const void*>(&rms_bwd_ring_kernel<T, FULL, Q8, PHASE>), done, d.dev, kBwdRing);
   if (e != cudaSuccess) return e;
-  return launch_train(rms_bwd_ring_kernel<T, VEC, FULL, Q8>, dim3(b.parts), dim3(kBwdThreads),
-                      ring_bytes<T, Q8>(p, b), st, p, b.r,
-                      RingWait{d.status, d.wait_limit_ns, d.debug_stop});
-}
-template <typename T, bool Q8>
-cudaError_t bwd_any(const RmsBwd& p, const BwdPlan& b, const TrainDevice& d, cudaStream_t st) {
-  static std::atomic<int> done[64];
-  const cudaError_t e =
-      allow_ring(reinterpret_cast<const void*>(&rms_bwd_any_kernel<T, Q8>), done, d.dev);
-  if (e != cudaSuccess) return e;
-  return launch_train(rms_bwd_any_kernel<T, Q8>, dim3(b.parts), dim3(kBwdThreads),
-                      ring_bytes<T, Q8>(p, b), st, p, b.r,
+  // the rings, and at the end the groups' column sums
+  const size_t rings = (size_t)b.r.groups * b.r.stages * slot_of(p.cols, sizeof(T), PHASE, p.dtotal, Q8);
+  const size_t sums = (size_t)b.r.groups * p.cols * sizeof(float);
+  return launch_train(rms_bwd_ring_kernel<T, FULL, Q8, PHASE>, dim3(b.parts), dim3(b.r.groups * b.r.nt),
+                      rings > sums ? rings : sums, st, p, b.r,
                       RingWait{d.status, d.wait_limit_ns, d.debug_stop});
 }
 
-template <typename T, bool Q8>
-cudaError_t bwd_launch(RmsBwd p, const BwdPlan& b, const TrainDevice& d, cudaStream_t st) {
-  constexpr int VEC = 16 / sizeof(T);
-  p.chunks = p.cols / VEC;
+template <typename T, bool Q8, Rows ROWS>
+cudaError_t bwd_launch(RmsBwd p, int dtype, const TrainDevice& d, cudaStream_t st) {
+  p.chunks = (int)ceil_div(p.cols, kVec<T>);
+  const BwdPlan b = bwd_plan(p.rows, p.cols, dtype, d.sms, ROWS, p.dtotal, Q8);
   cudaError_t e = cudaSuccess;
-  switch (b.kind) {
-    case kDirect:
-      e = launch_train(rms_bwd_kernel<T, VEC, Q8>, dim3(b.parts), dim3(kBwdThreads),
-                       (size_t)b.r.groups * p.cols * sizeof(float), st, p, b.r.nt, b.r.groups);
-      break;
-    case kRing:
-      e = b.r.nt * 16 == p.cols ? bwd_ring<T, VEC, true, Q8>(p, b, d, st)
-                                : bwd_ring<T, VEC, false, Q8>(p, b, d, st);
-      break;
-    case kAny:
-      e = bwd_any<T, Q8>(p, b, d, st);
-      break;
-    case kWide:
-      if (p.dw)
-        e = launch_train(rms_bwd_cols_kernel<T, Q8>, dim3((unsigned)ceil_div(p.cols, 256), b.parts),
-                         dim3(256), 0, st, p);
-      if (e == cudaSuccess)
-        e = launch_train(rms_bwd_wide_kernel<T, Q8>, dim3((unsigned)p.rows), dim3(1024), 0, st, p);
+  if (b.kind == kDirect) {
+    e = launch_train(rms_bwd_kernel<T, Q8, ROWS != kAligned>, dim3(b.parts), dim3(kBwdThreads),
+                     (size_t)b.r.groups * p.cols * sizeof(float), st, p, b.r.nt, b.r.groups);
+  } else if (b.kind == kRing) {
+    if constexpr (ROWS == kPhase)
+      e = bwd_ring<T, false, Q8, true>(p, b, d, st);
+    else if (b.r.nt * 16 == p.cols)
+      e = bwd_ring<T, true, Q8, false>(p, b, d, st);
+    else
+      e = bwd_ring<T, false, Q8, false>(p, b, d, st);
+  } else {
+    if (p.dw)
+      e = launch_train(rms_bwd_cols_kernel<T, Q8>, dim3((unsigned)ceil_div(p.chunks, 64), b.parts), dim3(64),
+                       0, st, p);
+    if (e == cudaSuccess)
+      e = launch_train(rms_bwd_wide_kernel<T, Q8>, dim3((unsigned)p.rows), dim3(1024), 0, st, p);
   }
   if (e == cudaSuccess && p.dw && (b.parts > 1 || b.kind == kWide))
     e = launch_train(rms_bwd_reduce_kernel<T>, dim3((unsigned)ceil_div(p.cols, 32)), dim3(32, 16), 0,
                      st, (const float*)p.part, b.parts, p.cols, static_cast<T*>(p.dw));
   return e;
 }
+
+// Whether matrices (those that are given) have their rows at the same places within a 16-byte
+// unit.
+struct Place16 {
+  bool same = true;
+  int at = -1;
+  long long step = 0;
+  void add(const void* q, long long ld, int dtype) {
+    if (!q) return;
+    const int a = (int)(reinterpret_cast<uintptr_t>(q) & 15u);
+    const long long s = ld * (long long)type_size(dtype) % 16;
+    if (at < 0) at = a, step = s;
+    same = same && a == at && s == step;
+  }
+};
 
 int check_rows(int dtype, long long rows, int cols) {
   if (!type_ok(dtype)) return B2G_ERR_INVALID_TYPE;
@@ -805,8 +896,11 @@ size_t bwd_bytes(long long rows, int cols, int sms) {
   return (size_t)(rows < most ? rows : most) * cols * sizeof(float);
 }
 
-Rows8 rows8(void* q, long long ldq, void* s, long long lds) {
-  return Rows8{static_cast<unsigned char*>(q), ldq, static_cast<unsigned char*>(s), lds};
+// vec: codes that go at a time.
+Rows8 rows8(void* q, long long ldq, void* s, long long lds, int vec) {
+  Rows8 r{static_cast<unsigned char*>(q), ldq, static_cast<unsigned char*>(s), lds, 0};
+  r.vec = codes_vec(r, vec);
+  return r;
 }
 
 }  // namespace
@@ -824,8 +918,9 @@ int b2g_rmsnorm(int dtype, long long rows, int cols, const void* x, long long ld
   int rc = check_rows(dtype, rows, cols);
   if (rc) return rc;
   if (!(eps >= 0.f)) return B2G_ERR_INVALID_DIM;
-  const Rows8 y8 = rows8(y_codes, ldyq, y_scales, ldys);
-  const Rows8 t8 = rows8(total_codes, ldtq, total_scales, ldts);
+  const int vec = dtype == B2G_F32 ? 4 : 8;
+  const Rows8 y8 = rows8(y_codes, ldyq, y_scales, ldys, vec);
+  const Rows8 t8 = rows8(total_codes, ldtq, total_scales, ldts, vec);
   if (!ld_ok(&rc, ldx, cols) || !ld_ok(residual, ldr, cols) || !ld_ok(total, ldt, cols) ||
       !ld_ok(y, ldy, cols) || !codes_ok(y8, cols) || !codes_ok(t8, cols))
     return B2G_ERR_INVALID_LD;
@@ -838,13 +933,18 @@ int b2g_rmsnorm(int dtype, long long rows, int cols, const void* x, long long ld
                  total, ldt, y,   ldy, y8, t8,       rstd};
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto row16 = [&](const void* q, long long ld) { return !q || (vec16(q) && vec16_ld(ld, dtype)); };
-  const int vec = dtype == B2G_F32 ? 4 : 8;
   const bool v = row16(x, ldx) && row16(residual, ldr) && row16(total, ldt) && row16(y, ldy) &&
-                 row16(weight, cols) && vec16_ld(cols, dtype) && codes_vec(y8, vec) &&
-                 codes_vec(t8, vec);
+                 row16(weight, cols) && vec16_ld(cols, dtype) && y8.vec && t8.vec;
+  Place16 at;
+  at.add(x, ldx, dtype), at.add(residual, ldr, dtype), at.add(total, ldt, dtype), at.add(y, ldy, dtype);
+  const bool phase = at.same && !y8.q && !t8.q;  // a scale's columns are counted from the row's first
   if (dtype == B2G_F32)
-    return launch_code(v ? fwd_launch<float, 4>(p, d.sms, st) : fwd_launch<float, 1>(p, d.sms, st));
-  return launch_code(v ? fwd_launch<Bf16, 8>(p, d.sms, st) : fwd_launch<Bf16, 1>(p, d.sms, st));
+    return launch_code(v       ? fwd_launch<float, kAligned>(p, d.sms, st)
+                       : phase ? fwd_launch<float, kPhase>(p, d.sms, st)
+                               : fwd_launch<float, kAny>(p, d.sms, st));
+  return launch_code(v       ? fwd_launch<Bf16, kAligned>(p, d.sms, st)
+                     : phase ? fwd_launch<Bf16, kPhase>(p, d.sms, st)
+                             : fwd_launch<Bf16, kAny>(p, d.sms, st));
 }
 
 int b2g_rmsnorm_backward_workspace_size(int dtype, long long rows, int cols, size_t* bytes) {
@@ -864,8 +964,9 @@ int b2g_rmsnorm_backward(int dtype, long long rows, int cols, const void* dy, lo
                          size_t workspace_bytes, void* stream) {
   int rc = check_rows(dtype, rows, cols);
   if (rc) return rc;
-  const Rows8 k8 = total_scales ? rows8(const_cast<void*>(total), ldt, const_cast<void*>(total_scales), ldts)
-                                : Rows8{};
+  const Rows8 k8 = total_scales ? rows8(const_cast<void*>(total), ldt, const_cast<void*>(total_scales), ldts,
+                                       dtype == B2G_F32 ? 4 : 8)
+                               : Rows8{};
   if (!ld_ok(&rc, lddy, cols) || !ld_ok(&rc, ldt, cols) || !codes_ok(k8, cols) ||
       !ld_ok(dtotal, lddt, cols) || !ld_ok(&rc, lddx, cols))
     return B2G_ERR_INVALID_LD;
@@ -887,10 +988,21 @@ int b2g_rmsnorm_backward(int dtype, long long rows, int cols, const void* dy, lo
   const bool v = row16(dy, lddy) && row16(p.x, ldt) && row16(dtotal, lddt) && row16(dx, lddx) &&
                  row16(weight, cols) && vec16_ld(cols, dtype) &&
                  (!q8 || (vec16(k8.q) && k8.ldq % 16 == 0 && cols % 16 == 0));
-  const BwdPlan b = bwd_plan(rows, cols, dtype, d.sms, v, dtotal != nullptr, q8);
-  if (dtype == B2G_F32)
-    return launch_code(q8 ? bwd_launch<float, true>(p, b, d, st) : bwd_launch<float, false>(p, b, d, st));
-  return launch_code(q8 ? bwd_launch<Bf16, true>(p, b, d, st) : bwd_launch<Bf16, false>(p, b, d, st));
+  Place16 at;
+  at.add(dy, lddy, dtype), at.add(p.x, ldt, dtype), at.add(dtotal, lddt, dtype), at.add(dx, lddx, dtype);
+  const bool phase = at.same && (!q8 || (vec16(k8.q) && k8.ldq % 16 == 0));
+  auto run = [&](auto kept, auto how) {
+    constexpr bool Q8 = decltype(kept)::value;
+    constexpr Rows ROWS = decltype(how)::value;
+    return launch_code(dtype == B2G_F32 ? bwd_launch<float, Q8, ROWS>(p, dtype, d, st)
+                                        : bwd_launch<Bf16, Q8, ROWS>(p, dtype, d, st));
+  };
+  auto with = [&](auto kept) {
+    return v       ? run(kept, std::integral_constant<Rows, kAligned>())
+           : phase ? run(kept, std::integral_constant<Rows, kPhase>())
+                   : run(kept, std::integral_constant<Rows, kAny>());
+  };
+  return q8 ? with(std::true_type()) : with(std::false_type());
 }
 
 }  // extern "C"

@@ -13,6 +13,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -62,8 +63,9 @@ struct Kind {
     if (t.dim() != 1 || t.device() != device || !t.is_contiguous()) return 0;
     return t.scalar_type() == at::kLong ? 8 : t.scalar_type() == at::kInt ? 4 : 0;
   }
+  // What at::empty ends in on this device, without its dispatch.
   Tensor empty(at::IntArrayRef shape, at::ScalarType t) const {
-    return at::empty(shape, at::TensorOptions().dtype(t).device(device));
+    return at::detail::empty_cuda(shape, t, device, c10::nullopt);
   }
   Tensor empty(at::IntArrayRef shape) const { return empty(shape, type); }
   Tensor bytes(size_t n) const { return empty({(int64_t)n}, at::kByte); }

@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(256) dw8_join_kernel(const __grid_constant__ D
 struct Prepare {
   int tokens;
   Rows8 k;
-  int width, vec;
+  int width;
   Bf16* x;
   long long ldx;
   const void* dy;
@@ -356,16 +356,8 @@ __global__ void __launch_bounds__(256) dw8_prepare_kernel(const __grid_constant_
     if (i < nx) {
       const long long row = i / gx;
       const int c = (int)(i - row * gx) * 8;
-      const unsigned char* q = p.k.q + row * p.k.ldq + c;
       Codes<8> codes;
-      if (p.vec) {
-        codes.load(q);
-      } else {
-        codes.zero();
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c + j < p.width) codes.w[j >> 2] |= (uint32_t)q[j] << (8 * (j & 3));
-      }
+      load_codes<8, true>(codes, p.k, row, c / 8, p.width);
       const float s = scale_value(p.k.s[row * p.k.lds + c / kScaleBlock]);
       float f[8];
       codes.get(f);
@@ -527,10 +519,9 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
   Prepare q = {};
   q.tokens = tokens;
   q.k = Rows8{static_cast<unsigned char*>(const_cast<void*>(codes)), ldq,
-              static_cast<unsigned char*>(const_cast<void*>(scales)), lds};
+              static_cast<unsigned char*>(const_cast<void*>(scales)), lds, 0};
   q.width = width, q.x = reinterpret_cast<Bf16*>(ws + l.x), q.ldx = l.ldx;
-  // eight codes at once: also where the last ones are past the row but inside its stride
-  q.vec = codes_vec(q.k, 8) && (width % 8 == 0);
+  q.k.vec = codes_vec(q.k, 8);
   q.dy = dy, q.lddy = lddy, q.outs = outs, q.planes = l.copy_dy ? l.planes : 0;
   q.d = reinterpret_cast<Bf16*>(ws + l.d), q.ldd = l.ldd;
   const long long blocks = ceil_div((l.ldx + (l.copy_dy ? l.ldd : 0)) / 8 * tokens, 256);
