@@ -211,4 +211,42 @@ __device__ __forceinline__ void store_chunk(const Pack<T, kVec<T>>& k, T* row, i
   }
 }
 
+// How blocks of 256 threads walk a matrix, four chunks a thread.  A warp's lanes stand in
+// 2^lane_rows rows of consecutive chunks; its four passes are 2^pass_cols of them along the
+// rows, the others down the matrix.  So long rows and short ones fill a warp, an aligned group
+// of `least` lanes stays in one row and one pass, and places come without divisions but one by
+// the pieces of a row.
+constexpr int kPasses = 4;
+struct Walk {
+  long long rows;
+  int chunks;       // of a row
+  unsigned pieces;  // warps a row
+  int lane_rows, pass_cols;
+  long long blocks;
+};
+inline Walk walk_of(long long rows, int chunks, int least) {
+  Walk w{rows, chunks, 1, 0, 0, 0};
+  while ((32 >> w.lane_rows) / 2 >= least && (32 >> w.lane_rows) / 2 >= chunks) ++w.lane_rows;
+  while ((1 << w.pass_cols) < kPasses && (32 << w.pass_cols) < chunks) ++w.pass_cols;
+  w.pieces = (unsigned)ceil_div(chunks, 32 << w.pass_cols);
+  w.blocks = ceil_div(ceil_div(rows, (long long)(kPasses >> w.pass_cols) << w.lane_rows) * w.pieces, 8);
+  return w;
+}
+struct Places {
+  long long row;
+  int c, lanes, rows, mask, shift;
+  __device__ __forceinline__ Places(const Walk& w, long long block) {
+    const long long warp = block * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const long long line = w.pieces == 1 ? warp : warp / w.pieces;
+    const int piece = (int)(warp - line * w.pieces);
+    lanes = 32 >> w.lane_rows, rows = 1 << w.lane_rows;
+    shift = w.pass_cols, mask = (1 << shift) - 1;
+    row = line * ((kPasses >> shift) * rows) + lane / lanes;
+    c = (piece << shift) * 32 + (lane & (lanes - 1));
+  }
+  __device__ __forceinline__ long long row_of(int u) const { return row + (u >> shift) * rows; }
+  __device__ __forceinline__ int chunk_of(int u) const { return c + (u & mask) * 32; }
+};
+
 }  // namespace b2g

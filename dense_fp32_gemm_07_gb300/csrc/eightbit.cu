@@ -5,39 +5,13 @@
 namespace b2g {
 namespace {
 
-constexpr int kPasses = 4;
-
-// Four chunks of 16 bytes of x a thread.  A warp's lanes stand in 2^lane_rows rows of consecutive
-// chunks; its four passes are 2^pass_cols of them along the rows, the others down the matrix.
-// So a scale's block is in one pass, long rows and short ones fill a warp, and places come
-// without divisions but one by the pieces of a row.
+// A block of 32 columns stays within a pass of a warp.
 struct Convert {
-  long long rows;
+  Walk walk;
   int cols;
-  int chunks;     // of a row
-  unsigned pieces;  // warps a row
-  int lane_rows, pass_cols;
-  void* x;        // read by quantize, written by dequantize
+  void* x;  // read by quantize, written by dequantize
   long long ldx;
   Rows8 k;
-};
-
-template <int U>
-struct Places {
-  long long row;
-  int c, lanes, rows, mask, shift;
-  __device__ __forceinline__ Places(const Convert& p) {
-    const long long warp = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    const long long line = p.pieces == 1 ? warp : warp / p.pieces;
-    const int piece = (int)(warp - line * p.pieces);
-    lanes = 32 >> p.lane_rows, rows = 1 << p.lane_rows;
-    shift = p.pass_cols, mask = (1 << shift) - 1;
-    row = line * ((U >> shift) * rows) + lane / lanes;
-    c = (piece << shift) * 32 + (lane & (lanes - 1));
-  }
-  __device__ __forceinline__ long long row_of(int u) const { return row + (u >> shift) * rows; }
-  __device__ __forceinline__ int chunk_of(int u) const { return c + (u & mask) * 32; }
 };
 
 // Bound: bytes.
@@ -45,7 +19,7 @@ template <typename T, bool ANY>
 __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ Convert p) {
   constexpr int VEC = kVec<T>, U = kPasses, lanes = kScaleBlock / VEC;
   pdl_launch_dependents();
-  const Places<U> at(p);
+  const Places at(p.walk, blockIdx.x);
   pdl_wait();
   Pack<T, VEC> k[U];
   Fetched raw[ANY ? U : 1];
@@ -53,7 +27,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ C
   for (int u = 0; u < U; ++u) {
     const long long row = at.row_of(u);
     const int c = at.chunk_of(u);
-    const bool in = row < p.rows && c < p.chunks;
+    const bool in = row < p.walk.rows && c < p.walk.chunks;
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
     if constexpr (ANY) {
       fetch<T>(raw[u], x, c * VEC, p.cols, in);
@@ -69,7 +43,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ C
       const long long row = at.row_of(u);
       const int c = at.chunk_of(u);
       finish<T>(k[u], raw[u], static_cast<const T*>(p.x) + row * p.ldx, c * VEC, p.cols,
-                row < p.rows && c < p.chunks);
+                row < p.walk.rows && c < p.walk.chunks);
     }
     k[u].get(f[u]);
   }
@@ -80,7 +54,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ C
   for (int u = 0; u < U; ++u) {
     const long long row = at.row_of(u);
     const int c = at.chunk_of(u);
-    if (row < p.rows && c < p.chunks) {
+    if (row < p.walk.rows && c < p.walk.chunks) {
       store_codes<VEC, ANY>(codes[u], p.k, row, c, p.cols);
       if (c % lanes == 0) p.k.s[row * p.k.lds + c / lanes] = (unsigned char)byte[u];
     }
@@ -91,7 +65,7 @@ template <typename T, bool ANY>
 __global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__ Convert p) {
   constexpr int VEC = kVec<T>, U = kPasses;
   pdl_launch_dependents();
-  const Places<U> at(p);
+  const Places at(p.walk, blockIdx.x);
   pdl_wait();
   Codes<VEC> k[U];
   uint32_t byte[U];
@@ -99,7 +73,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__
   for (int u = 0; u < U; ++u) {
     const long long row = at.row_of(u);
     const int c = at.chunk_of(u);
-    if (row < p.rows && c < p.chunks) {
+    if (row < p.walk.rows && c < p.walk.chunks) {
       load_codes<VEC, ANY>(k[u], p.k, row, c, p.cols);
       byte[u] = p.k.s[row * p.k.lds + c / (kScaleBlock / VEC)];
     }
@@ -108,7 +82,7 @@ __global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__
   for (int u = 0; u < U; ++u) {
     const long long row = at.row_of(u);
     const int c = at.chunk_of(u);
-    const bool in = row < p.rows && c < p.chunks;
+    const bool in = row < p.walk.rows && c < p.walk.chunks;
     Pack<T, VEC> o;
     o.zero();
     if (in) {
@@ -135,16 +109,9 @@ int check(int dtype, long long rows, int cols, const void* x, long long ldx, con
 
 template <typename T, bool ANY>
 cudaError_t launch(bool back, Convert p, cudaStream_t st) {
-  constexpr int U = kPasses, lanes = kScaleBlock / kVec<T>;
-  p.chunks = (int)ceil_div(p.cols, kVec<T>);
-  while ((32 >> p.lane_rows) / 2 >= lanes && (32 >> p.lane_rows) / 2 >= p.chunks)
-    ++p.lane_rows;  // whole scale blocks a row
-  while ((1 << p.pass_cols) < U && (32 << p.pass_cols) < p.chunks) ++p.pass_cols;
-  p.pieces = (unsigned)ceil_div(p.chunks, 32 << p.pass_cols);
-  const long long lines = ceil_div(p.rows, (long long)(U >> p.pass_cols) << p.lane_rows);
-  const long long blocks = ceil_div(lines * p.pieces, 8);
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_train(back ? dequantize_kernel<T, ANY> : quantize_kernel<T, ANY>, dim3((unsigned)blocks),
+  p.walk = walk_of(p.walk.rows, (int)ceil_div(p.cols, kVec<T>), kScaleBlock / kVec<T>);
+  if (p.walk.blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_train(back ? dequantize_kernel<T, ANY> : quantize_kernel<T, ANY>, dim3((unsigned)p.walk.blocks),
                       dim3(256), 0, st, p);
 }
 
@@ -172,7 +139,7 @@ int b2g_quantize8(int dtype, long long rows, int cols, const void* x, long long 
   const int rc = check(dtype, rows, cols, x, ldx, codes, ldq, scales, lds);
   if (rc || rows == 0 || cols == 0) return rc;
   return convert(false, dtype,
-                 Convert{rows, cols, 0, 0, 0, 0, const_cast<void*>(x), ldx,
+                 Convert{{rows}, cols, const_cast<void*>(x), ldx,
                          {static_cast<unsigned char*>(codes), ldq, static_cast<unsigned char*>(scales), lds, 0}},
                  stream);
 }
@@ -182,7 +149,7 @@ int b2g_dequantize8(int dtype, long long rows, int cols, const void* codes, long
   const int rc = check(dtype, rows, cols, y, ldy, codes, ldq, scales, lds);
   if (rc || rows == 0 || cols == 0) return rc;
   return convert(true, dtype,
-                 Convert{rows, cols, 0, 0, 0, 0, y, ldy,
+                 Convert{{rows}, cols, y, ldy,
                          {static_cast<unsigned char*>(const_cast<void*>(codes)), ldq,
                           static_cast<unsigned char*>(const_cast<void*>(scales)), lds, 0}},
                  stream);

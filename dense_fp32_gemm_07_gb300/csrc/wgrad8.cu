@@ -41,7 +41,7 @@ struct Dw8Gemm {
   int tiles_m, tiles_n, k_tiles;
   int tile_n;                // columns of a tile: 256, or 128
   int full, rest;            // whole tiles a pair; tiles that remain
-  long long piece;           // k tiles of a pair's piece of the rest
+  unsigned piece;            // k tiles of a pair's piece of the rest
   int split;                 // pieces leave sums
   int group;                 // k tiles that add up in tensor memory before FP32 takes over
   unsigned long long wait_limit_ns;
@@ -68,11 +68,12 @@ __device__ __forceinline__ bool unit_at(const Dw8Gemm& p, int pair, int pairs, i
     return true;
   }
   k -= p.full;
-  const long long all = (long long)p.rest * p.k_tiles;
-  const long long from = pair * p.piece, to = min(from + p.piece, all);
-  const long long tile = from / p.k_tiles, edge = (tile + 1) * p.k_tiles;  // a piece spans two tiles at most
+  // below 76 * 2^25: k tiles of the rest
+  const unsigned kt = (unsigned)p.k_tiles, all = (unsigned)p.rest * kt;
+  const unsigned from = pair * p.piece, to = min(from + p.piece, all);
+  const unsigned tile = from / kt, edge = (tile + 1) * kt;  // a piece spans two tiles at most
   if (k > 1 || from >= to || (k == 1 && to <= edge)) return false;
-  const long long a = k ? edge : from, b = k ? to : min(to, edge), base = (tile + k) * p.k_tiles;
+  const unsigned a = k ? edge : from, b = k ? to : min(to, edge), base = (tile + k) * kt;
   u = Unit{p.full * pairs + (int)tile + k, (int)(a - base), (int)(b - base), p.split ? 2 * pair + k : -1};
   return true;
 }
@@ -300,26 +301,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The remaining tiles' results: their pieces' sums, added in the order of k.
-// Block (t, y): rows 4y .. 4y + 3 of tile t.
-template <typename T>
+// The remaining tiles' results: their pieces' sums, added in the order of k.  Block (t, y) takes
+// four rows of tile t, one 64 threads; where a tile has many pieces (MANY), one row, whose pieces
+// the four groups of 64 threads take in turns before their four sums are added in order.
+template <typename T, bool MANY>
 __global__ void __launch_bounds__(256) dw8_join_kernel(const __grid_constant__ Dw8Gemm p,
                                                        const float* part, int pairs) {
+  __shared__ float4 sums[MANY ? 256 : 1];
   pdl_launch_dependents();
-  pdl_wait();
-  const int t = blockIdx.x, row = blockIdx.y * 4 + (threadIdx.x >> 6), col = (threadIdx.x & 63) * 4;
+  const int t = blockIdx.x, q = threadIdx.x >> 6, col = (threadIdx.x & 63) * 4;
+  const int row = MANY ? blockIdx.y : blockIdx.y * 4 + q;
   int tm, tn;
   tile_at(p, p.full * pairs + t, tm, tn);
   const int r = tm * kTile + row, c = tn * p.tile_n + col;
-  if (r >= p.rows || c >= p.cols || col >= p.tile_n) return;
-  const long long from = (long long)t * p.k_tiles, last = (from + p.k_tiles - 1) / p.piece;
+  const bool in = r < p.rows && c < p.cols && col < p.tile_n;
+  const unsigned from = (unsigned)t * p.k_tiles, first = from / p.piece;
+  const unsigned n = (from + p.k_tiles - 1) / p.piece - first + 1;
+  // the first piece began before the tile: its second fragment
+  const float* at = part + ((size_t)2 * first * kTile + row) * p.tile_n + col;
+  const size_t step = (size_t)2 * kTile * p.tile_n, shift = first * p.piece < from ? step / 2 : 0;
+  pdl_wait();
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (in) {
 #pragma unroll 4
-  for (long long i = from / p.piece; i <= last; ++i) {
-    const long long slot = 2 * i + (i * p.piece < from ? 1 : 0);
-    const float4 v = *reinterpret_cast<const float4*>(part + (slot * kTile + row) * p.tile_n + col);
-    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    for (unsigned i = MANY ? q : 0; i < n; i += MANY ? 4 : 1) {
+      const float4 v = *reinterpret_cast<const float4*>(at + i * step + (i == 0 ? shift : 0));
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
   }
+  if constexpr (MANY) {
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    if (q) return;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      const float4 v = sums[threadIdx.x + 64 * i];
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+  }
+  if (!in) return;
   T* o = static_cast<T*>(p.out) + (long long)r * p.ldo + c;
   const float f[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
@@ -329,10 +349,10 @@ __global__ void __launch_bounds__(256) dw8_join_kernel(const __grid_constant__ D
 
 // ---------------------------------------------------------------- operands
 
-// x from its 8-bit form to BF16 rows of ldo elements (zeros past the width), and dy to
-// `planes` BF16 planes where it cannot be read as it is (planes == 0: it is).  Eight
-// columns a thread.
+// x from its 8-bit form to BF16 rows, and dy to `planes` BF16 planes where it cannot be read
+// as it is.  The first blocks work on x.
 struct Prepare {
+  Walk wx, wd;  // wd.blocks == 0: dy is read as it is
   int tokens;
   Rows8 k;
   int width;
@@ -347,41 +367,60 @@ struct Prepare {
 
 template <typename T>
 __global__ void __launch_bounds__(256) dw8_prepare_kernel(const __grid_constant__ Prepare p) {
+  constexpr int V = kVec<T>;
   pdl_launch_dependents();
+  const bool second = blockIdx.x >= p.wx.blocks;
+  const Walk& walk = second ? p.wd : p.wx;
+  const Places at(walk, second ? blockIdx.x - p.wx.blocks : blockIdx.x);
   pdl_wait();
-  const long long gx = p.ldx / 8, gd = p.planes ? p.ldd / 8 : 0;
-  const long long nx = gx * p.tokens, total = nx + gd * p.tokens;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (long long)gridDim.x * 256) {
-    if (i < nx) {
-      const long long row = i / gx;
-      const int c = (int)(i - row * gx) * 8;
-      Codes<8> codes;
-      load_codes<8, true>(codes, p.k, row, c / 8, p.width);
-      const float s = scale_value(p.k.s[row * p.k.lds + c / kScaleBlock]);
-      float f[8];
-      codes.get(f);
+  auto in = [&](int u) { return at.row_of(u) < walk.rows && at.chunk_of(u) < walk.chunks; };
+  if (!second) {
+    Codes<8> k[kPasses];
+    uint32_t byte[kPasses];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] *= s;
-      Pack<Bf16, 8> o;
-      o.set(f);
-      o.store(p.x + row * p.ldx + c);
-    } else {
-      const long long at = i - nx, row = at / gd;
-      const int c = (int)(at - row * gd) * 8;
-      const T* y = static_cast<const T*>(p.dy) + row * p.lddy + c;
-      float f[8];
+    for (int u = 0; u < kPasses; ++u) {
+      const long long row = at.row_of(u);
+      const int c = at.chunk_of(u);
+      if (in(u)) {
+        load_codes<8, true>(k[u], p.k, row, c, p.width);
+        byte[u] = p.k.s[row * p.k.lds + c / (kScaleBlock / 8)];
+      }
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = c + j < p.outs ? to_f32(y[j]) : 0.f;
-      for (int pl = 0; pl < p.planes; ++pl) {
-        uint32_t w[4];
+    for (int u = 0; u < kPasses; ++u) {
+      if (in(u)) {
+        const float s = scale_value(byte[u]);
+        float f[8];
+        k[u].get(f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = p.planes == 1 ? pack_bf16(f[2 * j], f[2 * j + 1])
-                 : pl == 0     ? split_plane<true>(f[2 * j], f[2 * j + 1])
-                               : split_plane<false>(f[2 * j], f[2 * j + 1]);
-        *reinterpret_cast<uint4*>(p.d + (pl * (long long)p.tokens + row) * p.ldd + c) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+        for (int j = 0; j < 8; ++j) f[j] *= s;
+        Pack<Bf16, 8> o;
+        o.set(f);
+        o.store(p.x + at.row_of(u) * p.ldx + at.chunk_of(u) * 8);
+      }
+    }
+  } else {
+    Fetched raw[kPasses];
+    auto row_of = [&](int u) { return static_cast<const T*>(p.dy) + at.row_of(u) * p.lddy; };
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) fetch<T>(raw[u], row_of(u), at.chunk_of(u) * V, p.outs, in(u));
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) {
+      Pack<T, V> k;
+      finish<T>(k, raw[u], row_of(u), at.chunk_of(u) * V, p.outs, in(u));
+      if (!in(u)) continue;
+      Bf16* to = p.d + at.row_of(u) * p.ldd + at.chunk_of(u) * V;
+      if constexpr (V == 8) {
+        *reinterpret_cast<uint4*>(to) = k.u;
+      } else {
+        float f[4];
+        k.get(f);
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) {
+          const uint32_t a = pl == 0 ? split_plane<true>(f[0], f[1]) : split_plane<false>(f[0], f[1]);
+          const uint32_t b = pl == 0 ? split_plane<true>(f[2], f[3]) : split_plane<false>(f[2], f[3]);
+          *reinterpret_cast<uint2*>(to + (long long)pl * p.tokens * p.ldd) = make_uint2(a, b);
+        }
       }
     }
   }
@@ -524,8 +563,10 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
   q.k.vec = codes_vec(q.k, 8);
   q.dy = dy, q.lddy = lddy, q.outs = outs, q.planes = l.copy_dy ? l.planes : 0;
   q.d = reinterpret_cast<Bf16*>(ws + l.d), q.ldd = l.ldd;
-  const long long blocks = ceil_div((l.ldx + (l.copy_dy ? l.ldd : 0)) / 8 * tokens, 256);
-  const dim3 grid((unsigned)(blocks < 16LL * d.sms ? blocks : 16LL * d.sms));
+  q.wx = walk_of(tokens, (int)ceil_div(width, 8), 1);
+  if (l.copy_dy) q.wd = walk_of(tokens, (int)ceil_div(outs, f32 ? 4 : 8), 1);
+  if (q.wx.blocks + q.wd.blocks > 0x7fffffffLL) return B2G_ERR_INVALID_DIM;
+  const dim3 grid((unsigned)(q.wx.blocks + q.wd.blocks));
   rc = launch_code(f32 ? launch_train(dw8_prepare_kernel<float>, grid, dim3(256), 0, st, q)
                        : launch_train(dw8_prepare_kernel<Bf16>, grid, dim3(256), 0, st, q));
   if (rc) return rc;
@@ -533,7 +574,7 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
   Dw8Gemm g = {};
   g.rows = outs, g.cols = width;
   g.tiles_m = l.tiles_m, g.tiles_n = l.tiles_n, g.k_tiles = l.k_tiles, g.tile_n = l.tile_n;
-  g.full = l.full, g.rest = l.rest, g.piece = l.piece, g.split = l.split;
+  g.full = l.full, g.rest = l.rest, g.piece = (unsigned)l.piece, g.split = l.split;
   g.group = f32 ? 4 : kGroupK / kBK;
   g.wait_limit_ns = d.wait_limit_ns, g.debug_stop = d.debug_stop, g.status = d.status;
   g.out = dw, g.ldo = lddw, g.out_bf16 = !f32, g.accumulate = accumulate != 0;
@@ -554,11 +595,13 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
   if (rc) return rc;
   rc = f32 ? launch<3>(g, maps, l.pairs, d, st) : launch<1>(g, maps, l.pairs, d, st);
   if (rc || !l.split) return rc;
-  const dim3 tiles((unsigned)l.rest, kTile / 4);
-  return launch_code(f32 ? launch_train(dw8_join_kernel<float>, tiles, dim3(256), 0, st, g,
-                                        (const float*)part, l.pairs)
-                         : launch_train(dw8_join_kernel<Bf16>, tiles, dim3(256), 0, st, g,
-                                        (const float*)part, l.pairs));
+  const bool many = l.k_tiles / l.piece > 6;
+  const dim3 tiles((unsigned)l.rest, many ? kTile : kTile / 4);
+  auto join = [&](auto kernel) {
+    return launch_code(launch_train(kernel, tiles, dim3(256), 0, st, g, (const float*)part, l.pairs));
+  };
+  if (f32) return many ? join(dw8_join_kernel<float, true>) : join(dw8_join_kernel<float, false>);
+  return many ? join(dw8_join_kernel<Bf16, true>) : join(dw8_join_kernel<Bf16, false>);
 }
 
 }  // extern "C"
