@@ -349,10 +349,10 @@ __global__ void __launch_bounds__(256) dw8_join_kernel(const __grid_constant__ D
 
 // ---------------------------------------------------------------- operands
 
-// x from its 8-bit form to BF16 rows, and dy to `planes` BF16 planes where it cannot be read
-// as it is.  The first blocks work on x.
+// x from its 8-bit form to BF16 rows, and (DY) dy to `planes` BF16 planes where it cannot be
+// read as it is.  The first blocks work on x.
 struct Prepare {
-  Walk wx, wd;  // wd.blocks == 0: dy is read as it is
+  Walk wx, wd;
   int tokens;
   Rows8 k;
   int width;
@@ -365,11 +365,11 @@ struct Prepare {
   long long ldd;
 };
 
-template <typename T>
+template <typename T, bool DY>
 __global__ void __launch_bounds__(256) dw8_prepare_kernel(const __grid_constant__ Prepare p) {
   constexpr int V = kVec<T>;
   pdl_launch_dependents();
-  const bool second = blockIdx.x >= p.wx.blocks;
+  const bool second = DY && blockIdx.x >= p.wx.blocks;
   const Walk& walk = second ? p.wd : p.wx;
   const Places at(walk, second ? blockIdx.x - p.wx.blocks : blockIdx.x);
   pdl_wait();
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(256) dw8_prepare_kernel(const __grid_constant_
         o.store(p.x + at.row_of(u) * p.ldx + at.chunk_of(u) * 8);
       }
     }
-  } else {
+  } else if constexpr (DY) {
     Fetched raw[kPasses];
     auto row_of = [&](int u) { return static_cast<const T*>(p.dy) + at.row_of(u) * p.lddy; };
 #pragma unroll
@@ -567,8 +567,9 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
   if (l.copy_dy) q.wd = walk_of(tokens, (int)ceil_div(outs, f32 ? 4 : 8), 1);
   if (q.wx.blocks + q.wd.blocks > 0x7fffffffLL) return B2G_ERR_INVALID_DIM;
   const dim3 grid((unsigned)(q.wx.blocks + q.wd.blocks));
-  rc = launch_code(f32 ? launch_train(dw8_prepare_kernel<float>, grid, dim3(256), 0, st, q)
-                       : launch_train(dw8_prepare_kernel<Bf16>, grid, dim3(256), 0, st, q));
+  rc = launch_code(f32 ? launch_train(dw8_prepare_kernel<float, true>, grid, dim3(256), 0, st, q)
+                   : l.copy_dy ? launch_train(dw8_prepare_kernel<Bf16, true>, grid, dim3(256), 0, st, q)
+                               : launch_train(dw8_prepare_kernel<Bf16, false>, grid, dim3(256), 0, st, q));
   if (rc) return rc;
 
   Dw8Gemm g = {};
