@@ -11,7 +11,8 @@
 // accumulators in tensor memory, double buffered).  As many tiles as fill all pairs are
 // whole; the k range of the rest, taken one after another, is cut into equal pieces, one a
 // pair, so that all pairs end together.  A piece that is not a whole tile leaves FP32 sums,
-// which a last kernel adds in order.
+// which a last kernel adds in order: straight from registers, 32 rows x 4 columns (512 bytes)
+// at a time, the order in which a warp holds them.
 #include <atomic>
 
 #include "eightbit.cuh"
@@ -42,6 +43,7 @@ struct Dw8Gemm {
   int tile_n;                // columns of a tile: 256, or 128
   int full, rest;            // whole tiles a pair; tiles that remain
   unsigned piece;            // k tiles of a pair's piece of the rest
+  unsigned span;             // k tiles that a tile of the rest counts for: its own, or whole pieces
   int split;                 // pieces leave sums
   int group;                 // k tiles that add up in tensor memory before FP32 takes over
   unsigned long long wait_limit_ns;
@@ -52,9 +54,10 @@ struct Dw8Gemm {
   void* out;
   long long ldo;
   int out_bf16, accumulate;
+  float* part;               // the sums, [slot][16 warps][columns / 4][32 rows][4]
 };
 struct alignas(64) Dw8Maps {
-  CUtensorMap dy, x, out, part;
+  CUtensorMap dy, x, out;
 };
 
 struct Unit {
@@ -68,12 +71,12 @@ __device__ __forceinline__ bool unit_at(const Dw8Gemm& p, int pair, int pairs, i
     return true;
   }
   k -= p.full;
-  // below 76 * 2^25: k tiles of the rest
-  const unsigned kt = (unsigned)p.k_tiles, all = (unsigned)p.rest * kt;
+  const unsigned all = (unsigned)p.rest * p.span;  // below 2^32
   const unsigned from = pair * p.piece, to = min(from + p.piece, all);
-  const unsigned tile = from / kt, edge = (tile + 1) * kt;  // a piece spans two tiles at most
+  const unsigned tile = from / p.span, edge = (tile + 1) * p.span;  // a piece spans two tiles at most
   if (k > 1 || from >= to || (k == 1 && to <= edge)) return false;
-  const unsigned a = k ? edge : from, b = k ? to : min(to, edge), base = (tile + k) * kt;
+  const unsigned a = k ? edge : from, base = (tile + k) * p.span;
+  const unsigned b = min(k ? to : min(to, edge), base + p.k_tiles);
   u = Unit{p.full * pairs + (int)tile + k, (int)(a - base), (int)(b - base), p.split ? 2 * pair + k : -1};
   return true;
 }
@@ -91,15 +94,22 @@ __device__ __forceinline__ int groups_of(const Dw8Gemm& p, int kts) {
   return (kts + p.group - 1) / p.group;
 }
 
-// This warp's columns of rows row0 .. row0 + 31 of a finished tile to the result, or to
-// the sums in `slot`.
-__device__ __forceinline__ void put_tile(const Dw8Gemm& p, const Dw8Maps& maps, float (&v)[128],
-                                         int row0, int local_row, int n0, int local_n, int left,
-                                         int slot, uint32_t buf, int lane) {
-  if (row0 >= p.rows || left <= 0) return;
-  if (slot >= 0 || (p.out_tma && !p.out_bf16)) {
-    const CUtensorMap* m = slot >= 0 ? &maps.part : &maps.out;
-    const int x = slot >= 0 ? local_n : n0, y = slot >= 0 ? slot * kTile + local_row : row0;
+// Where a slot's sums of a warp's 32 rows (block `rows` of 8) and columns (`half` of 2) begin;
+// four columns of its 32 rows follow one another.
+__device__ __forceinline__ size_t sums_at(unsigned slot, int rows, int half, int tile_n) {
+  return ((size_t)slot * 16 + rows * 2 + half) * (32 * (tile_n / 2));
+}
+__device__ __forceinline__ void put_sums(float* part, const float (&v)[128], int left, int lane) {
+  float4* to = reinterpret_cast<float4*>(part) + lane;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (4 * j < left) to[32 * j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+
+// This warp's columns of rows row0 .. row0 + 31 of a finished tile to the result.
+__device__ __forceinline__ void put_tile(const Dw8Gemm& p, const CUtensorMap* m, float (&v)[128], int row0,
+                                         int n0, int left, uint32_t buf, int lane) {
+  if (p.out_tma && !p.out_bf16) {
 #pragma unroll
     for (int c = 0; c < 128; c += 32) {
       if (c < left) {
@@ -108,7 +118,7 @@ __device__ __forceinline__ void put_tile(const Dw8Gemm& p, const Dw8Maps& maps, 
         for (int j = 0; j < 8; ++j)
           w[j] = make_uint4(__float_as_uint(v[c + 4 * j]), __float_as_uint(v[c + 4 * j + 1]),
                             __float_as_uint(v[c + 4 * j + 2]), __float_as_uint(v[c + 4 * j + 3]));
-        store_rows(buf, m, x + c, y, 0, w, slot < 0 && p.add, lane);
+        store_rows(buf, m, n0 + c, row0, 0, w, p.add, lane);
       }
     }
   } else if (p.out_tma) {
@@ -122,7 +132,7 @@ __device__ __forceinline__ void put_tile(const Dw8Gemm& p, const Dw8Maps& maps, 
           w[j] = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
                             pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
         }
-        store_rows(buf, &maps.out, n0 + c, row0, 0, w, false, lane);
+        store_rows(buf, m, n0 + c, row0, 0, w, false, lane);
       }
     }
   } else if (p.out_bf16) {
@@ -285,9 +295,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       int tm, tn;
       tile_at(p, u.tile, tm, tn);
-      const int local_row = (int)rank * 128 + 32 * q, n0 = tn * p.tile_n + half * span;
-      put_tile(p, maps, acc, tm * kTile + local_row, local_row, n0, half * span,
-               min(span, p.cols - n0), u.slot, buf, lane);
+      const int rows = (int)rank * 4 + q, row0 = tm * kTile + 32 * rows, n0 = tn * p.tile_n + half * span;
+      const int left = min(span, p.cols - n0);
+      if (row0 < p.rows && left > 0) {
+        if (u.slot >= 0)
+          put_sums(p.part + sums_at(u.slot, rows, half, p.tile_n), acc, left, lane);
+        else
+          put_tile(p, &maps.out, acc, row0, n0, left, buf, lane);
+      }
     }
     if (lane == 0) stores_done();
   }
@@ -301,50 +316,85 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The remaining tiles' results: their pieces' sums, added in the order of k.  Block (t, y) takes
-// four rows of tile t, one 64 threads; where a tile has many pieces (MANY), one row, whose pieces
-// the four groups of 64 threads take in turns before their four sums are added in order.
+// The remaining tiles' results: their pieces' sums, added in the order of k.  Block (t, y, z)
+// takes 32 of the columns and all 32 rows that one warp y of tile t left, four columns a warp;
+// where a tile has more than kFewPieces pieces (MANY), 16 columns, and two warps each half of
+// the pieces, one and the next in turns.  The results leave through shared memory, row by row.
+constexpr int kFewPieces = 8;
+template <bool MANY>
+constexpr int kJoinCols = MANY ? 16 : 32;
 template <typename T, bool MANY>
-__global__ void __launch_bounds__(256) dw8_join_kernel(const __grid_constant__ Dw8Gemm p,
-                                                       const float* part, int pairs) {
-  __shared__ float4 sums[MANY ? 256 : 1];
+__global__ void __launch_bounds__(256) dw8_join_kernel(const __grid_constant__ Dw8Gemm p, int pairs) {
+  constexpr int kCols = kJoinCols<MANY>, kPitch = kCols + 4;
+  __shared__ __align__(16) float sm[(MANY ? 2 : 1) * 32 * kPitch];
   pdl_launch_dependents();
-  const int t = blockIdx.x, q = threadIdx.x >> 6, col = (threadIdx.x & 63) * 4;
-  const int row = MANY ? blockIdx.y : blockIdx.y * 4 + q;
+  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int span = p.tile_n / 2, rows = blockIdx.y >> 1, half = blockIdx.y & 1;
+  const int j0 = blockIdx.z * kCols;  // the block's first column
   int tm, tn;
   tile_at(p, p.full * pairs + t, tm, tn);
-  const int r = tm * kTile + row, c = tn * p.tile_n + col;
-  const bool in = r < p.rows && c < p.cols && col < p.tile_n;
-  const unsigned from = (unsigned)t * p.k_tiles, first = from / p.piece;
+  const int r0 = tm * kTile + 32 * rows, c0 = tn * p.tile_n + half * span + j0;
+  const int left = min(min(span - j0, kCols), p.cols - c0);
+  if (r0 >= p.rows || left <= 0) return;
+  const unsigned from = (unsigned)t * p.span, first = from / p.piece;
   const unsigned n = (from + p.k_tiles - 1) / p.piece - first + 1;
-  // the first piece began before the tile: its second fragment
-  const float* at = part + ((size_t)2 * first * kTile + row) * p.tile_n + col;
-  const size_t step = (size_t)2 * kTile * p.tile_n, shift = first * p.piece < from ? step / 2 : 0;
+  // a piece that began before the tile: its second fragment
+  const unsigned shift = first * p.piece < from ? 1 : 0;
+  const size_t step = sums_at(2, 0, 0, p.tile_n);
+  const float* at = p.part + sums_at(2 * first, rows, half, p.tile_n) + j0 * 32 + lane * 4;
   pdl_wait();
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (in) {
-#pragma unroll 4
-    for (unsigned i = MANY ? q : 0; i < n; i += MANY ? 4 : 1) {
-      const float4 v = *reinterpret_cast<const float4*>(at + i * step + (i == 0 ? shift : 0));
-      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+  const int j = MANY ? warp & 3 : warp, mine = MANY ? warp >> 2 : 0;  // columns 4 j ..
+  if (4 * j < left) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto sum = [&](unsigned i) {
+      return *reinterpret_cast<const float4*>(at + j * 128 + i * step +
+                                              (i == 0 && shift ? sums_at(1, 0, 0, p.tile_n) : 0));
+    };
+    auto add = [&](const float4& v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
+    if constexpr (MANY) {
+#pragma unroll 8
+      for (unsigned i = mine; i < n; i += 2) add(sum(i));
+    } else {
+      float4 v[kFewPieces];
+#pragma unroll
+      for (int i = 0; i < kFewPieces; ++i)
+        if (i < n) v[i] = sum(i);
+#pragma unroll
+      for (int i = 0; i < kFewPieces; ++i)
+        if (i < n) add(v[i]);
+    }
+    *reinterpret_cast<float4*>(sm + (mine * 32 + lane) * kPitch + 4 * j) = s;
+  }
+  __syncthreads();
+  // the rows: 4 columns a lane where they can be written together
+  const int rows_left = min(32, p.rows - r0);
+  T* out = static_cast<T*>(p.out) + (long long)r0 * p.ldo + c0;
+  const bool vec = (reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.ldo * sizeof(T))) % (4 * sizeof(T)) == 0;
+  constexpr int kLanes = kCols / 4;  // lanes a row
+  for (int i = threadIdx.x / kLanes; i < rows_left; i += 256 / kLanes) {
+    const int c = (threadIdx.x % kLanes) * 4;
+    float f[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] = sm[i * kPitch + c + e];
+      if (MANY) f[e] += sm[(32 + i) * kPitch + c + e];
+    }
+    T* o = out + (long long)i * p.ldo + c;
+    if (vec && c + 4 <= left) {
+      if (p.accumulate) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] += to_f32(o[e]);
+      }
+      if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(o) = make_float4(f[0], f[1], f[2], f[3]);
+      else
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < left) o[e] = from_f32<T>(p.accumulate ? f[e] + to_f32(o[e]) : f[e]);
     }
   }
-  if constexpr (MANY) {
-    sums[threadIdx.x] = s;
-    __syncthreads();
-    if (q) return;
-#pragma unroll
-    for (int i = 1; i < 4; ++i) {
-      const float4 v = sums[threadIdx.x + 64 * i];
-      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-    }
-  }
-  if (!in) return;
-  T* o = static_cast<T*>(p.out) + (long long)r * p.ldo + c;
-  const float f[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (c + j < p.cols) o[j] = from_f32<T>(p.accumulate ? f[j] + to_f32(o[j]) : f[j]);
 }
 
 // ---------------------------------------------------------------- operands
@@ -443,34 +493,49 @@ struct Layout {
   bool copy_dy;
   long long ldx, ldd;
   int tile_n, tiles_m, tiles_n, k_tiles, pairs, full, rest;
-  long long piece;
+  long long piece, span;
   bool split;
   size_t x, d, part, total;
 };
 
 // Cycles of a k tile: BF16 its copies (64 bytes a cycle and SM), FP32 its three products.
-// Leaving sums costs about 6000 more, for the launch that adds them.
-long long k_tile_cost(int planes, int tile_n) { return planes == 1 ? kTile + tile_n : 1600; }
-constexpr long long kJoinCost = 6000;
+long long k_tile_cost(int planes, int tile_n) { return planes == 1 ? kTile + tile_n : 1900; }
+// Leaving sums instead of a result, and a second time; the launch that adds them, and for each
+// piece.  2048 tokens on 1024 x 1024 BF16, us without the operands' preparation: whole tiles
+// 14.3; each cut in 2, 3, 4: 14.7, 13.8, 13.1; one piece a pair across tiles 15.3.
+constexpr long long kSumCost = 2200, kSecondCost = 4500, kJoinCost = 3000, kJoinPiece = 90;
 
 // false: more tiles than can be counted.
 bool layout(int dtype, int tokens, int outs, int width, const void* dy, long long lddy, Layout& l) {
   l.planes = dtype == B2G_F32 ? 3 : 1;
   l.copy_dy = dtype == B2G_F32 || !vec16(dy) || lddy % 8;
-  l.ldx = (long long)round_up(width, 8), l.ldd = (long long)round_up(outs, 8);
+  // the copies' rows on 128-byte lines: off them a k tile of BF16 takes twice as long
+  l.ldx = (long long)round_up(width, 64), l.ldd = (long long)round_up(outs, 64);
   l.tile_n = width > 128 ? 256 : 128;
   l.k_tiles = (int)ceil_div(tokens, kBK);
   l.tiles_m = (int)ceil_div(outs, kTile), l.tiles_n = (int)ceil_div(width, l.tile_n);
   const long long tiles = (long long)l.tiles_m * l.tiles_n;
   if (tiles > 0x3fffffffLL) return false;
   l.full = (int)(tiles / kPairs), l.rest = (int)(tiles % kPairs);
-  const long long all = (long long)l.rest * l.k_tiles;
-  l.piece = l.k_tiles, l.split = false;
-  if (all) {
-    const long long least = ceil_div(all, kPairs);
-    if ((l.k_tiles - least) * k_tile_cost(l.planes, l.tile_n) > kJoinCost) l.piece = least, l.split = true;
+  // The rest: a tile a pair; each tile cut into the same pieces; or all of their k cut into
+  // one piece a pair, some of which then lie across two tiles and leave two sums.
+  l.piece = l.span = l.k_tiles, l.split = false;
+  long long pieces = l.rest;
+  if (l.rest) {
+    const long long kt = k_tile_cost(l.planes, l.tile_n);
+    long long best = l.k_tiles * kt;
+    const long long slices = kPairs / l.rest;
+    for (long long s = 2; s <= slices && s <= l.k_tiles; ++s) {
+      const long long len = ceil_div(l.k_tiles, s), used = ceil_div(l.k_tiles, len);
+      const long long cost = len * kt + kSumCost + kJoinCost + l.rest * used * kJoinPiece;
+      if (cost < best) best = cost, l.piece = len, l.span = len * used, l.split = true, pieces = l.rest * used;
+    }
+    const long long len = ceil_div((long long)l.rest * l.k_tiles, kPairs);
+    const long long n = ceil_div((long long)l.rest * l.k_tiles, len);
+    const long long cost = len * kt + kSumCost + kSecondCost + kJoinCost + (n + l.rest) * kJoinPiece;
+    if (len < l.k_tiles && cost < best) l.piece = len, l.span = l.k_tiles, l.split = true, pieces = n;
   }
-  l.pairs = l.full ? kPairs : (int)ceil_div(all, l.piece);
+  l.pairs = l.full ? kPairs : (int)pieces;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -479,7 +544,7 @@ bool layout(int dtype, int tokens, int outs, int width, const void* dy, long lon
   };
   l.x = take((size_t)tokens * l.ldx * 2);
   l.d = l.copy_dy ? take((size_t)l.planes * tokens * l.ldd * 2) : 0;
-  l.part = l.split ? take((size_t)2 * ceil_div(all, l.piece) * kTile * l.tile_n * 4) : 0;
+  l.part = l.split ? take((size_t)2 * pieces * kTile * l.tile_n * 4) : 0;
   l.total = at;
   return true;
 }
@@ -575,7 +640,8 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
   Dw8Gemm g = {};
   g.rows = outs, g.cols = width;
   g.tiles_m = l.tiles_m, g.tiles_n = l.tiles_n, g.k_tiles = l.k_tiles, g.tile_n = l.tile_n;
-  g.full = l.full, g.rest = l.rest, g.piece = (unsigned)l.piece, g.split = l.split;
+  g.full = l.full, g.rest = l.rest, g.piece = (unsigned)l.piece, g.span = (unsigned)l.span, g.split = l.split;
+  g.part = reinterpret_cast<float*>(ws + l.part);
   g.group = f32 ? 4 : kGroupK / kBK;
   g.wait_limit_ns = d.wait_limit_ns, g.debug_stop = d.debug_stop, g.status = d.status;
   g.out = dw, g.ldo = lddw, g.out_bf16 = !f32, g.accumulate = accumulate != 0;
@@ -583,23 +649,20 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
   // adds in the output's type: right for FP32 only
   g.out_tma = vec16(dw) && vec16_ld(lddw, dtype) && vec16_ld(width, dtype) && !(accumulate && !f32);
   g.add = accumulate != 0;
-  float* part = reinterpret_cast<float*>(ws + l.part);
   Dw8Maps maps = {};
   rc = l.copy_dy ? encode_rows(&maps.dy, false, q.d, outs, tokens, l.ldd, l.planes,
                                (long long)tokens * l.ldd, 64)
                  : encode_rows(&maps.dy, false, dy, outs, tokens, lddy, 1, 0, 64);
   if (!rc) rc = encode_rows(&maps.x, false, q.x, width, tokens, l.ldx, 1, 0, 64);
   if (!rc && g.out_tma) rc = encode_rows(&maps.out, f32, dw, width, outs, lddw, 1, 0, 32);
-  if (!rc && l.split)
-    rc = encode_rows(&maps.part, true, part, l.tile_n,
-                     2 * ceil_div((long long)l.rest * l.k_tiles, l.piece) * kTile, l.tile_n, 1, 0, 32);
   if (rc) return rc;
   rc = f32 ? launch<3>(g, maps, l.pairs, d, st) : launch<1>(g, maps, l.pairs, d, st);
   if (rc || !l.split) return rc;
-  const bool many = l.k_tiles / l.piece > 6;
-  const dim3 tiles((unsigned)l.rest, many ? kTile : kTile / 4);
+  // of a tile; one more where pieces lie across tiles
+  const bool many = ceil_div(l.k_tiles, l.piece) + (l.span % l.piece ? 1 : 0) > kFewPieces;
+  const dim3 blocks((unsigned)l.rest, 16, (unsigned)(l.tile_n / 2 / (many ? kJoinCols<true> : kJoinCols<false>)));
   auto join = [&](auto kernel) {
-    return launch_code(launch_train(kernel, tiles, dim3(256), 0, st, g, (const float*)part, l.pairs));
+    return launch_code(launch_train(kernel, blocks, dim3(256), 0, st, g, l.pairs));
   };
   if (f32) return many ? join(dw8_join_kernel<float, true>) : join(dw8_join_kernel<float, false>);
   return many ? join(dw8_join_kernel<Bf16, true>) : join(dw8_join_kernel<Bf16, false>);
