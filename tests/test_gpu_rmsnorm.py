@@ -128,6 +128,8 @@ def test_without_weight_and_residual(b2g, rows, cols, dtype):
     none, total, rstd, y8, t8 = b2g.rms_norm_8bit(x)
     assert none is None and t8 is None and total is x
     check_y8(y8, *check_forward(x, None, None, None, total, rstd))
+    kept = b2g.rms_norm_8bit(x, keep_total=True)[4]
+    assert all(e8.same_bytes(a, b) for a, b in zip(kept, b2g.quantize_8bit(x)))
     if dtype is F32:
         got = b2g.rms_norm_8bit(x, with_y=True)
         assert all(e8.same_bytes(a, b) for a, b in zip(got[3], b2g.quantize_8bit(got[0])))
