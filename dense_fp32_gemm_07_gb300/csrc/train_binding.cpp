@@ -351,11 +351,18 @@ struct Eight {
   int64_t rows, cols;
   long long ldq, lds;
 
-  // New ones, rows on 16-byte boundaries.
+  // New ones, rows on 16-byte boundaries, in one piece of memory: they live together.
   Eight(const Kind& k, int64_t r, int64_t c) : rows(r), cols(c), ldq((c + 15) / 16 * 16), lds((c + 31) / 32) {
-    q = k.empty({r, (int64_t)ldq}, at::kFloat8_e4m3fn);
-    if (ldq != c) q = q.narrow(1, 0, c);
-    s = k.empty({r, (int64_t)lds}, at::kFloat8_e8m0fnu);
+    const Tensor all = k.bytes((size_t)(r * (ldq + lds)));
+    auto part = [&](at::ScalarType t, int64_t n, int64_t ld, int64_t at) {
+      const Tensor x = at::detail::make_tensor<c10::TensorImpl>(
+          c10::Storage(all.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+          c10::scalarTypeToTypeMeta(t));
+      x.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef{r, n}, at::IntArrayRef{ld, 1}, at);
+      return x;
+    };
+    q = part(at::kFloat8_e4m3fn, c, ldq, 0);
+    s = part(at::kFloat8_e8m0fnu, lds, lds, r * ldq);
   }
   Eight(const Tensor& codes, const Tensor& scales) : q(codes), s(scales) {}
   // Whether given ones are on the kind's device and fit each other.
