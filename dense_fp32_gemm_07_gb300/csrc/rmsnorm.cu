@@ -352,9 +352,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = (t + i * nt) * VEC;
+    float* q = sums + (size_t)group * p.cols + c;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j)
-      if (c + j < p.cols) sums[(size_t)group * p.cols + c + j] = aw[i][j];
+    for (int j = 0; j < VEC; j += 4) {
+      if constexpr (!ANY) {
+        if (c < p.cols)
+          *reinterpret_cast<float4*>(q + j) = make_float4(aw[i][j], aw[i][j + 1], aw[i][j + 2], aw[i][j + 3]);
+      } else {
+#pragma unroll
+        for (int e = j; e < j + 4; ++e)
+          if (c + e < p.cols) q[e] = aw[i][e];
+      }
+    }
   }
   __syncthreads();
   leave_sums<T>(p, sums, groups);
@@ -627,15 +636,17 @@ __global__ void __launch_bounds__(PHASE ? kPhaseThreads : kBwdThreads, 1)
   for (int i = 0; i < NCH; ++i) {
     const int c = first_of(i);
 #pragma unroll
-    for (int j = 0; j < H; ++j) {
+    for (int j = 0; j < H; j += 2) {
       float* q = sums + (size_t)group * p.cols + c + 2 * j;
+      float4 v;
+      f2_split(aw[i][j], v.x, v.y), f2_split(aw[i][j + 1], v.z, v.w);
       if constexpr (PHASE) {
-        float a, b;
-        f2_split(aw[i][j], a, b);
-        if (c + 2 * j >= 0 && c + 2 * j < p.cols) q[0] = a;
-        if (c + 2 * j + 1 >= 0 && c + 2 * j + 1 < p.cols) q[1] = b;
+        const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + 2 * j + e >= 0 && c + 2 * j + e < p.cols) q[e] = f[e];
       } else if (FULL || c < p.cols) {
-        *reinterpret_cast<F2*>(q) = aw[i][j];
+        *reinterpret_cast<float4*>(q) = v;
       }
     }
   }
