@@ -9,10 +9,10 @@
 //
 // The product runs on 256 x 256 tiles of a CTA pair (tcgen05.mma.cta_group::2, FP32
 // accumulators in tensor memory, double buffered).  As many tiles as fill all pairs are
-// whole; the k range of the rest, taken one after another, is cut into equal pieces, one a
-// pair, so that all pairs end together.  A piece that is not a whole tile leaves FP32 sums,
-// which a last kernel adds in order: straight from registers, 32 rows x 4 columns (512 bytes)
-// at a time, the order in which a warp holds them.
+// whole; the rest are whole too, or halves of 128 columns, or their k range is cut into pieces,
+// so that more of the pairs have work to the end.  A piece leaves FP32 sums, which a last
+// kernel adds in order: straight from registers, 32 rows x 4 columns (512 bytes) at a time, the
+// order in which a warp holds them.
 #include <atomic>
 
 #include "eightbit.cuh"
@@ -42,6 +42,7 @@ struct Dw8Gemm {
   int tiles_m, tiles_n, k_tiles;
   int tile_n;                // columns of a tile: 256, or 128
   int full, rest;            // whole tiles a pair; tiles that remain
+  int halves;                // which then go as two of 128 columns
   unsigned piece;            // k tiles of a pair's piece of the rest
   unsigned span;             // k tiles that a tile of the rest counts for: its own, or whole pieces
   int split;                 // pieces leave sums
@@ -61,23 +62,29 @@ struct alignas(64) Dw8Maps {
 };
 
 struct Unit {
-  int tile, kt0, kt1, slot;  // slot: of the sums, -1 for a whole tile
+  int tile, kt0, kt1, slot;  // slot: of the sums, -1 for a result
+  int col, cols;             // its columns of the tile
 };
 
 // The k-th unit of this pair; false: there is none.
 __device__ __forceinline__ bool unit_at(const Dw8Gemm& p, int pair, int pairs, int k, Unit& u) {
   if (k < p.full) {
-    u = Unit{k * pairs + pair, 0, p.k_tiles, -1};
+    u = Unit{k * pairs + pair, 0, p.k_tiles, -1, 0, p.tile_n};
     return true;
   }
   k -= p.full;
+  if (p.halves) {
+    u = Unit{p.full * pairs + (pair >> 1), 0, p.k_tiles, -1, (pair & 1) * 128, 128};
+    return k == 0 && pair < 2 * p.rest;
+  }
   const unsigned all = (unsigned)p.rest * p.span;  // below 2^32
   const unsigned from = pair * p.piece, to = min(from + p.piece, all);
   const unsigned tile = from / p.span, edge = (tile + 1) * p.span;  // a piece spans two tiles at most
   if (k > 1 || from >= to || (k == 1 && to <= edge)) return false;
   const unsigned a = k ? edge : from, base = (tile + k) * p.span;
   const unsigned b = min(k ? to : min(to, edge), base + p.k_tiles);
-  u = Unit{p.full * pairs + (int)tile + k, (int)(a - base), (int)(b - base), p.split ? 2 * pair + k : -1};
+  u = Unit{p.full * pairs + (int)tile + k, (int)(a - base), (int)(b - base), p.split ? 2 * pair + k : -1,
+           0, p.tile_n};
   return true;
 }
 
@@ -201,14 +208,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         int s = 0, issued = 0;
         uint32_t ph = 0;
         const uint32_t full_even = even ? full(0) : mapa_shared(full(0), 0);
-        const bool wide = p.tile_n > 128;
-        const uint32_t tx = 2 * (PLANES * kOperand + (uint32_t)(p.tile_n / 2) * kBK * 2);
         bool on = true;
         Unit u;
         for (int k = 0; on && unit_at(p, pair, pairs, k, u); ++k) {
           int tm, tn;
           tile_at(p, u.tile, tm, tn);
-          const int m0 = tm * kTile + (int)rank * 128, n0 = tn * p.tile_n + (int)rank * (p.tile_n / 2);
+          const int m0 = tm * kTile + (int)rank * 128;
+          const int n0 = tn * p.tile_n + u.col + (int)rank * (u.cols / 2);
+          const bool wide = u.cols > 128;
+          const uint32_t tx = 2 * (PLANES * kOperand + (uint32_t)(u.cols / 2) * kBK * 2);
           for (int kt = u.kt0; kt < u.kt1; ++kt) {
             if ((p.debug_stop >= 0 && issued >= p.debug_stop) ||
                 !wait_phase(empty(s), ph ^ 1u, p, kStatusTimeoutEmpty)) {
@@ -241,12 +249,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ph = 0, aph = 0;
         const uint32_t empty_odd = mapa_shared(empty(0), 1), tfull_odd = mapa_shared(tfull(0), 1);
         const uint32_t a0 = desc_lo<true>(base), b0 = desc_lo<true>(base + PLANES * kOperand);
-        const uint32_t idesc = idesc_bf16(kTile, p.tile_n, true, true);
         constexpr uint32_t step = kDescStep<true>;
         bool on = true;
         Unit u;
         for (int k = 0; on && unit_at(p, pair, pairs, k, u); ++k) {
           const int groups = groups_of(p, u.kt1 - u.kt0);
+          const uint32_t idesc = idesc_bf16(kTile, u.cols, true, true);
           for (int g = 0; on && g < groups; ++g) {
             if (!(on = wait_phase(tempty(a), aph ^ 1u, p, kStatusTimeoutTmem))) break;
             tc_fence_after_sync();
@@ -281,8 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------- epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int q = warp & 3, half = (warp - 4) >> 2;
-    const int span = p.tile_n / 2;  // this warp's columns
-    const uint32_t tmem_row = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * span);
+    const uint32_t tmem_row = tmem + ((uint32_t)(32 * q) << 16);
     const uint32_t buf = outs + (uint32_t)(warp - 4) * kOutBytes;
     const uint32_t tempty_even = even ? 0u : mapa_shared(tempty(0), 0);
     int a = 0;
@@ -290,12 +297,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     Unit u;
     for (int k = 0; unit_at(p, pair, pairs, k, u); ++k) {
       float acc[128];
-      if (!collect(p, acc, tmem_row, span, groups_of(p, u.kt1 - u.kt0), a, aph, tfull(0), tempty(0),
+      const int span = u.cols / 2;  // this warp's columns
+      if (!collect(p, acc, tmem_row + (uint32_t)(half * span), span, groups_of(p, u.kt1 - u.kt0), a, aph, tfull(0), tempty(0),
                    tempty_even, even, lane))
         break;
       int tm, tn;
       tile_at(p, u.tile, tm, tn);
-      const int rows = (int)rank * 4 + q, row0 = tm * kTile + 32 * rows, n0 = tn * p.tile_n + half * span;
+      const int rows = (int)rank * 4 + q, row0 = tm * kTile + 32 * rows;
+      const int n0 = tn * p.tile_n + u.col + half * span;
       const int left = min(span, p.cols - n0);
       if (row0 < p.rows && left > 0) {
         if (u.slot >= 0)
@@ -494,12 +503,16 @@ struct Layout {
   long long ldx, ldd;
   int tile_n, tiles_m, tiles_n, k_tiles, pairs, full, rest;
   long long piece, span;
-  bool split;
+  bool split, halves;
   size_t x, d, part, total;
 };
 
 // Cycles of a k tile: BF16 its copies (64 bytes a cycle and SM), FP32 its three products.
 long long k_tile_cost(int planes, int tile_n) { return planes == 1 ? kTile + tile_n : 1900; }
+// Halves of a tile: their products take as long as the whole one's (2048 tokens on 1024 x 1024
+// BF16: 17.0 us so), but there is half as much to write at the end (300 on 512 x 256: 7.4 us for
+// 8.1; 1000 on 1025 x 777: 15.6 for 17.5).
+constexpr long long kHalfSaves = 1500;
 // Leaving sums instead of a result, and a second time; the launch that adds them, and for each
 // piece.  2048 tokens on 1024 x 1024 BF16, us without the operands' preparation: whole tiles
 // 14.3; each cut in 2, 3, 4: 14.7, 13.8, 13.1; one piece a pair across tiles 15.3.
@@ -517,23 +530,27 @@ bool layout(int dtype, int tokens, int outs, int width, const void* dy, long lon
   const long long tiles = (long long)l.tiles_m * l.tiles_n;
   if (tiles > 0x3fffffffLL) return false;
   l.full = (int)(tiles / kPairs), l.rest = (int)(tiles % kPairs);
-  // The rest: a tile a pair; each tile cut into the same pieces; or all of their k cut into
-  // one piece a pair, some of which then lie across two tiles and leave two sums.
-  l.piece = l.span = l.k_tiles, l.split = false;
+  // The rest: a tile a pair; half a tile a pair; each tile cut into the same pieces; or all of
+  // their k cut into one piece a pair, some of which then lie across two tiles and leave two sums.
+  l.piece = l.span = l.k_tiles, l.split = l.halves = false;
   long long pieces = l.rest;
   if (l.rest) {
     const long long kt = k_tile_cost(l.planes, l.tile_n);
     long long best = l.k_tiles * kt;
+    const long long half = best - kHalfSaves;
+    if (l.tile_n == 256 && 2 * l.rest <= kPairs) best = half, l.halves = true, pieces = 2 * l.rest;
     const long long slices = kPairs / l.rest;
     for (long long s = 2; s <= slices && s <= l.k_tiles; ++s) {
       const long long len = ceil_div(l.k_tiles, s), used = ceil_div(l.k_tiles, len);
       const long long cost = len * kt + kSumCost + kJoinCost + l.rest * used * kJoinPiece;
-      if (cost < best) best = cost, l.piece = len, l.span = len * used, l.split = true, pieces = l.rest * used;
+      if (cost < best)
+        best = cost, l.piece = len, l.span = len * used, l.split = true, l.halves = false, pieces = l.rest * used;
     }
     const long long len = ceil_div((long long)l.rest * l.k_tiles, kPairs);
     const long long n = ceil_div((long long)l.rest * l.k_tiles, len);
     const long long cost = len * kt + kSumCost + kSecondCost + kJoinCost + (n + l.rest) * kJoinPiece;
-    if (len < l.k_tiles && cost < best) l.piece = len, l.span = l.k_tiles, l.split = true, pieces = n;
+    if (len < l.k_tiles && cost < best)
+      l.piece = len, l.span = l.k_tiles, l.split = true, l.halves = false, pieces = n;
   }
   l.pairs = l.full ? kPairs : (int)pieces;
   size_t at = 0;
@@ -640,7 +657,7 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
   Dw8Gemm g = {};
   g.rows = outs, g.cols = width;
   g.tiles_m = l.tiles_m, g.tiles_n = l.tiles_n, g.k_tiles = l.k_tiles, g.tile_n = l.tile_n;
-  g.full = l.full, g.rest = l.rest, g.piece = (unsigned)l.piece, g.span = (unsigned)l.span, g.split = l.split;
+  g.full = l.full, g.rest = l.rest, g.halves = l.halves, g.piece = (unsigned)l.piece, g.span = (unsigned)l.span, g.split = l.split;
   g.part = reinterpret_cast<float*>(ws + l.part);
   g.group = f32 ? 4 : kGroupK / kBK;
   g.wait_limit_ns = d.wait_limit_ns, g.debug_stop = d.debug_stop, g.status = d.status;
