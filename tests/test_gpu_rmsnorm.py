@@ -340,3 +340,37 @@ def test_rows_at_one_place_in_their_units(b2g, rows, cols, ld, offset, dtype):
     assert untouched(flat, out, before)
     check_backward(b2g, dy, b2g.quantize_8bit(x), w, rstd, None, out=out)
     assert untouched(flat, out, before)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,cols,offset", [(40, 512, 0), (40, 513, 0), (40, 513, 3), (3, 20001, 1), (700, 96, 1)])
+def test_sum_over_the_residual(b2g, rows, cols, offset, dtype):
+    """The C call's total may stand where x or the residual was, and y where x was."""
+    gen = torch.Generator().manual_seed(cols)
+    mk = lambda o: padded(torch.randn(rows, cols, generator=gen, dtype=torch.float64), dtype, cols, o)[0]  # noqa: E731
+    x, res = mk(offset), mk(0)
+    w = torch.randn(cols, generator=gen, dtype=torch.float64).to(dtype).cuda()
+    want = b2g.rms_norm(x, w, res, EPS)
+    lib, st = b2g.train_library(), torch.cuda.current_stream().cuda_stream
+    code = 0 if dtype is F32 else 1
+    for over in range(2):
+        args = [x.clone(), res.clone()] if offset == 0 else [mk(offset).copy_(x), mk(0).copy_(res)]
+        y = args[0] if over else torch.empty_like(x)
+        rstd = torch.empty(rows, device="cuda")
+        rc = lib.b2g_rmsnorm(code, rows, cols, args[0].data_ptr(), cols, args[1].data_ptr(), cols, w.data_ptr(),
+                             EPS, args[1].data_ptr(), cols, y.data_ptr(), cols, None, 0, None, 0, None, 0, None,
+                             0, rstd.data_ptr(), st)
+        torch.cuda.synchronize()
+        assert rc == 0 and torch.equal(args[1], want[1])
+        check_forward(x, res, w, y, args[1], rstd)
+
+
+def test_scales_that_are_nan(b2g):
+    """A NaN scale makes its own row's results NaN, whatever the rows beside it hold."""
+    for cols in (96, 1000, 1001):
+        x = torch.randn(1500, cols, device="cuda")
+        kept = b2g.quantize_8bit(x)
+        kept[1].view(torch.uint8)[7, 1] = 255
+        rstd = torch.ones(1500, device="cuda")
+        dx, _ = b2g.rms_norm_backward(x, kept, None, rstd)
+        assert torch.isnan(dx[7]).all() and torch.isfinite(dx[:7]).all() and torch.isfinite(dx[8:]).all()
