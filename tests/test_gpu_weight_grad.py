@@ -40,7 +40,8 @@ def operands(tokens, outs, width, dtype, seed=0, **kw):
 
 SHAPES = [(1, 1, 1), (3, 5, 33), (64, 64, 64), (65, 130, 257), (300, 512, 256), (1000, 1025, 777),
           (17, 300, 31), (2000, 96, 4000), (5000, 40, 70), (16, 4096, 4096), (128, 256, 256),
-          (129, 255, 128), (4096, 512, 520), (700, 1200, 264), (40000, 24, 72)]
+          (129, 255, 128), (4096, 512, 520), (700, 1200, 264), (40000, 24, 72), (1, 8, 16), (63, 72, 48), (1000, 264, 784),
+          (5000, 128, 1008), (70, 4096, 4096), (3000, 64, 6944), (20000, 64, 64), (40000, 40, 144)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
