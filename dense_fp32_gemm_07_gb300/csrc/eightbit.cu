@@ -14,7 +14,9 @@ struct Convert {
   Rows8 k;
 };
 
-// Bound: bytes.
+// Four chunks a thread are on their way before the first is converted, and all four blocks'
+// largest values are found together.  Bound: bytes.  BF16 16384 x 4096 33.8 us (6.0 TB/s),
+// 8192 x 4096 18.3 (2.7 of them the launch), 8192 x 4095 30; FP32 4096 x 4096 14.5, 8192 x 4095 45.
 template <typename T, bool ANY>
 __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ Convert p) {
   constexpr int VEC = kVec<T>, U = kPasses, lanes = kScaleBlock / VEC;
@@ -61,6 +63,8 @@ __global__ void __launch_bounds__(256) quantize_kernel(const __grid_constant__ C
   }
 }
 
+// Bound: bytes.  BF16 16384 x 4096 31.2 us (6.5 TB/s), 8192 x 4096 16.8, 8192 x 4095 33; FP32
+// 4096 x 4096 14.4, 8192 x 4095 45.
 template <typename T, bool ANY>
 __global__ void __launch_bounds__(256) dequantize_kernel(const __grid_constant__ Convert p) {
   constexpr int VEC = kVec<T>, U = kPasses;

@@ -51,12 +51,36 @@ __device__ __forceinline__ void add_residual(Pack<T, kVec<T>>& x, const Pack<T, 
   x.get(f);
 }
 
+// The sum of a chunk's squares, added in pairs: few roundings reach the row's sum.
+template <int VEC>
+__device__ __forceinline__ float squares(const float (&f)[VEC]) {
+  float s[VEC / 2];
+#pragma unroll
+  for (int j = 0; j < VEC / 2; ++j) s[j] = fmaf(f[2 * j + 1], f[2 * j + 1], f[2 * j] * f[2 * j]);
+#pragma unroll
+  for (int n = VEC / 4; n; n /= 2)
+#pragma unroll
+    for (int j = 0; j < n; ++j) s[j] += s[j + n];
+  return s[0];
+}
+__device__ __forceinline__ float rstd_of(float sum, int cols, float eps) {
+  return __frsqrt_rn(sum / (float)cols + eps);
+}
+
 // How a call's rows stand in memory (anyrow.cuh): on 16-byte boundaries; all of its
 // matrices' at the same places within a 16-byte unit; anyhow.
 enum Rows { kAligned, kPhase, kAny };
 
 // One row per blockDim.x threads (from 8 lanes of a warp up; threadIdx.y picks the row of
-// a block that has several), NCH chunks a thread, the weights fetched with the row.
+// a block that has several), NCH chunks a thread, the weights fetched with the row.  Rows
+// anyhow take shifted vectors (anyrow.cuh) and so do all rows off the boundaries whose
+// results leave in 8 bits, since a scale's 32 columns are counted from the row's first.
+//
+// Several blocks an SM, each with all of its row on its way, keep HBM busy by themselves: a
+// ring as in the backward pass is not needed.  With a residual, BF16: 8192 x 4096 40.3 us
+// (6.66 TB/s), to 8 bits 36.7 (6.4), to both with total kept in 8 bits 51.8 (6.5); 8192 x 4095
+// 51 us, to 8 bits 72; FP32 90 and 124.  One row of 4096: 1.9 us, the latency of a launch, a
+// read, a sum over the block and a write.
 template <typename T, int NCH, Rows ROWS>
 __global__ void __launch_bounds__(kMaxRowThreads) rms_fwd_kernel(const __grid_constant__ RmsFwd p) {
   constexpr int VEC = kVec<T>;
@@ -109,11 +133,10 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_fwd_kernel(const __grid_co
     else
       raw[i].get(f[0]);
     if (p.total) put(p.total, p.ldt, raw[i], i);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) sum = fmaf(f[0][j], f[0][j], sum);
+    sum += squares<VEC>(f[0]);
     if (ROWS != kPhase && p.t8.q) encode_to<VEC, 1, ANY>(p.t8, row, t + i * nt, 0, chunks, p.cols, f);
   }
-  const float rstd = 1.f / sqrtf(row_sum(sum, red, nt) / (float)p.cols + p.eps);
+  const float rstd = rstd_of(row_sum(sum, red, nt), p.cols, p.eps);
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     float f[1][VEC], wf[VEC];
@@ -155,10 +178,9 @@ __global__ void __launch_bounds__(1024) rms_fwd_wide_kernel(const __grid_constan
   float f[1][VEC], sum = 0.f;
   for (int c = threadIdx.x; c < p.chunks; c += blockDim.x) {
     load(c, k, f);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) sum = fmaf(f[0][j], f[0][j], sum);
+    sum += squares<VEC>(f[0]);
   }
-  const float rstd = 1.f / sqrtf(block_sum(sum, red, blockDim.x >> 5) / (float)p.cols + p.eps);
+  const float rstd = rstd_of(block_sum(sum, red, blockDim.x >> 5), p.cols, p.eps);
   for (int c0 = 0; c0 < p.chunks; c0 += blockDim.x) {  // whole warps, for the scales
     const int c = c0 + threadIdx.x;
     load(c, k, f);
@@ -238,7 +260,9 @@ __device__ __forceinline__ void leave_sums(const RmsBwd& p, const float* sums, i
 }
 
 // Few or short rows: groups of nt threads (from 4 lanes of a warp up) with a row each, 16
-// columns a thread, all of whose loads are on their way together.
+// columns a thread, all of whose loads are on their way together.  One row of 4096 BF16: 3.5
+// us, a block's sums written by itself; 128 rows 5.9 with the launch that adds 64 blocks';
+// 16384 x 64 FP32 7.8.
 template <typename T, bool Q8, bool ANY>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     rms_bwd_kernel(const __grid_constant__ RmsBwd p, int nt, int groups) {
@@ -400,6 +424,10 @@ struct RowUnits {
 // that the place, and with it a thread's columns, stays; the slots hold whole units.  The
 // first and last rows, whose units may begin before the matrix or end after it, are read where
 // they are.
+// BF16, with dtotal and the sums' reduction: 8192 x 4096 45.6 us (5.9 TB/s), from 8 bits 44.2;
+// 16384 x 4096 81 (6.6 TB/s): a further row costs what its bytes do, the first ones 9 us.
+// 8192 x 4095 60 us (FP32 87), from 8 bits 78 (104); read row by row into registers, as above,
+// 8192 x 4096 took 88.
 template <typename T, bool FULL, bool Q8, bool PHASE>
 __global__ void __launch_bounds__(PHASE ? kPhaseThreads : kBwdThreads, 1)
     rms_bwd_ring_kernel(const __grid_constant__ RmsBwd p, const __grid_constant__ Ring g,
@@ -429,8 +457,8 @@ __global__ void __launch_bounds__(PHASE ? kPhaseThreads : kBwdThreads, 1)
   const T* dy0 = static_cast<const T*>(p.dy) + row0 * p.lddy;
   const int pad = PHASE ? (int)((reinterpret_cast<uintptr_t>(dy0) & 15u) / ES) : 0;
   const int chunks = PHASE ? (p.cols + pad + VEC - 1) / VEC : p.chunks;
-  // A chunk's first column; of 8-bit rows computed anew each time with PHASE, as keeping what depends on it
-  // for all rows would spill.
+  // A chunk's first column; of 8-bit rows computed anew each time with PHASE, as keeping what
+  // depends on it for all rows would spill.
   auto first_of = [&](int i) {
     int c = t + i * g.nt;
     if (PHASE && Q8) asm volatile("" : "+r"(c));
@@ -729,7 +757,7 @@ __global__ void __launch_bounds__(64) rms_bwd_cols_kernel(const __grid_constant_
 }
 
 // dweight: warp y adds the partial rows y, y + 16, ... in order, then the warps' sums are
-// added in warp order.
+// added in warp order.  Bound: latency, about 3 us.
 template <typename T>
 __global__ void __launch_bounds__(512) rms_bwd_reduce_kernel(const float* part, int parts, int cols,
                                                              T* dweight) {
@@ -792,7 +820,10 @@ struct BwdPlan {
 };
 
 constexpr int kBwdRing = 224 * 1024;  // bytes of the rings
-constexpr int kNarrow = 128;          // columns of a row that a warp has too many lanes for
+// Rows up to these lengths, of which a warp of the ring has too few columns for its lanes, go to
+// the direct kernel.  BF16, us there and in the ring: 16384 x 128 8.1 and 11.5, x 256 11.5 and
+// 12.7, x 512 17.0 and 17.3; off the boundaries x 101 15.8 and 18.6, x 201 27 and 20.
+constexpr int kNarrow = 256, kNarrowPhase = 128;
 
 uint32_t slot_of(int cols, size_t es, bool phase, bool past, bool q8) {
   const int e = (int)es, k = q8 ? 1 : e;
@@ -819,7 +850,7 @@ BwdPlan bwd_plan(long long rows, int cols, int dtype, int sms, Rows how, bool pa
     b.kind = kRing;
     // short rows, and one row a group: no second row to wait for
     if (how == kAny || (how == kPhase && sms < 8) || rows <= (long long)b.r.groups * sms ||
-        cols <= kNarrow || b.r.stages < 2) {
+        cols <= (how == kPhase ? kNarrowPhase : kNarrow) || b.r.stages < 2) {
       b.kind = kDirect;
       b.r.nt = 4;
       while (b.r.nt * 16 < cols) b.r.nt *= 2;
