@@ -16,6 +16,7 @@
 
 #include "eightbit.cuh"
 #include "ring.cuh"
+#include "tcgen05.cuh"
 
 namespace b2g {
 namespace {
@@ -221,9 +222,11 @@ struct RmsBwd {
   long long lddx;
   float* part;  // [grid][cols]: partial dweight
   void* dw;     // NULL: it is not wanted.  One block writes it, several their parts
+  int cluster;  // the direct kernel's blocks are one cluster, which writes it
 };
 
 constexpr int kBwdThreads = 512;  // 16 columns a thread
+constexpr int kCluster = 8;       // blocks of a cluster, at most
 // Rows off the 16-byte boundaries: 24 columns a thread and a third more registers, which their
 // ends take.
 constexpr int kPhaseThreads = 384, kPhaseCols = 24;
@@ -259,10 +262,31 @@ __device__ __forceinline__ void leave_sums(const RmsBwd& p, const float* sums, i
   }
 }
 
+// The same of a cluster that is the whole grid: block k adds its share of the columns over the
+// blocks, in their order, from their shared memory.
+template <typename T>
+__device__ __forceinline__ void leave_cluster(const RmsBwd& p, float* sums, int groups) {
+  for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
+    float a = sums[c];
+    for (int i = 1; i < groups; ++i) a += sums[(size_t)i * p.cols + c];
+    sums[c] = a;
+  }
+  cluster_sync();
+  for (int c = threadIdx.x + blockIdx.x * blockDim.x; c < p.cols; c += gridDim.x * blockDim.x) {
+    float v[kCluster], a = 0.f;
+#pragma unroll
+    for (int k = 0; k < kCluster; ++k)
+      v[k] = k < gridDim.x ? ld_shared_cluster_f32(mapa_shared(smem_addr(sums + c), k)) : 0.f;
+#pragma unroll
+    for (int k = 0; k < kCluster; ++k) a += v[k];
+    static_cast<T*>(p.dw)[c] = from_f32<T>(a);
+  }
+  cluster_sync();  // nobody leaves while its sums are read
+}
+
 // Few or short rows: groups of nt threads (from 4 lanes of a warp up) with a row each, 16
-// columns a thread, all of whose loads are on their way together.  One row of 4096 BF16: 3.5
-// us, a block's sums written by itself; 128 rows 5.9 with the launch that adds 64 blocks';
-// 16384 x 64 FP32 7.8.
+// columns a thread, all of whose loads are on their way together.  Up to kCluster blocks are
+// a cluster, which needs no second launch for dweight.
 template <typename T, bool Q8, bool ANY>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     rms_bwd_kernel(const __grid_constant__ RmsBwd p, int nt, int groups) {
@@ -318,7 +342,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
       }
     };
-    load(dy, rd);
+    constexpr bool TOGETHER = ANY && NCH == 2;  // BF16 has registers for all of the row at once
+    if constexpr (TOGETHER) {
+      Fetched fd[2], fx[2], ft[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int e = e0 + i * step;
+        fetch<T>(fd[i], rd, e, p.cols, in(i));
+        if (!Q8) fetch<T>(fx[i], rx, e, p.cols, in(i));
+        if (p.dtotal) fetch<T>(ft[i], rt, e, p.cols, in(i));
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int e = e0 + i * step;
+        finish<T>(dy[i], fd[i], rd, e, p.cols, in(i));
+        if (!Q8) finish<T>(x[i], fx[i], rx, e, p.cols, in(i));
+        if (p.dtotal) finish<T>(dt[i], ft[i], rt, e, p.cols, in(i));
+      }
+    } else {
+      load(dy, rd);
+      if (!Q8) load(x, rx);
+      if (!ANY && p.dtotal) load(dt, rt);
+    }
+    if (ANY && w) load(wr, w);
     if constexpr (Q8) {
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
@@ -330,11 +376,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         if (ANY) asm volatile("" ::: "memory");  // one after another, for the registers
       }
-    } else {
-      load(x, rx);
     }
-    if (!ANY && p.dtotal) load(dt, rt);
-    if (ANY && w) load(wr, w);
     float xh[NCH][VEC], g[NCH][VEC], along = 0.f;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
@@ -358,7 +400,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     const float mean = (nt < 32 ? row_sum(along, nullptr, nt) : group_sum(along, red[turn], group, nt)) * inv;
     turn ^= 1;
-    if (ANY && p.dtotal) load(dt, rt);
+    if (ANY && !TOGETHER && p.dtotal) load(dt, rt);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int c = t + i * nt;
@@ -390,7 +432,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
   }
   __syncthreads();
-  leave_sums<T>(p, sums, groups);
+  if (p.cluster)
+    leave_cluster<T>(p, sums, groups);
+  else
+    leave_sums<T>(p, sums, groups);
 }
 
 // Bytes of a ring's slot that one row of `cols` elements of `es` bytes takes: with PHASE, in
@@ -817,6 +862,7 @@ struct BwdPlan {
   BwdKind kind;
   Ring r;     // stages only where there is a ring
   int parts;  // blocks, each leaving one partial row of dweight
+  bool cluster;
 };
 
 constexpr int kBwdRing = 224 * 1024;  // bytes of the rings
@@ -833,7 +879,7 @@ uint32_t slot_of(int cols, size_t es, bool phase, bool past, bool q8) {
 
 // past: a dtotal; q8: 8-bit rows.
 BwdPlan bwd_plan(long long rows, int cols, int dtype, int sms, Rows how, bool past, bool q8) {
-  BwdPlan b{kWide, {}, 0};
+  BwdPlan b{kWide, {}, 0, false};
   const size_t es = type_size(dtype);
   // whole warps that hold a row with the part of a unit before it
   auto ring = [&](int threads, int per, bool phase) {
@@ -861,7 +907,27 @@ BwdPlan bwd_plan(long long rows, int cols, int dtype, int sms, Rows how, bool pa
   const long long fair = ceil_div(rows, b.kind != kWide ? b.r.groups : 4);
   if (b.kind == kRing && how == kPhase) most = sms / 8 * 8;  // steps of whole 16-byte units
   b.parts = (int)(fair < most ? fair : most);
+  // As fast as a second launch while groups have one row each (16 x 4096 BF16 5.0 us both ways,
+  // 48 rows 7.4 in a cluster and 5.2), and a launch less for the host.
+  b.cluster = b.kind == kDirect && fair > 1 && fair <= kCluster;
   return b;
+}
+
+// launch_train of blocks that are one cluster.
+template <typename... P, typename... A>
+cudaError_t launch_cluster(void (*kern)(P...), int blocks, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  return [&](P... typed) {
+    void* ptrs[] = {const_cast<void*>(static_cast<const void*>(&typed))...};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks), cfg.blockDim = block, cfg.dynamicSmemBytes = smem, cfg.stream = st;
+    cfg.attrs = attr, cfg.numAttrs = 2;
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kern), ptrs);
+  }(args...);
 }
 
 template <typename T, bool FULL, bool Q8, bool PHASE>
@@ -884,8 +950,12 @@ cudaError_t bwd_launch(RmsBwd p, int dtype, const TrainDevice& d, cudaStream_t s
   const BwdPlan b = bwd_plan(p.rows, p.cols, dtype, d.sms, ROWS, p.dtotal, Q8);
   cudaError_t e = cudaSuccess;
   if (b.kind == kDirect) {
-    e = launch_train(rms_bwd_kernel<T, Q8, ROWS != kAligned>, dim3(b.parts), dim3(kBwdThreads),
-                     (size_t)b.r.groups * p.cols * sizeof(float), st, p, b.r.nt, b.r.groups);
+    const size_t sums = (size_t)b.r.groups * p.cols * sizeof(float);
+    p.cluster = b.cluster;
+    e = b.cluster ? launch_cluster(rms_bwd_kernel<T, Q8, ROWS != kAligned>, b.parts, dim3(kBwdThreads), sums, st,
+                                   p, b.r.nt, b.r.groups)
+                  : launch_train(rms_bwd_kernel<T, Q8, ROWS != kAligned>, dim3(b.parts), dim3(kBwdThreads), sums,
+                                 st, p, b.r.nt, b.r.groups);
   } else if (b.kind == kRing) {
     if constexpr (ROWS == kPhase)
       e = bwd_ring<T, false, Q8, true>(p, b, d, st);
@@ -900,7 +970,7 @@ cudaError_t bwd_launch(RmsBwd p, int dtype, const TrainDevice& d, cudaStream_t s
     if (e == cudaSuccess)
       e = launch_train(rms_bwd_wide_kernel<T, Q8>, dim3((unsigned)p.rows), dim3(1024), 0, st, p);
   }
-  if (e == cudaSuccess && p.dw && (b.parts > 1 || b.kind == kWide))
+  if (e == cudaSuccess && p.dw && !b.cluster && (b.parts > 1 || b.kind == kWide))
     e = launch_train(rms_bwd_reduce_kernel<T>, dim3((unsigned)ceil_div(p.cols, 32)), dim3(32, 16), 0,
                      st, (const float*)p.part, b.parts, p.cols, static_cast<T*>(p.dw));
   return e;
@@ -1025,7 +1095,7 @@ int b2g_rmsnorm_backward(int dtype, long long rows, int cols, const void* dy, lo
     return B2G_ERR_WORKSPACE;
   const bool q8 = total_scales != nullptr;
   const RmsBwd p{rows, cols,   0,    dy, lddy, q8 ? nullptr : total, ldt, k8, weight, rstd, dtotal,
-                 lddt, dx,     lddx, static_cast<float*>(workspace), dweight};
+                 lddt, dx,     lddx, static_cast<float*>(workspace), dweight, 0};
   auto row16 = [&](const void* q, long long ld) { return !q || (vec16(q) && vec16_ld(ld, dtype)); };
   const bool v = row16(dy, lddy) && row16(p.x, ldt) && row16(dtotal, lddt) && row16(dx, lddx) &&
                  row16(weight, cols) && vec16_ld(cols, dtype) &&
