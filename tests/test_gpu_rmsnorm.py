@@ -120,6 +120,25 @@ def test_forward_and_backward(b2g, rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,cols", [(3, 4096), (16, 4096), (17, 4096), (2, 8192), (9, 8191),
+                                       (63, 777), (64, 777), (65, 777), (129, 40), (1024, 40),
+                                       (1025, 33), (640, 96)])
+def test_backward_of_few_blocks(b2g, rows, cols, dtype):
+    """dweight of 2 to 9 blocks: a cluster that adds its blocks' sums, or a launch that does."""
+    gen = torch.Generator().manual_seed(rows + cols)
+    mk = lambda *s: torch.randn(*s, generator=gen, dtype=torch.float64)  # noqa: E731
+    x, dy, dtotal = (mk(rows, cols).to(dtype).cuda() for _ in range(3))
+    w = (mk(cols) * 0.3 + 1).to(dtype).cuda()
+    _, total, rstd = b2g.rms_norm(x, w)
+    kept = b2g.quantize_8bit(total)
+    for held in (total, kept):
+        check_backward(b2g, dy, held, w, rstd, dtotal)
+        check_backward(b2g, dy, held, w, rstd, None)
+        one, two = (b2g.rms_norm_backward(dy, held, w, rstd, dtotal) for _ in range(2))
+        assert all(torch.equal(a, b) for a, b in zip(one, two))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("rows,cols", [(50, 640), (30, 333), (2000, 1024), (1500, 333), (5, 9001)])
 def test_without_weight_and_residual(b2g, rows, cols, dtype):
     x = (torch.randn(rows, cols, dtype=torch.float64) + 3).to(dtype).cuda()
