@@ -32,13 +32,15 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
 }
 
 // mbar_wait without a function call: registers are redistributed among the warps
-// here, and a called function would have to fit the smallest share.
-template <typename P>
+// here, and a called function would have to fit the smallest share.  CLUSTER: for what
+// the other CTA's threads wrote.
+template <bool CLUSTER = false, typename P>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const P& p,
                                            unsigned int flag) {
-  if (mbar_try_wait(bar, parity)) return true;
+  auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (done()) return true;
   const uint64_t t0 = global_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!done()) {
     if (global_ns() - t0 > p.wait_limit_ns) {
       atomicOr(p.status, flag);
       return false;

@@ -3,9 +3,10 @@
 //
 // dw (outs x width) is a sum over the tokens, so both operands are read with their rows
 // as k ("MN-major") and nothing is transposed.  x's values have 4 significant bits and
-// power-of-two scales: a first kernel writes them as BF16, exactly.  BF16 dy is multiplied
-// as it is; FP32 dy is split into three BF16 planes, dy = d0 + d1 + d2 to 24 bits, and
-// the three products d x are added up, the smallest first.
+// power-of-two scales: BF16 holds them exactly.  A first kernel writes them so; or, where there
+// are few products for each of them, warps of the product's kernel on their way to the stages.
+// BF16 dy is multiplied as it is; FP32 dy is split into three BF16 planes, dy = d0 + d1 + d2
+// to 24 bits, and the three products d x are added up, the smallest first.
 //
 // The product runs on 256 x 256 tiles of a CTA pair (tcgen05.mma.cta_group::2, FP32
 // accumulators in tensor memory, double buffered).  As many tiles as fill all pairs are
@@ -16,11 +17,13 @@
 //
 // Bound: the tensor cores; short sums, writing the result.  BF16: 16384 tokens on 11008 x 4096
 // 775 to 870 us (1.70 to 1.91 PFLOP/s, under the power cap), 4096 on 4096 x 4096 86 us, of
-// which the products 70 and the preparation 8 to 10; 64 on 4096 x 4096 15.8 (34 MB written).
-// FP32: 4096 on 4096 x 4096 237 us, 1.74 PFLOP/s of the three products.  Converting x on its
-// way to the stages instead, by the epilogue's warps, took 2800 cycles a k tile where the
-// products take 520.
+// which the products 70 and the preparation 8 to 10; 64 on 4096 x 4096 12.8 (34 MB written; 15.8
+// with a preparation).  FP32: 4096 on 4096 x 4096 237 us, 1.74 PFLOP/s of the three products.
+// Converting x on its way takes about 900 cycles a k tile, the products 520: bit operations, at half
+// the rate of multiplications, keep the converting warps busy for 450, and the rest is the latency
+// of barriers, loads and stores, half hidden by two groups of warps with a k tile each.
 #include <atomic>
+#include <type_traits>
 
 #include "eightbit.cuh"
 #include "pair.cuh"
@@ -28,18 +31,30 @@
 namespace b2g {
 namespace {
 
-constexpr int kThreads = 128 + 32 * kEpiWarps;  // warp 0 copies, warp 1 multiplies, 2 and 3 idle
+// Warp 0 copies, warp 1 multiplies; with EIGHT warp 2 copies x's codes, kCvtWarps more warps
+// write them to the stages as BF16, and warp 3 of the odd CTA tells the even one.
+constexpr int kCvtWarps = 8;
+// Groups of them with a k tile each (4096 tokens on 4096 x 4096: 102 us; all on one 126).
+constexpr int kCvtGroups = 2;
+template <bool EIGHT>
+constexpr int kThreads = 128 + 32 * (kEpiWarps + (EIGHT ? kCvtWarps : 0));
 // Registers, as in the cross entropy's product: 128 * 72 + 256 * 216 = 64,512 of the 168 a
-// thread that the block starts with.
-constexpr int kIssueRegs = 72, kEpiRegs = 216;
+// thread that the block starts with; with EIGHT 128 * 72 + 256 * 120 + 256 * 80 = 60,416 of 96.
+constexpr int kIssueRegs = 72;
+template <bool EIGHT>
+constexpr int kEpiRegs = EIGHT ? 120 : 216;
+constexpr int kCvtRegs = 80;
 constexpr uint32_t kOperand = 128 * kBK * 2;    // a CTA's 128 rows of one plane: 16 KB
-// A stage holds all planes of a k tile of dy, and x's.
-template <int PLANES>
-constexpr int kStages = 12 / (PLANES + 1);
+// A stage holds all planes of a k tile of dy, and x's.  With EIGHT two of the twelve operands'
+// places hold codes.
+template <int PLANES, bool EIGHT>
+constexpr int kStages = (EIGHT ? 10 : 12) / (PLANES + 1);
 template <int PLANES>
 constexpr uint32_t kStageBytes = (PLANES + 1) * kOperand;
 constexpr int kMaxStages = 6;
-constexpr int kNumBars = 2 * kMaxStages + 5;
+constexpr int kCodeTiles = 4;                   // 64 tokens x 128 codes
+constexpr uint32_t kCodeBytes = kBK * 128;
+constexpr int kNumBars = 3 * kMaxStages + 5 + 2 * kCodeTiles;
 constexpr int kSmemBytes = 12 * kOperand + kEpiWarps * kOutBytes + 1024 + kNumBars * 8 + 16;
 constexpr uint32_t kTmemCols = 2 * kTile;
 constexpr int kPairs = 76;  // what the work is shared out among (GB300: 152 SMs)
@@ -63,9 +78,12 @@ struct Dw8Gemm {
   long long ldo;
   int out_bf16, accumulate;
   float* part;               // the sums, [slot][16 warps][columns / 4][32 rows][4]
+  const unsigned char* scales;  // with EIGHT: x's, of `tokens` rows
+  long long lds;
+  int tokens;
 };
 struct alignas(64) Dw8Maps {
-  CUtensorMap dy, x, out;
+  CUtensorMap dy, x, out;    // x: BF16, or with EIGHT the codes
 };
 
 struct Unit {
@@ -156,15 +174,102 @@ __device__ __forceinline__ void put_tile(const Dw8Gemm& p, const CUtensorMap* m,
   }
 }
 
+// A unit of one accumulation group to BF16 by bulk-tensor stores, or its sums, 64 columns at a time.
+// False when the wait for it ran out.
+__device__ __forceinline__ bool put_bf16(const Dw8Gemm& p, const Unit& u, const CUtensorMap* m,
+                                         uint32_t tmem_lane, int span, int rows, int half, int row0, int n0,
+                                         int left, int& a, uint32_t& aph, uint32_t tfull0, uint32_t tempty0,
+                                         uint32_t tempty0_even, bool even, uint32_t buf, int lane) {
+  if (!__all_sync(0xffffffffu, wait_phase(tfull0 + 8u * a, aph, p, kStatusTimeoutTmem))) return false;
+  tc_fence_after_sync();
+#pragma unroll 1
+  for (int c = 0; c < span; c += 64) {
+    uint32_t v[32], x[32];
+    tmem_ld32(tmem_lane + (uint32_t)(a * kTile + c), v);
+    tmem_ld32(tmem_lane + (uint32_t)(a * kTile + c + 32), x);
+    tmem_ld_wait();
+    tie32(v);
+    tie32(x);
+    if (c + 64 == span) {  // the tile may be overwritten
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (even)
+          mbar_arrive(tempty0 + 8u * a);
+        else
+          mbar_arrive_remote(tempty0_even + 8u * a);
+      }
+    }
+    if (c >= left) continue;
+    if (u.slot >= 0) {
+      uint4* to = reinterpret_cast<uint4*>(p.part + sums_at(u.slot, rows, half, p.tile_n)) + 8 * c + lane;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (c + 4 * j < left) to[32 * j] = make_uint4(v[4 * j], v[4 * j + 2], v[4 * j + 1], v[4 * j + 3]);
+        if (c + 4 * j + 32 < left)
+          to[32 * j + 256] = make_uint4(x[4 * j], x[4 * j + 2], x[4 * j + 1], x[4 * j + 3]);
+      }
+    } else {
+      uint4 w[8];
+      auto two = [](uint32_t lo, uint32_t hi) { return pack_bf16(__uint_as_float(lo), __uint_as_float(hi)); };
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = 8 * j;
+        w[j] = make_uint4(two(v[i], v[i + 2]), two(v[i + 1], v[i + 3]), two(v[i + 4], v[i + 6]),
+                          two(v[i + 5], v[i + 7]));
+        w[4 + j] = make_uint4(two(x[i], x[i + 2]), two(x[i + 1], x[i + 3]), two(x[i + 4], x[i + 6]),
+                              two(x[i + 5], x[i + 7]));
+      }
+      store_rows(buf, m, n0 + c, row0, 0, w, false, lane);
+    }
+  }
+  if (++a == 2) a = 0, aph ^= 1u;
+  return true;
+}
+
+// Sixteen codes times their scale as BF16, exactly (up to BF16's range); of each four columns the
+// second and third change places.  A code's bits in BF16's places are its value times 2^-120,
+// subnormal ones too, so that one multiplication does, but for RARE ones.
+__device__ __forceinline__ bool rare_codes(const uint4& w, uint32_t byte) {  // NaN; scales above 2^7
+  constexpr uint32_t low = 0x7F7F7F7Fu, one = 0x01010101u;
+  const uint32_t nan =
+      ((w.x & low) + one) | ((w.y & low) + one) | ((w.z & low) + one) | ((w.w & low) + one);
+  return (nan & 0x80808080u) || byte > 134u;
+}
+template <bool RARE>
+__device__ __forceinline__ void codes_to_bf16(const uint4& codes, uint32_t byte, uint32_t (&o)[8]) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (RARE) {
+      const float s = scale_value(byte);
+      float f[4];
+      decode2(w[i] & 0xFFFFu, f[0], f[1]);
+      decode2(w[i] >> 16, f[2], f[3]);
+      o[2 * i] = pack_bf16(f[0] * s, f[2] * s), o[2 * i + 1] = pack_bf16(f[1] * s, f[3] * s);
+    } else {
+      auto two = [](const uint32_t& bits) { return *reinterpret_cast<const __nv_bfloat162*>(&bits); };
+      const __nv_bfloat162 s = two((byte + 120u) * 0x00800080u);  // 2^(byte - 7)
+      const __nv_bfloat162 a = __hmul2(two((w[i] << 4 & 0x07F007F0u) | (w[i] << 8 & 0x80008000u)), s);
+      const __nv_bfloat162 b = __hmul2(two((w[i] >> 4 & 0x07F007F0u) | (w[i] & 0x80008000u)), s);
+      o[2 * i] = *reinterpret_cast<const uint32_t*>(&a), o[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+}
+
 // CTA r of a pair stages columns 128r .. of the tile's part of dy and its half of x's and
 // holds rows 128r .. of the accumulator.  Both CTAs' copies of a stage complete on the even
 // CTA's `full` barrier; its warp 1 issues the pair's MMAs and commits "stage read" and
 // "accumulator final" to both CTAs.  Every wait is bounded: on a timeout the kernel flags
 // the status word, waits (bounded) for what it started, frees its tensor memory and returns.
-template <int PLANES>
-__global__ void __launch_bounds__(kThreads, 1)
+//
+// With EIGHT x's operand comes from its codes: warp 2 copies 64 tokens x 128 codes at a time, and the
+// converting warps write them as BF16 in the order of a bulk-tensor copy with the 128-byte
+// swizzle; `full` then counts their arrivals too.
+template <int PLANES, bool EIGHT>
+__global__ void __launch_bounds__(kThreads<EIGHT>, 1)
     dw8_kernel(const __grid_constant__ Dw8Gemm p, const __grid_constant__ Dw8Maps maps) {
-  constexpr int S = kStages<PLANES>;
+  constexpr int S = kStages<PLANES, EIGHT>;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // 128-byte swizzle atoms: 1024-byte aligned
@@ -175,14 +280,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tfull = [&](int a) { return bars + 8u * (2 * kMaxStages + a); };
   auto tempty = [&](int a) { return bars + 8u * (2 * kMaxStages + 2 + a); };
   const uint32_t drain = bars + 8u * (2 * kMaxStages + 4);
+  const uint32_t codes = base + 10 * kOperand;
+  auto cfull = [&](int c) { return bars + 8u * (2 * kMaxStages + 5 + c); };
+  auto cempty = [&](int c) { return bars + 8u * (2 * kMaxStages + 5 + kCodeTiles + c); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (bars - raw) + kNumBars * 8);
   const uint32_t rank = cluster_ctarank() & 1u;
   const bool even = rank == 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
+  auto odd_full = [&](int s) { return bars + 8u * (2 * kMaxStages + 5 + 2 * kCodeTiles + s); };
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), 1);
+      mbar_init(full(s), EIGHT ? 2 + kCvtWarps / kCvtGroups : 1);
+      if (EIGHT) mbar_init(odd_full(s), kCvtWarps / kCvtGroups);
       mbar_init(empty(s), 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -190,6 +300,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(tempty(a), 2 * kEpiWarps);
     }
     mbar_init(drain, 1);
+    if (EIGHT)
+      for (int c = 0; c < kCodeTiles; ++c) {
+        mbar_init(cfull(c), 1);
+        mbar_init(cempty(c), kCvtWarps / kCvtGroups);
+      }
     fence_mbar_init();
     fence_proxy_async_smem();
   }
@@ -223,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int m0 = tm * kTile + (int)rank * 128;
           const int n0 = tn * p.tile_n + u.col + (int)rank * (u.cols / 2);
           const bool wide = u.cols > 128;
-          const uint32_t tx = 2 * (PLANES * kOperand + (uint32_t)(u.cols / 2) * kBK * 2);
+          const uint32_t tx = 2 * (PLANES * kOperand + (EIGHT ? 0 : (uint32_t)(u.cols / 2) * kBK * 2));
           for (int kt = u.kt0; kt < u.kt1; ++kt) {
             if ((p.debug_stop >= 0 && issued >= p.debug_stop) ||
                 !wait_phase(empty(s), ph ^ 1u, p, kStatusTimeoutEmpty)) {
@@ -236,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < PLANES; ++i)
               load_operand<true>(st + i * kOperand, &maps.dy, m0, kt, i, fb);
-            load_operand<true>(st + PLANES * kOperand, &maps.x, n0, kt, 0, fb, wide);
+            if (!EIGHT) load_operand<true>(st + PLANES * kOperand, &maps.x, n0, kt, 0, fb, wide);
             ++issued;
             if (++s == S) s = 0, ph ^= 1u;
           }
@@ -268,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t d = tmem + (uint32_t)(a * kTile);
             const int kts = min(p.group, u.kt1 - u.kt0 - g * p.group);
             for (int it = 0; it < kts; ++it) {
-              if (!(on = wait_phase(full(s), ph, p, kStatusTimeoutFull))) break;
+              if (!(on = wait_phase<EIGHT>(full(s), ph, p, kStatusTimeoutFull))) break;
               tc_fence_after_sync();
               const uint32_t off = (uint32_t)s * (kStageBytes<PLANES> >> 4);
 #pragma unroll
@@ -291,10 +406,144 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_phase(drain, 0, p, kStatusTimeoutTmem);
       }
       __syncwarp();
+    } else if (EIGHT && warp == 2) {
+      // ---------------------------------------------------------- copies of codes
+      if (lane == 0) {
+        prefetch_tmap(&maps.x);
+        int c = 0, issued = 0;
+        uint32_t ph = 0;
+        bool on = true;
+        Unit u;
+        for (int k = 0; on && unit_at(p, pair, pairs, k, u); ++k) {
+          int tm, tn;
+          tile_at(p, u.tile, tm, tn);
+          const int n0 = tn * p.tile_n + u.col + (int)rank * (u.cols / 2);
+          for (int kt = u.kt0; kt < u.kt1; ++kt) {
+            if (!(on = wait_phase(cempty(c), ph ^ 1u, p, kStatusTimeoutEmpty))) break;
+            mbar_arrive_expect_tx(cfull(c), u.cols > 128 ? kCodeBytes : kCodeBytes / 2);
+            tma_load_3d(codes + c * kCodeBytes, &maps.x, n0, kt * kBK, 0, cfull(c));
+            if (u.cols > 128)
+              tma_load_3d(codes + c * kCodeBytes + kCodeBytes / 2, &maps.x, n0 + 64, kt * kBK, 0, cfull(c));
+            ++issued;
+            if (++c == kCodeTiles) c = 0, ph ^= 1u;
+          }
+        }
+        for (int d = 0, pending = min(issued, kCodeTiles); d < pending; ++d) {
+          if (--c < 0) c = kCodeTiles - 1, ph ^= 1u;
+          if (!wait_phase(cfull(c), ph, p, kStatusTimeoutDrain)) break;
+        }
+      }
+      __syncwarp();
+    } else if (EIGHT && !even) {
+      // ---------------------------------------------------------- the odd CTA's converted tiles
+      // What is announced lies in this CTA's shared memory, where its writers have made it visible
+      // to the tensor core (fence.proxy.async) before this thread saw them arrive; the even
+      // CTA only learns of it.  So the arrival orders no other memory of this thread: as a release
+      // for the cluster it took 1400 cycles a k tile (4096 tokens on 4096 x 4096 218 us for 125).
+      if (lane == 0) {
+        const uint32_t full_even = mapa_shared(full(0), 0);
+        int s = 0;
+        uint32_t ph = 0;
+        bool on = true;
+        Unit u;
+        for (int k = 0; on && unit_at(p, pair, pairs, k, u); ++k) {
+          for (int kt = u.kt0; kt < u.kt1; ++kt) {
+            if (!(on = wait_phase(odd_full(s), ph, p, kStatusTimeoutFull))) break;
+            mbar_signal_remote(full_even + 8u * s);
+            if (++s == S) s = 0, ph ^= 1u;
+          }
+        }
+      }
+      __syncwarp();
+    }
+  } else if (EIGHT && warp >= 4 + kEpiWarps) {
+    // ---------------------------------------------------------- codes to BF16
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCvtRegs));
+    constexpr int G = kCvtGroups, N = 2 * G;  // every G-th k tile is a group's; chunks a thread
+    constexpr int kRows = kBK / G;            // tokens that a group's threads hold at a time
+    const int group = (warp - 4 - kEpiWarps) / (kCvtWarps / G);
+    const int t = (threadIdx.x - (128 + 32 * kEpiWarps)) & (256 / G - 1);
+    // 16 columns of tokens `token` and (with two groups) token + 32, in either half of the columns:
+    // chunk h is of half h & 1.  Eight lanes' units of 16 bytes lie in eight different places of
+    // 128 bytes, here and there.
+    const int chunk = t & 3, token = t >> 2;
+    const uint32_t done = even ? full(0) : odd_full(0);
+    const uint32_t from0 = codes + token * 64 + chunk * 16;
+    const uint32_t to0 = base + PLANES * kOperand + token * 128 + ((2 * chunk ^ (token & 7)) << 4);
+    int s = group, c = group, seen = 0;
+    uint32_t ph = 0, cph = 0;
+    bool on = true;
+    Unit u;
+    for (int k = 0; on && unit_at(p, pair, pairs, k, u); ++k) {
+      int tm, tn;
+      tile_at(p, u.tile, tm, tn);
+      const int col = tn * p.tile_n + u.col + (int)rank * (u.cols / 2) + 16 * chunk;
+      const bool wide = u.cols > 128;
+      int kt = u.kt0 + ((group - seen) & (G - 1));
+      seen += u.kt1 - u.kt0;
+      // the scales of this group's next k tile are on their way
+      uint32_t b[N];
+      int row = kt * kBK + token;
+      const unsigned char* from = p.scales + row * p.lds + col / kScaleBlock;
+      auto scales = [&] {
+#pragma unroll
+        for (int h = 0; h < N; ++h) {
+          b[h] = 127u;
+          if (row + kRows * (h >> 1) < p.tokens && col + 64 * (h & 1) < p.cols)
+            b[h] = from[(h >> 1) * kRows * p.lds + (h & 1) * (64 / kScaleBlock)];
+        }
+      };
+      scales();
+      for (; kt < u.kt1; kt += G) {
+        // both are asked for before either answer is waited for
+        const bool here = mbar_try_wait(cfull(c), cph), clear = mbar_try_wait(empty(s), ph ^ 1u);
+        if (!here) on = wait_phase(cfull(c), cph, p, kStatusTimeoutFull);
+        if (!clear) on = wait_phase(empty(s), ph ^ 1u, p, kStatusTimeoutEmpty) && on;
+        on = __all_sync(0xffffffffu, on);
+        if (!on) break;
+        uint4 q[N];
+        bool rare = false;
+#pragma unroll
+        for (int h = 0; h < N; ++h) {
+          q[h] = make_uint4(0, 0, 0, 0);
+          if (wide || !(h & 1))
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(q[h].x), "=r"(q[h].y), "=r"(q[h].z), "=r"(q[h].w)
+                         : "r"(from0 + c * kCodeBytes + (h & 1) * (kCodeBytes / 2) + (h >> 1) * kRows * 64));
+        }
+#pragma unroll
+        for (int h = 0; h < N; ++h) rare = rare | rare_codes(q[h], b[h]);
+        auto convert = [&](auto kind) {
+#pragma unroll
+          for (int h = 0; h < N; ++h) {
+            uint32_t o[8];
+            codes_to_bf16<kind.value>(q[h], b[h], o);
+            const uint32_t to = to0 + s * kStageBytes<PLANES> + (h & 1) * (kOperand / 2) + (h >> 1) * kRows * 128;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(o[0]), "r"(o[1]),
+                         "r"(o[2]), "r"(o[3]));
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to ^ 16u), "r"(o[4]), "r"(o[5]),
+                         "r"(o[6]), "r"(o[7]));
+          }
+        };
+        if (rare)
+          convert(std::true_type());
+        else
+          convert(std::false_type());
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(cempty(c));
+          mbar_arrive(done + 8u * s);
+        }
+        row += G * kBK, from += (long long)G * kBK * p.lds;
+        scales();
+        if ((s += G) >= S) s -= S, ph ^= 1u;
+        if ((c += G) >= kCodeTiles) c -= kCodeTiles, cph ^= 1u;
+      }
     }
   } else {
     // ---------------------------------------------------------- epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs<EIGHT>));
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t tmem_row = tmem + ((uint32_t)(32 * q) << 16);
     const uint32_t buf = outs + (uint32_t)(warp - 4) * kOutBytes;
@@ -303,20 +552,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t aph = 0;
     Unit u;
     for (int k = 0; unit_at(p, pair, pairs, k, u); ++k) {
-      float acc[128];
       const int span = u.cols / 2;  // this warp's columns
-      if (!collect(p, acc, tmem_row + (uint32_t)(half * span), span, groups_of(p, u.kt1 - u.kt0), a, aph, tfull(0), tempty(0),
-                   tempty_even, even, lane))
-        break;
       int tm, tn;
       tile_at(p, u.tile, tm, tn);
       const int rows = (int)rank * 4 + q, row0 = tm * kTile + 32 * rows;
       const int n0 = tn * p.tile_n + u.col + half * span;
-      const int left = min(span, p.cols - n0);
-      if (row0 < p.rows && left > 0) {
-        if (u.slot >= 0)
+      const int left = row0 < p.rows ? min(span, p.cols - n0) : 0;
+      const uint32_t lane0 = tmem_row + (uint32_t)(half * span);
+      if constexpr (EIGHT) {
+        if (!put_bf16(p, u, &maps.out, lane0, span, rows, half, row0, n0, left, a, aph, tfull(0), tempty(0),
+                      tempty_even, even, buf, lane))
+          break;
+      } else {
+        float acc[128];
+        if (!collect(p, acc, lane0, span, groups_of(p, u.kt1 - u.kt0), a, aph, tfull(0), tempty(0),
+                     tempty_even, even, lane))
+          break;
+        if (left > 0 && u.slot >= 0)
           put_sums(p.part + sums_at(u.slot, rows, half, p.tile_n), acc, left, lane);
-        else
+        else if (left > 0)
           put_tile(p, &maps.out, acc, row0, n0, left, buf, lane);
       }
     }
@@ -512,11 +766,18 @@ struct Layout {
   int tile_n, tiles_m, tiles_n, k_tiles, pairs, full, rest;
   long long piece, span;
   bool split, halves;
+  bool eight;      // x from its codes, without a copy
+  long long cost;  // of a pair's work, in cycles
   size_t x, d, part, total;
 };
 
-// Cycles of a k tile: BF16 its copies (64 bytes a cycle and SM), FP32 its three products.
-long long k_tile_cost(int planes, int tile_n) { return planes == 1 ? kTile + tile_n : 1900; }
+// Cycles of a k tile: BF16 its copies (64 bytes a cycle and SM), with EIGHT the conversion, FP32
+// its three products.
+long long k_tile_cost(int planes, int tile_n, bool eight) {
+  return planes == 3 ? 1900 : eight ? 900 : kTile + tile_n;
+}
+// The launch that prepares x, and the bytes that it moves in a cycle.
+constexpr long long kPrepareCost = 4000, kPrepareBytes = 3200;
 // Halves of a tile: their products take as long as the whole one's (2048 tokens on 1024 x 1024
 // BF16: 17.0 us so), but there is half as much to write at the end (300 on 512 x 256: 7.4 us for
 // 8.1; 1000 on 1025 x 777: 15.6 for 17.5).
@@ -527,7 +788,8 @@ constexpr long long kHalfSaves = 1500;
 constexpr long long kSumCost = 2200, kSecondCost = 4500, kJoinCost = 3000, kJoinPiece = 90;
 
 // false: more tiles than can be counted.
-bool layout(int dtype, int tokens, int outs, int width, const void* dy, long long lddy, Layout& l) {
+bool layout(int dtype, int tokens, int outs, int width, const void* dy, long long lddy, bool eight, Layout& l) {
+  l.eight = eight;
   l.planes = dtype == B2G_F32 ? 3 : 1;
   l.copy_dy = dtype == B2G_F32 || !vec16(dy) || lddy % 8;
   // the copies' rows on 128-byte lines: off them a k tile of BF16 takes twice as long
@@ -542,8 +804,9 @@ bool layout(int dtype, int tokens, int outs, int width, const void* dy, long lon
   // their k cut into one piece a pair, some of which then lie across two tiles and leave two sums.
   l.piece = l.span = l.k_tiles, l.split = l.halves = false;
   long long pieces = l.rest;
+  const long long kt = k_tile_cost(l.planes, l.tile_n, eight);
+  l.cost = l.full * l.k_tiles * kt;
   if (l.rest) {
-    const long long kt = k_tile_cost(l.planes, l.tile_n);
     long long best = l.k_tiles * kt;
     const long long half = best - kHalfSaves;
     if (l.tile_n == 256 && 2 * l.rest <= kPairs) best = half, l.halves = true, pieces = 2 * l.rest;
@@ -558,7 +821,8 @@ bool layout(int dtype, int tokens, int outs, int width, const void* dy, long lon
     const long long n = ceil_div((long long)l.rest * l.k_tiles, len);
     const long long cost = len * kt + kSumCost + kSecondCost + kJoinCost + (n + l.rest) * kJoinPiece;
     if (len < l.k_tiles && cost < best)
-      l.piece = len, l.span = l.k_tiles, l.split = true, l.halves = false, pieces = n;
+      best = cost, l.piece = len, l.span = l.k_tiles, l.split = true, l.halves = false, pieces = n;
+    l.cost += best;
   }
   l.pairs = l.full ? kPairs : (int)pieces;
   size_t at = 0;
@@ -567,19 +831,47 @@ bool layout(int dtype, int tokens, int outs, int width, const void* dy, long lon
     at += round_up(bytes, 256);
     return o;
   };
-  l.x = take((size_t)tokens * l.ldx * 2);
+  l.x = eight ? 0 : take((size_t)tokens * l.ldx * 2);
   l.d = l.copy_dy ? take((size_t)l.planes * tokens * l.ldd * 2) : 0;
   l.part = l.split ? take((size_t)2 * pieces * kTile * l.tile_n * 4) : 0;
   l.total = at;
   return true;
 }
 
-template <int PLANES>
+// {width, tokens} codes, boxes of 64 x kBK.
+int encode_codes(CUtensorMap* m, const void* codes, int width, int tokens, long long ldq) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return B2G_ERR_TENSOR_MAP;
+  cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)tokens, 1}, strides[2] = {(cuuint64_t)ldq, 16};
+  cuuint32_t box[3] = {64, kBK, 1}, estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? 0 : B2G_ERR_TENSOR_MAP;
+}
+
+// Either way's layout; x is read from its codes where that costs less than the launch that
+// prepares it (us, prepared and from the codes: 300 tokens on 512 x 256 7.4 and 6.4; 5844 on 128 x
+// 6944 43 and 29; 8192 on 2048 x 2048 48.5 and 56; 4096 on 4096 x 4096 86 and 102).
+// `total` is enough for both: rows off the 16-byte boundaries are prepared.
+bool layouts(int dtype, int tokens, int outs, int width, const void* dy, long long lddy, Layout& prepared,
+             Layout& l) {
+  if (!layout(dtype, tokens, outs, width, dy, lddy, false, prepared)) return false;
+  l = prepared;
+  if (prepared.copy_dy || prepared.k_tiles > kGroupK / kBK) return true;
+  layout(dtype, tokens, outs, width, dy, lddy, true, l);
+  if (l.cost >= prepared.cost + kPrepareCost + (long long)tokens * width / kPrepareBytes * 3)
+    l = prepared;
+  else
+    l.total = prepared.total = l.total > prepared.total ? l.total : prepared.total;
+  return true;
+}
+
+template <int PLANES, bool EIGHT>
 int launch(const Dw8Gemm& g, const Dw8Maps& maps, int pairs, const TrainDevice& d, cudaStream_t st) {
   static std::atomic<int> done[64];
   if (d.dev < 0 || d.dev >= 64) return B2G_ERR_DEVICE;
   if (!done[d.dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(dw8_kernel<PLANES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(dw8_kernel<PLANES, EIGHT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes) != cudaSuccess)
       return B2G_ERR_CUDA;
     done[d.dev].store(1, std::memory_order_release);
@@ -591,13 +883,13 @@ int launch(const Dw8Gemm& g, const Dw8Maps& maps, int pairs, const TrainDevice& 
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * pairs));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreads<EIGHT>);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   void* args[] = {const_cast<Dw8Gemm*>(&g), const_cast<Dw8Maps*>(&maps)};
-  return launch_code(cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&dw8_kernel<PLANES>), args));
+  return launch_code(cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&dw8_kernel<PLANES, EIGHT>), args));
 }
 
 }  // namespace
@@ -614,8 +906,8 @@ int b2g_linear_dweight8_workspace_size(int dtype, int tokens, int outs, int widt
   if (!bytes) return B2G_ERR_NULL;
   *bytes = 0;
   if (!tokens || !outs || !width) return 0;
-  Layout l;
-  if (!layout(dtype, tokens, outs, width, dy, lddy, l)) return B2G_ERR_INVALID_DIM;
+  Layout l, prepared;
+  if (!layouts(dtype, tokens, outs, width, dy, lddy, prepared, l)) return B2G_ERR_INVALID_DIM;
   *bytes = l.total;
   return 0;
 }
@@ -640,27 +932,14 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
   const size_t es = type_size(dtype);
   if (tokens == 0)
     return cudaMemset2DAsync(dw, lddw * es, 0, width * es, outs, st) == cudaSuccess ? 0 : B2G_ERR_CUDA;
-  Layout l;
-  if (!layout(dtype, tokens, outs, width, dy, lddy, l)) return B2G_ERR_INVALID_DIM;
+  Layout l, prepared;
+  if (!layouts(dtype, tokens, outs, width, dy, lddy, prepared, l)) return B2G_ERR_INVALID_DIM;
+  // a bulk-tensor store writes whole 16-byte units, those past the last column too; and it
+  // adds in the output's type: right for FP32 only
+  const bool out_tma = vec16(dw) && vec16_ld(lddw, dtype) && vec16_ld(width, dtype) && !(accumulate && !f32);
+  if (!out_tma || !vec16(codes) || ldq % 16) l = prepared;
   if (!workspace || !vec16(workspace) || workspace_bytes < l.total) return B2G_ERR_WORKSPACE;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-
-  Prepare q = {};
-  q.tokens = tokens;
-  q.k = Rows8{static_cast<unsigned char*>(const_cast<void*>(codes)), ldq,
-              static_cast<unsigned char*>(const_cast<void*>(scales)), lds, 0};
-  q.width = width, q.x = reinterpret_cast<Bf16*>(ws + l.x), q.ldx = l.ldx;
-  q.k.vec = codes_vec(q.k, 8);
-  q.dy = dy, q.lddy = lddy, q.outs = outs, q.planes = l.copy_dy ? l.planes : 0;
-  q.d = reinterpret_cast<Bf16*>(ws + l.d), q.ldd = l.ldd;
-  q.wx = walk_of(tokens, (int)ceil_div(width, 8), 1);
-  if (l.copy_dy) q.wd = walk_of(tokens, (int)ceil_div(outs, f32 ? 4 : 8), 1);
-  if (q.wx.blocks + q.wd.blocks > 0x7fffffffLL) return B2G_ERR_INVALID_DIM;
-  const dim3 grid((unsigned)(q.wx.blocks + q.wd.blocks));
-  rc = launch_code(f32 ? launch_train(dw8_prepare_kernel<float, true>, grid, dim3(256), 0, st, q)
-                   : l.copy_dy ? launch_train(dw8_prepare_kernel<Bf16, true>, grid, dim3(256), 0, st, q)
-                               : launch_train(dw8_prepare_kernel<Bf16, false>, grid, dim3(256), 0, st, q));
-  if (rc) return rc;
 
   Dw8Gemm g = {};
   g.rows = outs, g.cols = width;
@@ -673,18 +952,41 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
   g.group = f32 ? 4 : kGroupK / kBK;
   g.wait_limit_ns = d.wait_limit_ns, g.debug_stop = d.debug_stop, g.status = d.status;
   g.out = dw, g.ldo = lddw, g.out_bf16 = !f32, g.accumulate = accumulate != 0;
-  // a bulk-tensor store writes whole 16-byte units, those past the last column too; and it
-  // adds in the output's type: right for FP32 only
-  g.out_tma = vec16(dw) && vec16_ld(lddw, dtype) && vec16_ld(width, dtype) && !(accumulate && !f32);
-  g.add = accumulate != 0;
+  g.out_tma = out_tma, g.add = accumulate != 0;
+  g.scales = static_cast<const unsigned char*>(scales), g.lds = lds, g.tokens = tokens;
+
+  Bf16* const x = reinterpret_cast<Bf16*>(ws + l.x);
+  Bf16* const planes = reinterpret_cast<Bf16*>(ws + l.d);
+  if (!l.eight) {
+    Prepare q = {};
+    q.tokens = tokens;
+    q.k = Rows8{static_cast<unsigned char*>(const_cast<void*>(codes)), ldq,
+                static_cast<unsigned char*>(const_cast<void*>(scales)), lds, 0};
+    q.width = width, q.x = x, q.ldx = l.ldx;
+    q.k.vec = codes_vec(q.k, 8);
+    q.dy = dy, q.lddy = lddy, q.outs = outs, q.planes = l.copy_dy ? l.planes : 0;
+    q.d = planes, q.ldd = l.ldd;
+    q.wx = walk_of(tokens, (int)ceil_div(width, 8), 1);
+    if (l.copy_dy) q.wd = walk_of(tokens, (int)ceil_div(outs, f32 ? 4 : 8), 1);
+    if (q.wx.blocks + q.wd.blocks > 0x7fffffffLL) return B2G_ERR_INVALID_DIM;
+    const dim3 grid((unsigned)(q.wx.blocks + q.wd.blocks));
+    rc = launch_code(f32 ? launch_train(dw8_prepare_kernel<float, true>, grid, dim3(256), 0, st, q)
+                     : l.copy_dy ? launch_train(dw8_prepare_kernel<Bf16, true>, grid, dim3(256), 0, st, q)
+                                 : launch_train(dw8_prepare_kernel<Bf16, false>, grid, dim3(256), 0, st, q));
+    if (rc) return rc;
+  }
   Dw8Maps maps = {};
-  rc = l.copy_dy ? encode_rows(&maps.dy, false, q.d, outs, tokens, l.ldd, l.planes,
+  rc = l.copy_dy ? encode_rows(&maps.dy, false, planes, outs, tokens, l.ldd, l.planes,
                                (long long)tokens * l.ldd, 64)
                  : encode_rows(&maps.dy, false, dy, outs, tokens, lddy, 1, 0, 64);
-  if (!rc) rc = encode_rows(&maps.x, false, q.x, width, tokens, l.ldx, 1, 0, 64);
+  if (!rc)
+    rc = l.eight ? encode_codes(&maps.x, codes, width, tokens, ldq)
+                 : encode_rows(&maps.x, false, x, width, tokens, l.ldx, 1, 0, 64);
   if (!rc && g.out_tma) rc = encode_rows(&maps.out, f32, dw, width, outs, lddw, 1, 0, 32);
   if (rc) return rc;
-  rc = f32 ? launch<3>(g, maps, l.pairs, d, st) : launch<1>(g, maps, l.pairs, d, st);
+  rc = f32       ? launch<3, false>(g, maps, l.pairs, d, st)
+       : l.eight ? launch<1, true>(g, maps, l.pairs, d, st)
+                 : launch<1, false>(g, maps, l.pairs, d, st);
   if (rc || !l.split) return rc;
   // of a tile; one more where pieces lie across tiles
   const bool many = ceil_div(l.k_tiles, l.piece) + (l.span % l.piece ? 1 : 0) > kFewPieces;

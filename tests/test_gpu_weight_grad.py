@@ -70,6 +70,29 @@ def test_strides_accumulate_and_guards(b2g, tokens, outs, width, offset, extra, 
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("ld", [256, 257])
+def test_every_code_and_scale(b2g, ld, dtype):
+    """dy = the identity returns x's values: exactly, each is one BF16 number.  Scales from 2^-110
+    up to the largest whose products with 448 BF16 holds."""
+    r, c = torch.arange(256)[:, None], torch.arange(256)[None]
+    codes = ((r + c) % 256).to(torch.uint8)
+    codes[codes & 127 == 127] = 0
+    scales = (17 + (8 * r + torch.arange(8)[None]) % 230).to(torch.uint8)
+    flat = torch.zeros(256, ld, dtype=torch.uint8, device="cuda")
+    flat[:, :256] = codes
+    kept = flat.view(torch.float8_e4m3fn)[:, :256], scales.cuda().view(torch.float8_e8m0fnu)
+    dw = b2g.linear_weight_grad_8bit(torch.eye(256, dtype=dtype, device="cuda"), *kept)
+    assert torch.equal(dw.cpu().double(), e8.values(*kept))
+    # NaN stays in its column, a NaN scale in its 32
+    flat[5, 40], flat[255, 200] = 127, 255
+    kept[1].view(torch.uint8)[7, 3] = 255
+    dw = b2g.linear_weight_grad_8bit(torch.eye(256, dtype=dtype, device="cuda"), *kept)
+    lost = torch.zeros(256, dtype=torch.bool, device="cuda")
+    lost[40] = lost[200] = lost[96:128] = True
+    assert torch.isnan(dw[:, lost]).all() and torch.isfinite(dw[:, ~lost]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_no_tokens(b2g, dtype):
     dy = torch.empty(0, 40, dtype=dtype, device="cuda")
     kept = b2g.quantize_8bit(torch.empty(0, 72, dtype=dtype, device="cuda"))
