@@ -19,9 +19,10 @@
 // 775 to 870 us (1.70 to 1.91 PFLOP/s, under the power cap), 4096 on 4096 x 4096 86 us, of
 // which the products 70 and the preparation 8 to 10; 64 on 4096 x 4096 12.8 (34 MB written; 15.8
 // with a preparation).  FP32: 4096 on 4096 x 4096 237 us, 1.74 PFLOP/s of the three products.
-// Converting x on its way takes about 900 cycles a k tile, the products 520: bit operations, at half
-// the rate of multiplications, keep the converting warps busy for 450, and the rest is the latency
-// of barriers, loads and stores, half hidden by two groups of warps with a k tile each.
+// Converting x on its way takes about 900 cycles a k tile, the products alone 520: 80 KB through
+// shared memory (dy and codes in, codes out, BF16 in, both operands out) are 640 cycles, and the
+// converting warps' loads, bit operations (360 cycles of a scheduler's, at half rate) and barriers
+// follow one another, half hidden by two groups of warps with a k tile each.
 #include <atomic>
 #include <type_traits>
 

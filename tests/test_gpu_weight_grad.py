@@ -69,6 +69,26 @@ def test_strides_accumulate_and_guards(b2g, tokens, outs, width, offset, extra, 
         check(out, dy, x, was if accumulate else None)
 
 
+@pytest.mark.parametrize("lds", [0, 3])
+@pytest.mark.parametrize("tokens,outs,width", [
+    (70, 96, 200), (900, 520, 776), (1, 8, 8), (2000, 100, 136), (129, 1000, 72), (64, 300, 1000),
+    (65, 256, 264), (3000, 64, 520), (333, 264, 24), (1024, 2048, 2048), (2500, 600, 640)])
+def test_aligned_rows_in_larger_buffers(b2g, tokens, outs, width, lds):
+    """All rows on 16-byte boundaries, widths that end inside 16 and 32 columns; NaN codes and
+    scales behind x's rows, and nothing written behind dw's."""
+    dy, kept = operands(tokens, outs, width, BF16, seed=lds, lds=-(-width // 32) + lds,
+                        ld=-(-width // 16) * 16 + 16)
+    dy, _ = padded(dy.cpu().double(), BF16, -(-outs // 8) * 8 + 8)
+    out, flat = padded(torch.zeros(outs, width, dtype=torch.float64), BF16, width + 8)
+    before = flat.clone()
+    assert b2g.linear_weight_grad_8bit(dy, *kept, dw=out) is out
+    assert untouched(flat, out, before)
+    check(out, dy, e8.values(*kept))
+    # the same values in rows off the boundaries take the other way
+    _, other = operands(tokens, outs, width, BF16, seed=lds, offset=1, ld=width + 1)
+    check(b2g.linear_weight_grad_8bit(dy, *other), dy, e8.values(*kept))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("ld", [256, 257])
 def test_every_code_and_scale(b2g, ld, dtype):
@@ -192,6 +212,17 @@ def test_rows_past_32_bits_of_offset(b2g):
     x = torch.ones(70000, 48, dtype=BF16, device="cuda")
     dw = b2g.linear_weight_grad_8bit(dy, *b2g.quantize_8bit(x))
     assert (dw == -2).all()
+
+
+def test_codes_past_32_bits_of_offset(b2g):
+    flat = torch.zeros(20000, 1 << 18, dtype=torch.uint8, device="cuda")
+    scales = torch.full((20000, 1 << 17), 127, dtype=torch.uint8, device="cuda")
+    flat[0, :64], flat[-1, :64] = 0x38, 0xC0  # 1 and -2
+    scales[-1, :2] = 129
+    dw = b2g.linear_weight_grad_8bit(torch.ones(20000, 40, dtype=BF16, device="cuda"),
+                                     flat.view(torch.float8_e4m3fn)[:, :64],
+                                     scales.view(torch.float8_e8m0fnu)[:, :2])
+    assert (dw == 1 - 8).all()
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
