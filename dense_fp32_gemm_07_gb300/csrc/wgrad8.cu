@@ -875,6 +875,12 @@ int launch(const Dw8Gemm& g, const Dw8Maps& maps, int pairs, const TrainDevice& 
     if (cudaFuncSetAttribute(dw8_kernel<PLANES, EIGHT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes) != cudaSuccess)
       return B2G_ERR_CUDA;
+    // the warps' shares of registers have to be there at the start, or raising them never ends
+    constexpr int regs = 128 * kIssueRegs + 32 * kEpiWarps * kEpiRegs<EIGHT> + (EIGHT ? 32 * kCvtWarps * kCvtRegs : 0);
+    cudaFuncAttributes has;
+    if (cudaFuncGetAttributes(&has, dw8_kernel<PLANES, EIGHT>) != cudaSuccess ||
+        has.numRegs * kThreads<EIGHT> < regs)
+      return B2G_ERR_CUDA;
     done[d.dev].store(1, std::memory_order_release);
   }
   cudaLaunchAttribute attr[2];
