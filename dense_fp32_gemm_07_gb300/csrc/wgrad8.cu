@@ -850,17 +850,17 @@ int encode_codes(CUtensorMap* m, const void* codes, int width, int tokens, long 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? 0 : B2G_ERR_TENSOR_MAP;
 }
 
-// Either way's layout; x is read from its codes where that costs less than the launch that
-// prepares it (us, prepared and from the codes: 300 tokens on 512 x 256 7.4 and 6.4; 5844 on 128 x
+// Either way's layout; x is read from its codes where that costs less than preparing it, which
+// takes a launch (there is one all the same where dy has to be copied; us, prepared and from the codes: 300 tokens on 512 x 256 7.4 and 6.4; 5844 on 128 x
 // 6944 43 and 29; 8192 on 2048 x 2048 48.5 and 56; 4096 on 4096 x 4096 86 and 102).
 // `total` is enough for both: rows off the 16-byte boundaries are prepared.
 bool layouts(int dtype, int tokens, int outs, int width, const void* dy, long long lddy, Layout& prepared,
              Layout& l) {
   if (!layout(dtype, tokens, outs, width, dy, lddy, false, prepared)) return false;
   l = prepared;
-  if (prepared.copy_dy || prepared.k_tiles > kGroupK / kBK) return true;
+  if (prepared.planes > 1 || prepared.k_tiles > kGroupK / kBK) return true;
   layout(dtype, tokens, outs, width, dy, lddy, true, l);
-  if (l.cost >= prepared.cost + kPrepareCost + (long long)tokens * width / kPrepareBytes * 3)
+  if (l.cost >= prepared.cost + (l.copy_dy ? 0 : kPrepareCost) + (long long)tokens * width / kPrepareBytes * 3)
     l = prepared;
   else
     l.total = prepared.total = l.total > prepared.total ? l.total : prepared.total;
@@ -964,7 +964,7 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
 
   Bf16* const x = reinterpret_cast<Bf16*>(ws + l.x);
   Bf16* const planes = reinterpret_cast<Bf16*>(ws + l.d);
-  if (!l.eight) {
+  if (!l.eight || l.copy_dy) {
     Prepare q = {};
     q.tokens = tokens;
     q.k = Rows8{static_cast<unsigned char*>(const_cast<void*>(codes)), ldq,
@@ -973,7 +973,7 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
     q.k.vec = codes_vec(q.k, 8);
     q.dy = dy, q.lddy = lddy, q.outs = outs, q.planes = l.copy_dy ? l.planes : 0;
     q.d = planes, q.ldd = l.ldd;
-    q.wx = walk_of(tokens, (int)ceil_div(width, 8), 1);
+    if (!l.eight) q.wx = walk_of(tokens, (int)ceil_div(width, 8), 1);
     if (l.copy_dy) q.wd = walk_of(tokens, (int)ceil_div(outs, f32 ? 4 : 8), 1);
     if (q.wx.blocks + q.wd.blocks > 0x7fffffffLL) return B2G_ERR_INVALID_DIM;
     const dim3 grid((unsigned)(q.wx.blocks + q.wd.blocks));

@@ -71,7 +71,7 @@ def test_strides_accumulate_and_guards(b2g, tokens, outs, width, offset, extra, 
 
 @pytest.mark.parametrize("lds", [0, 3])
 @pytest.mark.parametrize("tokens,outs,width", [
-    (70, 96, 200), (900, 520, 776), (1, 8, 8), (2000, 100, 136), (129, 1000, 72), (64, 300, 1000),
+    (70, 96, 200), (900, 520, 776), (900, 77, 1000), (1, 8, 8), (2000, 100, 136), (129, 1000, 72), (64, 300, 1000),
     (65, 256, 264), (3000, 64, 520), (333, 264, 24), (1024, 2048, 2048), (2500, 600, 640)])
 def test_aligned_rows_in_larger_buffers(b2g, tokens, outs, width, lds):
     """All rows on 16-byte boundaries, widths that end inside 16 and 32 columns; NaN codes and
