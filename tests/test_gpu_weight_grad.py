@@ -84,6 +84,8 @@ def test_aligned_rows_in_larger_buffers(b2g, tokens, outs, width, lds):
     assert b2g.linear_weight_grad_8bit(dy, *kept, dw=out) is out
     assert untouched(flat, out, before)
     check(out, dy, e8.values(*kept))
+    odd, _ = padded(dy.cpu().double(), BF16, outs + 1, 3)
+    check(b2g.linear_weight_grad_8bit(odd, *kept), dy, e8.values(*kept))
     # the same values in rows off the boundaries take the other way
     _, other = operands(tokens, outs, width, BF16, seed=lds, offset=1, ld=width + 1)
     check(b2g.linear_weight_grad_8bit(dy, *other), dy, e8.values(*kept))
