@@ -152,11 +152,11 @@ __device__ __forceinline__ void stores_done() {
 // v (plus the old values) to a warp's rows of a result that a bulk-tensor store
 // cannot write (alignment) or add to (BF16): 32 columns at a time through the buffer,
 // so that each store is a stretch of one row.
-template <typename T, typename P>
-__device__ __forceinline__ void put_rows(T* out, const float (&v)[128], const P& p, int row0,
+template <typename T, int N, typename P>
+__device__ __forceinline__ void put_rows(T* out, const float (&v)[N], const P& p, int row0,
                                          int left, uint32_t buf, int lane) {
 #pragma unroll
-  for (int c = 0; c < 128; c += 32) {
+  for (int c = 0; c < N; c += 32) {
     if (c < left) {
       uint4 w[8];
 #pragma unroll

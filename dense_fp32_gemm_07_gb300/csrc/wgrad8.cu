@@ -175,7 +175,8 @@ __device__ __forceinline__ void put_tile(const Dw8Gemm& p, const CUtensorMap* m,
   }
 }
 
-// A unit of one accumulation group to BF16 by bulk-tensor stores, or its sums, 64 columns at a time.
+// A unit of one accumulation group to BF16, or its sums, 64 columns at a time; of each four the
+// second and third are back in their places.
 // False when the wait for it ran out.
 __device__ __forceinline__ bool put_bf16(const Dw8Gemm& p, const Unit& u, const CUtensorMap* m,
                                          uint32_t tmem_lane, int span, int rows, int half, int row0, int n0,
@@ -210,6 +211,16 @@ __device__ __forceinline__ bool put_bf16(const Dw8Gemm& p, const Unit& u, const 
         if (c + 4 * j + 32 < left)
           to[32 * j + 256] = make_uint4(x[4 * j], x[4 * j + 2], x[4 * j + 1], x[4 * j + 3]);
       }
+    } else if (!p.out_tma) {
+      float f[64];
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        f[j] = __uint_as_float(v[j]), f[j + 1] = __uint_as_float(v[j + 2]);
+        f[j + 2] = __uint_as_float(v[j + 1]), f[j + 3] = __uint_as_float(v[j + 3]);
+        f[32 + j] = __uint_as_float(x[j]), f[33 + j] = __uint_as_float(x[j + 2]);
+        f[34 + j] = __uint_as_float(x[j + 1]), f[35 + j] = __uint_as_float(x[j + 3]);
+      }
+      put_rows(static_cast<Bf16*>(p.out) + (long long)row0 * p.ldo + n0 + c, f, p, row0, left - c, buf, lane);
     } else {
       uint4 w[8];
       auto two = [](uint32_t lo, uint32_t hi) { return pack_bf16(__uint_as_float(lo), __uint_as_float(hi)); };
@@ -941,10 +952,7 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
     return cudaMemset2DAsync(dw, lddw * es, 0, width * es, outs, st) == cudaSuccess ? 0 : B2G_ERR_CUDA;
   Layout l, prepared;
   if (!layouts(dtype, tokens, outs, width, dy, lddy, prepared, l)) return B2G_ERR_INVALID_DIM;
-  // a bulk-tensor store writes whole 16-byte units, those past the last column too; and it
-  // adds in the output's type: right for FP32 only
-  const bool out_tma = vec16(dw) && vec16_ld(lddw, dtype) && vec16_ld(width, dtype) && !(accumulate && !f32);
-  if (!out_tma || !vec16(codes) || ldq % 16) l = prepared;
+  if (!vec16(codes) || ldq % 16) l = prepared;
   if (!workspace || !vec16(workspace) || workspace_bytes < l.total) return B2G_ERR_WORKSPACE;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
 
@@ -959,7 +967,10 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
   g.group = f32 ? 4 : kGroupK / kBK;
   g.wait_limit_ns = d.wait_limit_ns, g.debug_stop = d.debug_stop, g.status = d.status;
   g.out = dw, g.ldo = lddw, g.out_bf16 = !f32, g.accumulate = accumulate != 0;
-  g.out_tma = out_tma, g.add = accumulate != 0;
+  // a bulk-tensor store writes whole 16-byte units, those past the last column too; and it
+  // adds in the output's type: right for FP32 only
+  g.out_tma = vec16(dw) && vec16_ld(lddw, dtype) && vec16_ld(width, dtype) && !(accumulate && !f32);
+  g.add = accumulate != 0;
   g.scales = static_cast<const unsigned char*>(scales), g.lds = lds, g.tokens = tokens;
 
   Bf16* const x = reinterpret_cast<Bf16*>(ws + l.x);
