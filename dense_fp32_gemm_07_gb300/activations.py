@@ -271,8 +271,8 @@ def linear_weight_grad_8bit(dy, codes, scales, dw=None, accumulate: bool = False
     `dw` takes the result; with `accumulate` it is added to the values there.  x's values
     are exact in the products, which add up in float32; with float32 dy all its 24 bits
     take part (dy must be finite)."""
-    if dw is None and stream is None and not accumulate:
-        got = _fast().linear_weight_grad_8bit(dy, codes, scales)
+    if stream is None:
+        got = _fast().linear_weight_grad_8bit(dy, codes, scales, dw, accumulate)
         if got is not None:
             return _plain(got)
     n, o, lddy = _matrix(dy, "dy")

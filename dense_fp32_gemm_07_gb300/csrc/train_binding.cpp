@@ -508,23 +508,42 @@ PyObject* rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// linear_weight_grad_8bit(dy, codes, scales)
+// Whether a contiguous tensor and `bytes` from `at` on have nothing in common.
+bool clear_of(const Tensor& t, const void* at, int64_t bytes) {
+  const char *a = static_cast<const char*>(ptr(t)), *b = static_cast<const char*>(at);
+  return a + t.nbytes() <= b || b + bytes <= a;
+}
+
+// linear_weight_grad_8bit(dy, codes, scales, dw, accumulate)
 PyObject* linear_weight_grad_8bit(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 3 || !is_tensor(a[0]) || !is_tensor(a[1]) || !is_tensor(a[2])) Py_RETURN_NONE;
-  const Tensor& dy = tensor(a[0]);
+  if (n != 5 || !is_tensor(a[0]) || !is_tensor(a[1]) || !is_tensor(a[2]) || !is_tensor_or_none(a[3]) ||
+      !PyBool_Check(a[4]))
+    Py_RETURN_NONE;
+  const Tensor &dy = tensor(a[0]), &given = tensor(a[3]);
+  const bool accumulate = a[4] == Py_True;
   Eight e(tensor(a[1]), tensor(a[2]));
   Kind k;
   if (!k.take(dy) || !k.matrix(dy) || !e.take(k) || e.rows != dy.size(0)) Py_RETURN_NONE;
   const int64_t t = e.rows, o = dy.size(1);
   if (!small(t) || !small(o) || !small(e.cols)) Py_RETURN_NONE;
+  if (given.defined()) {
+    if (!k.matrix(given) || given.size(0) != o || given.size(1) != e.cols ||
+        !clear_of(given, ptr(dy), dy.nbytes()) || !clear_of(given, ptr(e.q), e.rows * e.ldq) ||
+        !clear_of(given, ptr(e.s), e.rows * e.lds))
+      Py_RETURN_NONE;
+  } else if (accumulate) {
+    Py_RETURN_NONE;
+  }
   size_t bytes = 0;
   int rc = b2g_linear_dweight8_workspace_size(k.code, (int)t, (int)o, (int)e.cols, ptr(dy), ld(o), &bytes);
   if (rc) return PyLong_FromLong(rc);
-  const Tensor dw = k.empty({o, e.cols}), ws = k.bytes(bytes);
+  const Tensor dw = given.defined() ? given : k.empty({o, e.cols}), ws = k.bytes(bytes);
   rc = b2g_linear_dweight8(k.code, (int)t, (int)o, (int)e.cols, ptr(dy), ld(o), ptr(e.q), e.ldq, ptr(e.s),
-                           e.lds, 0, ptr(dw), e.cols, ptr(ws), bytes, k.stream);
-  return answer(rc, dw);
+                           e.lds, accumulate, ptr(dw), e.cols, ptr(ws), bytes, k.stream);
+  if (rc || !given.defined()) return answer(rc, dw);
+  Py_INCREF(a[3]);
+  return a[3];
   END_HANDLE_TH_ERRORS
 }
 
