@@ -862,9 +862,10 @@ int encode_codes(CUtensorMap* m, const void* codes, int width, int tokens, long 
 }
 
 // Either way's layout; x is read from its codes where that costs less than preparing it, which
-// takes a launch (there is one all the same where dy has to be copied; us, prepared and from the codes: 300 tokens on 512 x 256 7.4 and 6.4; 5844 on 128 x
-// 6944 43 and 29; 8192 on 2048 x 2048 48.5 and 56; 4096 on 4096 x 4096 86 and 102).
-// `total` is enough for both: rows off the 16-byte boundaries are prepared.
+// takes a launch (there is one all the same where dy has to be copied).  Us, prepared and from the
+// codes: 300 tokens on 512 x 256 7.4 and 6.4; 5844 on 128 x 6944 43 and 27; 8192 on 2048 x 2048
+// 48.5 and 56; 4096 on 4096 x 4096 86 and 102.  `total` is enough for both, since codes off
+// the 16-byte boundaries are prepared in any case.
 bool layouts(int dtype, int tokens, int outs, int width, const void* dy, long long lddy, Layout& prepared,
              Layout& l) {
   if (!layout(dtype, tokens, outs, width, dy, lddy, false, prepared)) return false;
