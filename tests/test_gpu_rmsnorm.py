@@ -393,3 +393,25 @@ def test_scales_that_are_nan(b2g):
         rstd = torch.ones(1500, device="cuda")
         dx, _ = b2g.rms_norm_backward(x, kept, None, rstd)
         assert torch.isnan(dx[7]).all() and torch.isfinite(dx[:7]).all() and torch.isfinite(dx[8:]).all()
+
+
+@pytest.mark.parametrize("rows,cols", [(16, 4096), (9, 777)])
+def test_few_rows_captured_and_on_another_stream(b2g, rows, cols):
+    x, dy, dtotal = (torch.randn(rows, cols, device="cuda").bfloat16() for _ in range(3))
+    w = torch.randn(cols, device="cuda").bfloat16()
+    _, total, rstd = b2g.rms_norm(x, w)
+    want = b2g.rms_norm_backward(dy, total, w, rstd, dtotal)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = b2g.rms_norm_backward(dy, total, w, rstd, dtotal, stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(other, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = [b2g.rms_norm_backward(dy, total, w, rstd, dtotal) for _ in range(3)]
+    for _ in range(3):
+        dy.mul_(1.25)
+        g.replay()
+        want = b2g.rms_norm_backward(dy, total, w, rstd, dtotal)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for out in outs for a, b in zip(out, want))

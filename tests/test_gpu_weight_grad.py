@@ -207,6 +207,27 @@ def test_other_stream_and_graphs(b2g):
             assert torch.equal(outs[k], want)
 
 
+@pytest.mark.parametrize("tokens,outs,width", [(300, 512, 256), (1000, 128, 4096), (64, 100, 255)])
+def test_two_streams_at_once(b2g, tokens, outs, width):
+    """Calls that run side by side, one writing over its own result and one adding to it."""
+    dy, kept = operands(tokens, outs, width, BF16)
+    want = b2g.linear_weight_grad_8bit(dy, *kept)
+    twice = b2g.linear_weight_grad_8bit(dy, *kept, dw=want.clone(), accumulate=True)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs8 = [[], []]
+    for _ in range(20):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                dw = b2g.linear_weight_grad_8bit(dy, *kept)
+                if k:
+                    assert b2g.linear_weight_grad_8bit(dy, *kept, dw=dw, accumulate=True) is dw
+                outs8[k].append(dw)
+    torch.cuda.synchronize()
+    assert all(torch.equal(dw, want) for dw in outs8[0])
+    assert all(torch.equal(dw, twice) for dw in outs8[1])
+
+
 def test_rows_past_32_bits_of_offset(b2g):
     flat = torch.zeros(70000, 32768, dtype=BF16, device="cuda")
     dy = flat[:, :40]
