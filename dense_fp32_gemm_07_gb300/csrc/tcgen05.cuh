@@ -112,9 +112,13 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
                : "memory");
 }
 
-// The same where the arrival has nothing of this thread's to order for the other CTA.
-__device__ __forceinline__ void mbar_signal_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// The same in two steps, for several arrivals at once: the fence orders what this thread
+// wrote, and what it knows of from others, before the arrivals that follow.
+__device__ __forceinline__ void fence_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // mbar_try_wait that also orders what other CTAs of the cluster wrote before they arrived.

@@ -17,12 +17,13 @@
 //
 // Bound: the tensor cores; short sums, writing the result.  BF16: 16384 tokens on 11008 x 4096
 // 775 to 870 us (1.70 to 1.91 PFLOP/s, under the power cap), 4096 on 4096 x 4096 86 us, of
-// which the products 70 and the preparation 8 to 10; 64 on 4096 x 4096 12.8 (34 MB written; 15.8
+// which the products 70 and the preparation 8 to 10; 64 on 4096 x 4096 13.7 (34 MB written; 15.5
 // with a preparation).  FP32: 4096 on 4096 x 4096 237 us, 1.74 PFLOP/s of the three products.
-// Converting x on its way takes about 900 cycles a k tile, the products alone 520: 80 KB through
-// shared memory (dy and codes in, codes out, BF16 in, both operands out) are 640 cycles, and the
+// Converting x on its way takes about 1150 cycles a k tile, the products alone 520: 80 KB through
+// shared memory (dy and codes in, codes out, BF16 in, both operands out) are 640 cycles; the
 // converting warps' loads, bit operations (360 cycles of a scheduler's, at half rate) and barriers
-// follow one another, half hidden by two groups of warps with a k tile each.
+// follow one another, half hidden by two groups of warps with a k tile each; and the odd CTA's
+// tiles wait for a fence of the cluster, which the five stages do not hide altogether.
 #include <atomic>
 #include <type_traits>
 
@@ -33,9 +34,9 @@ namespace b2g {
 namespace {
 
 // Warp 0 copies, warp 1 multiplies; with EIGHT warp 2 copies x's codes, kCvtWarps more warps
-// write them to the stages as BF16, and warp 3 of the odd CTA tells the even one.
+// write them to the stages as BF16, and warps 1 and 3 of the odd CTA tell the even one.
 constexpr int kCvtWarps = 8;
-// Groups of them with a k tile each (4096 tokens on 4096 x 4096: 102 us; all on one 126).
+// Groups of them with a k tile each: what the warps of one wait for, the other one hides.
 constexpr int kCvtGroups = 2;
 template <bool EIGHT>
 constexpr int kThreads = 128 + 32 * (kEpiWarps + (EIGHT ? kCvtWarps : 0));
@@ -55,7 +56,12 @@ constexpr uint32_t kStageBytes = (PLANES + 1) * kOperand;
 constexpr int kMaxStages = 6;
 constexpr int kCodeTiles = 4;                   // 64 tokens x 128 codes
 constexpr uint32_t kCodeBytes = kBK * 128;
-constexpr int kNumBars = 3 * kMaxStages + 5 + 2 * kCodeTiles;
+// Barriers on which a group of converting warps of the odd CTA announces its k tiles in turns.
+// Their tiles reach as far as the stages, so that none is announced a second time before the
+// even CTA has been told of the first.
+constexpr int kTellSlots = 3;
+static_assert(kCvtGroups == 2 && kCvtGroups * kTellSlots >= kStages<1, true>);
+constexpr int kNumBars = 2 * kMaxStages + 5 + 2 * kCodeTiles + kCvtGroups * kTellSlots;
 constexpr int kSmemBytes = 12 * kOperand + kEpiWarps * kOutBytes + 1024 + kNumBars * 8 + 16;
 constexpr uint32_t kTmemCols = 2 * kTile;
 constexpr int kPairs = 76;  // what the work is shared out among (GB300: 152 SMs)
@@ -300,13 +306,16 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
   const bool even = rank == 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
-  auto odd_full = [&](int s) { return bars + 8u * (2 * kMaxStages + 5 + 2 * kCodeTiles + s); };
+  auto tell = [&](int g, int i) {
+    return bars + 8u * (2 * kMaxStages + 5 + 2 * kCodeTiles + g * kTellSlots + i);
+  };
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full(s), EIGHT ? 2 + kCvtWarps / kCvtGroups : 1);
-      if (EIGHT) mbar_init(odd_full(s), kCvtWarps / kCvtGroups);
       mbar_init(empty(s), 1);
     }
+    if (EIGHT)
+      for (int i = 0; i < kCvtGroups * kTellSlots; ++i) mbar_init(tell(0, i), kCvtWarps / kCvtGroups);
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull(a), 1);
       mbar_init(tempty(a), 2 * kEpiWarps);
@@ -376,9 +385,9 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
         }
       }
       __syncwarp();
-    } else if (warp == 1) {
-      // ---------------------------------------------------------- MMA issuer (even CTA)
-      if (even && lane == 0) {
+    } else if (warp == 1 && even) {
+      // ---------------------------------------------------------- MMA issuer
+      if (lane == 0) {
         int s = 0, a = 0;
         uint32_t ph = 0, aph = 0;
         const uint32_t empty_odd = mapa_shared(empty(0), 1), tfull_odd = mapa_shared(tfull(0), 1);
@@ -448,21 +457,35 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
       __syncwarp();
     } else if (EIGHT && !even) {
       // ---------------------------------------------------------- the odd CTA's converted tiles
-      // What is announced lies in this CTA's shared memory, where its writers have made it visible
-      // to the tensor core (fence.proxy.async) before this thread saw them arrive; the even
-      // CTA only learns of it.  So the arrival orders no other memory of this thread: as a release
-      // for the cluster it took 1400 cycles a k tile (4096 tokens on 4096 x 4096 218 us for 125).
+      // Warps 1 and 3 tell the even CTA of a group's tiles each: its MMAs read them in this CTA's
+      // shared memory.  The converting warps' writes (and their fence.proxy.async) reach the MMAs'
+      // issuer by two links: the release and acquire of `tell` within this CTA, then the fence here
+      // and the issuer's acquire, both for the cluster.  The fence takes about 1400 cycles, more
+      // than a k tile does; so each group has a thread of its own for it, and one fence does for
+      // all of the tiles that are there.
       if (lane == 0) {
+        const int group = warp >> 1;
         const uint32_t full_even = mapa_shared(full(0), 0);
-        int s = 0;
+        int s = group, i = 0;
         uint32_t ph = 0;
+        unsigned seen = 0;
         bool on = true;
         Unit u;
         for (int k = 0; on && unit_at(p, pair, pairs, k, u); ++k) {
-          for (int kt = u.kt0; kt < u.kt1; ++kt) {
-            if (!(on = wait_phase(odd_full(s), ph, p, kStatusTimeoutFull))) break;
-            mbar_signal_remote(full_even + 8u * s);
-            if (++s == S) s = 0, ph ^= 1u;
+          int kt = u.kt0 + (int)((group - seen) & (kCvtGroups - 1));
+          seen += u.kt1 - u.kt0;
+          while (kt < u.kt1) {
+            if (!(on = wait_phase(tell(group, i), ph, p, kStatusTimeoutFull))) break;
+            int n = 0;
+            do {
+              ++n, kt += kCvtGroups;
+              if (++i == kTellSlots) i = 0, ph ^= 1u;
+            } while (n < kTellSlots && kt < u.kt1 && mbar_test_wait(tell(group, i), ph));
+            fence_cluster();
+            for (; n; --n) {
+              mbar_arrive_remote_relaxed(full_even + 8u * s);
+              if ((s += kCvtGroups) >= S) s -= S;
+            }
           }
         }
       }
@@ -479,11 +502,11 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
     // chunk h is of half h & 1.  Eight lanes' units of 16 bytes lie in eight different places of
     // 128 bytes, here and there.
     const int chunk = t & 3, token = t >> 2;
-    const uint32_t done = even ? full(0) : odd_full(0);
     const uint32_t from0 = codes + token * 64 + chunk * 16;
     const uint32_t to0 = base + PLANES * kOperand + token * 128 + ((2 * chunk ^ (token & 7)) << 4);
-    int s = group, c = group, seen = 0;
+    int s = group, c = group, told = 0;
     uint32_t ph = 0, cph = 0;
+    unsigned seen = 0;
     bool on = true;
     Unit u;
     for (int k = 0; on && unit_at(p, pair, pairs, k, u); ++k) {
@@ -491,7 +514,7 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
       tile_at(p, u.tile, tm, tn);
       const int col = tn * p.tile_n + u.col + (int)rank * (u.cols / 2) + 16 * chunk;
       const bool wide = u.cols > 128;
-      int kt = u.kt0 + ((group - seen) & (G - 1));
+      int kt = u.kt0 + (int)((group - seen) & (G - 1));
       seen += u.kt1 - u.kt0;
       // the scales of this group's next k tile are on their way
       uint32_t b[N];
@@ -545,8 +568,9 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(cempty(c));
-          mbar_arrive(done + 8u * s);
+          mbar_arrive(even ? full(s) : tell(group, told));
         }
+        if (++told == kTellSlots) told = 0;
         row += G * kBK, from += (long long)G * kBK * p.lds;
         scales();
         if ((s += G) >= S) s -= S, ph ^= 1u;
@@ -783,10 +807,10 @@ struct Layout {
   size_t x, d, part, total;
 };
 
-// Cycles of a k tile: BF16 its copies (64 bytes a cycle and SM), with EIGHT the conversion, FP32
-// its three products.
+// Cycles of a k tile: BF16 its copies (64 bytes a cycle and SM), with EIGHT the conversion and its
+// announcement to the other CTA, FP32 its three products.
 long long k_tile_cost(int planes, int tile_n, bool eight) {
-  return planes == 3 ? 1900 : eight ? 900 : kTile + tile_n;
+  return planes == 3 ? 1900 : eight ? 1150 : kTile + tile_n;
 }
 // The launch that prepares x, and the bytes that it moves in a cycle.
 constexpr long long kPrepareCost = 4000, kPrepareBytes = 3200;
@@ -863,9 +887,9 @@ int encode_codes(CUtensorMap* m, const void* codes, int width, int tokens, long 
 
 // Either way's layout; x is read from its codes where that costs less than preparing it, which
 // takes a launch (there is one all the same where dy has to be copied).  Us, prepared and from the
-// codes: 300 tokens on 512 x 256 7.4 and 6.4; 5844 on 128 x 6944 43 and 27; 8192 on 2048 x 2048
-// 48.5 and 56; 4096 on 4096 x 4096 86 and 102.  `total` is enough for both, since codes off
-// the 16-byte boundaries are prepared in any case.
+// codes: 300 tokens on 512 x 256 7.3 and 7.1; 5844 on 128 x 6944 43 and 31; 16384 on 512 x 8192
+// 141 and 143; 8192 on 2048 x 2048 48.5 and 72; 4096 on 4096 x 4096 86 and 127.  `total` is enough
+// for both, since codes off the 16-byte boundaries are prepared in any case.
 bool layouts(int dtype, int tokens, int outs, int width, const void* dy, long long lddy, Layout& prepared,
              Layout& l) {
   if (!layout(dtype, tokens, outs, width, dy, lddy, false, prepared)) return false;
