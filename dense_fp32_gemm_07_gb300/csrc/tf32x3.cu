@@ -505,6 +505,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
         tc_unit(p, u, tile, kt0, kt1, part);
         if (!mbar_wait(tempty(a), aph ^ 1u, p.wait_limit_ns, p.status, kStatusTimeoutTmem))
           goto mma_done;
+        mbar_try_wait_cluster(tempty(a), aph ^ 1u);  // true by now; for the odd CTA's arrivals
         tc_fence_after_sync();
         const uint32_t d = tmem + (uint32_t)(a * PN);
         for (int kt = kt0; kt < kt1; ++kt) {

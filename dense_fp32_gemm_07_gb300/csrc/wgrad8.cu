@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads<EIGHT>, 1)
           const int groups = groups_of(p, u.kt1 - u.kt0);
           const uint32_t idesc = idesc_bf16(kTile, u.cols, true, true);
           for (int g = 0; on && g < groups; ++g) {
-            if (!(on = wait_phase(tempty(a), aph ^ 1u, p, kStatusTimeoutTmem))) break;
+            if (!(on = wait_phase<true>(tempty(a), aph ^ 1u, p, kStatusTimeoutTmem))) break;
             tc_fence_after_sync();
             const uint32_t d = tmem + (uint32_t)(a * kTile);
             const int kts = min(p.group, u.kt1 - u.kt0 - g * p.group);

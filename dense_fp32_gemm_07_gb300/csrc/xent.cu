@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           slice_range(p, slice, kt0, kt1);
           const int groups = groups_of(p, kt1 - kt0);
           for (int g = 0; g < groups; ++g) {
-            if (!wait_phase(tempty(a), aph ^ 1u, p0, kStatusTimeoutTmem))
+            if (!wait_phase<true>(tempty(a), aph ^ 1u, p0, kStatusTimeoutTmem))
               return false;
             tc_fence_after_sync();
             const uint32_t d = tmem + (uint32_t)(a * kTile);
