@@ -179,7 +179,7 @@ def _rms(x, weight, residual, eps, with_y, with_y8, with_t8, out, stream):
             if t is not None and (out.data_ptr() != t.data_ptr() or ldy != ld):
                 _apart(out, (name, t))
         _apart(out, ("weight", weight))
-        if residual is None and out.data_ptr() == x.data_ptr():
+        if residual is None and out.data_ptr() == x.data_ptr() and x.numel():
             # total would be x, which y overwrites
             raise ValueError("out may be x only with a residual")
     elif with_y:
