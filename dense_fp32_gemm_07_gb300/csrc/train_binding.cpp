@@ -6,14 +6,17 @@
 //
 // Each function answers a result as train.py documents it, or the library's error
 // code as an int, or None when an argument is not of that plain kind (strided,
-// another stream, `out` given, wrong in some way); train.py then goes through its
-// own checks, which serve it or say what is wrong.
+// another stream, `out` given, wrong in some way) or torch's dispatcher is watched;
+// train.py then goes through its own checks, which serve it or say what is wrong.
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/Context.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <ATen/record_function.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -26,6 +29,16 @@
 namespace {
 
 using at::Tensor;
+
+// Whether somebody looks at the operators that torch dispatches (a mode, a tracer, a function
+// transform, a profiler), or wants uninitialised memory filled: both happen in at::empty, which
+// Kind::empty goes past.
+bool watched() {
+  const auto& more = c10::impl::tls_local_dispatch_key_set().included_;
+  if (!(more - c10::default_included_set).empty() || at::hasCallbacks()) return true;
+  const auto& context = at::globalContext();
+  return context.deterministicAlgorithms() && context.deterministicFillUninitializedMemory();
+}
 
 // A call's element type and device, from its first operand.
 struct Kind {
@@ -47,7 +60,7 @@ struct Kind {
   // The device alone.
   bool at(const Tensor& t) {
     device = t.device();
-    if (!device.is_cuda() || device.index() != c10::cuda::current_device()) return false;
+    if (!device.is_cuda() || device.index() != c10::cuda::current_device() || watched()) return false;
     stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
     return true;
   }
