@@ -292,7 +292,8 @@ def linear_weight_grad_8bit(dy, codes, scales, dw=None, accumulate: bool = False
         lddw = _result(dw, "dw", (o, w), dt, dev)
         _apart(dw, ("dy", dy), ("codes", codes), ("scales", scales))
     code, pdy = _CODES[dt], dy.data_ptr()
-    nb = _size(_train._lib.b2g_linear_dweight8_workspace_size, code, n, o, w, pdy, lddy)
+    nb = _size(_train._lib.b2g_linear_dweight8_workspace_size_ex, code, n, o, w, pdy, lddy,
+               codes.data_ptr(), ldq)
     ws = on.empty((nb,), _torch().uint8, device)
     rc = _train._lib.b2g_linear_dweight8(code, n, o, w, pdy, lddy, codes.data_ptr(), ldq,
                                          scales.data_ptr(), lds, 1 if accumulate else 0,

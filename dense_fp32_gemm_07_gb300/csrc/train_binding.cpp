@@ -549,7 +549,8 @@ PyObject* linear_weight_grad_8bit(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   }
   size_t bytes = 0;
-  int rc = b2g_linear_dweight8_workspace_size(k.code, (int)t, (int)o, (int)e.cols, ptr(dy), ld(o), &bytes);
+  int rc = b2g_linear_dweight8_workspace_size_ex(k.code, (int)t, (int)o, (int)e.cols, ptr(dy), ld(o), ptr(e.q),
+                                                 e.ldq, &bytes);
   if (rc) return PyLong_FromLong(rc);
   const Tensor dw = given.defined() ? given : k.empty({o, e.cols}), ws = k.bytes(bytes);
   rc = b2g_linear_dweight8(k.code, (int)t, (int)o, (int)e.cols, ptr(dy), ld(o), ptr(e.q), e.ldq, ptr(e.s),

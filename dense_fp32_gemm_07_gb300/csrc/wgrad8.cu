@@ -888,8 +888,8 @@ int encode_codes(CUtensorMap* m, const void* codes, int width, int tokens, long 
 // Either way's layout; x is read from its codes where that costs less than preparing it, which
 // takes a launch (there is one all the same where dy has to be copied).  Us, prepared and from the
 // codes: 300 tokens on 512 x 256 7.3 and 7.1; 5844 on 128 x 6944 43 and 31; 16384 on 512 x 8192
-// 141 and 143; 8192 on 2048 x 2048 48.5 and 72; 4096 on 4096 x 4096 86 and 127.  `total` is enough
-// for both, since codes off the 16-byte boundaries are prepared in any case.
+// 141 and 143; 8192 on 2048 x 2048 48.5 and 72; 4096 on 4096 x 4096 86 and 127.  Codes off the
+// 16-byte boundaries are prepared in any case.
 bool layouts(int dtype, int tokens, int outs, int width, const void* dy, long long lddy, Layout& prepared,
              Layout& l) {
   if (!layout(dtype, tokens, outs, width, dy, lddy, false, prepared)) return false;
@@ -898,9 +898,19 @@ bool layouts(int dtype, int tokens, int outs, int width, const void* dy, long lo
   layout(dtype, tokens, outs, width, dy, lddy, true, l);
   if (l.cost >= prepared.cost + (l.copy_dy ? 0 : kPrepareCost) + (long long)tokens * width / kPrepareBytes * 3)
     l = prepared;
-  else
-    l.total = prepared.total = l.total > prepared.total ? l.total : prepared.total;
   return true;
+}
+bool codes_fit(const void* codes, long long ldq) { return vec16(codes) && ldq % 16 == 0; }
+
+// Both layouts for a workspace query; without a product they need nothing.
+int query(int dtype, int tokens, int outs, int width, const void* dy, long long lddy, const size_t* bytes,
+          Layout& prepared, Layout& l) {
+  const int rc = check(dtype, tokens, outs, width);
+  if (rc) return rc;
+  if (!bytes) return B2G_ERR_NULL;
+  l = prepared = {};
+  if (!tokens || !outs || !width) return 0;
+  return layouts(dtype, tokens, outs, width, dy, lddy, prepared, l) ? 0 : B2G_ERR_INVALID_DIM;
 }
 
 template <int PLANES, bool EIGHT>
@@ -944,15 +954,19 @@ extern "C" {
 
 int b2g_linear_dweight8_workspace_size(int dtype, int tokens, int outs, int width, const void* dy,
                                        long long lddy, size_t* bytes) {
-  const int rc = check(dtype, tokens, outs, width);
-  if (rc) return rc;
-  if (!bytes) return B2G_ERR_NULL;
-  *bytes = 0;
-  if (!tokens || !outs || !width) return 0;
   Layout l, prepared;
-  if (!layouts(dtype, tokens, outs, width, dy, lddy, prepared, l)) return B2G_ERR_INVALID_DIM;
-  *bytes = l.total;
-  return 0;
+  const int rc = query(dtype, tokens, outs, width, dy, lddy, bytes, prepared, l);
+  if (!rc) *bytes = l.total > prepared.total ? l.total : prepared.total;
+  return rc;
+}
+
+int b2g_linear_dweight8_workspace_size_ex(int dtype, int tokens, int outs, int width, const void* dy,
+                                          long long lddy, const void* codes, long long ldq,
+                                          size_t* bytes) {
+  Layout l, prepared;
+  const int rc = query(dtype, tokens, outs, width, dy, lddy, bytes, prepared, l);
+  if (!rc) *bytes = codes_fit(codes, ldq) ? l.total : prepared.total;
+  return rc;
 }
 
 int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* dy, long long lddy,
@@ -977,8 +991,8 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
     return cudaMemset2DAsync(dw, lddw * es, 0, width * es, outs, st) == cudaSuccess ? 0 : B2G_ERR_CUDA;
   Layout l, prepared;
   if (!layouts(dtype, tokens, outs, width, dy, lddy, prepared, l)) return B2G_ERR_INVALID_DIM;
-  if (!vec16(codes) || ldq % 16) l = prepared;
-  if (!workspace || !vec16(workspace) || workspace_bytes < l.total) return B2G_ERR_WORKSPACE;
+  if (!codes_fit(codes, ldq)) l = prepared;
+  if (l.total && (!workspace || !vec16(workspace) || workspace_bytes < l.total)) return B2G_ERR_WORKSPACE;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
 
   Dw8Gemm g = {};

@@ -40,6 +40,7 @@ TRAIN_EXPORTS = (
     "b2g_rmsnorm", "b2g_rmsnorm_backward", "b2g_rmsnorm_backward_workspace_size",
     "b2g_quantize8", "b2g_dequantize8",
     "b2g_linear_dweight8", "b2g_linear_dweight8_workspace_size",
+    "b2g_linear_dweight8_workspace_size_ex",
 )
 
 _lib = None
@@ -81,6 +82,7 @@ def train_library():
     lib.b2g_dequantize8.argtypes = [i, ll, i, vp, ll, vp, ll, vp, ll, vp]
     lib.b2g_linear_dweight8.argtypes = [i, i, i, i, vp, ll, vp, ll, vp, ll, i, vp, ll, vp, sz, vp]
     lib.b2g_linear_dweight8_workspace_size.argtypes = [i, i, i, i, vp, ll, psz]
+    lib.b2g_linear_dweight8_workspace_size_ex.argtypes = [i, i, i, i, vp, ll, vp, ll, psz]
     _lib = lib
     return lib
 

@@ -248,9 +248,16 @@ int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* 
                         const void* codes, long long ldq, const void* scales, long long lds,
                         int accumulate, void* dw, long long lddw, void* workspace,
                         size_t workspace_bytes, void* stream);
-/* dy is inspected for its alignment only. */
+/*
+ * dy is inspected for its alignment only.  The first query's bytes are enough for any codes;
+ * the second one's for these (inspected alike), which are fewer where x is read from its codes
+ * without a copy.
+ */
 int b2g_linear_dweight8_workspace_size(int dtype, int tokens, int outs, int width, const void* dy,
                                        long long lddy, size_t* bytes);
+int b2g_linear_dweight8_workspace_size_ex(int dtype, int tokens, int outs, int width, const void* dy,
+                                          long long lddy, const void* codes, long long ldq,
+                                          size_t* bytes);
 
 #ifdef __cplusplus
 }
