@@ -269,8 +269,9 @@ def linear_weight_grad_8bit(dy, codes, scales, dw=None, accumulate: bool = False
     input was kept in 8 bits as (codes, scales), tokens x inputs.  dy is tokens x outputs.
 
     `dw` takes the result; with `accumulate` it is added to the values there.  x's values
-    are exact in the products, which add up in float32; with float32 dy all its 24 bits
-    take part (dy must be finite)."""
+    are exact in the products (with scales of 2^-110 or more, as made here), which add up in
+    float32; with float32 dy all its 24 bits take part, of values below 2^-110 what is left of
+    them above 2^-134 (dy must be finite)."""
     if stream is None:
         got = _fast().linear_weight_grad_8bit(dy, codes, scales, dw, accumulate)
         if got is not None:

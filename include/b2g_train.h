@@ -239,9 +239,10 @@ int b2g_rmsnorm_backward_workspace_size(int dtype, long long rows, int cols, siz
  *     dw = dy^T x  (plus dw's previous value when accumulate != 0).
  *   dy             tokens x outs, lddy.   codes, scales  x: tokens x width, ldq, lds.
  *   dw             outs x width, lddw; it must not overlap the operands.
- * x's values enter as BF16, in which those of b2g_quantize8 are exact; BF16 dy enters as it
- * is, FP32 dy as three BF16 pieces that carry its 24 bits (it must be finite).  Products add
- * up in FP32.  A value of x that is NaN or infinite makes its column of dw NaN or infinite
+ * x's values enter as BF16, in which those of b2g_quantize8, and all with scales from 2^-110
+ * on, are exact (below, rounded to BF16's subnormals); BF16 dy enters as it is, FP32 dy as three
+ * BF16 pieces that carry its 24 bits from 2^-110 on (below, they are off by 2^-134 at most; dy must
+ * be finite).  Products add up in FP32.  A value of x that is NaN or infinite makes its column of dw NaN or infinite
  * whatever dy is.  tokens == 0 writes zeros (nothing when accumulate != 0).
  */
 int b2g_linear_dweight8(int dtype, int tokens, int outs, int width, const void* dy, long long lddy,
