@@ -12,6 +12,10 @@ The 8-bit form of a rows x cols matrix is a pair of tensors:
 and stands for codes * scales.  The scale is the smallest power of two, 2^-110 at least,
 that brings the block's largest finite value to 448 or below, so a value is rounded once,
 by at most 2^-4 of itself or 2^-10 of the scale; infinities and NaN are kept as NaN.
+
+Codes and scales made by a call with plain arguments share one storage, those of other calls
+have one each: nothing should resize, free or move one of a pair by its storage, and saving
+or keeping either keeps both.
 """
 from __future__ import annotations
 
@@ -137,7 +141,7 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-5, out=None, stream=
 
     weight is a vector of cols elements of x's type (None: ones); rstd, 1 / sqrt(mean
     of total^2 + eps), a float32 vector for the backward pass.  `out` takes y and may be
-    x or residual itself."""
+    the residual itself or, where there is one, x (without one total is x)."""
     if out is None and stream is None:
         got = _fast().rms_norm(x, weight, residual, eps)
         if got is not None:
