@@ -138,13 +138,12 @@ inline int row_threads(int chunks, int per, int least) {
 
 // The ring of a block of `threads` for rows of `cols` columns in slots of `slot` bytes,
 // `per` columns a thread, leaving `reserved` bytes; stages < 2 when they do not fit.
-inline Ring ring_of(int threads, int per, int cols, size_t slot, size_t reserved,
-                    size_t bytes = kRingBytes) {
+inline Ring ring_of(int threads, int per, int cols, size_t slot, size_t reserved) {
   Ring r{32, 0, 0};
   while (r.nt < threads && r.nt * per < cols) r.nt *= 2;
   r.groups = threads / r.nt;
-  if (r.nt * per < cols || reserved >= bytes) return r;
-  const size_t s = (bytes - reserved) / (slot * r.groups);
+  if (r.nt * per < cols || reserved >= kRingBytes) return r;
+  const size_t s = (kRingBytes - reserved) / (slot * r.groups);
   r.stages = (int)(s < (size_t)kRingStages ? s : (size_t)kRingStages);
   return r;
 }

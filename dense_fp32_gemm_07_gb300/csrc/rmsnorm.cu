@@ -980,9 +980,9 @@ int check_rows(int dtype, long long rows, int cols) {
   return 0;
 }
 
-bool ld_ok(const void* p, long long ld, int cols) { return !p || ld >= (cols > 1 ? cols : 1); }
-bool codes_ok(const Rows8& k, int cols) {
-  return ld_ok(k.q, k.ldq, cols) && (!k.q || k.lds >= scale_count(cols > 1 ? cols : 1));
+bool ld_ok(long long ld, int cols) { return ld >= (cols > 1 ? cols : 1); }
+bool codes_ok(const Rows8& k, int cols) {  // where they are given
+  return !k.q || (ld_ok(k.ldq, cols) && k.lds >= scale_count(cols > 1 ? cols : 1));
 }
 
 // Partial rows of whichever way the pass runs: the query does not know the operands.
@@ -1016,8 +1016,8 @@ int b2g_rmsnorm(int dtype, long long rows, int cols, const void* x, long long ld
   const int vec = dtype == B2G_F32 ? 4 : 8;
   const Rows8 y8 = rows8(y_codes, ldyq, y_scales, ldys, vec);
   const Rows8 t8 = rows8(total_codes, ldtq, total_scales, ldts, vec);
-  if (!ld_ok(&rc, ldx, cols) || !ld_ok(residual, ldr, cols) || !ld_ok(total, ldt, cols) ||
-      !ld_ok(y, ldy, cols) || !codes_ok(y8, cols) || !codes_ok(t8, cols))
+  if (!ld_ok(ldx, cols) || (residual && !ld_ok(ldr, cols)) || (total && !ld_ok(ldt, cols)) ||
+      (y && !ld_ok(ldy, cols)) || !codes_ok(y8, cols) || !codes_ok(t8, cols))
     return B2G_ERR_INVALID_LD;
   if (rows == 0 || cols == 0) return 0;
   if (!x || (!y8.q) != (!y8.s) || (!t8.q) != (!t8.s)) return B2G_ERR_NULL;
@@ -1062,8 +1062,8 @@ int b2g_rmsnorm_backward(int dtype, long long rows, int cols, const void* dy, lo
   const Rows8 k8 = total_scales ? rows8(const_cast<void*>(total), ldt, const_cast<void*>(total_scales), ldts,
                                        dtype == B2G_F32 ? 4 : 8)
                                : Rows8{};
-  if (!ld_ok(&rc, lddy, cols) || !ld_ok(&rc, ldt, cols) || !codes_ok(k8, cols) ||
-      !ld_ok(dtotal, lddt, cols) || !ld_ok(&rc, lddx, cols))
+  if (!ld_ok(lddy, cols) || !ld_ok(ldt, cols) || !codes_ok(k8, cols) || (dtotal && !ld_ok(lddt, cols)) ||
+      !ld_ok(lddx, cols))
     return B2G_ERR_INVALID_LD;
   if (cols == 0 || (rows == 0 && !dweight)) return 0;
   if (rows > 0 && (!dy || !total || !rstd || !dx)) return B2G_ERR_NULL;
