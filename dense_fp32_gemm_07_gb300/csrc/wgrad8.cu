@@ -17,7 +17,7 @@
 //
 // Bound: the tensor cores; short sums, writing the result.  BF16: 16384 tokens on 11008 x 4096
 // 775 to 870 us (1.70 to 1.91 PFLOP/s, under the power cap), 4096 on 4096 x 4096 86 us, of
-// which the products 70 and the preparation 8 to 10; 64 on 4096 x 4096 13.7 (34 MB written; 15.5
+// which the products 70 and the preparation 8 to 10; 64 on 4096 x 4096 13.9 (34 MB written; 15.6
 // with a preparation).  FP32: 4096 on 4096 x 4096 237 us, 1.74 PFLOP/s of the three products.
 // Converting x on its way takes about 1150 cycles a k tile, the products alone 520: 80 KB through
 // shared memory (dy and codes in, codes out, BF16 in, both operands out) are 640 cycles; the
@@ -891,7 +891,7 @@ int encode_codes(CUtensorMap* m, const void* codes, int width, int tokens, long 
 
 // Either way's layout; x is read from its codes where that costs less than preparing it, which
 // takes a launch (there is one all the same where dy has to be copied).  Us, prepared and from the
-// codes: 300 tokens on 512 x 256 7.3 and 7.1; 5844 on 128 x 6944 43 and 31; 16384 on 512 x 8192
+// codes: 300 tokens on 512 x 256 7.3 and 7.0; 5844 on 128 x 6944 43 and 33; 16384 on 512 x 8192
 // 141 and 143; 8192 on 2048 x 2048 48.5 and 72; 4096 on 4096 x 4096 86 and 127.  Codes off the
 // 16-byte boundaries are prepared in any case.
 bool layouts(int dtype, int tokens, int outs, int width, const void* dy, long long lddy, Layout& prepared,
